@@ -109,6 +109,19 @@ def load_library(debug: bool | None = None) -> ctypes.CDLL:
     lib.attn_fwd_debug_build.restype = ctypes.c_int
     lib.attn_fwd_debug_selftest.argtypes = lib.attn_fwd.argtypes
     lib.attn_fwd_debug_selftest.restype = ctypes.c_int
+    vp, ci, cf = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+    lib.attn_fwd_lse.argtypes = [vp] * 5 + [ci] + [i64] * 6 + [cf, ci, ci, vp]
+    lib.attn_fwd_lse.restype = ci
+    lib.attn_fwd_varlen_lse.argtypes = [vp] * 7 + [i64] * 7 + [cf, ci, ci, vp]
+    lib.attn_fwd_varlen_lse.restype = ci
+    lib.attn_bwd.argtypes = [vp] * 9 + [ci] + [i64] * 6 + [cf, ci, ci, vp, i64, vp]
+    lib.attn_bwd.restype = ci
+    lib.attn_bwd_workspace_bytes.argtypes = [i64] * 6
+    lib.attn_bwd_workspace_bytes.restype = i64
+    lib.attn_bwd_varlen.argtypes = [vp] * 11 + [i64] * 8 + [cf, ci, ci, vp, i64, vp]
+    lib.attn_bwd_varlen.restype = ci
+    lib.attn_bwd_varlen_workspace_bytes.argtypes = [i64] * 8
+    lib.attn_bwd_varlen_workspace_bytes.restype = i64
     _libs[debug] = lib
     return lib
 
@@ -330,6 +343,218 @@ def attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, *,
     return out
 
 
+def _check_bf16(named, dim: int, form: str):
+    """Every (name, tensor) is a contiguous bf16 CUDA tensor of `dim` dimensions on
+    one device."""
+    import torch
+
+    for name, t in named:
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda:
+            raise TypeError(f"{name} must be a bf16 CUDA tensor")
+        if t.dim() != dim or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {form} tensor")
+        if t.device != named[0][1].device:
+            raise ValueError(f"{name} must be on {named[0][0]}'s device")
+
+
+def _check_offsets(named, device):
+    import torch
+
+    for name, t in named:
+        if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda
+                or t.dim() != 1 or not t.is_contiguous()):
+            raise TypeError(f"{name} must be a contiguous 1-D int32 CUDA tensor")
+        if t.device != device:
+            raise ValueError("q, k, v and the offsets must be on one device")
+    if named[0][1].numel() != named[1][1].numel() or named[0][1].numel() < 2:
+        raise ValueError("cu_seqlens_q and cu_seqlens_k must both have B + 1 >= 2 entries")
+
+
+def _lse_like(lse, shape, device):
+    """lse as given (checked), or a new one."""
+    import torch
+
+    if lse is None:
+        return torch.empty(shape, dtype=torch.float32, device=device)
+    if (not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32 or tuple(lse.shape) != shape
+            or not lse.is_contiguous() or lse.device != device):
+        raise ValueError(f"lse must be a contiguous fp32 tensor of shape {shape} on {device}")
+    return lse
+
+
+def _call(fn, *args):
+    """A C entry point whose nonzero status is raised."""
+    st = fn(*args)
+    if st != ATTN_OK:
+        raise AttnError(int(st), status_str(st))
+
+
+def _size(n: int) -> int:
+    if n < 0:
+        raise AttnError(int(n), status_str(int(n)))
+    return int(n)
+
+
+def attn_fwd_lse(q, k, v, *, causal: bool = False, layout: str = "bhsd",
+                 scale: float | None = None, rounding: str = "rtne", out=None, lse=None):
+    """attn_fwd_ex that also returns each query row's log-sum-exp: (out, lse), lse
+    fp32 of shape (B, Hq, Sq) in either layout. ``attn_bwd`` takes both."""
+    import torch
+
+    if layout not in LAYOUTS or rounding not in ROUNDINGS:
+        raise ValueError("unknown layout or rounding mode")
+    _check_bf16((("q", q), ("k", k), ("v", v)), 4, "4-D")
+    B, Hq, Sq, D = _dims(q, layout)
+    Bk, Hkv, Sk, Dk = _dims(k, layout)
+    if (Bk, Dk) != (B, D) or tuple(v.shape) != tuple(k.shape) or Hkv < 1 or Hq % Hkv:
+        raise ValueError("shape mismatch")
+    if out is None:
+        out = torch.empty_like(q)
+    _check_out(out, q)
+    lse = _lse_like(lse, (B, Hq, Sq), q.device)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    with _on_device(q.device):
+        _call(load_library().attn_fwd_lse, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+              lse.data_ptr(), LAYOUTS[layout], B, Hq, Hkv, Sq, Sk, D, float(scale),
+              ROUNDINGS[rounding], ATTN_FLAG_CAUSAL if causal else 0,
+              torch.cuda.current_stream(q.device).cuda_stream)
+    return out, lse
+
+
+def attn_fwd_varlen_lse(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, *,
+                        causal: bool = False, scale: float | None = None, rounding: str = "rtne",
+                        out=None, lse=None):
+    """attn_fwd_varlen that also returns each query row's log-sum-exp: (out, lse), lse
+    fp32 of shape (Hq, total_q). Tokens of no sequence are left as they were."""
+    import torch
+
+    if rounding not in ROUNDINGS:
+        raise ValueError("unknown rounding mode")
+    _check_bf16((("q", q), ("k", k), ("v", v)), 3, "(tokens, heads, d)")
+    _check_offsets((("cu_seqlens_q", cu_seqlens_q), ("cu_seqlens_k", cu_seqlens_k)), q.device)
+    total_q, Hq, D = q.shape
+    total_k, Hkv, Dk = k.shape
+    if Dk != D or tuple(v.shape) != tuple(k.shape) or Hkv < 1 or Hq % Hkv:
+        raise ValueError("shape mismatch")
+    if out is None:
+        out = torch.empty_like(q)
+    _check_out(out, q)
+    lse = _lse_like(lse, (Hq, total_q), q.device)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    with _on_device(q.device):
+        _call(load_library().attn_fwd_varlen_lse, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+              out.data_ptr(), lse.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(),
+              cu_seqlens_q.numel() - 1, Hq, Hkv, total_q, total_k, int(max_seqlen_q), D,
+              float(scale), ROUNDINGS[rounding], ATTN_FLAG_CAUSAL if causal else 0,
+              torch.cuda.current_stream(q.device).cuda_stream)
+    return out, lse
+
+
+def bwd_workspace_bytes(B: int, Hq: int, Hkv: int, Sq: int, Sk: int, d: int = 128) -> int:
+    """Device workspace attn_bwd needs on the current device."""
+    return _size(load_library().attn_bwd_workspace_bytes(B, Hq, Hkv, Sq, Sk, d))
+
+
+def bwd_varlen_workspace_bytes(B: int, Hq: int, Hkv: int, total_q: int, total_k: int,
+                               max_seqlen_q: int, max_seqlen_k: int, d: int = 128) -> int:
+    """Device workspace attn_bwd_varlen needs on the current device."""
+    return _size(load_library().attn_bwd_varlen_workspace_bytes(
+        B, Hq, Hkv, total_q, total_k, max_seqlen_q, max_seqlen_k, d))
+
+
+def _grads(q, k, v, dq, dk, dv, workspace, need: int):
+    """The gradients and the workspace as given (checked), or new ones."""
+    import torch
+
+    got = []
+    for name, g, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        if g is None:
+            g = torch.empty_like(like)
+        elif (not isinstance(g, torch.Tensor) or g.dtype != torch.bfloat16 or g.shape != like.shape
+              or not g.is_contiguous() or g.device != like.device):
+            raise ValueError(f"{name} must be a contiguous bf16 tensor shaped like {name[1:]} on its device")
+        got.append(g)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _check_workspace(workspace, q.device)
+    return (*got, workspace)
+
+
+def attn_bwd(dout, q, k, v, out, lse, *, causal: bool = False, layout: str = "bhsd",
+             scale: float | None = None, rounding: str = "rtne", dq=None, dk=None, dv=None,
+             workspace=None):
+    """Gradients (dq, dk, dv) of ``out, lse = attn_fwd_lse(q, k, v, ...)`` for the
+    output's gradient ``dout``, with the forward call's causal, layout and scale.
+
+    ``workspace``: a CUDA tensor of at least ``bwd_workspace_bytes(...)`` bytes;
+    allocated here if not given (the C entry point itself never allocates)."""
+    import torch
+
+    if layout not in LAYOUTS or rounding not in ROUNDINGS:
+        raise ValueError("unknown layout or rounding mode")
+    _check_bf16((("q", q), ("k", k), ("v", v), ("dout", dout), ("out", out)), 4, "4-D")
+    B, Hq, Sq, D = _dims(q, layout)
+    Bk, Hkv, Sk, Dk = _dims(k, layout)
+    if ((Bk, Dk) != (B, D) or v.shape != k.shape or dout.shape != q.shape or out.shape != q.shape
+            or Hkv < 1 or Hq % Hkv):
+        raise ValueError("shape mismatch")
+    if lse is None:
+        raise ValueError("lse must be what attn_fwd_lse returned")
+    lse = _lse_like(lse, (B, Hq, Sq), q.device)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    with _on_device(q.device):
+        dq, dk, dv, workspace = _grads(q, k, v, dq, dk, dv, workspace,
+                                       bwd_workspace_bytes(B, Hq, Hkv, Sq, Sk, D))
+        _call(load_library().attn_bwd, dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+              out.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+              LAYOUTS[layout], B, Hq, Hkv, Sq, Sk, D, float(scale), ROUNDINGS[rounding],
+              ATTN_FLAG_CAUSAL if causal else 0, workspace.data_ptr(),
+              workspace.numel() * workspace.element_size(),
+              torch.cuda.current_stream(q.device).cuda_stream)
+    return dq, dk, dv
+
+
+def attn_bwd_varlen(dout, q, k, v, out, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int,
+                    max_seqlen_k: int, *, causal: bool = False, scale: float | None = None,
+                    rounding: str = "rtne", dq=None, dk=None, dv=None, workspace=None):
+    """Gradients (dq, dk, dv) of ``out, lse = attn_fwd_varlen_lse(q, k, v, ...)``. Tokens of
+    no sequence are left as they were (unset where the gradients are allocated here).
+    Invalid offsets are found on the device: check ``attn_fwd_last_error()`` after a sync."""
+    import torch
+
+    if rounding not in ROUNDINGS:
+        raise ValueError("unknown rounding mode")
+    _check_bf16((("q", q), ("k", k), ("v", v), ("dout", dout), ("out", out)), 3, "(tokens, heads, d)")
+    _check_offsets((("cu_seqlens_q", cu_seqlens_q), ("cu_seqlens_k", cu_seqlens_k)), q.device)
+    total_q, Hq, D = q.shape
+    total_k, Hkv, Dk = k.shape
+    if (Dk != D or v.shape != k.shape or dout.shape != q.shape or out.shape != q.shape or Hkv < 1
+            or Hq % Hkv):
+        raise ValueError("shape mismatch")
+    if lse is None:
+        raise ValueError("lse must be what attn_fwd_varlen_lse returned")
+    lse = _lse_like(lse, (Hq, total_q), q.device)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    B = cu_seqlens_q.numel() - 1
+    with _on_device(q.device):
+        dq, dk, dv, workspace = _grads(
+            q, k, v, dq, dk, dv, workspace,
+            bwd_varlen_workspace_bytes(B, Hq, Hkv, total_q, total_k, int(max_seqlen_q),
+                                       int(max_seqlen_k), D))
+        _call(load_library().attn_bwd_varlen, dout.data_ptr(), q.data_ptr(), k.data_ptr(),
+              v.data_ptr(), out.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+              dv.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, Hq, Hkv, total_q,
+              total_k, int(max_seqlen_q), int(max_seqlen_k), D, float(scale), ROUNDINGS[rounding],
+              ATTN_FLAG_CAUSAL if causal else 0, workspace.data_ptr(),
+              workspace.numel() * workspace.element_size(),
+              torch.cuda.current_stream(q.device).cuda_stream)
+    return dq, dk, dv
+
+
 def host_workspace_bytes(B: int, Hq: int, Hkv: int, Sq: int, Sk: int, d: int = 128) -> int:
     """Device workspace attn_fwd_host needs (negative: a status code)."""
     return load_library().attn_fwd_host_workspace_bytes(B, Hq, Hkv, Sq, Sk, d)
@@ -534,4 +759,6 @@ __all__ = ["attn_fwd", "attn_fwd_raw", "attn_fwd_last_error", "attn_fwd_timeout_
            "attn_fwd_varlen", "attn_fwd_varlen_raw", "ATTN_ERR_SEQLENS",
            "attn_fwd_host", "attn_fwd_host_raw", "host_workspace_bytes", "attn_fwd_varlen_host", "status_str", "load_library",
            "AttnError", "LAYOUTS", "ROUNDINGS", "lib_path", "ATTN_ERR_DEBUG_CHECK",
-           "ATTN_FLAG_CAUSAL", "ATTN_FLAG_SPLIT_TAIL", "split_tail_items"]
+           "ATTN_FLAG_CAUSAL", "ATTN_FLAG_SPLIT_TAIL", "split_tail_items",
+           "attn_fwd_lse", "attn_fwd_varlen_lse", "attn_bwd", "attn_bwd_varlen",
+           "bwd_workspace_bytes", "bwd_varlen_workspace_bytes"]

@@ -6,8 +6,8 @@
 same kernels with bounds and protocol checks that report through the device
 status word (see include/attn_fwd.h).
 
-Two translation units (the kernels with their launcher, and the host-buffer
-pipeline), one -gencode; the CUDA runtime is linked statically and the driver's
+Three translation units (the forward kernels with their launcher, the backward
+ones, and the host-buffer pipeline), compiled at once, one -gencode; the CUDA runtime is linked statically and the driver's
 tensor-map encoder is looked up at run time, so the library loads (and
 reports ATTN_ERR_NO_DEVICE) on a machine without a GPU.
 """
@@ -25,7 +25,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libattn_fwd.so")
 LIB_PATH_DEBUG = os.path.join(LIB_DIR, "libattn_fwd_debug.so")
-SOURCES = [os.path.join(CSRC, "attn_fwd.cu"), os.path.join(CSRC, "attn_host.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("attn_fwd.cu", "attn_bwd.cu", "attn_host.cu")]
 GENCODE = "arch=compute_103a,code=sm_103a"
 
 
@@ -67,7 +67,7 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     os.makedirs(LIB_DIR, exist_ok=True)
     tmp = path + f".tmp{os.getpid()}"
     cmd = [nvcc_path(), "-gencode", GENCODE, "-O3", "-lineinfo", "-std=c++17",
-           "-Xcompiler", "-fPIC", "-shared", "-I", INCLUDE, "-o", tmp] + SOURCES
+           "--threads", "0", "-Xcompiler", "-fPIC", "-shared", "-I", INCLUDE, "-o", tmp] + SOURCES
     if debug:
         cmd.insert(1, "-DATTN_DEBUG=1")
     if verbose:

@@ -5,8 +5,6 @@
 // BHSD are read in place), sizes the grid (one CTA per pair of 128-row query
 // tiles of one (batch, head), consecutive CTAs on the same head so that K/V
 // stay in L2) and launches the kernel on the caller's stream.
-#include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -15,28 +13,14 @@
 
 #include "attn_fwd.h"
 #include "attn_fwd_kernel.cuh"
+#include "host_common.h"
 #include "splitkv_combine.cuh"
 
 namespace {
 
+using namespace attn_host;
+
 constexpr int kVersion = 100;  // 0.1.0
-constexpr unsigned long long kTimeoutNs = 2000000000ull;  // 2 s per wait
-constexpr int kMaxDevices = 64;
-
-std::once_flag g_encode_once;
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  std::call_once(g_encode_once, [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult qres;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                         &qres) == cudaSuccess &&
-        qres == cudaDriverEntryPointSuccess)
-      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  });
-  return g_encode;
-}
 
 std::mutex g_dev_mutex;
 int g_dev_state[kMaxDevices];  // 0 = not set up, 1 = ready, negative = status to return
@@ -81,11 +65,21 @@ int device_ready(int dev) {
       reinterpret_cast<const void*>(attn::attn_fwd_kernel<false, false, false, true>),
       reinterpret_cast<const void*>(attn::attn_fwd_kernel<false, false, false, false, true>),
       reinterpret_cast<const void*>(attn::attn_fwd_kernel<false, false, false, true, false, 1>),
-      reinterpret_cast<const void*>(attn::attn_fwd_kernel<false, false, false, true, false, 2>)};
+      reinterpret_cast<const void*>(attn::attn_fwd_kernel<false, false, false, true, false, 2>),
+      // The log-sum-exp forms of the whole-range ones, in the same order.
+      reinterpret_cast<const void*>(attn::attn_fwd_kernel<false, false, false, false, false, 0, true>),
+      reinterpret_cast<const void*>(attn::attn_fwd_kernel<false, true, false, false, false, 0, true>),
+      reinterpret_cast<const void*>(attn::attn_fwd_kernel<false, false, true, false, false, 0, true>),
+      reinterpret_cast<const void*>(attn::attn_fwd_kernel<false, true, true, false, false, 0, true>),
+      reinterpret_cast<const void*>(attn::attn_fwd_kernel<false, false, false, true, false, 0, true>),
+      reinterpret_cast<const void*>(attn::attn_fwd_kernel<false, false, false, true, false, 1, true>),
+      reinterpret_cast<const void*>(attn::attn_fwd_kernel<false, false, false, true, false, 2, true>)};
   for (const void* fn : variants) {
-    const bool persist = fn == variants[5] || fn == variants[7] || fn == variants[8];
+    const bool persist = fn == variants[5] || fn == variants[7] || fn == variants[8] ||
+                         fn == variants[13] || fn == variants[14] || fn == variants[15];
     const bool pair = fn == variants[6];
-    const bool row_limit = fn == variants[2] || fn == variants[3] || fn == variants[4];
+    const bool row_limit = fn == variants[2] || fn == variants[3] || fn == variants[4] ||
+                           fn == variants[10] || fn == variants[11] || fn == variants[12];
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              persist ? attn::kSmemBytesPersist
                              : pair  ? attn::kSmemBytesPair
@@ -154,48 +148,8 @@ int64_t pair_tail_items(int dev, int64_t n_items, int64_t kv_tiles) {
   return (tail > 0 && tail <= g_dev_pairs[dev] && kv_tiles >= kPairMinKvTiles) ? tail : 0;
 }
 
-// 4-D map over a (B, H, S, 128) bf16 tensor in the given layout, box of
-// 64 columns x box_rows rows, 128-byte swizzle, zero fill outside the tensor.
-bool make_map(CUtensorMap* map, const void* ptr, int layout, int64_t B, int64_t H, int64_t S,
-              uint32_t box_rows) {
-  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
-  if (!encode) return false;
-  const cuuint64_t row = 128 * 2;
-  cuuint64_t dims[4], strides[3];
-  cuuint32_t box[4];
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  if (layout == ATTN_LAYOUT_BHSD) {
-    dims[0] = 128; dims[1] = S; dims[2] = H; dims[3] = B;
-    strides[0] = row; strides[1] = S * row; strides[2] = H * S * row;
-    box[0] = 64; box[1] = box_rows; box[2] = 1; box[3] = 1;
-  } else {
-    dims[0] = 128; dims[1] = H; dims[2] = S; dims[3] = B;
-    strides[0] = row; strides[1] = H * row; strides[2] = S * H * row;
-    box[0] = 64; box[1] = 1; box[2] = box_rows; box[3] = 1;
-  }
-  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims,
-                            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
-bool overlaps(const void* a, uint64_t na, const void* b, uint64_t nb) {
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + nb && b0 < a0 + na;
-}
-
 int64_t kv_tiles_of(int64_t Sk) { return (Sk + attn::kBN - 1) / attn::kBN; }
 
-// Causal schedule: (batch, head) items per longest-first group, so that the K/V
-// of one group (512 bytes per key and head) take at most 48 MiB of the 126 MiB L2.
-int head_group_of(int64_t BH, int64_t keys_per_head) {
-  const int64_t per = 512 * (keys_per_head > 0 ? keys_per_head : 1);
-  int64_t g = (int64_t(48) << 20) / per;
-  if (g < 1) g = 1;
-  if (g > BH) g = BH;
-  return static_cast<int>(g);
-}
 int64_t qpairs_of(int64_t Sq) { return (Sq + 2 * attn::kBM - 1) / (2 * attn::kBM); }
 
 // Split workspace: unnormalised rows (128 fp32) then (reference max, row sum).
@@ -233,11 +187,50 @@ int attn_fwd_version(void) { return kVersion; }
 
 namespace {
 
+// Whether a call without a mask takes the persistent variant (n_items and kv_tiles
+// as in kPersistMaxKvTiles's comment).
+bool persists(int dev, int n_splits, const attn::Params& p) {
+  return n_splits == 1 && p.kv_tiles <= kPersistMaxKvTiles && p.n_items > g_dev_sms[dev];
+}
+
+struct WholeLaunch {
+  const CUtensorMap &tq, &tk, &tv, &to;
+  const attn::Params& p;
+  unsigned grid, sms;
+  cudaStream_t stream;
+};
+
+// One launch over the whole key range, with or without the rows' log-sum-exp.
+template <bool kLse>
+void launch_whole(const WholeLaunch& a, bool causal, bool persist) {
+  if (causal) {
+    attn::attn_fwd_kernel<false, true, false, false, false, 0, kLse>
+        <<<a.grid, attn::kThreads, attn::kSmemBytesRowLimit, a.stream>>>(a.tq, a.tk, a.tv, a.to, a.p);
+  } else if (!persist) {
+    attn::attn_fwd_kernel<false, false, false, false, false, 0, kLse>
+        <<<a.grid, attn::kThreads, attn::kSmemBytes, a.stream>>>(a.tq, a.tk, a.tv, a.to, a.p);
+  } else if (a.p.kv_tiles == 1 && a.p.kv_tail < attn::kBN) {
+    // Items of at most 4 key tiles ending in a ragged one: a short persistent
+    // variant (the partial in TMEM until the epilogue, S kept in registers between
+    // the softmax passes, the ragged tile's P V cut at its last key chunk). One
+    // tile and 2 to 4 tiles are separate instantiations: the general form cost the
+    // one-tile case 4%.
+    attn::attn_fwd_kernel<false, false, false, true, false, 1, kLse>
+        <<<a.sms, attn::kThreads, attn::kSmemBytesPersist, a.stream>>>(a.tq, a.tk, a.tv, a.to, a.p);
+  } else if (a.p.kv_tiles <= attn::kShortMaxKvTiles && a.p.kv_tail < attn::kBN) {
+    attn::attn_fwd_kernel<false, false, false, true, false, 2, kLse>
+        <<<a.sms, attn::kThreads, attn::kSmemBytesPersist, a.stream>>>(a.tq, a.tk, a.tv, a.to, a.p);
+  } else {
+    attn::attn_fwd_kernel<false, false, false, true, false, 0, kLse>
+        <<<a.sms, attn::kThreads, attn::kSmemBytesPersist, a.stream>>>(a.tq, a.tk, a.tv, a.to, a.p);
+  }
+}
+
 int attn_fwd_impl(const void* q, const void* k, const void* v, void* out, int layout, int64_t B,
                   int64_t H, int64_t Sq, int64_t Sk, int64_t d, float scale, int rounding_mode,
                   void* stream, unsigned long long timeout_ns, int withhold_s0, int n_splits,
                   void* workspace, int64_t workspace_bytes, int64_t Hkv = 0, int causal = 0,
-                  int dbg_poison = 0, int split_tail = 0) {
+                  int dbg_poison = 0, int split_tail = 0, float* lse = nullptr) {
   if (Hkv == 0) Hkv = H;
   // ---- host-side validation (nothing is launched on failure)
   if (!q || !k || !v || !out) return ATTN_ERR_INVALID_ARG;
@@ -263,6 +256,13 @@ int attn_fwd_impl(const void* q, const void* k, const void* v, void* out, int la
   if (overlaps(out, bytes_q, q, bytes_q) || overlaps(out, bytes_q, k, bytes_kv) ||
       overlaps(out, bytes_q, v, bytes_kv))
     return ATTN_ERR_ALIASING;
+  if (lse) {
+    const uint64_t bytes_lse = uint64_t(B) * H * Sq * 4;
+    if (reinterpret_cast<uintptr_t>(lse) & 3u) return ATTN_ERR_MISALIGNED;
+    if (overlaps(lse, bytes_lse, q, bytes_q) || overlaps(lse, bytes_lse, k, bytes_kv) ||
+        overlaps(lse, bytes_lse, v, bytes_kv) || overlaps(lse, bytes_lse, out, bytes_q))
+      return ATTN_ERR_ALIASING;
+  }
   if (n_splits > 1) {
     const int64_t need = splitkv_bytes(B, H, Sq, n_splits);
     if (!workspace || workspace_bytes < need) return ATTN_ERR_INVALID_ARG;
@@ -315,6 +315,7 @@ int attn_fwd_impl(const void* q, const void* k, const void* v, void* out, int la
   p.n_items = static_cast<int>(B * H * n_qpairs * n_splits);
   p.item_base = 0;
   p.early_dependents = 0;
+  p.lse = lse;
 
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const int64_t n_items1 = B * H * n_qpairs;
@@ -322,27 +323,12 @@ int attn_fwd_impl(const void* q, const void* k, const void* v, void* out, int la
       (split_tail && !causal && n_splits == 1 && !dbg_poison) ? pair_tail_items(dev, n_items1, p.kv_tiles)
                                                               : 0;
   const unsigned grid = static_cast<unsigned>(B * H * n_qpairs * n_splits);
-  if (causal) {
-    attn::attn_fwd_kernel<false, true, false>
-        <<<grid, attn::kThreads, attn::kSmemBytesRowLimit, cs>>>(tq, tk, tv, to, p);
-  } else if (n_splits == 1 && p.kv_tiles <= kPersistMaxKvTiles && p.n_items > g_dev_sms[dev]) {
-    // Items of at most 4 key tiles ending in a ragged one: a short persistent
-    // variant (the partial in TMEM until the epilogue, S kept in registers between
-    // the softmax passes, the ragged tile's P V cut at its last key chunk). One
-    // tile and 2 to 4 tiles are separate instantiations: the general form cost the
-    // one-tile case 4%.
-    if (p.kv_tiles == 1 && p.kv_tail < attn::kBN)
-      attn::attn_fwd_kernel<false, false, false, true, false, 1>
-          <<<static_cast<unsigned>(g_dev_sms[dev]), attn::kThreads, attn::kSmemBytesPersist, cs>>>(
-              tq, tk, tv, to, p);
-    else if (p.kv_tiles <= attn::kShortMaxKvTiles && p.kv_tail < attn::kBN)
-      attn::attn_fwd_kernel<false, false, false, true, false, 2>
-          <<<static_cast<unsigned>(g_dev_sms[dev]), attn::kThreads, attn::kSmemBytesPersist, cs>>>(
-              tq, tk, tv, to, p);
+  if (causal || lse || persists(dev, n_splits, p)) {
+    const WholeLaunch at{tq, tk, tv, to, p, grid, static_cast<unsigned>(g_dev_sms[dev]), cs};
+    if (lse)
+      launch_whole<true>(at, causal != 0, persists(dev, n_splits, p));
     else
-      attn::attn_fwd_kernel<false, false, false, true>
-          <<<static_cast<unsigned>(g_dev_sms[dev]), attn::kThreads, attn::kSmemBytesPersist, cs>>>(
-              tq, tk, tv, to, p);
+      launch_whole<false>(at, causal != 0, persists(dev, n_splits, p));
   } else if (n_tail > 0) {
     // The full waves as usual, then the tail items as 2-CTA clusters, each with
     // its key range split in two halves and merged on chip (pair variant).
@@ -437,11 +423,15 @@ int attn_fwd_ex(const void* q, const void* k, const void* v, void* out, int layo
                        (flags & ATTN_FLAG_SPLIT_TAIL) ? 1 : 0);
 }
 
-int attn_fwd_varlen(const void* q, const void* k, const void* v, void* out,
-                    const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int64_t B,
-                    int64_t Hq, int64_t Hkv, int64_t total_q, int64_t total_k,
-                    int64_t max_seqlen_q, int64_t d, float scale, int rounding_mode, int flags,
-                    void* stream) {
+}  // extern "C"
+
+namespace {
+
+int attn_fwd_varlen_impl(const void* q, const void* k, const void* v, void* out, float* lse,
+                         const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int64_t B,
+                         int64_t Hq, int64_t Hkv, int64_t total_q, int64_t total_k,
+                         int64_t max_seqlen_q, int64_t d, float scale, int rounding_mode, int flags,
+                         void* stream) {
   // ---- host-side validation (nothing is launched on failure); the offsets
   // themselves live on the device and are checked by the kernel.
   if (!q || !k || !v || !out || !cu_seqlens_q || !cu_seqlens_k) return ATTN_ERR_INVALID_ARG;
@@ -469,6 +459,15 @@ int attn_fwd_varlen(const void* q, const void* k, const void* v, void* out,
       overlaps(out, bytes_q, cu_seqlens_q, uint64_t(B + 1) * 4) ||
       overlaps(out, bytes_q, cu_seqlens_k, uint64_t(B + 1) * 4))
     return ATTN_ERR_ALIASING;
+  if (lse) {
+    const uint64_t bytes_lse = uint64_t(total_q) * Hq * 4;
+    if (reinterpret_cast<uintptr_t>(lse) & 3u) return ATTN_ERR_MISALIGNED;
+    if (overlaps(lse, bytes_lse, q, bytes_q) || overlaps(lse, bytes_lse, k, bytes_kv) ||
+        overlaps(lse, bytes_lse, v, bytes_kv) || overlaps(lse, bytes_lse, out, bytes_q) ||
+        overlaps(lse, bytes_lse, cu_seqlens_q, uint64_t(B + 1) * 4) ||
+        overlaps(lse, bytes_lse, cu_seqlens_k, uint64_t(B + 1) * 4))
+      return ATTN_ERR_ALIASING;
+  }
 
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -515,17 +514,57 @@ int attn_fwd_varlen(const void* q, const void* k, const void* v, void* out,
   p.n_items = static_cast<int>(B * Hq * n_qpairs);
   p.item_base = 0;
   p.early_dependents = 0;
+  p.lse = lse;
 
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const unsigned grid = static_cast<unsigned>(B * Hq * n_qpairs);
-  if (p.causal)
+  if (p.causal && lse)
+    attn::attn_fwd_kernel<false, true, true, false, false, 0, true>
+        <<<grid, attn::kThreads, attn::kSmemBytesRowLimit, cs>>>(tq, tk, tv, to, p);
+  else if (p.causal)
     attn::attn_fwd_kernel<false, true, true>
+        <<<grid, attn::kThreads, attn::kSmemBytesRowLimit, cs>>>(tq, tk, tv, to, p);
+  else if (lse)
+    attn::attn_fwd_kernel<false, false, true, false, false, 0, true>
         <<<grid, attn::kThreads, attn::kSmemBytesRowLimit, cs>>>(tq, tk, tv, to, p);
   else
     attn::attn_fwd_kernel<false, false, true>
         <<<grid, attn::kThreads, attn::kSmemBytesRowLimit, cs>>>(tq, tk, tv, to, p);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_LAUNCH;
   return ATTN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_fwd_varlen(const void* q, const void* k, const void* v, void* out,
+                    const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int64_t B,
+                    int64_t Hq, int64_t Hkv, int64_t total_q, int64_t total_k,
+                    int64_t max_seqlen_q, int64_t d, float scale, int rounding_mode, int flags,
+                    void* stream) {
+  return attn_fwd_varlen_impl(q, k, v, out, nullptr, cu_seqlens_q, cu_seqlens_k, B, Hq, Hkv, total_q,
+                              total_k, max_seqlen_q, d, scale, rounding_mode, flags, stream);
+}
+
+int attn_fwd_varlen_lse(const void* q, const void* k, const void* v, void* out, float* lse,
+                        const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int64_t B,
+                        int64_t Hq, int64_t Hkv, int64_t total_q, int64_t total_k,
+                        int64_t max_seqlen_q, int64_t d, float scale, int rounding_mode, int flags,
+                        void* stream) {
+  if (!lse) return ATTN_ERR_INVALID_ARG;
+  return attn_fwd_varlen_impl(q, k, v, out, lse, cu_seqlens_q, cu_seqlens_k, B, Hq, Hkv, total_q,
+                              total_k, max_seqlen_q, d, scale, rounding_mode, flags, stream);
+}
+
+int attn_fwd_lse(const void* q, const void* k, const void* v, void* out, float* lse, int layout,
+                 int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int64_t Sk, int64_t d, float scale,
+                 int rounding_mode, int flags, void* stream) {
+  if (flags & ~ATTN_FLAG_CAUSAL) return ATTN_ERR_UNSUPPORTED;
+  if (!lse || Hkv < 1) return ATTN_ERR_INVALID_ARG;
+  return attn_fwd_impl(q, k, v, out, layout, B, Hq, Sq, Sk, d, scale, rounding_mode, stream,
+                       kTimeoutNs, 0, 1, nullptr, 0, Hkv, (flags & ATTN_FLAG_CAUSAL) ? 1 : 0, 0, 0,
+                       lse);
 }
 
 int64_t attn_fwd_splitkv_workspace_bytes(int64_t B, int64_t H, int64_t Sq, int64_t Sk, int64_t d,
@@ -605,13 +644,8 @@ int attn_fwd_debug_selftest(const void* q, const void* k, const void* v, void* o
 
 int attn_fwd_last_error(void) {
   unsigned int s = 0;
-  if (cudaMemcpyFromSymbol(&s, attn::g_attn_status, sizeof(s)) != cudaSuccess) {
-    cudaGetLastError();
-    return ATTN_ERR_NO_DEVICE;
-  }
+  if (!take_status(attn::g_attn_status, &s) || !bwd_take_status(&s)) return ATTN_ERR_NO_DEVICE;
   if (s == 0) return ATTN_OK;
-  const unsigned int zero = 0;
-  cudaMemcpyToSymbol(attn::g_attn_status, &zero, sizeof(zero));
   if (s & 1u) return ATTN_ERR_TIMEOUT;
   return (s & 2u) ? ATTN_ERR_SEQLENS : ATTN_ERR_DEBUG_CHECK;
 }

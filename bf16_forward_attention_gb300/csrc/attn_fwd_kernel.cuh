@@ -173,12 +173,14 @@ struct Params {
   int n_items;      // persistent variant: work items; CTA c takes c, c + gridDim.x, ...
   int item_base;    // pair variant: the work item of block 0 (CTA b takes item_base + b)
   int early_dependents;  // base variant: a pair launch follows and may start early
+  float* lse;  // log-sum-exp variants: one fp32 per query row, see store_lse
 };
 
 // Bit 0: some wait timed out. Bit 1: a variable-length batch's offsets were
 // invalid (that sequence's output is left unwritten). Bit 2 (debug build): a
-// bounds or protocol check failed.
-__device__ unsigned int g_attn_status;
+// bounds or protocol check failed. One word per translation unit with kernels;
+// attn_fwd_last_error reads them all.
+static __device__ unsigned int g_attn_status;
 
 // Debug build (-DATTN_DEBUG=1): dbg_ok(cond) records a failed check in bit 2 of
 // the status word and returns cond, so that the caller can skip the access it
@@ -654,6 +656,14 @@ __device__ __forceinline__ uint2 merge_splits4(const float* part_o, const float*
                     round_bf16_bits(o.z * inv, mode) | (round_bf16_bits(o.w * inv, mode) << 16));
 }
 
+// The row's log-sum-exp, natural log of sum_j exp(scale q.k_j) over the keys it
+// sees: l = sum_j 2^(t_j - m) with t in log2 units, so it is ln 2 (m + log2 l).
+// A row that sees no key has m = -Inf and l = 0: -Inf. A NaN row's is NaN. One
+// store per row and call, 4 bytes next to the row's 256: not measurable.
+__device__ __forceinline__ void store_lse(float* lse, size_t at, float m, float l) {
+  lse[at] = 0.6931471805599453f * (m + log2f(l));
+}
+
 // The CTA's share of the work: (batch, head, query-tile pair, key split) and the
 // split's key tiles. Splits of one pair are adjacent in the grid, pairs of one
 // head are adjacent (so K/V of a head stay in L2); under the causal mask the
@@ -767,9 +777,12 @@ __device__ __forceinline__ int first_masked_tile(const Work& w) {
 // epilogue (no fold) and the softmax keeps S in the row's registers between its
 // two passes; on the ragged last tile the P V MMAs and pass B stop at the last
 // 16-key chunk holding a key.
+// kLse: the epilogue also stores every row's log-sum-exp (training's backward
+// pass reads it; parts of a key range are merged by it), at (b*H + h)*Sq + row,
+// or head * total_q + token for a packed batch.
 // Each is compiled separately so that the other variants carry none of it.
 template <bool kPartial, bool kCausal, bool kVarlen, bool kPersist = false, bool kPair = false,
-          int kShort = 0>
+          int kShort = 0, bool kLse = false>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
@@ -787,6 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   static_assert(!kPersist || (!kPartial && !kCausal && !kVarlen), "persistent: base path only");
   static_assert(!kPair || (!kPartial && !kCausal && !kVarlen && !kPersist), "pair: base path only");
   static_assert(kShort == 0 || (kPersist && kShort <= 2), "short: a persistent variant");
+  static_assert(!kLse || (!kPartial && !kPair), "log-sum-exp: whole key range per CTA");
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   // A key limit per row (rising along the causal diagonal, or the sequence's
@@ -1363,6 +1377,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int q_row0 = (2 * wk.pair + t) * kBM + wq * 32;
         const bool rtne = p.mode == 0;
         const uint32_t bias = p.mode == 1 ? 0x8000u : 0u;
+        if constexpr (kLse) {
+          if (q_row0 + lane < p.Sq)
+            store_lse(p.lse, static_cast<size_t>(wk.bh) * p.Sq + q_row0 + lane, m_used, l);
+        }
         const float inv_l = __frcp_rn(l);  // 0 -> Inf, so an all -Inf row gives 0 * Inf = NaN
         const uint64_t inv2 = ptx::f2_pack(inv_l, inv_l);
 #pragma unroll
@@ -1646,6 +1664,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         // 128-byte swizzle, and store this warp's 32 rows with two TMA boxes.
         const uint32_t stage_base = sQ + t * kTileBytes;
         const int mode = p.mode;
+        // Where the row's log-sum-exp is stored, before its rounding or after, is
+        // what leaves each variant free of spills.
+        constexpr bool kLseFirst = kCausal && !kVarlen;
+        auto put_lse = [&]() {
+          const int q = (2 * wk.pair + t) * kBM + row;  // within the sequence
+          if (q < wk.sq && dbg_ok(wk.q_base + q < p.Sq))
+            store_lse(p.lse,
+                      static_cast<size_t>(kVarlen ? wk.head : wk.bh) * p.Sq + wk.q_base + q, m_used,
+                      l);
+        };
+        if constexpr (kLse && kLseFirst) put_lse();
         const float inv_l = __frcp_rn(l);  // 0 -> Inf, so an all -Inf row gives 0 * Inf = NaN
         uint64_t inv2 = ptx::f2_pack(inv_l, inv_l);
         if constexpr (kRowLimit) {
@@ -1742,6 +1771,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             dst[cix] = *reinterpret_cast<const uint4*>(stage + off);
           }
         }
+        if constexpr (kLse && !kLseFirst) put_lse();
         __syncwarp();
       }
     }

@@ -1,0 +1,91 @@
+// host_common.h - what the library's translation units with kernels share on the
+// host: the tensor-map encoder, argument checks, the status words.
+#pragma once
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <mutex>
+
+#include "attn_fwd.h"
+
+namespace attn_host {
+
+constexpr unsigned long long kTimeoutNs = 2000000000ull;  // 2 s per wait
+constexpr int kMaxDevices = 64;
+
+inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static std::once_flag once;
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  std::call_once(once, [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult qres;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                         &qres) == cudaSuccess &&
+        qres == cudaDriverEntryPointSuccess)
+      encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  return encode;
+}
+
+// 4-D map over a (B, H, S, 128) bf16 tensor in the given layout, box of
+// 64 columns x box_rows rows, 128-byte swizzle, zero fill outside the tensor.
+inline bool make_map(CUtensorMap* map, const void* ptr, int layout, int64_t B, int64_t H, int64_t S,
+              uint32_t box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (!encode) return false;
+  const cuuint64_t row = 128 * 2;
+  cuuint64_t dims[4], strides[3];
+  cuuint32_t box[4];
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  if (layout == ATTN_LAYOUT_BHSD) {
+    dims[0] = 128; dims[1] = S; dims[2] = H; dims[3] = B;
+    strides[0] = row; strides[1] = S * row; strides[2] = H * S * row;
+    box[0] = 64; box[1] = box_rows; box[2] = 1; box[3] = 1;
+  } else {
+    dims[0] = 128; dims[1] = H; dims[2] = S; dims[3] = B;
+    strides[0] = row; strides[1] = H * row; strides[2] = S * H * row;
+    box[0] = 64; box[1] = 1; box[2] = box_rows; box[3] = 1;
+  }
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims,
+                            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+inline bool overlaps(const void* a, uint64_t na, const void* b, uint64_t nb) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a0 < b0 + nb && b0 < a0 + na;
+}
+
+// Causal schedule: (batch, head) items per longest-first group, so that the K/V
+// of one group (512 bytes per key and head) take at most 48 MiB of the 126 MiB L2.
+inline int head_group_of(int64_t BH, int64_t keys_per_head) {
+  const int64_t per = 512 * (keys_per_head > 0 ? keys_per_head : 1);
+  int64_t g = (int64_t(48) << 20) / per;
+  if (g < 1) g = 1;
+  if (g > BH) g = BH;
+  return static_cast<int>(g);
+}
+
+// Adds a translation unit's device status word of the current device to *s and
+// clears it.
+template <typename Word>
+bool take_status(Word& word, unsigned int* s) {
+  unsigned int x = 0;
+  if (cudaMemcpyFromSymbol(&x, word, sizeof(x)) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  if (x != 0) {
+    const unsigned int zero = 0;
+    cudaMemcpyToSymbol(word, &zero, sizeof(zero));
+    *s |= x;
+  }
+  return true;
+}
+bool bwd_take_status(unsigned int* s);  // attn_bwd.cu
+
+}  // namespace attn_host

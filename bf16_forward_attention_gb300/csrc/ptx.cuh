@@ -129,6 +129,15 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint
       : "memory");
 }
 
+// Contiguous copy global -> shared (both 16-byte aligned, a multiple of 16 bytes),
+// completion signalled on `bar` (tx bytes).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
 // L2 eviction policies for the cache-hinted copies: evict_first for data read
 // or written once (query tiles, output), evict_last for data many CTAs reread
 // (key and value tiles).

@@ -209,6 +209,87 @@ int attn_fwd_varlen(const void* q, const void* k, const void* v, void* out,
                     int64_t max_seqlen_q, int64_t d, float scale, int rounding_mode, int flags,
                     void* stream);
 
+/*
+ * attn_fwd_lse, attn_fwd_varlen_lse - attn_fwd_ex and attn_fwd_varlen that also
+ * leave every query row's log-sum-exp, lse = ln sum_j exp(scale q.k_j) over the
+ * keys the row sees (fp32, whatever the rounding mode). attn_bwd reads it; the
+ * results of attention over parts of a key range are joined by it. The pages
+ * describe inference only and have no counterpart.
+ *
+ *   lse    device, fp32, written, 4-byte aligned, overlapping no other tensor:
+ *          attn_fwd_lse: (B, Hq, Sq) in either layout, row (b, h, i) at
+ *          (b*Hq + h)*Sq + i; attn_fwd_varlen_lse: (Hq, total_q), row (h, token)
+ *          at h*total_q + token (tokens of no sequence are left as they were).
+ *          A row that sees no key: -Inf; a row with a NaN or +Inf logit: NaN.
+ *   flags  0 or ATTN_FLAG_CAUSAL.
+ * out has the bits that attn_fwd_ex / attn_fwd_varlen give. Other arguments,
+ * ownership and errors as there.
+ */
+int attn_fwd_lse(const void* q, const void* k, const void* v, void* out, float* lse, int layout,
+                 int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int64_t Sk, int64_t d, float scale,
+                 int rounding_mode, int flags, void* stream);
+int attn_fwd_varlen_lse(const void* q, const void* k, const void* v, void* out, float* lse,
+                        const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int64_t B,
+                        int64_t Hq, int64_t Hkv, int64_t total_q, int64_t total_k,
+                        int64_t max_seqlen_q, int64_t d, float scale, int rounding_mode, int flags,
+                        void* stream);
+
+/*
+ * attn_bwd - gradients of attn_fwd_lse with respect to q, k and v. With
+ * P = exp(scale q.k - lse) recomputed, D = sum_c dout*out per row, dP = dout v^T
+ * and dS = P o (dP - D):
+ *   dv = P^T dout     dk = scale dS^T q     dq = scale dS k
+ * dk and dv sum over the query heads that share a key/value head. No counterpart
+ * on the pages, which describe inference.
+ *
+ *   dout      device, bf16, like q                            (read only)
+ *   q, k, v   device, bf16, as given to attn_fwd_lse          (read only)
+ *   out, lse  device, as attn_fwd_lse left them               (read only)
+ *   dq        device, bf16, like q                            (written)
+ *   dk, dv    device, bf16, like k                            (written)
+ *   rounding_mode  of the gradients, one rounding from fp32 sums (P and dS are
+ *             rounded to bf16, to nearest, as operands of the products)
+ *   flags     0 or ATTN_FLAG_CAUSAL, as in the forward call
+ *   workspace device, 16-byte aligned, attn_bwd_workspace_bytes(...) bytes, owned
+ *             by the caller; its contents on entry do not matter. Calls that
+ *             share a workspace must not overlap in time.
+ * Written tensors and the workspace overlap nothing else. A row that sees no key
+ * takes no part: its dq is 0. A hidden pair takes no part: a non-finite value in
+ * a row or at a key reaches only the gradients of the pairs that see it (where the
+ * exact gradient is infinite it may come out NaN). Results are bit-identical
+ * from run to run: no sum depends on the order in which CTAs finish. Several
+ * kernels are launched on `stream`; other errors and rules as attn_fwd_ex.
+ */
+int attn_bwd(const void* dout, const void* q, const void* k, const void* v, const void* out,
+             const float* lse, void* dq, void* dk, void* dv, int layout, int64_t B, int64_t Hq,
+             int64_t Hkv, int64_t Sq, int64_t Sk, int64_t d, float scale, int rounding_mode, int flags,
+             void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes attn_bwd needs on the current device, or a negative status code. */
+int64_t attn_bwd_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int64_t Sk,
+                                 int64_t d);
+
+/*
+ * attn_bwd_varlen - the same for a packed batch: gradients of attn_fwd_varlen_lse.
+ *   dout, q, k, v, out, lse, offsets   as given to, and left by, that call
+ *   dq like q; dk, dv like k. Tokens of no sequence are left as they were; a
+ *   sequence without queries gets dk = dv = 0, one without keys dq = 0.
+ *   max_seqlen_q, max_seqlen_k  upper bounds on every sequence's lengths; they size
+ *                               the grids
+ * Invalid offsets are found on the device as in attn_fwd_varlen: that sequence's
+ * gradients are left unwritten and attn_fwd_last_error() reports
+ * ATTN_ERR_SEQLENS. Other arguments as attn_bwd.
+ */
+int attn_bwd_varlen(const void* dout, const void* q, const void* k, const void* v, const void* out,
+                    const float* lse, void* dq, void* dk, void* dv, const int32_t* cu_seqlens_q,
+                    const int32_t* cu_seqlens_k, int64_t B, int64_t Hq, int64_t Hkv,
+                    int64_t total_q, int64_t total_k, int64_t max_seqlen_q, int64_t max_seqlen_k,
+                    int64_t d, float scale, int rounding_mode, int flags, void* workspace,
+                    int64_t workspace_bytes, void* stream);
+int64_t attn_bwd_varlen_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t total_q,
+                                        int64_t total_k, int64_t max_seqlen_q,
+                                        int64_t max_seqlen_k, int64_t d);
+
 /* Workspace bytes attn_fwd_splitkv needs (0 for num_splits == 1), or a negative
  * status code: ATTN_ERR_INVALID_ARG / ATTN_ERR_UNSUPPORTED for invalid sizes,
  * ATTN_ERR_TOO_LARGE when a size exceeds 2^31 - 1 or the launch would need more
