@@ -122,6 +122,10 @@ def load_library(debug: bool | None = None) -> ctypes.CDLL:
     lib.attn_bwd_varlen.restype = ci
     lib.attn_bwd_varlen_workspace_bytes.argtypes = [i64] * 8
     lib.attn_bwd_varlen_workspace_bytes.restype = i64
+    lib.attn_fwd_prefix.argtypes = [vp] * 8 + [ci] + [i64] * 7 + [cf, ci, ci, vp, i64, vp]
+    lib.attn_fwd_prefix.restype = ci
+    lib.attn_fwd_prefix_workspace_bytes.argtypes = [i64] * 7
+    lib.attn_fwd_prefix_workspace_bytes.restype = i64
     _libs[debug] = lib
     return lib
 
@@ -555,6 +559,69 @@ def attn_bwd_varlen(dout, q, k, v, out, lse, cu_seqlens_q, cu_seqlens_k, max_seq
     return dq, dk, dv
 
 
+def prefix_workspace_bytes(B: int, Hq: int, Hkv: int, Sq: int, Sp: int, cap: int, d: int = 128) -> int:
+    """Device workspace attn_fwd_prefix needs on the current device."""
+    return _size(load_library().attn_fwd_prefix_workspace_bytes(B, Hq, Hkv, Sq, Sp, cap, d))
+
+
+def attn_fwd_prefix(q, k_prefix, v_prefix, k, v, seqlens, *, causal: bool = False,
+                    layout: str = "bhsd", scale: float | None = None, rounding: str = "rtne",
+                    out=None, lse=None, workspace=None):
+    """Attention of a batch whose sequences share a prefix (sampling many completions
+    of one prompt): (out, lse).
+
+    bf16 CUDA tensors, for "bshd": q (B, Sq, Hq, 128) new tokens, k_prefix and v_prefix
+    (Sp, Hkv, 128) shared by all, k and v (B, cap, Hkv, 128) the sequences' own caches
+    with ``seqlens`` (int32 CUDA, B) keys in use; for "bhsd" heads come before tokens.
+    Every query sees the whole prefix and its own sequence's keys; with ``causal`` the
+    Sq tokens are the sequence's last and see only what is before them. k_prefix and
+    v_prefix may be None: no prefix. A length outside 0..cap is found on the device:
+    check ``attn_fwd_last_error()`` after a sync."""
+    import torch
+
+    if layout not in LAYOUTS or rounding not in ROUNDINGS:
+        raise ValueError("unknown layout or rounding mode")
+    _check_bf16((("q", q), ("k", k), ("v", v)), 4, "4-D")
+    B, Hq, Sq, D = _dims(q, layout)
+    Bk, Hkv, cap, Dk = _dims(k, layout)
+    if (Bk, Dk) != (B, D) or v.shape != k.shape or Hkv < 1 or Hq % Hkv:
+        raise ValueError("shape mismatch")
+    if (k_prefix is None) != (v_prefix is None):
+        raise ValueError("k_prefix and v_prefix must be given together")
+    Sp = 0
+    if k_prefix is not None:
+        _check_bf16((("k_prefix", k_prefix), ("v_prefix", v_prefix)), 3, "3-D")
+        Sp = k_prefix.shape[0 if layout == "bshd" else 1]
+        if k_prefix.device != q.device:
+            raise ValueError("k_prefix must be on q's device")
+        if (v_prefix.shape != k_prefix.shape or k_prefix.shape[2] != D
+                or k_prefix.shape[1 if layout == "bshd" else 0] != Hkv):
+            raise ValueError("shape mismatch")
+    if (not isinstance(seqlens, torch.Tensor) or seqlens.dtype != torch.int32 or not seqlens.is_cuda
+            or tuple(seqlens.shape) != (B,) or not seqlens.is_contiguous()):
+        raise TypeError("seqlens must be a contiguous int32 CUDA tensor of B entries")
+    if seqlens.device != q.device:
+        raise ValueError("seqlens must be on q's device")
+    if out is None:
+        out = torch.empty_like(q)
+    _check_out(out, q)
+    lse = _lse_like(lse, (B, Hq, Sq), q.device)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    with _on_device(q.device):
+        if workspace is None:
+            workspace = torch.empty(prefix_workspace_bytes(B, Hq, Hkv, Sq, Sp, cap, D), dtype=torch.uint8,
+                                    device=q.device)
+        _check_workspace(workspace, q.device)
+        _call(load_library().attn_fwd_prefix, q.data_ptr(), k_prefix.data_ptr() if Sp else None,
+              v_prefix.data_ptr() if Sp else None, k.data_ptr(), v.data_ptr(), seqlens.data_ptr(),
+              out.data_ptr(), lse.data_ptr(), LAYOUTS[layout], B, Hq, Hkv, Sq, Sp, cap, D,
+              float(scale), ROUNDINGS[rounding], ATTN_FLAG_CAUSAL if causal else 0,
+              workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+              torch.cuda.current_stream(q.device).cuda_stream)
+    return out, lse
+
+
 def host_workspace_bytes(B: int, Hq: int, Hkv: int, Sq: int, Sk: int, d: int = 128) -> int:
     """Device workspace attn_fwd_host needs (negative: a status code)."""
     return load_library().attn_fwd_host_workspace_bytes(B, Hq, Hkv, Sq, Sk, d)
@@ -761,4 +828,5 @@ __all__ = ["attn_fwd", "attn_fwd_raw", "attn_fwd_last_error", "attn_fwd_timeout_
            "AttnError", "LAYOUTS", "ROUNDINGS", "lib_path", "ATTN_ERR_DEBUG_CHECK",
            "ATTN_FLAG_CAUSAL", "ATTN_FLAG_SPLIT_TAIL", "split_tail_items",
            "attn_fwd_lse", "attn_fwd_varlen_lse", "attn_bwd", "attn_bwd_varlen",
-           "bwd_workspace_bytes", "bwd_varlen_workspace_bytes"]
+           "bwd_workspace_bytes", "bwd_varlen_workspace_bytes", "attn_fwd_prefix",
+           "prefix_workspace_bytes"]

@@ -6,8 +6,9 @@
 same kernels with bounds and protocol checks that report through the device
 status word (see include/attn_fwd.h).
 
-Three translation units (the forward kernels with their launcher, the backward
-ones, and the host-buffer pipeline), compiled at once, one -gencode; the CUDA runtime is linked statically and the driver's
+Four translation units (the forward kernels with their launcher, the backward
+ones, those of a batch on a shared prefix, and the host-buffer pipeline), compiled
+at once, one -gencode; the CUDA runtime is linked statically and the driver's
 tensor-map encoder is looked up at run time, so the library loads (and
 reports ATTN_ERR_NO_DEVICE) on a machine without a GPU.
 """
@@ -25,7 +26,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libattn_fwd.so")
 LIB_PATH_DEBUG = os.path.join(LIB_DIR, "libattn_fwd_debug.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("attn_fwd.cu", "attn_bwd.cu", "attn_host.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("attn_fwd.cu", "attn_bwd.cu", "attn_prefix.cu", "attn_host.cu")]
 GENCODE = "arch=compute_103a,code=sm_103a"
 
 

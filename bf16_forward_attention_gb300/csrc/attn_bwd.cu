@@ -62,18 +62,6 @@ int device_ready(int dev) {
 
 int64_t tiles_of(int64_t n) { return (n + bwd::kTile - 1) / bwd::kTile; }
 
-// SMs of the current device (152, a GB300's, where there is none: size queries
-// work without one).
-int sms_here() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
-    cudaGetLastError();
-    return 152;
-  }
-  return sms;
-}
-
 // How many CTAs share one owned tile's streamed tiles: the count with the least
 // estimated time, in units of one streamed tile (about 1 us). A wave costs its
 // tiles, 2 units of start and end, and for a shared result `part` units to write
@@ -135,26 +123,6 @@ struct Span {
   const void* p;
   uint64_t n;
 };
-
-// A launch that may start while the kernel before it on the stream drains (each of
-// these kernels waits on the device for what it reads).
-template <typename... Params, typename... Args>
-bool launch(void (*fn)(Params...), int64_t grid, int threads, int smem, cudaStream_t stream, bool dependent,
-            Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = dependent ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, fn, std::forward<Args>(args)...) == cudaSuccess) return true;
-  cudaGetLastError();
-  return false;
-}
 
 int bwd_impl(const void* dout, const void* q, const void* k, const void* v, const void* out,
              const float* lse, void* dq, void* dk, void* dv, const int32_t* cu_q, const int32_t* cu_k,

@@ -644,13 +644,57 @@ int attn_fwd_debug_selftest(const void* q, const void* k, const void* v, void* o
 
 int attn_fwd_last_error(void) {
   unsigned int s = 0;
-  if (!take_status(attn::g_attn_status, &s) || !bwd_take_status(&s)) return ATTN_ERR_NO_DEVICE;
+  if (!take_status(attn::g_attn_status, &s) || !bwd_take_status(&s) ||
+      !prefix_take_status(&s))
+    return ATTN_ERR_NO_DEVICE;
   if (s == 0) return ATTN_OK;
   if (s & 1u) return ATTN_ERR_TIMEOUT;
   return (s & 2u) ? ATTN_ERR_SEQLENS : ATTN_ERR_DEBUG_CHECK;
 }
 
 }  // extern "C"
+
+namespace attn_host {
+
+int split_parts(const void* q, const void* k, const void* v, int layout, int64_t B, int64_t H, int64_t Sq,
+                int64_t Sk, float scale, int n_splits, float* part_o, float* part_rl, cudaStream_t stream) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return ATTN_ERR_NO_DEVICE;
+  }
+  const int st = device_ready(dev);
+  if (st != ATTN_OK) return st;
+  CUtensorMap tq, tk, tv;
+  if (!make_map(&tq, q, layout, B, H, Sq, attn::kBM) || !make_map(&tk, k, layout, B, H, Sk, attn::kBN) ||
+      !make_map(&tv, v, layout, B, H, Sk, attn::kBN))
+    return ATTN_ERR_LAUNCH;
+  attn::Params p = {};
+  p.Sq = static_cast<int>(Sq);
+  p.Sk = static_cast<int>(Sk);
+  p.H = static_cast<int>(H);
+  p.n_qpairs = static_cast<int>(qpairs_of(Sq));
+  p.kv_tiles = static_cast<int>(kv_tiles_of(Sk));
+  p.kv_tail = static_cast<int>(Sk - int64_t(p.kv_tiles - 1) * attn::kBN);
+  p.n_splits = n_splits;
+  p.BH = static_cast<int>(B * H);
+  p.sq_pad = p.n_qpairs * 2 * attn::kBM;
+  p.part_o = part_o;
+  p.part_rl = part_rl;
+  p.layout = layout;
+  p.c = scale * 1.4426950408889634f;
+  p.timeout_ns = kTimeoutNs;
+  p.group = 1;
+  p.max_sq = p.Sq;
+  p.head_group = 1;
+  p.n_items = p.BH * p.n_qpairs * n_splits;
+  // (The split form stores no bf16 output: its fourth map is only prefetched.)
+  attn::attn_fwd_kernel<true, false, false>
+      <<<static_cast<unsigned>(p.n_items), attn::kThreads, attn::kSmemBytes, stream>>>(tq, tk, tv, tq, p);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+}  // namespace attn_host
 
 // ---------------------------------------------------------------- no-allocation split-KV
 //

@@ -1,0 +1,382 @@
+// attn_prefix_kernel.cuh - attention of a batch whose sequences share a prefix.
+//
+// Every query sees the Sp shared keys and the keys of its own sequence. With the two
+// parts' unnormalised sums O_s, l_s relative to references r_s (log2 units),
+//   O = sum_s 2^(r_s - R) O_s / sum_s 2^(r_s - R) l_s,   lse = ln 2 (R + log2 L),
+// for any R. The parts are computed apart and joined:
+//   * the prefix, once for all sequences: the queries of one key/value head (all
+//     sequences, all heads of the group) are packed as the rows of one product
+//     with the prefix, which the fused kernel's split form computes on the tensor
+//     cores; the prefix is read once per 256 rows instead of once per sequence;
+//   * each sequence's own keys, by attn_prefix_own below: few rows against keys
+//     that nobody else reads, so it is bound by HBM;
+//   * the join, attn_prefix_join, in a fixed order.
+#pragma once
+#include "attn_fwd_kernel.cuh"
+
+namespace attn {
+namespace prefix {
+
+constexpr int kWarps = 4;
+constexpr int kOwnThreads = 32 * kWarps;
+constexpr int kKeys = 16;                       // keys per warp tile
+constexpr int kKvBytes = kKeys * kD * 2;        // 4 KiB: a tile of K or of V
+constexpr int kOwnStages = 3;
+constexpr int kWarpBytes = kOwnStages * 2 * kKvBytes;
+constexpr int kOwnOffMl = kWarps * kWarpBytes;  // [warp][row][2] floats
+constexpr int kMaxRows = 32;                    // rows of a block at most
+constexpr int kOwnSmem = kOwnOffMl + kWarps * kMaxRows * 8;
+static_assert(kWarpBytes >= kMaxRows * kD * 4, "a warp's stages hold its fp32 rows at the end");
+
+struct OwnParams {
+  const uint16_t* q;
+  const uint16_t* k;       // caches: (B, cap, Hkv, 128) or (B, Hkv, cap, 128)
+  const uint16_t* v;
+  const int* seqlens;      // keys of each sequence, 0..cap
+  uint16_t* q_packed;      // the prefix product's rows, or null
+  float* part_o;           // [split][kv head][rows_pad][128], this kernel's first split
+  float* part_rl;          // [split][kv head][rows_pad][2]
+  int B, Hq, Hkv, group, Sq, cap, layout, causal;
+  int rows;                // B * Sq * group: packed rows of a kv head
+  int rows_pad, n_splits, n_blocks;  // blocks of 16 * MT rows per (sequence, kv head)
+  float c;                 // scale * log2(e)
+};
+
+// Packed row r of a kv head is token (r / group) of the batch, head r % group of the
+// group. Element offset of its query (or output) row.
+__device__ __forceinline__ size_t query_at(int layout, int Hq, int Sq, int group, int kvh, int r) {
+  const int tok = r / group, h = kvh * group + r % group;
+  const int b = tok / Sq, i = tok % Sq;
+  return (layout == 0 ? (static_cast<size_t>(b) * Hq + h) * Sq + i
+                      : (static_cast<size_t>(b) * Sq + i) * Hq + h) * kD;
+}
+
+// Keys of its own sequence that query token i sees.
+__device__ __forceinline__ int own_limit(int i, int len, int Sq, int causal) {
+  return causal ? max(0, min(len, i + len - Sq + 1)) : len;
+}
+
+// Shared-memory offset of 16-byte chunk c of key row r: the chunk's low bits are
+// turned by the row, so that the 8 rows of an ldmatrix lie in distinct banks.
+__device__ __forceinline__ uint32_t kv_at(int r, int c) {
+  return static_cast<uint32_t>(r * 256 + ((c ^ (r & 7)) << 4));
+}
+
+// One block: 16 * kMT rows of one (sequence, kv head) against one split of its keys.
+// The four warps take its 16-key tiles in turn, each with a ring of its own (cp.async,
+// 3 stages of 8 KiB: 96 KiB a block in flight or in use, two blocks a SM) and no
+// synchronisation but __syncwarp, and are joined in shared memory at the end. Rows
+// past the end and keys past the sequence's length are zeros. Bound by HBM: per 8 KiB
+// a warp issues some 200 instructions, a tenth of what the SM has in the time the
+// bytes take. P enters the product with V as two bf16 terms, as in the fused kernel.
+template <int kMT>
+__global__ void __launch_bounds__(kOwnThreads, 2) attn_prefix_own(const OwnParams p) {
+  extern __shared__ __align__(128) uint8_t smem_own[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = blockIdx.x % p.n_splits;
+  int rest = blockIdx.x / p.n_splits;
+  const int block = rest % p.n_blocks;
+  rest /= p.n_blocks;
+  const int kvh = rest % p.Hkv, b = rest / p.Hkv;
+  const int R = p.Sq * p.group;                    // rows of the sequence
+  const int r0 = block * 16 * kMT;                 // first row of the block
+  const int n_rows = min(16 * kMT, R - r0);
+  const int first = b * R + r0;                    // packed row of the block's first
+  const float neg_inf = -__int_as_float(0x7F800000);
+
+  if (p.q_packed && split == 0) {
+    for (int x = threadIdx.x; x < n_rows * 16; x += kOwnThreads) {
+      const int r = first + (x >> 4);
+      const size_t dst = (p.layout == 0 ? static_cast<size_t>(kvh) * p.rows + r
+                                        : static_cast<size_t>(r) * p.Hkv + kvh) * kD;
+      reinterpret_cast<uint4*>(p.q_packed + dst)[x & 15] = reinterpret_cast<const uint4*>(
+          p.q + query_at(p.layout, p.Hq, p.Sq, p.group, kvh, r))[x & 15];
+    }
+  }
+  const int len = __ldg(p.seqlens + b);
+  if (len < 0 || len > p.cap) {
+    if (threadIdx.x == 0) atomicOr(&g_attn_status, 2u);
+    return;
+  }
+  // Limits rise with the row: the block's least and largest.
+  const int min_lim = own_limit(r0 / p.group, len, p.Sq, p.causal);
+  const int max_lim = own_limit((r0 + n_rows - 1) / p.group, len, p.Sq, p.causal);
+  const int tiles = (max_lim + kKeys - 1) / kKeys;
+  const int t_first = static_cast<int>(static_cast<long long>(tiles) * split / p.n_splits);
+  const int t_end = static_cast<int>(static_cast<long long>(tiles) * (split + 1) / p.n_splits);
+
+  // This lane's rows of m-tile m: lane / 4 and lane / 4 + 8.
+  uint32_t qf[kMT][8][4];
+  int lim[kMT][2];
+#pragma unroll
+  for (int m = 0; m < kMT; ++m) {
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int r = 16 * m + (lane >> 2) + 8 * hf;
+      const bool in = r < n_rows;
+      lim[m][hf] = in ? own_limit((r0 + r) / p.group, len, p.Sq, p.causal) : 0;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(
+          p.q + query_at(p.layout, p.Hq, p.Sq, p.group, kvh, in ? first + r : first));
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        qf[m][ks][hf] = in ? __ldg(src + 8 * ks + (lane & 3)) : 0u;
+        qf[m][ks][2 + hf] = in ? __ldg(src + 8 * ks + 4 + (lane & 3)) : 0u;
+      }
+    }
+  }
+  const size_t key_stride = (p.layout == 0 ? 1 : static_cast<size_t>(p.Hkv)) * kD;
+  const size_t kv_first = (p.layout == 0 ? (static_cast<size_t>(b) * p.Hkv + kvh) * p.cap
+                                         : static_cast<size_t>(b) * p.cap * p.Hkv + kvh) * kD;
+  const uint32_t ring = ptx::smem_u32(smem_own) + warp * kWarpBytes;
+  // Tile t into stage s: a half-warp reads one key's 256 bytes.
+  auto load = [&](int t, int s) {
+    const uint32_t dst = ring + s * 2 * kKvBytes;
+    const int c = lane & 15;
+#pragma unroll
+    for (int u = 0; u < kKeys / 2; ++u) {
+      const int r = 2 * u + (lane >> 4);
+      const int key = t * kKeys + r;
+      const int ok = key < len;
+      const size_t at = kv_first + (ok ? key : 0) * key_stride + 8 * c;
+      ptx::cp_async16(dst + kv_at(r, c), p.k + at, ok);
+      ptx::cp_async16(dst + kKvBytes + kv_at(r, c), p.v + at, ok);
+    }
+  };
+
+  float o[kMT][16][4];
+  float mref[kMT][2], l[kMT][2];
+#pragma unroll
+  for (int m = 0; m < kMT; ++m) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[m][i][e] = 0.f;
+    mref[m][0] = mref[m][1] = neg_inf;
+    l[m][0] = l[m][1] = 0.f;
+  }
+  const int t0 = t_first + warp;
+  const int n = t0 < t_end ? (t_end - t0 + kWarps - 1) / kWarps : 0;  // this warp's tiles
+#pragma unroll
+  for (int s = 0; s < kOwnStages - 1; ++s) {
+    if (s < n) load(t0 + s * kWarps, s);
+    ptx::cp_async_commit();
+  }
+  for (int i = 0; i < n; ++i) {
+    ptx::cp_async_wait<kOwnStages - 2>();
+    __syncwarp();  // every lane's copies of this tile; every lane is done with the last one
+    if (i + kOwnStages - 1 < n)
+      load(t0 + (i + kOwnStages - 1) * kWarps, (i + kOwnStages - 1) % kOwnStages);
+    ptx::cp_async_commit();
+    const uint32_t kt = ring + (i % kOwnStages) * 2 * kKvBytes, vt = kt + kKvBytes;
+    const int key0 = (t0 + i * kWarps) * kKeys;
+    const bool masked = key0 + kKeys > min_lim;
+
+    // S: keys key0 + 8 nt + 2 (lane % 4) + {0, 1} of rows lane / 4 (elements 0, 1)
+    // and lane / 4 + 8 (elements 2, 3).
+    float s[kMT][2][4];
+#pragma unroll
+    for (int m = 0; m < kMT; ++m)
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[m][nt][e] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) {
+      uint32_t kf[4];
+      ptx::ldmatrix4(kt + kv_at(((lane >> 4) << 3) + (lane & 7), 2 * ks + ((lane >> 3) & 1)), kf);
+#pragma unroll
+      for (int m = 0; m < kMT; ++m) {
+        ptx::mma_16816(s[m][0], qf[m][ks], kf[0], kf[1]);
+        ptx::mma_16816(s[m][1], qf[m][ks], kf[2], kf[3]);
+      }
+    }
+    uint32_t hi[kMT][4], lo[kMT][4];
+#pragma unroll
+    for (int m = 0; m < kMT; ++m) {
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float t[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          t[e] = s[m][e >> 1][2 * hf + (e & 1)] * p.c;
+          if (masked && key0 + 8 * (e >> 1) + 2 * (lane & 3) + (e & 1) >= lim[m][hf]) t[e] = neg_inf;
+        }
+        // The row's largest (a NaN is left out here and comes back through its weight).
+        float mx = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+        const bool need = mx > mref[m][hf] + kTau;
+        if (__any_sync(0xFFFFFFFFu, need)) {
+          const float f = need ? ptx::ex2(mref[m][hf] - mx) : 1.f;  // 0 from -Inf
+          if (need) mref[m][hf] = mx;
+          l[m][hf] *= f;
+#pragma unroll
+          for (int d = 0; d < 16; ++d) {
+            o[m][d][2 * hf] *= f;
+            o[m][d][2 * hf + 1] *= f;
+          }
+        }
+        const float ref = mref[m][hf] == neg_inf ? 0.f : mref[m][hf];
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          w[e] = ptx::ex2(t[e] - ref);
+          l[m][hf] += w[e];
+        }
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          const uint32_t h = ptx::pack_bf16x2(w[2 * nt], w[2 * nt + 1]);
+          hi[m][2 * nt + hf] = h;
+          lo[m][2 * nt + hf] = ptx::pack_bf16x2(w[2 * nt] - __uint_as_float(h << 16),
+                                                w[2 * nt + 1] - __uint_as_float(h & 0xFFFF0000u));
+        }
+      }
+    }
+    // A key that some row does not see has weight 0 there, and 0 * NaN would carry a
+    // non-finite element of its V to that row. Only tiles at the causal edge have
+    // such keys; if V holds a non-finite element there, the rows are summed key by
+    // key over what they see.
+    bool apart = false;
+    if (masked && p.causal) {
+      uint32_t acc = 0;
+#pragma unroll
+      for (int u = 0; u < kKvBytes / 512; ++u) {
+        const uint4 x = ptx::ld_shared_v4(vt + (u * 32 + lane) * 16);
+        acc = ptx::bf16x2_nonfinite_acc(x.x, ptx::bf16x2_nonfinite_acc(x.y, acc));
+        acc = ptx::bf16x2_nonfinite_acc(x.z, ptx::bf16x2_nonfinite_acc(x.w, acc));
+      }
+      apart = __any_sync(0xFFFFFFFFu, acc != 0);
+    }
+    if (!apart) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t vf[4];
+        ptx::ldmatrix4_trans(vt + kv_at((((lane >> 3) & 1) << 3) + (lane & 7), 2 * j + (lane >> 4)), vf);
+#pragma unroll
+        for (int m = 0; m < kMT; ++m) {
+          ptx::mma_16816(o[m][2 * j], hi[m], vf[0], vf[1]);
+          ptx::mma_16816(o[m][2 * j + 1], hi[m], vf[2], vf[3]);
+          ptx::mma_16816(o[m][2 * j], lo[m], vf[0], vf[1]);
+          ptx::mma_16816(o[m][2 * j + 1], lo[m], vf[2], vf[3]);
+        }
+      }
+    } else {
+#pragma unroll 1
+      for (int kk = 0; kk < kKeys; ++kk) {
+        const int src = (lane & ~3) | ((kk & 7) >> 1);
+#pragma unroll
+        for (int m = 0; m < kMT; ++m) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const uint32_t ph = __shfl_sync(0xFFFFFFFFu, kk < 8 ? hi[m][hf] : hi[m][2 + hf], src);
+            const uint32_t pl = __shfl_sync(0xFFFFFFFFu, kk < 8 ? lo[m][hf] : lo[m][2 + hf], src);
+            const float w = (kk & 1) ? __uint_as_float(ph & 0xFFFF0000u) + __uint_as_float(pl & 0xFFFF0000u)
+                                     : __uint_as_float(ph << 16) + __uint_as_float(pl << 16);
+            if (key0 + kk >= lim[m][hf]) continue;
+#pragma unroll
+            for (int d = 0; d < 16; ++d) {
+              const uint32_t x = ptx::ld_shared_u32(vt + kv_at(kk, d) + 4 * (lane & 3));
+              o[m][d][2 * hf] = fmaf(w, __uint_as_float(x << 16), o[m][d][2 * hf]);
+              o[m][d][2 * hf + 1] = fmaf(w, __uint_as_float(x & 0xFFFF0000u), o[m][d][2 * hf + 1]);
+            }
+          }
+        }
+      }
+    }
+  }
+  // ---- the warps' rows, joined through shared memory (each warp's own ring).
+  ptx::cp_async_wait<0>();
+  __syncwarp();
+  float* ml = reinterpret_cast<float*>(smem_own + kOwnOffMl) + warp * kMaxRows * 2;
+  float* mine = reinterpret_cast<float*>(smem_own + warp * kWarpBytes);
+#pragma unroll
+  for (int m = 0; m < kMT; ++m) {
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      float sum = l[m][hf];
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+      const int r = 16 * m + (lane >> 2) + 8 * hf;
+      if ((lane & 3) == 0) {
+        ml[2 * r] = mref[m][hf];
+        ml[2 * r + 1] = sum;
+      }
+#pragma unroll
+      for (int d = 0; d < 16; ++d)
+        *reinterpret_cast<float2*>(mine + r * kD + 8 * d + 2 * (lane & 3)) =
+            make_float2(o[m][d][2 * hf], o[m][d][2 * hf + 1]);
+    }
+  }
+  __syncthreads();
+  const float* all_ml = reinterpret_cast<const float*>(smem_own + kOwnOffMl);
+  const size_t row_base = (static_cast<size_t>(split) * p.Hkv + kvh) * p.rows_pad + first;
+  for (int r = 0; r < n_rows; ++r) {
+    float M = neg_inf;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, all_ml[w * kMaxRows * 2 + 2 * r]);
+    const float ref = M == neg_inf ? 0.f : M;
+    float L = 0.f, x = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = ptx::ex2(all_ml[w * kMaxRows * 2 + 2 * r] - ref);
+      L = fmaf(all_ml[w * kMaxRows * 2 + 2 * r + 1], f, L);
+      x = fmaf(reinterpret_cast<const float*>(smem_own + w * kWarpBytes)[r * kD + threadIdx.x], f, x);
+    }
+    p.part_o[(row_base + r) * kD + threadIdx.x] = x;
+    if (threadIdx.x == 0) reinterpret_cast<float2*>(p.part_rl)[row_base + r] = make_float2(M, L);
+  }
+}
+
+// ---------------------------------------------------------------- join
+struct JoinParams {
+  const float* part_o;   // [split][kv head][rows_pad][128], the prefix's splits first
+  const float* part_rl;
+  const int* seqlens;
+  uint16_t* out;
+  float* lse;            // (B, Hq, Sq)
+  int Hq, Hkv, group, Sq, cap, layout, mode, rows, rows_pad, n_parts;
+};
+
+constexpr int kJoinRows = 4;
+
+// A warp per packed row, four columns a lane; parts in a fixed order.
+__global__ void __launch_bounds__(32 * kJoinRows) attn_prefix_join(const JoinParams p) {
+  const long long x = static_cast<long long>(blockIdx.x) * kJoinRows + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  ptx::grid_dependency_wait();
+  if (x >= static_cast<long long>(p.rows) * p.Hkv) return;
+  const int kvh = static_cast<int>(x / p.rows), r = static_cast<int>(x % p.rows);
+  const int tok = r / p.group, h = kvh * p.group + r % p.group;
+  const int b = tok / p.Sq, i = tok % p.Sq;
+  const int len = __ldg(p.seqlens + b);
+  if (len < 0 || len > p.cap) return;  // reported by attn_prefix_own
+  const float neg_inf = -__int_as_float(0x7F800000);
+  const size_t pitch = static_cast<size_t>(p.Hkv) * p.rows_pad;
+  const size_t row0 = static_cast<size_t>(kvh) * p.rows_pad + r;
+  const float2* rl = reinterpret_cast<const float2*>(p.part_rl);
+  float R = neg_inf;
+  for (int s = 0; s < p.n_parts; ++s) R = fmaxf(R, rl[row0 + s * pitch].x);
+  const float ref = R == neg_inf ? 0.f : R;
+  float L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = 0; s < p.n_parts; ++s) {
+    const float2 ml = rl[row0 + s * pitch];
+    const float w = ptx::ex2(ml.x - ref);
+    const float4 y = *reinterpret_cast<const float4*>(p.part_o + (row0 + s * pitch) * kD + 4 * lane);
+    L = fmaf(ml.y, w, L);
+    o.x = fmaf(y.x, w, o.x);
+    o.y = fmaf(y.y, w, o.y);
+    o.z = fmaf(y.z, w, o.z);
+    o.w = fmaf(y.w, w, o.w);
+  }
+  const float inv = __frcp_rn(L);
+  const uint2 w2 = make_uint2(
+      round_bf16_bits(o.x * inv, p.mode) | (round_bf16_bits(o.y * inv, p.mode) << 16),
+      round_bf16_bits(o.z * inv, p.mode) | (round_bf16_bits(o.w * inv, p.mode) << 16));
+  *reinterpret_cast<uint2*>(p.out + query_at(p.layout, p.Hq, p.Sq, p.group, kvh, r) + 4 * lane) = w2;
+  if (lane == 0) store_lse(p.lse, (static_cast<size_t>(b) * p.Hq + h) * p.Sq + i, R, L);
+}
+
+}  // namespace prefix
+}  // namespace attn

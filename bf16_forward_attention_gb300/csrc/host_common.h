@@ -7,6 +7,7 @@
 
 #include <cstdint>
 #include <mutex>
+#include <utility>
 
 #include "attn_fwd.h"
 
@@ -86,6 +87,46 @@ bool take_status(Word& word, unsigned int* s) {
   }
   return true;
 }
-bool bwd_take_status(unsigned int* s);  // attn_bwd.cu
+bool bwd_take_status(unsigned int* s);     // attn_bwd.cu
+bool prefix_take_status(unsigned int* s);  // attn_prefix.cu
+
+// Streaming multiprocessors of the current device (152, a GB300's, where there is
+// none: size queries work without one).
+inline int sms_here() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
+    cudaGetLastError();
+    return 152;
+  }
+  return sms;
+}
+
+// A launch that, when `dependent`, may start while the kernel before it on the
+// stream drains: its kernel waits on the device for what it reads.
+template <typename... Params, typename... Args>
+bool launch(void (*fn)(Params...), int64_t grid, int threads, int smem, cudaStream_t stream, bool dependent,
+            Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, fn, std::forward<Args>(args)...) == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
+}
+
+// attn_fwd.cu: the split form of the fused kernel without its merge. Each of
+// n_splits parts of the keys leaves unnormalised rows [split][b*H + h][sq_pad][128]
+// and (reference, row sum) [split][b*H + h][sq_pad][2], sq_pad = Sq rounded up to
+// 256. Arguments are checked by the caller; returns a status code.
+int split_parts(const void* q, const void* k, const void* v, int layout, int64_t B, int64_t H, int64_t Sq,
+                int64_t Sk, float scale, int n_splits, float* part_o, float* part_rl, cudaStream_t stream);
 
 }  // namespace attn_host

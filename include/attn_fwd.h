@@ -290,6 +290,49 @@ int64_t attn_bwd_varlen_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int6
                                         int64_t total_k, int64_t max_seqlen_q,
                                         int64_t max_seqlen_k, int64_t d);
 
+/*
+ * attn_fwd_prefix - attention of a batch whose sequences share a prefix, the form
+ * of sampling many completions of one prompt. Each query sees every key of the
+ * shared prefix and the keys of its own sequence, read from a cache of `cap` slots
+ * per sequence; the prefix is read once for the whole batch. Serving attention with
+ * caches is among what the pages' kernel lacks (snilld.dk, "Autoregressiv
+ * serving, de praktiske hager"); the pages have no counterpart of this call.
+ *
+ *   q, out     device, bf16, (B, Sq, Hq, 128) for BSHD, (B, Hq, Sq, 128) for BHSD:
+ *              Sq new tokens per sequence (1 when sampling token by token)
+ *   k_prefix, v_prefix  device, bf16, (Sp, Hkv, 128) for BSHD, (Hkv, Sp, 128) for
+ *              BHSD; Sp may be 0 (they are then not read and may be NULL)
+ *   k, v       device, bf16, the sequences' own caches: (B, cap, Hkv, 128) for BSHD,
+ *              (B, Hkv, cap, 128) for BHSD; slots at and after a sequence's length
+ *              are not read
+ *   seqlens    device, int32, B entries: own keys of each sequence, 0 .. cap, the new
+ *              tokens' included. A length outside that range is found on the
+ *              device: that sequence's out and lse are left unwritten and
+ *              attn_fwd_last_error() reports ATTN_ERR_SEQLENS.
+ *   lse        device, fp32, (B, Hq, Sq), written: each row's log-sum-exp over all
+ *              the keys it sees
+ *   flags      0: a query sees all its sequence's own keys; ATTN_FLAG_CAUSAL: query i
+ *              sees own key j iff j <= i + seqlens[b] - Sq (the Sq new tokens are the
+ *              last of the sequence). The prefix comes before every query.
+ *   workspace  device, 16-byte aligned, attn_fwd_prefix_workspace_bytes(...) bytes,
+ *              owned by the caller; calls that share one must not overlap in time
+ * A row that sees no key (no prefix and no own key) comes out NaN, lse -Inf. out
+ * holds attn_fwd's numerics contract; results are bit-identical from run to run
+ * and depend on the call's sizes (how keys are cut into parts), not on other
+ * sequences' values. Hidden keys take no part. Meant for few new tokens per
+ * sequence: their rows go through the own keys 32 at a time. Other arguments,
+ * ownership and errors as attn_fwd_ex.
+ */
+int attn_fwd_prefix(const void* q, const void* k_prefix, const void* v_prefix, const void* k,
+                    const void* v, const int32_t* seqlens, void* out, float* lse, int layout,
+                    int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int64_t Sp, int64_t cap,
+                    int64_t d, float scale, int rounding_mode, int flags, void* workspace,
+                    int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes attn_fwd_prefix needs on the current device, or a negative status. */
+int64_t attn_fwd_prefix_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int64_t Sp,
+                                        int64_t cap, int64_t d);
+
 /* Workspace bytes attn_fwd_splitkv needs (0 for num_splits == 1), or a negative
  * status code: ATTN_ERR_INVALID_ARG / ATTN_ERR_UNSUPPORTED for invalid sizes,
  * ATTN_ERR_TOO_LARGE when a size exceeds 2^31 - 1 or the launch would need more
