@@ -268,6 +268,96 @@ __device__ __forceinline__ void store_part(uint32_t tacc, bool zero, float* dst,
   }
 }
 
+// The softmax threads' turns, over 64 columns each. kMask is a template argument:
+// as a run-time test inside, its compares ran in every tile (half of the
+// instructions of the unmasked loop).
+__device__ __forceinline__ uint64_t pair_of(const uint32_t (&r)[32], int x) {
+  return ptx::f2_pack(__uint_as_float(r[x]), __uint_as_float(r[x + 1]));
+}
+
+// dkv: P from S (a lane's key against 64 queries, whose -lse log2(e) are in shared
+// memory); kept in pr, and written over S as bf16.
+template <bool kMask>
+__device__ __forceinline__ void dkv_p(uint32_t tS, const ulonglong2* stat, uint64_t c2, int lo, int hi,
+                                      Half& pr) {
+  uint32_t a[32], b[32];
+  load_half(tS, a, b);
+#pragma unroll
+  for (int ch = 0; ch < 2; ++ch) {
+    uint32_t w[16];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const ulonglong2 nl = stat[8 * ch + e];  // four columns
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int x = 4 * e + 2 * u;
+        float t0, t1;
+        ptx::f2_unpack(ptx::f2_fma(pair_of(ch ? b : a, x), c2, u ? nl.y : nl.x), t0, t1);
+        float p0 = ptx::ex2(t0), p1 = ptx::ex2(t1);
+        if (kMask) {
+          const int col = 32 * ch + x;
+          if (col < lo || col >= hi) p0 = 0.f;
+          if (col + 1 < lo || col + 1 >= hi) p1 = 0.f;
+        }
+        pr[16 * ch + 2 * e + u] = ptx::f2_pack(p0, p1);
+        w[2 * e + u] = ptx::pack_bf16x2(p0, p1);
+      }
+    }
+    ptx::tmem_st16(tS + 16 * ch, w);
+  }
+}
+
+// dkv: dS from dP and P, written over dP as bf16.
+template <bool kMask>
+__device__ __forceinline__ void dkv_ds(uint32_t tP, const ulonglong2* stat, int lo, int hi, const Half& pr) {
+  uint32_t a[32], b[32];
+  load_half(tP, a, b);
+#pragma unroll
+  for (int ch = 0; ch < 2; ++ch) {
+    uint32_t w[16];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const ulonglong2 nd = stat[32 + 8 * ch + e];  // four columns of -D
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int x = 4 * e + 2 * u;
+        float s0, s1;
+        ptx::f2_unpack(
+            ptx::f2_mul(pr[16 * ch + 2 * e + u], ptx::f2_add(pair_of(ch ? b : a, x), u ? nd.y : nd.x)), s0, s1);
+        if (kMask) {
+          const int col = 32 * ch + x;
+          if (col < lo || col >= hi) s0 = 0.f;
+          if (col + 1 < lo || col + 1 >= hi) s1 = 0.f;
+        }
+        w[2 * e + u] = ptx::pack_bf16x2(s0, s1);
+      }
+    }
+    ptx::tmem_st16(tP + 16 * ch, w);
+  }
+}
+
+// dq: dS from dP and P (a lane's query against 64 keys), written over S as bf16.
+template <bool kMask>
+__device__ __forceinline__ void dq_ds(uint32_t tP, uint32_t tS, uint64_t nd2, int hi, const Half& pr) {
+  uint32_t a[32], b[32];
+  load_half(tP, a, b);
+#pragma unroll
+  for (int ch = 0; ch < 2; ++ch) {
+    uint32_t w[16];
+#pragma unroll
+    for (int x = 0; x < 16; ++x) {
+      float s0, s1;
+      ptx::f2_unpack(ptx::f2_mul(pr[16 * ch + x], ptx::f2_add(pair_of(ch ? b : a, 2 * x), nd2)), s0, s1);
+      if (kMask) {
+        if (32 * ch + 2 * x >= hi) s0 = 0.f;
+        if (32 * ch + 2 * x + 1 >= hi) s1 = 0.f;
+      }
+      w[x] = ptx::pack_bf16x2(s0, s1);
+    }
+    ptx::tmem_st16(tS + 16 * ch, w);
+  }
+}
+
 // ---------------------------------------------------------------- row statistics
 //
 // Per query row -lse log2(e) and -D, in the tiles the two kernels read: rows past the
@@ -603,69 +693,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                            p.timeout_ns)))
         break;
       ptx::tc_fence_after();
-      {
-        uint32_t a[32], b[32];
-        load_half(tSh, a, b);
-#pragma unroll
-        for (int ch = 0; ch < 2; ++ch) {
-          uint32_t w[16];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const ulonglong2 nl = stat[8 * ch + e];  // four columns of -lse log2(e)
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int x = 4 * e + 2 * u;
-              const uint64_t s2 = ch ? ptx::f2_pack(__uint_as_float(b[x]), __uint_as_float(b[x + 1]))
-                                     : ptx::f2_pack(__uint_as_float(a[x]), __uint_as_float(a[x + 1]));
-              float t0, t1;
-              ptx::f2_unpack(ptx::f2_fma(s2, c2, u ? nl.y : nl.x), t0, t1);
-              float p0 = ptx::ex2(t0), p1 = ptx::ex2(t1);
-              if (mk) {
-                const int col = 32 * ch + x;
-                if (col < lo || col >= hi) p0 = 0.f;
-                if (col + 1 < lo || col + 1 >= hi) p1 = 0.f;
-              }
-              pr[16 * ch + 2 * e + u] = ptx::f2_pack(p0, p1);
-              w[2 * e + u] = ptx::pack_bf16x2(p0, p1);
-            }
-          }
-          ptx::tmem_st16(tSh + 16 * ch, w);
-        }
-      }
+      if (mk)
+        dkv_p<true>(tSh, stat, c2, lo, hi, pr);
+      else
+        dkv_p<false>(tSh, stat, c2, lo, hi, pr);
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
       ptx::mbar_arrive(bar(kDkvPFull));
 
       if (!(ok = warp_wait(bar(kDkvDpFull), i & 1, abort_flag, p.timeout_ns))) break;
       ptx::tc_fence_after();
-      {
-        uint32_t a[32], b[32];
-        load_half(tPh, a, b);
-#pragma unroll
-        for (int ch = 0; ch < 2; ++ch) {
-          uint32_t w[16];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const ulonglong2 nd = stat[32 + 8 * ch + e];  // four columns of -D
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int x = 4 * e + 2 * u;
-              const uint64_t d2 = ch ? ptx::f2_pack(__uint_as_float(b[x]), __uint_as_float(b[x + 1]))
-                                     : ptx::f2_pack(__uint_as_float(a[x]), __uint_as_float(a[x + 1]));
-              float s0, s1;
-              ptx::f2_unpack(ptx::f2_mul(pr[16 * ch + 2 * e + u], ptx::f2_add(d2, u ? nd.y : nd.x)), s0,
-                             s1);
-              if (mk) {
-                const int col = 32 * ch + x;
-                if (col < lo || col >= hi) s0 = 0.f;
-                if (col + 1 < lo || col + 1 >= hi) s1 = 0.f;
-              }
-              w[2 * e + u] = ptx::pack_bf16x2(s0, s1);
-            }
-          }
-          ptx::tmem_st16(tPh + 16 * ch, w);
-        }
-      }
+      if (mk)
+        dkv_ds<true>(tPh, stat, lo, hi, pr);
+      else
+        dkv_ds<false>(tPh, stat, lo, hi, pr);
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
       ptx::mbar_arrive(bar(kDkvDsFull));
@@ -956,27 +997,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!(ok = warp_wait(bar(kDqDpFull), j & 1, abort_flag, p.timeout_ns))) break;
       ptx::tc_fence_after();
-      {
-        uint32_t a[32], b[32];
-        load_half(tPh, a, b);
-#pragma unroll
-        for (int ch = 0; ch < 2; ++ch) {
-          uint32_t w[16];
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            const uint64_t d2 = ch ? ptx::f2_pack(__uint_as_float(b[2 * x]), __uint_as_float(b[2 * x + 1]))
-                                   : ptx::f2_pack(__uint_as_float(a[2 * x]), __uint_as_float(a[2 * x + 1]));
-            float s0, s1;
-            ptx::f2_unpack(ptx::f2_mul(pr[16 * ch + x], ptx::f2_add(d2, nd2)), s0, s1);
-            if (mk) {
-              if (32 * ch + 2 * x >= hi) s0 = 0.f;
-              if (32 * ch + 2 * x + 1 >= hi) s1 = 0.f;
-            }
-            w[x] = ptx::pack_bf16x2(s0, s1);
-          }
-          ptx::tmem_st16(tSh + 16 * ch, w);
-        }
-      }
+      if (mk)
+        dq_ds<true>(tPh, tSh, nd2, hi, pr);
+      else
+        dq_ds<false>(tPh, tSh, nd2, hi, pr);
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
       ptx::mbar_arrive(bar(kDqDsFull));
