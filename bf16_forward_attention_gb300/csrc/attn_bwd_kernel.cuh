@@ -27,7 +27,7 @@
 // cost 3 more products for less than a factor of 2 in the final error.
 //
 // Both kernels: 384 threads. Warp 0: TMA producer. Warp 1: TMEM allocation and
-// the single tcgen05.mma issuer. Warps 2-3: check of the tiles where some pairs
+// the tcgen05.mma issue (one elected lane, in warp-uniform code). Warps 2-3: check of the tiles where some pairs
 // are hidden (see check_rows / check_keys). Warps 4-7 and 8-11: softmax, each
 // thread one TMEM lane (a key in dkv, a query in dq) and one 64-column half.
 // Every wait is bounded, as in the forward kernel.
@@ -133,6 +133,20 @@ __device__ __forceinline__ void load_half(uint32_t taddr, uint32_t (&a)[32], uin
   ptx::reg_fence32(b);
 }
 
+// D = A B^T over head_dim, both K-major in shared memory: 8 MMAs of K = 16 (the whole
+// warp issues; see issue_s for the offsets).
+template <int... kK>
+__device__ __forceinline__ void issue_first_seq(uint32_t tmem_d, uint32_t a_lo, uint32_t b_lo,
+                                                std::integer_sequence<int, kK...>) {
+  constexpr uint32_t idesc = idesc_bf16(kTile, kTile, 0);
+  (ptx::mma_ss_warp<((kK >> 2) << 10) + ((kK & 3) << 1), ((kK >> 2) << 10) + ((kK & 3) << 1)>(
+       tmem_d, a_lo, b_lo, kDescHi, idesc, kK > 0 ? 1u : 0u),
+   ...);
+}
+__device__ __forceinline__ void issue_first(uint32_t tmem_d, uint32_t a_lo, uint32_t b_lo) {
+  issue_first_seq(tmem_d, a_lo, b_lo, std::make_integer_sequence<int, 8>{});
+}
+
 // acc += A[tmem: 128 x 128 bf16] * B[smem, MN-major]: 8 MMAs of K = 16. A's columns
 // 0..63 sit packed at tmem_a, columns 64..127 at tmem_a + 64 (each softmax
 // warpgroup writes its half over the first half of the columns that it read).
@@ -141,7 +155,7 @@ __device__ __forceinline__ void issue_second_seq(uint32_t tmem_d, uint32_t tmem_
                                                  uint32_t accumulate,
                                                  std::integer_sequence<int, kK...>) {
   constexpr uint32_t idesc = idesc_bf16(kTile, kD, 1);
-  (ptx::mma_ts_imm<(kK < 4 ? 8 * kK : 64 + 8 * (kK - 4)), (kK << 7)>(
+  (ptx::mma_ts_warp<(kK < 4 ? 8 * kK : 64 + 8 * (kK - 4)), (kK << 7)>(
        tmem_d, tmem_a, b_lo, kDescHi, idesc, kK == 0 ? accumulate : 1u),
    ...);
 }
@@ -491,7 +505,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kDkvOffSlot + 4);
   int* poison_q = reinterpret_cast<int*>(smem + kDkvOffPoison);
   auto bar = [&](int i) -> uint32_t { return sbase + kDkvOffBar + 8u * static_cast<uint32_t>(i); };
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (Through a shuffle, so that the compiler knows it to be the same on every lane.)
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   constexpr bool kCheck = kCausal || kVarlen;
 
   const Seq s = seq_of<kCausal, kVarlen, false>(p, static_cast<int>(blockIdx.x));
@@ -578,13 +593,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA issuer
-    if (lane == 0 && rg.n > 0) {
+    // ---------------------------------------------------------------- MMA issuer (whole warp)
+    if (rg.n > 0) {
       const uint32_t k_desc = desc_lo(sbase + kDkvOffK, 16), v_desc = desc_lo(sbase + kDkvOffV, 16);
       auto q_tile = [&](int i) -> uint32_t { return sbase + kDkvOffQ + (i % kDkvStages) * kTileBytes; };
       auto o_tile = [&](int i) -> uint32_t { return sbase + kDkvOffO + (i % kDkvStages) * kTileBytes; };
       auto wait = [&](int b, uint32_t par) -> bool {
-        const bool r = wait_bounded(bar(b), par & 1, abort_flag, p.timeout_ns, true);
+        const bool r = warp_wait(bar(b), par & 1, abort_flag, p.timeout_ns);
         ptx::tc_fence_after();
         return r;
       };
@@ -595,18 +610,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait(kDkvQFull + i % kDkvStages, i / kDkvStages)) return false;
         if (kCheck && masked((rg.first_qt + (rg.t0 + i) % rg.per) * kTile)) {
           if (!wait(kDkvOFull + i % kDkvStages, i / kDkvStages)) return false;
-          ptx::mbar_arrive(bar(kDkvLanded));
+          if (lane == 0) ptx::mbar_arrive(bar(kDkvLanded));
           if (!wait(kDkvChecked, checks)) return false;
           ++checks;
         }
-        issue_s(tS, k_desc, desc_lo(q_tile(i), 16));
-        ptx::mma_commit(bar(kDkvSFull));
+        issue_first(tS, k_desc, desc_lo(q_tile(i), 16));
+        ptx::mma_commit_warp(bar(kDkvSFull));
         return true;
       };
       auto do_dp = [&](int i) -> bool {
         if (!wait(kDkvOFull + i % kDkvStages, i / kDkvStages)) return false;
-        issue_s(tP, v_desc, desc_lo(o_tile(i), 16));
-        ptx::mma_commit(bar(kDkvDpFull));
+        issue_first(tP, v_desc, desc_lo(o_tile(i), 16));
+        ptx::mma_commit_warp(bar(kDkvDpFull));
         return true;
       };
       bool ok = wait(kDkvKV, 0) && do_s(0) && do_dp(0);
@@ -614,15 +629,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool more = i + 1 < rg.n;
         if (!(ok = wait(kDkvPFull, i))) break;
         issue_second(tV, tS, desc_lo(o_tile(i), kHalfBytes), i > 0);
-        ptx::mma_commit(bar(kDkvOEmpty + i % kDkvStages));
+        ptx::mma_commit_warp(bar(kDkvOEmpty + i % kDkvStages));
         if (more && !(ok = do_s(i + 1))) break;
         if (!(ok = wait(kDkvDsFull, i))) break;
         issue_second(tK, tP, desc_lo(q_tile(i), kHalfBytes), i > 0);
-        ptx::mma_commit(bar(kDkvQEmpty + i % kDkvStages));
+        ptx::mma_commit_warp(bar(kDkvQEmpty + i % kDkvStages));
         if (more && !(ok = do_dp(i + 1))) break;
       }
-      if (ok) ptx::mma_commit(bar(kDkvAcc));
-      ptx::mma_commit(bar(kDkvDrain));
+      if (ok) ptx::mma_commit_warp(bar(kDkvAcc));
+      ptx::mma_commit_warp(bar(kDkvDrain));
       wait_bounded(bar(kDkvDrain), 0, abort_flag, p.timeout_ns, false);
     }
     __syncwarp();
@@ -678,8 +693,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tSh = tS + lane_base + 64 * g, tPh = tP + lane_base + 64 * g;
     const uint64_t c2 = ptx::f2_pack(p.c, p.c);
     bool ok = true;
-    for (int i = 0; i < rg.n; ++i) {
-      const int q0 = (rg.first_qt + (rg.t0 + i) % rg.per) * kTile;
+    int q0 = rg.n > 0 ? (rg.first_qt + rg.t0 % rg.per) * kTile : 0;  // the tile's first query
+    const int q_last = (rg.first_qt + rg.per - 1) * kTile;           // of a head
+    for (int i = 0; i < rg.n; ++i, q0 = q0 == q_last ? rg.first_qt * kTile : q0 + kTile) {
       const bool mk = masked(q0);
       // The columns of this half that this key is visible to: [lo, hi).
       const int lo = kCausal ? k0 + row - off - q0 - 64 * g : 0;
@@ -789,7 +805,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kDqOffSlot + 4);
   int* poison_k = reinterpret_cast<int*>(smem + kDqOffPoison);
   auto bar = [&](int i) -> uint32_t { return sbase + kDqOffBar + 8u * static_cast<uint32_t>(i); };
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (Through a shuffle, so that the compiler knows it to be the same on every lane.)
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   constexpr bool kCheck = kCausal || kVarlen;
   constexpr int kNever = 0x7FFFFFFF;
 
@@ -875,29 +892,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA issuer
-    if (lane == 0 && n > 0) {
+    // ---------------------------------------------------------------- MMA issuer (whole warp)
+    if (n > 0) {
       const uint32_t q_desc = desc_lo(sbase + kDqOffQ, 16), o_desc = desc_lo(sbase + kDqOffO, 16);
       auto k_tile = [&](int j) -> uint32_t { return sbase + kDqOffK + (j % kDqKStages) * kTileBytes; };
       auto v_tile = [&](int j) -> uint32_t { return sbase + kDqOffV + (j % kDqVStages) * kTileBytes; };
       auto wait = [&](int b, uint32_t par) -> bool {
-        const bool r = wait_bounded(bar(b), par & 1, abort_flag, p.timeout_ns, true);
+        const bool r = warp_wait(bar(b), par & 1, abort_flag, p.timeout_ns);
         ptx::tc_fence_after();
         return r;
       };
       const int jm = max(0, first_masked - t0);  // first masked tile of this CTA's part
       auto do_s = [&](int j) -> bool {
         if (!wait(kDqKFull + j % kDqKStages, j / kDqKStages)) return false;
-        issue_s(tmem + 128 * (j & 1), q_desc, desc_lo(k_tile(j), 16));
-        ptx::mma_commit(bar(kDqSFull + (j & 1)));
-        if (kCheck && masked(j)) ptx::mbar_arrive(bar(kDqLanded + (j - jm)));
+        issue_first(tmem + 128 * (j & 1), q_desc, desc_lo(k_tile(j), 16));
+        ptx::mma_commit_warp(bar(kDqSFull + (j & 1)));
+        if (kCheck && masked(j) && lane == 0) ptx::mbar_arrive(bar(kDqLanded + (j - jm)));
         return true;
       };
       auto do_dp = [&](int j) -> bool {
         if (!wait(kDqVFull + j % kDqVStages, j / kDqVStages)) return false;
-        issue_s(tP, o_desc, desc_lo(v_tile(j), 16));
-        ptx::mma_commit(bar(kDqDpFull));
-        ptx::mma_commit(bar(kDqVEmpty + j % kDqVStages));
+        issue_first(tP, o_desc, desc_lo(v_tile(j), 16));
+        ptx::mma_commit_warp(bar(kDqDpFull));
+        ptx::mma_commit_warp(bar(kDqVEmpty + j % kDqVStages));
         return true;
       };
       bool ok = wait(kDqQ, 0) && do_s(0) && do_dp(0) && (n == 1 || do_s(1));
@@ -906,11 +923,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j + 1 < n && !(ok = do_dp(j + 1))) break;
         if (kCheck && masked(j) && !(ok = wait(kDqChecked + (j - jm), 0))) break;
         issue_second(tQ, tmem + 128 * (j & 1), desc_lo(k_tile(j), kHalfBytes), j > 0);
-        ptx::mma_commit(bar(kDqKEmpty + j % kDqKStages));
+        ptx::mma_commit_warp(bar(kDqKEmpty + j % kDqKStages));
         if (j + 2 < n && !(ok = do_s(j + 2))) break;
       }
-      if (ok) ptx::mma_commit(bar(kDqAcc));
-      ptx::mma_commit(bar(kDqDrain));
+      if (ok) ptx::mma_commit_warp(bar(kDqAcc));
+      ptx::mma_commit_warp(bar(kDqDrain));
       wait_bounded(bar(kDqDrain), 0, abort_flag, p.timeout_ns, false);
     }
     __syncwarp();

@@ -274,6 +274,47 @@ __device__ __forceinline__ void mma_ts_imm(uint32_t d_tmem, uint32_t a_tmem, uin
       : "memory");
 }
 
+// The same two MMAs for a warp whose 32 lanes execute them together: one elected lane
+// issues (always the same one). In warp-uniform code the compiler keeps descriptors
+// and addresses in uniform registers; issued from a lane-0 branch each operand is
+// first moved there, and back-to-back 128 x 128 x 16 MMAs take 89 cycles each
+// instead of the tensor pipe's 64.
+template <uint32_t kAOff, uint32_t kBOff>
+__device__ __forceinline__ void mma_ss_warp(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .b32 al, bl;\n\t.reg .b64 ad, bd;\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "add.u32 al, %1, %6;\n\tadd.u32 bl, %2, %7;\n\t"
+      "mov.b64 ad, {al, %3};\n\tmov.b64 bd, {bl, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "n"(kAOff), "n"(kBOff)
+      : "memory");
+}
+
+template <uint32_t kAColOff, uint32_t kBOff>
+__device__ __forceinline__ void mma_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t hi,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .b32 at, bl;\n\t.reg .b64 bd;\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "add.u32 at, %1, %6;\n\tadd.u32 bl, %2, %7;\n\t"
+      "mov.b64 bd, {bl, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [at], bd, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "n"(kAColOff), "n"(kBOff)
+      : "memory");
+}
+
+// Arrive (once) on `bar` when every MMA issued so far by that lane is done.
+__device__ __forceinline__ void mma_commit_warp(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      : "memory");
+}
+
 // Arrive (once) on `bar` when every tcgen05 op issued so far by this thread is done.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile(
