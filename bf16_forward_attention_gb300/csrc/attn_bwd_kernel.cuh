@@ -133,20 +133,6 @@ __device__ __forceinline__ void load_half(uint32_t taddr, uint32_t (&a)[32], uin
   ptx::reg_fence32(b);
 }
 
-// D = A B^T over head_dim, both K-major in shared memory: 8 MMAs of K = 16 (the whole
-// warp issues; see issue_s for the offsets).
-template <int... kK>
-__device__ __forceinline__ void issue_first_seq(uint32_t tmem_d, uint32_t a_lo, uint32_t b_lo,
-                                                std::integer_sequence<int, kK...>) {
-  constexpr uint32_t idesc = idesc_bf16(kTile, kTile, 0);
-  (ptx::mma_ss_warp<((kK >> 2) << 10) + ((kK & 3) << 1), ((kK >> 2) << 10) + ((kK & 3) << 1)>(
-       tmem_d, a_lo, b_lo, kDescHi, idesc, kK > 0 ? 1u : 0u),
-   ...);
-}
-__device__ __forceinline__ void issue_first(uint32_t tmem_d, uint32_t a_lo, uint32_t b_lo) {
-  issue_first_seq(tmem_d, a_lo, b_lo, std::make_integer_sequence<int, 8>{});
-}
-
 // acc += A[tmem: 128 x 128 bf16] * B[smem, MN-major]: 8 MMAs of K = 16. A's columns
 // 0..63 sit packed at tmem_a, columns 64..127 at tmem_a + 64 (each softmax
 // warpgroup writes its half over the first half of the columns that it read).
@@ -614,13 +600,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!wait(kDkvChecked, checks)) return false;
           ++checks;
         }
-        issue_first(tS, k_desc, desc_lo(q_tile(i), 16));
+        issue_s(tS, k_desc, desc_lo(q_tile(i), 16));
         ptx::mma_commit_warp(bar(kDkvSFull));
         return true;
       };
       auto do_dp = [&](int i) -> bool {
         if (!wait(kDkvOFull + i % kDkvStages, i / kDkvStages)) return false;
-        issue_first(tP, v_desc, desc_lo(o_tile(i), 16));
+        issue_s(tP, v_desc, desc_lo(o_tile(i), 16));
         ptx::mma_commit_warp(bar(kDkvDpFull));
         return true;
       };
@@ -905,14 +891,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int jm = max(0, first_masked - t0);  // first masked tile of this CTA's part
       auto do_s = [&](int j) -> bool {
         if (!wait(kDqKFull + j % kDqKStages, j / kDqKStages)) return false;
-        issue_first(tmem + 128 * (j & 1), q_desc, desc_lo(k_tile(j), 16));
+        issue_s(tmem + 128 * (j & 1), q_desc, desc_lo(k_tile(j), 16));
         ptx::mma_commit_warp(bar(kDqSFull + (j & 1)));
         if (kCheck && masked(j) && lane == 0) ptx::mbar_arrive(bar(kDqLanded + (j - jm)));
         return true;
       };
       auto do_dp = [&](int j) -> bool {
         if (!wait(kDqVFull + j % kDqVStages, j / kDqVStages)) return false;
-        issue_first(tP, o_desc, desc_lo(v_tile(j), 16));
+        issue_s(tP, o_desc, desc_lo(v_tile(j), 16));
         ptx::mma_commit_warp(bar(kDqDpFull));
         ptx::mma_commit_warp(bar(kDqVEmpty + j % kDqVStages));
         return true;

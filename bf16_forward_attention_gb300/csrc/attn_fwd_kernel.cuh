@@ -8,7 +8,8 @@
 // One CTA owns two 128-row query tiles of one (batch, head) and streams every
 // 128-key tile of K and V through a 4-stage shared-memory ring. Roles (warps):
 //   warp 0      TMA producer: Q tiles once, then K_0, V_0, K_1, V_1, ...
-//   warp 1      TMEM allocator and the single tcgen05.mma issuer
+//   warp 1      TMEM allocator and the tcgen05.mma issuer (one elected
+//               lane, in warp-uniform code)
 //   warps 2-3   causal and variable-length variants: check V of the key tiles
 //               where some row hides keys for NaN / Inf (see "V check" below);
 //               otherwise idle (they complete the first warpgroup)
@@ -277,7 +278,7 @@ template <int... kK>
 __device__ __forceinline__ void issue_s_seq(uint32_t tmem_d, uint32_t q_lo, uint32_t k_lo,
                                             std::integer_sequence<int, kK...>) {
   constexpr uint32_t idesc = idesc_bf16(kBM, kBN, 0);
-  (ptx::mma_ss_imm<((kK >> 2) << 10) + ((kK & 3) << 1), ((kK >> 2) << 10) + ((kK & 3) << 1)>(
+  (ptx::mma_ss_warp<((kK >> 2) << 10) + ((kK & 3) << 1), ((kK >> 2) << 10) + ((kK & 3) << 1)>(
        tmem_d, q_lo, k_lo, kDescHi, idesc, kK > 0 ? 1u : 0u),
    ...);
 }
@@ -298,9 +299,9 @@ __device__ __forceinline__ void issue_pv_seq(uint32_t tmem_o, uint32_t tmem_p, u
                                              uint32_t accumulate,
                                              std::integer_sequence<int, kK...>) {
   constexpr uint32_t idesc = idesc_bf16(kBM, kD, 1);
-  ((ptx::mma_ts_imm<16 * kK, (kK << 7)>(tmem_o, tmem_p, v_lo, kDescHi, idesc,
+  ((ptx::mma_ts_warp<16 * kK, (kK << 7)>(tmem_o, tmem_p, v_lo, kDescHi, idesc,
                                          kK == 0 ? accumulate : 1u),
-    ptx::mma_ts_imm<16 * kK + 8, (kK << 7)>(tmem_o, tmem_p, v_lo, kDescHi, idesc, 1u)),
+    ptx::mma_ts_warp<16 * kK + 8, (kK << 7)>(tmem_o, tmem_p, v_lo, kDescHi, idesc, 1u)),
    ...);
 }
 
@@ -319,8 +320,8 @@ __device__ __forceinline__ void issue_pv_chunks(uint32_t tmem_o, uint32_t tmem_p
   for (int k = 0; k < n; ++k) {
     const uint32_t a = tmem_p + 16u * static_cast<uint32_t>(k);
     const uint32_t b = v_lo + (static_cast<uint32_t>(k) << 7);
-    ptx::mma_ts_imm<0, 0>(tmem_o, a, b, kDescHi, idesc, k == 0 ? accumulate : 1u);
-    ptx::mma_ts_imm<8, 0>(tmem_o, a, b, kDescHi, idesc, 1u);
+    ptx::mma_ts_warp<0, 0>(tmem_o, a, b, kDescHi, idesc, k == 0 ? accumulate : 1u);
+    ptx::mma_ts_warp<8, 0>(tmem_o, a, b, kDescHi, idesc, 1u);
   }
 }
 
@@ -801,7 +802,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   static_assert(!kPair || (!kPartial && !kCausal && !kVarlen && !kPersist), "pair: base path only");
   static_assert(kShort == 0 || (kPersist && kShort <= 2), "short: a persistent variant");
   static_assert(!kLse || (!kPartial && !kPair), "log-sum-exp: whole key range per CTA");
-  const int warp = threadIdx.x >> 5;
+  // (Through a shuffle, so that the compiler knows it to be the same on every lane.)
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
   // A key limit per row (rising along the causal diagonal, or the sequence's
   // key count) selects pass-A masking in every tile.
@@ -982,12 +984,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else if (warp == 1) {
-      // ------------------------------------------------------------ MMA issuer
-      if (lane == 0) {
+      // ------------------------------------------------------------ MMA issuer (whole warp)
+      {
         if constexpr (kPersist) {
           auto ring_wait = [&](int it) -> bool {
-            const bool r = wait_bounded(bar(kBarKvFull + it % kStages), (it / kStages) & 1, abort_flag,
-                                        p.timeout_ns, true);
+            const bool r = warp_wait(bar(kBarKvFull + it % kStages), (it / kStages) & 1, abort_flag, p.timeout_ns);
             ptx::tc_fence_after();
             return r;
           };
@@ -1005,28 +1006,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           int ktile = 0;  // key tiles of the items before this one (S and P phases)
           for (int item = blockIdx.x, iter = 0; ok && item < p.n_items; item += gridDim.x, ++iter) {
             const int n_kv = work_of<kCausal, kVarlen>(p, item).n_kv;
-            if (!(ok = wait_bounded(bar(kBarQ), iter & 1, abort_flag, p.timeout_ns, true))) break;
+            if (!(ok = warp_wait(bar(kBarQ), iter & 1, abort_flag, p.timeout_ns))) break;
             ptx::tc_fence_after();
             if (!(ok = ring_wait(fill))) break;
             // S of the first key tile. The previous item's last P V MMAs, issued
             // before these on the same pipe, have read the S/P columns first.
             issue_s(tmem + kTmemS0, q0_desc, k_desc(fill));
-            if (!p.withhold_s0) ptx::mma_commit(bar(kBarSFull + 0));
+            if (!p.withhold_s0) ptx::mma_commit_warp(bar(kBarSFull + 0));
             issue_s(tmem + kTmemS0 + 128, q1_desc, k_desc(fill));
-            ptx::mma_commit(bar(kBarSFull + 1));
-            ptx::mma_commit(bar(kBarKvEmpty + fill % kStages));
-            if (n_kv == 1) ptx::mma_commit(bar(kBarQFree));  // the item's last S MMAs
+            ptx::mma_commit_warp(bar(kBarSFull + 1));
+            ptx::mma_commit_warp(bar(kBarKvEmpty + fill % kStages));
+            if (n_kv == 1) ptx::mma_commit_warp(bar(kBarQFree));  // the item's last S MMAs
             for (int j = 0; ok && j < n_kv; ++j) {
               const int vit = fill + 2 * j + 1;
               const int kit = fill + 2 * j + 2;
               const bool more = j + 1 < n_kv;
               if (!(ok = ring_wait(vit))) break;
-              if (!(ok = wait_bounded(bar(kBarPFull + 0), (ktile + j) & 1, abort_flag, p.timeout_ns, true)))
+              if (!(ok = warp_wait(bar(kBarPFull + 0), (ktile + j) & 1, abort_flag, p.timeout_ns)))
                 break;
               // The first P V of an item starts a fresh partial in O: the previous
               // item's epilogue must have read it.
               if (j == 0 && iter > 0 &&
-                  !(ok = wait_bounded(bar(kBarOFree + 0), (iter - 1) & 1, abort_flag, p.timeout_ns, true)))
+                  !(ok = warp_wait(bar(kBarOFree + 0), (iter - 1) & 1, abort_flag, p.timeout_ns)))
                 break;
               ptx::tc_fence_after();
               const uint32_t acc_o = (j % kFoldOf<kPartial>) != 0 ? 1u : 0u;  // partial continues
@@ -1037,29 +1038,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 issue_pv_chunks(tmem + kTmemO0, tmem + kTmemS0, v_desc(vit), acc_o, n_pv);
               else
                 issue_pv(tmem + kTmemO0, tmem + kTmemS0, v_desc(vit), acc_o);
-              if (!more) ptx::mma_commit(bar(kBarOFull + 0));
+              if (!more) ptx::mma_commit_warp(bar(kBarOFull + 0));
               if (more) {
                 if (!(ok = ring_wait(kit))) break;
                 issue_s(tmem + kTmemS0, q0_desc, k_desc(kit));
-                ptx::mma_commit(bar(kBarSFull + 0));
+                ptx::mma_commit_warp(bar(kBarSFull + 0));
               }
-              if (!(ok = wait_bounded(bar(kBarPFull + 1), (ktile + j) & 1, abort_flag, p.timeout_ns, true)))
+              if (!(ok = warp_wait(bar(kBarPFull + 1), (ktile + j) & 1, abort_flag, p.timeout_ns)))
                 break;
               if (j == 0 && iter > 0 &&
-                  !(ok = wait_bounded(bar(kBarOFree + 1), (iter - 1) & 1, abort_flag, p.timeout_ns, true)))
+                  !(ok = warp_wait(bar(kBarOFree + 1), (iter - 1) & 1, abort_flag, p.timeout_ns)))
                 break;
               ptx::tc_fence_after();
               if (kShort == 1 || (kShort == 2 && n_pv < 8))
                 issue_pv_chunks(tmem + kTmemO0 + 128, tmem + kTmemS0 + 128, v_desc(vit), acc_o, n_pv);
               else
                 issue_pv(tmem + kTmemO0 + 128, tmem + kTmemS0 + 128, v_desc(vit), acc_o);
-              ptx::mma_commit(bar(kBarKvEmpty + vit % kStages));
-              if (!more) ptx::mma_commit(bar(kBarOFull + 1));
+              ptx::mma_commit_warp(bar(kBarKvEmpty + vit % kStages));
+              if (!more) ptx::mma_commit_warp(bar(kBarOFull + 1));
               if (more) {
                 issue_s(tmem + kTmemS0 + 128, q1_desc, k_desc(kit));
-                ptx::mma_commit(bar(kBarSFull + 1));
-                ptx::mma_commit(bar(kBarKvEmpty + kit % kStages));
-                if (j + 2 == n_kv) ptx::mma_commit(bar(kBarQFree));  // the item's last S MMAs
+                ptx::mma_commit_warp(bar(kBarSFull + 1));
+                ptx::mma_commit_warp(bar(kBarKvEmpty + kit % kStages));
+                if (j + 2 == n_kv) ptx::mma_commit_warp(bar(kBarQFree));  // the item's last S MMAs
               }
             }
             fill += 2 * n_kv;
@@ -1070,11 +1071,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int n_kv = wk.n_kv;
           // Masked key tiles (key-limit variants): V is checked first.
           const int jm = kRowLimit ? first_masked_tile<kCausal>(wk) : n_kv;
-          bool ok = wait_bounded(bar(kBarQ), 0, abort_flag, p.timeout_ns, true);
+          bool ok = warp_wait(bar(kBarQ), 0, abort_flag, p.timeout_ns);
           ptx::tc_fence_after();
           auto ring_wait = [&](int it) -> bool {
-            const bool r = wait_bounded(bar(kBarKvFull + it % kStages), (it / kStages) & 1, abort_flag,
-                                        p.timeout_ns, true);
+            const bool r = warp_wait(bar(kBarKvFull + it % kStages), (it / kStages) & 1, abort_flag, p.timeout_ns);
             ptx::tc_fence_after();
             return r;
           };
@@ -1090,14 +1090,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok) ok = ring_wait(0);
           if (ok) {
             issue_s(tmem + kTmemS0, q0_desc, k_desc(0));
-            if (!p.withhold_s0) ptx::mma_commit(bar(kBarSFull + 0));
+            if (!p.withhold_s0) ptx::mma_commit_warp(bar(kBarSFull + 0));
             issue_s(tmem + kTmemS0 + 128, q1_desc, k_desc(0));
-            ptx::mma_commit(bar(kBarSFull + 1));
-            ptx::mma_commit(bar(kBarKvEmpty + 0));
+            ptx::mma_commit_warp(bar(kBarSFull + 1));
+            ptx::mma_commit_warp(bar(kBarKvEmpty + 0));
           }
+          auto arrive_landed = [&](int t) {
+            if (lane == 0) ptx::mbar_arrive(bar(kBarVLanded + t));
+          };
           // V of a masked key tile: tell the V check it has landed, one key tile
           // ahead of its P V products.
-          if (kRowLimit && ok && jm == 0 && (ok = ring_wait(1))) ptx::mbar_arrive(bar(kBarVLanded + 0));
+          if (kRowLimit && ok && jm == 0 && (ok = ring_wait(1))) arrive_landed(0);
           for (int j = 0; ok && j < n_kv; ++j) {
             const int vit = 2 * j + 1;
             const int kit = 2 * j + 2;
@@ -1106,40 +1109,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (kRowLimit && j >= jm && j - jm < kMaxMaskedTiles &&
                 !(ok = wait_bounded(bar(kBarVChk + (j - jm)), 0, abort_flag, p.timeout_ns, true)))
               break;
-            if (!(ok = wait_bounded(bar(kBarPFull + 0), j & 1, abort_flag, p.timeout_ns, true))) break;
+            if (!(ok = warp_wait(bar(kBarPFull + 0), j & 1, abort_flag, p.timeout_ns))) break;
             ptx::tc_fence_after();
             const uint32_t acc_o = (j % kFoldOf<kPartial>) != 0 ? 1u : 0u;  // partial continues
             issue_pv(tmem + kTmemO0, tmem + kTmemS0, v_desc(vit), acc_o);
-            if (!more) ptx::mma_commit(bar(kBarOFull + 0));
+            if (!more) ptx::mma_commit_warp(bar(kBarOFull + 0));
             if (more) {
               if (!(ok = ring_wait(kit))) break;
               issue_s(tmem + kTmemS0, q0_desc, k_desc(kit));
-              ptx::mma_commit(bar(kBarSFull + 0));
+              ptx::mma_commit_warp(bar(kBarSFull + 0));
             }
-            if (!(ok = wait_bounded(bar(kBarPFull + 1), j & 1, abort_flag, p.timeout_ns, true))) break;
+            if (!(ok = warp_wait(bar(kBarPFull + 1), j & 1, abort_flag, p.timeout_ns))) break;
             ptx::tc_fence_after();
             issue_pv(tmem + kTmemO0 + 128, tmem + kTmemS0 + 128, v_desc(vit), acc_o);
-            ptx::mma_commit(bar(kBarKvEmpty + vit % kStages));
-            if (!more) ptx::mma_commit(bar(kBarOFull + 1));
+            ptx::mma_commit_warp(bar(kBarKvEmpty + vit % kStages));
+            if (!more) ptx::mma_commit_warp(bar(kBarOFull + 1));
             if (more) {
               issue_s(tmem + kTmemS0 + 128, q1_desc, k_desc(kit));
-              ptx::mma_commit(bar(kBarSFull + 1));
-              ptx::mma_commit(bar(kBarKvEmpty + kit % kStages));
+              ptx::mma_commit_warp(bar(kBarSFull + 1));
+              ptx::mma_commit_warp(bar(kBarKvEmpty + kit % kStages));
               const int mnext = j + 1 - jm;  // the next key tile's index among the masked ones
               if (kRowLimit && mnext >= 0 && mnext < kMaxMaskedTiles) {
                 if (!(ok = ring_wait(vit + 2))) break;
-                ptx::mbar_arrive(bar(kBarVLanded + mnext));
+                arrive_landed(mnext);
               }
             }
           }
         }
         // Wait until every MMA issued so far has finished (immediate on the normal
         // path, where the softmax warps have already waited for the last ones).
-        ptx::mma_commit(bar(kBarDrain));
+        ptx::mma_commit_warp(bar(kBarDrain));
         const bool drained = wait_bounded(bar(kBarDrain), 0, abort_flag, p.timeout_ns, false);
         // Pair variant, rank 0: no MMA or copy uses the ring any more; rank 1 may
         // write its rows into it.
-        if (kPair && drained && ptx::cluster_ctarank() == 0)
+        if (kPair && drained && lane == 0 && ptx::cluster_ctarank() == 0)
           ptx::mbar_arrive_cluster(ptx::map_to_rank(bar(kBarPeerReady), 1));
       }
       __syncwarp();

@@ -244,38 +244,10 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
       : "memory");
 }
 
-// Same two MMAs with the descriptors built inside the asm statement from a
-// 32-bit lower word plus an immediate offset (16-byte units) and the shared upper
-// word, so that between MMAs no 64-bit descriptor occupies registers and each
-// MMA costs the issuing thread only a few instructions.
-template <uint32_t kAOff, uint32_t kBOff>
-__device__ __forceinline__ void mma_ss_imm(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
-                                          uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .b32 al, bl;\n\t.reg .b64 ad, bd;\n\t.reg .pred p;\n\t"
-      "add.u32 al, %1, %6;\n\tadd.u32 bl, %2, %7;\n\t"
-      "mov.b64 ad, {al, %3};\n\tmov.b64 bd, {bl, %3};\n\t"
-      "setp.ne.b32 p, %5, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %4, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "n"(kAOff), "n"(kBOff)
-      : "memory");
-}
-
-template <uint32_t kAColOff, uint32_t kBOff>
-__device__ __forceinline__ void mma_ts_imm(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t hi,
-                                          uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .b32 at, bl;\n\t.reg .b64 bd;\n\t.reg .pred p;\n\t"
-      "add.u32 at, %1, %6;\n\tadd.u32 bl, %2, %7;\n\t"
-      "mov.b64 bd, {bl, %3};\n\t"
-      "setp.ne.b32 p, %5, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [at], bd, %4, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "n"(kAColOff), "n"(kBOff)
-      : "memory");
-}
-
-// The same two MMAs for a warp whose 32 lanes execute them together: one elected lane
-// issues (always the same one). In warp-uniform code the compiler keeps descriptors
+// The same two MMAs, issued by a warp whose 32 lanes execute them together: one elected
+// lane (always the same one) issues. The descriptors are built inside the asm statement
+// from a 32-bit lower word plus an immediate offset (16-byte units) and the shared upper
+// word, so that between MMAs no 64-bit descriptor occupies registers. In warp-uniform code the compiler keeps descriptors
 // and addresses in uniform registers; issued from a lane-0 branch each operand is
 // first moved there, and back-to-back 128 x 128 x 16 MMAs take 89 cycles each
 // instead of the tensor pipe's 64.
