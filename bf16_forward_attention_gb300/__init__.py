@@ -8,7 +8,9 @@ there is no Python or CPU fallback - if the library is missing, calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import math
 import os
 
@@ -352,12 +354,17 @@ def _check_bf16(named, dim: int, form: str):
     one device."""
     import torch
 
+    tensor, bf16 = torch.Tensor, torch.bfloat16
+    first = None
     for name, t in named:
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda:
+        if not isinstance(t, tensor) or t.dtype != bf16 or not t.is_cuda:
             raise TypeError(f"{name} must be a bf16 CUDA tensor")
         if t.dim() != dim or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {form} tensor")
-        if t.device != named[0][1].device:
+        index = t.get_device()
+        if first is None:
+            first = index
+        elif index != first:
             raise ValueError(f"{name} must be on {named[0][0]}'s device")
 
 
@@ -393,10 +400,21 @@ def _call(fn, *args):
         raise AttnError(int(st), status_str(st))
 
 
-def _size(n: int) -> int:
+@functools.lru_cache(maxsize=4096)
+def _workspace_of(lib, entry: str, device: int, *sizes: int) -> int:
+    """Bytes that a *_workspace_bytes entry point asks for at these sizes. They depend on the
+    device's SM count beside the sizes, so they are looked up once."""
+    n = getattr(lib, entry)(*sizes)
     if n < 0:
         raise AttnError(int(n), status_str(int(n)))
     return int(n)
+
+
+def _here() -> int:
+    """The current CUDA device, -1 without one."""
+    import torch
+
+    return torch.cuda.current_device() if torch.cuda.is_available() else -1
 
 
 def attn_fwd_lse(q, k, v, *, causal: bool = False, layout: str = "bhsd",
@@ -414,7 +432,8 @@ def attn_fwd_lse(q, k, v, *, causal: bool = False, layout: str = "bhsd",
         raise ValueError("shape mismatch")
     if out is None:
         out = torch.empty_like(q)
-    _check_out(out, q)
+    else:
+        _check_out(out, q)
     lse = _lse_like(lse, (B, Hq, Sq), q.device)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
@@ -422,7 +441,7 @@ def attn_fwd_lse(q, k, v, *, causal: bool = False, layout: str = "bhsd",
         _call(load_library().attn_fwd_lse, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
               lse.data_ptr(), LAYOUTS[layout], B, Hq, Hkv, Sq, Sk, D, float(scale),
               ROUNDINGS[rounding], ATTN_FLAG_CAUSAL if causal else 0,
-              torch.cuda.current_stream(q.device).cuda_stream)
+              torch.cuda.current_stream().cuda_stream)
     return out, lse
 
 
@@ -443,7 +462,8 @@ def attn_fwd_varlen_lse(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, 
         raise ValueError("shape mismatch")
     if out is None:
         out = torch.empty_like(q)
-    _check_out(out, q)
+    else:
+        _check_out(out, q)
     lse = _lse_like(lse, (Hq, total_q), q.device)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
@@ -452,20 +472,20 @@ def attn_fwd_varlen_lse(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, 
               out.data_ptr(), lse.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(),
               cu_seqlens_q.numel() - 1, Hq, Hkv, total_q, total_k, int(max_seqlen_q), D,
               float(scale), ROUNDINGS[rounding], ATTN_FLAG_CAUSAL if causal else 0,
-              torch.cuda.current_stream(q.device).cuda_stream)
+              torch.cuda.current_stream().cuda_stream)
     return out, lse
 
 
 def bwd_workspace_bytes(B: int, Hq: int, Hkv: int, Sq: int, Sk: int, d: int = 128) -> int:
     """Device workspace attn_bwd needs on the current device."""
-    return _size(load_library().attn_bwd_workspace_bytes(B, Hq, Hkv, Sq, Sk, d))
+    return _workspace_of(load_library(), "attn_bwd_workspace_bytes", _here(), B, Hq, Hkv, Sq, Sk, d)
 
 
 def bwd_varlen_workspace_bytes(B: int, Hq: int, Hkv: int, total_q: int, total_k: int,
                                max_seqlen_q: int, max_seqlen_k: int, d: int = 128) -> int:
     """Device workspace attn_bwd_varlen needs on the current device."""
-    return _size(load_library().attn_bwd_varlen_workspace_bytes(
-        B, Hq, Hkv, total_q, total_k, max_seqlen_q, max_seqlen_k, d))
+    return _workspace_of(load_library(), "attn_bwd_varlen_workspace_bytes", _here(), B, Hq, Hkv, total_q,
+                         total_k, max_seqlen_q, max_seqlen_k, d)
 
 
 def _grads(q, k, v, dq, dk, dv, workspace, need: int):
@@ -482,7 +502,8 @@ def _grads(q, k, v, dq, dk, dv, workspace, need: int):
         got.append(g)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _check_workspace(workspace, q.device)
+    else:
+        _check_workspace(workspace, q.device)
     return (*got, workspace)
 
 
@@ -509,15 +530,17 @@ def attn_bwd(dout, q, k, v, out, lse, *, causal: bool = False, layout: str = "bh
     lse = _lse_like(lse, (B, Hq, Sq), q.device)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
+    lib = load_library()
     with _on_device(q.device):
-        dq, dk, dv, workspace = _grads(q, k, v, dq, dk, dv, workspace,
-                                       bwd_workspace_bytes(B, Hq, Hkv, Sq, Sk, D))
-        _call(load_library().attn_bwd, dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        dq, dk, dv, workspace = _grads(
+            q, k, v, dq, dk, dv, workspace,
+            _workspace_of(lib, "attn_bwd_workspace_bytes", q.get_device(), B, Hq, Hkv, Sq, Sk, D))
+        _call(lib.attn_bwd, dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
               out.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
               LAYOUTS[layout], B, Hq, Hkv, Sq, Sk, D, float(scale), ROUNDINGS[rounding],
               ATTN_FLAG_CAUSAL if causal else 0, workspace.data_ptr(),
               workspace.numel() * workspace.element_size(),
-              torch.cuda.current_stream(q.device).cuda_stream)
+              torch.cuda.current_stream().cuda_stream)
     return dq, dk, dv
 
 
@@ -544,24 +567,25 @@ def attn_bwd_varlen(dout, q, k, v, out, lse, cu_seqlens_q, cu_seqlens_k, max_seq
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     B = cu_seqlens_q.numel() - 1
+    lib = load_library()
     with _on_device(q.device):
         dq, dk, dv, workspace = _grads(
             q, k, v, dq, dk, dv, workspace,
-            bwd_varlen_workspace_bytes(B, Hq, Hkv, total_q, total_k, int(max_seqlen_q),
-                                       int(max_seqlen_k), D))
-        _call(load_library().attn_bwd_varlen, dout.data_ptr(), q.data_ptr(), k.data_ptr(),
+            _workspace_of(lib, "attn_bwd_varlen_workspace_bytes", q.get_device(), B, Hq, Hkv, total_q,
+                          total_k, int(max_seqlen_q), int(max_seqlen_k), D))
+        _call(lib.attn_bwd_varlen, dout.data_ptr(), q.data_ptr(), k.data_ptr(),
               v.data_ptr(), out.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(),
               dv.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, Hq, Hkv, total_q,
               total_k, int(max_seqlen_q), int(max_seqlen_k), D, float(scale), ROUNDINGS[rounding],
               ATTN_FLAG_CAUSAL if causal else 0, workspace.data_ptr(),
               workspace.numel() * workspace.element_size(),
-              torch.cuda.current_stream(q.device).cuda_stream)
+              torch.cuda.current_stream().cuda_stream)
     return dq, dk, dv
 
 
 def prefix_workspace_bytes(B: int, Hq: int, Hkv: int, Sq: int, Sp: int, cap: int, d: int = 128) -> int:
     """Device workspace attn_fwd_prefix needs on the current device."""
-    return _size(load_library().attn_fwd_prefix_workspace_bytes(B, Hq, Hkv, Sq, Sp, cap, d))
+    return _workspace_of(load_library(), "attn_fwd_prefix_workspace_bytes", _here(), B, Hq, Hkv, Sq, Sp, cap, d)
 
 
 def attn_fwd_prefix(q, k_prefix, v_prefix, k, v, seqlens, *, causal: bool = False,
@@ -604,21 +628,25 @@ def attn_fwd_prefix(q, k_prefix, v_prefix, k, v, seqlens, *, causal: bool = Fals
         raise ValueError("seqlens must be on q's device")
     if out is None:
         out = torch.empty_like(q)
-    _check_out(out, q)
+    else:
+        _check_out(out, q)
     lse = _lse_like(lse, (B, Hq, Sq), q.device)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
+    lib = load_library()
     with _on_device(q.device):
         if workspace is None:
-            workspace = torch.empty(prefix_workspace_bytes(B, Hq, Hkv, Sq, Sp, cap, D), dtype=torch.uint8,
-                                    device=q.device)
-        _check_workspace(workspace, q.device)
-        _call(load_library().attn_fwd_prefix, q.data_ptr(), k_prefix.data_ptr() if Sp else None,
+            need = _workspace_of(lib, "attn_fwd_prefix_workspace_bytes", q.get_device(), B, Hq, Hkv, Sq, Sp,
+                                 cap, D)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        else:
+            _check_workspace(workspace, q.device)
+        _call(lib.attn_fwd_prefix, q.data_ptr(), k_prefix.data_ptr() if Sp else None,
               v_prefix.data_ptr() if Sp else None, k.data_ptr(), v.data_ptr(), seqlens.data_ptr(),
               out.data_ptr(), lse.data_ptr(), LAYOUTS[layout], B, Hq, Hkv, Sq, Sp, cap, D,
               float(scale), ROUNDINGS[rounding], ATTN_FLAG_CAUSAL if causal else 0,
               workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-              torch.cuda.current_stream(q.device).cuda_stream)
+              torch.cuda.current_stream().cuda_stream)
     return out, lse
 
 
@@ -740,16 +768,17 @@ def attn_fwd_last_error() -> int:
     return load_library().attn_fwd_last_error()
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on_device(device):
     """The device context for a library call: none when `device` is already the
     current CUDA device (entering torch.cuda.device costs a few microseconds, a
     noticeable share of a small call)."""
-    import contextlib
-
     import torch
 
     if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
+        return _HERE
     return torch.cuda.device(device)
 
 
