@@ -81,6 +81,17 @@ int choose_splits(int64_t items, int64_t tiles, int64_t sms, int part) {
   return best;
 }
 
+// Causal schedule: heads whose tiles are launched longest first together, in groups of
+// one size whose streamed tensors (`bytes` a head) take at most 80 MiB of the 126 MiB
+// L2. A group's last tiles are short, so it fills the SMs that the next one's first
+// tiles leave; a small last group would start its longest tiles at the very end.
+int heads_together(int64_t heads, int64_t bytes) {
+  int64_t most = (int64_t(80) << 20) / (bytes > 0 ? bytes : 1);
+  if (most < 1) most = 1;
+  const int64_t groups = (heads + most - 1) / most;
+  return static_cast<int>((heads + groups - 1) / groups);
+}
+
 struct Plan {
   int64_t q_tiles, k_tiles;  // per sequence (grid)
   int64_t q_slots, k_slots;  // tile slots per head
@@ -174,11 +185,10 @@ int bwd_impl(const void* dout, const void* q, const void* k, const void* v, cons
   const int st = device_ready(dev);
   if (st != ATTN_OK) return st;
 
-  CUtensorMap tq, tk, tv, tdo, tdq, tdk, tdv;
+  CUtensorMap tq, tk, tv, tdo;
   if (!make_map(&tq, q, layout, rep, Hq, Sq, bwd::kTile) || !make_map(&tk, k, layout, rep, Hkv, Sk, bwd::kTile) ||
       !make_map(&tv, v, layout, rep, Hkv, Sk, bwd::kTile) ||
-      !make_map(&tdo, dout, layout, rep, Hq, Sq, bwd::kTile) || !make_map(&tdq, dq, layout, rep, Hq, Sq, 32) ||
-      !make_map(&tdk, dk, layout, rep, Hkv, Sk, 32) || !make_map(&tdv, dv, layout, rep, Hkv, Sk, 32))
+      !make_map(&tdo, dout, layout, rep, Hq, Sq, bwd::kTile))
     return ATTN_ERR_LAUNCH;
 
   char* ws = static_cast<char*>(workspace);
@@ -238,13 +248,13 @@ int bwd_impl(const void* dout, const void* q, const void* k, const void* v, cons
 
   p.BH = static_cast<int>(B * Hq);
   p.n_tiles = static_cast<int>(pl.q_tiles);
-  p.head_group = causal ? head_group_of(B * Hq, keys_per_head) : 1;
+  p.head_group = causal ? heads_together(B * Hq, 512 * keys_per_head * Hkv / Hq) : 1;
   p.n_splits = pl.dq_splits;
   p.part = dq_part;
   auto* dq_fn = varlen ? (causal ? bwd::attn_bwd_dq<true, true> : bwd::attn_bwd_dq<false, true>)
                        : (causal ? bwd::attn_bwd_dq<true, false> : bwd::attn_bwd_dq<false, false>);
   if (!launch(dq_fn, B * Hq * pl.q_tiles * pl.dq_splits, attn::kThreads, bwd::kDqSmem, cs, true, tq, tk, tv, tdo,
-              tdq, p))
+              p))
     return ATTN_ERR_LAUNCH;
   if (pl.dq_splits > 1) {
     jp.part = dq_part;
@@ -267,13 +277,13 @@ int bwd_impl(const void* dout, const void* q, const void* k, const void* v, cons
 
   p.BH = static_cast<int>(B * Hkv);
   p.n_tiles = static_cast<int>(pl.k_tiles);
-  p.head_group = causal ? head_group_of(B * Hkv, rows_per_head * (Hq / Hkv)) : 1;
+  p.head_group = causal ? heads_together(B * Hkv, 512 * rows_per_head * (Hq / Hkv)) : 1;
   p.n_splits = pl.dkv_splits;
   p.part = dkv_part;
   auto* dkv_fn = varlen ? (causal ? bwd::attn_bwd_dkv<true, true> : bwd::attn_bwd_dkv<false, true>)
                         : (causal ? bwd::attn_bwd_dkv<true, false> : bwd::attn_bwd_dkv<false, false>);
   if (!launch(dkv_fn, B * Hkv * pl.k_tiles * pl.dkv_splits, attn::kThreads, bwd::kDkvSmem, cs, true, tq, tk, tv,
-              tdo, tdk, tdv, p))
+              tdo, p))
     return ATTN_ERR_LAUNCH;
   if (pl.dkv_splits > 1) {
     jp.part = dkv_part;

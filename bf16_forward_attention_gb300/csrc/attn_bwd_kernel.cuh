@@ -56,7 +56,7 @@ struct BwdParams {
   int q_slots, k_slots;    // tile slots per head (see tile_slot)
   const float* stats;      // [head][slot][2][128]
   float* part;             // n_splits > 1: [split][result][head * slots][128][128] fp32
-  uint16_t *dq, *dk, *dv;  // results (plain stores; full tiles go through TMA)
+  uint16_t *dq, *dk, *dv;  // results
 };
 
 // Tile slots: a dense head has ceil(S / 128) tiles. A packed batch has no host copy
@@ -193,19 +193,18 @@ __device__ __forceinline__ size_t row_at(int layout, int batch, int H, int S, in
                       : (static_cast<size_t>(batch) * S + row) * H + head) * kD;
 }
 
-// A finished 128-column row of a result in TMEM -> bf16 in the staging tile (128-byte
-// swizzle) -> global memory: whole warps through TMA, a warp that holds the end
-// of a packed sequence row by row. `poison(col)`: the column is NaN. zero: no
-// product was formed, the result is 0. All lanes of the warp call it.
-template <bool kVarlen, typename F>
-__device__ __forceinline__ void store_result(uint32_t tacc, bool zero, float factor, int mode,
-                                             uint32_t stage, uint8_t* stage_ptr, int row, int wq, int lane,
-                                             const CUtensorMap* map, uint16_t* out, int layout, int batch,
-                                             int H, int S, int head, int base, int first, int len,
-                                             F poison) {
-  const float nan = __int_as_float(0x7FC00000);
+// kCols finished columns of a row of a result in TMEM -> bf16 in global memory (dst null:
+// a row past the end; its lane still takes part in the loads). A thread holds one row,
+// so its stores are 16 bytes of consecutive addresses each and need no staging.
+// `poison(col)`: the column is NaN; any: there is such a column. zero: no product
+// was formed, the result is 0.
+template <int kCols, typename F>
+__device__ __forceinline__ void store_row(uint32_t tacc, bool zero, float factor, int mode, uint16_t* dst,
+                                          bool any, F poison) {
+  const uint64_t f2 = ptx::f2_pack(factor, factor);
+  const uint32_t bias = mode == 1 ? 0x8000u : 0u;
 #pragma unroll
-  for (int ch = 0; ch < 4; ++ch) {
+  for (int ch = 0; ch < kCols / 32; ++ch) {
     uint32_t r[32];
     if (!zero) {
       ptx::tmem_ld32(tacc + 32 * ch, r);
@@ -213,44 +212,33 @@ __device__ __forceinline__ void store_result(uint32_t tacc, bool zero, float fac
 #pragma unroll
       for (int i = 0; i < 32; ++i) r[i] = 0;
     }
+    if (any) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      uint32_t w[4];
+      for (int i = 0; i < 32; ++i)
+        if (poison(32 * ch + i)) r[i] = 0x7FC00000u;
+    }
+    uint32_t w[16];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int col = 8 * u + 2 * i;
-        const float x0 = poison(32 * ch + col) ? nan : __uint_as_float(r[col]) * factor;
-        const float x1 = poison(32 * ch + col + 1) ? nan : __uint_as_float(r[col + 1]) * factor;
-        w[i] = round_bf16_bits(x0, mode) | (round_bf16_bits(x1, mode) << 16);
-      }
-      ptx::st_shared_v4(stage + chunk_at(row, 4 * ch + u), w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 16; ++i) {
+      float x0, x1;
+      ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), f2),
+                     x0, x1);
+      w[i] = mode == 0 ? round_pair_bf16_rtne(x0, x1) : round_pair_bf16(x0, x1, bias);
+    }
+    if (dst) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        reinterpret_cast<uint4*>(dst)[4 * ch + u] = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
     }
   }
-  ptx::fence_proxy_async_smem();
-  __syncwarp();
-  const int row0 = first + wq * 32;  // within the sequence
-  if (!kVarlen || row0 + 32 <= len) {
-    if (lane == 0 && row0 < len && dbg_ok(base + row0 < S)) {
-      int c1, c2;
-      tma_coords(layout, base + row0, head, c1, c2);
-      for (int hf = 0; hf < 2; ++hf)
-        ptx::tma_store_4d(map, stage + hf * kHalfBytes + wq * 32 * 128, 64 * hf, c1, c2, batch);
-      ptx::bulk_commit_group();
-      ptx::bulk_wait_group_0();
-    }
-  } else if (row0 + lane < len && dbg_ok(base + row0 + lane < S)) {
-    uint4* dst = reinterpret_cast<uint4*>(out + row_at(layout, batch, H, S, head, base + row0 + lane));
-    for (int c = 0; c < 16; ++c) dst[c] = *reinterpret_cast<const uint4*>(stage_ptr + chunk_at(row, c));
-  }
-  __syncwarp();
 }
 
 // The same row as fp32 into the split workspace (one of n_splits terms of a sum).
-template <typename F>
+template <int kCols, typename F>
 __device__ __forceinline__ void store_part(uint32_t tacc, bool zero, float* dst, F poison) {
   const float nan = __int_as_float(0x7FC00000);
 #pragma unroll 1
-  for (int ch = 0; ch < 8; ++ch) {
+  for (int ch = 0; ch < kCols / 16; ++ch) {
     uint32_t r[16];
     if (!zero) {
       ptx::tmem_ld16(tacc + 16 * ch, r);
@@ -457,7 +445,7 @@ constexpr int kDkvOffK = 0, kDkvOffV = kTileBytes, kDkvOffQ = 2 * kTileBytes,
               kDkvOffO = kDkvOffQ + kDkvStages * kTileBytes,
               kDkvOffStats = kDkvOffO + kDkvStages * kTileBytes,
               kDkvOffPoison = kDkvOffStats + kDkvStages * kStatFloats * 4,
-              kDkvOffBar = kDkvOffPoison + kD * 4, kDkvOffSlot = kDkvOffBar + kDkvBars * 8,
+              kDkvOffBar = kDkvOffPoison + kD * 4 + 16, kDkvOffSlot = kDkvOffBar + kDkvBars * 8,
               kDkvSmem = kDkvOffSlot + 8 + 1024;
 static_assert(kDkvSmem <= 232448, "shared memory budget (dkv)");
 
@@ -481,7 +469,6 @@ template <bool kCausal, bool kVarlen>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_bwd_dkv(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
-                 const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dv,
                  const BwdParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
@@ -490,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kDkvOffSlot);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kDkvOffSlot + 4);
   int* poison_q = reinterpret_cast<int*>(smem + kDkvOffPoison);
+  volatile int* poison_any = poison_q + kD;
   auto bar = [&](int i) -> uint32_t { return sbase + kDkvOffBar + 8u * static_cast<uint32_t>(i); };
   // (Through a shuffle, so that the compiler knows it to be the same on every lane.)
   const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -517,12 +505,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kDkvBars; ++i)
-      ptx::mbar_init(bar(i), (i == kDkvPFull || i == kDkvDsFull) ? 256 : 1);
+      ptx::mbar_init(bar(i), (i == kDkvPFull || i == kDkvDsFull) ? 8 : 1);
     *abort_flag = 0;
+    *poison_any = 0;
     ptx::fence_mbar_init();
     ptx::fence_proxy_async_smem();
   }
   if (threadIdx.x < kD) poison_q[threadIdx.x] = -1;
+  if (warp == 0 && lane == 0) {
+    ptx::prefetch_tmap(&tm_q);
+    ptx::prefetch_tmap(&tm_k);
+    ptx::prefetch_tmap(&tm_v);
+    ptx::prefetch_tmap(&tm_do);
+  }
   if (warp == 1) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), kTmemCols);
     ptx::tmem_relinquish();
@@ -660,7 +655,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             dirty = true;
           } else if (isnan(nl) || isnan(nd)) {
             clean_row(qt, r, [](int) {});
-            clean_row(ot, r, [&](int col) { atomicMax(&poison_q[col], q0 + r); });
+            clean_row(ot, r, [&](int col) {
+              atomicMax(&poison_q[col], q0 + r);
+              *poison_any = 1;
+            });
             dirty = true;
           }
         }
@@ -701,7 +699,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         dkv_p<false>(tSh, stat, c2, lo, hi, pr);
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
-      ptx::mbar_arrive(bar(kDkvPFull));
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(kDkvPFull));
 
       if (!(ok = warp_wait(bar(kDkvDpFull), i & 1, abort_flag, p.timeout_ns))) break;
       ptx::tc_fence_after();
@@ -711,7 +710,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         dkv_ds<false>(tPh, stat, lo, hi, pr);
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
-      ptx::mbar_arrive(bar(kDkvDsFull));
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(kDkvDsFull));
     }
     // ---- epilogue: warpgroup 0 stores dK, warpgroup 1 dV.
     if (ok && rg.n > 0) ok = warp_wait(bar(kDkvAcc), 0, abort_flag, p.timeout_ns);
@@ -723,16 +723,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int seen = kCausal ? max(0, k0 + row - off) : 0;
       auto poison = [&](int col) -> bool { return kCheck && g == 1 && poison_q[col] >= seen; };
       if (p.n_splits == 1) {
-        const int off_stage = g == 0 ? kDkvOffK : kDkvOffV;
-        store_result<kVarlen>(tacc, zero, g == 0 ? p.scale : 1.f, p.mode, sbase + off_stage,
-                              smem + off_stage, row, wq, lane, g == 0 ? &tm_dk : &tm_dv,
-                              g == 0 ? p.dk : p.dv, p.layout, s.batch, p.Hkv, p.Sk, s.head, s.k_base, k0,
-                              s.sk, poison);
+        const bool in = k0 + row < s.sk && dbg_ok(s.k_base + k0 + row < p.Sk);
+        uint16_t* dst = (g == 0 ? p.dk : p.dv) +
+                        row_at(p.layout, s.batch, p.Hkv, p.Sk, s.head, s.k_base + k0 + (in ? row : 0));
+        store_row<kD>(tacc, zero, g == 0 ? p.scale : 1.f, p.mode, in ? dst : nullptr,
+                      kCheck && g == 1 && *poison_any, poison);
       } else {
         const size_t slots = static_cast<size_t>(p.k_slots) * (kVarlen ? p.Hkv : p.BH);
         const size_t slot = static_cast<size_t>(s.slot_k) + static_cast<size_t>(s.head) * p.k_slots + s.tile;
         float* dst = p.part + (((static_cast<size_t>(s.split) * 2 + g) * slots + slot) * kTile + row) * kD;
-        store_part(tacc, zero, dst, poison);
+        store_part<kD>(tacc, zero, dst, poison);
       }
     }
   }
@@ -774,7 +774,7 @@ enum : int {
 };
 constexpr int kDqOffQ = 0, kDqOffO = kTileBytes, kDqOffK = 2 * kTileBytes,
               kDqOffV = kDqOffK + kDqKStages * kTileBytes,
-              kDqOffPoison = kDqOffV + kDqVStages * kTileBytes, kDqOffBar = kDqOffPoison + kD * 4,
+              kDqOffPoison = kDqOffV + kDqVStages * kTileBytes, kDqOffBar = kDqOffPoison + kD * 4 + 16,
               kDqOffSlot = kDqOffBar + kDqBars * 8, kDqSmem = kDqOffSlot + 8 + 1024;
 static_assert(kDqSmem <= 232448, "shared memory budget (dq)");
 
@@ -782,7 +782,7 @@ template <bool kCausal, bool kVarlen>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_bwd_dq(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
-                const __grid_constant__ CUtensorMap tm_dq, const BwdParams p) {
+                const BwdParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -790,6 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kDqOffSlot);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kDqOffSlot + 4);
   int* poison_k = reinterpret_cast<int*>(smem + kDqOffPoison);
+  volatile int* poison_any = poison_k + kD;
   auto bar = [&](int i) -> uint32_t { return sbase + kDqOffBar + 8u * static_cast<uint32_t>(i); };
   // (Through a shuffle, so that the compiler knows it to be the same on every lane.)
   const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -825,12 +826,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kv_head = s.head / p.group;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kDqBars; ++i) ptx::mbar_init(bar(i), i == kDqDsFull ? 256 : 1);
+    for (int i = 0; i < kDqBars; ++i) ptx::mbar_init(bar(i), i == kDqDsFull ? 8 : 1);
     *abort_flag = 0;
+    *poison_any = 0;
     ptx::fence_mbar_init();
     ptx::fence_proxy_async_smem();
   }
   if (threadIdx.x < kD) poison_k[threadIdx.x] = kNever;
+  if (warp == 0 && lane == 0) {
+    ptx::prefetch_tmap(&tm_q);
+    ptx::prefetch_tmap(&tm_k);
+    ptx::prefetch_tmap(&tm_v);
+    ptx::prefetch_tmap(&tm_do);
+  }
   if (warp == 1) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), kTmemCols);
     ptx::tmem_relinquish();
@@ -949,7 +957,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             acc = ptx::bf16x2_nonfinite_acc(x.z, ptx::bf16x2_nonfinite_acc(x.w, acc));
           }
           if (acc != 0) {
-            clean_row(kt, r, [&](int col) { atomicMin(&poison_k[col], first + r); });
+            clean_row(kt, r, [&](int col) {
+              atomicMin(&poison_k[col], first + r);
+              *poison_any = 1;
+            });
             dirty = true;
           }
         }
@@ -1006,23 +1017,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         dq_ds<false>(tPh, tSh, nd2, hi, pr);
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
-      ptx::mbar_arrive(bar(kDqDsFull));
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(kDqDsFull));
     }
-    // ---- epilogue: warpgroup 0 stores the rows.
+    // ---- epilogue: each warpgroup stores 64 columns of the rows.
     if (ok && n > 0) ok = warp_wait(bar(kDqAcc), 0, abort_flag, p.timeout_ns);
-    if (ok && g == 0) {
+    if (ok) {
       ptx::tc_fence_after();
-      const uint32_t tacc = tQ + lane_base;
-      auto poison = [&](int col) -> bool { return kCheck && poison_k[col] < limit; };
+      const uint32_t tacc = tQ + lane_base + 64 * g;
+      auto poison = [&](int col) -> bool { return kCheck && poison_k[64 * g + col] < limit; };
       if (p.n_splits == 1) {
-        store_result<kVarlen>(tacc, n == 0, p.scale, p.mode, sbase + kDqOffQ, smem + kDqOffQ, row, wq, lane,
-                              &tm_dq, p.dq, p.layout, s.batch, p.Hq, p.Sq, s.head, s.q_base, q0, s.sq,
-                              poison);
+        const bool in = q0 + row < s.sq && dbg_ok(s.q_base + q0 + row < p.Sq);
+        uint16_t* dst =
+            p.dq + row_at(p.layout, s.batch, p.Hq, p.Sq, s.head, s.q_base + q0 + (in ? row : 0)) + 64 * g;
+        store_row<64>(tacc, n == 0, p.scale, p.mode, in ? dst : nullptr, kCheck && *poison_any, poison);
       } else {
         const size_t slots = static_cast<size_t>(p.q_slots) * (kVarlen ? p.Hq : p.BH);
         const size_t slot = static_cast<size_t>(s.slot_q) + static_cast<size_t>(s.head) * p.q_slots + s.tile;
-        float* dst = p.part + ((static_cast<size_t>(s.split) * slots + slot) * kTile + row) * kD;
-        store_part(tacc, n == 0, dst, poison);
+        float* dst = p.part + ((static_cast<size_t>(s.split) * slots + slot) * kTile + row) * kD + 64 * g;
+        store_part<64>(tacc, n == 0, dst, poison);
       }
     }
   }
