@@ -1,7 +1,7 @@
 // attn_bwd.cu - host side of the backward pass declared in include/attn_fwd.h:
-// checks the call, lays out the workspace and launches, on the caller's stream,
-// the row statistics, dQ, and dK with dV (attn_bwd_kernel.cuh), each a
-// programmatic dependent of the one before; results that several CTAs share the
+// checks the call, lays out the workspace and launches, on the caller's stream, dQ
+// with the row statistics, then dK with dV (attn_bwd_kernel.cuh), each a programmatic
+// dependent of the one before; results that several CTAs share the
 // streamed axis of are joined by one more kernel each.
 #include <cuda_runtime.h>
 
@@ -59,6 +59,8 @@ int device_ready(int dev) {
   g_state[dev] = 1;
   return ATTN_OK;
 }
+
+constexpr int kJoinPer = bwd::kTile / bwd::kJoinRows;  // join blocks per tile
 
 int64_t tiles_of(int64_t n) { return (n + bwd::kTile - 1) / bwd::kTile; }
 
@@ -185,10 +187,11 @@ int bwd_impl(const void* dout, const void* q, const void* k, const void* v, cons
   const int st = device_ready(dev);
   if (st != ATTN_OK) return st;
 
-  CUtensorMap tq, tk, tv, tdo;
+  CUtensorMap tq, tk, tv, tdo, tout;
   if (!make_map(&tq, q, layout, rep, Hq, Sq, bwd::kTile) || !make_map(&tk, k, layout, rep, Hkv, Sk, bwd::kTile) ||
       !make_map(&tv, v, layout, rep, Hkv, Sk, bwd::kTile) ||
-      !make_map(&tdo, dout, layout, rep, Hq, Sq, bwd::kTile))
+      !make_map(&tdo, dout, layout, rep, Hq, Sq, bwd::kTile) ||
+      !make_map(&tout, out, layout, rep, Hq, Sq, bwd::kTile))
     return ATTN_ERR_LAUNCH;
 
   char* ws = static_cast<char*>(workspace);
@@ -196,19 +199,6 @@ int bwd_impl(const void* dout, const void* q, const void* k, const void* v, cons
   float* dq_part = reinterpret_cast<float*>(ws + pl.stats_bytes);
   float* dkv_part = reinterpret_cast<float*>(ws + pl.stats_bytes + pl.dq_bytes);
   const bool causal = (flags & ATTN_FLAG_CAUSAL) != 0;
-
-  bwd::StatsParams sp;
-  sp.dout = static_cast<const uint16_t*>(dout);
-  sp.out = static_cast<const uint16_t*>(out);
-  sp.lse = lse;
-  sp.stats = stats;
-  sp.cu_q = cu_q;
-  sp.Sq = static_cast<int>(Sq);
-  sp.Hq = static_cast<int>(Hq);
-  sp.max_sq = static_cast<int>(max_sq);
-  sp.q_slots = static_cast<int>(pl.q_slots);
-  sp.layout = layout;
-  sp.n_tiles = static_cast<int>(pl.q_tiles);
 
   bwd::BwdParams p;
   p.Sq = static_cast<int>(Sq);
@@ -227,6 +217,7 @@ int bwd_impl(const void* dout, const void* q, const void* k, const void* v, cons
   p.max_sk = static_cast<int>(max_sk);
   p.q_slots = static_cast<int>(pl.q_slots);
   p.k_slots = static_cast<int>(pl.k_slots);
+  p.lse = lse;
   p.stats = stats;
   p.dq = static_cast<uint16_t*>(dq);
   p.dk = static_cast<uint16_t*>(dk);
@@ -235,10 +226,6 @@ int bwd_impl(const void* dout, const void* q, const void* k, const void* v, cons
   const int64_t keys_per_head = varlen ? (Sk + B - 1) / B : Sk;
   const int64_t rows_per_head = varlen ? (Sq + B - 1) / B : Sq;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-
-  if (!launch(varlen ? bwd::attn_bwd_stats<true> : bwd::attn_bwd_stats<false>, B * Hq * pl.q_tiles,
-              bwd::kStatsThreads, 0, cs, false, sp))
-    return ATTN_ERR_LAUNCH;
 
   bwd::JoinParams jp;
   jp.layout = layout;
@@ -253,12 +240,12 @@ int bwd_impl(const void* dout, const void* q, const void* k, const void* v, cons
   p.part = dq_part;
   auto* dq_fn = varlen ? (causal ? bwd::attn_bwd_dq<true, true> : bwd::attn_bwd_dq<false, true>)
                        : (causal ? bwd::attn_bwd_dq<true, false> : bwd::attn_bwd_dq<false, false>);
-  if (!launch(dq_fn, B * Hq * pl.q_tiles * pl.dq_splits, attn::kThreads, bwd::kDqSmem, cs, true, tq, tk, tv, tdo,
-              p))
+  if (!launch(dq_fn, B * Hq * pl.q_tiles * pl.dq_splits, attn::kThreads, bwd::kDqSmem, cs, false, tq, tk, tv,
+              tdo, tout, p))
     return ATTN_ERR_LAUNCH;
   if (pl.dq_splits > 1) {
     jp.part = dq_part;
-    jp.out = p.dq;
+    jp.out[0] = jp.out[1] = p.dq;
     jp.cu = cu_q;
     jp.cu2 = cu_k;
     jp.S = p.Sq;
@@ -270,9 +257,8 @@ int bwd_impl(const void* dout, const void* q, const void* k, const void* v, cons
     jp.n_tiles = static_cast<int>(pl.q_tiles);
     jp.n_splits = pl.dq_splits;
     jp.results = 1;
-    jp.result = 0;
-    jp.factor = scale;
-    if (!launch(join, B * Hq * pl.q_tiles, 256, 0, cs, true, jp)) return ATTN_ERR_LAUNCH;
+    jp.factor[0] = jp.factor[1] = scale;
+    if (!launch(join, B * Hq * pl.q_tiles * kJoinPer, 16 * bwd::kJoinRows, 0, cs, true, jp)) return ATTN_ERR_LAUNCH;
   }
 
   p.BH = static_cast<int>(B * Hkv);
@@ -298,12 +284,12 @@ int bwd_impl(const void* dout, const void* q, const void* k, const void* v, cons
     jp.n_tiles = static_cast<int>(pl.k_tiles);
     jp.n_splits = pl.dkv_splits;
     jp.results = 2;
-    for (int r = 0; r < 2; ++r) {
-      jp.result = r;
-      jp.out = r == 0 ? p.dk : p.dv;
-      jp.factor = r == 0 ? scale : 1.f;
-      if (!launch(join, B * Hkv * pl.k_tiles, 256, 0, cs, true, jp)) return ATTN_ERR_LAUNCH;
-    }
+    jp.out[0] = p.dk;
+    jp.out[1] = p.dv;
+    jp.factor[0] = scale;
+    jp.factor[1] = 1.f;
+    if (!launch(join, 2 * B * Hkv * pl.k_tiles * kJoinPer, 16 * bwd::kJoinRows, 0, cs, true, jp))
+      return ATTN_ERR_LAUNCH;
   }
   return ATTN_OK;
 }

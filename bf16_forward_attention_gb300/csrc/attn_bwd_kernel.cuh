@@ -54,7 +54,8 @@ struct BwdParams {
   const int* cu_k;
   int max_sq, max_sk;
   int q_slots, k_slots;    // tile slots per head (see tile_slot)
-  const float* stats;      // [head][slot][2][128]
+  const float* lse;
+  float* stats;            // [head][slot][2][128]: written by dq, read by dkv
   float* part;             // n_splits > 1: [split][result][head * slots][128][128] fp32
   uint16_t *dq, *dk, *dv;  // results
 };
@@ -343,71 +344,6 @@ __device__ __forceinline__ void dq_ds(uint32_t tP, uint32_t tS, uint64_t nd2, in
       w[x] = ptx::pack_bf16x2(s0, s1);
     }
     ptx::tmem_st16(tS + 16 * ch, w);
-  }
-}
-
-// ---------------------------------------------------------------- row statistics
-//
-// Per query row -lse log2(e) and -D, in the tiles the two kernels read: rows past the
-// end, and rows that see no key, get -Inf and 0 (P = 0). A non-finite D becomes
-// NaN: it marks a row whose dO or O has a non-finite element. 16 lanes read a row
-// (dO and O once, 512 bytes a row; bound by HBM).
-struct StatsParams {
-  const uint16_t *dout, *out;
-  const float* lse;
-  float* stats;
-  const int* cu_q;
-  int Sq, Hq, max_sq, q_slots, layout, n_tiles;  // one block per (batch, head, tile)
-};
-
-constexpr int kStatsThreads = 256;
-
-template <bool kVarlen>
-__global__ void __launch_bounds__(kStatsThreads) attn_bwd_stats(const StatsParams p) {
-  const int tile = blockIdx.x % p.n_tiles, bh = blockIdx.x / p.n_tiles;
-  const int h = bh % p.Hq, b = bh / p.Hq;
-  ptx::launch_dependents();
-  int base = 0, sq = p.Sq, batch = b, slot = b * p.Hq * p.q_slots;
-  if (kVarlen) {
-    base = __ldg(p.cu_q + b);
-    sq = __ldg(p.cu_q + b + 1) - base;
-    batch = 0;
-    slot = tile_slot<true>(base, b);
-    if (base < 0 || sq < 0 || sq > p.max_sq || base + sq > p.Sq) return;  // reported by the kernels
-  }
-  if (tile * kTile >= sq) return;
-  float* st = p.stats + (static_cast<size_t>(slot) + static_cast<size_t>(h) * p.q_slots + tile) * kStatFloats;
-  const int sub = threadIdx.x & 15;
-  for (int r0 = threadIdx.x >> 4; r0 < kTile; r0 += kStatsThreads / 16) {
-    const int row = tile * kTile + r0;
-    float acc = 0.f;
-    if (row < sq) {
-      const size_t at = row_at(p.layout, batch, p.Hq, p.Sq, h, base + row) + 8 * sub;
-      const uint4 x = *reinterpret_cast<const uint4*>(p.dout + at);
-      const uint4 y = *reinterpret_cast<const uint4*>(p.out + at);
-      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc = fmaf(__uint_as_float(xs[i] << 16), __uint_as_float(ys[i] << 16), acc);
-        acc = fmaf(__uint_as_float(xs[i] & 0xFFFF0000u), __uint_as_float(ys[i] & 0xFFFF0000u), acc);
-      }
-    }
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) acc += __shfl_xor_sync(0xFFFFFFFFu, acc, o);
-    if (sub == 0) {
-      float nl = -__int_as_float(0x7F800000), nd = 0.f;
-      if (row < sq) {
-        const size_t at = kVarlen ? static_cast<size_t>(h) * p.Sq + base + row
-                                  : (static_cast<size_t>(b) * p.Hq + h) * p.Sq + row;
-        const float l = p.lse[at];
-        if (l != -__int_as_float(0x7F800000)) {
-          nl = -l * 1.4426950408889634f;
-          nd = isfinite(acc) ? -acc : __int_as_float(0x7FC00000);
-        }
-      }
-      st[r0] = nl;
-      st[kTile + r0] = nd;
-    }
   }
 }
 
@@ -755,6 +691,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 // [256,384), dQ [384,512). With two S buffers the tensor pipe forms S_{j+1} and
 // dP_{j+1} around dQ_j, and a turn of the softmax (exponentials of S_{j+1}, then
 // dS once dP_{j+1} is there) has 1536 tensor cycles.
+//
+// It also leaves the row statistics that dkv reads: per query row -lse log2(e) and -D,
+// D = sum_c dO_ic O_ic, formed from the dO tile it has and the O tile, which passes
+// through K's third stage before that is first needed. (A kernel of its own for them
+// read dO once more and cost 25 us of 2.35 ms on 8K self-attention, 47 of 1039 us on a
+// packed batch, and a launch.) Rows past the end, and rows that see no key, get -Inf
+// and 0 (P = 0). A non-finite D becomes NaN: it marks a row whose dO or O has a
+// non-finite element.
 constexpr int kDqKStages = 3, kDqVStages = 2;  // K_j is in use while K_{j+2} loads
 constexpr int kDqMasked = 2;  // 128 rows' causal limits span at most 127 keys
 enum : int {
@@ -767,6 +711,8 @@ enum : int {
   kDqDpFull = kDqSFull + 2,
   kDqDsFull,
   kDqAcc,
+  kDqOutFull,   // O has landed in K's last stage
+  kDqOutRead,   // and has been read
   kDqLanded,
   kDqChecked = kDqLanded + kDqMasked,
   kDqDrain = kDqChecked + kDqMasked,
@@ -774,7 +720,8 @@ enum : int {
 };
 constexpr int kDqOffQ = 0, kDqOffO = kTileBytes, kDqOffK = 2 * kTileBytes,
               kDqOffV = kDqOffK + kDqKStages * kTileBytes,
-              kDqOffPoison = kDqOffV + kDqVStages * kTileBytes, kDqOffBar = kDqOffPoison + kD * 4 + 16,
+              kDqOffPoison = kDqOffV + kDqVStages * kTileBytes, kDqOffDots = kDqOffPoison + kD * 4 + 16,
+              kDqOffBar = kDqOffDots + 2 * kTile * 4,
               kDqOffSlot = kDqOffBar + kDqBars * 8, kDqSmem = kDqOffSlot + 8 + 1024;
 static_assert(kDqSmem <= 232448, "shared memory budget (dq)");
 
@@ -782,7 +729,7 @@ template <bool kCausal, bool kVarlen>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_bwd_dq(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
-                const BwdParams p) {
+                const __grid_constant__ CUtensorMap tm_out, const BwdParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -826,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kv_head = s.head / p.group;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kDqBars; ++i) ptx::mbar_init(bar(i), i == kDqDsFull ? 8 : 1);
+    for (int i = 0; i < kDqBars; ++i) ptx::mbar_init(bar(i), (i == kDqDsFull || i == kDqOutRead) ? 8 : 1);
     *abort_flag = 0;
     *poison_any = 0;
     ptx::fence_mbar_init();
@@ -838,6 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::prefetch_tmap(&tm_k);
     ptx::prefetch_tmap(&tm_v);
     ptx::prefetch_tmap(&tm_do);
+    ptx::prefetch_tmap(&tm_out);
   }
   if (warp == 1) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), kTmemCols);
@@ -847,6 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  ptx::launch_dependents();  // the next kernel waits for this grid before it reads its results
   const uint32_t tP = tmem + 256, tQ = tmem + 384;
 
   if (warp == 0) {
@@ -858,6 +807,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_arrive_expect_tx(bar(kDqQ), 2 * kTileBytes);
       load_tile(sbase + kDqOffQ, &tm_q, bar(kDqQ), p.layout, s.q_base + q0, s.head, s.batch, pol_once);
       load_tile(sbase + kDqOffO, &tm_do, bar(kDqQ), p.layout, s.q_base + q0, s.head, s.batch, pol_once);
+      constexpr int kOutStage = kDqKStages - 1;
+      ptx::mbar_arrive_expect_tx(bar(kDqOutFull), kTileBytes);
+      load_tile(sbase + kDqOffK + kOutStage * kTileBytes, &tm_out, bar(kDqOutFull), p.layout, s.q_base + q0,
+                s.head, s.batch, pol_once);
       int k_issued = 0, v_issued = 0;
       for (int j = 0; j < n; ++j) {
         const int row = s.k_base + (t0 + j) * kTile;
@@ -865,6 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int ks = j % kDqKStages, vs = j % kDqVStages;
         if (!wait_bounded(bar(kDqKEmpty + ks), ((j / kDqKStages) & 1) ^ 1, abort_flag, p.timeout_ns, true))
           break;
+        if (j == kOutStage && !wait_bounded(bar(kDqOutRead), 0, abort_flag, p.timeout_ns, true)) break;
         ptx::mbar_arrive_expect_tx(bar(kDqKFull + ks), kTileBytes);
         load_tile(sbase + kDqOffK + ks * kTileBytes, &tm_k, bar(kDqKFull + ks), p.layout, row, kv_head,
                   s.batch, pol_reuse);
@@ -877,6 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++v_issued;
       }
       wait_bounded(bar(kDqQ), 0, abort_flag, p.timeout_ns, false);
+      wait_bounded(bar(kDqOutFull), 0, abort_flag, p.timeout_ns, false);
       for (int st = 0; st < kDqKStages && st < k_issued; ++st)
         wait_bounded(bar(kDqKFull + st), ((k_issued - 1 - st) / kDqKStages) & 1, abort_flag, p.timeout_ns,
                      false);
@@ -983,14 +938,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     uint64_t nl2 = 0, nd2 = 0;
     if (n > 0) {
-      ptx::grid_dependency_wait();  // the row statistics
-      const float* st = p.stats + (static_cast<size_t>(s.slot_q) + static_cast<size_t>(s.head) * p.q_slots +
-                                   s.tile) * kStatFloats;
-      const float nl = st[row], nd = st[kTile + row];
+      // The row's statistics: each warpgroup adds its 64 columns of dO O. (lse is read
+      // before the waits, whose time covers its latency.)
+      float dot = 0.f, lse = -__int_as_float(0x7F800000);
+      if (q0 + row < s.sq)
+        lse = __ldg(p.lse + (kVarlen ? static_cast<size_t>(s.head) * p.Sq + s.q_base + q0 + row
+                                     : (static_cast<size_t>(s.batch) * p.Hq + s.head) * p.Sq + q0 + row));
+      ok = warp_wait(bar(kDqQ), 0, abort_flag, p.timeout_ns) &&
+           warp_wait(bar(kDqOutFull), 0, abort_flag, p.timeout_ns);
+      if (ok) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint4 x = ptx::ld_shared_v4(sbase + kDqOffO + chunk_at(row, 8 * g + c));
+          const uint4 y =
+              ptx::ld_shared_v4(sbase + kDqOffK + (kDqKStages - 1) * kTileBytes + chunk_at(row, 8 * g + c));
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            dot = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), dot);
+            dot = fmaf(__uint_as_float(xs[e] & 0xFFFF0000u), __uint_as_float(ys[e] & 0xFFFF0000u), dot);
+          }
+        }
+        // (The stage is refilled by TMA: order these reads before it.)
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(kDqOutRead));
+      }
+      float* dots = reinterpret_cast<float*>(smem + kDqOffDots);
+      dots[g * kTile + row] = dot;
+      ptx::named_barrier_sync(2, 256);  // (both warpgroups, whatever their waits said)
+      const float D = dots[row] + dots[kTile + row];
+      float nl = -__int_as_float(0x7F800000), nd = 0.f;
+      if (lse != -__int_as_float(0x7F800000)) {
+        nl = -lse * 1.4426950408889634f;
+        nd = isfinite(D) ? -D : __int_as_float(0x7FC00000);
+      }
+      if (g == 0 && s.split == 0) {
+        float* st = p.stats + (static_cast<size_t>(s.slot_q) + static_cast<size_t>(s.head) * p.q_slots + s.tile) *
+                                  kStatFloats;
+        st[row] = nl;
+        st[kTile + row] = nd;
+      }
       nl2 = ptx::f2_pack(nl, nl);
       nd2 = ptx::f2_pack(nd, nd);
     }
-    for (int j = 0; j < n; ++j) {
+    for (int j = 0; ok && j < n; ++j) {
       const uint32_t tSh = tmem + 128 * (j & 1) + lane_base + 64 * g;
       const bool mk = masked(j);
       const int hi = limit - (t0 + j) * kTile - 64 * g;  // columns of this half the row sees
@@ -1053,20 +1045,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------- join of the splits
 //
 // A result owned by n_splits CTAs: their fp32 terms are added in split order, scaled
-// and rounded. One block per 128 x 128 tile, 16 threads per row (32 bytes each).
+// and rounded. One block per 16 rows of a tile, 16 threads per row (32 bytes each).
 struct JoinParams {
   const float* part;
-  uint16_t* out;
-  const int* cu;    // packed batch: the owned axis's offsets
-  const int* cu2;   // and the other axis's (a sequence with bad offsets is left alone)
-  int S, S2, H, max_s, max_s2, slots, B, n_tiles, n_splits, results, result, layout, mode;
-  float factor;
+  uint16_t* out[2];  // dq, or dk and dv
+  float factor[2];
+  const int* cu;     // packed batch: the owned axis's offsets
+  const int* cu2;    // and the other axis's (a sequence with bad offsets is left alone)
+  int S, S2, H, max_s, max_s2, slots, B, n_tiles, n_splits, results, layout, mode;
 };
 
+constexpr int kJoinRows = 16;
+
 template <bool kVarlen>
-__global__ void __launch_bounds__(256) attn_bwd_join(const JoinParams p) {
-  const int tile = blockIdx.x % p.n_tiles, bh = blockIdx.x / p.n_tiles;
-  const int h = bh % p.H, b = bh / p.H;
+__global__ void __launch_bounds__(16 * kJoinRows) attn_bwd_join(const JoinParams p) {
+  constexpr int kPer = kTile / kJoinRows;  // blocks per tile
+  const int r = (blockIdx.x % kPer) * kJoinRows + (threadIdx.x >> 4);
+  int item = blockIdx.x / kPer;
+  const int tile = item % p.n_tiles;
+  item /= p.n_tiles;
+  const int h = item % p.H;
+  item /= p.H;
+  const int b = item % p.B, result = item / p.B;
   ptx::grid_dependency_wait();
   int base = 0, len = p.S, batch = b;
   size_t slot = (static_cast<size_t>(b) * p.H + h) * p.slots + tile;
@@ -1080,27 +1080,27 @@ __global__ void __launch_bounds__(256) attn_bwd_join(const JoinParams p) {
     batch = 0;
     slot = static_cast<size_t>(h) * p.slots + tile_slot<true>(base, b) + tile;
   }
+  const int row = tile * kTile + r;
+  if (row >= len) return;
   const size_t slots = static_cast<size_t>(p.slots) * p.H * (kVarlen ? 1 : p.B);
   const int c0 = (threadIdx.x & 15) * 8;
-  for (int r = threadIdx.x >> 4; r < kTile; r += 16) {
-    const int row = tile * kTile + r;
-    if (row >= len) return;
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < p.n_splits; ++k) {
-      const float4* src = reinterpret_cast<const float4*>(
-          p.part + (((static_cast<size_t>(k) * p.results + p.result) * slots + slot) * kTile + r) * kD + c0);
-      const float4 u = src[0], v = src[1];
-      x[0] += u.x; x[1] += u.y; x[2] += u.z; x[3] += u.w;
-      x[4] += v.x; x[5] += v.y; x[6] += v.z; x[7] += v.w;
-    }
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = round_bf16_bits(x[2 * i] * p.factor, p.mode) |
-             (round_bf16_bits(x[2 * i + 1] * p.factor, p.mode) << 16);
-    *reinterpret_cast<uint4*>(p.out + row_at(p.layout, batch, p.H, p.S, h, base + row) + c0) =
-        make_uint4(w[0], w[1], w[2], w[3]);
+  float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int k = 0; k < p.n_splits; ++k) {
+    const float4* src = reinterpret_cast<const float4*>(
+        p.part + (((static_cast<size_t>(k) * p.results + result) * slots + slot) * kTile + r) * kD + c0);
+    const float4 u = src[0], v = src[1];
+    x[0] += u.x; x[1] += u.y; x[2] += u.z; x[3] += u.w;
+    x[4] += v.x; x[5] += v.y; x[6] += v.z; x[7] += v.w;
   }
+  const float f = result ? p.factor[1] : p.factor[0];
+  uint16_t* out = result ? p.out[1] : p.out[0];
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = round_bf16_bits(x[2 * i] * f, p.mode) | (round_bf16_bits(x[2 * i + 1] * f, p.mode) << 16);
+  *reinterpret_cast<uint4*>(out + row_at(p.layout, batch, p.H, p.S, h, base + row) + c0) =
+      make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 }  // namespace bwd
