@@ -54,6 +54,7 @@ struct Plan {
   int64_t rows, rows_pad;  // packed rows of a kv head
   int mt;                  // 16-row tiles of a block (own keys)
   int64_t blocks;          // blocks per (sequence, kv head)
+  int64_t prefix_blocks;   // few packed rows: blocks per kv head against the prefix; else 0
   int prefix_splits, own_splits;
   int64_t packed_bytes, o_bytes, rl_bytes;
   int64_t bytes() const { return packed_bytes + o_bytes + rl_bytes; }
@@ -67,24 +68,37 @@ bool make_plan(Plan* pl, int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int64_t
   pl->rows = B * Sq * group;
   pl->rows_pad = up256(pl->rows);
   const int64_t per_seq = Sq * group;
-  pl->mt = per_seq <= 16 ? 1 : 2;
+  // Two row tiles for a sequence of more than 16 rows, or for a batch of 17 to 32 (one
+  // block then holds it against the prefix, below).
+  pl->mt = per_seq > 16 || (pl->rows > 16 && pl->rows <= 32) ? 2 : 1;
   pl->blocks = (per_seq + 16 * pl->mt - 1) / (16 * pl->mt);
   // 128 parts at most: rows, grids and row numbers then stay ints.
   if (Hkv > kLim31 / pl->rows_pad / 128 || B > kLim31 / Hkv / pl->blocks / 64) return false;
   const int64_t sms = sms_here();
-  // Own keys: four blocks for every SM, of at least 256 keys of the cache each
-  // (lengths are on the device; a short sequence's parts are shorter).
+  // Own keys: two blocks for every SM (what it holds at once), of at least 256 keys of
+  // the cache each (lengths are on the device; a short sequence's parts are shorter).
   const int64_t items = B * Hkv * pl->blocks;
-  int64_t s = (4 * sms + items - 1) / items;
+  int64_t s = (2 * sms + items - 1) / items;
   const int64_t most = (cap + 255) / 256;
   if (s > most) s = most;
   if (s > 64) s = 64;
   pl->own_splits = static_cast<int>(s);
-  // Prefix: the split count with the least estimated time, in key tiles: a wave costs
-  // its tiles, about 4 more to start and end, and every split some traffic of the
-  // join (1040 bytes a row, against 64 KiB of keys a tile).
+  pl->prefix_blocks = 0;
   pl->prefix_splits = 0;
-  if (Sp > 0) {
+  if (Sp > 0 && pl->rows <= 16 * pl->mt) {
+    // All packed rows of a kv head fit one block: the kernel of the own keys takes the
+    // prefix as well, in the same launch, read once. (The fused kernel's 256-row items
+    // would be nearly empty, and it needs the rows packed first.)
+    pl->prefix_blocks = 1;
+    int64_t n = (2 * sms + Hkv - 1) / Hkv;
+    const int64_t cut = (Sp + 255) / 256;
+    if (n > cut) n = cut;
+    if (n > 64) n = 64;
+    pl->prefix_splits = static_cast<int>(n);
+  } else if (Sp > 0) {
+    // The split count with the least estimated time, in key tiles: a wave costs its
+    // tiles, about 4 more to start and end, and every split some traffic of the join
+    // (1040 bytes a row, against 64 KiB of keys a tile).
     const int64_t tiles = (Sp + attn::kBN - 1) / attn::kBN;
     const int64_t cta = Hkv * (pl->rows_pad / 256);
     double least = 1e30;
@@ -99,7 +113,7 @@ bool make_plan(Plan* pl, int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int64_t
     }
   }
   const int64_t parts = pl->prefix_splits + pl->own_splits;
-  pl->packed_bytes = Sp > 0 ? up256(pl->rows * Hkv * 256) : 0;
+  pl->packed_bytes = Sp > 0 && pl->prefix_blocks == 0 ? up256(pl->rows * Hkv * 256) : 0;
   pl->o_bytes = parts * Hkv * pl->rows_pad * attn::kD * 4;
   pl->rl_bytes = parts * Hkv * pl->rows_pad * 8;
   return true;
@@ -174,7 +188,6 @@ int attn_fwd_prefix(const void* q, const void* k_prefix, const void* v_prefix, c
   uint16_t* packed = reinterpret_cast<uint16_t*>(ws);
   float* part_o = reinterpret_cast<float*>(ws + pl.packed_bytes);
   float* part_rl = reinterpret_cast<float*>(ws + pl.packed_bytes + pl.o_bytes);
-  const size_t part_rows = static_cast<size_t>(Hkv) * pl.rows_pad;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
 
   pre::OwnParams p;
@@ -182,9 +195,12 @@ int attn_fwd_prefix(const void* q, const void* k_prefix, const void* v_prefix, c
   p.k = static_cast<const uint16_t*>(k);
   p.v = static_cast<const uint16_t*>(v);
   p.seqlens = seqlens;
-  p.q_packed = Sp > 0 ? packed : nullptr;
-  p.part_o = part_o + pl.prefix_splits * part_rows * attn::kD;
-  p.part_rl = part_rl + pl.prefix_splits * part_rows * 2;
+  p.kp = static_cast<const uint16_t*>(k_prefix);
+  p.vp = static_cast<const uint16_t*>(v_prefix);
+  const bool fused_prefix = Sp > 0 && pl.prefix_blocks == 0;
+  p.q_packed = fused_prefix ? packed : nullptr;
+  p.part_o = part_o;
+  p.part_rl = part_rl;
   p.B = static_cast<int>(B);
   p.Hq = static_cast<int>(Hq);
   p.Hkv = static_cast<int>(Hkv);
@@ -195,13 +211,18 @@ int attn_fwd_prefix(const void* q, const void* k_prefix, const void* v_prefix, c
   p.causal = (flags & ATTN_FLAG_CAUSAL) ? 1 : 0;
   p.rows = static_cast<int>(pl.rows);
   p.rows_pad = static_cast<int>(pl.rows_pad);
-  p.n_splits = pl.own_splits;
-  p.n_blocks = static_cast<int>(pl.blocks);
+  p.Sp = static_cast<int>(Sp);
+  p.own_splits = pl.own_splits;
+  p.own_blocks = static_cast<int>(pl.blocks);
+  p.prefix_splits = pl.prefix_splits;
+  p.prefix_blocks = static_cast<int>(pl.prefix_blocks);
+  const int64_t prefix_items = Hkv * pl.prefix_blocks * pl.prefix_splits;
+  p.prefix_items = static_cast<int>(prefix_items);
   p.c = scale * 1.4426950408889634f;
   if (!launch(pl.mt == 1 ? pre::attn_prefix_own<1> : pre::attn_prefix_own<2>,
-              B * Hkv * pl.blocks * pl.own_splits, pre::kOwnThreads, pre::kOwnSmem, cs, false, p))
+              prefix_items + B * Hkv * pl.blocks * pl.own_splits, pre::kOwnThreads, pre::kOwnSmem, cs, false, p))
     return ATTN_ERR_LAUNCH;
-  if (Sp > 0) {
+  if (fused_prefix) {
     st = split_parts(packed, k_prefix, v_prefix, layout, 1, Hkv, pl.rows, Sp, scale, pl.prefix_splits, part_o,
                      part_rl, cs);
     if (st != ATTN_OK) return st;

@@ -23,8 +23,9 @@ constexpr int kKeys = 16;                       // keys per warp tile
 constexpr int kKvBytes = kKeys * kD * 2;        // 4 KiB: a tile of K or of V
 constexpr int kOwnStages = 3;
 constexpr int kWarpBytes = kOwnStages * 2 * kKvBytes;
-constexpr int kOwnOffMl = kWarps * kWarpBytes;  // [warp][row][2] floats
 constexpr int kMaxRows = 32;                    // rows of a block at most
+constexpr int kOwnOffQ = kWarps * kWarpBytes;   // the block's queries
+constexpr int kOwnOffMl = kOwnOffQ + kMaxRows * kD * 2;  // [warp][row][2] floats
 constexpr int kOwnSmem = kOwnOffMl + kWarps * kMaxRows * 8;
 static_assert(kWarpBytes >= kMaxRows * kD * 4, "a warp's stages hold its fp32 rows at the end");
 
@@ -32,23 +33,29 @@ struct OwnParams {
   const uint16_t* q;
   const uint16_t* k;       // caches: (B, cap, Hkv, 128) or (B, Hkv, cap, 128)
   const uint16_t* v;
+  const uint16_t* kp;      // the prefix, when its rows are few (prefix_blocks > 0)
+  const uint16_t* vp;
   const int* seqlens;      // keys of each sequence, 0..cap
   uint16_t* q_packed;      // the prefix product's rows, or null
-  float* part_o;           // [split][kv head][rows_pad][128], this kernel's first split
-  float* part_rl;          // [split][kv head][rows_pad][2]
-  int B, Hq, Hkv, group, Sq, cap, layout, causal;
+  float* part_o;           // [part][kv head][rows_pad][128], the prefix's parts first
+  float* part_rl;          // [part][kv head][rows_pad][2]
+  int B, Hq, Hkv, group, Sq, Sp, cap, layout, causal;
   int rows;                // B * Sq * group: packed rows of a kv head
-  int rows_pad, n_splits, n_blocks;  // blocks of 16 * MT rows per (sequence, kv head)
+  int rows_pad;
+  int own_splits, own_blocks;        // blocks of 16 * MT rows per (sequence, kv head)
+  int prefix_splits, prefix_blocks;  // blocks of 16 * MT packed rows per kv head
+  int prefix_items;                  // the grid's first blocks: prefix
   float c;                 // scale * log2(e)
 };
 
 // Packed row r of a kv head is token (r / group) of the batch, head r % group of the
 // group. Element offset of its query (or output) row.
 __device__ __forceinline__ size_t query_at(int layout, int Hq, int Sq, int group, int kvh, int r) {
-  const int tok = r / group, h = kvh * group + r % group;
-  const int b = tok / Sq, i = tok % Sq;
-  return (layout == 0 ? (static_cast<size_t>(b) * Hq + h) * Sq + i
-                      : (static_cast<size_t>(b) * Sq + i) * Hq + h) * kD;
+  const unsigned tok = static_cast<unsigned>(r) / static_cast<unsigned>(group);
+  const int h = kvh * group + r - static_cast<int>(tok) * group;
+  if (layout != 0) return (static_cast<size_t>(tok) * Hq + h) * kD;
+  const unsigned b = tok / static_cast<unsigned>(Sq);
+  return ((static_cast<size_t>(b) * Hq + h) * Sq + (tok - b * Sq)) * kD;
 }
 
 // Keys of its own sequence that query token i sees.
@@ -56,90 +63,117 @@ __device__ __forceinline__ int own_limit(int i, int len, int Sq, int causal) {
   return causal ? max(0, min(len, i + len - Sq + 1)) : len;
 }
 
-// Shared-memory offset of 16-byte chunk c of key row r: the chunk's low bits are
-// turned by the row, so that the 8 rows of an ldmatrix lie in distinct banks.
+// Shared-memory offset of 16-byte chunk c of row r: the chunk's low bits are turned by
+// the row, so that the 8 rows of an ldmatrix lie in distinct banks.
 __device__ __forceinline__ uint32_t kv_at(int r, int c) {
   return static_cast<uint32_t>(r * 256 + ((c ^ (r & 7)) << 4));
 }
 
-// One block: 16 * kMT rows of one (sequence, kv head) against one split of its keys.
-// The four warps take its 16-key tiles in turn, each with a ring of its own (cp.async,
-// 3 stages of 8 KiB: 96 KiB a block in flight or in use, two blocks a SM) and no
-// synchronisation but __syncwarp, and are joined in shared memory at the end. Rows
-// past the end and keys past the sequence's length are zeros. Bound by HBM: per 8 KiB
-// a warp issues some 200 instructions, a tenth of what the SM has in the time the
-// bytes take. P enters the product with V as two bf16 terms, as in the fused kernel.
+// One block: up to 16 * kMT rows against one split of their keys: a sequence's rows of
+// a kv head against its cache, or (few packed rows) those of the whole batch against
+// the prefix. The four warps take the 16-key tiles in turn, each with a ring of its own
+// (cp.async, 3 stages of 8 KiB: 96 KiB a block in flight or in use, two blocks a SM) and
+// no synchronisation but __syncwarp, and are joined in shared memory at the end. Rows
+// past the end and keys past the range are zeros. Bound by HBM where ranges are long
+// (1.1 GB of caches: 170 us, 6.5 TB/s); a short one is bound by the latency of its
+// first loads and the instructions around the loop, kept few for that. P enters the
+// product with V as two bf16 terms, as in the fused kernel.
 template <int kMT>
 __global__ void __launch_bounds__(kOwnThreads, 2) attn_prefix_own(const OwnParams p) {
   extern __shared__ __align__(128) uint8_t smem_own[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int split = blockIdx.x % p.n_splits;
-  int rest = blockIdx.x / p.n_splits;
-  const int block = rest % p.n_blocks;
-  rest /= p.n_blocks;
-  const int kvh = rest % p.Hkv, b = rest / p.Hkv;
-  const int R = p.Sq * p.group;                    // rows of the sequence
-  const int r0 = block * 16 * kMT;                 // first row of the block
-  const int n_rows = min(16 * kMT, R - r0);
-  const int first = b * R + r0;                    // packed row of the block's first
   const float neg_inf = -__int_as_float(0x7F800000);
-
-  if (p.q_packed && split == 0) {
-    for (int x = threadIdx.x; x < n_rows * 16; x += kOwnThreads) {
-      const int r = first + (x >> 4);
-      const size_t dst = (p.layout == 0 ? static_cast<size_t>(kvh) * p.rows + r
-                                        : static_cast<size_t>(r) * p.Hkv + kvh) * kD;
-      reinterpret_cast<uint4*>(p.q_packed + dst)[x & 15] = reinterpret_cast<const uint4*>(
-          p.q + query_at(p.layout, p.Hq, p.Sq, p.group, kvh, r))[x & 15];
+  // ---- which rows and keys.
+  int kvh, first, n_rows, len, min_lim, max_lim, split, n_splits, part;
+  int i0 = 0;              // own keys: the block's first row within its sequence
+  bool causal = false;
+  const uint16_t *kb, *vb;  // key 0
+  {
+    int item = static_cast<int>(blockIdx.x);
+    if (item < p.prefix_items) {
+      n_splits = p.prefix_splits;
+      split = item % n_splits;
+      item /= n_splits;
+      const int block = item % p.prefix_blocks;
+      kvh = item / p.prefix_blocks;
+      first = block * 16 * kMT;
+      n_rows = min(16 * kMT, p.rows - first);
+      len = min_lim = max_lim = p.Sp;
+      part = split;
+      const size_t at = (p.layout == 0 ? static_cast<size_t>(kvh) * p.Sp : static_cast<size_t>(kvh)) * kD;
+      kb = p.kp + at;
+      vb = p.vp + at;
+    } else {
+      item -= p.prefix_items;
+      n_splits = p.own_splits;
+      split = item % n_splits;
+      item /= n_splits;
+      const int block = item % p.own_blocks;
+      item /= p.own_blocks;
+      kvh = item % p.Hkv;
+      const int b = item / p.Hkv;
+      len = __ldg(p.seqlens + b);
+      const int R = p.Sq * p.group;  // rows of the sequence
+      i0 = block * 16 * kMT;
+      n_rows = min(16 * kMT, R - i0);
+      first = b * R + i0;
+      causal = p.causal != 0;
+      part = p.prefix_splits + split;
+      const size_t at = (p.layout == 0 ? (static_cast<size_t>(b) * p.Hkv + kvh) * p.cap
+                                       : static_cast<size_t>(b) * p.cap * p.Hkv + kvh) * kD;
+      kb = p.k + at;
+      vb = p.v + at;
     }
   }
-  const int len = __ldg(p.seqlens + b);
-  if (len < 0 || len > p.cap) {
-    if (threadIdx.x == 0) atomicOr(&g_attn_status, 2u);
-    return;
-  }
-  // Limits rise with the row: the block's least and largest.
-  const int min_lim = own_limit(r0 / p.group, len, p.Sq, p.causal);
-  const int max_lim = own_limit((r0 + n_rows - 1) / p.group, len, p.Sq, p.causal);
-  const int tiles = (max_lim + kKeys - 1) / kKeys;
-  const int t_first = static_cast<int>(static_cast<long long>(tiles) * split / p.n_splits);
-  const int t_end = static_cast<int>(static_cast<long long>(tiles) * (split + 1) / p.n_splits);
-
-  // This lane's rows of m-tile m: lane / 4 and lane / 4 + 8.
-  uint32_t qf[kMT][8][4];
-  int lim[kMT][2];
+  // ---- queries: into shared memory, and packed for the prefix product.
+  const uint32_t qs = ptx::smem_u32(smem_own) + kOwnOffQ;
+  const bool pack = p.q_packed && split == 0;
 #pragma unroll
-  for (int m = 0; m < kMT; ++m) {
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int r = 16 * m + (lane >> 2) + 8 * hf;
-      const bool in = r < n_rows;
-      lim[m][hf] = in ? own_limit((r0 + r) / p.group, len, p.Sq, p.causal) : 0;
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(
-          p.q + query_at(p.layout, p.Hq, p.Sq, p.group, kvh, in ? first + r : first));
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks) {
-        qf[m][ks][hf] = in ? __ldg(src + 8 * ks + (lane & 3)) : 0u;
-        qf[m][ks][2 + hf] = in ? __ldg(src + 8 * ks + 4 + (lane & 3)) : 0u;
+  for (int it = 0; it < 2 * kMT; ++it) {
+    const int r = it * 8 + (threadIdx.x >> 4), c = threadIdx.x & 15;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (r < n_rows) {
+      x = __ldg(reinterpret_cast<const uint4*>(
+                    p.q + query_at(p.layout, p.Hq, p.Sq, p.group, kvh, first + r)) + c);
+      if (pack) {
+        const size_t dst = (p.layout == 0 ? static_cast<size_t>(kvh) * p.rows + first + r
+                                          : static_cast<size_t>(first + r) * p.Hkv + kvh) * kD;
+        reinterpret_cast<uint4*>(p.q_packed + dst)[c] = x;
       }
     }
+    ptx::st_shared_v4(qs + kv_at(r, c), x.x, x.y, x.z, x.w);
   }
-  const size_t key_stride = (p.layout == 0 ? 1 : static_cast<size_t>(p.Hkv)) * kD;
-  const size_t kv_first = (p.layout == 0 ? (static_cast<size_t>(b) * p.Hkv + kvh) * p.cap
-                                         : static_cast<size_t>(b) * p.cap * p.Hkv + kvh) * kD;
-  const uint32_t ring = ptx::smem_u32(smem_own) + warp * kWarpBytes;
+  const bool own = static_cast<int>(blockIdx.x) >= p.prefix_items;
+  if (own) {
+    if (len < 0 || len > p.cap) {
+      if (threadIdx.x == 0) atomicOr(&g_attn_status, 2u);
+      return;
+    }
+    // Limits rise with the row: the block's least and largest.
+    min_lim = own_limit(i0 / p.group, len, p.Sq, causal);
+    max_lim = own_limit((i0 + n_rows - 1) / p.group, len, p.Sq, causal);
+  }
+  const int tiles = (max_lim + kKeys - 1) / kKeys;
+  const int t_first = static_cast<int>(static_cast<long long>(tiles) * split / n_splits);
+  const int t_end = static_cast<int>(static_cast<long long>(tiles) * (split + 1) / n_splits);
+
   // Tile t into stage s: a half-warp reads one key's 256 bytes.
+  const size_t key_stride = (p.layout == 0 ? 1 : static_cast<size_t>(p.Hkv)) * kD;
+  const uint32_t ring = ptx::smem_u32(smem_own) + warp * kWarpBytes;
+  const int half = lane >> 4, chunk = lane & 15;
+  const uint32_t lane_dst = ring + kv_at(half, chunk);  // keys 2 u + half: + 512 u, chunk turned by 2 u
   auto load = [&](int t, int s) {
-    const uint32_t dst = ring + s * 2 * kKvBytes;
-    const int c = lane & 15;
+    const int key = t * kKeys + half;
+    const size_t at = key * key_stride + 8 * chunk;
+    const uint16_t *ks = kb + at, *vs = vb + at;
+    const uint32_t dst = lane_dst + s * 2 * kKvBytes;
 #pragma unroll
     for (int u = 0; u < kKeys / 2; ++u) {
-      const int r = 2 * u + (lane >> 4);
-      const int key = t * kKeys + r;
-      const int ok = key < len;
-      const size_t at = kv_first + (ok ? key : 0) * key_stride + 8 * c;
-      ptx::cp_async16(dst + kv_at(r, c), p.k + at, ok);
-      ptx::cp_async16(dst + kKvBytes + kv_at(r, c), p.v + at, ok);
+      const int ok = key + 2 * u < len;
+      const uint32_t d = (dst ^ ((2 * u & 6) << 4)) + 512 * u;
+      const size_t step = ok ? 2 * u * key_stride : 0;
+      ptx::cp_async16(d, ok ? ks + step : kb, ok);
+      ptx::cp_async16(d + kKvBytes, ok ? vs + step : vb, ok);
     }
   };
 
@@ -154,6 +188,15 @@ __global__ void __launch_bounds__(kOwnThreads, 2) attn_prefix_own(const OwnParam
     mref[m][0] = mref[m][1] = neg_inf;
     l[m][0] = l[m][1] = 0.f;
   }
+  // This lane's rows of m-tile m: lane / 4 and lane / 4 + 8, and the keys they see.
+  int lim[kMT][2];
+#pragma unroll
+  for (int m = 0; m < kMT; ++m)
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int r = 16 * m + (lane >> 2) + 8 * hf;
+      lim[m][hf] = r >= n_rows ? 0 : causal ? own_limit((i0 + r) / p.group, len, p.Sq, 1) : len;
+    }
   const int t0 = t_first + warp;
   const int n = t0 < t_end ? (t_end - t0 + kWarps - 1) / kWarps : 0;  // this warp's tiles
 #pragma unroll
@@ -161,6 +204,13 @@ __global__ void __launch_bounds__(kOwnThreads, 2) attn_prefix_own(const OwnParam
     if (s < n) load(t0 + s * kWarps, s);
     ptx::cp_async_commit();
   }
+  __syncthreads();  // the queries
+  uint32_t qf[kMT][8][4];
+#pragma unroll
+  for (int m = 0; m < kMT; ++m)
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks)
+      ptx::ldmatrix4(qs + kv_at(16 * m + (((lane >> 3) & 1) << 3) + (lane & 7), 2 * ks + (lane >> 4)), qf[m][ks]);
   for (int i = 0; i < n; ++i) {
     ptx::cp_async_wait<kOwnStages - 2>();
     __syncwarp();  // every lane's copies of this tile; every lane is done with the last one
@@ -237,7 +287,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) attn_prefix_own(const OwnParam
     // such keys; if V holds a non-finite element there, the rows are summed key by
     // key over what they see.
     bool apart = false;
-    if (masked && p.causal) {
+    if (masked && causal) {
       uint32_t acc = 0;
 #pragma unroll
       for (int u = 0; u < kKvBytes / 512; ++u) {
@@ -308,22 +358,32 @@ __global__ void __launch_bounds__(kOwnThreads, 2) attn_prefix_own(const OwnParam
     }
   }
   __syncthreads();
+  // Four rows at a time, a warp a row, four columns a lane.
   const float* all_ml = reinterpret_cast<const float*>(smem_own + kOwnOffMl);
-  const size_t row_base = (static_cast<size_t>(split) * p.Hkv + kvh) * p.rows_pad + first;
-  for (int r = 0; r < n_rows; ++r) {
+  const size_t row_base = (static_cast<size_t>(part) * p.Hkv + kvh) * p.rows_pad + first;
+  for (int r = warp; r < n_rows; r += kWarps) {
+    float2 ml4[kWarps];
     float M = neg_inf;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, all_ml[w * kMaxRows * 2 + 2 * r]);
+    for (int w = 0; w < kWarps; ++w) {
+      ml4[w] = reinterpret_cast<const float2*>(all_ml)[w * kMaxRows + r];
+      M = fmaxf(M, ml4[w].x);
+    }
     const float ref = M == neg_inf ? 0.f : M;
-    float L = 0.f, x = 0.f;
+    float L = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = ptx::ex2(all_ml[w * kMaxRows * 2 + 2 * r] - ref);
-      L = fmaf(all_ml[w * kMaxRows * 2 + 2 * r + 1], f, L);
-      x = fmaf(reinterpret_cast<const float*>(smem_own + w * kWarpBytes)[r * kD + threadIdx.x], f, x);
+      const float f = ptx::ex2(ml4[w].x - ref);
+      const float4 y = reinterpret_cast<const float4*>(smem_own + w * kWarpBytes)[r * (kD / 4) + lane];
+      L = fmaf(ml4[w].y, f, L);
+      x.x = fmaf(y.x, f, x.x);
+      x.y = fmaf(y.y, f, x.y);
+      x.z = fmaf(y.z, f, x.z);
+      x.w = fmaf(y.w, f, x.w);
     }
-    p.part_o[(row_base + r) * kD + threadIdx.x] = x;
-    if (threadIdx.x == 0) reinterpret_cast<float2*>(p.part_rl)[row_base + r] = make_float2(M, L);
+    reinterpret_cast<float4*>(p.part_o)[(row_base + r) * (kD / 4) + lane] = x;
+    if (lane == 0) reinterpret_cast<float2*>(p.part_rl)[row_base + r] = make_float2(M, L);
   }
 }
 
@@ -338,6 +398,7 @@ struct JoinParams {
 };
 
 constexpr int kJoinRows = 4;
+constexpr int kMaxParts = 128;  // 64 of the prefix, 64 of the own keys
 
 // A warp per packed row, four columns a lane; parts in a fixed order.
 __global__ void __launch_bounds__(32 * kJoinRows) attn_prefix_join(const JoinParams p) {
@@ -353,22 +414,38 @@ __global__ void __launch_bounds__(32 * kJoinRows) attn_prefix_join(const JoinPar
   const float neg_inf = -__int_as_float(0x7F800000);
   const size_t pitch = static_cast<size_t>(p.Hkv) * p.rows_pad;
   const size_t row0 = static_cast<size_t>(kvh) * p.rows_pad + r;
+  // Lane s holds the reference and row sum of parts s, s + 32, ...; the largest
+  // reference is a warp's maximum (NaN left out: it comes back through its weight).
   const float2* rl = reinterpret_cast<const float2*>(p.part_rl);
+  float2 mine[kMaxParts / 32];
   float R = neg_inf;
-  for (int s = 0; s < p.n_parts; ++s) R = fmaxf(R, rl[row0 + s * pitch].x);
+#pragma unroll
+  for (int u = 0; u < kMaxParts / 32; ++u) {
+    const int s = 32 * u + lane;
+    mine[u] = s < p.n_parts ? rl[row0 + s * pitch] : make_float2(neg_inf, 0.f);
+    R = fmaxf(R, mine[u].x);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) R = fmaxf(R, __shfl_xor_sync(0xFFFFFFFFu, R, d));
   const float ref = R == neg_inf ? 0.f : R;
   float L = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int s = 0; s < p.n_parts; ++s) {
-    const float2 ml = rl[row0 + s * pitch];
-    const float w = ptx::ex2(ml.x - ref);
-    const float4 y = *reinterpret_cast<const float4*>(p.part_o + (row0 + s * pitch) * kD + 4 * lane);
-    L = fmaf(ml.y, w, L);
-    o.x = fmaf(y.x, w, o.x);
-    o.y = fmaf(y.y, w, o.y);
-    o.z = fmaf(y.z, w, o.z);
-    o.w = fmaf(y.w, w, o.w);
+#pragma unroll
+  for (int u = 0; u < kMaxParts / 32; ++u) {
+    if (32 * u >= p.n_parts) break;
+    mine[u].x = ptx::ex2(mine[u].x - ref);
+    const int n = min(32, p.n_parts - 32 * u);
+#pragma unroll 8
+    for (int s = 0; s < n; ++s) {
+      const float w = __shfl_sync(0xFFFFFFFFu, mine[u].x, s), l = __shfl_sync(0xFFFFFFFFu, mine[u].y, s);
+      const float4 y =
+          *reinterpret_cast<const float4*>(p.part_o + (row0 + (32 * u + s) * pitch) * kD + 4 * lane);
+      L = fmaf(l, w, L);
+      o.x = fmaf(y.x, w, o.x);
+      o.y = fmaf(y.y, w, o.y);
+      o.z = fmaf(y.z, w, o.z);
+      o.w = fmaf(y.w, w, o.w);
+    }
   }
   const float inv = __frcp_rn(L);
   const uint2 w2 = make_uint2(

@@ -89,6 +89,9 @@ def _run(t, lens, layout, **kw):
     ("bhsd", 2, 1, 40, 2, 64, 2000, [2000, 999], False),      # long own keys: several parts
     ("bshd", 70, 1, 16, 2, 200, 16, None, False),             # more than 256 packed rows
     ("bshd", 1, 9, 4, 4, 2500, 40, [40], True),
+    ("bhsd", 5, 1, 12, 2, 3001, 30, [0, 30, 7, 1, 22], False),  # 30 packed rows: one block of 32
+    ("bshd", 16, 1, 2, 2, 5000, 8, None, True),               # 16 packed rows, many prefix parts
+    ("bhsd", 9, 2, 4, 2, 900, 33, None, True),                # 36 packed rows: the fused kernel
 ])
 def test_parity(layout, B, Sq, Hq, Hkv, Sp, cap, lens, causal):
     t = _inputs(layout, B, Sq, Hq, Hkv, Sp, cap, seed=B * 100 + Sp + cap)
