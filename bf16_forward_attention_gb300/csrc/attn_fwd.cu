@@ -689,9 +689,10 @@ int split_parts(const void* q, const void* k, const void* v, int layout, int64_t
   p.head_group = 1;
   p.n_items = p.BH * p.n_qpairs * n_splits;
   // (The split form stores no bf16 output: its fourth map is only prefetched.)
-  attn::attn_fwd_kernel<true, false, false>
-      <<<static_cast<unsigned>(p.n_items), attn::kThreads, attn::kSmemBytes, stream>>>(tq, tk, tv, tq, p);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+  return launch(attn::attn_fwd_kernel<true, false, false>, p.n_items, attn::kThreads, attn::kSmemBytes, stream,
+                true, tq, tk, tv, tq, p)
+             ? ATTN_OK
+             : ATTN_ERR_LAUNCH;
 }
 
 }  // namespace attn_host

@@ -950,6 +950,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int kv_head = wk.kv_head, q_base = wk.q_base, k_base = wk.k_base;
           int issued = 0;  // ring fills started so far (fill i goes to stage i % kStages)
           int c1, c2;
+          // The split form may be launched as a programmatic dependent of the kernel that
+          // lays out its queries (no effect otherwise).
+          if constexpr (kPartial) ptx::grid_dependency_wait();
           dbg_ok(q_base + 2 * pair * kBM < p.Sq);  // the first query tile starts inside
           ptx::mbar_arrive_expect_tx(bar(kBarQ), kQTiles * kTileBytes);
           for (int t = 0; t < kQTiles; ++t) {

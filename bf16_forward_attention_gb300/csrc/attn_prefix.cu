@@ -1,7 +1,7 @@
 // attn_prefix.cu - host side of attention on a shared prefix, declared in
 // include/attn_fwd.h: checks the call, lays out the workspace (packed queries and
 // the parts' unnormalised rows) and launches, on the caller's stream, the
-// sequences' own keys, the prefix (the fused kernel's split form) and the join.
+// prefix (the fused kernel's split form), beside it the sequences' own keys, and the join.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -96,16 +96,22 @@ bool make_plan(Plan* pl, int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int64_t
     if (n > 64) n = 64;
     pl->prefix_splits = static_cast<int>(n);
   } else if (Sp > 0) {
-    // The split count with the least estimated time, in key tiles: a wave costs its
-    // tiles, about 4 more to start and end, and every split some traffic of the join
-    // (1040 bytes a row, against 64 KiB of keys a tile).
+    // The prefix product runs beside the own keys' kernel, on one SM per CTA. The split
+    // count with the least estimated time: the product takes 1.9 us per key tile of 128
+    // keys and 256 rows, and 8 us a CTA to start and end; meanwhile the own keys (half
+    // of each cache, as lengths are on the device) are read by the other SMs, of which 70
+    // reach the full 6.5 TB/s; what is left is read afterwards. A split more costs the
+    // join 1040 bytes a row.
     const int64_t tiles = (Sp + attn::kBN - 1) / attn::kBN;
     const int64_t cta = Hkv * (pl->rows_pad / 256);
+    const double own_us = static_cast<double>(B) * Hkv * cap * 256 / 6.5e6;
     double least = 1e30;
     for (int n = 1; n <= 64 && n <= tiles; ++n) {
       const int64_t waves = (cta * n + sms - 1) / sms;
-      const double cost = static_cast<double>(waves) * ((tiles + n - 1) / n + 4) +
-                          static_cast<double>(cta) * n * 256 * 1040 / (65536.0 * sms);
+      const double us = static_cast<double>(waves) * (1.9 * ((tiles + n - 1) / n) + 8);
+      const double rate = cta * n >= sms ? 0.0 : (sms - cta * n >= 70 ? 1.0 : (sms - cta * n) / 70.0);
+      const double left = own_us > us * rate ? own_us - us * rate : 0.0;
+      const double cost = us + left + static_cast<double>(cta) * n * 256 * 1040 * 2 / 6.5e6;
       if (cost < least) {
         least = cost;
         pl->prefix_splits = n;
@@ -198,7 +204,7 @@ int attn_fwd_prefix(const void* q, const void* k_prefix, const void* v_prefix, c
   p.kp = static_cast<const uint16_t*>(k_prefix);
   p.vp = static_cast<const uint16_t*>(v_prefix);
   const bool fused_prefix = Sp > 0 && pl.prefix_blocks == 0;
-  p.q_packed = fused_prefix ? packed : nullptr;
+  p.beside_prefix = fused_prefix ? 1 : 0;
   p.part_o = part_o;
   p.part_rl = part_rl;
   p.B = static_cast<int>(B);
@@ -219,14 +225,28 @@ int attn_fwd_prefix(const void* q, const void* k_prefix, const void* v_prefix, c
   const int64_t prefix_items = Hkv * pl.prefix_blocks * pl.prefix_splits;
   p.prefix_items = static_cast<int>(prefix_items);
   p.c = scale * 1.4426950408889634f;
-  if (!launch(pl.mt == 1 ? pre::attn_prefix_own<1> : pre::attn_prefix_own<2>,
-              prefix_items + B * Hkv * pl.blocks * pl.own_splits, pre::kOwnThreads, pre::kOwnSmem, cs, false, p))
-    return ATTN_ERR_LAUNCH;
   if (fused_prefix) {
+    pre::PackParams k;
+    k.q = p.q;
+    k.packed = packed;
+    k.Hq = p.Hq;
+    k.Hkv = p.Hkv;
+    k.group = p.group;
+    k.Sq = p.Sq;
+    k.layout = layout;
+    k.rows = p.rows;
+    constexpr int kPackRows = pre::kPackThreads / 16;
+    if (!launch(pre::attn_prefix_pack, (pl.rows * Hkv + kPackRows - 1) / kPackRows, pre::kPackThreads, 0, cs, false,
+                k))
+      return ATTN_ERR_LAUNCH;
     st = split_parts(packed, k_prefix, v_prefix, layout, 1, Hkv, pl.rows, Sp, scale, pl.prefix_splits, part_o,
                      part_rl, cs);
     if (st != ATTN_OK) return st;
   }
+  if (!launch(pl.mt == 1 ? pre::attn_prefix_own<1> : pre::attn_prefix_own<2>,
+              prefix_items + B * Hkv * pl.blocks * pl.own_splits, pre::kOwnThreads, pre::kOwnSmem, cs, fused_prefix,
+              p))
+    return ATTN_ERR_LAUNCH;
   pre::JoinParams j;
   j.part_o = part_o;
   j.part_rl = part_rl;

@@ -9,7 +9,8 @@
 //     with the prefix, which the fused kernel's split form computes on the tensor
 //     cores; the prefix is read once per 256 rows instead of once per sequence;
 //   * each sequence's own keys, by attn_prefix_own below: few rows against keys
-//     that nobody else reads, so it is bound by HBM;
+//     that nobody else reads, so it is bound by HBM. It runs beside the prefix product,
+//     on the SMs that this leaves: one is bound by the tensor cores, the other by memory;
 //   * the join, attn_prefix_join, in a fixed order.
 #pragma once
 #include "attn_fwd_kernel.cuh"
@@ -36,7 +37,7 @@ struct OwnParams {
   const uint16_t* kp;      // the prefix, when its rows are few (prefix_blocks > 0)
   const uint16_t* vp;
   const int* seqlens;      // keys of each sequence, 0..cap
-  uint16_t* q_packed;      // the prefix product's rows, or null
+  int beside_prefix;       // the launch before this one is the prefix product
   float* part_o;           // [part][kv head][rows_pad][128], the prefix's parts first
   float* part_rl;          // [part][kv head][rows_pad][2]
   int B, Hq, Hkv, group, Sq, Sp, cap, layout, causal;
@@ -67,6 +68,32 @@ __device__ __forceinline__ int own_limit(int i, int len, int Sq, int causal) {
 // the row, so that the 8 rows of an ldmatrix lie in distinct banks.
 __device__ __forceinline__ uint32_t kv_at(int r, int c) {
   return static_cast<uint32_t>(r * 256 + ((c ^ (r & 7)) << 4));
+}
+
+// This kernel starts while the prefix product runs and reads nothing of it; its last block
+// stays until that grid has finished, so that the end of this grid is the end of both.
+__device__ __forceinline__ void end_with_prefix(const OwnParams& p) {
+  if (p.beside_prefix && blockIdx.x == gridDim.x - 1) ptx::grid_dependency_wait();
+}
+
+// The queries of each kv head as consecutive rows, in the layout of a batch of one: 16
+// bytes a thread.
+struct PackParams {
+  const uint16_t* q;
+  uint16_t* packed;
+  int Hq, Hkv, group, Sq, layout, rows;
+};
+
+constexpr int kPackThreads = 256;
+
+__global__ void __launch_bounds__(kPackThreads) attn_prefix_pack(const PackParams p) {
+  ptx::launch_dependents();
+  const long long x = static_cast<long long>(blockIdx.x) * (kPackThreads / 16) + (threadIdx.x >> 4);
+  if (x >= static_cast<long long>(p.rows) * p.Hkv) return;
+  const int kvh = static_cast<int>(x / p.rows), r = static_cast<int>(x % p.rows);
+  const size_t dst = (p.layout == 0 ? static_cast<size_t>(x) : static_cast<size_t>(r) * p.Hkv + kvh) * kD;
+  reinterpret_cast<uint4*>(p.packed + dst)[threadIdx.x & 15] = __ldg(
+      reinterpret_cast<const uint4*>(p.q + query_at(p.layout, p.Hq, p.Sq, p.group, kvh, r)) + (threadIdx.x & 15));
 }
 
 // One block: up to 16 * kMT rows against one split of their keys: a sequence's rows of
@@ -125,28 +152,22 @@ __global__ void __launch_bounds__(kOwnThreads, 2) attn_prefix_own(const OwnParam
       vb = p.v + at;
     }
   }
-  // ---- queries: into shared memory, and packed for the prefix product.
+  // ---- queries: into shared memory.
   const uint32_t qs = ptx::smem_u32(smem_own) + kOwnOffQ;
-  const bool pack = p.q_packed && split == 0;
 #pragma unroll
   for (int it = 0; it < 2 * kMT; ++it) {
     const int r = it * 8 + (threadIdx.x >> 4), c = threadIdx.x & 15;
     uint4 x = make_uint4(0, 0, 0, 0);
-    if (r < n_rows) {
+    if (r < n_rows)
       x = __ldg(reinterpret_cast<const uint4*>(
                     p.q + query_at(p.layout, p.Hq, p.Sq, p.group, kvh, first + r)) + c);
-      if (pack) {
-        const size_t dst = (p.layout == 0 ? static_cast<size_t>(kvh) * p.rows + first + r
-                                          : static_cast<size_t>(first + r) * p.Hkv + kvh) * kD;
-        reinterpret_cast<uint4*>(p.q_packed + dst)[c] = x;
-      }
-    }
     ptx::st_shared_v4(qs + kv_at(r, c), x.x, x.y, x.z, x.w);
   }
   const bool own = static_cast<int>(blockIdx.x) >= p.prefix_items;
   if (own) {
     if (len < 0 || len > p.cap) {
       if (threadIdx.x == 0) atomicOr(&g_attn_status, 2u);
+      end_with_prefix(p);
       return;
     }
     // Limits rise with the row: the block's least and largest.
@@ -385,6 +406,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) attn_prefix_own(const OwnParam
     reinterpret_cast<float4*>(p.part_o)[(row_base + r) * (kD / 4) + lane] = x;
     if (lane == 0) reinterpret_cast<float2*>(p.part_rl)[row_base + r] = make_float2(M, L);
   }
+  end_with_prefix(p);
 }
 
 // ---------------------------------------------------------------- join

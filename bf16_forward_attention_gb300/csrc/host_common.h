@@ -125,7 +125,8 @@ bool launch(void (*fn)(Params...), int64_t grid, int threads, int smem, cudaStre
 // attn_fwd.cu: the split form of the fused kernel without its merge. Each of
 // n_splits parts of the keys leaves unnormalised rows [split][b*H + h][sq_pad][128]
 // and (reference, row sum) [split][b*H + h][sq_pad][2], sq_pad = Sq rounded up to
-// 256. Arguments are checked by the caller; returns a status code.
+// 256. A programmatic dependent of the launch before it (which writes q): it reads q
+// after that has finished. Arguments are checked by the caller; returns a status code.
 int split_parts(const void* q, const void* k, const void* v, int layout, int64_t B, int64_t H, int64_t Sq,
                 int64_t Sk, float scale, int n_splits, float* part_o, float* part_rl, cudaStream_t stream);
 
