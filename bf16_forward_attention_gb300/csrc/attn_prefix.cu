@@ -26,6 +26,10 @@ namespace pre = attn::prefix;
 std::mutex g_mutex;
 int g_state[kMaxDevices];  // 0 = not set up, 1 = ready, negative = status to return
 
+using OwnKernel = void (*)(const pre::OwnParams);
+constexpr OwnKernel kOwn[4] = {pre::attn_prefix_own<1>, pre::attn_prefix_own<2>, pre::attn_prefix_own<3>,
+                               pre::attn_prefix_own<4>};  // by 8-row tiles of a block
+
 int device_ready(int dev) {
   if (dev < 0 || dev >= kMaxDevices) return ATTN_ERR_NO_DEVICE;
   std::lock_guard<std::mutex> lock(g_mutex);
@@ -37,13 +41,12 @@ int device_ready(int dev) {
     return ATTN_ERR_NO_DEVICE;
   }
   if (major != 10 || minor != 3) return g_state[dev] = ATTN_ERR_ARCH;
-  if (cudaFuncSetAttribute(pre::attn_prefix_own<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           pre::kOwnSmem) != cudaSuccess ||
-      cudaFuncSetAttribute(pre::attn_prefix_own<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           pre::kOwnSmem) != cudaSuccess) {
-    cudaGetLastError();
-    return ATTN_ERR_LAUNCH;
-  }
+  for (OwnKernel fn : kOwn)
+    if (cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             pre::kOwnSmem) != cudaSuccess) {
+      cudaGetLastError();
+      return ATTN_ERR_LAUNCH;
+    }
   g_state[dev] = 1;
   return ATTN_OK;
 }
@@ -52,7 +55,7 @@ constexpr int64_t kLim31 = (int64_t(1) << 31) - 1;
 
 struct Plan {
   int64_t rows, rows_pad;  // packed rows of a kv head
-  int mt;                  // 16-row tiles of a block (own keys)
+  int64_t block_rows;      // of a block of the own keys' kernel, at most 32
   int64_t blocks;          // blocks per (sequence, kv head)
   int64_t prefix_blocks;   // few packed rows: blocks per kv head against the prefix; else 0
   int prefix_splits, own_splits;
@@ -68,10 +71,11 @@ bool make_plan(Plan* pl, int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int64_t
   pl->rows = B * Sq * group;
   pl->rows_pad = up256(pl->rows);
   const int64_t per_seq = Sq * group;
-  // Two row tiles for a sequence of more than 16 rows, or for a batch of 17 to 32 (one
-  // block then holds it against the prefix, below).
-  pl->mt = per_seq > 16 || (pl->rows > 16 && pl->rows <= 32) ? 2 : 1;
-  pl->blocks = (per_seq + 16 * pl->mt - 1) / (16 * pl->mt);
+  // A sequence's rows in blocks of equal size; a batch of up to 32 rows in one (the
+  // block then takes the prefix as well, below).
+  pl->blocks = (per_seq + pre::kMaxRows - 1) / pre::kMaxRows;
+  pl->block_rows = (per_seq + pl->blocks - 1) / pl->blocks;
+  if (Sp > 0 && pl->rows <= pre::kMaxRows) pl->block_rows = pl->rows;
   // 128 parts at most: rows, grids and row numbers then stay ints.
   if (Hkv > kLim31 / pl->rows_pad / 128 || B > kLim31 / Hkv / pl->blocks / 64) return false;
   const int64_t sms = sms_here();
@@ -85,7 +89,7 @@ bool make_plan(Plan* pl, int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int64_t
   pl->own_splits = static_cast<int>(s);
   pl->prefix_blocks = 0;
   pl->prefix_splits = 0;
-  if (Sp > 0 && pl->rows <= 16 * pl->mt) {
+  if (Sp > 0 && pl->rows <= pre::kMaxRows) {
     // All packed rows of a kv head fit one block: the kernel of the own keys takes the
     // prefix as well, in the same launch, read once. (The fused kernel's 256-row items
     // would be nearly empty, and it needs the rows packed first.)
@@ -243,7 +247,8 @@ int attn_fwd_prefix(const void* q, const void* k_prefix, const void* v_prefix, c
                      part_rl, cs);
     if (st != ATTN_OK) return st;
   }
-  if (!launch(pl.mt == 1 ? pre::attn_prefix_own<1> : pre::attn_prefix_own<2>,
+  p.block_rows = static_cast<int>(pl.block_rows);
+  if (!launch(kOwn[(pl.block_rows + 7) / 8 - 1],
               prefix_items + B * Hkv * pl.blocks * pl.own_splits, pre::kOwnThreads, pre::kOwnSmem, cs, fused_prefix,
               p))
     return ATTN_ERR_LAUNCH;

@@ -28,7 +28,8 @@ constexpr int kMaxRows = 32;                    // rows of a block at most
 constexpr int kOwnOffQ = kWarps * kWarpBytes;   // the block's queries
 constexpr int kOwnOffMl = kOwnOffQ + kMaxRows * kD * 2;  // [warp][row][2] floats
 constexpr int kOwnSmem = kOwnOffMl + kWarps * kMaxRows * 8;
-static_assert(kWarpBytes >= kMaxRows * kD * 4, "a warp's stages hold its fp32 rows at the end");
+constexpr int kRowPitch = kD + 4;               // fp32 rows in shared memory: distinct banks
+static_assert(kWarpBytes >= kMaxRows * kRowPitch * 4, "a warp's stages hold its fp32 rows at the end");
 
 struct OwnParams {
   const uint16_t* q;
@@ -43,8 +44,9 @@ struct OwnParams {
   int B, Hq, Hkv, group, Sq, Sp, cap, layout, causal;
   int rows;                // B * Sq * group: packed rows of a kv head
   int rows_pad;
-  int own_splits, own_blocks;        // blocks of 16 * MT rows per (sequence, kv head)
-  int prefix_splits, prefix_blocks;  // blocks of 16 * MT packed rows per kv head
+  int own_splits, own_blocks;        // blocks of block_rows rows per (sequence, kv head)
+  int prefix_splits, prefix_blocks;  // the same of packed rows, per kv head
+  int block_rows;          // at most 8 * kNT
   int prefix_items;                  // the grid's first blocks: prefix
   float c;                 // scale * log2(e)
 };
@@ -96,16 +98,20 @@ __global__ void __launch_bounds__(kPackThreads) attn_prefix_pack(const PackParam
       reinterpret_cast<const uint4*>(p.q + query_at(p.layout, p.Hq, p.Sq, p.group, kvh, r)) + (threadIdx.x & 15));
 }
 
-// One block: up to 16 * kMT rows against one split of their keys: a sequence's rows of
-// a kv head against its cache, or (few packed rows) those of the whole batch against
-// the prefix. The four warps take the 16-key tiles in turn, each with a ring of its own
+// One block: up to 8 * kNT rows against one split of their keys: a sequence's rows of a
+// kv head against its cache, or (few packed rows) those of the whole batch against the
+// prefix. The four warps take the 16-key tiles in turn, each with a ring of its own
 // (cp.async, 3 stages of 8 KiB: 96 KiB a block in flight or in use, two blocks a SM) and
 // no synchronisation but __syncwarp, and are joined in shared memory at the end. Rows
-// past the end and keys past the range are zeros. Bound by HBM where ranges are long
-// (1.1 GB of caches: 170 us, 6.5 TB/s); a short one is bound by the latency of its
-// first loads and the instructions around the loop, kept few for that. P enters the
-// product with V as two bf16 terms, as in the fused kernel.
-template <int kMT>
+// past the end and keys past the range are zeros.
+// The products are transposed, S^T = K Q^T and O^T = V^T P^T, so that the rows are the
+// short side of the 16 x 8 x 16 products: with the rows as the long side a decode's 4 to 8
+// rows filled a quarter to a half of each product and of the softmax's registers (370
+// instructions a tile at 4 rows; 200 this way). A lane holds the same two rows of S^T
+// and O^T, and P^T turns into an operand by movmatrix. P enters as two bf16 terms, as in the
+// fused kernel. Bound by HBM where ranges are long; a short one is bound by the latency
+// of its first loads and the instructions around the loop, kept few for that.
+template <int kNT>
 __global__ void __launch_bounds__(kOwnThreads, 2) attn_prefix_own(const OwnParams p) {
   extern __shared__ __align__(128) uint8_t smem_own[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -123,8 +129,8 @@ __global__ void __launch_bounds__(kOwnThreads, 2) attn_prefix_own(const OwnParam
       item /= n_splits;
       const int block = item % p.prefix_blocks;
       kvh = item / p.prefix_blocks;
-      first = block * 16 * kMT;
-      n_rows = min(16 * kMT, p.rows - first);
+      first = block * p.block_rows;
+      n_rows = min(p.block_rows, p.rows - first);
       len = min_lim = max_lim = p.Sp;
       part = split;
       const size_t at = (p.layout == 0 ? static_cast<size_t>(kvh) * p.Sp : static_cast<size_t>(kvh)) * kD;
@@ -141,8 +147,8 @@ __global__ void __launch_bounds__(kOwnThreads, 2) attn_prefix_own(const OwnParam
       const int b = item / p.Hkv;
       len = __ldg(p.seqlens + b);
       const int R = p.Sq * p.group;  // rows of the sequence
-      i0 = block * 16 * kMT;
-      n_rows = min(16 * kMT, R - i0);
+      i0 = block * p.block_rows;
+      n_rows = min(p.block_rows, R - i0);
       first = b * R + i0;
       causal = p.causal != 0;
       part = p.prefix_splits + split;
@@ -155,7 +161,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) attn_prefix_own(const OwnParam
   // ---- queries: into shared memory.
   const uint32_t qs = ptx::smem_u32(smem_own) + kOwnOffQ;
 #pragma unroll
-  for (int it = 0; it < 2 * kMT; ++it) {
+  for (int it = 0; it < kNT; ++it) {
     const int r = it * 8 + (threadIdx.x >> 4), c = threadIdx.x & 15;
     uint4 x = make_uint4(0, 0, 0, 0);
     if (r < n_rows)
@@ -198,26 +204,25 @@ __global__ void __launch_bounds__(kOwnThreads, 2) attn_prefix_own(const OwnParam
     }
   };
 
-  float o[kMT][16][4];
-  float mref[kMT][2], l[kMT][2];
+  // O^T: d = 16 dt + lane / 4 (elements 0, 1) and + 8 (2, 3) of rows 8 nt + 2 (lane % 4)
+  // + {0, 1}; S^T has keys in the place of d.
+  float o[8][kNT][4];
+  float mref[kNT][2], l[kNT][2];
+  int lim[kNT][2];  // keys the lane's rows see
 #pragma unroll
-  for (int m = 0; m < kMT; ++m) {
+  for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int dt = 0; dt < 8; ++dt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[m][i][e] = 0.f;
-    mref[m][0] = mref[m][1] = neg_inf;
-    l[m][0] = l[m][1] = 0.f;
-  }
-  // This lane's rows of m-tile m: lane / 4 and lane / 4 + 8, and the keys they see.
-  int lim[kMT][2];
+      for (int e = 0; e < 4; ++e) o[dt][nt][e] = 0.f;
 #pragma unroll
-  for (int m = 0; m < kMT; ++m)
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int r = 16 * m + (lane >> 2) + 8 * hf;
-      lim[m][hf] = r >= n_rows ? 0 : causal ? own_limit((i0 + r) / p.group, len, p.Sq, 1) : len;
+    for (int e = 0; e < 2; ++e) {
+      const int r = 8 * nt + 2 * (lane & 3) + e;
+      lim[nt][e] = r >= n_rows ? 0 : causal ? own_limit((i0 + r) / p.group, len, p.Sq, 1) : len;
+      mref[nt][e] = neg_inf;
+      l[nt][e] = 0.f;
     }
+  }
   const int t0 = t_first + warp;
   const int n = t0 < t_end ? (t_end - t0 + kWarps - 1) / kWarps : 0;  // this warp's tiles
 #pragma unroll
@@ -226,12 +231,16 @@ __global__ void __launch_bounds__(kOwnThreads, 2) attn_prefix_own(const OwnParam
     ptx::cp_async_commit();
   }
   __syncthreads();  // the queries
-  uint32_t qf[kMT][8][4];
+  uint32_t qf[kNT][4][4];  // Q^T of two 16-column steps each
 #pragma unroll
-  for (int m = 0; m < kMT; ++m)
+  for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-    for (int ks = 0; ks < 8; ++ks)
-      ptx::ldmatrix4(qs + kv_at(16 * m + (((lane >> 3) & 1) << 3) + (lane & 7), 2 * ks + (lane >> 4)), qf[m][ks]);
+    for (int k2 = 0; k2 < 4; ++k2)
+      ptx::ldmatrix4(qs + kv_at(8 * nt + (lane & 7), 4 * k2 + (lane >> 3)), qf[nt][k2]);
+  // Row and chunk of this lane's address in an ldmatrix of K (keys x d), and of V (read
+  // transposed).
+  const int k_row = (((lane >> 3) & 1) << 3) + (lane & 7), k_chunk = lane >> 4;
+  const int v_row = ((lane >> 4) << 3) + (lane & 7), v_chunk = (lane >> 3) & 1;
   for (int i = 0; i < n; ++i) {
     ptx::cp_async_wait<kOwnStages - 2>();
     __syncwarp();  // every lane's copies of this tile; every lane is done with the last one
@@ -242,65 +251,64 @@ __global__ void __launch_bounds__(kOwnThreads, 2) attn_prefix_own(const OwnParam
     const int key0 = (t0 + i * kWarps) * kKeys;
     const bool masked = key0 + kKeys > min_lim;
 
-    // S: keys key0 + 8 nt + 2 (lane % 4) + {0, 1} of rows lane / 4 (elements 0, 1)
-    // and lane / 4 + 8 (elements 2, 3).
-    float s[kMT][2][4];
+    float s[kNT][4];
 #pragma unroll
-    for (int m = 0; m < kMT; ++m)
+    for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[m][nt][e] = 0.f;
+      for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
       uint32_t kf[4];
-      ptx::ldmatrix4(kt + kv_at(((lane >> 4) << 3) + (lane & 7), 2 * ks + ((lane >> 3) & 1)), kf);
+      ptx::ldmatrix4(kt + kv_at(k_row, 2 * ks + k_chunk), kf);
 #pragma unroll
-      for (int m = 0; m < kMT; ++m) {
-        ptx::mma_16816(s[m][0], qf[m][ks], kf[0], kf[1]);
-        ptx::mma_16816(s[m][1], qf[m][ks], kf[2], kf[3]);
-      }
+      for (int nt = 0; nt < kNT; ++nt)
+        ptx::mma_16816(s[nt], kf, qf[nt][ks >> 1][2 * (ks & 1)], qf[nt][ks >> 1][2 * (ks & 1) + 1]);
     }
-    uint32_t hi[kMT][4], lo[kMT][4];
+    uint32_t hi[kNT][2], lo[kNT][2];  // P^T: keys lane / 4 and + 8, the lane's two rows
 #pragma unroll
-    for (int m = 0; m < kMT; ++m) {
+    for (int nt = 0; nt < kNT; ++nt) {
+      float mx[2];
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        float t[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          t[e] = s[m][e >> 1][2 * hf + (e & 1)] * p.c;
-          if (masked && key0 + 8 * (e >> 1) + 2 * (lane & 3) + (e & 1) >= lim[m][hf]) t[e] = neg_inf;
+      for (int e = 0; e < 2; ++e) {
+        s[nt][e] *= p.c;
+        s[nt][2 + e] *= p.c;
+        if (masked) {
+          if (key0 + (lane >> 2) >= lim[nt][e]) s[nt][e] = neg_inf;
+          if (key0 + (lane >> 2) + 8 >= lim[nt][e]) s[nt][2 + e] = neg_inf;
         }
         // The row's largest (a NaN is left out here and comes back through its weight).
-        float mx = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-        const bool need = mx > mref[m][hf] + kTau;
-        if (__any_sync(0xFFFFFFFFu, need)) {
-          const float f = need ? ptx::ex2(mref[m][hf] - mx) : 1.f;  // 0 from -Inf
-          if (need) mref[m][hf] = mx;
-          l[m][hf] *= f;
+        mx[e] = fmaxf(s[nt][e], s[nt][2 + e]);
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 4));
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 8));
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 16));
+      }
+      const bool need0 = mx[0] > mref[nt][0] + kTau, need1 = mx[1] > mref[nt][1] + kTau;
+      if (__any_sync(0xFFFFFFFFu, need0 || need1)) {
+        const float f0 = need0 ? ptx::ex2(mref[nt][0] - mx[0]) : 1.f;  // 0 from -Inf
+        const float f1 = need1 ? ptx::ex2(mref[nt][1] - mx[1]) : 1.f;
+        if (need0) mref[nt][0] = mx[0];
+        if (need1) mref[nt][1] = mx[1];
+        l[nt][0] *= f0;
+        l[nt][1] *= f1;
 #pragma unroll
-          for (int d = 0; d < 16; ++d) {
-            o[m][d][2 * hf] *= f;
-            o[m][d][2 * hf + 1] *= f;
-          }
+        for (int dt = 0; dt < 8; ++dt) {
+          o[dt][nt][0] *= f0;
+          o[dt][nt][1] *= f1;
+          o[dt][nt][2] *= f0;
+          o[dt][nt][3] *= f1;
         }
-        const float ref = mref[m][hf] == neg_inf ? 0.f : mref[m][hf];
-        float w[4];
+      }
+      const float ref0 = mref[nt][0] == neg_inf ? 0.f : mref[nt][0];
+      const float ref1 = mref[nt][1] == neg_inf ? 0.f : mref[nt][1];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          w[e] = ptx::ex2(t[e] - ref);
-          l[m][hf] += w[e];
-        }
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const uint32_t h = ptx::pack_bf16x2(w[2 * nt], w[2 * nt + 1]);
-          hi[m][2 * nt + hf] = h;
-          lo[m][2 * nt + hf] = ptx::pack_bf16x2(w[2 * nt] - __uint_as_float(h << 16),
-                                                w[2 * nt + 1] - __uint_as_float(h & 0xFFFF0000u));
-        }
+      for (int u = 0; u < 2; ++u) {
+        const float w0 = ptx::ex2(s[nt][2 * u] - ref0), w1 = ptx::ex2(s[nt][2 * u + 1] - ref1);
+        l[nt][0] += w0;
+        l[nt][1] += w1;
+        const uint32_t h = ptx::pack_bf16x2(w0, w1);
+        hi[nt][u] = h;
+        lo[nt][u] =
+            ptx::pack_bf16x2(w0 - __uint_as_float(h << 16), w1 - __uint_as_float(h & 0xFFFF0000u));
       }
     }
     // A key that some row does not see has weight 0 there, and 0 * NaN would carry a
@@ -319,36 +327,46 @@ __global__ void __launch_bounds__(kOwnThreads, 2) attn_prefix_own(const OwnParam
       apart = __any_sync(0xFFFFFFFFu, acc != 0);
     }
     if (!apart) {
+      uint32_t ph[kNT][2], pl[kNT][2];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          ph[nt][u] = ptx::movmatrix_trans(hi[nt][u]);
+          pl[nt][u] = ptx::movmatrix_trans(lo[nt][u]);
+        }
+#pragma unroll
+      for (int dt = 0; dt < 8; ++dt) {
         uint32_t vf[4];
-        ptx::ldmatrix4_trans(vt + kv_at((((lane >> 3) & 1) << 3) + (lane & 7), 2 * j + (lane >> 4)), vf);
+        ptx::ldmatrix4_trans(vt + kv_at(v_row, 2 * dt + v_chunk), vf);
 #pragma unroll
-        for (int m = 0; m < kMT; ++m) {
-          ptx::mma_16816(o[m][2 * j], hi[m], vf[0], vf[1]);
-          ptx::mma_16816(o[m][2 * j + 1], hi[m], vf[2], vf[3]);
-          ptx::mma_16816(o[m][2 * j], lo[m], vf[0], vf[1]);
-          ptx::mma_16816(o[m][2 * j + 1], lo[m], vf[2], vf[3]);
+        for (int nt = 0; nt < kNT; ++nt) {
+          ptx::mma_16816(o[dt][nt], vf, ph[nt][0], ph[nt][1]);
+          ptx::mma_16816(o[dt][nt], vf, pl[nt][0], pl[nt][1]);
         }
       }
     } else {
 #pragma unroll 1
       for (int kk = 0; kk < kKeys; ++kk) {
-        const int src = (lane & ~3) | ((kk & 7) >> 1);
+        const int src = ((kk & 7) << 2) | (lane & 3);
 #pragma unroll
-        for (int m = 0; m < kMT; ++m) {
+        for (int nt = 0; nt < kNT; ++nt) {
+          const uint32_t h = __shfl_sync(0xFFFFFFFFu, kk < 8 ? hi[nt][0] : hi[nt][1], src);
+          const uint32_t w = __shfl_sync(0xFFFFFFFFu, kk < 8 ? lo[nt][0] : lo[nt][1], src);
+          const float w0 = __uint_as_float(h << 16) + __uint_as_float(w << 16);
+          const float w1 = __uint_as_float(h & 0xFFFF0000u) + __uint_as_float(w & 0xFFFF0000u);
+          const bool see0 = key0 + kk < lim[nt][0], see1 = key0 + kk < lim[nt][1];
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const uint32_t ph = __shfl_sync(0xFFFFFFFFu, kk < 8 ? hi[m][hf] : hi[m][2 + hf], src);
-            const uint32_t pl = __shfl_sync(0xFFFFFFFFu, kk < 8 ? lo[m][hf] : lo[m][2 + hf], src);
-            const float w = (kk & 1) ? __uint_as_float(ph & 0xFFFF0000u) + __uint_as_float(pl & 0xFFFF0000u)
-                                     : __uint_as_float(ph << 16) + __uint_as_float(pl << 16);
-            if (key0 + kk >= lim[m][hf]) continue;
-#pragma unroll
-            for (int d = 0; d < 16; ++d) {
-              const uint32_t x = ptx::ld_shared_u32(vt + kv_at(kk, d) + 4 * (lane & 3));
-              o[m][d][2 * hf] = fmaf(w, __uint_as_float(x << 16), o[m][d][2 * hf]);
-              o[m][d][2 * hf + 1] = fmaf(w, __uint_as_float(x & 0xFFFF0000u), o[m][d][2 * hf + 1]);
+          for (int dt = 0; dt < 8; ++dt) {
+            const float a = ptx::ld_shared_bf16(vt + kv_at(kk, 2 * dt) + 2 * (lane >> 2));
+            const float c = ptx::ld_shared_bf16(vt + kv_at(kk, 2 * dt + 1) + 2 * (lane >> 2));
+            if (see0) {
+              o[dt][nt][0] = fmaf(w0, a, o[dt][nt][0]);
+              o[dt][nt][2] = fmaf(w0, c, o[dt][nt][2]);
+            }
+            if (see1) {
+              o[dt][nt][1] = fmaf(w1, a, o[dt][nt][1]);
+              o[dt][nt][3] = fmaf(w1, c, o[dt][nt][3]);
             }
           }
         }
@@ -361,21 +379,23 @@ __global__ void __launch_bounds__(kOwnThreads, 2) attn_prefix_own(const OwnParam
   float* ml = reinterpret_cast<float*>(smem_own + kOwnOffMl) + warp * kMaxRows * 2;
   float* mine = reinterpret_cast<float*>(smem_own + warp * kWarpBytes);
 #pragma unroll
-  for (int m = 0; m < kMT; ++m) {
+  for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      float sum = l[m][hf];
-      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-      const int r = 16 * m + (lane >> 2) + 8 * hf;
-      if ((lane & 3) == 0) {
-        ml[2 * r] = mref[m][hf];
+    for (int e = 0; e < 2; ++e) {
+      float sum = l[nt][e];
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 4);
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 8);
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
+      const int r = 8 * nt + 2 * (lane & 3) + e;
+      if ((lane >> 2) == 0) {
+        ml[2 * r] = mref[nt][e];
         ml[2 * r + 1] = sum;
       }
 #pragma unroll
-      for (int d = 0; d < 16; ++d)
-        *reinterpret_cast<float2*>(mine + r * kD + 8 * d + 2 * (lane & 3)) =
-            make_float2(o[m][d][2 * hf], o[m][d][2 * hf + 1]);
+      for (int dt = 0; dt < 8; ++dt) {
+        mine[r * kRowPitch + 16 * dt + (lane >> 2)] = o[dt][nt][e];
+        mine[r * kRowPitch + 16 * dt + 8 + (lane >> 2)] = o[dt][nt][2 + e];
+      }
     }
   }
   __syncthreads();
@@ -396,7 +416,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) attn_prefix_own(const OwnParam
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float f = ptx::ex2(ml4[w].x - ref);
-      const float4 y = reinterpret_cast<const float4*>(smem_own + w * kWarpBytes)[r * (kD / 4) + lane];
+      const float4 y = reinterpret_cast<const float4*>(smem_own + w * kWarpBytes)[r * (kRowPitch / 4) + lane];
       L = fmaf(ml4[w].y, f, L);
       x.x = fmaf(y.x, f, x.x);
       x.y = fmaf(y.y, f, x.y);
