@@ -194,6 +194,17 @@ __global__ void __launch_bounds__(kOwnThreads, 2) attn_prefix_own(const OwnParam
     const size_t at = key * key_stride + 8 * chunk;
     const uint16_t *ks = kb + at, *vs = vb + at;
     const uint32_t dst = lane_dst + s * 2 * kKvBytes;
+    if ((t + 1) * kKeys <= len) {  // a whole tile (most): no key to test
+#pragma unroll
+      for (int u = 0; u < kKeys / 2; ++u) {
+        const uint32_t d = (dst ^ ((2 * u & 6) << 4)) + 512 * u;
+        ptx::cp_async16(d, ks);
+        ptx::cp_async16(d + kKvBytes, vs);
+        ks += 2 * key_stride;
+        vs += 2 * key_stride;
+      }
+      return;
+    }
 #pragma unroll
     for (int u = 0; u < kKeys / 2; ++u) {
       const int ok = key + 2 * u < len;

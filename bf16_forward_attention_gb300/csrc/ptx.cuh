@@ -382,8 +382,13 @@ __device__ __forceinline__ void tmem_wait_st() {
 }
 
 // ---------------------------------------------------------------- warp-level products
-// 16-byte asynchronous copy global -> shared; valid == 0 writes zeros and reads
-// nothing.
+// 16-byte asynchronous copy global -> shared.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src))
+               : "memory");
+}
+
+// The same; valid == 0 writes zeros and reads nothing.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
                "l"(reinterpret_cast<uint64_t>(src)), "r"(valid ? 16 : 0)
