@@ -30,7 +30,13 @@
 // the tcgen05.mma issue (one elected lane, in warp-uniform code). Warps 2-3: check of the tiles where some pairs
 // are hidden (see check_rows / check_keys). Warps 4-7 and 8-11: softmax, each
 // thread one TMEM lane (a key in dkv, a query in dq) and one 64-column half.
-// Every wait is bounded, as in the forward kernel.
+// A CTA works on one item (an owned tile, or a part of its streamed range) after another:
+// it takes over CTAs of its grid that have not been launched yet (cluster launch
+// control), in launch order, so the schedule is the hardware's dynamic one, longest
+// items first, while barriers, tensor memory and the rings live on, the next item's loads
+// start when the last products of this one have read their tiles, and a result is stored
+// while the next item's first products run. (One item per CTA cost 11,000 cycles around
+// each item's loop.) Every wait is bounded, as in the forward kernel.
 #pragma once
 #include "attn_fwd_kernel.cuh"
 
@@ -117,6 +123,45 @@ __device__ __forceinline__ Seq seq_of(const BwdParams& p, int block) {
   return s;
 }
 
+// The items of a CTA, in order, for its warps: item 0 is the CTA's own number, and answer
+// `it` names item it + 1. The producer asks when it has issued an item's last loads, a few
+// tiles before its end: an item claimed earlier would wait for this CTA while others
+// run out of work. Two slots: answer (16 bytes), and per slot a barrier for the answer and one for its readers.
+struct Items {
+  uint32_t resp, full, empty;  // shared-memory addresses of slot 0
+  volatile int* abort_flag;
+  unsigned long long timeout_ns;
+
+  // By the producer's lane.
+  __device__ __forceinline__ void ask(int it) const {
+    const uint32_t slot = it & 1;
+    if (!wait_bounded(empty + 8 * slot, ((it >> 1) & 1) ^ 1, abort_flag, timeout_ns, true)) return;
+    ptx::mbar_arrive_expect_tx(full + 8 * slot, 16);
+    ptx::clc_try_cancel(resp + 16 * slot, full + 8 * slot);
+  }
+  // By one lane of a role: the item after item `it`, -1 at the end.
+  __device__ __forceinline__ int next_lane(int it) const {
+    const uint32_t slot = it & 1;
+    if (!wait_bounded(full + 8 * slot, (it >> 1) & 1, abort_flag, timeout_ns, true)) return -1;
+    const int item = ptx::clc_answer(resp + 16 * slot);
+    ptx::fence_proxy_async_smem();  // the read, before the slot's next answer
+    ptx::mbar_arrive(empty + 8 * slot);
+    return item;
+  }
+  // By a whole warp.
+  __device__ __forceinline__ int next_warp(int it, int lane) const {
+    const uint32_t slot = it & 1;
+    if (!warp_wait(full + 8 * slot, (it >> 1) & 1, abort_flag, timeout_ns)) return -1;
+    const int item = ptx::clc_answer(resp + 16 * slot);
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(empty + 8 * slot);
+    return __shfl_sync(0xFFFFFFFFu, item, 0);
+  }
+};
+// Readers of an answer: producer, MMA warp, softmax warps, and the check's.
+__host__ __device__ constexpr int item_readers(bool check) { return 10 + (check ? 2 : 0); }
+
 // Part `split` of n streamed tiles: [first, first + count).
 __device__ __forceinline__ void part_of(int n, int splits, int split, int& first, int& count) {
   const int base = n / splits, rem = n % splits;
@@ -127,11 +172,17 @@ __device__ __forceinline__ void part_of(int n, int splits, int split, int& first
 // 64 columns of a TMEM row as 32 packed pairs of fp32.
 using Half = uint64_t[32];
 
-__device__ __forceinline__ void load_half(uint32_t taddr, uint32_t (&a)[32], uint32_t (&b)[32]) {
+// Runs half(ch, r) on the 32-column halves of a 64-column TMEM row: the second is loaded
+// while the first is worked on.
+template <typename F>
+__device__ __forceinline__ void by_halves(uint32_t taddr, F half) {
+  uint32_t a[32], b[32];
   ptx::tmem_ld32_nowait(taddr, a);
-  ptx::tmem_ld32_nowait(taddr + 32, b);
   ptx::tmem_wait_ld32(a);
-  ptx::reg_fence32(b);
+  ptx::tmem_ld32_nowait(taddr + 32, b);
+  half(0, a);
+  ptx::tmem_wait_ld32(b);
+  half(1, b);
 }
 
 // acc += A[tmem: 128 x 128 bf16] * B[smem, MN-major]: 8 MMAs of K = 16. A's columns
@@ -177,6 +228,19 @@ __device__ __forceinline__ void clean_row(uint32_t tile, int r, F with_col) {
     }
     if (dirty) ptx::st_shared_v4(tile + chunk_at(r, c), w[0], w[1], w[2], w[3]);
   }
+}
+
+// Records of non-finite elements found in masked tiles, for two items: per result column
+// the last (or first) row that has one, and whether there is any.
+constexpr int kPoisonWords = kD + 4, kPoisonBytes = 2 * kPoisonWords * 4;
+
+// By the 256 softmax threads, which all found the record set: once every one has read it.
+__device__ __forceinline__ void clear_poison(int* rec, int none) {
+  ptx::named_barrier_sync(3, 256);
+  const int t = static_cast<int>(threadIdx.x) - 32 * kSoftmaxWarp0;
+  if (t < kD) rec[t] = none;
+  if (t == kD) rec[kD] = 0;
+  ptx::named_barrier_sync(3, 256);
 }
 
 // TMA load of one 128 x 128 tile (two 64-column boxes).
@@ -269,10 +333,7 @@ __device__ __forceinline__ uint64_t pair_of(const uint32_t (&r)[32], int x) {
 template <bool kMask>
 __device__ __forceinline__ void dkv_p(uint32_t tS, const ulonglong2* stat, uint64_t c2, int lo, int hi,
                                       Half& pr) {
-  uint32_t a[32], b[32];
-  load_half(tS, a, b);
-#pragma unroll
-  for (int ch = 0; ch < 2; ++ch) {
+  by_halves(tS, [&](int ch, const uint32_t (&r)[32]) {
     uint32_t w[16];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -281,7 +342,7 @@ __device__ __forceinline__ void dkv_p(uint32_t tS, const ulonglong2* stat, uint6
       for (int u = 0; u < 2; ++u) {
         const int x = 4 * e + 2 * u;
         float t0, t1;
-        ptx::f2_unpack(ptx::f2_fma(pair_of(ch ? b : a, x), c2, u ? nl.y : nl.x), t0, t1);
+        ptx::f2_unpack(ptx::f2_fma(pair_of(r, x), c2, u ? nl.y : nl.x), t0, t1);
         float p0 = ptx::ex2(t0), p1 = ptx::ex2(t1);
         if (kMask) {
           const int col = 32 * ch + x;
@@ -293,16 +354,13 @@ __device__ __forceinline__ void dkv_p(uint32_t tS, const ulonglong2* stat, uint6
       }
     }
     ptx::tmem_st16(tS + 16 * ch, w);
-  }
+  });
 }
 
 // dkv: dS from dP and P, written over dP as bf16.
 template <bool kMask>
 __device__ __forceinline__ void dkv_ds(uint32_t tP, const ulonglong2* stat, int lo, int hi, const Half& pr) {
-  uint32_t a[32], b[32];
-  load_half(tP, a, b);
-#pragma unroll
-  for (int ch = 0; ch < 2; ++ch) {
+  by_halves(tP, [&](int ch, const uint32_t (&r)[32]) {
     uint32_t w[16];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -312,7 +370,7 @@ __device__ __forceinline__ void dkv_ds(uint32_t tP, const ulonglong2* stat, int 
         const int x = 4 * e + 2 * u;
         float s0, s1;
         ptx::f2_unpack(
-            ptx::f2_mul(pr[16 * ch + 2 * e + u], ptx::f2_add(pair_of(ch ? b : a, x), u ? nd.y : nd.x)), s0, s1);
+            ptx::f2_mul(pr[16 * ch + 2 * e + u], ptx::f2_add(pair_of(r, x), u ? nd.y : nd.x)), s0, s1);
         if (kMask) {
           const int col = 32 * ch + x;
           if (col < lo || col >= hi) s0 = 0.f;
@@ -322,21 +380,18 @@ __device__ __forceinline__ void dkv_ds(uint32_t tP, const ulonglong2* stat, int 
       }
     }
     ptx::tmem_st16(tP + 16 * ch, w);
-  }
+  });
 }
 
 // dq: dS from dP and P (a lane's query against 64 keys), written over S as bf16.
 template <bool kMask>
 __device__ __forceinline__ void dq_ds(uint32_t tP, uint32_t tS, uint64_t nd2, int hi, const Half& pr) {
-  uint32_t a[32], b[32];
-  load_half(tP, a, b);
-#pragma unroll
-  for (int ch = 0; ch < 2; ++ch) {
+  by_halves(tP, [&](int ch, const uint32_t (&r)[32]) {
     uint32_t w[16];
 #pragma unroll
     for (int x = 0; x < 16; ++x) {
       float s0, s1;
-      ptx::f2_unpack(ptx::f2_mul(pr[16 * ch + x], ptx::f2_add(pair_of(ch ? b : a, 2 * x), nd2)), s0, s1);
+      ptx::f2_unpack(ptx::f2_mul(pr[16 * ch + x], ptx::f2_add(pair_of(r, 2 * x), nd2)), s0, s1);
       if (kMask) {
         if (32 * ch + 2 * x >= hi) s0 = 0.f;
         if (32 * ch + 2 * x + 1 >= hi) s1 = 0.f;
@@ -344,7 +399,7 @@ __device__ __forceinline__ void dq_ds(uint32_t tP, uint32_t tS, uint64_t nd2, in
       w[x] = ptx::pack_bf16x2(s0, s1);
     }
     ptx::tmem_st16(tS + 16 * ch, w);
-  }
+  });
 }
 
 // ---------------------------------------------------------------- dK and dV
@@ -363,6 +418,7 @@ __device__ __forceinline__ void dq_ds(uint32_t tP, uint32_t tS, uint64_t nd2, in
 constexpr int kDkvStages = 2;
 enum : int {
   kDkvKV = 0,
+  kDkvKVFree,   // the item's last S and dP products have read K and V
   kDkvQFull,
   kDkvQEmpty = kDkvQFull + kDkvStages,
   kDkvOFull = kDkvQEmpty + kDkvStages,
@@ -372,34 +428,64 @@ enum : int {
   kDkvDpFull,
   kDkvDsFull,
   kDkvAcc,
+  kDkvAccFree,  // the epilogue has read dK and dV
   kDkvLanded,
   kDkvChecked,
   kDkvDrain,
-  kDkvBars
+  kDkvItemFull,
+  kDkvItemEmpty = kDkvItemFull + 2,
+  kDkvBars = kDkvItemEmpty + 2
 };
 constexpr int kDkvOffK = 0, kDkvOffV = kTileBytes, kDkvOffQ = 2 * kTileBytes,
               kDkvOffO = kDkvOffQ + kDkvStages * kTileBytes,
               kDkvOffStats = kDkvOffO + kDkvStages * kTileBytes,
-              kDkvOffPoison = kDkvOffStats + kDkvStages * kStatFloats * 4,
-              kDkvOffBar = kDkvOffPoison + kD * 4 + 16, kDkvOffSlot = kDkvOffBar + kDkvBars * 8,
-              kDkvSmem = kDkvOffSlot + 8 + 1024;
+              kDkvOffItems = kDkvOffStats + kDkvStages * kStatFloats * 4,
+              kDkvOffPoison = kDkvOffItems + 32, kDkvOffBar = kDkvOffPoison + kPoisonBytes,
+              kDkvOffSlot = kDkvOffBar + kDkvBars * 8, kDkvSmem = kDkvOffSlot + 8 + 1024;
 static_assert(kDkvSmem <= 232448, "shared memory budget (dkv)");
 
-// The streamed tiles of a CTA: `per` query tiles from first_qt on, for each query
-// head of the group.
-struct DkvRange {
+// An item: an owned key tile and the part of its streamed tiles: query tiles from first_qt
+// on, for each query head of the group, n of them from number t0 on (skip: nothing
+// to do, not even a zero to store).
+struct DkvItem {
+  Seq s;
   int first_qt, per, t0, n;
+  int off, k0;  // key j is visible to query i iff j <= i + off (causal); the tile's first key
+  bool skip;
 };
-template <bool kCausal>
-__device__ __forceinline__ DkvRange dkv_range(const BwdParams& p, const Seq& s) {
-  DkvRange r;
+
+template <bool kCausal, bool kVarlen>
+__device__ __forceinline__ DkvItem dkv_item(const BwdParams& p, int item) {
+  DkvItem r;
+  r.s = seq_of<kCausal, kVarlen, false>(p, item);
+  const Seq& s = r.s;
+  r.off = s.sk - s.sq;
+  r.k0 = s.tile * kTile;
+  r.skip = kVarlen && (s.bad || r.k0 >= s.sk);
   const int nqt = (s.sq + kTile - 1) / kTile;
-  r.first_qt = 0;
-  if (kCausal) r.first_qt = min(max(0, s.tile * kTile - (s.sk - s.sq)) / kTile, nqt);
+  r.first_qt = kCausal ? min(max(0, r.k0 - r.off) / kTile, nqt) : 0;
   r.per = nqt - r.first_qt;
   part_of(r.per * p.group, p.n_splits, s.split, r.t0, r.n);
+  if (r.skip) r.n = 0;
   return r;
 }
+
+// A tile some of whose pairs are hidden: crossed by the diagonal, or past the end.
+template <bool kCausal>
+__device__ __forceinline__ bool dkv_masked(int q0, int sq, int off, int k0) {
+  return q0 + kTile > sq || (kCausal && q0 + off < k0 + kTile - 1);
+}
+
+// First query of the item's streamed tiles, one after another (no division per tile).
+struct QueryTiles {
+  int q0, first, last;
+  __device__ __forceinline__ explicit QueryTiles(const DkvItem& w) {
+    first = w.first_qt * kTile;
+    last = (w.first_qt + w.per - 1) * kTile;
+    q0 = w.n > 0 ? (w.first_qt + w.t0 % w.per) * kTile : 0;
+  }
+  __device__ __forceinline__ void step() { q0 = q0 == last ? first : q0 + kTile; }
+};
 
 template <bool kCausal, bool kVarlen>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -412,42 +498,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_raw + (sbase - raw);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kDkvOffSlot);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kDkvOffSlot + 4);
-  int* poison_q = reinterpret_cast<int*>(smem + kDkvOffPoison);
-  volatile int* poison_any = poison_q + kD;
+  int* poison = reinterpret_cast<int*>(smem + kDkvOffPoison);
   auto bar = [&](int i) -> uint32_t { return sbase + kDkvOffBar + 8u * static_cast<uint32_t>(i); };
   // (Through a shuffle, so that the compiler knows it to be the same on every lane.)
   const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   constexpr bool kCheck = kCausal || kVarlen;
-
-  const Seq s = seq_of<kCausal, kVarlen, false>(p, static_cast<int>(blockIdx.x));
-  if (kVarlen) {
-    if (s.bad) {
-      if (threadIdx.x == 0) atomicOr(&g_attn_status, 2u);
-      ptx::grid_dependency_wait();
-      return;
-    }
-    if (s.tile * kTile >= s.sk) {
-      ptx::grid_dependency_wait();
-      return;
-    }
-  }
-  const DkvRange rg = dkv_range<kCausal>(p, s);
-  const int off = s.sk - s.sq;   // key j is visible to query i iff j <= i + off (causal)
-  const int k0 = s.tile * kTile; // first key of the tile
-  // A tile some of whose pairs are hidden: crossed by the diagonal, or past the end.
-  auto masked = [&](int q0) -> bool {
-    return q0 + kTile > s.sq || (kCausal && q0 + off < k0 + kTile - 1);
-  };
+  const Items items{sbase + kDkvOffItems, bar(kDkvItemFull), bar(kDkvItemEmpty), abort_flag, p.timeout_ns};
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kDkvBars; ++i)
-      ptx::mbar_init(bar(i), (i == kDkvPFull || i == kDkvDsFull) ? 8 : 1);
+      ptx::mbar_init(bar(i), (i == kDkvPFull || i == kDkvDsFull || i == kDkvAccFree) ? 8
+                             : i >= kDkvItemEmpty                                    ? item_readers(kCheck)
+                                                                                     : 1);
     *abort_flag = 0;
-    *poison_any = 0;
     ptx::fence_mbar_init();
     ptx::fence_proxy_async_smem();
   }
-  if (threadIdx.x < kD) poison_q[threadIdx.x] = -1;
+  for (int i = threadIdx.x; i < 2 * kPoisonWords; i += kThreads) poison[i] = i % kPoisonWords < kD ? -1 : 0;
   if (warp == 0 && lane == 0) {
     ptx::prefetch_tmap(&tm_q);
     ptx::prefetch_tmap(&tm_k);
@@ -464,41 +531,61 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const uint32_t tS = tmem, tP = tmem + 128, tK = tmem + 256, tV = tmem + 384;
 
+  // In every role: `used` counts the items with streamed tiles so far (the phases of the
+  // per-item barriers), `tile` their streamed tiles (the phases of the per-tile ones;
+  // tile t goes to ring stage t % kDkvStages).
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
-    if (lane == 0 && rg.n > 0) {
+    if (lane == 0) {
       const uint64_t pol_once = ptx::l2_policy_evict_first();
       const uint64_t pol_reuse = ptx::l2_policy_evict_last();
-      dbg_ok(s.k_base + k0 < p.Sk);
-      ptx::mbar_arrive_expect_tx(bar(kDkvKV), 2 * kTileBytes);
-      load_tile(sbase + kDkvOffK, &tm_k, bar(kDkvKV), p.layout, s.k_base + k0, s.head, s.batch, pol_once);
-      load_tile(sbase + kDkvOffV, &tm_v, bar(kDkvKV), p.layout, s.k_base + k0, s.head, s.batch, pol_once);
-      ptx::grid_dependency_wait();  // the row statistics
-      int q_issued = 0, o_issued = 0;
-      for (int i = 0; i < rg.n; ++i) {
-        const int st = i % kDkvStages;
-        const uint32_t par = ((i / kDkvStages) & 1) ^ 1;
-        const int t = rg.t0 + i;
-        const int h = s.head * p.group + t / rg.per;
-        const int qt = rg.first_qt + t % rg.per;
-        dbg_ok(s.q_base + qt * kTile < p.Sq && h < p.Hq);
-        if (!wait_bounded(bar(kDkvQEmpty + st), par, abort_flag, p.timeout_ns, true)) break;
-        ptx::mbar_arrive_expect_tx(bar(kDkvQFull + st), kTileBytes + kStatFloats * 4);
-        load_tile(sbase + kDkvOffQ + st * kTileBytes, &tm_q, bar(kDkvQFull + st), p.layout,
-                  s.q_base + qt * kTile, h, s.batch, pol_reuse);
-        const float* src = p.stats + (static_cast<size_t>(s.slot_q) + static_cast<size_t>(h) * p.q_slots + qt) *
-                                         kStatFloats;
-        ptx::bulk_load(sbase + kDkvOffStats + st * kStatFloats * 4, src, kStatFloats * 4,
-                       bar(kDkvQFull + st));
-        ++q_issued;
-        if (!wait_bounded(bar(kDkvOEmpty + st), par, abort_flag, p.timeout_ns, true)) break;
-        ptx::mbar_arrive_expect_tx(bar(kDkvOFull + st), kTileBytes);
-        load_tile(sbase + kDkvOffO + st * kTileBytes, &tm_do, bar(kDkvOFull + st), p.layout,
-                  s.q_base + qt * kTile, h, s.batch, pol_reuse);
-        ++o_issued;
+      int used = 0, q_issued = 0, o_issued = 0, asked = 0;
+      bool ok = true;
+      for (int item = static_cast<int>(blockIdx.x), it = 0; ok && item >= 0; ++it) {
+        const DkvItem w = dkv_item<kCausal, kVarlen>(p, item);
+        const Seq& s = w.s;
+        if (kVarlen && s.bad) atomicOr(&g_attn_status, 2u);
+        if (w.n > 0) {
+          if (used > 0 && !(ok = wait_bounded(bar(kDkvKVFree), (used - 1) & 1, abort_flag, p.timeout_ns, true)))
+            break;
+          dbg_ok(s.k_base + w.k0 < p.Sk);
+          ptx::mbar_arrive_expect_tx(bar(kDkvKV), 2 * kTileBytes);
+          load_tile(sbase + kDkvOffK, &tm_k, bar(kDkvKV), p.layout, s.k_base + w.k0, s.head, s.batch, pol_once);
+          load_tile(sbase + kDkvOffV, &tm_v, bar(kDkvKV), p.layout, s.k_base + w.k0, s.head, s.batch, pol_once);
+          if (used == 0) ptx::grid_dependency_wait();  // the row statistics
+          ++used;
+          QueryTiles qt(w);
+          int h = s.head * p.group + w.t0 / w.per;
+          for (int i = 0; i < w.n; ++i) {
+            const int st = q_issued % kDkvStages;
+            const uint32_t par = ((q_issued / kDkvStages) & 1) ^ 1;
+            dbg_ok(s.q_base + qt.q0 < p.Sq && h < p.Hq);
+            if (!(ok = wait_bounded(bar(kDkvQEmpty + st), par, abort_flag, p.timeout_ns, true))) break;
+            ptx::mbar_arrive_expect_tx(bar(kDkvQFull + st), kTileBytes + kStatFloats * 4);
+            load_tile(sbase + kDkvOffQ + st * kTileBytes, &tm_q, bar(kDkvQFull + st), p.layout,
+                      s.q_base + qt.q0, h, s.batch, pol_reuse);
+            const float* src = p.stats + (static_cast<size_t>(s.slot_q) + static_cast<size_t>(h) * p.q_slots +
+                                          qt.q0 / kTile) * kStatFloats;
+            ptx::bulk_load(sbase + kDkvOffStats + st * kStatFloats * 4, src, kStatFloats * 4,
+                           bar(kDkvQFull + st));
+            ++q_issued;
+            if (!(ok = wait_bounded(bar(kDkvOEmpty + st), par, abort_flag, p.timeout_ns, true))) break;
+            ptx::mbar_arrive_expect_tx(bar(kDkvOFull + st), kTileBytes);
+            load_tile(sbase + kDkvOffO + st * kTileBytes, &tm_do, bar(kDkvOFull + st), p.layout,
+                      s.q_base + qt.q0, h, s.batch, pol_reuse);
+            ++o_issued;
+            if (qt.q0 == qt.last) ++h;
+            qt.step();
+          }
+          if (!ok) break;
+        }
+        items.ask(it);
+        ++asked;
+        item = items.next_lane(it);
       }
-      // Every copy this thread started lands before the CTA can exit.
-      wait_bounded(bar(kDkvKV), 0, abort_flag, p.timeout_ns, false);
+      // Every copy this thread started lands before the CTA can exit, and so does the
+      // last answer asked for.
+      if (used > 0) wait_bounded(bar(kDkvKV), (used - 1) & 1, abort_flag, p.timeout_ns, false);
       for (int st = 0; st < kDkvStages; ++st) {
         if (st < q_issued)
           wait_bounded(bar(kDkvQFull + st), ((q_issued - 1 - st) / kDkvStages) & 1, abort_flag,
@@ -507,56 +594,72 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_bounded(bar(kDkvOFull + st), ((o_issued - 1 - st) / kDkvStages) & 1, abort_flag,
                        p.timeout_ns, false);
       }
+      if (asked > 0)
+        wait_bounded(items.full + 8 * ((asked - 1) & 1), ((asked - 1) >> 1) & 1, abort_flag, p.timeout_ns, false);
     }
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer (whole warp)
-    if (rg.n > 0) {
-      const uint32_t k_desc = desc_lo(sbase + kDkvOffK, 16), v_desc = desc_lo(sbase + kDkvOffV, 16);
-      auto q_tile = [&](int i) -> uint32_t { return sbase + kDkvOffQ + (i % kDkvStages) * kTileBytes; };
-      auto o_tile = [&](int i) -> uint32_t { return sbase + kDkvOffO + (i % kDkvStages) * kTileBytes; };
-      auto wait = [&](int b, uint32_t par) -> bool {
-        const bool r = warp_wait(bar(b), par & 1, abort_flag, p.timeout_ns);
-        ptx::tc_fence_after();
-        return r;
-      };
-      int checks = 0;
-      // S_i: Q_i has landed; a masked tile's rows have been checked first (both of
-      // its tiles, so dO_i has landed too).
-      auto do_s = [&](int i) -> bool {
-        if (!wait(kDkvQFull + i % kDkvStages, i / kDkvStages)) return false;
-        if (kCheck && masked((rg.first_qt + (rg.t0 + i) % rg.per) * kTile)) {
-          if (!wait(kDkvOFull + i % kDkvStages, i / kDkvStages)) return false;
-          if (lane == 0) ptx::mbar_arrive(bar(kDkvLanded));
-          if (!wait(kDkvChecked, checks)) return false;
-          ++checks;
+    const uint32_t k_desc = desc_lo(sbase + kDkvOffK, 16), v_desc = desc_lo(sbase + kDkvOffV, 16);
+    auto q_tile = [&](int t) -> uint32_t { return sbase + kDkvOffQ + (t % kDkvStages) * kTileBytes; };
+    auto o_tile = [&](int t) -> uint32_t { return sbase + kDkvOffO + (t % kDkvStages) * kTileBytes; };
+    auto wait = [&](int b, uint32_t par) -> bool {
+      const bool r = warp_wait(bar(b), par & 1, abort_flag, p.timeout_ns);
+      ptx::tc_fence_after();
+      return r;
+    };
+    int used = 0, tile = 0, checks = 0;
+    bool ok = true;
+    for (int item = static_cast<int>(blockIdx.x), it = 0; ok && item >= 0; ++it) {
+      const DkvItem w = dkv_item<kCausal, kVarlen>(p, item);
+      if (w.n > 0) {
+        QueryTiles qt(w);  // of the next S
+        // S_i: Q_i has landed; a masked tile's rows have been checked first (both of
+        // its tiles, so dO_i has landed too).
+        auto do_s = [&](int t) -> bool {
+          if (!wait(kDkvQFull + t % kDkvStages, t / kDkvStages)) return false;
+          if (kCheck && dkv_masked<kCausal>(qt.q0, w.s.sq, w.off, w.k0)) {
+            if (!wait(kDkvOFull + t % kDkvStages, t / kDkvStages)) return false;
+            if (lane == 0) ptx::mbar_arrive(bar(kDkvLanded));
+            if (!wait(kDkvChecked, checks)) return false;
+            ++checks;
+          }
+          qt.step();
+          issue_s(tS, k_desc, desc_lo(q_tile(t), 16));
+          ptx::mma_commit_warp(bar(kDkvSFull));
+          return true;
+        };
+        auto do_dp = [&](int t) -> bool {
+          if (!wait(kDkvOFull + t % kDkvStages, t / kDkvStages)) return false;
+          issue_s(tP, v_desc, desc_lo(o_tile(t), 16));
+          ptx::mma_commit_warp(bar(kDkvDpFull));
+          return true;
+        };
+        ok = wait(kDkvKV, used) && do_s(tile) && do_dp(tile);
+        if (ok && w.n == 1) ptx::mma_commit_warp(bar(kDkvKVFree));
+        for (int i = 0; ok && i < w.n; ++i) {
+          const int t = tile + i;
+          const bool more = i + 1 < w.n;
+          if (!(ok = wait(kDkvPFull, t))) break;
+          // The item's first second product starts dV (and dK) anew.
+          if (i == 0 && used > 0 && !(ok = wait(kDkvAccFree, used - 1))) break;
+          issue_second(tV, tS, desc_lo(o_tile(t), kHalfBytes), i > 0);
+          ptx::mma_commit_warp(bar(kDkvOEmpty + t % kDkvStages));
+          if (more && !(ok = do_s(t + 1))) break;
+          if (!(ok = wait(kDkvDsFull, t))) break;
+          issue_second(tK, tP, desc_lo(q_tile(t), kHalfBytes), i > 0);
+          ptx::mma_commit_warp(bar(kDkvQEmpty + t % kDkvStages));
+          if (more && !(ok = do_dp(t + 1))) break;
+          if (i + 2 == w.n) ptx::mma_commit_warp(bar(kDkvKVFree));  // the last dP was issued
         }
-        issue_s(tS, k_desc, desc_lo(q_tile(i), 16));
-        ptx::mma_commit_warp(bar(kDkvSFull));
-        return true;
-      };
-      auto do_dp = [&](int i) -> bool {
-        if (!wait(kDkvOFull + i % kDkvStages, i / kDkvStages)) return false;
-        issue_s(tP, v_desc, desc_lo(o_tile(i), 16));
-        ptx::mma_commit_warp(bar(kDkvDpFull));
-        return true;
-      };
-      bool ok = wait(kDkvKV, 0) && do_s(0) && do_dp(0);
-      for (int i = 0; ok && i < rg.n; ++i) {
-        const bool more = i + 1 < rg.n;
-        if (!(ok = wait(kDkvPFull, i))) break;
-        issue_second(tV, tS, desc_lo(o_tile(i), kHalfBytes), i > 0);
-        ptx::mma_commit_warp(bar(kDkvOEmpty + i % kDkvStages));
-        if (more && !(ok = do_s(i + 1))) break;
-        if (!(ok = wait(kDkvDsFull, i))) break;
-        issue_second(tK, tP, desc_lo(q_tile(i), kHalfBytes), i > 0);
-        ptx::mma_commit_warp(bar(kDkvQEmpty + i % kDkvStages));
-        if (more && !(ok = do_dp(i + 1))) break;
+        if (ok) ptx::mma_commit_warp(bar(kDkvAcc));
+        tile += w.n;
+        ++used;
       }
-      if (ok) ptx::mma_commit_warp(bar(kDkvAcc));
-      ptx::mma_commit_warp(bar(kDkvDrain));
-      wait_bounded(bar(kDkvDrain), 0, abort_flag, p.timeout_ns, false);
+      if (ok) item = items.next_warp(it, lane);
     }
+    ptx::mma_commit_warp(bar(kDkvDrain));
+    wait_bounded(bar(kDkvDrain), 0, abort_flag, p.timeout_ns, false);  // every MMA is done
     __syncwarp();
   } else if (warp < kSoftmaxWarp0) {
     // ------------------------------------------------ check of the masked tiles (warps 2-3)
@@ -566,42 +669,54 @@ __global__ void __launch_bounds__(kThreads, 1)
     // with a non-finite element has a NaN among its statistics; its non-finite
     // elements are set to 0 as well. The keys that do see it still get NaN: in
     // every column of dK (and of dV, when it is Q) through the statistics, and in
-    // the column of a non-finite dO element through poison_q, the last row that
-    // has one there.
+    // the column of a non-finite dO element through `poison`, the last row that has
+    // one there. Two items' records are kept, for the one being finished and the next;
+    // an item's epilogue clears its own.
     if constexpr (kCheck) {
       const int tid = static_cast<int>(threadIdx.x) - 64;
-      int m = 0;
-      for (int i = 0; i < rg.n; ++i) {
-        const int q0 = (rg.first_qt + (rg.t0 + i) % rg.per) * kTile;
-        if (!masked(q0)) continue;
-        const bool ok = wait_bounded(bar(kDkvLanded), m & 1, abort_flag, p.timeout_ns, true);
-        if (ptx::named_barrier_or(1, 64, !ok)) break;
-        ++m;
-        const int st = i % kDkvStages;
-        const uint32_t qt = sbase + kDkvOffQ + st * kTileBytes, ot = sbase + kDkvOffO + st * kTileBytes;
-        const float* stat = reinterpret_cast<const float*>(smem + kDkvOffStats) + st * kStatFloats;
-        bool dirty = false;
-        for (int r = tid; r < kTile; r += 64) {
-          const float nl = stat[r], nd = stat[kTile + r];
-          const bool past = q0 + r >= s.sq;  // (zero already in a dense tensor's tile)
-          if (past && !kVarlen) continue;
-          if (past || nl == -__int_as_float(0x7F800000)) {
-            zero_row(qt, r);
-            zero_row(ot, r);
-            dirty = true;
-          } else if (isnan(nl) || isnan(nd)) {
-            clean_row(qt, r, [](int) {});
-            clean_row(ot, r, [&](int col) {
-              atomicMax(&poison_q[col], q0 + r);
-              *poison_any = 1;
-            });
-            dirty = true;
+      int used = 0, tile = 0, m = 0;
+      bool ok = true;
+      for (int item = static_cast<int>(blockIdx.x), it = 0; ok && item >= 0; ++it) {
+        const DkvItem w = dkv_item<kCausal, kVarlen>(p, item);
+        const Seq& s = w.s;
+        int* rec = poison + (used & 1) * kPoisonWords;
+        QueryTiles qt(w);
+        for (int i = 0; i < w.n; ++i, qt.step()) {
+          const int q0 = qt.q0;
+          if (!dkv_masked<kCausal>(q0, s.sq, w.off, w.k0)) continue;
+          ok = wait_bounded(bar(kDkvLanded), m & 1, abort_flag, p.timeout_ns, true);
+          ok = !ptx::named_barrier_or(1, 64, !ok);
+          if (!ok) break;
+          ++m;
+          const int st = (tile + i) % kDkvStages;
+          const uint32_t q_t = sbase + kDkvOffQ + st * kTileBytes, o_t = sbase + kDkvOffO + st * kTileBytes;
+          const float* stat = reinterpret_cast<const float*>(smem + kDkvOffStats) + st * kStatFloats;
+          bool dirty = false;
+          for (int r = tid; r < kTile; r += 64) {
+            const float nl = stat[r], nd = stat[kTile + r];
+            const bool past = q0 + r >= s.sq;  // (zero already in a dense tensor's tile)
+            if (past && !kVarlen) continue;
+            if (past || nl == -__int_as_float(0x7F800000)) {
+              zero_row(q_t, r);
+              zero_row(o_t, r);
+              dirty = true;
+            } else if (isnan(nl) || isnan(nd)) {
+              clean_row(q_t, r, [](int) {});
+              clean_row(o_t, r, [&](int col) {
+                atomicMax(&rec[col], q0 + r);
+                *static_cast<volatile int*>(rec + kD) = 1;
+              });
+              dirty = true;
+            }
           }
+          if (dirty) ptx::fence_proxy_async_smem();
+          __syncwarp();
+          ptx::named_barrier_sync(1, 64);
+          if (tid == 0) ptx::mbar_arrive(bar(kDkvChecked));
         }
-        if (dirty) ptx::fence_proxy_async_smem();
-        __syncwarp();
-        ptx::named_barrier_sync(1, 64);
-        if (tid == 0) ptx::mbar_arrive(bar(kDkvChecked));
+        tile += w.n;
+        if (w.n > 0) ++used;
+        if (ok) item = items.next_warp(it, lane);
       }
     }
   } else {
@@ -612,64 +727,85 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tSh = tS + lane_base + 64 * g, tPh = tP + lane_base + 64 * g;
     const uint64_t c2 = ptx::f2_pack(p.c, p.c);
+    int used = 0, tile = 0;
     bool ok = true;
-    int q0 = rg.n > 0 ? (rg.first_qt + rg.t0 % rg.per) * kTile : 0;  // the tile's first query
-    const int q_last = (rg.first_qt + rg.per - 1) * kTile;           // of a head
-    for (int i = 0; i < rg.n; ++i, q0 = q0 == q_last ? rg.first_qt * kTile : q0 + kTile) {
-      const bool mk = masked(q0);
-      // The columns of this half that this key is visible to: [lo, hi).
-      const int lo = kCausal ? k0 + row - off - q0 - 64 * g : 0;
-      const int hi = s.sq - q0 - 64 * g;
-      const ulonglong2* stat = reinterpret_cast<const ulonglong2*>(
-          smem + kDkvOffStats + (i % kDkvStages) * kStatFloats * 4 + 256 * g);
-      Half pr;
-      if (!(ok = warp_wait(bar(kDkvSFull), i & 1, abort_flag, p.timeout_ns))) break;
-      // (Q's barrier, for the statistics that landed with it: long complete.)
-      if (!(ok = warp_wait(bar(kDkvQFull + i % kDkvStages), (i / kDkvStages) & 1, abort_flag,
-                           p.timeout_ns)))
-        break;
-      ptx::tc_fence_after();
-      if (mk)
-        dkv_p<true>(tSh, stat, c2, lo, hi, pr);
-      else
-        dkv_p<false>(tSh, stat, c2, lo, hi, pr);
-      ptx::tmem_wait_st();
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar(kDkvPFull));
+    for (int item = static_cast<int>(blockIdx.x), it = 0; ok && item >= 0; ++it) {
+      const DkvItem w = dkv_item<kCausal, kVarlen>(p, item);
+      const int first_row = w.k0 + row - w.off;  // the first query that sees this key (causal)
+      const int n = w.n, sq = w.s.sq, off = w.off, k0 = w.k0;
+      QueryTiles qt(w);
+      for (int i = 0; i < n; ++i, ++tile, qt.step()) {
+        const bool mk = dkv_masked<kCausal>(qt.q0, sq, off, k0);
+        // The columns of this half that this key is visible to: [lo, hi).
+        const int lo = kCausal ? first_row - qt.q0 - 64 * g : 0;
+        const int hi = sq - qt.q0 - 64 * g;
+        const ulonglong2* stat = reinterpret_cast<const ulonglong2*>(
+            smem + kDkvOffStats + (tile % kDkvStages) * kStatFloats * 4 + 256 * g);
+        Half pr;
+        if (!(ok = warp_wait(bar(kDkvSFull), tile & 1, abort_flag, p.timeout_ns))) break;
+        // (Q's barrier, for the statistics that landed with it: long complete.)
+        if (!(ok = warp_wait(bar(kDkvQFull + tile % kDkvStages), (tile / kDkvStages) & 1, abort_flag,
+                             p.timeout_ns)))
+          break;
+        ptx::tc_fence_after();
+        if (mk)
+          dkv_p<true>(tSh, stat, c2, lo, hi, pr);
+        else
+          dkv_p<false>(tSh, stat, c2, lo, hi, pr);
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(kDkvPFull));
 
-      if (!(ok = warp_wait(bar(kDkvDpFull), i & 1, abort_flag, p.timeout_ns))) break;
-      ptx::tc_fence_after();
-      if (mk)
-        dkv_ds<true>(tPh, stat, lo, hi, pr);
-      else
-        dkv_ds<false>(tPh, stat, lo, hi, pr);
-      ptx::tmem_wait_st();
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar(kDkvDsFull));
-    }
-    // ---- epilogue: warpgroup 0 stores dK, warpgroup 1 dV.
-    if (ok && rg.n > 0) ok = warp_wait(bar(kDkvAcc), 0, abort_flag, p.timeout_ns);
-    if (ok) {
-      ptx::tc_fence_after();
-      const uint32_t tacc = (g == 0 ? tK : tV) + lane_base;
-      const bool zero = rg.n == 0;
-      // The last query row whose non-finite dO element a key may see (see above).
-      const int seen = kCausal ? max(0, k0 + row - off) : 0;
-      auto poison = [&](int col) -> bool { return kCheck && g == 1 && poison_q[col] >= seen; };
-      if (p.n_splits == 1) {
-        const bool in = k0 + row < s.sk && dbg_ok(s.k_base + k0 + row < p.Sk);
-        uint16_t* dst = (g == 0 ? p.dk : p.dv) +
-                        row_at(p.layout, s.batch, p.Hkv, p.Sk, s.head, s.k_base + k0 + (in ? row : 0));
-        store_row<kD>(tacc, zero, g == 0 ? p.scale : 1.f, p.mode, in ? dst : nullptr,
-                      kCheck && g == 1 && *poison_any, poison);
-      } else {
-        const size_t slots = static_cast<size_t>(p.k_slots) * (kVarlen ? p.Hkv : p.BH);
-        const size_t slot = static_cast<size_t>(s.slot_k) + static_cast<size_t>(s.head) * p.k_slots + s.tile;
-        float* dst = p.part + (((static_cast<size_t>(s.split) * 2 + g) * slots + slot) * kTile + row) * kD;
-        store_part<kD>(tacc, zero, dst, poison);
+        if (!(ok = warp_wait(bar(kDkvDpFull), tile & 1, abort_flag, p.timeout_ns))) break;
+        ptx::tc_fence_after();
+        if (mk)
+          dkv_ds<true>(tPh, stat, lo, hi, pr);
+        else
+          dkv_ds<false>(tPh, stat, lo, hi, pr);
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(kDkvDsFull));
       }
+      if (!ok) break;
+      // ---- epilogue: warpgroup 0 stores dK, warpgroup 1 dV.
+      const bool zero = n == 0;
+      if (!zero && !(ok = warp_wait(bar(kDkvAcc), used & 1, abort_flag, p.timeout_ns))) break;
+      ptx::tc_fence_after();
+      // (The item again, from an opaque copy of its number: nothing of it is kept across
+      // the loop.)
+      int again = item;
+      asm volatile("" : "+r"(again));
+      const DkvItem v = dkv_item<kCausal, kVarlen>(p, again);
+      if (!v.skip) {
+        const Seq& s = v.s;
+        const uint32_t tacc = (g == 0 ? tK : tV) + lane_base;
+        int* rec = poison + (used & 1) * kPoisonWords;
+        const bool any = kCheck && !zero && *static_cast<volatile int*>(rec + kD);
+        // The last query row whose non-finite dO element a key may see (see above).
+        const int seen = kCausal ? max(0, v.k0 + row - v.off) : 0;
+        auto is_nan = [&](int col) -> bool { return any && g == 1 && rec[col] >= seen; };
+        if (p.n_splits == 1) {
+          const bool in = v.k0 + row < s.sk && dbg_ok(s.k_base + v.k0 + row < p.Sk);
+          uint16_t* dst = (g == 0 ? p.dk : p.dv) +
+                          row_at(p.layout, s.batch, p.Hkv, p.Sk, s.head, s.k_base + v.k0 + (in ? row : 0));
+          store_row<kD>(tacc, zero, g == 0 ? p.scale : 1.f, p.mode, in ? dst : nullptr, any && g == 1, is_nan);
+        } else {
+          const size_t slots = static_cast<size_t>(p.k_slots) * (kVarlen ? p.Hkv : p.BH);
+          const size_t slot = static_cast<size_t>(s.slot_k) + static_cast<size_t>(s.head) * p.k_slots + s.tile;
+          float* dst = p.part + (((static_cast<size_t>(s.split) * 2 + g) * slots + slot) * kTile + row) * kD;
+          store_part<kD>(tacc, zero, dst, is_nan);
+        }
+        if (any) clear_poison(rec, -1);
+      }
+      if (!zero) {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(kDkvAccFree));
+        ++used;
+      }
+      item = items.next_warp(it, lane);
     }
   }
   ptx::tc_fence_before();
@@ -694,15 +830,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 //
 // It also leaves the row statistics that dkv reads: per query row -lse log2(e) and -D,
 // D = sum_c dO_ic O_ic, formed from the dO tile it has and the O tile, which passes
-// through K's third stage before that is first needed. (A kernel of its own for them
+// through K's ring. (A kernel of its own for them
 // read dO once more and cost 25 us of 2.35 ms on 8K self-attention, 47 of 1039 us on a
 // packed batch, and a launch.) Rows past the end, and rows that see no key, get -Inf
 // and 0 (P = 0). A non-finite D becomes NaN: it marks a row whose dO or O has a
 // non-finite element.
 constexpr int kDqKStages = 3, kDqVStages = 2;  // K_j is in use while K_{j+2} loads
-constexpr int kDqMasked = 2;  // 128 rows' causal limits span at most 127 keys
+constexpr int kDqChecks = 4;  // masked tiles between landing and being checked: at most 2
 enum : int {
   kDqQ = 0,
+  kDqQFree,     // the item's last S and dP products, and the statistics, have read Q and dO
   kDqKFull,
   kDqKEmpty = kDqKFull + kDqKStages,
   kDqVFull = kDqKEmpty + kDqKStages,
@@ -711,19 +848,53 @@ enum : int {
   kDqDpFull = kDqSFull + 2,
   kDqDsFull,
   kDqAcc,
-  kDqOutFull,   // O has landed in K's last stage
-  kDqOutRead,   // and has been read
+  kDqAccFree,   // the epilogue has read dQ
   kDqLanded,
-  kDqChecked = kDqLanded + kDqMasked,
-  kDqDrain = kDqChecked + kDqMasked,
-  kDqBars
+  kDqChecked = kDqLanded + kDqChecks,
+  kDqDrain = kDqChecked + kDqChecks,
+  kDqItemFull,
+  kDqItemEmpty = kDqItemFull + 2,
+  kDqBars = kDqItemEmpty + 2
 };
 constexpr int kDqOffQ = 0, kDqOffO = kTileBytes, kDqOffK = 2 * kTileBytes,
               kDqOffV = kDqOffK + kDqKStages * kTileBytes,
-              kDqOffPoison = kDqOffV + kDqVStages * kTileBytes, kDqOffDots = kDqOffPoison + kD * 4 + 16,
-              kDqOffBar = kDqOffDots + 2 * kTile * 4,
+              kDqOffItems = kDqOffV + kDqVStages * kTileBytes, kDqOffPoison = kDqOffItems + 32,
+              kDqOffDots = kDqOffPoison + kPoisonBytes, kDqOffBar = kDqOffDots + kTile * 4,
               kDqOffSlot = kDqOffBar + kDqBars * 8, kDqSmem = kDqOffSlot + 8 + 1024;
 static_assert(kDqSmem <= 232448, "shared memory budget (dq)");
+
+// An item: an owned query tile and the part [t0, t0 + n) of the key tiles any of its rows
+// sees; from first_masked on some row does not see every key (the causal diagonal, or
+// the ragged last tile). skip: nothing to do, not even a zero to store.
+struct DqItem {
+  Seq s;
+  int off, q0, t0, n, first_masked;
+  bool skip;
+};
+
+template <bool kCausal, bool kVarlen>
+__device__ __forceinline__ DqItem dq_item(const BwdParams& p, int item) {
+  DqItem r;
+  r.s = seq_of<kCausal, kVarlen, true>(p, item);
+  const Seq& s = r.s;
+  r.off = s.sk - s.sq;
+  r.q0 = s.tile * kTile;
+  r.skip = kVarlen && (s.bad || r.q0 >= s.sq);
+  int n_kv = (s.sk + kTile - 1) / kTile;
+  r.first_masked = s.sk / kTile;
+  if (kCausal) {
+    const int last = min(s.sq, r.q0 + kTile) + r.off;  // keys the last row sees
+    n_kv = min(n_kv, last <= 0 ? 0 : (last + kTile - 1) / kTile);
+    r.first_masked = min(r.first_masked, max(0, r.q0 + r.off + 1) / kTile);
+  }
+  part_of(n_kv, p.n_splits, s.split, r.t0, r.n);
+  if (r.skip) r.n = 0;
+  return r;
+}
+
+// The ring of K takes, per item, O, K_0, K_1, ... (O's stage is free again by the time K_2
+// is wanted): fill of K_j, counted from the item's first.
+__device__ __forceinline__ int k_fill(int j) { return j + 1; }
 
 template <bool kCausal, bool kVarlen>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -736,50 +907,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_raw + (sbase - raw);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kDqOffSlot);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kDqOffSlot + 4);
-  int* poison_k = reinterpret_cast<int*>(smem + kDqOffPoison);
-  volatile int* poison_any = poison_k + kD;
+  int* poison = reinterpret_cast<int*>(smem + kDqOffPoison);
   auto bar = [&](int i) -> uint32_t { return sbase + kDqOffBar + 8u * static_cast<uint32_t>(i); };
   // (Through a shuffle, so that the compiler knows it to be the same on every lane.)
   const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   constexpr bool kCheck = kCausal || kVarlen;
   constexpr int kNever = 0x7FFFFFFF;
-
-  const Seq s = seq_of<kCausal, kVarlen, true>(p, static_cast<int>(blockIdx.x));
-  if (kVarlen) {
-    if (s.bad) {
-      if (threadIdx.x == 0) atomicOr(&g_attn_status, 2u);
-      ptx::grid_dependency_wait();
-      return;
-    }
-    if (s.tile * kTile >= s.sq) {
-      ptx::grid_dependency_wait();
-      return;
-    }
-  }
-  const int off = s.sk - s.sq;
-  const int q0 = s.tile * kTile;
-  // Key tiles any row sees, and of these the first in which some row does not see
-  // every key: the causal diagonal, or the ragged last tile.
-  int n_kv = (s.sk + kTile - 1) / kTile;
-  int first_masked = s.sk / kTile;
-  if (kCausal) {
-    const int last = min(s.sq, q0 + kTile) - 1 + off + 1;  // keys the last row sees
-    n_kv = min(n_kv, last <= 0 ? 0 : (last + kTile - 1) / kTile);
-    first_masked = min(first_masked, max(0, q0 + off + 1) / kTile);
-  }
-  int t0, n;
-  part_of(n_kv, p.n_splits, s.split, t0, n);
-  auto masked = [&](int j) -> bool { return t0 + j >= first_masked; };
-  const int kv_head = s.head / p.group;
+  const Items items{sbase + kDqOffItems, bar(kDqItemFull), bar(kDqItemEmpty), abort_flag, p.timeout_ns};
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kDqBars; ++i) ptx::mbar_init(bar(i), (i == kDqDsFull || i == kDqOutRead) ? 8 : 1);
+    for (int i = 0; i < kDqBars; ++i)
+      ptx::mbar_init(bar(i), (i == kDqDsFull || i == kDqAccFree) ? 8
+                             : i >= kDqItemEmpty                 ? item_readers(kCheck)
+                             : i == kDqQFree                     ? 2
+                                                                 : 1);
     *abort_flag = 0;
-    *poison_any = 0;
     ptx::fence_mbar_init();
     ptx::fence_proxy_async_smem();
   }
-  if (threadIdx.x < kD) poison_k[threadIdx.x] = kNever;
+  for (int i = threadIdx.x; i < 2 * kPoisonWords; i += kThreads) poison[i] = i % kPoisonWords < kD ? kNever : 0;
   if (warp == 0 && lane == 0) {
     ptx::prefetch_tmap(&tm_q);
     ptx::prefetch_tmap(&tm_k);
@@ -798,131 +944,198 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::launch_dependents();  // the next kernel waits for this grid before it reads its results
   const uint32_t tP = tmem + 256, tQ = tmem + 384;
 
+  // In every role: `used` counts the items with key tiles so far (the phases of the
+  // per-item barriers), `tile` their key tiles (S buffer tile & 1), k_base the fills of
+  // K's ring before the item.
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
-    if (lane == 0 && n > 0) {
+    if (lane == 0) {
       const uint64_t pol_once = ptx::l2_policy_evict_first();
       const uint64_t pol_reuse = ptx::l2_policy_evict_last();
-      dbg_ok(s.q_base + q0 < p.Sq);
-      ptx::mbar_arrive_expect_tx(bar(kDqQ), 2 * kTileBytes);
-      load_tile(sbase + kDqOffQ, &tm_q, bar(kDqQ), p.layout, s.q_base + q0, s.head, s.batch, pol_once);
-      load_tile(sbase + kDqOffO, &tm_do, bar(kDqQ), p.layout, s.q_base + q0, s.head, s.batch, pol_once);
-      constexpr int kOutStage = kDqKStages - 1;
-      ptx::mbar_arrive_expect_tx(bar(kDqOutFull), kTileBytes);
-      load_tile(sbase + kDqOffK + kOutStage * kTileBytes, &tm_out, bar(kDqOutFull), p.layout, s.q_base + q0,
-                s.head, s.batch, pol_once);
-      int k_issued = 0, v_issued = 0;
-      for (int j = 0; j < n; ++j) {
-        const int row = s.k_base + (t0 + j) * kTile;
-        dbg_ok(row < p.Sk);
-        const int ks = j % kDqKStages, vs = j % kDqVStages;
-        if (!wait_bounded(bar(kDqKEmpty + ks), ((j / kDqKStages) & 1) ^ 1, abort_flag, p.timeout_ns, true))
-          break;
-        if (j == kOutStage && !wait_bounded(bar(kDqOutRead), 0, abort_flag, p.timeout_ns, true)) break;
-        ptx::mbar_arrive_expect_tx(bar(kDqKFull + ks), kTileBytes);
-        load_tile(sbase + kDqOffK + ks * kTileBytes, &tm_k, bar(kDqKFull + ks), p.layout, row, kv_head,
-                  s.batch, pol_reuse);
-        ++k_issued;
-        if (!wait_bounded(bar(kDqVEmpty + vs), ((j / kDqVStages) & 1) ^ 1, abort_flag, p.timeout_ns, true))
-          break;
-        ptx::mbar_arrive_expect_tx(bar(kDqVFull + vs), kTileBytes);
-        load_tile(sbase + kDqOffV + vs * kTileBytes, &tm_v, bar(kDqVFull + vs), p.layout, row, kv_head,
-                  s.batch, pol_reuse);
-        ++v_issued;
+      int used = 0, k_issued = 0, v_issued = 0, asked = 0;
+      bool ok = true;
+      auto k_slot = [&]() -> bool {
+        return wait_bounded(bar(kDqKEmpty + k_issued % kDqKStages), ((k_issued / kDqKStages) & 1) ^ 1,
+                            abort_flag, p.timeout_ns, true);
+      };
+      for (int item = static_cast<int>(blockIdx.x), it = 0; ok && item >= 0; ++it) {
+        const DqItem w = dq_item<kCausal, kVarlen>(p, item);
+        const Seq& s = w.s;
+        if (kVarlen && s.bad) atomicOr(&g_attn_status, 2u);
+        if (w.n > 0) {
+          const int kv_head = s.head / p.group;
+          if (used > 0 && !(ok = wait_bounded(bar(kDqQFree), (used - 1) & 1, abort_flag, p.timeout_ns, true)))
+            break;
+          dbg_ok(s.q_base + w.q0 < p.Sq);
+          ptx::mbar_arrive_expect_tx(bar(kDqQ), 2 * kTileBytes);
+          load_tile(sbase + kDqOffQ, &tm_q, bar(kDqQ), p.layout, s.q_base + w.q0, s.head, s.batch, pol_once);
+          load_tile(sbase + kDqOffO, &tm_do, bar(kDqQ), p.layout, s.q_base + w.q0, s.head, s.batch, pol_once);
+          ++used;
+          if (!(ok = k_slot())) break;
+          const int os = k_issued % kDqKStages;
+          ptx::mbar_arrive_expect_tx(bar(kDqKFull + os), kTileBytes);
+          load_tile(sbase + kDqOffK + os * kTileBytes, &tm_out, bar(kDqKFull + os), p.layout, s.q_base + w.q0,
+                    s.head, s.batch, pol_once);
+          ++k_issued;
+          for (int j = 0; j < w.n; ++j) {
+            const int row = s.k_base + (w.t0 + j) * kTile;
+            dbg_ok(row < p.Sk);
+            if (!(ok = k_slot())) break;
+            const int ks = k_issued % kDqKStages, vs = v_issued % kDqVStages;
+            ptx::mbar_arrive_expect_tx(bar(kDqKFull + ks), kTileBytes);
+            load_tile(sbase + kDqOffK + ks * kTileBytes, &tm_k, bar(kDqKFull + ks), p.layout, row, kv_head,
+                      s.batch, pol_reuse);
+            ++k_issued;
+            if (!(ok = wait_bounded(bar(kDqVEmpty + vs), ((v_issued / kDqVStages) & 1) ^ 1, abort_flag,
+                                    p.timeout_ns, true)))
+              break;
+            ptx::mbar_arrive_expect_tx(bar(kDqVFull + vs), kTileBytes);
+            load_tile(sbase + kDqOffV + vs * kTileBytes, &tm_v, bar(kDqVFull + vs), p.layout, row, kv_head,
+                      s.batch, pol_reuse);
+            ++v_issued;
+          }
+          if (!ok) break;
+        }
+        items.ask(it);
+        ++asked;
+        item = items.next_lane(it);
       }
-      wait_bounded(bar(kDqQ), 0, abort_flag, p.timeout_ns, false);
-      wait_bounded(bar(kDqOutFull), 0, abort_flag, p.timeout_ns, false);
+      // Every copy this thread started lands before the CTA can exit, and so does the
+      // last answer asked for.
+      if (used > 0) wait_bounded(bar(kDqQ), (used - 1) & 1, abort_flag, p.timeout_ns, false);
       for (int st = 0; st < kDqKStages && st < k_issued; ++st)
         wait_bounded(bar(kDqKFull + st), ((k_issued - 1 - st) / kDqKStages) & 1, abort_flag, p.timeout_ns,
                      false);
       for (int st = 0; st < kDqVStages && st < v_issued; ++st)
         wait_bounded(bar(kDqVFull + st), ((v_issued - 1 - st) / kDqVStages) & 1, abort_flag, p.timeout_ns,
                      false);
+      if (asked > 0)
+        wait_bounded(items.full + 8 * ((asked - 1) & 1), ((asked - 1) >> 1) & 1, abort_flag, p.timeout_ns, false);
     }
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer (whole warp)
-    if (n > 0) {
-      const uint32_t q_desc = desc_lo(sbase + kDqOffQ, 16), o_desc = desc_lo(sbase + kDqOffO, 16);
-      auto k_tile = [&](int j) -> uint32_t { return sbase + kDqOffK + (j % kDqKStages) * kTileBytes; };
-      auto v_tile = [&](int j) -> uint32_t { return sbase + kDqOffV + (j % kDqVStages) * kTileBytes; };
-      auto wait = [&](int b, uint32_t par) -> bool {
-        const bool r = warp_wait(bar(b), par & 1, abort_flag, p.timeout_ns);
-        ptx::tc_fence_after();
-        return r;
-      };
-      const int jm = max(0, first_masked - t0);  // first masked tile of this CTA's part
-      auto do_s = [&](int j) -> bool {
-        if (!wait(kDqKFull + j % kDqKStages, j / kDqKStages)) return false;
-        issue_s(tmem + 128 * (j & 1), q_desc, desc_lo(k_tile(j), 16));
-        ptx::mma_commit_warp(bar(kDqSFull + (j & 1)));
-        if (kCheck && masked(j) && lane == 0) ptx::mbar_arrive(bar(kDqLanded + (j - jm)));
-        return true;
-      };
-      auto do_dp = [&](int j) -> bool {
-        if (!wait(kDqVFull + j % kDqVStages, j / kDqVStages)) return false;
-        issue_s(tP, o_desc, desc_lo(v_tile(j), 16));
-        ptx::mma_commit_warp(bar(kDqDpFull));
-        ptx::mma_commit_warp(bar(kDqVEmpty + j % kDqVStages));
-        return true;
-      };
-      bool ok = wait(kDqQ, 0) && do_s(0) && do_dp(0) && (n == 1 || do_s(1));
-      for (int j = 0; ok && j < n; ++j) {
-        if (!(ok = wait(kDqDsFull, j))) break;
-        if (j + 1 < n && !(ok = do_dp(j + 1))) break;
-        if (kCheck && masked(j) && !(ok = wait(kDqChecked + (j - jm), 0))) break;
-        issue_second(tQ, tmem + 128 * (j & 1), desc_lo(k_tile(j), kHalfBytes), j > 0);
-        ptx::mma_commit_warp(bar(kDqKEmpty + j % kDqKStages));
-        if (j + 2 < n && !(ok = do_s(j + 2))) break;
+    const uint32_t q_desc = desc_lo(sbase + kDqOffQ, 16), o_desc = desc_lo(sbase + kDqOffO, 16);
+    auto wait = [&](int b, uint32_t par) -> bool {
+      const bool r = warp_wait(bar(b), par & 1, abort_flag, p.timeout_ns);
+      ptx::tc_fence_after();
+      return r;
+    };
+    int used = 0, tile = 0, k_base = 0, landed = 0, checked = 0;
+    bool ok = true;
+    for (int item = static_cast<int>(blockIdx.x), it = 0; ok && item >= 0; ++it) {
+      const DqItem w = dq_item<kCausal, kVarlen>(p, item);
+      const int n = w.n;
+      if (n > 0) {
+        auto k_tile = [&](int j) -> uint32_t {
+          return sbase + kDqOffK + ((k_base + k_fill(j)) % kDqKStages) * kTileBytes;
+        };
+        auto masked = [&](int j) -> bool { return kCheck && w.t0 + j >= w.first_masked; };
+        auto do_s = [&](int j) -> bool {
+          const int f = k_base + k_fill(j);
+          if (!wait(kDqKFull + f % kDqKStages, f / kDqKStages)) return false;
+          issue_s(tmem + 128 * ((tile + j) & 1), q_desc, desc_lo(k_tile(j), 16));
+          ptx::mma_commit_warp(bar(kDqSFull + ((tile + j) & 1)));
+          if (masked(j)) {
+            if (lane == 0) ptx::mbar_arrive(bar(kDqLanded + landed % kDqChecks));
+            ++landed;
+          }
+          return true;
+        };
+        auto do_dp = [&](int j) -> bool {
+          const int f = tile + j;
+          if (!wait(kDqVFull + f % kDqVStages, f / kDqVStages)) return false;
+          issue_s(tP, o_desc, desc_lo(sbase + kDqOffV + (f % kDqVStages) * kTileBytes, 16));
+          ptx::mma_commit_warp(bar(kDqDpFull));
+          ptx::mma_commit_warp(bar(kDqVEmpty + f % kDqVStages));
+          // The item's last S was issued before its last dP.
+          if (j + 1 == n) ptx::mma_commit_warp(bar(kDqQFree));
+          return true;
+        };
+        ok = wait(kDqQ, used) && do_s(0) && (n == 1 ? do_dp(0) : do_dp(0) && do_s(1));
+        for (int j = 0; ok && j < n; ++j) {
+          if (!(ok = wait(kDqDsFull, tile + j))) break;
+          if (j + 1 < n && !(ok = do_dp(j + 1))) break;
+          if (masked(j)) {
+            if (!(ok = wait(kDqChecked + checked % kDqChecks, checked / kDqChecks))) break;
+            ++checked;
+          }
+          // The item's first product with K starts dQ anew.
+          if (j == 0 && used > 0 && !(ok = wait(kDqAccFree, used - 1))) break;
+          issue_second(tQ, tmem + 128 * ((tile + j) & 1), desc_lo(k_tile(j), kHalfBytes), j > 0);
+          ptx::mma_commit_warp(bar(kDqKEmpty + (k_base + k_fill(j)) % kDqKStages));
+          if (j + 2 < n && !(ok = do_s(j + 2))) break;
+        }
+        if (ok) ptx::mma_commit_warp(bar(kDqAcc));
+        tile += n;
+        k_base += n + 1;
+        ++used;
       }
-      if (ok) ptx::mma_commit_warp(bar(kDqAcc));
-      ptx::mma_commit_warp(bar(kDqDrain));
-      wait_bounded(bar(kDqDrain), 0, abort_flag, p.timeout_ns, false);
+      if (ok) item = items.next_warp(it, lane);
     }
+    ptx::mma_commit_warp(bar(kDqDrain));
+    wait_bounded(bar(kDqDrain), 0, abort_flag, p.timeout_ns, false);  // every MMA is done
     __syncwarp();
   } else if (warp < kSoftmaxWarp0) {
     // ------------------------------------------------ check of the masked tiles (warps 2-3)
     // A hidden pair has dS = 0, and 0 * NaN in dS K would carry a non-finite element of
     // its key to a query that does not see it. Once S has been formed, the tile's
     // rows past the sequence's end and its non-finite elements are set to 0; the
-    // queries that see such a key get NaN in that column through poison_k, the
-    // first key that has one there.
+    // queries that see such a key get NaN in that column through `poison`, the first key
+    // that has one there. Two items' records are kept, for the one being finished and
+    // the next; an item's epilogue clears its own.
     if constexpr (kCheck) {
       const int tid = static_cast<int>(threadIdx.x) - 64;
-      for (int j = max(0, first_masked - t0), m = 0; j < n && m < kDqMasked; ++j, ++m) {
-        const bool ok = wait_bounded(bar(kDqLanded + m), 0, abort_flag, p.timeout_ns, true) &&
-                        wait_bounded(bar(kDqSFull + (j & 1)), (j >> 1) & 1, abort_flag, p.timeout_ns, true);
-        if (ptx::named_barrier_or(1, 64, !ok)) break;
-        const uint32_t kt = sbase + kDqOffK + (j % kDqKStages) * kTileBytes;
-        const int first = (t0 + j) * kTile;
-        bool dirty = false;
-        for (int r = tid; r < kTile; r += 64) {
-          if (first + r >= s.sk) {
-            if (kVarlen) {  // (a dense tile's rows past the end are zero already)
-              zero_row(kt, r);
+      int used = 0, tile = 0, k_base = 0, m = 0;
+      bool ok = true;
+      for (int item = static_cast<int>(blockIdx.x), it = 0; ok && item >= 0; ++it) {
+        const DqItem w = dq_item<kCausal, kVarlen>(p, item);
+        const Seq& s = w.s;
+        int* rec = poison + (used & 1) * kPoisonWords;
+        for (int j = max(0, w.first_masked - w.t0); j < w.n; ++j, ++m) {
+          ok = wait_bounded(bar(kDqLanded + m % kDqChecks), (m / kDqChecks) & 1, abort_flag, p.timeout_ns,
+                            true) &&
+               wait_bounded(bar(kDqSFull + ((tile + j) & 1)), ((tile + j) >> 1) & 1, abort_flag, p.timeout_ns,
+                            true);
+          ok = !ptx::named_barrier_or(1, 64, !ok);
+          if (!ok) break;
+          const uint32_t kt = sbase + kDqOffK + ((k_base + k_fill(j)) % kDqKStages) * kTileBytes;
+          const int first = (w.t0 + j) * kTile;
+          bool dirty = false;
+          for (int r = tid; r < kTile; r += 64) {
+            if (first + r >= s.sk) {
+              if (kVarlen) {  // (a dense tile's rows past the end are zero already)
+                zero_row(kt, r);
+                dirty = true;
+              }
+              continue;
+            }
+            uint32_t acc = 0;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const uint4 x = ptx::ld_shared_v4(kt + chunk_at(r, c));
+              acc = ptx::bf16x2_nonfinite_acc(x.x, ptx::bf16x2_nonfinite_acc(x.y, acc));
+              acc = ptx::bf16x2_nonfinite_acc(x.z, ptx::bf16x2_nonfinite_acc(x.w, acc));
+            }
+            if (acc != 0) {
+              clean_row(kt, r, [&](int col) {
+                atomicMin(&rec[col], first + r);
+                *static_cast<volatile int*>(rec + kD) = 1;
+              });
               dirty = true;
             }
-            continue;
           }
-          uint32_t acc = 0;
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const uint4 x = ptx::ld_shared_v4(kt + chunk_at(r, c));
-            acc = ptx::bf16x2_nonfinite_acc(x.x, ptx::bf16x2_nonfinite_acc(x.y, acc));
-            acc = ptx::bf16x2_nonfinite_acc(x.z, ptx::bf16x2_nonfinite_acc(x.w, acc));
-          }
-          if (acc != 0) {
-            clean_row(kt, r, [&](int col) {
-              atomicMin(&poison_k[col], first + r);
-              *poison_any = 1;
-            });
-            dirty = true;
-          }
+          if (dirty) ptx::fence_proxy_async_smem();
+          __syncwarp();
+          ptx::named_barrier_sync(1, 64);
+          if (tid == 0) ptx::mbar_arrive(bar(kDqChecked + m % kDqChecks));
         }
-        if (dirty) ptx::fence_proxy_async_smem();
-        __syncwarp();
-        ptx::named_barrier_sync(1, 64);
-        if (tid == 0) ptx::mbar_arrive(bar(kDqChecked + m));
+        if (w.n > 0) {
+          tile += w.n;
+          k_base += w.n + 1;
+          ++used;
+        }
+        if (ok) item = items.next_warp(it, lane);
       }
     }
   } else {
@@ -932,103 +1145,131 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = wq * 32 + lane;             // query within the tile
     const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tPh = tP + lane_base + 64 * g;
-    // Keys this row sees.
-    const int limit = kCausal ? min(q0 + row + off + 1, s.sk) : s.sk;
     const uint64_t c2 = ptx::f2_pack(p.c, p.c);
+    int used = 0, tile = 0, k_base = 0;
     bool ok = true;
-    uint64_t nl2 = 0, nd2 = 0;
-    if (n > 0) {
-      // The row's statistics: each warpgroup adds its 64 columns of dO O. (lse is read
-      // before the waits, whose time covers its latency.)
-      float dot = 0.f, lse = -__int_as_float(0x7F800000);
-      if (q0 + row < s.sq)
-        lse = __ldg(p.lse + (kVarlen ? static_cast<size_t>(s.head) * p.Sq + s.q_base + q0 + row
-                                     : (static_cast<size_t>(s.batch) * p.Hq + s.head) * p.Sq + q0 + row));
-      ok = warp_wait(bar(kDqQ), 0, abort_flag, p.timeout_ns) &&
-           warp_wait(bar(kDqOutFull), 0, abort_flag, p.timeout_ns);
-      if (ok) {
+    for (int item = static_cast<int>(blockIdx.x), it = 0; ok && item >= 0; ++it) {
+      const DqItem w = dq_item<kCausal, kVarlen>(p, item);
+      const int n = w.n;
+      // Keys this row sees, counted from the part's first.
+      const int limit = (kCausal ? min(w.q0 + row + w.off + 1, w.s.sk) : w.s.sk) - w.t0 * kTile;
+      const int first_masked = w.first_masked - w.t0;
+      uint64_t nl2 = 0, nd2 = 0;
+      if (n > 0) {
+        const Seq& s = w.s;
+        // The row's statistics: each warpgroup adds its 64 columns of dO O. (lse is read
+        // before the waits, whose time covers its latency.)
+        float dot = 0.f, lse = -__int_as_float(0x7F800000);
+        if (w.q0 + row < s.sq)
+          lse = __ldg(p.lse + (kVarlen ? static_cast<size_t>(s.head) * p.Sq + s.q_base + w.q0 + row
+                                       : (static_cast<size_t>(s.batch) * p.Hq + s.head) * p.Sq + w.q0 + row));
+        const int fo = k_base, os = fo % kDqKStages;
+        ok = warp_wait(bar(kDqQ), used & 1, abort_flag, p.timeout_ns) &&
+             warp_wait(bar(kDqKFull + os), (fo / kDqKStages) & 1, abort_flag, p.timeout_ns);
+        if (ok) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint4 x = ptx::ld_shared_v4(sbase + kDqOffO + chunk_at(row, 8 * g + c));
-          const uint4 y =
-              ptx::ld_shared_v4(sbase + kDqOffK + (kDqKStages - 1) * kTileBytes + chunk_at(row, 8 * g + c));
-          const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+          for (int c = 0; c < 8; ++c) {
+            const uint4 x = ptx::ld_shared_v4(sbase + kDqOffO + chunk_at(row, 8 * g + c));
+            const uint4 y = ptx::ld_shared_v4(sbase + kDqOffK + os * kTileBytes + chunk_at(row, 8 * g + c));
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            dot = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), dot);
-            dot = fmaf(__uint_as_float(xs[e] & 0xFFFF0000u), __uint_as_float(ys[e] & 0xFFFF0000u), dot);
+            for (int e = 0; e < 4; ++e) {
+              dot = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), dot);
+              dot = fmaf(__uint_as_float(xs[e] & 0xFFFF0000u), __uint_as_float(ys[e] & 0xFFFF0000u), dot);
+            }
           }
+          ptx::fence_proxy_async_smem();  // these reads, before the stage is refilled
         }
-        // (The stage is refilled by TMA: order these reads before it.)
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(kDqOutRead));
+        // The other half's dot product: warpgroup 1 hands its own over and takes the sum
+        // back, in the same word (both warpgroups, whatever their waits said).
+        float* dots = reinterpret_cast<float*>(smem + kDqOffDots);
+        if (g == 1) dots[row] = dot;
+        ptx::named_barrier_sync(2, 256);
+        if (g == 0) dots[row] = dot = dot + dots[row];
+        ptx::named_barrier_sync(2, 256);
+        if (g == 1) dot = dots[row];
+        if (!ok) break;
+        if (threadIdx.x == 32 * kSoftmaxWarp0) {  // O and dO have been read
+          ptx::mbar_arrive(bar(kDqKEmpty + os));
+          ptx::mbar_arrive(bar(kDqQFree));
+        }
+        float nl = -__int_as_float(0x7F800000), nd = 0.f;
+        if (lse != -__int_as_float(0x7F800000)) {
+          nl = -lse * 1.4426950408889634f;
+          nd = isfinite(dot) ? -dot : __int_as_float(0x7FC00000);
+        }
+        if (g == 0 && s.split == 0) {
+          float* st = p.stats + (static_cast<size_t>(s.slot_q) + static_cast<size_t>(s.head) * p.q_slots +
+                                 s.tile) * kStatFloats;
+          st[row] = nl;
+          st[kTile + row] = nd;
+        }
+        nl2 = ptx::f2_pack(nl, nl);
+        nd2 = ptx::f2_pack(nd, nd);
       }
-      float* dots = reinterpret_cast<float*>(smem + kDqOffDots);
-      dots[g * kTile + row] = dot;
-      ptx::named_barrier_sync(2, 256);  // (both warpgroups, whatever their waits said)
-      const float D = dots[row] + dots[kTile + row];
-      float nl = -__int_as_float(0x7F800000), nd = 0.f;
-      if (lse != -__int_as_float(0x7F800000)) {
-        nl = -lse * 1.4426950408889634f;
-        nd = isfinite(D) ? -D : __int_as_float(0x7FC00000);
-      }
-      if (g == 0 && s.split == 0) {
-        float* st = p.stats + (static_cast<size_t>(s.slot_q) + static_cast<size_t>(s.head) * p.q_slots + s.tile) *
-                                  kStatFloats;
-        st[row] = nl;
-        st[kTile + row] = nd;
-      }
-      nl2 = ptx::f2_pack(nl, nl);
-      nd2 = ptx::f2_pack(nd, nd);
-    }
-    for (int j = 0; ok && j < n; ++j) {
-      const uint32_t tSh = tmem + 128 * (j & 1) + lane_base + 64 * g;
-      const bool mk = masked(j);
-      const int hi = limit - (t0 + j) * kTile - 64 * g;  // columns of this half the row sees
-      Half pr;
-      if (!(ok = warp_wait(bar(kDqSFull + (j & 1)), (j >> 1) & 1, abort_flag, p.timeout_ns))) break;
-      ptx::tc_fence_after();
-      {
-        uint32_t a[32], b[32];
-        load_half(tSh, a, b);
+      for (int j = 0; j < n; ++j, ++tile) {
+        const uint32_t tSh = tmem + 128 * (tile & 1) + lane_base + 64 * g;
+        const int hi = limit - j * kTile - 64 * g;  // columns of this half the row sees
+        Half pr;
+        if (!(ok = warp_wait(bar(kDqSFull + (tile & 1)), (tile >> 1) & 1, abort_flag, p.timeout_ns))) break;
+        ptx::tc_fence_after();
+        by_halves(tSh, [&](int ch, const uint32_t (&r)[32]) {
 #pragma unroll
-        for (int x = 0; x < 32; ++x) {
-          const uint64_t s2 = x < 16 ? ptx::f2_pack(__uint_as_float(a[2 * x]), __uint_as_float(a[2 * x + 1]))
-                                     : ptx::f2_pack(__uint_as_float(b[2 * x - 32]), __uint_as_float(b[2 * x - 31]));
-          float e0, e1;
-          ptx::f2_unpack(ptx::f2_fma(s2, c2, nl2), e0, e1);
-          pr[x] = ptx::f2_pack(ptx::ex2(e0), ptx::ex2(e1));
+          for (int x = 0; x < 16; ++x) {
+            float e0, e1;
+            ptx::f2_unpack(ptx::f2_fma(pair_of(r, 2 * x), c2, nl2), e0, e1);
+            pr[16 * ch + x] = ptx::f2_pack(ptx::ex2(e0), ptx::ex2(e1));
+          }
+        });
+        if (!(ok = warp_wait(bar(kDqDpFull), tile & 1, abort_flag, p.timeout_ns))) break;
+        ptx::tc_fence_after();
+        if (j >= first_masked)
+          dq_ds<true>(tPh, tSh, nd2, hi, pr);
+        else
+          dq_ds<false>(tPh, tSh, nd2, hi, pr);
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(kDqDsFull));
+      }
+      if (!ok) break;
+      // ---- epilogue: each warpgroup stores 64 columns of the rows.
+      const bool zero = n == 0;
+      if (!zero && !(ok = warp_wait(bar(kDqAcc), used & 1, abort_flag, p.timeout_ns))) break;
+      ptx::tc_fence_after();
+      // (The item again, from an opaque copy of its number: nothing of it is kept across
+      // the loop.)
+      int again = item;
+      asm volatile("" : "+r"(again));
+      const DqItem v = dq_item<kCausal, kVarlen>(p, again);
+      if (!v.skip) {
+        const Seq& s = v.s;
+        const uint32_t tacc = tQ + lane_base + 64 * g;
+        int* rec = poison + (used & 1) * kPoisonWords;
+        const bool any = kCheck && !zero && *static_cast<volatile int*>(rec + kD);
+        const int sees = kCausal ? min(v.q0 + row + v.off + 1, s.sk) : s.sk;
+        auto is_nan = [&](int col) -> bool { return any && rec[64 * g + col] < sees; };
+        if (p.n_splits == 1) {
+          const bool in = v.q0 + row < s.sq && dbg_ok(s.q_base + v.q0 + row < p.Sq);
+          uint16_t* dst =
+              p.dq + row_at(p.layout, s.batch, p.Hq, p.Sq, s.head, s.q_base + v.q0 + (in ? row : 0)) + 64 * g;
+          store_row<64>(tacc, zero, p.scale, p.mode, in ? dst : nullptr, any, is_nan);
+        } else {
+          const size_t slots = static_cast<size_t>(p.q_slots) * (kVarlen ? p.Hq : p.BH);
+          const size_t slot = static_cast<size_t>(s.slot_q) + static_cast<size_t>(s.head) * p.q_slots + s.tile;
+          float* dst = p.part + ((static_cast<size_t>(s.split) * slots + slot) * kTile + row) * kD + 64 * g;
+          store_part<64>(tacc, zero, dst, is_nan);
         }
+        if (any) clear_poison(rec, kNever);
       }
-      if (!(ok = warp_wait(bar(kDqDpFull), j & 1, abort_flag, p.timeout_ns))) break;
-      ptx::tc_fence_after();
-      if (mk)
-        dq_ds<true>(tPh, tSh, nd2, hi, pr);
-      else
-        dq_ds<false>(tPh, tSh, nd2, hi, pr);
-      ptx::tmem_wait_st();
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar(kDqDsFull));
-    }
-    // ---- epilogue: each warpgroup stores 64 columns of the rows.
-    if (ok && n > 0) ok = warp_wait(bar(kDqAcc), 0, abort_flag, p.timeout_ns);
-    if (ok) {
-      ptx::tc_fence_after();
-      const uint32_t tacc = tQ + lane_base + 64 * g;
-      auto poison = [&](int col) -> bool { return kCheck && poison_k[64 * g + col] < limit; };
-      if (p.n_splits == 1) {
-        const bool in = q0 + row < s.sq && dbg_ok(s.q_base + q0 + row < p.Sq);
-        uint16_t* dst =
-            p.dq + row_at(p.layout, s.batch, p.Hq, p.Sq, s.head, s.q_base + q0 + (in ? row : 0)) + 64 * g;
-        store_row<64>(tacc, n == 0, p.scale, p.mode, in ? dst : nullptr, kCheck && *poison_any, poison);
-      } else {
-        const size_t slots = static_cast<size_t>(p.q_slots) * (kVarlen ? p.Hq : p.BH);
-        const size_t slot = static_cast<size_t>(s.slot_q) + static_cast<size_t>(s.head) * p.q_slots + s.tile;
-        float* dst = p.part + ((static_cast<size_t>(s.split) * slots + slot) * kTile + row) * kD + 64 * g;
-        store_part<64>(tacc, n == 0, dst, poison);
+      if (!zero) {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(kDqAccFree));
+        k_base += n + 1;
+        ++used;
       }
+      item = items.next_warp(it, lane);
     }
   }
   ptx::tc_fence_before();

@@ -74,6 +74,34 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
   return ok != 0;
 }
 
+// ---------------------------------------------------------------- work items
+// Asks for a CTA of this grid that has not been launched yet: it is then not launched,
+// and its number is the asking CTA's to work on (cluster launch control). The 16-byte
+// answer is written to `resp` (16-byte aligned) and signalled on `bar` (16 tx bytes).
+__device__ __forceinline__ void clc_try_cancel(uint32_t resp, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          resp),
+      "r"(bar)
+      : "memory");
+}
+
+// The CTA number (x) in an answer, -1 if there was none left. No further CTA may be asked
+// for after that.
+__device__ __forceinline__ int clc_answer(uint32_t resp) {
+  int x;
+  asm volatile(
+      "{\n\t.reg .b128 c;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 c, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, c;\n\t"
+      "mov.s32 %0, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, c;\n\t}"
+      : "=r"(x)
+      : "r"(resp)
+      : "memory");
+  return x;
+}
+
 // ---------------------------------------------------------------- clusters
 // This CTA's rank in its cluster.
 __device__ __forceinline__ uint32_t cluster_ctarank() {
