@@ -125,8 +125,11 @@ __device__ __forceinline__ Seq seq_of(const BwdParams& p, int block) {
 
 // The items of a CTA, in order, for its warps: item 0 is the CTA's own number, and answer
 // `it` names item it + 1. The producer asks when it has issued an item's last loads, a few
-// tiles before its end: an item claimed earlier would wait for this CTA while others
-// run out of work. Two slots: answer (16 bytes), and per slot a barrier for the answer and one for its readers.
+// tiles before its end: an item claimed earlier would wait for this CTA while others run
+// out of work (asked one item earlier, a packed batch took 986 us instead of 900, and
+// where there are many equal items nothing was won). Per slot an answer (16 bytes), a barrier
+// for it and one for its readers.
+constexpr int kItemSlots = 2;
 struct Items {
   uint32_t resp, full, empty;  // shared-memory addresses of slot 0
   volatile int* abort_flag;
@@ -134,15 +137,15 @@ struct Items {
 
   // By the producer's lane.
   __device__ __forceinline__ void ask(int it) const {
-    const uint32_t slot = it & 1;
-    if (!wait_bounded(empty + 8 * slot, ((it >> 1) & 1) ^ 1, abort_flag, timeout_ns, true)) return;
+    const uint32_t slot = it % kItemSlots;
+    if (!wait_bounded(empty + 8 * slot, ((it / kItemSlots) & 1) ^ 1, abort_flag, timeout_ns, true)) return;
     ptx::mbar_arrive_expect_tx(full + 8 * slot, 16);
     ptx::clc_try_cancel(resp + 16 * slot, full + 8 * slot);
   }
   // By one lane of a role: the item after item `it`, -1 at the end.
   __device__ __forceinline__ int next_lane(int it) const {
-    const uint32_t slot = it & 1;
-    if (!wait_bounded(full + 8 * slot, (it >> 1) & 1, abort_flag, timeout_ns, true)) return -1;
+    const uint32_t slot = it % kItemSlots;
+    if (!wait_bounded(full + 8 * slot, (it / kItemSlots) & 1, abort_flag, timeout_ns, true)) return -1;
     const int item = ptx::clc_answer(resp + 16 * slot);
     ptx::fence_proxy_async_smem();  // the read, before the slot's next answer
     ptx::mbar_arrive(empty + 8 * slot);
@@ -150,13 +153,18 @@ struct Items {
   }
   // By a whole warp.
   __device__ __forceinline__ int next_warp(int it, int lane) const {
-    const uint32_t slot = it & 1;
-    if (!warp_wait(full + 8 * slot, (it >> 1) & 1, abort_flag, timeout_ns)) return -1;
+    const uint32_t slot = it % kItemSlots;
+    if (!warp_wait(full + 8 * slot, (it / kItemSlots) & 1, abort_flag, timeout_ns)) return -1;
     const int item = ptx::clc_answer(resp + 16 * slot);
     ptx::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(empty + 8 * slot);
     return __shfl_sync(0xFFFFFFFFu, item, 0);
+  }
+  // The answers asked for and not taken have landed (before the CTA exits).
+  __device__ __forceinline__ void drain(int asked) const {
+    for (int it = asked > kItemSlots ? asked - kItemSlots : 0; it < asked; ++it)
+      wait_bounded(full + 8 * (it % kItemSlots), (it / kItemSlots) & 1, abort_flag, timeout_ns, false);
   }
 };
 // Readers of an answer: producer, MMA warp, softmax warps, and the check's.
@@ -433,14 +441,14 @@ enum : int {
   kDkvChecked,
   kDkvDrain,
   kDkvItemFull,
-  kDkvItemEmpty = kDkvItemFull + 2,
-  kDkvBars = kDkvItemEmpty + 2
+  kDkvItemEmpty = kDkvItemFull + kItemSlots,
+  kDkvBars = kDkvItemEmpty + kItemSlots
 };
 constexpr int kDkvOffK = 0, kDkvOffV = kTileBytes, kDkvOffQ = 2 * kTileBytes,
               kDkvOffO = kDkvOffQ + kDkvStages * kTileBytes,
               kDkvOffStats = kDkvOffO + kDkvStages * kTileBytes,
               kDkvOffItems = kDkvOffStats + kDkvStages * kStatFloats * 4,
-              kDkvOffPoison = kDkvOffItems + 32, kDkvOffBar = kDkvOffPoison + kPoisonBytes,
+              kDkvOffPoison = kDkvOffItems + 16 * kItemSlots, kDkvOffBar = kDkvOffPoison + kPoisonBytes,
               kDkvOffSlot = kDkvOffBar + kDkvBars * 8, kDkvSmem = kDkvOffSlot + 8 + 1024;
 static_assert(kDkvSmem <= 232448, "shared memory budget (dkv)");
 
@@ -580,11 +588,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
         }
         items.ask(it);
-        ++asked;
+        asked = it + 1;
         item = items.next_lane(it);
       }
-      // Every copy this thread started lands before the CTA can exit, and so does the
-      // last answer asked for.
+      // Every copy this thread started lands before the CTA can exit, and so does every
+      // answer asked for.
       if (used > 0) wait_bounded(bar(kDkvKV), (used - 1) & 1, abort_flag, p.timeout_ns, false);
       for (int st = 0; st < kDkvStages; ++st) {
         if (st < q_issued)
@@ -594,8 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_bounded(bar(kDkvOFull + st), ((o_issued - 1 - st) / kDkvStages) & 1, abort_flag,
                        p.timeout_ns, false);
       }
-      if (asked > 0)
-        wait_bounded(items.full + 8 * ((asked - 1) & 1), ((asked - 1) >> 1) & 1, abort_flag, p.timeout_ns, false);
+      items.drain(asked);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -729,8 +736,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t c2 = ptx::f2_pack(p.c, p.c);
     int used = 0, tile = 0;
     bool ok = true;
-    for (int item = static_cast<int>(blockIdx.x), it = 0; ok && item >= 0; ++it) {
-      const DkvItem w = dkv_item<kCausal, kVarlen>(p, item);
+    int item = static_cast<int>(blockIdx.x);
+    DkvItem w = dkv_item<kCausal, kVarlen>(p, item);
+    for (int it = 0; ok && item >= 0; ++it) {
       const int first_row = w.k0 + row - w.off;  // the first query that sees this key (causal)
       const int n = w.n, sq = w.s.sq, off = w.off, k0 = w.k0;
       QueryTiles qt(w);
@@ -769,15 +777,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) ptx::mbar_arrive(bar(kDkvDsFull));
       }
       if (!ok) break;
-      // ---- epilogue: warpgroup 0 stores dK, warpgroup 1 dV.
+      // ---- epilogue: warpgroup 0 stores dK, warpgroup 1 dV. (The item again, from an
+      // opaque copy of its number: nothing of it is kept across the loop. And the next one,
+      // before the wait.)
       const bool zero = n == 0;
-      if (!zero && !(ok = warp_wait(bar(kDkvAcc), used & 1, abort_flag, p.timeout_ns))) break;
-      ptx::tc_fence_after();
-      // (The item again, from an opaque copy of its number: nothing of it is kept across
-      // the loop.)
       int again = item;
       asm volatile("" : "+r"(again));
       const DkvItem v = dkv_item<kCausal, kVarlen>(p, again);
+      item = items.next_warp(it, lane);
+      if (item >= 0) w = dkv_item<kCausal, kVarlen>(p, item);
+      if (!zero && !(ok = warp_wait(bar(kDkvAcc), used & 1, abort_flag, p.timeout_ns))) break;
+      ptx::tc_fence_after();
       if (!v.skip) {
         const Seq& s = v.s;
         const uint32_t tacc = (g == 0 ? tK : tV) + lane_base;
@@ -805,7 +815,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) ptx::mbar_arrive(bar(kDkvAccFree));
         ++used;
       }
-      item = items.next_warp(it, lane);
     }
   }
   ptx::tc_fence_before();
@@ -853,12 +862,12 @@ enum : int {
   kDqChecked = kDqLanded + kDqChecks,
   kDqDrain = kDqChecked + kDqChecks,
   kDqItemFull,
-  kDqItemEmpty = kDqItemFull + 2,
-  kDqBars = kDqItemEmpty + 2
+  kDqItemEmpty = kDqItemFull + kItemSlots,
+  kDqBars = kDqItemEmpty + kItemSlots
 };
 constexpr int kDqOffQ = 0, kDqOffO = kTileBytes, kDqOffK = 2 * kTileBytes,
               kDqOffV = kDqOffK + kDqKStages * kTileBytes,
-              kDqOffItems = kDqOffV + kDqVStages * kTileBytes, kDqOffPoison = kDqOffItems + 32,
+              kDqOffItems = kDqOffV + kDqVStages * kTileBytes, kDqOffPoison = kDqOffItems + 16 * kItemSlots,
               kDqOffDots = kDqOffPoison + kPoisonBytes, kDqOffBar = kDqOffDots + kTile * 4,
               kDqOffSlot = kDqOffBar + kDqBars * 8, kDqSmem = kDqOffSlot + 8 + 1024;
 static_assert(kDqSmem <= 232448, "shared memory budget (dq)");
@@ -997,11 +1006,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
         }
         items.ask(it);
-        ++asked;
+        asked = it + 1;
         item = items.next_lane(it);
       }
-      // Every copy this thread started lands before the CTA can exit, and so does the
-      // last answer asked for.
+      // Every copy this thread started lands before the CTA can exit, and so does every
+      // answer asked for.
       if (used > 0) wait_bounded(bar(kDqQ), (used - 1) & 1, abort_flag, p.timeout_ns, false);
       for (int st = 0; st < kDqKStages && st < k_issued; ++st)
         wait_bounded(bar(kDqKFull + st), ((k_issued - 1 - st) / kDqKStages) & 1, abort_flag, p.timeout_ns,
@@ -1009,8 +1018,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int st = 0; st < kDqVStages && st < v_issued; ++st)
         wait_bounded(bar(kDqVFull + st), ((v_issued - 1 - st) / kDqVStages) & 1, abort_flag, p.timeout_ns,
                      false);
-      if (asked > 0)
-        wait_bounded(items.full + 8 * ((asked - 1) & 1), ((asked - 1) >> 1) & 1, abort_flag, p.timeout_ns, false);
+      items.drain(asked);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -1148,8 +1156,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t c2 = ptx::f2_pack(p.c, p.c);
     int used = 0, tile = 0, k_base = 0;
     bool ok = true;
-    for (int item = static_cast<int>(blockIdx.x), it = 0; ok && item >= 0; ++it) {
-      const DqItem w = dq_item<kCausal, kVarlen>(p, item);
+    // The row's log-sum-exp is read when the item is known, long before it is used.
+    auto read_lse = [&](const DqItem& w) -> float {
+      if (w.n == 0 || w.q0 + row >= w.s.sq) return -__int_as_float(0x7F800000);
+      return __ldg(p.lse + (kVarlen ? static_cast<size_t>(w.s.head) * p.Sq + w.s.q_base + w.q0 + row
+                                    : (static_cast<size_t>(w.s.batch) * p.Hq + w.s.head) * p.Sq + w.q0 + row));
+    };
+    int item = static_cast<int>(blockIdx.x);
+    DqItem w = dq_item<kCausal, kVarlen>(p, item);
+    float lse = read_lse(w);
+    for (int it = 0; ok && item >= 0; ++it) {
       const int n = w.n;
       // Keys this row sees, counted from the part's first.
       const int limit = (kCausal ? min(w.q0 + row + w.off + 1, w.s.sk) : w.s.sk) - w.t0 * kTile;
@@ -1157,12 +1173,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t nl2 = 0, nd2 = 0;
       if (n > 0) {
         const Seq& s = w.s;
-        // The row's statistics: each warpgroup adds its 64 columns of dO O. (lse is read
-        // before the waits, whose time covers its latency.)
-        float dot = 0.f, lse = -__int_as_float(0x7F800000);
-        if (w.q0 + row < s.sq)
-          lse = __ldg(p.lse + (kVarlen ? static_cast<size_t>(s.head) * p.Sq + s.q_base + w.q0 + row
-                                       : (static_cast<size_t>(s.batch) * p.Hq + s.head) * p.Sq + w.q0 + row));
+        // The row's statistics: each warpgroup adds its 64 columns of dO O.
+        float dot = 0.f;
         const int fo = k_base, os = fo % kDqKStages;
         ok = warp_wait(bar(kDqQ), used & 1, abort_flag, p.timeout_ns) &&
              warp_wait(bar(kDqKFull + os), (fo / kDqKStages) & 1, abort_flag, p.timeout_ns);
@@ -1233,15 +1245,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) ptx::mbar_arrive(bar(kDqDsFull));
       }
       if (!ok) break;
-      // ---- epilogue: each warpgroup stores 64 columns of the rows.
+      // ---- epilogue: each warpgroup stores 64 columns of the rows. (The item again, from
+      // an opaque copy of its number: nothing of it is kept across the loop. And the next
+      // one, before the wait.)
       const bool zero = n == 0;
-      if (!zero && !(ok = warp_wait(bar(kDqAcc), used & 1, abort_flag, p.timeout_ns))) break;
-      ptx::tc_fence_after();
-      // (The item again, from an opaque copy of its number: nothing of it is kept across
-      // the loop.)
       int again = item;
       asm volatile("" : "+r"(again));
       const DqItem v = dq_item<kCausal, kVarlen>(p, again);
+      item = items.next_warp(it, lane);
+      if (item >= 0) {
+        w = dq_item<kCausal, kVarlen>(p, item);
+        lse = read_lse(w);
+      }
+      if (!zero && !(ok = warp_wait(bar(kDqAcc), used & 1, abort_flag, p.timeout_ns))) break;
+      ptx::tc_fence_after();
       if (!v.skip) {
         const Seq& s = v.s;
         const uint32_t tacc = tQ + lane_base + 64 * g;
@@ -1269,7 +1286,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         k_base += n + 1;
         ++used;
       }
-      item = items.next_warp(it, lane);
     }
   }
   ptx::tc_fence_before();
