@@ -209,6 +209,14 @@ __device__ __forceinline__ void issue_second(uint32_t tmem_d, uint32_t tmem_a, u
                                              uint32_t accumulate) {
   issue_second_seq(tmem_d, tmem_a, b_lo, accumulate, std::make_integer_sequence<int, 8>{});
 }
+// The same in two parts: the columns that each warpgroup writes first, then the others.
+__device__ __forceinline__ void issue_second_part(bool first, uint32_t tmem_d, uint32_t tmem_a, uint32_t b_lo,
+                                                  uint32_t accumulate) {
+  if (first)
+    issue_second_seq(tmem_d, tmem_a, b_lo, accumulate, std::integer_sequence<int, 0, 1, 4, 5>{});
+  else
+    issue_second_seq(tmem_d, tmem_a, b_lo, 1, std::integer_sequence<int, 2, 3, 6, 7>{});
+}
 
 // Byte offset of 16-byte chunk c (0..15) of row r in a 128 x 128 bf16 tile stored as
 // two 64-column halves in the 128-byte swizzle.
@@ -340,7 +348,7 @@ __device__ __forceinline__ uint64_t pair_of(const uint32_t (&r)[32], int x) {
 // memory); kept in pr, and written over S as bf16.
 template <bool kMask>
 __device__ __forceinline__ void dkv_p(uint32_t tS, const ulonglong2* stat, uint64_t c2, int lo, int hi,
-                                      Half& pr) {
+                                      Half& pr, uint32_t half_bar, int lane) {
   by_halves(tS, [&](int ch, const uint32_t (&r)[32]) {
     uint32_t w[16];
 #pragma unroll
@@ -362,6 +370,12 @@ __device__ __forceinline__ void dkv_p(uint32_t tS, const ulonglong2* stat, uint6
       }
     }
     ptx::tmem_st16(tS + 16 * ch, w);
+    if (ch == 0) {
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(half_bar);
+    }
   });
 }
 
@@ -432,6 +446,7 @@ enum : int {
   kDkvOFull = kDkvQEmpty + kDkvStages,
   kDkvOEmpty = kDkvOFull + kDkvStages,
   kDkvSFull = kDkvOEmpty + kDkvStages,
+  kDkvPHalf,    // each warpgroup's first 32 columns of P
   kDkvPFull,
   kDkvDpFull,
   kDkvDsFull,
@@ -515,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kDkvBars; ++i)
-      ptx::mbar_init(bar(i), (i == kDkvPFull || i == kDkvDsFull || i == kDkvAccFree) ? 8
+      ptx::mbar_init(bar(i), (i == kDkvPHalf || i == kDkvPFull || i == kDkvDsFull || i == kDkvAccFree) ? 8
                              : i >= kDkvItemEmpty                                    ? item_readers(kCheck)
                                                                                      : 1);
     *abort_flag = 0;
@@ -647,10 +662,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; ok && i < w.n; ++i) {
           const int t = tile + i;
           const bool more = i + 1 < w.n;
-          if (!(ok = wait(kDkvPFull, t))) break;
+          if (!(ok = wait(kDkvPHalf, t))) break;
           // The item's first second product starts dV (and dK) anew.
           if (i == 0 && used > 0 && !(ok = wait(kDkvAccFree, used - 1))) break;
-          issue_second(tV, tS, desc_lo(o_tile(t), kHalfBytes), i > 0);
+          issue_second_part(true, tV, tS, desc_lo(o_tile(t), kHalfBytes), i > 0);
+          if (!(ok = wait(kDkvPFull, t))) break;
+          issue_second_part(false, tV, tS, desc_lo(o_tile(t), kHalfBytes), 1);
           ptx::mma_commit_warp(bar(kDkvOEmpty + t % kDkvStages));
           if (more && !(ok = do_s(t + 1))) break;
           if (!(ok = wait(kDkvDsFull, t))) break;
@@ -757,9 +774,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         ptx::tc_fence_after();
         if (mk)
-          dkv_p<true>(tSh, stat, c2, lo, hi, pr);
+          dkv_p<true>(tSh, stat, c2, lo, hi, pr, bar(kDkvPHalf), lane);
         else
-          dkv_p<false>(tSh, stat, c2, lo, hi, pr);
+          dkv_p<false>(tSh, stat, c2, lo, hi, pr, bar(kDkvPHalf), lane);
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
