@@ -246,9 +246,9 @@ __device__ __forceinline__ void clean_row(uint32_t tile, int r, F with_col) {
   }
 }
 
-// Records of non-finite elements found in masked tiles, for two items: per result column
-// the last (or first) row that has one, and whether there is any.
-constexpr int kPoisonWords = kD + 4, kPoisonBytes = 2 * kPoisonWords * 4;
+// Record of an item's non-finite elements found in masked tiles: per result column the
+// last (or first) row that has one, and whether there is any.
+constexpr int kPoisonWords = kD + 4, kPoisonBytes = kPoisonWords * 4;
 
 // By the 256 softmax threads, which all found the record set: once every one has read it.
 __device__ __forceinline__ void clear_poison(int* rec, int none) {
@@ -437,15 +437,18 @@ __device__ __forceinline__ void dq_ds(uint32_t tP, uint32_t tS, uint64_t nd2, in
 // dS_i from dP_i; while dK_i and dP_{i+1} run, they form P_{i+1} from S_{i+1}.
 // Each turn has 1024 tensor cycles to cover 64 exponentials per thread, or 64
 // subtract-multiplies.
-constexpr int kDkvStages = 2;
+// Shared memory is full as well: K, V, three stages of Q and two of dO. Q_i is read last
+// (dK_i) shortly before S_{i+2} wants Q_{i+2}: with two stages its refill had 1024 cycles, and
+// takes some 1600 when every SM streams at L2's limit; dO has slack.
+constexpr int kDkvQStages = 3, kDkvOStages = 2;
 enum : int {
   kDkvKV = 0,
   kDkvKVFree,   // the item's last S and dP products have read K and V
   kDkvQFull,
-  kDkvQEmpty = kDkvQFull + kDkvStages,
-  kDkvOFull = kDkvQEmpty + kDkvStages,
-  kDkvOEmpty = kDkvOFull + kDkvStages,
-  kDkvSFull = kDkvOEmpty + kDkvStages,
+  kDkvQEmpty = kDkvQFull + kDkvQStages,
+  kDkvOFull = kDkvQEmpty + kDkvQStages,  // dO and the row statistics
+  kDkvOEmpty = kDkvOFull + kDkvOStages,
+  kDkvSFull = kDkvOEmpty + kDkvOStages,
   kDkvPHalf,    // each warpgroup's first 32 columns of P
   kDkvPFull,
   kDkvDpFull,
@@ -460,11 +463,11 @@ enum : int {
   kDkvBars = kDkvItemEmpty + kItemSlots
 };
 constexpr int kDkvOffK = 0, kDkvOffV = kTileBytes, kDkvOffQ = 2 * kTileBytes,
-              kDkvOffO = kDkvOffQ + kDkvStages * kTileBytes,
-              kDkvOffStats = kDkvOffO + kDkvStages * kTileBytes,
-              kDkvOffItems = kDkvOffStats + kDkvStages * kStatFloats * 4,
+              kDkvOffO = kDkvOffQ + kDkvQStages * kTileBytes,
+              kDkvOffStats = kDkvOffO + kDkvOStages * kTileBytes,
+              kDkvOffItems = kDkvOffStats + kDkvOStages * kStatFloats * 4,
               kDkvOffPoison = kDkvOffItems + 16 * kItemSlots, kDkvOffBar = kDkvOffPoison + kPoisonBytes,
-              kDkvOffSlot = kDkvOffBar + kDkvBars * 8, kDkvSmem = kDkvOffSlot + 8 + 1024;
+              kDkvOffSlot = kDkvOffBar + kDkvBars * 8, kDkvSmem = kDkvOffSlot + 8;
 static_assert(kDkvSmem <= 232448, "shared memory budget (dkv)");
 
 // An item: an owned key tile and the part of its streamed tiles: query tiles from first_qt
@@ -516,9 +519,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                  const BwdParams p) {
   extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = ptx::smem_u32(smem_raw);
-  const uint32_t sbase = (raw + 1023u) & ~1023u;
-  uint8_t* smem = smem_raw + (sbase - raw);
+  // Dynamic shared memory starts on a 1024-byte boundary here (the tiles' swizzle wants it,
+  // and there is no room to align it).
+  const uint32_t sbase = ptx::smem_u32(smem_raw);
+  uint8_t* smem = smem_raw;
+  if (sbase & 1023u) {
+    if (threadIdx.x == 0) atomicOr(&g_attn_status, 4u);
+    ptx::grid_dependency_wait();
+    return;
+  }
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kDkvOffSlot);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kDkvOffSlot + 4);
   int* poison = reinterpret_cast<int*>(smem + kDkvOffPoison);
@@ -537,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::fence_mbar_init();
     ptx::fence_proxy_async_smem();
   }
-  for (int i = threadIdx.x; i < 2 * kPoisonWords; i += kThreads) poison[i] = i % kPoisonWords < kD ? -1 : 0;
+  for (int i = threadIdx.x; i < kPoisonWords; i += kThreads) poison[i] = i < kD ? -1 : 0;
   if (warp == 0 && lane == 0) {
     ptx::prefetch_tmap(&tm_q);
     ptx::prefetch_tmap(&tm_k);
@@ -556,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // In every role: `used` counts the items with streamed tiles so far (the phases of the
   // per-item barriers), `tile` their streamed tiles (the phases of the per-tile ones;
-  // tile t goes to ring stage t % kDkvStages).
+  // tile t goes to stage t % kDkvQStages of Q's ring, t % kDkvOStages of dO's).
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
     if (lane == 0) {
@@ -580,22 +589,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           QueryTiles qt(w);
           int h = s.head * p.group + w.t0 / w.per;
           for (int i = 0; i < w.n; ++i) {
-            const int st = q_issued % kDkvStages;
-            const uint32_t par = ((q_issued / kDkvStages) & 1) ^ 1;
+            const int qs = q_issued % kDkvQStages, os = o_issued % kDkvOStages;
             dbg_ok(s.q_base + qt.q0 < p.Sq && h < p.Hq);
-            if (!(ok = wait_bounded(bar(kDkvQEmpty + st), par, abort_flag, p.timeout_ns, true))) break;
-            ptx::mbar_arrive_expect_tx(bar(kDkvQFull + st), kTileBytes + kStatFloats * 4);
-            load_tile(sbase + kDkvOffQ + st * kTileBytes, &tm_q, bar(kDkvQFull + st), p.layout,
+            if (!(ok = wait_bounded(bar(kDkvQEmpty + qs), ((q_issued / kDkvQStages) & 1) ^ 1, abort_flag,
+                                    p.timeout_ns, true)))
+              break;
+            ptx::mbar_arrive_expect_tx(bar(kDkvQFull + qs), kTileBytes);
+            load_tile(sbase + kDkvOffQ + qs * kTileBytes, &tm_q, bar(kDkvQFull + qs), p.layout,
+                      s.q_base + qt.q0, h, s.batch, pol_reuse);
+            ++q_issued;
+            if (!(ok = wait_bounded(bar(kDkvOEmpty + os), ((o_issued / kDkvOStages) & 1) ^ 1, abort_flag,
+                                    p.timeout_ns, true)))
+              break;
+            ptx::mbar_arrive_expect_tx(bar(kDkvOFull + os), kTileBytes + kStatFloats * 4);
+            load_tile(sbase + kDkvOffO + os * kTileBytes, &tm_do, bar(kDkvOFull + os), p.layout,
                       s.q_base + qt.q0, h, s.batch, pol_reuse);
             const float* src = p.stats + (static_cast<size_t>(s.slot_q) + static_cast<size_t>(h) * p.q_slots +
                                           qt.q0 / kTile) * kStatFloats;
-            ptx::bulk_load(sbase + kDkvOffStats + st * kStatFloats * 4, src, kStatFloats * 4,
-                           bar(kDkvQFull + st));
-            ++q_issued;
-            if (!(ok = wait_bounded(bar(kDkvOEmpty + st), par, abort_flag, p.timeout_ns, true))) break;
-            ptx::mbar_arrive_expect_tx(bar(kDkvOFull + st), kTileBytes);
-            load_tile(sbase + kDkvOffO + st * kTileBytes, &tm_do, bar(kDkvOFull + st), p.layout,
-                      s.q_base + qt.q0, h, s.batch, pol_reuse);
+            ptx::bulk_load(sbase + kDkvOffStats + os * kStatFloats * 4, src, kStatFloats * 4,
+                           bar(kDkvOFull + os));
             ++o_issued;
             if (qt.q0 == qt.last) ++h;
             qt.step();
@@ -609,22 +621,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Every copy this thread started lands before the CTA can exit, and so does every
       // answer asked for.
       if (used > 0) wait_bounded(bar(kDkvKV), (used - 1) & 1, abort_flag, p.timeout_ns, false);
-      for (int st = 0; st < kDkvStages; ++st) {
-        if (st < q_issued)
-          wait_bounded(bar(kDkvQFull + st), ((q_issued - 1 - st) / kDkvStages) & 1, abort_flag,
-                       p.timeout_ns, false);
-        if (st < o_issued)
-          wait_bounded(bar(kDkvOFull + st), ((o_issued - 1 - st) / kDkvStages) & 1, abort_flag,
-                       p.timeout_ns, false);
-      }
+      for (int st = 0; st < kDkvQStages && st < q_issued; ++st)
+        wait_bounded(bar(kDkvQFull + st), ((q_issued - 1 - st) / kDkvQStages) & 1, abort_flag, p.timeout_ns,
+                     false);
+      for (int st = 0; st < kDkvOStages && st < o_issued; ++st)
+        wait_bounded(bar(kDkvOFull + st), ((o_issued - 1 - st) / kDkvOStages) & 1, abort_flag, p.timeout_ns,
+                     false);
       items.drain(asked);
     }
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer (whole warp)
     const uint32_t k_desc = desc_lo(sbase + kDkvOffK, 16), v_desc = desc_lo(sbase + kDkvOffV, 16);
-    auto q_tile = [&](int t) -> uint32_t { return sbase + kDkvOffQ + (t % kDkvStages) * kTileBytes; };
-    auto o_tile = [&](int t) -> uint32_t { return sbase + kDkvOffO + (t % kDkvStages) * kTileBytes; };
+    auto q_tile = [&](int t) -> uint32_t { return sbase + kDkvOffQ + (t % kDkvQStages) * kTileBytes; };
+    auto o_tile = [&](int t) -> uint32_t { return sbase + kDkvOffO + (t % kDkvOStages) * kTileBytes; };
     auto wait = [&](int b, uint32_t par) -> bool {
       const bool r = warp_wait(bar(b), par & 1, abort_flag, p.timeout_ns);
       ptx::tc_fence_after();
@@ -639,9 +649,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // S_i: Q_i has landed; a masked tile's rows have been checked first (both of
         // its tiles, so dO_i has landed too).
         auto do_s = [&](int t) -> bool {
-          if (!wait(kDkvQFull + t % kDkvStages, t / kDkvStages)) return false;
+          if (!wait(kDkvQFull + t % kDkvQStages, t / kDkvQStages)) return false;
           if (kCheck && dkv_masked<kCausal>(qt.q0, w.s.sq, w.off, w.k0)) {
-            if (!wait(kDkvOFull + t % kDkvStages, t / kDkvStages)) return false;
+            if (!wait(kDkvOFull + t % kDkvOStages, t / kDkvOStages)) return false;
             if (lane == 0) ptx::mbar_arrive(bar(kDkvLanded));
             if (!wait(kDkvChecked, checks)) return false;
             ++checks;
@@ -652,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return true;
         };
         auto do_dp = [&](int t) -> bool {
-          if (!wait(kDkvOFull + t % kDkvStages, t / kDkvStages)) return false;
+          if (!wait(kDkvOFull + t % kDkvOStages, t / kDkvOStages)) return false;
           issue_s(tP, v_desc, desc_lo(o_tile(t), 16));
           ptx::mma_commit_warp(bar(kDkvDpFull));
           return true;
@@ -668,11 +678,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           issue_second_part(true, tV, tS, desc_lo(o_tile(t), kHalfBytes), i > 0);
           if (!(ok = wait(kDkvPFull, t))) break;
           issue_second_part(false, tV, tS, desc_lo(o_tile(t), kHalfBytes), 1);
-          ptx::mma_commit_warp(bar(kDkvOEmpty + t % kDkvStages));
           if (more && !(ok = do_s(t + 1))) break;
           if (!(ok = wait(kDkvDsFull, t))) break;
           issue_second(tK, tP, desc_lo(q_tile(t), kHalfBytes), i > 0);
-          ptx::mma_commit_warp(bar(kDkvQEmpty + t % kDkvStages));
+          ptx::mma_commit_warp(bar(kDkvQEmpty + t % kDkvQStages));
+          // (dO's last product is dV, but the statistics beside it are read until dS.)
+          ptx::mma_commit_warp(bar(kDkvOEmpty + t % kDkvOStages));
           if (more && !(ok = do_dp(t + 1))) break;
           if (i + 2 == w.n) ptx::mma_commit_warp(bar(kDkvKVFree));  // the last dP was issued
         }
@@ -694,8 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // elements are set to 0 as well. The keys that do see it still get NaN: in
     // every column of dK (and of dV, when it is Q) through the statistics, and in
     // the column of a non-finite dO element through `poison`, the last row that has
-    // one there. Two items' records are kept, for the one being finished and the next;
-    // an item's epilogue clears its own.
+    // one there. An item's epilogue clears it; only then are the next item's put in.
     if constexpr (kCheck) {
       const int tid = static_cast<int>(threadIdx.x) - 64;
       int used = 0, tile = 0, m = 0;
@@ -703,7 +713,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int item = static_cast<int>(blockIdx.x), it = 0; ok && item >= 0; ++it) {
         const DkvItem w = dkv_item<kCausal, kVarlen>(p, item);
         const Seq& s = w.s;
-        int* rec = poison + (used & 1) * kPoisonWords;
         QueryTiles qt(w);
         for (int i = 0; i < w.n; ++i, qt.step()) {
           const int q0 = qt.q0;
@@ -712,9 +721,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = !ptx::named_barrier_or(1, 64, !ok);
           if (!ok) break;
           ++m;
-          const int st = (tile + i) % kDkvStages;
-          const uint32_t q_t = sbase + kDkvOffQ + st * kTileBytes, o_t = sbase + kDkvOffO + st * kTileBytes;
-          const float* stat = reinterpret_cast<const float*>(smem + kDkvOffStats) + st * kStatFloats;
+          const int os = (tile + i) % kDkvOStages;
+          const uint32_t q_t = sbase + kDkvOffQ + ((tile + i) % kDkvQStages) * kTileBytes;
+          const uint32_t o_t = sbase + kDkvOffO + os * kTileBytes;
+          const float* stat = reinterpret_cast<const float*>(smem + kDkvOffStats) + os * kStatFloats;
           bool dirty = false;
           for (int r = tid; r < kTile; r += 64) {
             const float nl = stat[r], nd = stat[kTile + r];
@@ -725,10 +735,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               zero_row(o_t, r);
               dirty = true;
             } else if (isnan(nl) || isnan(nd)) {
+              if (used > 0)
+                wait_bounded(bar(kDkvAccFree), (used - 1) & 1, abort_flag, p.timeout_ns, true);
               clean_row(q_t, r, [](int) {});
               clean_row(o_t, r, [&](int col) {
-                atomicMax(&rec[col], q0 + r);
-                *static_cast<volatile int*>(rec + kD) = 1;
+                atomicMax(&poison[col], q0 + r);
+                *static_cast<volatile int*>(poison + kD) = 1;
               });
               dirty = true;
             }
@@ -765,11 +777,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int lo = kCausal ? first_row - qt.q0 - 64 * g : 0;
         const int hi = sq - qt.q0 - 64 * g;
         const ulonglong2* stat = reinterpret_cast<const ulonglong2*>(
-            smem + kDkvOffStats + (tile % kDkvStages) * kStatFloats * 4 + 256 * g);
+            smem + kDkvOffStats + (tile % kDkvOStages) * kStatFloats * 4 + 256 * g);
         Half pr;
         if (!(ok = warp_wait(bar(kDkvSFull), tile & 1, abort_flag, p.timeout_ns))) break;
-        // (Q's barrier, for the statistics that landed with it: long complete.)
-        if (!(ok = warp_wait(bar(kDkvQFull + tile % kDkvStages), (tile / kDkvStages) & 1, abort_flag,
+        // (dO's barrier, for the statistics that land with it.)
+        if (!(ok = warp_wait(bar(kDkvOFull + tile % kDkvOStages), (tile / kDkvOStages) & 1, abort_flag,
                              p.timeout_ns)))
           break;
         ptx::tc_fence_after();
@@ -808,11 +820,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!v.skip) {
         const Seq& s = v.s;
         const uint32_t tacc = (g == 0 ? tK : tV) + lane_base;
-        int* rec = poison + (used & 1) * kPoisonWords;
-        const bool any = kCheck && !zero && *static_cast<volatile int*>(rec + kD);
+        const bool any = kCheck && !zero && *static_cast<volatile int*>(poison + kD);
         // The last query row whose non-finite dO element a key may see (see above).
         const int seen = kCausal ? max(0, v.k0 + row - v.off) : 0;
-        auto is_nan = [&](int col) -> bool { return any && g == 1 && rec[col] >= seen; };
+        auto is_nan = [&](int col) -> bool { return any && g == 1 && poison[col] >= seen; };
         if (p.n_splits == 1) {
           const bool in = v.k0 + row < s.sk && dbg_ok(s.k_base + v.k0 + row < p.Sk);
           uint16_t* dst = (g == 0 ? p.dk : p.dv) +
@@ -824,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float* dst = p.part + (((static_cast<size_t>(s.split) * 2 + g) * slots + slot) * kTile + row) * kD;
           store_part<kD>(tacc, zero, dst, is_nan);
         }
-        if (any) clear_poison(rec, -1);
+        if (any) clear_poison(poison, -1);
       }
       if (!zero) {
         ptx::tc_fence_before();
@@ -951,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::fence_mbar_init();
     ptx::fence_proxy_async_smem();
   }
-  for (int i = threadIdx.x; i < 2 * kPoisonWords; i += kThreads) poison[i] = i % kPoisonWords < kD ? kNever : 0;
+  for (int i = threadIdx.x; i < kPoisonWords; i += kThreads) poison[i] = i < kD ? kNever : 0;
   if (warp == 0 && lane == 0) {
     ptx::prefetch_tmap(&tm_q);
     ptx::prefetch_tmap(&tm_k);
@@ -1107,8 +1118,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // its key to a query that does not see it. Once S has been formed, the tile's
     // rows past the sequence's end and its non-finite elements are set to 0; the
     // queries that see such a key get NaN in that column through `poison`, the first key
-    // that has one there. Two items' records are kept, for the one being finished and
-    // the next; an item's epilogue clears its own.
+    // that has one there. An item's epilogue clears it; only then are the next item's put
+    // in.
     if constexpr (kCheck) {
       const int tid = static_cast<int>(threadIdx.x) - 64;
       int used = 0, tile = 0, k_base = 0, m = 0;
@@ -1116,7 +1127,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int item = static_cast<int>(blockIdx.x), it = 0; ok && item >= 0; ++it) {
         const DqItem w = dq_item<kCausal, kVarlen>(p, item);
         const Seq& s = w.s;
-        int* rec = poison + (used & 1) * kPoisonWords;
         for (int j = max(0, w.first_masked - w.t0); j < w.n; ++j, ++m) {
           ok = wait_bounded(bar(kDqLanded + m % kDqChecks), (m / kDqChecks) & 1, abort_flag, p.timeout_ns,
                             true) &&
@@ -1143,9 +1153,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               acc = ptx::bf16x2_nonfinite_acc(x.z, ptx::bf16x2_nonfinite_acc(x.w, acc));
             }
             if (acc != 0) {
+              if (used > 0)
+                wait_bounded(bar(kDqAccFree), (used - 1) & 1, abort_flag, p.timeout_ns, true);
               clean_row(kt, r, [&](int col) {
-                atomicMin(&rec[col], first + r);
-                *static_cast<volatile int*>(rec + kD) = 1;
+                atomicMin(&poison[col], first + r);
+                *static_cast<volatile int*>(poison + kD) = 1;
               });
               dirty = true;
             }
@@ -1279,10 +1291,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!v.skip) {
         const Seq& s = v.s;
         const uint32_t tacc = tQ + lane_base + 64 * g;
-        int* rec = poison + (used & 1) * kPoisonWords;
-        const bool any = kCheck && !zero && *static_cast<volatile int*>(rec + kD);
+        const bool any = kCheck && !zero && *static_cast<volatile int*>(poison + kD);
         const int sees = kCausal ? min(v.q0 + row + v.off + 1, s.sk) : s.sk;
-        auto is_nan = [&](int col) -> bool { return any && rec[64 * g + col] < sees; };
+        auto is_nan = [&](int col) -> bool { return any && poison[64 * g + col] < sees; };
         if (p.n_splits == 1) {
           const bool in = v.q0 + row < s.sq && dbg_ok(s.q_base + v.q0 + row < p.Sq);
           uint16_t* dst =
@@ -1294,7 +1305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float* dst = p.part + ((static_cast<size_t>(s.split) * slots + slot) * kTile + row) * kD + 64 * g;
           store_part<64>(tacc, zero, dst, is_nan);
         }
-        if (any) clear_poison(rec, kNever);
+        if (any) clear_poison(poison, kNever);
       }
       if (!zero) {
         ptx::tc_fence_before();
