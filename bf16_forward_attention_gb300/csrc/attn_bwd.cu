@@ -94,6 +94,16 @@ int heads_together(int64_t heads, int64_t bytes) {
   return static_cast<int>((heads + groups - 1) / groups);
 }
 
+// What an item's number means (BH, n_tiles and n_splits are set).
+void place(bwd::BwdParams* p, int heads, int64_t owners) {
+  p->n_groups = (p->BH + heads - 1) / heads;
+  p->heads = bwd::Div::by(heads);
+  p->last = bwd::Div::by(p->BH - int64_t(p->n_groups - 1) * heads);
+  p->span = bwd::Div::by(int64_t(p->n_tiles) * heads);
+  p->splits = bwd::Div::by(p->n_splits);
+  p->owners = bwd::Div::by(owners);
+}
+
 struct Plan {
   int64_t q_tiles, k_tiles;  // per sequence (grid)
   int64_t q_slots, k_slots;  // tile slots per head
@@ -235,8 +245,8 @@ int bwd_impl(const void* dout, const void* q, const void* k, const void* v, cons
 
   p.BH = static_cast<int>(B * Hq);
   p.n_tiles = static_cast<int>(pl.q_tiles);
-  p.head_group = causal ? heads_together(B * Hq, 512 * keys_per_head * Hkv / Hq) : 1;
   p.n_splits = pl.dq_splits;
+  place(&p, causal ? heads_together(B * Hq, 512 * keys_per_head * Hkv / Hq) : 1, Hq);
   p.part = dq_part;
   auto* dq_fn = varlen ? (causal ? bwd::attn_bwd_dq<true, true> : bwd::attn_bwd_dq<false, true>)
                        : (causal ? bwd::attn_bwd_dq<true, false> : bwd::attn_bwd_dq<false, false>);
@@ -263,8 +273,8 @@ int bwd_impl(const void* dout, const void* q, const void* k, const void* v, cons
 
   p.BH = static_cast<int>(B * Hkv);
   p.n_tiles = static_cast<int>(pl.k_tiles);
-  p.head_group = causal ? heads_together(B * Hkv, 512 * rows_per_head * (Hq / Hkv)) : 1;
   p.n_splits = pl.dkv_splits;
+  place(&p, causal ? heads_together(B * Hkv, 512 * rows_per_head * (Hq / Hkv)) : 1, Hkv);
   p.part = dkv_part;
   auto* dkv_fn = varlen ? (causal ? bwd::attn_bwd_dkv<true, true> : bwd::attn_bwd_dkv<false, true>)
                         : (causal ? bwd::attn_bwd_dkv<true, false> : bwd::attn_bwd_dkv<false, false>);

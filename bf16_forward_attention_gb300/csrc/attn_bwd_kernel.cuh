@@ -46,13 +46,36 @@ namespace bwd {
 constexpr int kTile = 128;             // queries and keys per tile
 constexpr int kStatFloats = 2 * kTile; // per query tile: 128 of -lse log2(e), 128 of -D
 
+// Division of n in [0, 2^31) by a number fixed for a launch, as a product (Granlund and
+// Montgomery, "Division by invariant integers using multiplication"): with 2^(s+1) >= d and
+// mul = ceil(2^(32+s) / d), n * mul exceeds n 2^(32+s) / d by less than 2^(32+s) / d. An item's
+// place takes five divisions, some 500 cycles otherwise.
+struct Div {
+  uint32_t mul;
+  int shift, d;
+  __host__ static Div by(int64_t d) {
+    Div r;
+    r.d = static_cast<int>(d);
+    r.shift = 0;
+    while ((int64_t(2) << r.shift) < d) ++r.shift;
+    r.mul = static_cast<uint32_t>(((uint64_t(1) << (32 + r.shift)) + d - 1) / d);  // (d = 1: not used)
+    return r;
+  }
+  __device__ __forceinline__ int of(int n) const {
+    return d == 1 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), mul) >> shift);
+  }
+};
+
 struct BwdParams {
   int Sq, Sk;              // per batch entry, or packed totals
   int Hq, Hkv, group;      // group = Hq / Hkv
   int BH;                  // heads of the grid: B * Hq (dq) or B * Hkv (dkv)
   int n_tiles;             // tiles of the owned axis per head (grid)
-  int head_group;          // heads scheduled together (causal: longest first)
-  int n_splits;            // CTAs per owned tile, each over a part of the streamed tiles
+  int n_splits;            // items per owned tile, each over a part of the streamed tiles
+  // An item's place: heads are scheduled together in n_groups groups (causal: longest
+  // first), of heads.d heads each, the last one of last.d.
+  int n_groups;
+  Div splits, span, heads, last, owners;  // span = n_tiles * heads.d, owners = heads of the owned axis
   int layout, mode;
   float c, scale;          // c = scale * log2(e)
   unsigned long long timeout_ns;
@@ -88,19 +111,17 @@ struct Seq {
 template <bool kCausal, bool kVarlen, bool kOwnQ>
 __device__ __forceinline__ Seq seq_of(const BwdParams& p, int block) {
   Seq s;
-  s.split = block % p.n_splits;
-  const int item = block / p.n_splits;
-  const int span = p.n_tiles * p.head_group;
-  const int g = item / span, r = item - g * span;
-  const int gs = min(p.head_group, p.BH - g * p.head_group);
-  const int t = r / gs;
-  const int bh = g * p.head_group + r % gs;
+  const int item = p.splits.of(block);
+  s.split = block - item * p.n_splits;
+  const int g = p.span.of(item), r = item - g * p.span.d;
+  const bool last = g == p.n_groups - 1;
+  const int t = last ? p.last.of(r) : p.heads.of(r);
+  const int bh = g * p.heads.d + r - t * (last ? p.last.d : p.heads.d);
   // Longest ranges first under the causal mask: late queries see most keys, early
   // keys are seen by most queries.
   s.tile = (kOwnQ && kCausal) ? p.n_tiles - 1 - t : t;
-  const int H = kOwnQ ? p.Hq : p.Hkv;
-  const int b = bh / H;
-  s.head = bh % H;
+  const int b = p.owners.of(bh);
+  s.head = bh - b * p.owners.d;
   s.bad = false;
   if (kVarlen) {
     s.q_base = __ldg(p.cu_q + b);
@@ -274,42 +295,83 @@ __device__ __forceinline__ size_t row_at(int layout, int batch, int H, int S, in
                       : (static_cast<size_t>(batch) * S + row) * H + head) * kD;
 }
 
-// kCols finished columns of a row of a result in TMEM -> bf16 in global memory (dst null:
-// a row past the end; its lane still takes part in the loads). A thread holds one row,
-// so its stores are 16 bytes of consecutive addresses each and need no staging.
-// `poison(col)`: the column is NaN; any: there is such a column. zero: no product
-// was formed, the result is 0.
+// Two neighbouring fp32 of a TMEM row.
+__device__ __forceinline__ uint64_t pair_of(const uint32_t (&r)[32], int x) {
+  return ptx::f2_pack(__uint_as_float(r[x]), __uint_as_float(r[x + 1]));
+}
+
+// kCols finished columns of a warp's 32 rows of a result in TMEM -> bf16 in global memory.
+// A thread holds one row (lane 4 hi + lo: row 4 hi + lo); stored as it is, a warp's
+// 16-byte store would touch 32 lines (3,300 cycles an item in dq). So 64 columns at a
+// time, an 8 x 8 transposition across the lanes of one lo (hi against the 16-byte chunk,
+// three exchanges) leaves chunk hi of row 4 k + lo in register k, and each store writes
+// 128 bytes of four rows. `out`: row 0 of the warp, pitch: elements from row to row, rows:
+// how many are stored. `poison(col)`: the thread's row is NaN there; any: there is such
+// a column. zero: no product was formed, the result is 0.
 template <int kCols, typename F>
-__device__ __forceinline__ void store_row(uint32_t tacc, bool zero, float factor, int mode, uint16_t* dst,
-                                          bool any, F poison) {
+__device__ __forceinline__ void store_rows(uint32_t tacc, bool zero, float factor, int mode, uint16_t* out,
+                                           size_t pitch, int rows, int lane, bool any, F poison) {
   const uint64_t f2 = ptx::f2_pack(factor, factor);
   const uint32_t bias = mode == 1 ? 0x8000u : 0u;
+  const int hi = lane >> 2, lo = lane & 3;
 #pragma unroll
-  for (int ch = 0; ch < kCols / 32; ++ch) {
-    uint32_t r[32];
-    if (!zero) {
-      ptx::tmem_ld32(tacc + 32 * ch, r);
+  for (int part = 0; part < kCols / 64; ++part) {
+    uint32_t w[8][4];
+#pragma unroll
+    for (int ch = 0; ch < 2; ++ch) {
+      uint32_t r[32];
+      if (!zero) {
+        ptx::tmem_ld32(tacc + 64 * part + 32 * ch, r);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) r[i] = 0;
+      }
+      if (any) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (poison(64 * part + 32 * ch + i)) r[i] = 0x7FC00000u;
+      }
+      if (mode == 0) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float x0, x1;
+          ptx::f2_unpack(ptx::f2_mul(pair_of(r, 2 * i), f2), x0, x1);
+          w[4 * ch + i / 4][i % 4] = round_pair_bf16_rtne(x0, x1);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float x0, x1;
+          ptx::f2_unpack(ptx::f2_mul(pair_of(r, 2 * i), f2), x0, x1);
+          w[4 * ch + i / 4][i % 4] = round_pair_bf16(x0, x1, bias);
+        }
+      }
+    }
+#pragma unroll
+    for (int bit = 1; bit < 8; bit *= 2) {
+      const bool up = hi & bit;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        if (c & bit) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t x = __shfl_xor_sync(0xFFFFFFFFu, up ? w[c][e] : w[c | bit][e], 4 * bit);
+          if (up)
+            w[c][e] = x;
+          else
+            w[c | bit][e] = x;
+        }
+      }
+    }
+    uint16_t* dst = out + lo * pitch + 64 * part + 8 * hi;
+    if (rows >= 32) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k, dst += 4 * pitch)
+        *reinterpret_cast<uint4*>(dst) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) r[i] = 0;
-    }
-    if (any) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (poison(32 * ch + i)) r[i] = 0x7FC00000u;
-    }
-    uint32_t w[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float x0, x1;
-      ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), f2),
-                     x0, x1);
-      w[i] = mode == 0 ? round_pair_bf16_rtne(x0, x1) : round_pair_bf16(x0, x1, bias);
-    }
-    if (dst) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        reinterpret_cast<uint4*>(dst)[4 * ch + u] = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+      for (int k = 0; k < 8; ++k, dst += 4 * pitch)
+        if (4 * k + lo < rows) *reinterpret_cast<uint4*>(dst) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
     }
   }
 }
@@ -340,9 +402,6 @@ __device__ __forceinline__ void store_part(uint32_t tacc, bool zero, float* dst,
 // The softmax threads' turns, over 64 columns each. kMask is a template argument:
 // as a run-time test inside, its compares ran in every tile (half of the
 // instructions of the unmasked loop).
-__device__ __forceinline__ uint64_t pair_of(const uint32_t (&r)[32], int x) {
-  return ptx::f2_pack(__uint_as_float(r[x]), __uint_as_float(r[x + 1]));
-}
 
 // dkv: P from S (a lane's key against 64 queries, whose -lse log2(e) are in shared
 // memory); kept in pr, and written over S as bf16.
@@ -806,13 +865,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) ptx::mbar_arrive(bar(kDkvDsFull));
       }
       if (!ok) break;
-      // ---- epilogue: warpgroup 0 stores dK, warpgroup 1 dV. (The item again, from an
-      // opaque copy of its number: nothing of it is kept across the loop. And the next one,
+      // ---- epilogue: warpgroup 0 stores dK, warpgroup 1 dV. (The next item is taken up
       // before the wait.)
       const bool zero = n == 0;
-      int again = item;
-      asm volatile("" : "+r"(again));
-      const DkvItem v = dkv_item<kCausal, kVarlen>(p, again);
+      const DkvItem v = w;
       item = items.next_warp(it, lane);
       if (item >= 0) w = dkv_item<kCausal, kVarlen>(p, item);
       if (!zero && !(ok = warp_wait(bar(kDkvAcc), used & 1, abort_flag, p.timeout_ns))) break;
@@ -825,10 +881,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int seen = kCausal ? max(0, v.k0 + row - v.off) : 0;
         auto is_nan = [&](int col) -> bool { return any && g == 1 && poison[col] >= seen; };
         if (p.n_splits == 1) {
-          const bool in = v.k0 + row < s.sk && dbg_ok(s.k_base + v.k0 + row < p.Sk);
+          const int first = v.k0 + 32 * wq;  // of the warp's rows
+          const int rows = dbg_ok(s.k_base + s.sk <= p.Sk) ? s.sk - first : 0;
           uint16_t* dst = (g == 0 ? p.dk : p.dv) +
-                          row_at(p.layout, s.batch, p.Hkv, p.Sk, s.head, s.k_base + v.k0 + (in ? row : 0));
-          store_row<kD>(tacc, zero, g == 0 ? p.scale : 1.f, p.mode, in ? dst : nullptr, any && g == 1, is_nan);
+                          row_at(p.layout, s.batch, p.Hkv, p.Sk, s.head, s.k_base + (rows > 0 ? first : 0));
+          store_rows<kD>(tacc, zero, g == 0 ? p.scale : 1.f, p.mode, dst,
+                         static_cast<size_t>(p.layout == 0 ? 1 : p.Hkv) * kD, rows, lane, any && g == 1, is_nan);
         } else {
           const size_t slots = static_cast<size_t>(p.k_slots) * (kVarlen ? p.Hkv : p.BH);
           const size_t slot = static_cast<size_t>(s.slot_k) + static_cast<size_t>(s.head) * p.k_slots + s.tile;
@@ -896,7 +954,7 @@ enum : int {
 constexpr int kDqOffQ = 0, kDqOffO = kTileBytes, kDqOffK = 2 * kTileBytes,
               kDqOffV = kDqOffK + kDqKStages * kTileBytes,
               kDqOffItems = kDqOffV + kDqVStages * kTileBytes, kDqOffPoison = kDqOffItems + 16 * kItemSlots,
-              kDqOffDots = kDqOffPoison + kPoisonBytes, kDqOffBar = kDqOffDots + kTile * 4,
+              kDqOffDots = kDqOffPoison + kPoisonBytes, kDqOffBar = kDqOffDots + 2 * kTile * 4,
               kDqOffSlot = kDqOffBar + kDqBars * 8, kDqSmem = kDqOffSlot + 8 + 1024;
 static_assert(kDqSmem <= 232448, "shared memory budget (dq)");
 
@@ -1221,14 +1279,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ptx::fence_proxy_async_smem();  // these reads, before the stage is refilled
         }
-        // The other half's dot product: warpgroup 1 hands its own over and takes the sum
-        // back, in the same word (both warpgroups, whatever their waits said).
         float* dots = reinterpret_cast<float*>(smem + kDqOffDots);
-        if (g == 1) dots[row] = dot;
-        ptx::named_barrier_sync(2, 256);
-        if (g == 0) dots[row] = dot = dot + dots[row];
-        ptx::named_barrier_sync(2, 256);
-        if (g == 1) dot = dots[row];
+        dots[g * kTile + row] = dot;
+        ptx::named_barrier_sync(2, 256);  // (both warpgroups, whatever their waits said)
+        dot = dots[row] + dots[kTile + row];
         if (!ok) break;
         if (threadIdx.x == 32 * kSoftmaxWarp0) {  // O and dO have been read
           ptx::mbar_arrive(bar(kDqKEmpty + os));
@@ -1274,13 +1328,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) ptx::mbar_arrive(bar(kDqDsFull));
       }
       if (!ok) break;
-      // ---- epilogue: each warpgroup stores 64 columns of the rows. (The item again, from
-      // an opaque copy of its number: nothing of it is kept across the loop. And the next
-      // one, before the wait.)
+      // ---- epilogue: each warpgroup stores 64 columns of the rows. (The next item is taken
+      // up before the wait.)
       const bool zero = n == 0;
-      int again = item;
-      asm volatile("" : "+r"(again));
-      const DqItem v = dq_item<kCausal, kVarlen>(p, again);
+      const DqItem v = w;
       item = items.next_warp(it, lane);
       if (item >= 0) {
         w = dq_item<kCausal, kVarlen>(p, item);
@@ -1295,10 +1346,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int sees = kCausal ? min(v.q0 + row + v.off + 1, s.sk) : s.sk;
         auto is_nan = [&](int col) -> bool { return any && poison[64 * g + col] < sees; };
         if (p.n_splits == 1) {
-          const bool in = v.q0 + row < s.sq && dbg_ok(s.q_base + v.q0 + row < p.Sq);
+          const int first = v.q0 + 32 * wq;  // of the warp's rows
+          const int rows = dbg_ok(s.q_base + s.sq <= p.Sq) ? s.sq - first : 0;
           uint16_t* dst =
-              p.dq + row_at(p.layout, s.batch, p.Hq, p.Sq, s.head, s.q_base + v.q0 + (in ? row : 0)) + 64 * g;
-          store_row<64>(tacc, zero, p.scale, p.mode, in ? dst : nullptr, any, is_nan);
+              p.dq + row_at(p.layout, s.batch, p.Hq, p.Sq, s.head, s.q_base + (rows > 0 ? first : 0)) + 64 * g;
+          store_rows<64>(tacc, zero, p.scale, p.mode, dst, static_cast<size_t>(p.layout == 0 ? 1 : p.Hq) * kD, rows,
+                         lane, any, is_nan);
         } else {
           const size_t slots = static_cast<size_t>(p.q_slots) * (kVarlen ? p.Hq : p.BH);
           const size_t slot = static_cast<size_t>(s.slot_q) + static_cast<size_t>(s.head) * p.q_slots + s.tile;
