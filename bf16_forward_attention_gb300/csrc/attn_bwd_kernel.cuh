@@ -85,7 +85,7 @@ struct BwdParams {
   int q_slots, k_slots;    // tile slots per head (see tile_slot)
   const float* lse;
   float* stats;            // [head][slot][2][128]: written by dq, read by dkv
-  float* part;             // n_splits > 1: [split][result][head * slots][128][128] fp32
+  float* part;             // n_splits > 1: [split][result][head * slots] tiles of fp32 terms
   uint16_t *dq, *dk, *dv;  // results
 };
 
@@ -376,9 +376,11 @@ __device__ __forceinline__ void store_rows(uint32_t tacc, bool zero, float facto
   }
 }
 
-// The same row as fp32 into the split workspace (one of n_splits terms of a sum).
+// kCols columns of a row as fp32 into the split workspace (one of n_splits terms of a sum).
+// A tile's terms lie by chunks of four columns, [chunk][row][4], so that a warp's store is 512
+// consecutive bytes. `part`: the tile's terms, c0: the first column.
 template <int kCols, typename F>
-__device__ __forceinline__ void store_part(uint32_t tacc, bool zero, float* dst, F poison) {
+__device__ __forceinline__ void store_part(uint32_t tacc, bool zero, float* part, int row, int c0, F poison) {
   const float nan = __int_as_float(0x7FC00000);
 #pragma unroll 1
   for (int ch = 0; ch < kCols / 16; ++ch) {
@@ -394,7 +396,7 @@ __device__ __forceinline__ void store_part(uint32_t tacc, bool zero, float* dst,
       float x[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[e] = poison(16 * ch + i + e) ? nan : __uint_as_float(r[i + e]);
-      *reinterpret_cast<float4*>(dst + 16 * ch + i) = make_float4(x[0], x[1], x[2], x[3]);
+      reinterpret_cast<float4*>(part)[(c0 + 16 * ch + i) / 4 * kTile + row] = make_float4(x[0], x[1], x[2], x[3]);
     }
   }
 }
@@ -890,8 +892,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           const size_t slots = static_cast<size_t>(p.k_slots) * (kVarlen ? p.Hkv : p.BH);
           const size_t slot = static_cast<size_t>(s.slot_k) + static_cast<size_t>(s.head) * p.k_slots + s.tile;
-          float* dst = p.part + (((static_cast<size_t>(s.split) * 2 + g) * slots + slot) * kTile + row) * kD;
-          store_part<kD>(tacc, zero, dst, is_nan);
+          float* dst = p.part + ((static_cast<size_t>(s.split) * 2 + g) * slots + slot) * kTile * kD;
+          store_part<kD>(tacc, zero, dst, row, 0, is_nan);
         }
         if (any) clear_poison(poison, -1);
       }
@@ -1355,8 +1357,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           const size_t slots = static_cast<size_t>(p.q_slots) * (kVarlen ? p.Hq : p.BH);
           const size_t slot = static_cast<size_t>(s.slot_q) + static_cast<size_t>(s.head) * p.q_slots + s.tile;
-          float* dst = p.part + ((static_cast<size_t>(s.split) * slots + slot) * kTile + row) * kD + 64 * g;
-          store_part<64>(tacc, zero, dst, is_nan);
+          float* dst = p.part + (static_cast<size_t>(s.split) * slots + slot) * kTile * kD;
+          store_part<64>(tacc, zero, dst, row, 64 * g, is_nan);
         }
         if (any) clear_poison(poison, kNever);
       }
@@ -1383,7 +1385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------- join of the splits
 //
 // A result owned by n_splits CTAs: their fp32 terms are added in split order, scaled
-// and rounded. One block per 16 rows of a tile, 16 threads per row (32 bytes each).
+// and rounded. One block per 16 rows of a tile, eight columns a thread.
 struct JoinParams {
   const float* part;
   uint16_t* out[2];  // dq, or dk and dv
@@ -1398,7 +1400,7 @@ constexpr int kJoinRows = 16;
 template <bool kVarlen>
 __global__ void __launch_bounds__(16 * kJoinRows) attn_bwd_join(const JoinParams p) {
   constexpr int kPer = kTile / kJoinRows;  // blocks per tile
-  const int r = (blockIdx.x % kPer) * kJoinRows + (threadIdx.x >> 4);
+  const int r = (blockIdx.x % kPer) * kJoinRows + (threadIdx.x % kJoinRows);
   int item = blockIdx.x / kPer;
   const int tile = item % p.n_tiles;
   item /= p.n_tiles;
@@ -1421,13 +1423,13 @@ __global__ void __launch_bounds__(16 * kJoinRows) attn_bwd_join(const JoinParams
   const int row = tile * kTile + r;
   if (row >= len) return;
   const size_t slots = static_cast<size_t>(p.slots) * p.H * (kVarlen ? 1 : p.B);
-  const int c0 = (threadIdx.x & 15) * 8;
+  const int c0 = threadIdx.x / kJoinRows * 8;
   float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
   for (int k = 0; k < p.n_splits; ++k) {
     const float4* src = reinterpret_cast<const float4*>(
-        p.part + (((static_cast<size_t>(k) * p.results + result) * slots + slot) * kTile + r) * kD + c0);
-    const float4 u = src[0], v = src[1];
+        p.part + ((static_cast<size_t>(k) * p.results + result) * slots + slot) * kTile * kD);
+    const float4 u = src[c0 / 4 * kTile + r], v = src[(c0 / 4 + 1) * kTile + r];
     x[0] += u.x; x[1] += u.y; x[2] += u.z; x[3] += u.w;
     x[4] += v.x; x[5] += v.y; x[6] += v.z; x[7] += v.w;
   }

@@ -103,8 +103,8 @@ bool make_plan(Plan* pl, int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int64_t
     // The prefix product runs beside the own keys' kernel, on one SM per CTA. The split
     // count with the least estimated time: the product takes 1.9 us per key tile of 128
     // keys and 256 rows, and 8 us a CTA to start and end; meanwhile the own keys (half
-    // of each cache, as lengths are on the device) are read by the other SMs, of which 70
-    // reach the full 6.5 TB/s; what is left is read afterwards. A split more costs the
+    // of each cache, as lengths are on the device) are read by the other SMs, of which 105
+    // reach the full 6.5 TB/s (an SM takes 62 GB/s from L2); what is left is read afterwards. A split more costs the
     // join 1040 bytes a row.
     const int64_t tiles = (Sp + attn::kBN - 1) / attn::kBN;
     const int64_t cta = Hkv * (pl->rows_pad / 256);
@@ -113,7 +113,7 @@ bool make_plan(Plan* pl, int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int64_t
     for (int n = 1; n <= 64 && n <= tiles; ++n) {
       const int64_t waves = (cta * n + sms - 1) / sms;
       const double us = static_cast<double>(waves) * (1.9 * ((tiles + n - 1) / n) + 8);
-      const double rate = cta * n >= sms ? 0.0 : (sms - cta * n >= 70 ? 1.0 : (sms - cta * n) / 70.0);
+      const double rate = cta * n >= sms ? 0.0 : (sms - cta * n >= 105 ? 1.0 : (sms - cta * n) / 105.0);
       const double left = own_us > us * rate ? own_us - us * rate : 0.0;
       const double cost = us + left + static_cast<double>(cta) * n * 256 * 1040 * 2 / 6.5e6;
       if (cost < least) {
