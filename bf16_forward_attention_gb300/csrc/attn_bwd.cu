@@ -83,17 +83,6 @@ int choose_splits(int64_t items, int64_t tiles, int64_t sms, int part) {
   return best;
 }
 
-// Causal schedule: heads whose tiles are launched longest first together, in groups of
-// one size whose streamed tensors (`bytes` a head) take at most 80 MiB of the 126 MiB
-// L2. A group's last tiles are short, so it fills the SMs that the next one's first
-// tiles leave; a small last group would start its longest tiles at the very end.
-int heads_together(int64_t heads, int64_t bytes) {
-  int64_t most = (int64_t(80) << 20) / (bytes > 0 ? bytes : 1);
-  if (most < 1) most = 1;
-  const int64_t groups = (heads + most - 1) / most;
-  return static_cast<int>((heads + groups - 1) / groups);
-}
-
 // What an item's number means (BH, n_tiles and n_splits are set).
 void place(bwd::BwdParams* p, int heads, int64_t owners) {
   p->n_groups = (p->BH + heads - 1) / heads;

@@ -310,7 +310,7 @@ int attn_fwd_impl(const void* q, const void* k, const void* v, void* out, int la
   p.cu_k = nullptr;
   p.max_sq = p.Sq;
   p.out = static_cast<uint16_t*>(out);
-  p.head_group = head_group_of(B * H, Sk);
+  p.head_group = heads_together(B * H, 512 * Sk * Hkv / H);
   p.dbg_poison = dbg_poison;
   p.n_items = static_cast<int>(B * H * n_qpairs * n_splits);
   p.item_base = 0;
@@ -509,7 +509,7 @@ int attn_fwd_varlen_impl(const void* q, const void* k, const void* v, void* out,
   p.cu_k = cu_seqlens_k;
   p.max_sq = static_cast<int>(max_seqlen_q);
   p.out = static_cast<uint16_t*>(out);
-  p.head_group = p.causal ? head_group_of(B * Hq, total_k / B) : 1;
+  p.head_group = p.causal ? heads_together(B * Hq, 512 * (total_k / B) * Hkv / Hq) : 1;
   p.dbg_poison = 0;
   p.n_items = static_cast<int>(B * Hq * n_qpairs);
   p.item_base = 0;

@@ -61,14 +61,15 @@ inline bool overlaps(const void* a, uint64_t na, const void* b, uint64_t nb) {
   return a0 < b0 + nb && b0 < a0 + na;
 }
 
-// Causal schedule: (batch, head) items per longest-first group, so that the K/V
-// of one group (512 bytes per key and head) take at most 48 MiB of the 126 MiB L2.
-inline int head_group_of(int64_t BH, int64_t keys_per_head) {
-  const int64_t per = 512 * (keys_per_head > 0 ? keys_per_head : 1);
-  int64_t g = (int64_t(48) << 20) / per;
-  if (g < 1) g = 1;
-  if (g > BH) g = BH;
-  return static_cast<int>(g);
+// Causal schedule: heads whose tiles are launched longest first together, in groups of
+// one size whose streamed tensors (`bytes` a head) take at most 80 MiB of the 126 MiB
+// L2. A group's last tiles are short, so it fills the SMs that the next one's first
+// tiles leave; a small last group would start its longest tiles at the very end.
+inline int heads_together(int64_t heads, int64_t bytes) {
+  int64_t most = (int64_t(80) << 20) / (bytes > 0 ? bytes : 1);
+  if (most < 1) most = 1;
+  const int64_t groups = (heads + most - 1) / most;
+  return static_cast<int>((heads + groups - 1) / groups);
 }
 
 // Adds a translation unit's device status word of the current device to *s and
