@@ -1734,14 +1734,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             inv2 = ptx::f2_pack(1.0f, 1.0f);
           }
         }
+        const uint32_t bias = mode == 1 ? 0x8000u : 0u;
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch) {
           uint32_t w[16];
+          if (mode == 0) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float o0, o1;
-            ptx::f2_unpack(ptx::f2_mul(acc[16 * ch + i], inv2), o0, o1);
-            w[i] = round_bf16_bits(o0, mode) | (round_bf16_bits(o1, mode) << 16);
+            for (int i = 0; i < 16; ++i) {
+              float o0, o1;
+              ptx::f2_unpack(ptx::f2_mul(acc[16 * ch + i], inv2), o0, o1);
+              w[i] = round_pair_bf16_rtne(o0, o1);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float o0, o1;
+              ptx::f2_unpack(ptx::f2_mul(acc[16 * ch + i], inv2), o0, o1);
+              w[i] = round_pair_bf16(o0, o1, bias);
+            }
           }
           const uint32_t half_base = stage_base + (ch >> 1) * kHalfBytes + row * 128;
 #pragma unroll
@@ -1762,7 +1772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               ptx::tma_store_4d_hint(&tm_o, stage_base + hf * kHalfBytes + wq * 32 * 128, 64 * hf, c1,
                                      c2, wk.batch, ptx::l2_policy_evict_first());
             ptx::bulk_commit_group();
-            ptx::bulk_wait_group_0();
+            ptx::bulk_wait_group_read_0();  // (the writes end with the grid)
           }
         } else if (lane < wk.sq - q_row0 && dbg_ok(wk.q_base + q_row0 + lane < p.Sq)) {
           // The sequence ends inside this warp's rows: a TMA box would run into the
