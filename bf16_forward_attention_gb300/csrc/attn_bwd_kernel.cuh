@@ -497,7 +497,11 @@ __device__ __forceinline__ void dq_ds(uint32_t tP, uint32_t tS, uint64_t nd2, in
 // take turns with the tensor pipe: while dV_i and S_{i+1} run, the threads form
 // dS_i from dP_i; while dK_i and dP_{i+1} run, they form P_{i+1} from S_{i+1}.
 // Each turn has 1024 tensor cycles to cover 64 exponentials per thread, or 64
-// subtract-multiplies.
+// subtract-multiplies. P is handed over in two halves, so that dV starts on the first.
+// Bound by the tensor cores: of four products' 2048 cycles it takes 2,320 a tile pair (8192
+// x 8192, 32 heads: 1.2 ms); there the power cap sets the clock, and without the
+// exponentials, the statistics or the loads it takes as long. 64-query tiles would let S
+// and dP have two buffers, but an N = 64 product runs at two thirds of the rate.
 // Shared memory is full as well: K, V, three stages of Q and two of dO. Q_i is read last
 // (dK_i) shortly before S_{i+2} wants Q_{i+2}: with two stages its refill had 1024 cycles, and
 // takes some 1600 when every SM streams at L2's limit; dO has slack.
@@ -645,7 +649,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mbar_arrive_expect_tx(bar(kDkvKV), 2 * kTileBytes);
           load_tile(sbase + kDkvOffK, &tm_k, bar(kDkvKV), p.layout, s.k_base + w.k0, s.head, s.batch, pol_once);
           load_tile(sbase + kDkvOffV, &tm_v, bar(kDkvKV), p.layout, s.k_base + w.k0, s.head, s.batch, pol_once);
-          if (used == 0) ptx::grid_dependency_wait();  // the row statistics
+          if (used == 0) {  // the row statistics
+            ptx::grid_dependency_wait();
+            ptx::fence_proxy_async_global();
+          }
           ++used;
           QueryTiles qt(w);
           int h = s.head * p.group + w.t0 / w.per;
@@ -923,7 +930,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // MN-major from the tile that S used. Tensor memory: S/dS two buffers [0,256), dP
 // [256,384), dQ [384,512). With two S buffers the tensor pipe forms S_{j+1} and
 // dP_{j+1} around dQ_j, and a turn of the softmax (exponentials of S_{j+1}, then
-// dS once dP_{j+1} is there) has 1536 tensor cycles.
+// dS once dP_{j+1} is there) has 1536 tensor cycles. Bound by the tensor cores: 1,840 cycles a
+// tile pair (8192 x 8192, 32 heads: 0.87 ms); the streamed 64 KiB a step are near what L2
+// gives every SM at once (34 bytes a clock), yet sharing them by TMA multicast between
+// two CTAs of a cluster was slower (2.39 against 2.28 ms for the whole pass: both wait for
+// the slower one at every tile).
 //
 // It also leaves the row statistics that dkv reads: per query row -lse log2(e) and -D,
 // D = sum_c dO_ic O_ic, formed from the dO tile it has and the O tile, which passes

@@ -952,7 +952,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           int c1, c2;
           // The split form may be launched as a programmatic dependent of the kernel that
           // lays out its queries (no effect otherwise).
-          if constexpr (kPartial) ptx::grid_dependency_wait();
+          if constexpr (kPartial) {
+            ptx::grid_dependency_wait();
+            ptx::fence_proxy_async_global();
+          }
           dbg_ok(q_base + 2 * pair * kBM < p.Sq);  // the first query tile starts inside
           ptx::mbar_arrive_expect_tx(bar(kBarQ), kQTiles * kTileBytes);
           for (int t = 0; t < kQTiles; ++t) {
