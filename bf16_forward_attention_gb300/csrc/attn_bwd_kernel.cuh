@@ -27,9 +27,9 @@
 // cost 3 more products for less than a factor of 2 in the final error.
 //
 // Both kernels: 384 threads. Warp 0: TMA producer. Warp 1: TMEM allocation and
-// the tcgen05.mma issue (one elected lane, in warp-uniform code). Warps 2-3: check of the tiles where some pairs
-// are hidden (see check_rows / check_keys). Warps 4-7 and 8-11: softmax, each
-// thread one TMEM lane (a key in dkv, a query in dq) and one 64-column half.
+// the tcgen05.mma issue (one elected lane, in warp-uniform code). Warps 2-3: check of the
+// tiles where some pairs are hidden. Warps 4-7 and 8-11: softmax, each thread one TMEM
+// lane (a key in dkv, a query in dq) and one 64-column half.
 // A CTA works on one item (an owned tile, or a part of its streamed range) after another:
 // it takes over CTAs of its grid that have not been launched yet (cluster launch
 // control), in launch order, so the schedule is the hardware's dynamic one, longest
@@ -191,6 +191,12 @@ struct Items {
 // Readers of an answer: producer, MMA warp, softmax warps, and the check's.
 __host__ __device__ constexpr int item_readers(bool check) { return 10 + (check ? 2 : 0); }
 
+// The next item for warps 2 and 3, which meet at named barriers: -1 for both if it is for one.
+__device__ __forceinline__ int next_together(const Items& items, int it, int lane) {
+  const int item = items.next_warp(it, lane);
+  return ptx::named_barrier_or(1, 64, item < 0) ? -1 : item;
+}
+
 // Part `split` of n streamed tiles: [first, first + count).
 __device__ __forceinline__ void part_of(int n, int splits, int split, int& first, int& count) {
   const int base = n / splits, rem = n % splits;
@@ -271,13 +277,27 @@ __device__ __forceinline__ void clean_row(uint32_t tile, int r, F with_col) {
 // last (or first) row that has one, and whether there is any.
 constexpr int kPoisonWords = kD + 4, kPoisonBytes = kPoisonWords * 4;
 
-// By the 256 softmax threads, which all found the record set: once every one has read it.
-__device__ __forceinline__ void clear_poison(int* rec, int none) {
-  ptx::named_barrier_sync(3, 256);
+// A meeting of the eight softmax warps, on an mbarrier of eight arrivals: a named barrier would
+// hold the others for good when one has left the item's loop after a wait that ran out.
+struct Meeting {
+  uint32_t bar;
+  volatile int* abort_flag;
+  unsigned long long timeout_ns;
+  int met;
+  __device__ __forceinline__ bool meet(int lane) {
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(bar);
+    return warp_wait(bar, met++ & 1, abort_flag, timeout_ns);
+  }
+};
+
+// By the softmax warps, which all found the record set: once every one has read it.
+__device__ __forceinline__ bool clear_poison(int* rec, int none, Meeting& all, int lane) {
+  if (!all.meet(lane)) return false;
   const int t = static_cast<int>(threadIdx.x) - 32 * kSoftmaxWarp0;
   if (t < kD) rec[t] = none;
   if (t == kD) rec[kD] = 0;
-  ptx::named_barrier_sync(3, 256);
+  return all.meet(lane);
 }
 
 // TMA load of one 128 x 128 tile (two 64-column boxes).
@@ -523,6 +543,7 @@ enum : int {
   kDkvLanded,
   kDkvChecked,
   kDkvDrain,
+  kDkvMeet,     // the softmax warps among themselves
   kDkvItemFull,
   kDkvItemEmpty = kDkvItemFull + kItemSlots,
   kDkvBars = kDkvItemEmpty + kItemSlots
@@ -604,9 +625,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kDkvBars; ++i)
-      ptx::mbar_init(bar(i), (i == kDkvPHalf || i == kDkvPFull || i == kDkvDsFull || i == kDkvAccFree) ? 8
-                             : i >= kDkvItemEmpty                                    ? item_readers(kCheck)
-                                                                                     : 1);
+      ptx::mbar_init(bar(i), (i == kDkvPHalf || i == kDkvPFull || i == kDkvDsFull || i == kDkvAccFree || i == kDkvMeet)
+                                 ? 8
+                             : i >= kDkvItemEmpty ? item_readers(kCheck)
+                                                  : 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
     ptx::fence_proxy_async_smem();
@@ -820,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tile += w.n;
         if (w.n > 0) ++used;
-        if (ok) item = items.next_warp(it, lane);
+        if (ok) item = next_together(items, it, lane);
       }
     }
   } else {
@@ -831,6 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tSh = tS + lane_base + 64 * g, tPh = tP + lane_base + 64 * g;
     const uint64_t c2 = ptx::f2_pack(p.c, p.c);
+    Meeting all{bar(kDkvMeet), abort_flag, p.timeout_ns, 0};
     int used = 0, tile = 0;
     bool ok = true;
     int item = static_cast<int>(blockIdx.x);
@@ -902,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float* dst = p.part + ((static_cast<size_t>(s.split) * 2 + g) * slots + slot) * kTile * kD;
           store_part<kD>(tacc, zero, dst, row, 0, is_nan);
         }
-        if (any) clear_poison(poison, -1);
+        if (any && !(ok = clear_poison(poison, -1, all, lane))) break;
       }
       if (!zero) {
         ptx::tc_fence_before();
@@ -960,6 +983,7 @@ enum : int {
   kDqLanded,
   kDqChecked = kDqLanded + kDqChecks,
   kDqDrain = kDqChecked + kDqChecks,
+  kDqMeet,      // the softmax warps among themselves
   kDqItemFull,
   kDqItemEmpty = kDqItemFull + kItemSlots,
   kDqBars = kDqItemEmpty + kItemSlots
@@ -1025,10 +1049,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kDqBars; ++i)
-      ptx::mbar_init(bar(i), (i == kDqDsFull || i == kDqAccFree) ? 8
-                             : i >= kDqItemEmpty                 ? item_readers(kCheck)
-                             : i == kDqQFree                     ? 2
-                                                                 : 1);
+      ptx::mbar_init(bar(i), (i == kDqDsFull || i == kDqAccFree || i == kDqMeet) ? 8
+                             : i >= kDqItemEmpty                                 ? item_readers(kCheck)
+                             : i == kDqQFree                                     ? 2
+                                                                                 : 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
     ptx::fence_proxy_async_smem();
@@ -1243,7 +1267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           k_base += w.n + 1;
           ++used;
         }
-        if (ok) item = items.next_warp(it, lane);
+        if (ok) item = next_together(items, it, lane);
       }
     }
   } else {
@@ -1254,6 +1278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tPh = tP + lane_base + 64 * g;
     const uint64_t c2 = ptx::f2_pack(p.c, p.c);
+    Meeting all{bar(kDqMeet), abort_flag, p.timeout_ns, 0};
     int used = 0, tile = 0, k_base = 0;
     bool ok = true;
     // The row's log-sum-exp is read when the item is known, long before it is used.
@@ -1278,25 +1303,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int fo = k_base, os = fo % kDqKStages;
         ok = warp_wait(bar(kDqQ), used & 1, abort_flag, p.timeout_ns) &&
              warp_wait(bar(kDqKFull + os), (fo / kDqKStages) & 1, abort_flag, p.timeout_ns);
-        if (ok) {
+        if (!ok) break;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const uint4 x = ptx::ld_shared_v4(sbase + kDqOffO + chunk_at(row, 8 * g + c));
-            const uint4 y = ptx::ld_shared_v4(sbase + kDqOffK + os * kTileBytes + chunk_at(row, 8 * g + c));
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+        for (int c = 0; c < 8; ++c) {
+          const uint4 x = ptx::ld_shared_v4(sbase + kDqOffO + chunk_at(row, 8 * g + c));
+          const uint4 y = ptx::ld_shared_v4(sbase + kDqOffK + os * kTileBytes + chunk_at(row, 8 * g + c));
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              dot = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), dot);
-              dot = fmaf(__uint_as_float(xs[e] & 0xFFFF0000u), __uint_as_float(ys[e] & 0xFFFF0000u), dot);
-            }
+          for (int e = 0; e < 4; ++e) {
+            dot = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), dot);
+            dot = fmaf(__uint_as_float(xs[e] & 0xFFFF0000u), __uint_as_float(ys[e] & 0xFFFF0000u), dot);
           }
-          ptx::fence_proxy_async_smem();  // these reads, before the stage is refilled
         }
+        ptx::fence_proxy_async_smem();  // these reads, before the stage is refilled
         float* dots = reinterpret_cast<float*>(smem + kDqOffDots);
         dots[g * kTile + row] = dot;
-        ptx::named_barrier_sync(2, 256);  // (both warpgroups, whatever their waits said)
+        if (!(ok = all.meet(lane))) break;
         dot = dots[row] + dots[kTile + row];
-        if (!ok) break;
         if (threadIdx.x == 32 * kSoftmaxWarp0) {  // O and dO have been read
           ptx::mbar_arrive(bar(kDqKEmpty + os));
           ptx::mbar_arrive(bar(kDqQFree));
@@ -1371,7 +1394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float* dst = p.part + (static_cast<size_t>(s.split) * slots + slot) * kTile * kD;
           store_part<64>(tacc, zero, dst, row, 64 * g, is_nan);
         }
-        if (any) clear_poison(poison, kNever);
+        if (any && !(ok = clear_poison(poison, kNever, all, lane))) break;
       }
       if (!zero) {
         ptx::tc_fence_before();

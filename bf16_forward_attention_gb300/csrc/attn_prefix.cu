@@ -104,8 +104,8 @@ bool make_plan(Plan* pl, int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int64_t
     // count with the least estimated time: the product takes 1.9 us per key tile of 128
     // keys and 256 rows, and 8 us a CTA to start and end; meanwhile the own keys (half
     // of each cache, as lengths are on the device) are read by the other SMs, of which 105
-    // reach the full 6.5 TB/s (an SM takes 62 GB/s from L2); what is left is read afterwards. A split more costs the
-    // join 1040 bytes a row.
+    // reach the full 6.5 TB/s (an SM takes 62 GB/s from L2); what is left is read
+    // afterwards. A split more costs the join 1040 bytes a row.
     const int64_t tiles = (Sp + attn::kBN - 1) / attn::kBN;
     const int64_t cta = Hkv * (pl->rows_pad / 256);
     const double own_us = static_cast<double>(B) * Hkv * cap * 256 / 6.5e6;

@@ -256,35 +256,14 @@ __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
-// D[tmem] (+)= A[smem desc] * B[smem desc]; bf16 x bf16 -> fp32.
-__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                      uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// D[tmem] (+)= A[tmem] * B[smem desc]; bf16 x bf16 -> fp32.
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                      uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// The same two MMAs, issued by a warp whose 32 lanes execute them together: one elected
-// lane (always the same one) issues. The descriptors are built inside the asm statement
-// from a 32-bit lower word plus an immediate offset (16-byte units) and the shared upper
-// word, so that between MMAs no 64-bit descriptor occupies registers. In warp-uniform code the compiler keeps descriptors
-// and addresses in uniform registers; issued from a lane-0 branch each operand is
-// first moved there, and back-to-back 128 x 128 x 16 MMAs take 89 cycles each
-// instead of the tensor pipe's 64.
+// D[tmem] (+)= A * B, A from shared memory (mma_ss_warp) or tensor memory (mma_ts_warp), B
+// from shared memory; bf16 x bf16 -> fp32. Executed by a warp whose 32 lanes are together: one
+// elected lane (always the same one) issues. The descriptors are built inside the asm
+// statement from a 32-bit lower word plus an immediate offset (16-byte units) and the shared
+// upper word, so that between MMAs no 64-bit descriptor occupies registers. In warp-uniform
+// code the compiler keeps descriptors and addresses in uniform registers; issued from a lane-0
+// branch each operand is first moved there, and back-to-back 128 x 128 x 16 MMAs take 89 cycles
+// each instead of the tensor pipe's 64.
 template <uint32_t kAOff, uint32_t kBOff>
 __device__ __forceinline__ void mma_ss_warp(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
                                             uint32_t idesc, uint32_t accumulate) {
@@ -318,13 +297,6 @@ __device__ __forceinline__ void mma_commit_warp(uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
-      : "memory");
-}
-
-// Arrive (once) on `bar` when every tcgen05 op issued so far by this thread is done.
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
       : "memory");
 }
 
