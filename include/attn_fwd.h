@@ -46,15 +46,16 @@ enum {
   ATTN_ERR_INVALID_ARG = -1, /* null pointer, a size < 1, non-finite scale     */
   ATTN_ERR_UNSUPPORTED = -2, /* d != 128, unknown layout or rounding mode      */
   ATTN_ERR_MISALIGNED = -3,  /* a pointer not 16-byte aligned                  */
-  ATTN_ERR_ALIASING = -4,    /* out overlaps q, k or v                         */
+  ATTN_ERR_ALIASING = -4,    /* an output overlaps an input or another output  */
   ATTN_ERR_NO_DEVICE = -5,   /* no current CUDA device                         */
   ATTN_ERR_ARCH = -6,        /* current device is not compute capability 10.3  */
   ATTN_ERR_LAUNCH = -7,      /* the CUDA launch (or tensor-map setup) failed   */
   ATTN_ERR_TIMEOUT = -8,     /* a bounded device-side wait expired             */
   ATTN_ERR_TOO_LARGE = -9,   /* a size beyond the tensor-map / grid limits     */
   ATTN_ERR_SCRATCH = -10,    /* attn_fwd_splitkv_noalloc: workspace > 32 MiB   */
-  ATTN_ERR_SEQLENS = -11,    /* attn_fwd_varlen: invalid offsets, found on the
-                                device and reported by attn_fwd_last_error     */
+  ATTN_ERR_SEQLENS = -11,    /* packed batches: invalid offsets; shared prefix:
+                                an invalid length. Found on the device and
+                                reported by attn_fwd_last_error                */
   ATTN_ERR_DEBUG_CHECK = -12 /* debug build: a bounds or protocol check failed,
                                 reported by attn_fwd_last_error                */
 };
