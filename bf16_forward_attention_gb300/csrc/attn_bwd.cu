@@ -1,8 +1,8 @@
 // attn_bwd.cu - host side of the backward pass declared in include/attn_fwd.h:
 // checks the call, lays out the workspace and launches, on the caller's stream, dQ
-// with the row statistics, then dK with dV (attn_bwd_kernel.cuh), each a programmatic
-// dependent of the one before; results that several CTAs share the
-// streamed axis of are joined by one more kernel each.
+// with the row statistics, then dK with dV (attn_bwd_kernel.cuh), then the join of the results
+// that several CTAs share the streamed axis of, where there are any; the second and
+// the third each a programmatic dependent of the one before.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -226,12 +226,6 @@ int bwd_impl(const void* dout, const void* q, const void* k, const void* v, cons
   const int64_t rows_per_head = varlen ? (Sq + B - 1) / B : Sq;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
 
-  bwd::JoinParams jp;
-  jp.layout = layout;
-  jp.mode = rounding_mode;
-  jp.B = static_cast<int>(B);
-  auto* join = varlen ? bwd::attn_bwd_join<true> : bwd::attn_bwd_join<false>;
-
   p.BH = static_cast<int>(B * Hq);
   p.n_tiles = static_cast<int>(pl.q_tiles);
   p.n_splits = pl.dq_splits;
@@ -242,23 +236,6 @@ int bwd_impl(const void* dout, const void* q, const void* k, const void* v, cons
   if (!launch(dq_fn, B * Hq * pl.q_tiles * pl.dq_splits, attn::kThreads, bwd::kDqSmem, cs, false, tq, tk, tv,
               tdo, tout, p))
     return ATTN_ERR_LAUNCH;
-  if (pl.dq_splits > 1) {
-    jp.part = dq_part;
-    jp.out[0] = jp.out[1] = p.dq;
-    jp.cu = cu_q;
-    jp.cu2 = cu_k;
-    jp.S = p.Sq;
-    jp.S2 = p.Sk;
-    jp.H = p.Hq;
-    jp.max_s = p.max_sq;
-    jp.max_s2 = p.max_sk;
-    jp.slots = p.q_slots;
-    jp.n_tiles = static_cast<int>(pl.q_tiles);
-    jp.n_splits = pl.dq_splits;
-    jp.results = 1;
-    jp.factor[0] = jp.factor[1] = scale;
-    if (!launch(join, B * Hq * pl.q_tiles * kJoinPer, 16 * bwd::kJoinRows, 0, cs, true, jp)) return ATTN_ERR_LAUNCH;
-  }
 
   p.BH = static_cast<int>(B * Hkv);
   p.n_tiles = static_cast<int>(pl.k_tiles);
@@ -270,24 +247,40 @@ int bwd_impl(const void* dout, const void* q, const void* k, const void* v, cons
   if (!launch(dkv_fn, B * Hkv * pl.k_tiles * pl.dkv_splits, attn::kThreads, bwd::kDkvSmem, cs, true, tq, tk, tv,
               tdo, p))
     return ATTN_ERR_LAUNCH;
-  if (pl.dkv_splits > 1) {
-    jp.part = dkv_part;
-    jp.cu = cu_k;
-    jp.cu2 = cu_q;
-    jp.S = p.Sk;
-    jp.S2 = p.Sq;
-    jp.H = p.Hkv;
-    jp.max_s = p.max_sk;
-    jp.max_s2 = p.max_sq;
-    jp.slots = p.k_slots;
-    jp.n_tiles = static_cast<int>(pl.k_tiles);
-    jp.n_splits = pl.dkv_splits;
-    jp.results = 2;
-    jp.out[0] = p.dk;
-    jp.out[1] = p.dv;
-    jp.factor[0] = scale;
-    jp.factor[1] = 1.f;
-    if (!launch(join, 2 * B * Hkv * pl.k_tiles * kJoinPer, 16 * bwd::kJoinRows, 0, cs, true, jp))
+  if (pl.dq_splits > 1 || pl.dkv_splits > 1) {
+    bwd::JoinParams jp;
+    jp.layout = layout;
+    jp.mode = rounding_mode;
+    jp.B = static_cast<int>(B);
+    jp.dq.part = dq_part;
+    jp.dq.out[0] = jp.dq.out[1] = p.dq;
+    jp.dq.factor[0] = jp.dq.factor[1] = scale;
+    jp.dq.results = 1;
+    jp.dq.cu = jp.dkv.cu2 = cu_q;
+    jp.dq.cu2 = jp.dkv.cu = cu_k;
+    jp.dq.S = jp.dkv.S2 = p.Sq;
+    jp.dq.S2 = jp.dkv.S = p.Sk;
+    jp.dq.max_s = jp.dkv.max_s2 = p.max_sq;
+    jp.dq.max_s2 = jp.dkv.max_s = p.max_sk;
+    jp.dq.H = p.Hq;
+    jp.dkv.H = p.Hkv;
+    jp.dq.slots = p.q_slots;
+    jp.dkv.slots = p.k_slots;
+    jp.dq.n_tiles = static_cast<int>(pl.q_tiles);
+    jp.dkv.n_tiles = static_cast<int>(pl.k_tiles);
+    jp.dq.n_splits = pl.dq_splits;
+    jp.dkv.n_splits = pl.dkv_splits;
+    jp.dkv.part = dkv_part;
+    jp.dkv.out[0] = p.dk;
+    jp.dkv.out[1] = p.dv;
+    jp.dkv.factor[0] = scale;
+    jp.dkv.factor[1] = 1.f;
+    jp.dkv.results = 2;
+    const int64_t dq_blocks = pl.dq_splits > 1 ? B * Hq * pl.q_tiles * kJoinPer : 0;
+    const int64_t dkv_blocks = pl.dkv_splits > 1 ? 2 * B * Hkv * pl.k_tiles * kJoinPer : 0;
+    jp.dq_blocks = static_cast<int>(dq_blocks);
+    if (!launch(varlen ? bwd::attn_bwd_join<true> : bwd::attn_bwd_join<false>, dq_blocks + dkv_blocks,
+                16 * bwd::kJoinRows, 0, cs, true, jp))
       return ATTN_ERR_LAUNCH;
   }
   return ATTN_OK;

@@ -648,6 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  ptx::launch_dependents();
   const uint32_t tS = tmem, tP = tmem + 128, tK = tmem + 256, tV = tmem + 384;
 
   // In every role: `used` counts the items with streamed tiles so far (the phases of the
@@ -671,13 +672,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mbar_arrive_expect_tx(bar(kDkvKV), 2 * kTileBytes);
           load_tile(sbase + kDkvOffK, &tm_k, bar(kDkvKV), p.layout, s.k_base + w.k0, s.head, s.batch, pol_once);
           load_tile(sbase + kDkvOffV, &tm_v, bar(kDkvKV), p.layout, s.k_base + w.k0, s.head, s.batch, pol_once);
-          if (used == 0) {  // the row statistics
-            ptx::grid_dependency_wait();
-            ptx::fence_proxy_async_global();
-          }
-          ++used;
           QueryTiles qt(w);
           int h = s.head * p.group + w.t0 / w.per;
+          auto load_stats = [&](int os, int head, int q0) {
+            const float* src = p.stats + (static_cast<size_t>(s.slot_q) + static_cast<size_t>(head) * p.q_slots +
+                                          q0 / kTile) * kStatFloats;
+            ptx::bulk_load(sbase + kDkvOffStats + os * kStatFloats * 4, src, kStatFloats * 4,
+                           bar(kDkvOFull + os));
+          };
+          // The row statistics are the only thing here that the kernel before this one writes:
+          // the CTA's first tiles load while it ends.
+          const int early = used == 0 ? min(w.n, kDkvOStages) : 0;
+          QueryTiles late = qt;
+          int late_h = h;
+          ++used;
           for (int i = 0; i < w.n; ++i) {
             const int qs = q_issued % kDkvQStages, os = o_issued % kDkvOStages;
             dbg_ok(s.q_base + qt.q0 < p.Sq && h < p.Hq);
@@ -694,11 +702,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_arrive_expect_tx(bar(kDkvOFull + os), kTileBytes + kStatFloats * 4);
             load_tile(sbase + kDkvOffO + os * kTileBytes, &tm_do, bar(kDkvOFull + os), p.layout,
                       s.q_base + qt.q0, h, s.batch, pol_reuse);
-            const float* src = p.stats + (static_cast<size_t>(s.slot_q) + static_cast<size_t>(h) * p.q_slots +
-                                          qt.q0 / kTile) * kStatFloats;
-            ptx::bulk_load(sbase + kDkvOffStats + os * kStatFloats * 4, src, kStatFloats * 4,
-                           bar(kDkvOFull + os));
+            if (i >= early) load_stats(os, h, qt.q0);
             ++o_issued;
+            if (i + 1 == early) {
+              ptx::grid_dependency_wait();
+              ptx::fence_proxy_async_global();
+              for (int e = 0; e < early; ++e) {
+                load_stats(e, late_h, late.q0);
+                if (late.q0 == late.last) ++late_h;
+                late.step();
+              }
+            }
             if (qt.q0 == qt.last) ++h;
             qt.step();
           }
@@ -1419,62 +1433,77 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------- join of the splits
 //
 // A result owned by n_splits CTAs: their fp32 terms are added in split order, scaled
-// and rounded. One block per 16 rows of a tile, eight columns a thread.
-struct JoinParams {
+// and rounded. One block per 16 rows of a tile, eight columns a thread. Both kernels' results
+// in one launch after both (a join of its own between them held up the second one).
+struct JoinPart {
   const float* part;
   uint16_t* out[2];  // dq, or dk and dv
   float factor[2];
   const int* cu;     // packed batch: the owned axis's offsets
   const int* cu2;    // and the other axis's (a sequence with bad offsets is left alone)
-  int S, S2, H, max_s, max_s2, slots, B, n_tiles, n_splits, results, layout, mode;
+  int S, S2, H, max_s, max_s2, slots, n_tiles, n_splits, results;
+};
+struct JoinParams {
+  JoinPart dq, dkv;
+  int dq_blocks;     // the grid's first blocks: dq
+  int B, layout, mode;
 };
 
 constexpr int kJoinRows = 16;
 
 template <bool kVarlen>
-__global__ void __launch_bounds__(16 * kJoinRows) attn_bwd_join(const JoinParams p) {
+__device__ __forceinline__ void join_rows(const JoinPart& j, int B, int layout, int mode, int block) {
   constexpr int kPer = kTile / kJoinRows;  // blocks per tile
-  const int r = (blockIdx.x % kPer) * kJoinRows + (threadIdx.x % kJoinRows);
-  int item = blockIdx.x / kPer;
-  const int tile = item % p.n_tiles;
-  item /= p.n_tiles;
-  const int h = item % p.H;
-  item /= p.H;
-  const int b = item % p.B, result = item / p.B;
+  const int r = (block % kPer) * kJoinRows + (threadIdx.x % kJoinRows);
+  int item = block / kPer;
+  const int tile = item % j.n_tiles;
+  item /= j.n_tiles;
+  const int h = item % j.H;
+  item /= j.H;
+  const int b = item % B, result = item / B;
   ptx::grid_dependency_wait();
-  int base = 0, len = p.S, batch = b;
-  size_t slot = (static_cast<size_t>(b) * p.H + h) * p.slots + tile;
+  int base = 0, len = j.S, batch = b;
+  size_t slot = (static_cast<size_t>(b) * j.H + h) * j.slots + tile;
   if (kVarlen) {
-    base = __ldg(p.cu + b);
-    len = __ldg(p.cu + b + 1) - base;
-    const int base2 = __ldg(p.cu2 + b), len2 = __ldg(p.cu2 + b + 1) - base2;
-    if (base < 0 || len < 0 || len > p.max_s || base + len > p.S || base2 < 0 || len2 < 0 ||
-        len2 > p.max_s2 || base2 + len2 > p.S2)
+    base = __ldg(j.cu + b);
+    len = __ldg(j.cu + b + 1) - base;
+    const int base2 = __ldg(j.cu2 + b), len2 = __ldg(j.cu2 + b + 1) - base2;
+    if (base < 0 || len < 0 || len > j.max_s || base + len > j.S || base2 < 0 || len2 < 0 ||
+        len2 > j.max_s2 || base2 + len2 > j.S2)
       return;
     batch = 0;
-    slot = static_cast<size_t>(h) * p.slots + tile_slot<true>(base, b) + tile;
+    slot = static_cast<size_t>(h) * j.slots + tile_slot<true>(base, b) + tile;
   }
   const int row = tile * kTile + r;
   if (row >= len) return;
-  const size_t slots = static_cast<size_t>(p.slots) * p.H * (kVarlen ? 1 : p.B);
+  const size_t slots = static_cast<size_t>(j.slots) * j.H * (kVarlen ? 1 : B);
   const int c0 = threadIdx.x / kJoinRows * 8;
   float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-  for (int k = 0; k < p.n_splits; ++k) {
+  for (int k = 0; k < j.n_splits; ++k) {
     const float4* src = reinterpret_cast<const float4*>(
-        p.part + ((static_cast<size_t>(k) * p.results + result) * slots + slot) * kTile * kD);
+        j.part + ((static_cast<size_t>(k) * j.results + result) * slots + slot) * kTile * kD);
     const float4 u = src[c0 / 4 * kTile + r], v = src[(c0 / 4 + 1) * kTile + r];
     x[0] += u.x; x[1] += u.y; x[2] += u.z; x[3] += u.w;
     x[4] += v.x; x[5] += v.y; x[6] += v.z; x[7] += v.w;
   }
-  const float f = result ? p.factor[1] : p.factor[0];
-  uint16_t* out = result ? p.out[1] : p.out[0];
+  const float f = result ? j.factor[1] : j.factor[0];
+  uint16_t* out = result ? j.out[1] : j.out[0];
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    w[i] = round_bf16_bits(x[2 * i] * f, p.mode) | (round_bf16_bits(x[2 * i + 1] * f, p.mode) << 16);
-  *reinterpret_cast<uint4*>(out + row_at(p.layout, batch, p.H, p.S, h, base + row) + c0) =
+    w[i] = round_bf16_bits(x[2 * i] * f, mode) | (round_bf16_bits(x[2 * i + 1] * f, mode) << 16);
+  *reinterpret_cast<uint4*>(out + row_at(layout, batch, j.H, j.S, h, base + row) + c0) =
       make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <bool kVarlen>
+__global__ void __launch_bounds__(16 * kJoinRows) attn_bwd_join(const JoinParams p) {
+  const int block = static_cast<int>(blockIdx.x);
+  if (block < p.dq_blocks)
+    join_rows<kVarlen>(p.dq, p.B, p.layout, p.mode, block);
+  else
+    join_rows<kVarlen>(p.dkv, p.B, p.layout, p.mode, block - p.dq_blocks);
 }
 
 }  // namespace bwd
