@@ -750,16 +750,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const DkvItem w = dkv_item<kCausal, kVarlen>(p, item);
       if (w.n > 0) {
         QueryTiles qt(w);  // of the next S
-        // S_i: Q_i has landed; a masked tile's rows have been checked first (both of
-        // its tiles, so dO_i has landed too).
+        bool masked_s = false, masked = false;  // the tile of the last S, and of the last dP
         auto do_s = [&](int t) -> bool {
           if (!wait(kDkvQFull + t % kDkvQStages, t / kDkvQStages)) return false;
-          if (kCheck && dkv_masked<kCausal>(qt.q0, w.s.sq, w.off, w.k0)) {
-            if (!wait(kDkvOFull + t % kDkvOStages, t / kDkvOStages)) return false;
-            if (lane == 0) ptx::mbar_arrive(bar(kDkvLanded));
-            if (!wait(kDkvChecked, checks)) return false;
-            ++checks;
-          }
+          masked_s = kCheck && dkv_masked<kCausal>(qt.q0, w.s.sq, w.off, w.k0);
           qt.step();
           issue_s(tS, k_desc, desc_lo(q_tile(t), 16));
           ptx::mma_commit_warp(bar(kDkvSFull));
@@ -767,6 +761,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto do_dp = [&](int t) -> bool {
           if (!wait(kDkvOFull + t % kDkvOStages, t / kDkvOStages)) return false;
+          masked = masked_s;
+          if (masked && lane == 0) ptx::mbar_arrive(bar(kDkvLanded));
           issue_s(tP, v_desc, desc_lo(o_tile(t), 16));
           ptx::mma_commit_warp(bar(kDkvDpFull));
           return true;
@@ -779,6 +775,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = wait(kDkvPHalf, t))) break;
           // The item's first second product starts dV (and dK) anew.
           if (i == 0 && used > 0 && !(ok = wait(kDkvAccFree, used - 1))) break;
+          if (masked) {  // the second products read checked rows
+            if (!(ok = wait(kDkvChecked, checks))) break;
+            ++checks;
+          }
           issue_second_part(true, tV, tS, desc_lo(o_tile(t), kHalfBytes), i > 0);
           if (!(ok = wait(kDkvPFull, t))) break;
           issue_second_part(false, tV, tS, desc_lo(o_tile(t), kHalfBytes), 1);
@@ -810,6 +810,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // every column of dK (and of dV, when it is Q) through the statistics, and in
     // the column of a non-finite dO element through `poison`, the last row that has
     // one there. An item's epilogue clears it; only then are the next item's put in.
+    // S and dP need no checked rows (a hidden pair's are not used), so the check runs beside
+    // them, and only a row to be changed waits until they have read it. (Before S, the check
+    // held up every masked tile: 16
+    // causal sequences of 1900 tokens 620 us instead of 604.)
     if constexpr (kCheck) {
       const int tid = static_cast<int>(threadIdx.x) - 64;
       int used = 0, tile = 0, m = 0;
@@ -830,15 +834,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t o_t = sbase + kDkvOffO + os * kTileBytes;
           const float* stat = reinterpret_cast<const float*>(smem + kDkvOffStats) + os * kStatFloats;
           bool dirty = false;
+          auto products_done = [&] {
+            wait_bounded(bar(kDkvDpFull), (tile + i) & 1, abort_flag, p.timeout_ns, true);
+          };
           for (int r = tid; r < kTile; r += 64) {
             const float nl = stat[r], nd = stat[kTile + r];
             const bool past = q0 + r >= s.sq;  // (zero already in a dense tensor's tile)
             if (past && !kVarlen) continue;
             if (past || nl == -__int_as_float(0x7F800000)) {
+              products_done();
               zero_row(q_t, r);
               zero_row(o_t, r);
               dirty = true;
             } else if (isnan(nl) || isnan(nd)) {
+              products_done();
               if (used > 0)
                 wait_bounded(bar(kDkvAccFree), (used - 1) & 1, abort_flag, p.timeout_ns, true);
               clean_row(q_t, r, [](int) {});
