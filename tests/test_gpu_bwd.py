@@ -82,9 +82,9 @@ def _check(q, k, v, do, layout, out, lse, grads, causal=False, scale=SCALE, u_mo
     ("bhsd", 1, 1, 1, 50, 4000, False),      # key tiles shared by several CTAs
     ("bshd", 1, 2, 1, 1500, 1500, True),     # both shared, causal
     ("bshd", 3, 8, 8, 640, 640, False),      # more tiles than SMs
-    ("bshd", 1, 2, 1, 1100, 1100, True),     # nine tiles: the last pair's second tile is empty
+    ("bshd", 1, 2, 1, 1100, 1100, True),     # nine tiles
     ("bhsd", 1, 1, 1, 1000, 1290, False),
-    ("bhsd", 1, 2, 2, 1030, 900, True),      # rows without keys next to pairs
+    ("bhsd", 1, 2, 2, 1030, 900, True),      # rows without keys
 ])
 def test_gradients(layout, B, Hq, Hkv, Sq, Sk, causal):
     t = _inputs(layout, B, Hq, Hkv, Sq, Sk, seed=Sq * 7 + Sk + Hq)
@@ -161,7 +161,7 @@ def test_gradient_against_differences():
 @pytest.mark.parametrize("Hq,Hkv", [(2, 2), (6, 2)])
 @pytest.mark.parametrize("lq,lk", [
     ([130, 0, 1, 257, 40, 128], [200, 50, 1, 257, 0, 300]),
-    ([1100, 0, 130, 700, 257, 128], [1100, 300, 129, 1025, 0, 90]),   # long enough for pairs of tiles
+    ([1100, 0, 130, 700, 257, 128], [1100, 300, 129, 1025, 0, 90]),   # several tiles a sequence
 ])
 def test_packed(causal, Hq, Hkv, lq, lk):
     """Ragged sequences, one without queries, one without keys, and tokens behind the last
