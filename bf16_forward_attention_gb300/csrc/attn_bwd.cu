@@ -27,6 +27,23 @@ namespace bwd = attn::bwd;
 std::mutex g_mutex;
 int g_state[kMaxDevices];  // 0 = not set up, 1 = ready, negative = status to return
 
+// The kernels by variant_of.
+using DkvKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap,
+                           const bwd::BwdParams);
+using DqKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap,
+                          const CUtensorMap, const bwd::BwdParams);
+constexpr DkvKernel kDkv[8] = {
+    bwd::attn_bwd_dkv<false, false, false>, bwd::attn_bwd_dkv<true, false, false>,
+    bwd::attn_bwd_dkv<false, true, false>,  bwd::attn_bwd_dkv<true, true, false>,
+    bwd::attn_bwd_dkv<false, false, true>,  bwd::attn_bwd_dkv<true, false, true>,
+    bwd::attn_bwd_dkv<false, true, true>,   bwd::attn_bwd_dkv<true, true, true>};
+constexpr DqKernel kDq[8] = {
+    bwd::attn_bwd_dq<false, false, false>, bwd::attn_bwd_dq<true, false, false>,
+    bwd::attn_bwd_dq<false, true, false>,  bwd::attn_bwd_dq<true, true, false>,
+    bwd::attn_bwd_dq<false, false, true>,  bwd::attn_bwd_dq<true, false, true>,
+    bwd::attn_bwd_dq<false, true, true>,   bwd::attn_bwd_dq<true, true, true>};
+int variant_of(bool causal, bool varlen, bool is_long) { return causal + 2 * varlen + 4 * is_long; }
+
 template <typename F>
 bool raise_smem(F* fn, int bytes) {
   return cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
@@ -45,17 +62,11 @@ int device_ready(int dev) {
     return ATTN_ERR_NO_DEVICE;
   }
   if (major != 10 || minor != 3) return g_state[dev] = ATTN_ERR_ARCH;
-  if (!raise_smem(bwd::attn_bwd_dkv<false, false>, bwd::kDkvSmem) ||
-      !raise_smem(bwd::attn_bwd_dkv<true, false>, bwd::kDkvSmem) ||
-      !raise_smem(bwd::attn_bwd_dkv<false, true>, bwd::kDkvSmem) ||
-      !raise_smem(bwd::attn_bwd_dkv<true, true>, bwd::kDkvSmem) ||
-      !raise_smem(bwd::attn_bwd_dq<false, false>, bwd::kDqSmem) ||
-      !raise_smem(bwd::attn_bwd_dq<true, false>, bwd::kDqSmem) ||
-      !raise_smem(bwd::attn_bwd_dq<false, true>, bwd::kDqSmem) ||
-      !raise_smem(bwd::attn_bwd_dq<true, true>, bwd::kDqSmem)) {
-    cudaGetLastError();
-    return ATTN_ERR_LAUNCH;
-  }
+  for (int i = 0; i < 8; ++i)
+    if (!raise_smem(kDkv[i], bwd::kDkvSmem) || !raise_smem(kDq[i], bwd::kDqSmem)) {
+      cudaGetLastError();
+      return ATTN_ERR_LAUNCH;
+    }
   g_state[dev] = 1;
   return ATTN_OK;
 }
@@ -98,6 +109,7 @@ struct Plan {
   int64_t q_slots, k_slots;  // tile slots per head
   int64_t q_all, k_all;      // slots of all heads
   int dq_splits, dkv_splits;
+  bool dq_long, dkv_long;    // an item may have more tiles than one accumulator takes
   int64_t stats_bytes, dq_bytes, dkv_bytes;
   int64_t bytes() const { return stats_bytes + dq_bytes + dkv_bytes; }
 };
@@ -126,8 +138,12 @@ bool make_plan(Plan* pl, bool varlen, int64_t B, int64_t Hq, int64_t Hkv, int64_
   pl->dkv_splits = choose_splits(B * Hkv * nk, nq * (Hq / Hkv), sms, 5);
   const int64_t tile_bytes = int64_t(bwd::kTile) * attn::kD * 4;
   pl->stats_bytes = pl->q_all * bwd::kStatFloats * 4;
-  pl->dq_bytes = pl->dq_splits > 1 ? pl->dq_splits * pl->q_all * tile_bytes : 0;
-  pl->dkv_bytes = pl->dkv_splits > 1 ? 2 * pl->dkv_splits * pl->k_all * tile_bytes : 0;
+  // fp32 terms of results that several items share, and of items that take several accumulators.
+  auto longer = [](int64_t n, int splits) { return (n + splits - 1) / splits > bwd::kAccTiles; };
+  pl->dq_long = longer(pl->k_tiles, pl->dq_splits);
+  pl->dkv_long = longer(pl->q_tiles * (Hq / Hkv), pl->dkv_splits);
+  pl->dq_bytes = pl->dq_splits > 1 || pl->dq_long ? pl->dq_splits * pl->q_all * tile_bytes : 0;
+  pl->dkv_bytes = pl->dkv_splits > 1 || pl->dkv_long ? 2 * pl->dkv_splits * pl->k_all * tile_bytes : 0;
   return true;
 }
 
@@ -231,10 +247,8 @@ int bwd_impl(const void* dout, const void* q, const void* k, const void* v, cons
   p.n_splits = pl.dq_splits;
   place(&p, causal ? heads_together(B * Hq, 512 * keys_per_head * Hkv / Hq) : 1, Hq);
   p.part = dq_part;
-  auto* dq_fn = varlen ? (causal ? bwd::attn_bwd_dq<true, true> : bwd::attn_bwd_dq<false, true>)
-                       : (causal ? bwd::attn_bwd_dq<true, false> : bwd::attn_bwd_dq<false, false>);
-  if (!launch(dq_fn, B * Hq * pl.q_tiles * pl.dq_splits, attn::kThreads, bwd::kDqSmem, cs, false, tq, tk, tv,
-              tdo, tout, p))
+  if (!launch(kDq[variant_of(causal, varlen, pl.dq_long)], B * Hq * pl.q_tiles * pl.dq_splits, attn::kThreads,
+              bwd::kDqSmem, cs, false, tq, tk, tv, tdo, tout, p))
     return ATTN_ERR_LAUNCH;
 
   p.BH = static_cast<int>(B * Hkv);
@@ -242,10 +256,8 @@ int bwd_impl(const void* dout, const void* q, const void* k, const void* v, cons
   p.n_splits = pl.dkv_splits;
   place(&p, causal ? heads_together(B * Hkv, 512 * rows_per_head * (Hq / Hkv)) : 1, Hkv);
   p.part = dkv_part;
-  auto* dkv_fn = varlen ? (causal ? bwd::attn_bwd_dkv<true, true> : bwd::attn_bwd_dkv<false, true>)
-                        : (causal ? bwd::attn_bwd_dkv<true, false> : bwd::attn_bwd_dkv<false, false>);
-  if (!launch(dkv_fn, B * Hkv * pl.k_tiles * pl.dkv_splits, attn::kThreads, bwd::kDkvSmem, cs, true, tq, tk, tv,
-              tdo, p))
+  if (!launch(kDkv[variant_of(causal, varlen, pl.dkv_long)], B * Hkv * pl.k_tiles * pl.dkv_splits,
+              attn::kThreads, bwd::kDkvSmem, cs, true, tq, tk, tv, tdo, p))
     return ATTN_ERR_LAUNCH;
   if (pl.dq_splits > 1 || pl.dkv_splits > 1) {
     bwd::JoinParams jp;

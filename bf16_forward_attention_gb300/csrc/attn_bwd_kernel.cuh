@@ -25,6 +25,12 @@
 // about the weight of its own rounding to bf16, so a second term as in the forward
 // kernel's P (which has to hold every output to one unit in the last place) would
 // cost 3 more products for less than a factor of 2 in the final error.
+// The tensor pipe's fp32 accumulation truncates, a bias that grows with the number of
+// products in one accumulator: dV over 8192 tiles (131072 queries of 8 heads, dO of mean
+// 1) came out 0.63% small, more than its rounding to bf16. So an accumulator takes
+// kAccTiles streamed tiles at most (0.02% there); the softmax threads then add it, rounded to
+// nearest, to the item's fp32 terms in the workspace, and the next one starts anew (that
+// call: 18.5 -> 19.1 ms; shorter items are as they were).
 //
 // Both kernels: 384 threads. Warp 0: TMA producer. Warp 1: TMEM allocation and
 // the tcgen05.mma issue (one elected lane, in warp-uniform code). Warps 2-3: check of the
@@ -45,6 +51,16 @@ namespace bwd {
 
 constexpr int kTile = 128;             // queries and keys per tile
 constexpr int kStatFloats = 2 * kTile; // per query tile: 128 of -lse log2(e), 128 of -D
+constexpr int kAccTiles = 256;         // streamed tiles summed in one tensor-memory accumulator
+static_assert((kAccTiles & (kAccTiles - 1)) == 0, "used as a mask");
+
+// Accumulators that n streamed tiles take. Kernels are instantiated for calls whose items may
+// take several (kLong) and for the others: the loop and the reads of the terms so far cost
+// a call of a few tiles 3 to 7% (256 tokens: 12.9 -> 13.9 us).
+template <bool kLong>
+__device__ __forceinline__ int accumulators(int n) {
+  return kLong ? (n + kAccTiles - 1) / kAccTiles : n > 0;
+}
 
 // Division of n in [0, 2^31) by a number fixed for a launch, as a product (Granlund and
 // Montgomery, "Division by invariant integers using multiplication"): with 2^(s+1) >= d and
@@ -85,7 +101,9 @@ struct BwdParams {
   int q_slots, k_slots;    // tile slots per head (see tile_slot)
   const float* lse;
   float* stats;            // [head][slot][2][128]: written by dq, read by dkv
-  float* part;             // n_splits > 1: [split][result][head * slots] tiles of fp32 terms
+  // Tiles of fp32 terms, [split][result][head * slots]: of results shared by n_splits > 1
+  // items, and of items of more than kAccTiles streamed tiles.
+  float* part;
   uint16_t *dq, *dk, *dv;  // results
 };
 
@@ -327,10 +345,12 @@ __device__ __forceinline__ uint64_t pair_of(const uint32_t (&r)[32], int x) {
 // three exchanges) leaves chunk hi of row 4 k + lo in register k, and each store writes
 // 128 bytes of four rows. `out`: row 0 of the warp, pitch: elements from row to row, rows:
 // how many are stored. `poison(col)`: the thread's row is NaN there; any: there is such
-// a column. zero: no product was formed, the result is 0.
+// a column. zero: no product was formed, the result is 0. sum: the thread's terms so far
+// (the tile's, as store_part leaves them, at the thread's row and first column), or null.
 template <int kCols, typename F>
 __device__ __forceinline__ void store_rows(uint32_t tacc, bool zero, float factor, int mode, uint16_t* out,
-                                           size_t pitch, int rows, int lane, bool any, F poison) {
+                                           size_t pitch, int rows, int lane, const float4* sum, bool any,
+                                           F poison) {
   const uint64_t f2 = ptx::f2_pack(factor, factor);
   const uint32_t bias = mode == 1 ? 0x8000u : 0u;
   const int hi = lane >> 2, lo = lane & 3;
@@ -345,6 +365,16 @@ __device__ __forceinline__ void store_rows(uint32_t tacc, bool zero, float facto
       } else {
 #pragma unroll
         for (int i = 0; i < 32; ++i) r[i] = 0;
+      }
+      if (sum) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 x = sum[(16 * part + 8 * ch + i) * kTile];
+          r[4 * i] = __float_as_uint(__uint_as_float(r[4 * i]) + x.x);
+          r[4 * i + 1] = __float_as_uint(__uint_as_float(r[4 * i + 1]) + x.y);
+          r[4 * i + 2] = __float_as_uint(__uint_as_float(r[4 * i + 2]) + x.z);
+          r[4 * i + 3] = __float_as_uint(__uint_as_float(r[4 * i + 3]) + x.w);
+        }
       }
       if (any) {
 #pragma unroll
@@ -396,11 +426,12 @@ __device__ __forceinline__ void store_rows(uint32_t tacc, bool zero, float facto
   }
 }
 
-// kCols columns of a row as fp32 into the split workspace (one of n_splits terms of a sum).
-// A tile's terms lie by chunks of four columns, [chunk][row][4], so that a warp's store is 512
-// consecutive bytes. `part`: the tile's terms, c0: the first column.
+// kCols columns of a row as fp32 into the workspace (one of n_splits terms of a sum, or an
+// item's sum so far), or added to what the thread left there. A tile's terms lie by chunks of
+// four columns, [chunk][row][4], so that a warp's store is 512 consecutive bytes. `part`: the
+// tile's terms at the thread's row and first column.
 template <int kCols, typename F>
-__device__ __forceinline__ void store_part(uint32_t tacc, bool zero, float* part, int row, int c0, F poison) {
+__device__ __forceinline__ void store_part(uint32_t tacc, bool zero, float4* part, bool add, F poison) {
   const float nan = __int_as_float(0x7FC00000);
 #pragma unroll 1
   for (int ch = 0; ch < kCols / 16; ++ch) {
@@ -416,7 +447,12 @@ __device__ __forceinline__ void store_part(uint32_t tacc, bool zero, float* part
       float x[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[e] = poison(16 * ch + i + e) ? nan : __uint_as_float(r[i + e]);
-      reinterpret_cast<float4*>(part)[(c0 + 16 * ch + i) / 4 * kTile + row] = make_float4(x[0], x[1], x[2], x[3]);
+      float4* at = part + (4 * ch + i / 4) * kTile;
+      if (add) {
+        const float4 y = *at;
+        x[0] += y.x; x[1] += y.y; x[2] += y.z; x[3] += y.w;
+      }
+      *at = make_float4(x[0], x[1], x[2], x[3]);
     }
   }
 }
@@ -538,8 +574,8 @@ enum : int {
   kDkvPFull,
   kDkvDpFull,
   kDkvDsFull,
-  kDkvAcc,
-  kDkvAccFree,  // the epilogue has read dK and dV
+  kDkvAcc,      // dK and dV of an item, or of kAccTiles of its tiles
+  kDkvAccFree,  // the epilogue has read them
   kDkvLanded,
   kDkvChecked,
   kDkvDrain,
@@ -599,7 +635,7 @@ struct QueryTiles {
   __device__ __forceinline__ void step() { q0 = q0 == last ? first : q0 + kTile; }
 };
 
-template <bool kCausal, bool kVarlen>
+template <bool kCausal, bool kVarlen, bool kLong>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_bwd_dkv(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -744,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::tc_fence_after();
       return r;
     };
-    int used = 0, tile = 0, checks = 0;
+    int used = 0, tile = 0, checks = 0, accs = 0;
     bool ok = true;
     for (int item = static_cast<int>(blockIdx.x), it = 0; ok && item >= 0; ++it) {
       const DkvItem w = dkv_item<kCausal, kVarlen>(p, item);
@@ -773,25 +809,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int t = tile + i;
           const bool more = i + 1 < w.n;
           if (!(ok = wait(kDkvPHalf, t))) break;
-          // The item's first second product starts dV (and dK) anew.
-          if (i == 0 && used > 0 && !(ok = wait(kDkvAccFree, used - 1))) break;
+          // dV (and dK) start anew with the item, and after every kAccTiles tiles.
+          const int summed = kLong ? i & (kAccTiles - 1) : i;
+          if (summed == 0 && accs > 0 && !(ok = wait(kDkvAccFree, accs - 1))) break;
           if (masked) {  // the second products read checked rows
             if (!(ok = wait(kDkvChecked, checks))) break;
             ++checks;
           }
-          issue_second_part(true, tV, tS, desc_lo(o_tile(t), kHalfBytes), i > 0);
+          issue_second_part(true, tV, tS, desc_lo(o_tile(t), kHalfBytes), summed > 0);
           if (!(ok = wait(kDkvPFull, t))) break;
           issue_second_part(false, tV, tS, desc_lo(o_tile(t), kHalfBytes), 1);
           if (more && !(ok = do_s(t + 1))) break;
           if (!(ok = wait(kDkvDsFull, t))) break;
-          issue_second(tK, tP, desc_lo(q_tile(t), kHalfBytes), i > 0);
+          issue_second(tK, tP, desc_lo(q_tile(t), kHalfBytes), summed > 0);
           ptx::mma_commit_warp(bar(kDkvQEmpty + t % kDkvQStages));
           // (dO's last product is dV, but the statistics beside it are read until dS.)
           ptx::mma_commit_warp(bar(kDkvOEmpty + t % kDkvOStages));
+          if (kLong && more && summed == kAccTiles - 1) {
+            ptx::mma_commit_warp(bar(kDkvAcc));
+            ++accs;
+          }
           if (more && !(ok = do_dp(t + 1))) break;
           if (i + 2 == w.n) ptx::mma_commit_warp(bar(kDkvKVFree));  // the last dP was issued
         }
         if (ok) ptx::mma_commit_warp(bar(kDkvAcc));
+        ++accs;
         tile += w.n;
         ++used;
       }
@@ -816,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // causal sequences of 1900 tokens 620 us instead of 604.)
     if constexpr (kCheck) {
       const int tid = static_cast<int>(threadIdx.x) - 64;
-      int used = 0, tile = 0, m = 0;
+      int accs = 0, tile = 0, m = 0;  // accs: accumulators of the items before this one
       bool ok = true;
       for (int item = static_cast<int>(blockIdx.x), it = 0; ok && item >= 0; ++it) {
         const DkvItem w = dkv_item<kCausal, kVarlen>(p, item);
@@ -848,8 +890,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               dirty = true;
             } else if (isnan(nl) || isnan(nd)) {
               products_done();
-              if (used > 0)
-                wait_bounded(bar(kDkvAccFree), (used - 1) & 1, abort_flag, p.timeout_ns, true);
+              // (Past the item's first kAccTiles the last one's epilogue is long over.)
+              if (accs > 0 && (!kLong || i < kAccTiles))
+                wait_bounded(bar(kDkvAccFree), (accs - 1) & 1, abort_flag, p.timeout_ns, true);
               clean_row(q_t, r, [](int) {});
               clean_row(o_t, r, [&](int col) {
                 atomicMax(&poison[col], q0 + r);
@@ -864,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (tid == 0) ptx::mbar_arrive(bar(kDkvChecked));
         }
         tile += w.n;
-        if (w.n > 0) ++used;
+        accs += accumulators<kLong>(w.n);
         if (ok) item = next_together(items, it, lane);
       }
     }
@@ -877,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tSh = tS + lane_base + 64 * g, tPh = tP + lane_base + 64 * g;
     const uint64_t c2 = ptx::f2_pack(p.c, p.c);
     Meeting all{bar(kDkvMeet), abort_flag, p.timeout_ns, 0};
-    int used = 0, tile = 0;
+    int accs = 0, tile = 0;
     bool ok = true;
     int item = static_cast<int>(blockIdx.x);
     DkvItem w = dkv_item<kCausal, kVarlen>(p, item);
@@ -885,77 +928,88 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int first_row = w.k0 + row - w.off;  // the first query that sees this key (causal)
       const int n = w.n, sq = w.s.sq, off = w.off, k0 = w.k0;
       QueryTiles qt(w);
-      for (int i = 0; i < n; ++i, ++tile, qt.step()) {
-        const bool mk = dkv_masked<kCausal>(qt.q0, sq, off, k0);
-        // The columns of this half that this key is visible to: [lo, hi).
-        const int lo = kCausal ? first_row - qt.q0 - 64 * g : 0;
-        const int hi = sq - qt.q0 - 64 * g;
-        const ulonglong2* stat = reinterpret_cast<const ulonglong2*>(
-            smem + kDkvOffStats + (tile % kDkvOStages) * kStatFloats * 4 + 256 * g);
-        Half pr;
-        if (!(ok = warp_wait(bar(kDkvSFull), tile & 1, abort_flag, p.timeout_ns))) break;
-        // (dO's barrier, for the statistics that land with it.)
-        if (!(ok = warp_wait(bar(kDkvOFull + tile % kDkvOStages), (tile / kDkvOStages) & 1, abort_flag,
-                             p.timeout_ns)))
-          break;
-        ptx::tc_fence_after();
-        if (mk)
-          dkv_p<true>(tSh, stat, c2, lo, hi, pr, bar(kDkvPHalf), lane);
-        else
-          dkv_p<false>(tSh, stat, c2, lo, hi, pr, bar(kDkvPHalf), lane);
-        ptx::tmem_wait_st();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(kDkvPFull));
+      int i = 0;
+      do {
+        const int end = kLong ? min(n, i + kAccTiles) : n;
+        for (; i < end; ++i, ++tile, qt.step()) {
+          const bool mk = dkv_masked<kCausal>(qt.q0, sq, off, k0);
+          // The columns of this half that this key is visible to: [lo, hi).
+          const int lo = kCausal ? first_row - qt.q0 - 64 * g : 0;
+          const int hi = sq - qt.q0 - 64 * g;
+          const ulonglong2* stat = reinterpret_cast<const ulonglong2*>(
+              smem + kDkvOffStats + (tile % kDkvOStages) * kStatFloats * 4 + 256 * g);
+          Half pr;
+          if (!(ok = warp_wait(bar(kDkvSFull), tile & 1, abort_flag, p.timeout_ns))) break;
+          // (dO's barrier, for the statistics that land with it.)
+          if (!(ok = warp_wait(bar(kDkvOFull + tile % kDkvOStages), (tile / kDkvOStages) & 1, abort_flag,
+                               p.timeout_ns)))
+            break;
+          ptx::tc_fence_after();
+          if (mk)
+            dkv_p<true>(tSh, stat, c2, lo, hi, pr, bar(kDkvPHalf), lane);
+          else
+            dkv_p<false>(tSh, stat, c2, lo, hi, pr, bar(kDkvPHalf), lane);
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(kDkvPFull));
 
-        if (!(ok = warp_wait(bar(kDkvDpFull), tile & 1, abort_flag, p.timeout_ns))) break;
-        ptx::tc_fence_after();
-        if (mk)
-          dkv_ds<true>(tPh, stat, lo, hi, pr);
-        else
-          dkv_ds<false>(tPh, stat, lo, hi, pr);
-        ptx::tmem_wait_st();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(kDkvDsFull));
-      }
-      if (!ok) break;
-      // ---- epilogue: warpgroup 0 stores dK, warpgroup 1 dV. (The next item is taken up
-      // before the wait.)
-      const bool zero = n == 0;
-      const DkvItem v = w;
-      item = items.next_warp(it, lane);
-      if (item >= 0) w = dkv_item<kCausal, kVarlen>(p, item);
-      if (!zero && !(ok = warp_wait(bar(kDkvAcc), used & 1, abort_flag, p.timeout_ns))) break;
-      ptx::tc_fence_after();
-      if (!v.skip) {
-        const Seq& s = v.s;
-        const uint32_t tacc = (g == 0 ? tK : tV) + lane_base;
-        const bool any = kCheck && !zero && *static_cast<volatile int*>(poison + kD);
-        // The last query row whose non-finite dO element a key may see (see above).
-        const int seen = kCausal ? max(0, v.k0 + row - v.off) : 0;
-        auto is_nan = [&](int col) -> bool { return any && g == 1 && poison[col] >= seen; };
-        if (p.n_splits == 1) {
-          const int first = v.k0 + 32 * wq;  // of the warp's rows
-          const int rows = dbg_ok(s.k_base + s.sk <= p.Sk) ? s.sk - first : 0;
-          uint16_t* dst = (g == 0 ? p.dk : p.dv) +
-                          row_at(p.layout, s.batch, p.Hkv, p.Sk, s.head, s.k_base + (rows > 0 ? first : 0));
-          store_rows<kD>(tacc, zero, g == 0 ? p.scale : 1.f, p.mode, dst,
-                         static_cast<size_t>(p.layout == 0 ? 1 : p.Hkv) * kD, rows, lane, any && g == 1, is_nan);
-        } else {
-          const size_t slots = static_cast<size_t>(p.k_slots) * (kVarlen ? p.Hkv : p.BH);
-          const size_t slot = static_cast<size_t>(s.slot_k) + static_cast<size_t>(s.head) * p.k_slots + s.tile;
-          float* dst = p.part + ((static_cast<size_t>(s.split) * 2 + g) * slots + slot) * kTile * kD;
-          store_part<kD>(tacc, zero, dst, row, 0, is_nan);
+          if (!(ok = warp_wait(bar(kDkvDpFull), tile & 1, abort_flag, p.timeout_ns))) break;
+          ptx::tc_fence_after();
+          if (mk)
+            dkv_ds<true>(tPh, stat, lo, hi, pr);
+          else
+            dkv_ds<false>(tPh, stat, lo, hi, pr);
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(kDkvDsFull));
         }
-        if (any && !(ok = clear_poison(poison, -1, all, lane))) break;
-      }
-      if (!zero) {
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(kDkvAccFree));
-        ++used;
-      }
+        if (!ok) break;
+        // ---- epilogue: warpgroup 0 stores dK, warpgroup 1 dV, or adds them to the item's
+        // terms. (The next item is taken up before the wait.)
+        const bool zero = n == 0, last = !kLong || i == n;
+        const DkvItem v = w;
+        if (last) {
+          item = items.next_warp(it, lane);
+          if (item >= 0) w = dkv_item<kCausal, kVarlen>(p, item);
+        }
+        if (!zero && !(ok = warp_wait(bar(kDkvAcc), accs & 1, abort_flag, p.timeout_ns))) break;
+        ptx::tc_fence_after();
+        if (!v.skip) {
+          const Seq& s = v.s;
+          const uint32_t tacc = (g == 0 ? tK : tV) + lane_base;
+          const bool any = kCheck && !zero && last && *static_cast<volatile int*>(poison + kD);
+          // The last query row whose non-finite dO element a key may see (see above).
+          const int seen = kCausal ? max(0, v.k0 + row - v.off) : 0;
+          auto is_nan = [&](int col) -> bool { return any && g == 1 && poison[col] >= seen; };
+          auto terms = [&]() -> float4* {
+            const size_t slots = static_cast<size_t>(p.k_slots) * (kVarlen ? p.Hkv : p.BH);
+            const size_t slot = static_cast<size_t>(s.slot_k) + static_cast<size_t>(s.head) * p.k_slots + s.tile;
+            return reinterpret_cast<float4*>(
+                       p.part + ((static_cast<size_t>(s.split) * 2 + g) * slots + slot) * kTile * kD) + row;
+          };
+          if (last && p.n_splits == 1) {
+            const int first = v.k0 + 32 * wq;  // of the warp's rows
+            const int rows = dbg_ok(s.k_base + s.sk <= p.Sk) ? s.sk - first : 0;
+            uint16_t* dst = (g == 0 ? p.dk : p.dv) +
+                            row_at(p.layout, s.batch, p.Hkv, p.Sk, s.head, s.k_base + (rows > 0 ? first : 0));
+            store_rows<kD>(tacc, zero, g == 0 ? p.scale : 1.f, p.mode, dst,
+                           static_cast<size_t>(p.layout == 0 ? 1 : p.Hkv) * kD, rows, lane,
+                           kLong && n > kAccTiles ? terms() : nullptr, any && g == 1, is_nan);
+          } else {
+            store_part<kD>(tacc, zero, terms(), kLong && i > kAccTiles, is_nan);
+          }
+          if (any && !(ok = clear_poison(poison, -1, all, lane))) break;
+        }
+        if (!zero) {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(kDkvAccFree));
+          ++accs;
+        }
+      } while (kLong && i < n);
+      if (!ok) break;
     }
   }
   ptx::tc_fence_before();
@@ -1001,8 +1055,8 @@ enum : int {
   kDqSFull = kDqVEmpty + kDqVStages,
   kDqDpFull = kDqSFull + 2,
   kDqDsFull,
-  kDqAcc,
-  kDqAccFree,   // the epilogue has read dQ
+  kDqAcc,       // dQ of an item, or of kAccTiles of its tiles
+  kDqAccFree,   // the epilogue has read it
   kDqLanded,
   kDqChecked = kDqLanded + kDqChecks,
   kDqDrain = kDqChecked + kDqChecks,
@@ -1051,7 +1105,7 @@ __device__ __forceinline__ DqItem dq_item(const BwdParams& p, int item) {
 // is wanted): fill of K_j, counted from the item's first.
 __device__ __forceinline__ int k_fill(int j) { return j + 1; }
 
-template <bool kCausal, bool kVarlen>
+template <bool kCausal, bool kVarlen, bool kLong>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_bwd_dq(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -1175,7 +1229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::tc_fence_after();
       return r;
     };
-    int used = 0, tile = 0, k_base = 0, landed = 0, checked = 0;
+    int used = 0, tile = 0, k_base = 0, landed = 0, checked = 0, accs = 0;
     bool ok = true;
     for (int item = static_cast<int>(blockIdx.x), it = 0; ok && item >= 0; ++it) {
       const DqItem w = dq_item<kCausal, kVarlen>(p, item);
@@ -1214,13 +1268,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = wait(kDqChecked + checked % kDqChecks, checked / kDqChecks))) break;
             ++checked;
           }
-          // The item's first product with K starts dQ anew.
-          if (j == 0 && used > 0 && !(ok = wait(kDqAccFree, used - 1))) break;
-          issue_second(tQ, tmem + 128 * ((tile + j) & 1), desc_lo(k_tile(j), kHalfBytes), j > 0);
+          // dQ starts anew with the item, and after every kAccTiles tiles.
+          const int summed = kLong ? j & (kAccTiles - 1) : j;
+          if (summed == 0 && accs > 0 && !(ok = wait(kDqAccFree, accs - 1))) break;
+          issue_second(tQ, tmem + 128 * ((tile + j) & 1), desc_lo(k_tile(j), kHalfBytes), summed > 0);
           ptx::mma_commit_warp(bar(kDqKEmpty + (k_base + k_fill(j)) % kDqKStages));
+          if (kLong && j + 1 < n && summed == kAccTiles - 1) {
+            ptx::mma_commit_warp(bar(kDqAcc));
+            ++accs;
+          }
           if (j + 2 < n && !(ok = do_s(j + 2))) break;
         }
         if (ok) ptx::mma_commit_warp(bar(kDqAcc));
+        ++accs;
         tile += n;
         k_base += n + 1;
         ++used;
@@ -1240,7 +1300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // in.
     if constexpr (kCheck) {
       const int tid = static_cast<int>(threadIdx.x) - 64;
-      int used = 0, tile = 0, k_base = 0, m = 0;
+      int accs = 0, tile = 0, k_base = 0, m = 0;  // accs: accumulators of the items before this one
       bool ok = true;
       for (int item = static_cast<int>(blockIdx.x), it = 0; ok && item >= 0; ++it) {
         const DqItem w = dq_item<kCausal, kVarlen>(p, item);
@@ -1271,8 +1331,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               acc = ptx::bf16x2_nonfinite_acc(x.z, ptx::bf16x2_nonfinite_acc(x.w, acc));
             }
             if (acc != 0) {
-              if (used > 0)
-                wait_bounded(bar(kDqAccFree), (used - 1) & 1, abort_flag, p.timeout_ns, true);
+              // (Past the item's first kAccTiles the last one's epilogue is long over.)
+              if (accs > 0 && (!kLong || j < kAccTiles))
+                wait_bounded(bar(kDqAccFree), (accs - 1) & 1, abort_flag, p.timeout_ns, true);
               clean_row(kt, r, [&](int col) {
                 atomicMin(&poison[col], first + r);
                 *static_cast<volatile int*>(poison + kD) = 1;
@@ -1288,7 +1349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (w.n > 0) {
           tile += w.n;
           k_base += w.n + 1;
-          ++used;
+          accs += accumulators<kLong>(w.n);
         }
         if (ok) item = next_together(items, it, lane);
       }
@@ -1302,7 +1363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tPh = tP + lane_base + 64 * g;
     const uint64_t c2 = ptx::f2_pack(p.c, p.c);
     Meeting all{bar(kDqMeet), abort_flag, p.timeout_ns, 0};
-    int used = 0, tile = 0, k_base = 0;
+    int used = 0, tile = 0, k_base = 0, accs = 0;
     bool ok = true;
     // The row's log-sum-exp is read when the item is known, long before it is used.
     auto read_lse = [&](const DqItem& w) -> float {
@@ -1361,71 +1422,86 @@ __global__ void __launch_bounds__(kThreads, 1)
         nl2 = ptx::f2_pack(nl, nl);
         nd2 = ptx::f2_pack(nd, nd);
       }
-      for (int j = 0; j < n; ++j, ++tile) {
-        const uint32_t tSh = tmem + 128 * (tile & 1) + lane_base + 64 * g;
-        const int hi = limit - j * kTile - 64 * g;  // columns of this half the row sees
-        Half pr;
-        if (!(ok = warp_wait(bar(kDqSFull + (tile & 1)), (tile >> 1) & 1, abort_flag, p.timeout_ns))) break;
-        ptx::tc_fence_after();
-        by_halves(tSh, [&](int ch, const uint32_t (&r)[32]) {
+      int j = 0;
+      do {
+        const int end = kLong ? min(n, j + kAccTiles) : n;
+        for (; j < end; ++j, ++tile) {
+          const uint32_t tSh = tmem + 128 * (tile & 1) + lane_base + 64 * g;
+          const int hi = limit - j * kTile - 64 * g;  // columns of this half the row sees
+          Half pr;
+          if (!(ok = warp_wait(bar(kDqSFull + (tile & 1)), (tile >> 1) & 1, abort_flag, p.timeout_ns))) break;
+          ptx::tc_fence_after();
+          by_halves(tSh, [&](int ch, const uint32_t (&r)[32]) {
 #pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            float e0, e1;
-            ptx::f2_unpack(ptx::f2_fma(pair_of(r, 2 * x), c2, nl2), e0, e1);
-            pr[16 * ch + x] = ptx::f2_pack(ptx::ex2(e0), ptx::ex2(e1));
-          }
-        });
-        if (!(ok = warp_wait(bar(kDqDpFull), tile & 1, abort_flag, p.timeout_ns))) break;
-        ptx::tc_fence_after();
-        if (j >= first_masked)
-          dq_ds<true>(tPh, tSh, nd2, hi, pr);
-        else
-          dq_ds<false>(tPh, tSh, nd2, hi, pr);
-        ptx::tmem_wait_st();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(kDqDsFull));
-      }
-      if (!ok) break;
-      // ---- epilogue: each warpgroup stores 64 columns of the rows. (The next item is taken
-      // up before the wait.)
-      const bool zero = n == 0;
-      const DqItem v = w;
-      item = items.next_warp(it, lane);
-      if (item >= 0) {
-        w = dq_item<kCausal, kVarlen>(p, item);
-        lse = read_lse(w);
-      }
-      if (!zero && !(ok = warp_wait(bar(kDqAcc), used & 1, abort_flag, p.timeout_ns))) break;
-      ptx::tc_fence_after();
-      if (!v.skip) {
-        const Seq& s = v.s;
-        const uint32_t tacc = tQ + lane_base + 64 * g;
-        const bool any = kCheck && !zero && *static_cast<volatile int*>(poison + kD);
-        const int sees = kCausal ? min(v.q0 + row + v.off + 1, s.sk) : s.sk;
-        auto is_nan = [&](int col) -> bool { return any && poison[64 * g + col] < sees; };
-        if (p.n_splits == 1) {
-          const int first = v.q0 + 32 * wq;  // of the warp's rows
-          const int rows = dbg_ok(s.q_base + s.sq <= p.Sq) ? s.sq - first : 0;
-          uint16_t* dst =
-              p.dq + row_at(p.layout, s.batch, p.Hq, p.Sq, s.head, s.q_base + (rows > 0 ? first : 0)) + 64 * g;
-          store_rows<64>(tacc, zero, p.scale, p.mode, dst, static_cast<size_t>(p.layout == 0 ? 1 : p.Hq) * kD, rows,
-                         lane, any, is_nan);
-        } else {
-          const size_t slots = static_cast<size_t>(p.q_slots) * (kVarlen ? p.Hq : p.BH);
-          const size_t slot = static_cast<size_t>(s.slot_q) + static_cast<size_t>(s.head) * p.q_slots + s.tile;
-          float* dst = p.part + (static_cast<size_t>(s.split) * slots + slot) * kTile * kD;
-          store_part<64>(tacc, zero, dst, row, 64 * g, is_nan);
+            for (int x = 0; x < 16; ++x) {
+              float e0, e1;
+              ptx::f2_unpack(ptx::f2_fma(pair_of(r, 2 * x), c2, nl2), e0, e1);
+              pr[16 * ch + x] = ptx::f2_pack(ptx::ex2(e0), ptx::ex2(e1));
+            }
+          });
+          if (!(ok = warp_wait(bar(kDqDpFull), tile & 1, abort_flag, p.timeout_ns))) break;
+          ptx::tc_fence_after();
+          if (j >= first_masked)
+            dq_ds<true>(tPh, tSh, nd2, hi, pr);
+          else
+            dq_ds<false>(tPh, tSh, nd2, hi, pr);
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(kDqDsFull));
         }
-        if (any && !(ok = clear_poison(poison, kNever, all, lane))) break;
-      }
-      if (!zero) {
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(kDqAccFree));
-        k_base += n + 1;
-        ++used;
-      }
+        if (!ok) break;
+        // ---- epilogue: each warpgroup stores 64 columns of the rows, or adds them to the item's
+        // terms. (The next item is taken up before the wait.)
+        const bool zero = n == 0, last = !kLong || j == n;
+        const DqItem v = w;
+        if (last) {
+          item = items.next_warp(it, lane);
+          if (item >= 0) {
+            w = dq_item<kCausal, kVarlen>(p, item);
+            lse = read_lse(w);
+          }
+        }
+        if (!zero && !(ok = warp_wait(bar(kDqAcc), (kLong ? accs : used) & 1, abort_flag, p.timeout_ns))) break;
+        ptx::tc_fence_after();
+        if (!v.skip) {
+          const Seq& s = v.s;
+          const uint32_t tacc = tQ + lane_base + 64 * g;
+          const bool any = kCheck && !zero && last && *static_cast<volatile int*>(poison + kD);
+          const int sees = kCausal ? min(v.q0 + row + v.off + 1, s.sk) : s.sk;
+          auto is_nan = [&](int col) -> bool { return any && poison[64 * g + col] < sees; };
+          auto terms = [&]() -> float4* {
+            const size_t slots = static_cast<size_t>(p.q_slots) * (kVarlen ? p.Hq : p.BH);
+            const size_t slot = static_cast<size_t>(s.slot_q) + static_cast<size_t>(s.head) * p.q_slots + s.tile;
+            return reinterpret_cast<float4*>(
+                       p.part + (static_cast<size_t>(s.split) * slots + slot) * kTile * kD) + 16 * g * kTile + row;
+          };
+          if (last && p.n_splits == 1) {
+            const int first = v.q0 + 32 * wq;  // of the warp's rows
+            const int rows = dbg_ok(s.q_base + s.sq <= p.Sq) ? s.sq - first : 0;
+            uint16_t* dst =
+                p.dq + row_at(p.layout, s.batch, p.Hq, p.Sq, s.head, s.q_base + (rows > 0 ? first : 0)) + 64 * g;
+            store_rows<64>(tacc, zero, p.scale, p.mode, dst, static_cast<size_t>(p.layout == 0 ? 1 : p.Hq) * kD, rows,
+                           lane, kLong && n > kAccTiles ? terms() : nullptr, any, is_nan);
+          } else {
+            store_part<64>(tacc, zero, terms(), kLong && j > kAccTiles, is_nan);
+          }
+          if (any && !(ok = clear_poison(poison, kNever, all, lane))) break;
+        }
+        if (!zero) {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(kDqAccFree));
+          if (kLong) ++accs;
+          if (last) {
+            k_base += n + 1;
+            ++used;
+          }
+        }
+      } while (kLong && j < n);
+      // (The loop ends by its condition too. With this the compiler's order of the masked forms
+      // is the faster one, causal 4K 321 -> 313 us, and that of the unmasked one 1% slower.)
+      if (kCheck && !ok) break;
     }
   }
   ptx::tc_fence_before();

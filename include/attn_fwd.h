@@ -249,7 +249,10 @@ int attn_fwd_varlen_lse(const void* q, const void* k, const void* v, void* out, 
  *   dq        device, bf16, like q                            (written)
  *   dk, dv    device, bf16, like k                            (written)
  *   rounding_mode  of the gradients, one rounding from fp32 sums (P and dS are
- *             rounded to bf16, to nearest, as operands of the products)
+ *             rounded to bf16, to nearest, as operands of the products, and D is
+ *             formed from out as it was rounded). The tensor pipe truncates as it
+ *             sums; long sums are cut at 32768 rows and their parts added in fp32
+ *             to nearest, which keeps that below 2^-12 of a sum
  *   flags     0 or ATTN_FLAG_CAUSAL, as in the forward call
  *   workspace device, 16-byte aligned, attn_bwd_workspace_bytes(...) bytes, owned
  *             by the caller; its contents on entry do not matter. Calls that
