@@ -27,8 +27,11 @@ std::mutex g_mutex;
 int g_state[kMaxDevices];  // 0 = not set up, 1 = ready, negative = status to return
 
 using OwnKernel = void (*)(const pre::OwnParams);
-constexpr OwnKernel kOwn[4] = {pre::attn_prefix_own<1>, pre::attn_prefix_own<2>, pre::attn_prefix_own<3>,
-                               pre::attn_prefix_own<4>};  // by 8-row tiles of a block
+// By 8-row tiles of a block; the second four for long parts.
+constexpr OwnKernel kOwn[8] = {pre::attn_prefix_own<1, false>, pre::attn_prefix_own<2, false>,
+                               pre::attn_prefix_own<3, false>, pre::attn_prefix_own<4, false>,
+                               pre::attn_prefix_own<1, true>,  pre::attn_prefix_own<2, true>,
+                               pre::attn_prefix_own<3, true>,  pre::attn_prefix_own<4, true>};
 
 int device_ready(int dev) {
   if (dev < 0 || dev >= kMaxDevices) return ATTN_ERR_NO_DEVICE;
@@ -82,9 +85,14 @@ bool make_plan(Plan* pl, int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int64_t
   // Own keys: two blocks for every SM (what it holds at once), of at least 256 keys of
   // the cache each (lengths are on the device; a short sequence's parts are shorter).
   const int64_t items = B * Hkv * pl->blocks;
+  // Blocks of more than 16 rows are bound by their instructions, and the additions of kFold
+  // would cost them 5 to 28%: their parts are kept short instead.
+  const bool cut_short = pl->block_rows > 16;
+  auto parts_of = [](int64_t keys) { return (keys + pre::kFoldKeys - 1) / pre::kFoldKeys; };
   int64_t s = (2 * sms + items - 1) / items;
   const int64_t most = (cap + 255) / 256;
   if (s > most) s = most;
+  if (cut_short && s < parts_of(cap)) s = parts_of(cap);
   if (s > 64) s = 64;
   pl->own_splits = static_cast<int>(s);
   pl->prefix_blocks = 0;
@@ -97,6 +105,7 @@ bool make_plan(Plan* pl, int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int64_t
     int64_t n = (2 * sms + Hkv - 1) / Hkv;
     const int64_t cut = (Sp + 255) / 256;
     if (n > cut) n = cut;
+    if (cut_short && n < parts_of(Sp)) n = parts_of(Sp);
     if (n > 64) n = 64;
     pl->prefix_splits = static_cast<int>(n);
   } else if (Sp > 0) {
@@ -248,7 +257,9 @@ int attn_fwd_prefix(const void* q, const void* k_prefix, const void* v_prefix, c
     if (st != ATTN_OK) return st;
   }
   p.block_rows = static_cast<int>(pl.block_rows);
-  if (!launch(kOwn[(pl.block_rows + 7) / 8 - 1],
+  const bool fold = cap > int64_t(pre::kFoldKeys) * pl.own_splits ||
+                    (prefix_items > 0 && Sp > int64_t(pre::kFoldKeys) * pl.prefix_splits);
+  if (!launch(kOwn[(pl.block_rows + 7) / 8 - 1 + (fold ? 4 : 0)],
               prefix_items + B * Hkv * pl.blocks * pl.own_splits, pre::kOwnThreads, pre::kOwnSmem, cs, fused_prefix,
               p))
     return ATTN_ERR_LAUNCH;
