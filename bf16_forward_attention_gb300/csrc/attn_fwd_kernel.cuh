@@ -1113,7 +1113,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool more = j + 1 < n_kv;
             if (!(ok = ring_wait(vit))) break;
             if (kRowLimit && j >= jm && j - jm < kMaxMaskedTiles &&
-                !(ok = wait_bounded(bar(kBarVChk + (j - jm)), 0, abort_flag, p.timeout_ns, true)))
+                !(ok = warp_wait(bar(kBarVChk + (j - jm)), 0, abort_flag, p.timeout_ns)))
               break;
             if (!(ok = warp_wait(bar(kBarPFull + 0), j & 1, abort_flag, p.timeout_ns))) break;
             ptx::tc_fence_after();
