@@ -143,11 +143,10 @@ __device__ __forceinline__ Seq seq_of(const BwdParams& p, int block) {
   s.bad = false;
   if (kVarlen) {
     s.q_base = __ldg(p.cu_q + b);
-    s.sq = __ldg(p.cu_q + b + 1) - s.q_base;
+    s.sq = packed_len(s.q_base, __ldg(p.cu_q + b + 1), p.max_sq, p.Sq);
     s.k_base = __ldg(p.cu_k + b);
-    s.sk = __ldg(p.cu_k + b + 1) - s.k_base;
-    s.bad = s.q_base < 0 || s.sq < 0 || s.sq > p.max_sq || s.q_base + s.sq > p.Sq || s.k_base < 0 ||
-            s.sk < 0 || s.sk > p.max_sk || s.k_base + s.sk > p.Sk;
+    s.sk = packed_len(s.k_base, __ldg(p.cu_k + b + 1), p.max_sk, p.Sk);
+    s.bad = s.sq < 0 || s.sk < 0;
     s.batch = 0;
     s.slot_q = tile_slot<true>(s.q_base, b);  // the head's offset is added by the user
     s.slot_k = tile_slot<true>(s.k_base, b);
@@ -1551,11 +1550,8 @@ __device__ __forceinline__ void join_rows(const JoinPart& j, int B, int layout, 
   size_t slot = (static_cast<size_t>(b) * j.H + h) * j.slots + tile;
   if (kVarlen) {
     base = __ldg(j.cu + b);
-    len = __ldg(j.cu + b + 1) - base;
-    const int base2 = __ldg(j.cu2 + b), len2 = __ldg(j.cu2 + b + 1) - base2;
-    if (base < 0 || len < 0 || len > j.max_s || base + len > j.S || base2 < 0 || len2 < 0 ||
-        len2 > j.max_s2 || base2 + len2 > j.S2)
-      return;
+    len = packed_len(base, __ldg(j.cu + b + 1), j.max_s, j.S);
+    if (len < 0 || packed_len(__ldg(j.cu2 + b), __ldg(j.cu2 + b + 1), j.max_s2, j.S2) < 0) return;
     batch = 0;
     slot = static_cast<size_t>(h) * j.slots + tile_slot<true>(base, b) + tile;
   }

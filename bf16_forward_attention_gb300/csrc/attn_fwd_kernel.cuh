@@ -64,6 +64,7 @@
 
 #include <utility>
 
+#include "packed_range.h"
 #include "ptx.cuh"
 
 namespace attn {
@@ -711,11 +712,10 @@ __device__ __forceinline__ Work work_of(const Params& p, int work_item) {
     // runs (fully masked if the sequence has no key, so its rows come out NaN).
     const int b = w.batch;
     w.q_base = __ldg(p.cu_q + b);
-    w.sq = __ldg(p.cu_q + b + 1) - w.q_base;
+    w.sq = packed_len(w.q_base, __ldg(p.cu_q + b + 1), p.max_sq, p.Sq);
     w.k_base = __ldg(p.cu_k + b);
-    w.sk = __ldg(p.cu_k + b + 1) - w.k_base;
-    w.bad = w.q_base < 0 || w.sq < 0 || w.sq > p.max_sq || w.q_base + w.sq > p.Sq ||
-            w.k_base < 0 || w.sk < 0 || w.k_base + w.sk > p.Sk;
+    w.sk = packed_len(w.k_base, __ldg(p.cu_k + b + 1), p.Sk, p.Sk);
+    w.bad = w.sq < 0 || w.sk < 0;
     w.batch = 0;
     kv_tiles = w.sk > 0 ? (w.sk + kBN - 1) / kBN : 1;
   } else {
