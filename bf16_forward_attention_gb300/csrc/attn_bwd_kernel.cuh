@@ -1041,7 +1041,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // read dO once more and cost 25 us of 2.35 ms on 8K self-attention, 47 of 1039 us on a
 // packed batch, and a launch.) Rows past the end, and rows that see no key, get -Inf
 // and 0 (P = 0). A non-finite D becomes NaN: it marks a row whose dO or O has a
-// non-finite element.
+// non-finite element. A row whose keys all have the logit -Inf is NaN, as its output is.
 constexpr int kDqKStages = 3, kDqVStages = 2;  // K_j is in use while K_{j+2} loads
 constexpr int kDqChecks = 4;  // masked tiles between landing and being checked: at most 2
 enum : int {
@@ -1411,6 +1411,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lse != -__int_as_float(0x7F800000)) {
           nl = -lse * 1.4426950408889634f;
           nd = isfinite(dot) ? -dot : __int_as_float(0x7FC00000);
+        } else if (w.q0 + row < s.sq && limit + w.t0 * kTile > 0) {
+          nl = nd = __int_as_float(0x7FC00000);  // it sees keys, and every logit is -Inf
         }
         if (g == 0 && s.split == 0) {
           float* st = p.stats + (static_cast<size_t>(s.slot_q) + static_cast<size_t>(s.head) * p.q_slots +

@@ -258,11 +258,13 @@ int attn_fwd_varlen_lse(const void* q, const void* k, const void* v, void* out, 
  *             by the caller; its contents on entry do not matter. Calls that
  *             share a workspace must not overlap in time.
  * Written tensors and the workspace overlap nothing else. A row that sees no key
- * takes no part: its dq is 0. A hidden pair takes no part: a non-finite value in
- * a row or at a key reaches only the gradients of the pairs that see it (where the
- * exact gradient is infinite it may come out NaN). Results are bit-identical
- * from run to run: no sum depends on the order in which CTAs finish. Several
- * kernels are launched on `stream`; other errors and rules as attn_fwd_ex.
+ * takes no part: its dq is 0. (One that sees keys, all with the logit -Inf, has an lse
+ * of -Inf too, but an out of NaN: it and the keys get NaN.) A hidden pair takes no
+ * part: a non-finite value in a row or at a key reaches only the gradients of the
+ * pairs that see it (where the exact gradient is infinite it may come out NaN).
+ * Results are bit-identical from run to run: no sum depends on the order in which CTAs
+ * finish. Several kernels are launched on `stream`; other errors and rules as
+ * attn_fwd_ex.
  */
 int attn_bwd(const void* dout, const void* q, const void* k, const void* v, const void* out,
              const float* lse, void* dq, void* dk, void* dv, int layout, int64_t B, int64_t Hq,
