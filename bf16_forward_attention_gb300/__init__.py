@@ -118,6 +118,8 @@ def load_library(debug: bool | None = None) -> ctypes.CDLL:
     lib.attn_fwd_varlen_lse.restype = ci
     lib.attn_bwd.argtypes = [vp] * 9 + [ci] + [i64] * 6 + [cf, ci, ci, vp, i64, vp]
     lib.attn_bwd.restype = ci
+    lib.attn_bwd_timeout_selftest.argtypes = lib.attn_bwd.argtypes + [ctypes.c_uint64, ci]
+    lib.attn_bwd_timeout_selftest.restype = ci
     lib.attn_bwd_workspace_bytes.argtypes = [i64] * 6
     lib.attn_bwd_workspace_bytes.restype = i64
     lib.attn_bwd_varlen.argtypes = [vp] * 11 + [i64] * 8 + [cf, ci, ci, vp, i64, vp]

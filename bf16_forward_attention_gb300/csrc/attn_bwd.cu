@@ -156,7 +156,8 @@ int bwd_impl(const void* dout, const void* q, const void* k, const void* v, cons
              const float* lse, void* dq, void* dk, void* dv, const int32_t* cu_q, const int32_t* cu_k,
              int layout, int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int64_t Sk, int64_t max_sq,
              int64_t max_sk, int64_t d, float scale, int rounding_mode, int flags, void* workspace,
-             int64_t workspace_bytes, void* stream) {
+             int64_t workspace_bytes, void* stream, unsigned long long timeout_ns = kTimeoutNs,
+             int withhold = -1) {
   const bool varlen = cu_q != nullptr;
   // ---- host-side validation (nothing is launched on failure)
   if (!dout || !q || !k || !v || !out || !lse || !dq || !dk || !dv || !workspace)
@@ -225,7 +226,7 @@ int bwd_impl(const void* dout, const void* q, const void* k, const void* v, cons
   p.mode = rounding_mode;
   p.c = scale * 1.4426950408889634f;
   p.scale = scale;
-  p.timeout_ns = kTimeoutNs;
+  p.timeout_ns = timeout_ns;
   p.cu_q = cu_q;
   p.cu_k = cu_k;
   p.max_sq = static_cast<int>(max_sq);
@@ -245,6 +246,7 @@ int bwd_impl(const void* dout, const void* q, const void* k, const void* v, cons
   p.BH = static_cast<int>(B * Hq);
   p.n_tiles = static_cast<int>(pl.q_tiles);
   p.n_splits = pl.dq_splits;
+  p.withhold = withhold == 0;
   place(&p, causal ? heads_together(B * Hq, 512 * keys_per_head * Hkv / Hq) : 1, Hq);
   p.part = dq_part;
   if (!launch(kDq[variant_of(causal, varlen, pl.dq_long)], B * Hq * pl.q_tiles * pl.dq_splits, attn::kThreads,
@@ -254,6 +256,7 @@ int bwd_impl(const void* dout, const void* q, const void* k, const void* v, cons
   p.BH = static_cast<int>(B * Hkv);
   p.n_tiles = static_cast<int>(pl.k_tiles);
   p.n_splits = pl.dkv_splits;
+  p.withhold = withhold == 1;
   place(&p, causal ? heads_together(B * Hkv, 512 * rows_per_head * (Hq / Hkv)) : 1, Hkv);
   p.part = dkv_part;
   if (!launch(kDkv[variant_of(causal, varlen, pl.dkv_long)], B * Hkv * pl.k_tiles * pl.dkv_splits,
@@ -334,6 +337,16 @@ int attn_bwd_varlen(const void* dout, const void* q, const void* k, const void* 
   return bwd_impl(dout, q, k, v, out, lse, dq, dk, dv, cu_seqlens_q, cu_seqlens_k, ATTN_LAYOUT_BSHD, B, Hq, Hkv,
                   total_q, total_k, max_seqlen_q, max_seqlen_k, d, scale, rounding_mode, flags, workspace,
                   workspace_bytes, stream);
+}
+
+int attn_bwd_timeout_selftest(const void* dout, const void* q, const void* k, const void* v, const void* out,
+                              const float* lse, void* dq, void* dk, void* dv, int layout, int64_t B,
+                              int64_t Hq, int64_t Hkv, int64_t Sq, int64_t Sk, int64_t d, float scale,
+                              int rounding_mode, int flags, void* workspace, int64_t workspace_bytes,
+                              void* stream, uint64_t timeout_ns, int kernel) {
+  if (timeout_ns < 1 || timeout_ns > kTimeoutNs || kernel < 0 || kernel > 1) return ATTN_ERR_INVALID_ARG;
+  return bwd_impl(dout, q, k, v, out, lse, dq, dk, dv, nullptr, nullptr, layout, B, Hq, Hkv, Sq, Sk, Sq, Sk, d,
+                  scale, rounding_mode, flags, workspace, workspace_bytes, stream, timeout_ns, kernel);
 }
 
 int64_t attn_bwd_varlen_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t total_q, int64_t total_k,

@@ -95,6 +95,7 @@ struct BwdParams {
   int layout, mode;
   float c, scale;          // c = scale * log2(e)
   unsigned long long timeout_ns;
+  int withhold;            // self-test: the first S is waited for once more than it is announced
   const int* cu_q;         // packed batch: B + 1 offsets each (else null)
   const int* cu_k;
   int max_sq, max_sk;
@@ -663,6 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(bar(i), (i == kDkvPHalf || i == kDkvPFull || i == kDkvDsFull || i == kDkvAccFree || i == kDkvMeet)
                                  ? 8
                              : i >= kDkvItemEmpty ? item_readers(kCheck)
+                             : i == kDkvSFull     ? 1 + p.withhold
                                                   : 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
@@ -1128,6 +1130,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(bar(i), (i == kDqDsFull || i == kDqAccFree || i == kDqMeet) ? 8
                              : i >= kDqItemEmpty                                 ? item_readers(kCheck)
                              : i == kDqQFree                                     ? 2
+                             : i == kDqSFull                                     ? 1 + p.withhold
                                                                                  : 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();

@@ -490,6 +490,20 @@ int attn_fwd_timeout_selftest(const void* q, const void* k, const void* v, void*
                               int64_t B, int64_t H, int64_t Sq, int64_t Sk, int64_t d, float scale,
                               int rounding_mode, void* stream, uint64_t timeout_ns, int flags);
 
+/*
+ * attn_bwd_timeout_selftest - the same for the backward pass: arguments, checks and
+ * launches of attn_bwd, plus the wait limit and which kernel waits for one signal more
+ * than it sends (0: the one that forms dq, 1: the one that forms dk and dv). That kernel
+ * gives up; what it would have written, and what is formed from it afterwards, is
+ * undefined (its own results are left as they were where no tile is shared between
+ * CTAs), and attn_fwd_last_error() reports ATTN_ERR_TIMEOUT.
+ */
+int attn_bwd_timeout_selftest(const void* dout, const void* q, const void* k, const void* v, const void* out,
+                              const float* lse, void* dq, void* dk, void* dv, int layout, int64_t B,
+                              int64_t Hq, int64_t Hkv, int64_t Sq, int64_t Sk, int64_t d, float scale,
+                              int rounding_mode, int flags, void* workspace, int64_t workspace_bytes,
+                              void* stream, uint64_t timeout_ns, int kernel);
+
 /* Library version, as MAJOR*10000 + MINOR*100 + PATCH. */
 int attn_fwd_version(void);
 
