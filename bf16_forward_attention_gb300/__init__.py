@@ -413,11 +413,15 @@ def _workspace_of(lib, entry: str, device: int, *sizes: int) -> int:
 
 
 def _stream_of(t) -> int:
-    """The raw handle of the current stream of t's device (torch.cuda.current_stream wraps it
-    in an object first: 2.8 us of a small call's 35)."""
+    """The raw handle of the current stream of t's device. torch.cuda.current_stream wraps it in
+    an object first (2.8 us of a small call's 35), so the call beneath it is taken, where this
+    torch has it: it is not part of torch's public interface."""
     import torch
 
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return torch.cuda.current_stream(t.device).cuda_stream
+    return raw(t.get_device())
 
 
 def _here() -> int:
