@@ -60,7 +60,7 @@ struct Plan {
   int64_t rows, rows_pad;  // packed rows of a kv head
   int64_t block_rows;      // of a block of the own keys' kernel, at most 32
   int64_t blocks;          // blocks per (sequence, kv head)
-  int64_t prefix_blocks;   // few packed rows: blocks per kv head against the prefix; else 0
+  bool prefix_here;        // few packed rows: the own keys' kernel takes the prefix as well
   int prefix_splits, own_splits;
   int64_t packed_bytes, o_bytes, rl_bytes;
   int64_t bytes() const { return packed_bytes + o_bytes + rl_bytes; }
@@ -95,13 +95,12 @@ bool make_plan(Plan* pl, int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int64_t
   if (cut_short && s < parts_of(cap)) s = parts_of(cap);
   if (s > 64) s = 64;
   pl->own_splits = static_cast<int>(s);
-  pl->prefix_blocks = 0;
+  pl->prefix_here = Sp > 0 && pl->rows <= pre::kMaxRows;
   pl->prefix_splits = 0;
-  if (Sp > 0 && pl->rows <= pre::kMaxRows) {
+  if (pl->prefix_here) {
     // All packed rows of a kv head fit one block: the kernel of the own keys takes the
     // prefix as well, in the same launch, read once. (The fused kernel's 256-row items
     // would be nearly empty, and it needs the rows packed first.)
-    pl->prefix_blocks = 1;
     int64_t n = (2 * sms + Hkv - 1) / Hkv;
     const int64_t cut = (Sp + 255) / 256;
     if (n > cut) n = cut;
@@ -132,7 +131,7 @@ bool make_plan(Plan* pl, int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int64_t
     }
   }
   const int64_t parts = pl->prefix_splits + pl->own_splits;
-  pl->packed_bytes = Sp > 0 && pl->prefix_blocks == 0 ? up256(pl->rows * Hkv * 256) : 0;
+  pl->packed_bytes = Sp > 0 && !pl->prefix_here ? up256(pl->rows * Hkv * 256) : 0;
   pl->o_bytes = parts * Hkv * pl->rows_pad * attn::kD * 4;
   pl->rl_bytes = parts * Hkv * pl->rows_pad * 8;
   return true;
@@ -216,7 +215,7 @@ int attn_fwd_prefix(const void* q, const void* k_prefix, const void* v_prefix, c
   p.seqlens = seqlens;
   p.kp = static_cast<const uint16_t*>(k_prefix);
   p.vp = static_cast<const uint16_t*>(v_prefix);
-  const bool fused_prefix = Sp > 0 && pl.prefix_blocks == 0;
+  const bool fused_prefix = Sp > 0 && !pl.prefix_here;
   p.beside_prefix = fused_prefix ? 1 : 0;
   p.part_o = part_o;
   p.part_rl = part_rl;
@@ -234,8 +233,7 @@ int attn_fwd_prefix(const void* q, const void* k_prefix, const void* v_prefix, c
   p.own_splits = pl.own_splits;
   p.own_blocks = static_cast<int>(pl.blocks);
   p.prefix_splits = pl.prefix_splits;
-  p.prefix_blocks = static_cast<int>(pl.prefix_blocks);
-  const int64_t prefix_items = Hkv * pl.prefix_blocks * pl.prefix_splits;
+  const int64_t prefix_items = pl.prefix_here ? Hkv * pl.prefix_splits : 0;
   p.prefix_items = static_cast<int>(prefix_items);
   p.c = scale * 1.4426950408889634f;
   if (fused_prefix) {

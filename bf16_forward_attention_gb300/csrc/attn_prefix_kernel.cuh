@@ -36,7 +36,7 @@ struct OwnParams {
   const uint16_t* q;
   const uint16_t* k;       // caches: (B, cap, Hkv, 128) or (B, Hkv, cap, 128)
   const uint16_t* v;
-  const uint16_t* kp;      // the prefix, when its rows are few (prefix_blocks > 0)
+  const uint16_t* kp;      // the prefix, when its rows are few (prefix_items > 0)
   const uint16_t* vp;
   const int* seqlens;      // keys of each sequence, 0..cap
   int beside_prefix;       // the launch before this one is the prefix product
@@ -46,9 +46,9 @@ struct OwnParams {
   int rows;                // B * Sq * group: packed rows of a kv head
   int rows_pad;
   int own_splits, own_blocks;        // blocks of block_rows rows per (sequence, kv head)
-  int prefix_splits, prefix_blocks;  // the same of packed rows, per kv head
+  int prefix_splits;
   int block_rows;          // at most 8 * kNT
-  int prefix_items;                  // the grid's first blocks: prefix
+  int prefix_items;        // the grid's first blocks: prefix, all packed rows of a kv head each
   float c;                 // scale * log2(e)
 };
 
@@ -135,11 +135,9 @@ __global__ void __launch_bounds__(kOwnThreads, 2) attn_prefix_own(const OwnParam
     if (item < p.prefix_items) {
       n_splits = p.prefix_splits;
       split = item % n_splits;
-      item /= n_splits;
-      const int block = item % p.prefix_blocks;
-      kvh = item / p.prefix_blocks;
-      first = block * p.block_rows;
-      n_rows = min(p.block_rows, p.rows - first);
+      kvh = item / n_splits;
+      first = 0;
+      n_rows = p.rows;
       len = min_lim = max_lim = p.Sp;
       part = split;
       const size_t at = (p.layout == 0 ? static_cast<size_t>(kvh) * p.Sp : static_cast<size_t>(kvh)) * kD;
