@@ -165,13 +165,15 @@ __global__ void __launch_bounds__(kOwnThreads, 2) attn_prefix_own(const OwnParam
       vb = p.v + at;
     }
   }
+  dbg_ok(kvh >= 0 && kvh < p.Hkv && first >= 0 && n_rows >= 1 && n_rows <= 8 * kNT && first + n_rows <= p.rows &&
+         part < p.prefix_splits + p.own_splits);
   // ---- queries: into shared memory.
   const uint32_t qs = ptx::smem_u32(smem_own) + kOwnOffQ;
 #pragma unroll
   for (int it = 0; it < kNT; ++it) {
     const int r = it * 8 + (threadIdx.x >> 4), c = threadIdx.x & 15;
     uint4 x = make_uint4(0, 0, 0, 0);
-    if (r < n_rows)
+    if (r < n_rows && dbg_ok(first + r < p.rows))
       x = __ldg(reinterpret_cast<const uint4*>(
                     p.q + query_at(p.layout, p.Hq, p.Sq, p.group, kvh, first + r)) + c);
     ptx::st_shared_v4(qs + kv_at(r, c), x.x, x.y, x.z, x.w);
@@ -197,6 +199,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) attn_prefix_own(const OwnParam
   const int half = lane >> 4, chunk = lane & 15;
   const uint32_t lane_dst = ring + kv_at(half, chunk);  // keys 2 u + half: + 512 u, chunk turned by 2 u
   auto load = [&](int t, int s) {
+    if (!dbg_ok(t >= 0 && t * kKeys < len && len <= (own ? p.cap : p.Sp))) return;
     const int key = t * kKeys + half;
     const size_t at = key * key_stride + 8 * chunk;
     const uint16_t *ks = kb + at, *vs = vb + at;
@@ -429,6 +432,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) attn_prefix_own(const OwnParam
   const float* all_ml = reinterpret_cast<const float*>(smem_own + kOwnOffMl);
   const size_t row_base = (static_cast<size_t>(part) * p.Hkv + kvh) * p.rows_pad + first;
   for (int r = warp; r < n_rows; r += kWarps) {
+    if (!dbg_ok(first + r < p.rows_pad)) continue;
     float2 ml4[kWarps];
     float M = neg_inf;
 #pragma unroll
@@ -478,6 +482,7 @@ __global__ void __launch_bounds__(32 * kJoinRows) attn_prefix_join(const JoinPar
   const int kvh = static_cast<int>(x / p.rows), r = static_cast<int>(x % p.rows);
   const int tok = r / p.group, h = kvh * p.group + r % p.group;
   const int b = tok / p.Sq, i = tok % p.Sq;
+  if (!dbg_ok(h < p.Hq && static_cast<long long>(b) * p.Sq * p.group < p.rows && p.n_parts <= kMaxParts)) return;
   const int len = __ldg(p.seqlens + b);
   if (len < 0 || len > p.cap) return;  // reported by attn_prefix_own
   const float neg_inf = -__int_as_float(0x7F800000);
