@@ -434,7 +434,8 @@ def _here() -> int:
 def attn_fwd_lse(q, k, v, *, causal: bool = False, layout: str = "bhsd",
                  scale: float | None = None, rounding: str = "rtne", out=None, lse=None):
     """attn_fwd_ex that also returns each query row's log-sum-exp: (out, lse), lse
-    fp32 of shape (B, Hq, Sq) in either layout. ``attn_bwd`` takes both."""
+    fp32 of shape (B, Hq, Sq) in either layout. ``attn_bwd`` takes both. Like every call here it
+    records nothing for torch's autograd: the gradients are what ``attn_bwd`` returns."""
     import torch
 
     if layout not in LAYOUTS or rounding not in ROUNDINGS:
@@ -525,7 +526,8 @@ def attn_bwd(dout, q, k, v, out, lse, *, causal: bool = False, layout: str = "bh
              scale: float | None = None, rounding: str = "rtne", dq=None, dk=None, dv=None,
              workspace=None):
     """Gradients (dq, dk, dv) of ``out, lse = attn_fwd_lse(q, k, v, ...)`` for the
-    output's gradient ``dout``, with the forward call's causal, layout and scale.
+    output's gradient ``dout`` (none is taken of lse), with the forward call's causal,
+    layout and scale.
 
     ``workspace``: a CUDA tensor of at least ``bwd_workspace_bytes(...)`` bytes;
     allocated here if not given (the C entry point itself never allocates)."""

@@ -560,7 +560,7 @@ __device__ __forceinline__ void dq_ds(uint32_t tP, uint32_t tS, uint64_t nd2, in
 // and dP have two buffers, but an N = 64 product runs at two thirds of the rate.
 // Shared memory is full as well: K, V, three stages of Q and two of dO. Q_i is read last
 // (dK_i) shortly before S_{i+2} wants Q_{i+2}: with two stages its refill had 1024 cycles, and
-// takes some 1600 when every SM streams at L2's limit; dO has slack.
+// takes some 1600 when every SM streams; dO has slack.
 constexpr int kDkvQStages = 3, kDkvOStages = 2;
 enum : int {
   kDkvKV = 0,
@@ -1032,10 +1032,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // [256,384), dQ [384,512). With two S buffers the tensor pipe forms S_{j+1} and
 // dP_{j+1} around dQ_j, and a turn of the softmax (exponentials of S_{j+1}, then
 // dS once dP_{j+1} is there) has 1536 tensor cycles. Bound by the tensor cores: 1,840 cycles a
-// tile pair (8192 x 8192, 32 heads: 0.87 ms); the streamed 64 KiB a step are near what L2
-// gives every SM at once (34 bytes a clock), yet sharing them by TMA multicast between
-// two CTAs of a cluster was slower (2.39 against 2.28 ms for the whole pass: both wait for
-// the slower one at every tile).
+// tile pair (8192 x 8192, 32 heads: 0.87 ms). It streams 64 KiB in those, 36 bytes a clock (9.9
+// TB/s from L2, 27% of what that path can carry), and a copy without the loads takes as long;
+// sharing them by TMA multicast between two CTAs of a cluster was slower (2.39 against 2.28 ms
+// for the whole pass: both wait for the slower one at every tile).
 //
 // It also leaves the row statistics that dkv reads: per query row -lse log2(e) and -D,
 // D = sum_c dO_ic O_ic, formed from the dO tile it has and the O tile, which passes

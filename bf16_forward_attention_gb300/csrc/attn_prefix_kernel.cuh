@@ -113,7 +113,8 @@ __global__ void __launch_bounds__(kPackThreads) attn_prefix_pack(const PackParam
 // fused kernel. Bound by HBM where ranges are long (256 caches of up to 2048 keys, 8 kv heads,
 // 1.1 GB: 165 us, 6.7 TB/s; an SM by itself takes 62 GB/s, so beside the prefix product it
 // needs 105 of them for that); a short one is bound by the latency of its first loads and
-// the instructions around the loop, kept few for that.
+// the instructions around the loop, kept few for that. 25 to 32 rows a block take all 255
+// registers and spill 80 bytes.
 // The products' fp32 accumulation truncates, and a warp takes a quarter of a part's keys: with
 // O^T as the accumulator throughout, 99.5% of outputs over 131072 unit-normal keys a part came
 // within one unit in the last place, 99.88% over 32768 and 99.96% over 16384. kFold: a tile's

@@ -223,8 +223,8 @@ int attn_fwd_varlen(const void* q, const void* k, const void* v, void* out,
  *          at h*total_q + token (tokens of no sequence are left as they were).
  *          A row that sees no key: -Inf; a row with a NaN or +Inf logit: NaN.
  *   flags  0 or ATTN_FLAG_CAUSAL.
- * out has the bits that attn_fwd_ex / attn_fwd_varlen give. Other arguments,
- * ownership and errors as there.
+ * out has the bits that attn_fwd_ex / attn_fwd_varlen give. attn_bwd takes no
+ * gradient of lse itself. Other arguments, ownership and errors as there.
  */
 int attn_fwd_lse(const void* q, const void* k, const void* v, void* out, float* lse, int layout,
                  int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int64_t Sk, int64_t d, float scale,
@@ -281,7 +281,9 @@ int64_t attn_bwd_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq,
  *   dq like q; dk, dv like k. Tokens of no sequence are left as they were; a
  *   sequence without queries gets dk = dv = 0, one without keys dq = 0.
  *   max_seqlen_q, max_seqlen_k  upper bounds on every sequence's lengths; they size
- *                               the grids
+ *                               the grids, and where one is above 32768 rows (times
+ *                               the group for queries) the workspace, which then has
+ *                               room for fp32 sums of the longest items
  * Invalid offsets are found on the device as in attn_fwd_varlen: that sequence's
  * gradients are left unwritten and attn_fwd_last_error() reports
  * ATTN_ERR_SEQLENS. Other arguments as attn_bwd.
@@ -466,7 +468,8 @@ int attn_fwd_debug_selftest(const void* q, const void* k, const void* v, void* o
  * ATTN_ERR_TIMEOUT if some launch gave up on a wait that did not finish within
  * its time limit (the kernel then stops its work, waits for its own copies in
  * flight, frees its tensor memory and returns; its output is undefined); else
- * ATTN_ERR_SEQLENS if an attn_fwd_varlen launch found invalid offsets; else
+ * ATTN_ERR_SEQLENS if a call on a packed batch found invalid offsets, or a
+ * shared-prefix call an invalid length; else
  * ATTN_ERR_DEBUG_CHECK if a debug-build check failed.
  * Reading clears the status. Synchronize the stream that ran the calls first.
  */
