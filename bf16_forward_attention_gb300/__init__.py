@@ -32,8 +32,10 @@ ATTN_ERR_TOO_LARGE = -9
 ATTN_ERR_SCRATCH = -10
 ATTN_ERR_SEQLENS = -11
 ATTN_ERR_DEBUG_CHECK = -12
+ATTN_ERR_INDEX = -13
 ATTN_FLAG_CAUSAL = 1
 ATTN_FLAG_SPLIT_TAIL = 2
+ATTN_FLAG_INTERLEAVED = 4
 
 _libs: dict = {}
 
@@ -130,6 +132,14 @@ def load_library(debug: bool | None = None) -> ctypes.CDLL:
     lib.attn_fwd_prefix.restype = ci
     lib.attn_fwd_prefix_workspace_bytes.argtypes = [i64] * 7
     lib.attn_fwd_prefix_workspace_bytes.restype = i64
+    lib.attn_qk_norm_rope.argtypes = [vp] * 13 + [i64] * 7 + [cf, ci, ci, vp]
+    lib.attn_qk_norm_rope.restype = ci
+    lib.attn_qk_norm_rope_paged.argtypes = [vp] * 16 + [ci] + [i64] * 10 + [cf, ci, ci, vp]
+    lib.attn_qk_norm_rope_paged.restype = ci
+    lib.attn_qk_norm_rope_bwd.argtypes = [vp] * 19 + [i64] * 7 + [cf, ci, ci, vp, i64, vp]
+    lib.attn_qk_norm_rope_bwd.restype = ci
+    lib.attn_qk_norm_rope_bwd_workspace_bytes.argtypes = [i64] * 5
+    lib.attn_qk_norm_rope_bwd_workspace_bytes.restype = i64
     _libs[debug] = lib
     return lib
 
@@ -666,6 +676,206 @@ def attn_fwd_prefix(q, k_prefix, v_prefix, k, v, seqlens, *, causal: bool = Fals
     return out, lse
 
 
+@functools.lru_cache(maxsize=4096)
+def _strides(batch: int, token: int, head: int):
+    """Three strides as the C entry points read them (kept: making the array costs more than the
+    check of a small call's tensor)."""
+    return (ctypes.c_int64 * 3)(batch, token, head)
+
+
+def _rows_of(name, t, layout, device=None):
+    """(B, S, H, strides) of a bf16 CUDA tensor of rows of 128: (tokens, heads, 128), or 4-D in
+    `layout`, with any strides of tokens and heads."""
+    import torch
+
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda:
+        raise TypeError(f"{name} must be a bf16 CUDA tensor")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name} must be on q's device")
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 4:
+        if layout == "bshd":
+            B, S, H, _ = shape
+            at = _strides(stride[0], stride[1], stride[2])
+        else:
+            B, H, S, _ = shape
+            at = _strides(stride[0], stride[2], stride[1])
+    elif len(shape) == 3:
+        B, (S, H, _) = 1, shape
+        at = _strides(0, stride[0], stride[1])
+    else:
+        raise ValueError(f"{name} must be (tokens, heads, d) or 4-D")
+    if stride[-1] != 1 and shape[-1] != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return B, S, H, at
+
+
+def _rows_out(name, out, like, layout, device):
+    """An output of rows as given, or a new one shaped like `like`; with its strides."""
+    import torch
+
+    if out is None:
+        out = torch.empty(like.shape, dtype=torch.bfloat16, device=like.device)
+    elif not isinstance(out, torch.Tensor) or out.shape != like.shape:
+        raise ValueError(f"{name} must be a bf16 CUDA tensor of shape {tuple(like.shape)}")
+    return out, _rows_of(name, out, layout, device)[3]
+
+
+def _check_rope(q, k, q_weight, k_weight, cos, sin, positions, layout, rounding):
+    """Checks what the norm-and-rotation calls share; (B, S, Hq, Hkv, D, max_pos, rotary_dim,
+    q's strides, k's strides)."""
+    import torch
+
+    if layout not in LAYOUTS or rounding not in ROUNDINGS:
+        raise ValueError("unknown layout or rounding mode")
+    B, S, Hq, q_at = _rows_of("q", q, layout)
+    device = q.get_device()
+    Bk, Sk, Hkv, k_at = _rows_of("k", k, layout, device)
+    D = q.shape[-1]
+    if (Bk, Sk, k.shape[-1]) != (B, S, D) or q.dim() != k.dim():
+        raise ValueError("shape mismatch")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if (not isinstance(w, torch.Tensor) or w.dtype != torch.bfloat16 or tuple(w.shape) != (D,)
+                or not w.is_contiguous() or w.get_device() != device):
+            raise ValueError(f"{name} must be a contiguous bf16 tensor of {D} entries on q's device")
+    for name, t in (("cos", cos), ("sin", sin)):
+        if (not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.dim() != 2 or not t.is_contiguous()
+                or t.shape != cos.shape or t.get_device() != device):
+            raise ValueError(f"{name} must be a contiguous fp32 tensor of shape (max_pos, rotary_dim / 2) on q's device")
+    _check_per_token("positions", positions, B, S, q.dim(), device)
+    return B, S, Hq, Hkv, D, cos.shape[0], 2 * cos.shape[1], q_at, k_at
+
+
+def _check_per_token(name, t, B, S, dim, device):
+    import torch
+
+    if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.get_device() != device
+            or tuple(t.shape) != ((S,) if dim == 3 else (B, S)) or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 tensor with an entry for each token, on q's device")
+
+
+def attn_qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, *, eps: float = 1e-6,
+                      interleaved: bool = False, layout: str = "bhsd", rounding: str = "rtne",
+                      q_out=None, k_out=None):
+    """Each head's queries and keys RMS-normed, weighted and rotated by position, in one pass:
+    (q_out, k_out), what attn_fwd and its relatives take.
+
+    bf16 CUDA tensors: q (tokens, Hq, 128) and k (tokens, Hkv, 128), or 4-D in ``layout``, in
+    place wherever their rows lie (views of one projection's output, say); q_weight and k_weight
+    128 entries; cos and sin fp32 (max_pos, rotary_dim / 2); positions int32, (tokens,) or (B, S).
+    ``interleaved``: a pair is columns (2i, 2i + 1) instead of (i, i + rotary_dim / 2).
+    q_out may be q and k_out k. A position outside 0..max_pos-1 is found on the device: check
+    ``attn_fwd_last_error()`` after a sync. The gradients are what ``attn_qk_norm_rope_bwd``
+    returns."""
+    B, S, Hq, Hkv, D, max_pos, rot, q_at, k_at = _check_rope(q, k, q_weight, k_weight, cos, sin, positions, layout,
+                                                            rounding)
+    device = q.get_device()
+    with _on_device(q.device):
+        q_out, qo_at = _rows_out("q_out", q_out, q, layout, device)
+        k_out, ko_at = _rows_out("k_out", k_out, k, layout, device)
+        _call(load_library().attn_qk_norm_rope, q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(),
+              cos.data_ptr(), sin.data_ptr(), positions.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), q_at, k_at,
+              qo_at, ko_at, B, S, Hq, Hkv, D, max_pos, rot, float(eps), ROUNDINGS[rounding],
+              ATTN_FLAG_INTERLEAVED if interleaved else 0, _stream_of(q))
+    return q_out, k_out
+
+
+def _check_pages(k_pages, v_pages, layout, device):
+    """(n_pages, page_size, Hkv, D, page stride) of a cache's pages: 4-D bf16 tensors whose pages
+    are dense and may lie apart (halves of one tensor, layers of one)."""
+    import torch
+
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda:
+            raise TypeError(f"{name} must be a bf16 CUDA tensor")
+        if t.get_device() != device:
+            raise ValueError(f"{name} must be on q's device")
+    shape, stride = k_pages.shape, k_pages.stride()
+    if v_pages.shape != shape or v_pages.stride() != stride or len(shape) != 4:
+        raise ValueError("k_pages and v_pages must be 4-D tensors of one shape and strides")
+    n, a, b, D = shape
+    if stride[1:] != (b * D, D, 1) and not k_pages.is_contiguous():
+        raise ValueError("a page of k_pages and v_pages must be contiguous")
+    page_size, Hkv = (a, b) if layout == "bshd" else (b, a)
+    return n, page_size, Hkv, D, stride[0] if n > 1 else a * b * D
+
+
+def attn_qk_norm_rope_paged(q, k, v, q_weight, k_weight, cos, sin, positions, slots, k_pages, v_pages, *,
+                            eps: float = 1e-6, interleaved: bool = False, layout: str = "bhsd",
+                            rounding: str = "rtne", q_out=None):
+    """``attn_qk_norm_rope`` for tokens that are added to a paged cache: the rotated keys and the
+    values v go to the cache, the rotated queries are returned.
+
+    k_pages and v_pages: bf16 CUDA tensors (n_pages, page_size, Hkv, 128) for "bshd", (n_pages,
+    Hkv, page_size, 128) for "bhsd", each page contiguous. slots: int32, one a token like
+    positions, the place page * page_size + place in the page, or -1 for a token that is not
+    stored (padding); the slots of a call differ. A slot out of range is found on the device."""
+    B, S, Hq, Hkv, D, max_pos, rot, q_at, k_at = _check_rope(q, k, q_weight, k_weight, cos, sin, positions, layout,
+                                                            rounding)
+    device = q.get_device()
+    Bv, Sv, Hv, v_at = _rows_of("v", v, layout, device)
+    n_pages, page_size, Hp, Dp, page_stride = _check_pages(k_pages, v_pages, layout, device)
+    if v.shape != k.shape or (Hp, Dp) != (Hkv, D):
+        raise ValueError("shape mismatch")
+    _check_per_token("slots", slots, B, S, q.dim(), device)
+    with _on_device(q.device):
+        q_out, qo_at = _rows_out("q_out", q_out, q, layout, device)
+        _call(load_library().attn_qk_norm_rope_paged, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_weight.data_ptr(),
+              k_weight.data_ptr(), cos.data_ptr(), sin.data_ptr(), positions.data_ptr(), slots.data_ptr(),
+              q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), q_at, k_at, v_at, qo_at, LAYOUTS[layout], B, S,
+              Hq, Hkv, n_pages, page_size, page_stride, D, max_pos, rot, float(eps), ROUNDINGS[rounding],
+              ATTN_FLAG_INTERLEAVED if interleaved else 0, _stream_of(q))
+    return q_out
+
+
+def qk_norm_rope_bwd_workspace_bytes(B: int, S: int, Hq: int, Hkv: int, d: int = 128) -> int:
+    """Device workspace attn_qk_norm_rope_bwd needs on the current device."""
+    return _workspace_of(load_library(), "attn_qk_norm_rope_bwd_workspace_bytes", _here(), B, S, Hq, Hkv, d)
+
+
+def attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, cos, sin, positions, *, eps: float = 1e-6,
+                          interleaved: bool = False, layout: str = "bhsd", rounding: str = "rtne", dq=None,
+                          dk=None, dq_weight=None, dk_weight=None, workspace=None):
+    """Gradients (dq, dk, dq_weight, dk_weight) of ``attn_qk_norm_rope`` for the gradients dq_out
+    and dk_out of what it returned (attn_bwd's dq and dk); the weights' are fp32. dq may be dq_out
+    and dk dk_out.
+
+    ``workspace``: a CUDA tensor of at least ``qk_norm_rope_bwd_workspace_bytes(...)`` bytes;
+    allocated here if not given (the C entry point itself never allocates)."""
+    import torch
+
+    B, S, Hq, Hkv, D, max_pos, rot, q_at, k_at = _check_rope(q, k, q_weight, k_weight, cos, sin, positions, layout,
+                                                            rounding)
+    device = q.get_device()
+    gq_at, gk_at = _rows_of("dq_out", dq_out, layout, device)[3], _rows_of("dk_out", dk_out, layout, device)[3]
+    if dq_out.shape != q.shape or dk_out.shape != k.shape:
+        raise ValueError("shape mismatch")
+    lib = load_library()
+    with _on_device(q.device):
+        dq, dq_at = _rows_out("dq", dq, q, layout, device)
+        dk, dk_at = _rows_out("dk", dk, k, layout, device)
+        dws = []
+        for name, dw in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
+            if dw is None:
+                dw = torch.empty(D, dtype=torch.float32, device=q.device)
+            elif (not isinstance(dw, torch.Tensor) or dw.dtype != torch.float32 or tuple(dw.shape) != (D,)
+                  or not dw.is_contiguous() or dw.get_device() != device):
+                raise ValueError(f"{name} must be a contiguous fp32 tensor of {D} entries on q's device")
+            dws.append(dw)
+        if workspace is None:
+            workspace = torch.empty(_workspace_of(lib, "attn_qk_norm_rope_bwd_workspace_bytes", device, B, S, Hq,
+                                                  Hkv, D), dtype=torch.uint8, device=q.device)
+        else:
+            _check_workspace(workspace, q.device)
+        _call(lib.attn_qk_norm_rope_bwd, dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(),
+              q_weight.data_ptr(), k_weight.data_ptr(), cos.data_ptr(), sin.data_ptr(), positions.data_ptr(),
+              dq.data_ptr(), dk.data_ptr(), dws[0].data_ptr(), dws[1].data_ptr(), gq_at, gk_at, q_at, k_at, dq_at,
+              dk_at, B, S, Hq, Hkv, D, max_pos, rot, float(eps), ROUNDINGS[rounding],
+              ATTN_FLAG_INTERLEAVED if interleaved else 0, workspace.data_ptr(),
+              workspace.numel() * workspace.element_size(), _stream_of(q))
+    return dq, dk, dws[0], dws[1]
+
+
 def host_workspace_bytes(B: int, Hq: int, Hkv: int, Sq: int, Sk: int, d: int = 128) -> int:
     """Device workspace attn_fwd_host needs (negative: a status code)."""
     return load_library().attn_fwd_host_workspace_bytes(B, Hq, Hkv, Sq, Sk, d)
@@ -874,4 +1084,5 @@ __all__ = ["attn_fwd", "attn_fwd_raw", "attn_fwd_last_error", "attn_fwd_timeout_
            "ATTN_FLAG_CAUSAL", "ATTN_FLAG_SPLIT_TAIL", "split_tail_items",
            "attn_fwd_lse", "attn_fwd_varlen_lse", "attn_bwd", "attn_bwd_varlen",
            "bwd_workspace_bytes", "bwd_varlen_workspace_bytes", "attn_fwd_prefix",
-           "prefix_workspace_bytes"]
+           "prefix_workspace_bytes", "ATTN_ERR_INDEX", "ATTN_FLAG_INTERLEAVED", "attn_qk_norm_rope",
+           "attn_qk_norm_rope_paged", "attn_qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_bytes"]

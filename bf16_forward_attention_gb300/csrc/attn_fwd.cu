@@ -177,6 +177,7 @@ const char* attn_status_str(int status) {
     case ATTN_ERR_SCRATCH: return "split workspace needed exceeds the library's fixed 32 MiB device scratch";
     case ATTN_ERR_SEQLENS: return "invalid cu_seqlens contents (found on the device; those sequences were not computed)";
     case ATTN_ERR_DEBUG_CHECK: return "a bounds or protocol check of the debug build failed (the access it guards was skipped)";
+    case ATTN_ERR_INDEX: return "a position, slot or page number is out of range (found on the device; what it belongs to was not written)";
     default: return "unknown status";
   }
 }
@@ -645,11 +646,12 @@ int attn_fwd_debug_selftest(const void* q, const void* k, const void* v, void* o
 int attn_fwd_last_error(void) {
   unsigned int s = 0;
   if (!take_status(attn::g_attn_status, &s) || !bwd_take_status(&s) ||
-      !prefix_take_status(&s))
+      !prefix_take_status(&s) || !rope_take_status(&s))
     return ATTN_ERR_NO_DEVICE;
   if (s == 0) return ATTN_OK;
   if (s & 1u) return ATTN_ERR_TIMEOUT;
-  return (s & 2u) ? ATTN_ERR_SEQLENS : ATTN_ERR_DEBUG_CHECK;
+  if (s & 2u) return ATTN_ERR_SEQLENS;
+  return (s & 8u) ? ATTN_ERR_INDEX : ATTN_ERR_DEBUG_CHECK;
 }
 
 }  // extern "C"

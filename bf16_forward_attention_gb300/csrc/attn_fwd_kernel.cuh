@@ -180,7 +180,8 @@ struct Params {
 
 // Bit 0: some wait timed out. Bit 1: a variable-length batch's offsets were
 // invalid (that sequence's output is left unwritten). Bit 2 (debug build): a
-// bounds or protocol check failed. One word per translation unit with kernels;
+// bounds or protocol check failed. Bit 3: a position, slot or page number was out
+// of range. One word per translation unit with kernels;
 // attn_fwd_last_error reads them all.
 static __device__ unsigned int g_attn_status;
 

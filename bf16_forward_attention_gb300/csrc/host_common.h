@@ -5,11 +5,13 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <mutex>
 #include <utility>
 
 #include "attn_fwd.h"
+#include "rows.h"
 
 namespace attn_host {
 
@@ -90,6 +92,7 @@ bool take_status(Word& word, unsigned int* s) {
 }
 bool bwd_take_status(unsigned int* s);     // attn_bwd.cu
 bool prefix_take_status(unsigned int* s);  // attn_prefix.cu
+bool rope_take_status(unsigned int* s);    // attn_rope.cu
 
 // Streaming multiprocessors of the current device (152, a GB300's, where there is
 // none: size queries work without one).
@@ -101,6 +104,36 @@ inline int sms_here() {
     return 152;
   }
   return sms;
+}
+
+// ATTN_OK where the current device is one that the kernels are built for.
+inline int arch_here() {
+  static std::atomic<int> known[kMaxDevices];  // 0: not asked yet, 1: it is, negative: the status
+  int dev = -1, major = 0, minor = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    cudaGetLastError();
+    return ATTN_ERR_NO_DEVICE;
+  }
+  const int seen = known[dev].load(std::memory_order_relaxed);
+  if (seen != 0) return seen > 0 ? ATTN_OK : seen;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return ATTN_ERR_NO_DEVICE;
+  }
+  const int st = major == 10 && minor == 3 ? ATTN_OK : ATTN_ERR_ARCH;
+  known[dev].store(st == ATTN_OK ? 1 : st, std::memory_order_relaxed);
+  return st;
+}
+
+// The pages of a cache's keys and values as an entry point is given them.
+inline int check_pages(const void* k_pages, const void* v_pages, int64_t n_pages, int64_t page_size,
+                       int64_t page_stride, int64_t Hkv) {
+  if (!k_pages || !v_pages || n_pages < 1 || page_size < 1 || page_stride < 1 || Hkv < 1) return ATTN_ERR_INVALID_ARG;
+  if (!pages_in_range(n_pages, page_size, page_stride, Hkv)) return ATTN_ERR_TOO_LARGE;
+  if (n_pages > 1 && page_stride < page_size * Hkv * kRowElems) return ATTN_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(k_pages) | reinterpret_cast<uintptr_t>(v_pages)) & 15u) return ATTN_ERR_MISALIGNED;
+  return page_stride % kRowElems ? ATTN_ERR_MISALIGNED : ATTN_OK;
 }
 
 // A launch that, when `dependent`, may start while the kernel before it on the

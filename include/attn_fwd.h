@@ -56,8 +56,11 @@ enum {
   ATTN_ERR_SEQLENS = -11,    /* packed batches: invalid offsets; shared prefix:
                                 an invalid length. Found on the device and
                                 reported by attn_fwd_last_error                */
-  ATTN_ERR_DEBUG_CHECK = -12 /* debug build: a bounds or protocol check failed,
+  ATTN_ERR_DEBUG_CHECK = -12, /* debug build: a bounds or protocol check failed,
                                 reported by attn_fwd_last_error                */
+  ATTN_ERR_INDEX = -13       /* a position, cache slot or page number out of range
+                                (or a page listed twice, attn_cache_evict). Found on
+                                the device, reported by attn_fwd_last_error    */
 };
 
 /*
@@ -384,6 +387,100 @@ int attn_fwd_splitkv_noalloc(const void* q, const void* k, const void* v, void* 
                              int64_t B, int64_t H, int64_t Sq, int64_t Sk, int64_t d, float scale,
                              int rounding_mode, int num_splits, void* stream);
 
+/*
+ * attn_qk_norm_rope - what comes before attention in a layer that norms each head's
+ * queries and keys and then rotates them by position, in one pass. A row x of 128 (one
+ * head of one token at position t) becomes
+ *   u = x * weight * r,  r = (mean(x^2) + eps)^(-1/2),  and for each of rotary_dim / 2
+ *   pairs (a, b) of columns:  y_a = u_a cos - u_b sin,  y_b = u_b cos + u_a sin
+ * with cos and sin at (t, i); columns at and after rotary_dim are u. Formed in fp32 and
+ * rounded once, per rounding_mode. The pages describe attention alone and have no
+ * counterpart of these calls.
+ *
+ *   q, q_out   device, bf16, (B, S, Hq, 128);  k, k_out (B, S, Hkv, 128), each wherever
+ *              its rows lie: *_strides point to three host values, the element strides of
+ *              batch, token and head (multiples of 8, not negative; that of a dimension of
+ *              one entry is not looked at). So views of one projection's output and both
+ *              layouts of attn_fwd are taken as they are; a packed batch has B = 1.
+ *   q_weight, k_weight  device, bf16, 128 each
+ *   cos, sin   device, fp32, (max_pos, rotary_dim / 2) each
+ *   positions  device, int32, (B, S): each token's position, 0 .. max_pos - 1. A token
+ *              whose position is out of range is found on the device: nothing of it is
+ *              written and attn_fwd_last_error() reports ATTN_ERR_INDEX.
+ *   rotary_dim 16 .. 128, a multiple of 16 (otherwise ATTN_ERR_UNSUPPORTED)
+ *   eps        finite, not negative
+ *   flags      0: pair i is columns (i, i + rotary_dim / 2); ATTN_FLAG_INTERLEAVED:
+ *              columns (2i, 2i + 1)
+ * q_out may be q, and k_out k, row for row (same address and strides); otherwise an output
+ * overlaps no input and no other output (columns of the same tokens are told apart), and
+ * its rows do not overlap each other: ATTN_ERR_ALIASING. 16-byte alignment, stream and
+ * other rules as attn_fwd.
+ */
+enum { ATTN_FLAG_INTERLEAVED = 4 };
+int attn_qk_norm_rope(const void* q, const void* k, const void* q_weight, const void* k_weight,
+                      const float* cos, const float* sin, const int32_t* positions, void* q_out,
+                      void* k_out, const int64_t* q_strides, const int64_t* k_strides,
+                      const int64_t* q_out_strides, const int64_t* k_out_strides, int64_t B,
+                      int64_t S, int64_t Hq, int64_t Hkv, int64_t d, int64_t max_pos,
+                      int64_t rotary_dim, float eps, int rounding_mode, int flags, void* stream);
+
+/*
+ * attn_qk_norm_rope_paged - the same for tokens that are added to a paged cache: the
+ * rotated keys, and the values as they are, go to the cache, the rotated queries to q_out.
+ *
+ *   k_pages, v_pages  device, bf16, (n_pages, page_size, Hkv, 128) for BSHD,
+ *              (n_pages, Hkv, page_size, 128) for BHSD, pages page_stride elements apart (a
+ *              multiple of 128, at least a page; of both), dense within a page. Only the
+ *              tokens' slots are written.
+ *   slots      device, int32, (B, S): where a token's key and value go, slot = page *
+ *              page_size + place in the page; -1: nowhere (padding; its query is still
+ *              written). A slot out of range is treated as a position out of range is. The
+ *              slots of a call's tokens differ; of two tokens with one slot, which one's
+ *              values stay there (each 16 bytes for itself) is not defined.
+ *   v          device, bf16, (B, S, Hkv, 128), v_strides as k's
+ *   layout     of the pages; the tokens' rows lie where their strides say
+ * The pages overlap nothing else; keys and values may be halves of one tensor's pages.
+ */
+int attn_qk_norm_rope_paged(const void* q, const void* k, const void* v, const void* q_weight,
+                            const void* k_weight, const float* cos, const float* sin,
+                            const int32_t* positions, const int32_t* slots, void* q_out,
+                            void* k_pages, void* v_pages, const int64_t* q_strides,
+                            const int64_t* k_strides, const int64_t* v_strides,
+                            const int64_t* q_out_strides, int layout, int64_t B, int64_t S,
+                            int64_t Hq, int64_t Hkv, int64_t n_pages, int64_t page_size,
+                            int64_t page_stride, int64_t d, int64_t max_pos, int64_t rotary_dim,
+                            float eps, int rounding_mode, int flags, void* stream);
+
+/*
+ * attn_qk_norm_rope_bwd - gradients of attn_qk_norm_rope: with dy turned back by the
+ * rotation to du and dn = du * weight,
+ *   dweight = sum over tokens and heads of du * x * r,  dx = r (dn - x r mean(dn * x r)).
+ *
+ *   dq_out, dk_out  device, bf16, gradients of q_out and k_out      (read only)
+ *   q, k            as the forward call was given them              (read only)
+ *   dq, dk          device, bf16, written; dq may be dq_out and dk dk_out, row for row
+ *   dq_weight, dk_weight  device, fp32, 128 each, written
+ *   workspace       device, 16-byte aligned, attn_qk_norm_rope_bwd_workspace_bytes(...)
+ *                   bytes, owned by the caller; calls that share one must not overlap in time
+ * All six row tensors have their own strides. A token whose position is out of range adds
+ * nothing to the weights' gradients and its dq and dk are not written. Results are
+ * bit-identical from run to run. Other arguments, errors and rules as the forward call.
+ */
+int attn_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k,
+                          const void* q_weight, const void* k_weight, const float* cos,
+                          const float* sin, const int32_t* positions, void* dq, void* dk,
+                          float* dq_weight, float* dk_weight, const int64_t* dq_out_strides,
+                          const int64_t* dk_out_strides, const int64_t* q_strides,
+                          const int64_t* k_strides, const int64_t* dq_strides,
+                          const int64_t* dk_strides, int64_t B, int64_t S, int64_t Hq, int64_t Hkv,
+                          int64_t d, int64_t max_pos, int64_t rotary_dim, float eps,
+                          int rounding_mode, int flags, void* workspace, int64_t workspace_bytes,
+                          void* stream);
+
+/* Workspace bytes attn_qk_norm_rope_bwd needs on the current device, or a negative status. */
+int64_t attn_qk_norm_rope_bwd_workspace_bytes(int64_t B, int64_t S, int64_t Hq, int64_t Hkv,
+                                              int64_t d);
+
 /* Static English text for a status code (never NULL). */
 const char* attn_status_str(int status);
 
@@ -470,6 +567,7 @@ int attn_fwd_debug_selftest(const void* q, const void* k, const void* v, void* o
  * flight, frees its tensor memory and returns; its output is undefined); else
  * ATTN_ERR_SEQLENS if a call on a packed batch found invalid offsets, or a
  * shared-prefix call an invalid length; else
+ * ATTN_ERR_INDEX if a call found a position, slot or page number out of range; else
  * ATTN_ERR_DEBUG_CHECK if a debug-build check failed.
  * Reading clears the status. Synchronize the stream that ran the calls first.
  */
