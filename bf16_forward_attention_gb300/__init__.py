@@ -140,6 +140,10 @@ def load_library(debug: bool | None = None) -> ctypes.CDLL:
     lib.attn_qk_norm_rope_bwd.restype = ci
     lib.attn_qk_norm_rope_bwd_workspace_bytes.argtypes = [i64] * 5
     lib.attn_qk_norm_rope_bwd_workspace_bytes.restype = i64
+    lib.attn_fwd_paged.argtypes = [vp] * 8 + [ci] + [i64] * 9 + [cf, ci, ci, vp, i64, vp]
+    lib.attn_fwd_paged.restype = ci
+    lib.attn_fwd_paged_workspace_bytes.argtypes = [i64] * 7 + [ci]
+    lib.attn_fwd_paged_workspace_bytes.restype = i64
     _libs[debug] = lib
     return lib
 
@@ -876,6 +880,87 @@ def attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, cos, sin, po
     return dq, dk, dws[0], dws[1]
 
 
+def paged_workspace_bytes(B: int, Hq: int, Hkv: int, Sq: int, page_size: int, max_pages: int, *,
+                          with_mass: bool = False, d: int = 128) -> int:
+    """Device workspace attn_fwd_paged needs on the current device (``with_mass``: whether it is
+    given a mass)."""
+    return _workspace_of(load_library(), "attn_fwd_paged_workspace_bytes", _here(), B, Hq, Hkv, Sq, page_size,
+                         max_pages, d, int(with_mass))
+
+
+def _check_table(page_table, seqlens, device):
+    """(B, max_pages) of a page table and the lengths that go with it."""
+    import torch
+
+    for name, t, dim in (("page_table", page_table, 2), ("seqlens", seqlens, 1)):
+        if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or t.dim() != dim
+                or not t.is_contiguous()):
+            raise TypeError(f"{name} must be a contiguous {dim}-D int32 CUDA tensor")
+        if t.get_device() != device:
+            raise ValueError(f"{name} must be on the pages' device")
+    B, max_pages = page_table.shape
+    if seqlens.numel() != B:
+        raise ValueError("seqlens must have an entry for each row of page_table")
+    return B, max_pages
+
+
+def _check_mass(name, mass, shape, device):
+    import torch
+
+    if (not isinstance(mass, torch.Tensor) or mass.dtype != torch.float32 or tuple(mass.shape) != shape
+            or not mass.is_contiguous() or mass.get_device() != device):
+        raise ValueError(f"{name} must be a contiguous fp32 tensor of shape {shape} on the pages' device")
+
+
+def attn_fwd_paged(q, k_pages, v_pages, page_table, seqlens, *, causal: bool = False, layout: str = "bhsd",
+                   scale: float | None = None, rounding: str = "rtne", out=None, lse=None, mass=None,
+                   workspace=None):
+    """Attention of a batch's new tokens over a paged cache: (out, lse).
+
+    bf16 CUDA tensors, for "bshd": q (B, Sq, Hq, 128), k_pages and v_pages (n_pages, page_size,
+    Hkv, 128); for "bhsd" heads come before tokens. page_table (int32 CUDA, (B, max_pages)): key j
+    of sequence b is place j % page_size of page page_table[b, j // page_size]; seqlens (int32
+    CUDA, B) counts each sequence's keys, the new tokens' included (``attn_qk_norm_rope_paged``
+    puts them there). With ``causal`` the Sq tokens are the sequence's last and see only what is
+    before them. ``mass`` (fp32, (B, Hkv, max_pages * page_size)): every key's attention weight,
+    summed over the new tokens and the group's heads, is added to it. A length or page number out
+    of range is found on the device: check ``attn_fwd_last_error()`` after a sync."""
+    import torch
+
+    if layout not in LAYOUTS or rounding not in ROUNDINGS:
+        raise ValueError("unknown layout or rounding mode")
+    _check_bf16((("q", q),), 4, "4-D")
+    device = q.get_device()
+    B, Hq, Sq, D = _dims(q, layout)
+    n_pages, page_size, Hkv, Dp, page_stride = _check_pages(k_pages, v_pages, layout, device)
+    Bt, max_pages = _check_table(page_table, seqlens, device)
+    if (Bt, Dp) != (B, D) or Hkv < 1 or Hq % Hkv:
+        raise ValueError("shape mismatch")
+    if mass is not None:
+        _check_mass("mass", mass, (B, Hkv, max_pages * page_size), device)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check_out(out, q)
+    lse = _lse_like(lse, (B, Hq, Sq), q.device)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    lib = load_library()
+    with _on_device(q.device):
+        if workspace is None:
+            need = _workspace_of(lib, "attn_fwd_paged_workspace_bytes", device, B, Hq, Hkv, Sq, page_size, max_pages,
+                                 D, int(mass is not None))
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        else:
+            _check_workspace(workspace, q.device)
+        _call(lib.attn_fwd_paged, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+              seqlens.data_ptr(), out.data_ptr(), lse.data_ptr(), None if mass is None else mass.data_ptr(),
+              LAYOUTS[layout], B, Hq, Hkv, Sq, n_pages, page_size, page_stride, max_pages, D, float(scale),
+              ROUNDINGS[rounding], ATTN_FLAG_CAUSAL if causal else 0, workspace.data_ptr(),
+              workspace.numel() * workspace.element_size(), _stream_of(q))
+    return out, lse
+
+
 def host_workspace_bytes(B: int, Hq: int, Hkv: int, Sq: int, Sk: int, d: int = 128) -> int:
     """Device workspace attn_fwd_host needs (negative: a status code)."""
     return load_library().attn_fwd_host_workspace_bytes(B, Hq, Hkv, Sq, Sk, d)
@@ -1085,4 +1170,5 @@ __all__ = ["attn_fwd", "attn_fwd_raw", "attn_fwd_last_error", "attn_fwd_timeout_
            "attn_fwd_lse", "attn_fwd_varlen_lse", "attn_bwd", "attn_bwd_varlen",
            "bwd_workspace_bytes", "bwd_varlen_workspace_bytes", "attn_fwd_prefix",
            "prefix_workspace_bytes", "ATTN_ERR_INDEX", "ATTN_FLAG_INTERLEAVED", "attn_qk_norm_rope",
-           "attn_qk_norm_rope_paged", "attn_qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_bytes"]
+           "attn_qk_norm_rope_paged", "attn_qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_bytes",
+           "attn_fwd_paged", "paged_workspace_bytes"]

@@ -22,7 +22,7 @@ __device__ __forceinline__ uint32_t row_at(int r, int c) {
 
 // Keys of its own sequence that query token i of Sq sees, of `len`.
 __device__ __forceinline__ int own_limit(int i, int len, int Sq, int causal) {
-  return causal ? max(0, min(len, i + len - Sq + 1)) : len;
+  return causal ? max(0, len - (Sq - 1 - i)) : len;
 }
 
 // Row r of a (sequence, kv head)'s Sq * group rows, tokens first: element offset of its

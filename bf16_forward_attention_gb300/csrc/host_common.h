@@ -93,6 +93,7 @@ bool take_status(Word& word, unsigned int* s) {
 bool bwd_take_status(unsigned int* s);     // attn_bwd.cu
 bool prefix_take_status(unsigned int* s);  // attn_prefix.cu
 bool rope_take_status(unsigned int* s);    // attn_rope.cu
+bool paged_take_status(unsigned int* s);   // attn_paged.cu
 
 // Streaming multiprocessors of the current device (152, a GB300's, where there is
 // none: size queries work without one).
@@ -139,10 +140,10 @@ inline int check_pages(const void* k_pages, const void* v_pages, int64_t n_pages
 // A launch that, when `dependent`, may start while the kernel before it on the
 // stream drains: its kernel waits on the device for what it reads.
 template <typename... Params, typename... Args>
-bool launch(void (*fn)(Params...), int64_t grid, int threads, int smem, cudaStream_t stream, bool dependent,
+bool launch(void (*fn)(Params...), dim3 grid, int threads, int smem, cudaStream_t stream, bool dependent,
             Args&&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -154,6 +155,12 @@ bool launch(void (*fn)(Params...), int64_t grid, int threads, int smem, cudaStre
   if (cudaLaunchKernelEx(&cfg, fn, std::forward<Args>(args)...) == cudaSuccess) return true;
   cudaGetLastError();
   return false;
+}
+
+template <typename... Params, typename... Args>
+bool launch(void (*fn)(Params...), int64_t grid, int threads, int smem, cudaStream_t stream, bool dependent,
+            Args&&... args) {
+  return launch(fn, dim3(static_cast<unsigned>(grid)), threads, smem, stream, dependent, std::forward<Args>(args)...);
 }
 
 // attn_fwd.cu: the split form of the fused kernel without its merge. Each of

@@ -481,6 +481,56 @@ int attn_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q,
 int64_t attn_qk_norm_rope_bwd_workspace_bytes(int64_t B, int64_t S, int64_t Hq, int64_t Hkv,
                                               int64_t d);
 
+/*
+ * attn_fwd_paged - attention of a batch's new tokens over a paged key-value cache: the
+ * keys and values of sequence b are in the pages that its row of the page table lists.
+ * Serving attention with caches is among what the pages' kernel lacks (snilld.dk,
+ * "Autoregressiv serving, de praktiske hager"); the pages have no counterpart of this call.
+ *
+ *   q, out     device, bf16, (B, Sq, Hq, 128) for BSHD, (B, Hq, Sq, 128) for BHSD:
+ *              Sq new tokens per sequence (1 when sampling token by token)
+ *   k_pages, v_pages  device, bf16, as attn_qk_norm_rope_paged: (n_pages, page_size, Hkv,
+ *              128) for BSHD, (n_pages, Hkv, page_size, 128) for BHSD, pages page_stride
+ *              elements apart; any page_size >= 1
+ *   page_table device, int32, (B, max_pages): key j of sequence b is place j % page_size
+ *              of page page_table[b][j / page_size]. Entries past a sequence's last key are
+ *              not looked at; a page may be listed any number of times. A number outside
+ *              0 .. n_pages - 1 among the others is found on the device: that sequence's
+ *              results are left unwritten, its masses as they were, and
+ *              attn_fwd_last_error() reports ATTN_ERR_INDEX.
+ *   seqlens    device, int32, B entries: keys of each sequence, 0 .. max_pages * page_size,
+ *              the new tokens' included. A length outside that range: that sequence's
+ *              results are left unwritten and attn_fwd_last_error() reports ATTN_ERR_SEQLENS.
+ *   lse        device, fp32, (B, Hq, Sq), written: each row's log-sum-exp
+ *   mass       device, fp32, (B, Hkv, max_pages * page_size), or NULL: added to it, for every
+ *              key, its attention weight summed over the sequence's Sq tokens and the query
+ *              heads of the group, exp(scale q.k - lse). Entries at and after a sequence's
+ *              length are left as they are; a row that sees no key adds nothing. (What
+ *              attn_cache_evict goes by.)
+ *   flags      0: a query sees all its sequence's keys; ATTN_FLAG_CAUSAL: query i sees key
+ *              j iff j <= i + seqlens[b] - Sq (the Sq new tokens are the sequence's last)
+ *   workspace  device, 16-byte aligned, attn_fwd_paged_workspace_bytes(...) bytes, owned by
+ *              the caller; calls that share one must not overlap in time. With a mass it
+ *              holds every logit (4 bytes a row and key of the whole table).
+ * A row that sees no key comes out NaN, lse -Inf. out holds attn_fwd's numerics contract.
+ * Results are bit-identical from run to run; the keys are cut into parts by all sequences'
+ * lengths, so a row's last bits may depend on the others' lengths, not on their values.
+ * Hidden keys take no part. Meant for few new tokens per sequence: their rows go through the
+ * keys 32 at a time. Other arguments, ownership and errors as attn_fwd_ex.
+ */
+int attn_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
+                   const int32_t* page_table, const int32_t* seqlens, void* out, float* lse,
+                   float* mass, int layout, int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq,
+                   int64_t n_pages, int64_t page_size, int64_t page_stride, int64_t max_pages,
+                   int64_t d, float scale, int rounding_mode, int flags, void* workspace,
+                   int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes attn_fwd_paged needs on the current device (with_mass: whether a mass is
+ * given), or a negative status. */
+int64_t attn_fwd_paged_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq,
+                                       int64_t page_size, int64_t max_pages, int64_t d,
+                                       int with_mass);
+
 /* Static English text for a status code (never NULL). */
 const char* attn_status_str(int status);
 
