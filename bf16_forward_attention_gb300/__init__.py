@@ -144,6 +144,10 @@ def load_library(debug: bool | None = None) -> ctypes.CDLL:
     lib.attn_fwd_paged.restype = ci
     lib.attn_fwd_paged_workspace_bytes.argtypes = [i64] * 7 + [ci]
     lib.attn_fwd_paged_workspace_bytes.restype = i64
+    lib.attn_cache_evict.argtypes = [vp] * 7 + [ci] + [i64] * 9 + [vp, i64, vp]
+    lib.attn_cache_evict.restype = ci
+    lib.attn_cache_evict_workspace_bytes.argtypes = [i64] * 6
+    lib.attn_cache_evict_workspace_bytes.restype = i64
     _libs[debug] = lib
     return lib
 
@@ -961,6 +965,56 @@ def attn_fwd_paged(q, k_pages, v_pages, page_table, seqlens, *, causal: bool = F
     return out, lse
 
 
+def evict_workspace_bytes(B: int, Hkv: int, n_pages: int, page_size: int, max_pages: int, budget: int) -> int:
+    """Device workspace attn_cache_evict needs."""
+    return _workspace_of(load_library(), "attn_cache_evict_workspace_bytes", -1, B, Hkv, n_pages, page_size,
+                         max_pages, budget)
+
+
+def attn_cache_evict(k_pages, v_pages, page_table, seqlens, mass, budget: int, *, recent: int = 0,
+                     layout: str = "bhsd", mass_out=None, seqlens_out=None, workspace=None):
+    """A paged cache kept to ``budget`` keys a sequence: (seqlens_out, mass_out).
+
+    Of a longer sequence, each key/value head keeps its last ``recent`` keys and the
+    budget - recent of greatest mass before them (``attn_fwd_paged`` adds the masses up), moved
+    together in order to the front of the sequence's pages, in place. mass_out (zero at and after
+    the new lengths) may be mass, and seqlens_out seqlens. Pages and lengths out of range, and a
+    page listed twice of a sequence to be cut, are found on the device: that sequence stays as it
+    was; check ``attn_fwd_last_error()`` after a sync."""
+    import torch
+
+    if layout not in LAYOUTS:
+        raise ValueError("unknown layout")
+    if not isinstance(k_pages, torch.Tensor) or not k_pages.is_cuda:
+        raise TypeError("k_pages must be a bf16 CUDA tensor")
+    device = k_pages.get_device()
+    n_pages, page_size, Hkv, D, page_stride = _check_pages(k_pages, v_pages, layout, device)
+    B, max_pages = _check_table(page_table, seqlens, device)
+    shape = (B, Hkv, max_pages * page_size)
+    _check_mass("mass", mass, shape, device)
+    if mass_out is None:
+        mass_out = torch.empty_like(mass)
+    else:
+        _check_mass("mass_out", mass_out, shape, device)
+    if seqlens_out is None:
+        seqlens_out = torch.empty_like(seqlens)
+    else:
+        _check_table(page_table, seqlens_out, device)
+    lib = load_library()
+    with _on_device(k_pages.device):
+        if workspace is None:
+            workspace = torch.empty(_workspace_of(lib, "attn_cache_evict_workspace_bytes", -1, B, Hkv, n_pages,
+                                                  page_size, max_pages, int(budget)), dtype=torch.uint8,
+                                    device=k_pages.device)
+        else:
+            _check_workspace(workspace, k_pages.device)
+        _call(lib.attn_cache_evict, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), seqlens.data_ptr(),
+              mass.data_ptr(), mass_out.data_ptr(), seqlens_out.data_ptr(), LAYOUTS[layout], B, Hkv, n_pages,
+              page_size, page_stride, max_pages, D, int(budget), int(recent), workspace.data_ptr(),
+              workspace.numel() * workspace.element_size(), _stream_of(k_pages))
+    return seqlens_out, mass_out
+
+
 def host_workspace_bytes(B: int, Hq: int, Hkv: int, Sq: int, Sk: int, d: int = 128) -> int:
     """Device workspace attn_fwd_host needs (negative: a status code)."""
     return load_library().attn_fwd_host_workspace_bytes(B, Hq, Hkv, Sq, Sk, d)
@@ -1171,4 +1225,4 @@ __all__ = ["attn_fwd", "attn_fwd_raw", "attn_fwd_last_error", "attn_fwd_timeout_
            "bwd_workspace_bytes", "bwd_varlen_workspace_bytes", "attn_fwd_prefix",
            "prefix_workspace_bytes", "ATTN_ERR_INDEX", "ATTN_FLAG_INTERLEAVED", "attn_qk_norm_rope",
            "attn_qk_norm_rope_paged", "attn_qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_bytes",
-           "attn_fwd_paged", "paged_workspace_bytes"]
+           "attn_fwd_paged", "paged_workspace_bytes", "attn_cache_evict", "evict_workspace_bytes"]

@@ -8,7 +8,7 @@ status word (see include/attn_fwd.h).
 
 One translation unit per group of kernels with their launcher (the forward ones,
 the backward ones, a batch on a shared prefix, norms with rotation,
-a paged cache) and the
+attention over a paged cache, its eviction) and the
 host-buffer pipeline, compiled at once, one -gencode; the CUDA runtime is linked statically and the driver's
 tensor-map encoder is looked up at run time, so the library loads (and
 reports ATTN_ERR_NO_DEVICE) on a machine without a GPU.
@@ -28,7 +28,7 @@ LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libattn_fwd.so")
 LIB_PATH_DEBUG = os.path.join(LIB_DIR, "libattn_fwd_debug.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("attn_fwd.cu", "attn_bwd.cu", "attn_prefix.cu", "attn_rope.cu",
-                                            "attn_paged.cu", "attn_host.cu")]
+                                            "attn_paged.cu", "attn_evict.cu", "attn_host.cu")]
 GENCODE = "arch=compute_103a,code=sm_103a"
 
 

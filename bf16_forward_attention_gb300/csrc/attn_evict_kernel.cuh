@@ -1,0 +1,261 @@
+// attn_evict_kernel.cuh - a paged cache kept to a budget: of each (sequence, kv head), the keys of
+// greatest accumulated attention weight and the latest ones, moved together in order.
+//
+// Three steps on the stream: attn_evict_select finds, for each (sequence, kv head), which keys
+// stay (their places in ascending order, with their masses), and counts how often each page is
+// listed; attn_evict_move moves them to the first places. Kept keys move towards the front, so a
+// round of moves reads everything it moves before it writes (a barrier of the cluster between
+// the two), and later rounds read places that no earlier one wrote: place d takes key src[d] >= d,
+// and a later round's keys lie behind all of this round's.
+#pragma once
+#include "attn_fwd_kernel.cuh"
+
+namespace attn {
+namespace evict {
+
+struct Params {
+  uint16_t* k;             // pages
+  uint16_t* v;
+  const int* table;        // (B, max_pages)
+  const int* seqlens;
+  const float* mass;       // (B, Hkv, cap)
+  float* mass_out;         // may be mass
+  int* seqlens_out;        // may be seqlens
+  int* listed;             // [page]: how often the sequences list it; zeros at the start
+  int2* head;              // [b * Hkv + kvh]: length (or -1: leave the sequence), first place that moves
+  int* src;                // [b * Hkv + kvh][keep]: the kept keys of a sequence over its budget, ascending
+  float* src_mass;         // their masses
+  long long page_stride;   // elements
+  int B, Hkv, cap, layout, n_pages, page_size, page_shift, max_pages;
+  int budget, recent, keep;  // keep: min(budget, cap)
+};
+
+// Masses in an order of unsigned integers: greater is greater, -0 is 0, and NaN is above all.
+__device__ __forceinline__ uint32_t order_of(float x) {
+  const uint32_t u = __float_as_uint(x);
+  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 0xFFFFFFFFu;
+  if ((u & 0x7FFFFFFFu) == 0) return 0x80000000u;
+  return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+
+__device__ __forceinline__ int page_of(const Params& p, int key) {
+  return p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
+}
+
+// ---------------------------------------------------------------- select
+constexpr int kSelectWarps = 16;
+constexpr int kSelectThreads = 32 * kSelectWarps;
+constexpr int kBins = 2048;
+
+// One block per (sequence, kv head). The m-th greatest of the masses of the keys that are not
+// among the latest, by its digits of 11, 11 and 10 bits from the top: a histogram of a digit among the
+// masses that share the digits above it. Then every warp counts, in its stretch of the keys,
+// those above that value and those equal to it, and writes its kept keys behind the others';
+// of the equal ones the first stay.
+__global__ void __launch_bounds__(kSelectThreads) attn_evict_select(const Params p) {
+  __shared__ int bins[kBins];
+  __shared__ int warp_n[2][kSelectWarps];
+  __shared__ int found, rest, first_move;
+  const int b = blockIdx.x / p.Hkv, kvh = blockIdx.x - b * p.Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int len = __ldg(p.seqlens + b);
+  const int pages = len < 0 || len > p.cap ? 0 : (len + p.page_size - 1) / p.page_size;
+  bool bad = false;
+  for (int i = threadIdx.x; i < pages; i += kSelectThreads) {
+    const int id = __ldg(p.table + static_cast<size_t>(b) * p.max_pages + i);
+    if (id < 0 || id >= p.n_pages)
+      bad = true;
+    else if (kvh == 0)
+      atomicAdd(p.listed + id, 1);
+  }
+  if (threadIdx.x == 0) first_move = p.keep;
+  bad = __syncthreads_or(bad);
+  if (bad || len < 0 || len > p.cap) {
+    if (threadIdx.x == 0) {
+      p.head[blockIdx.x] = make_int2(-1, 0);
+      if (kvh == 0) atomicOr(&g_attn_status, bad ? 8u : 2u);
+    }
+    return;
+  }
+  if (len <= p.budget) {
+    if (threadIdx.x == 0) p.head[blockIdx.x] = make_int2(len, p.keep);
+    return;
+  }
+  const float* mass = p.mass + static_cast<size_t>(blockIdx.x) * p.cap;
+  const int old = len - p.recent;   // more than m
+  int m = p.budget - p.recent;      // how many of them stay
+  uint32_t above = 0;               // the value's digits so far
+  int shift = 32;
+#pragma unroll 1
+  for (int pass = 0; pass < 3 && m > 0; ++pass) {
+    const int width = pass < 2 ? 11 : 10;
+    const uint32_t high = pass == 0 ? 0u : 0xFFFFFFFFu << shift;
+    shift -= width;
+    for (int i = threadIdx.x; i < kBins; i += kSelectThreads) bins[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < old; i += kSelectThreads) {
+      const uint32_t x = order_of(mass[i]);
+      if ((x & high) == above) atomicAdd(&bins[(x >> shift) & ((1 << width) - 1)], 1);
+    }
+    __syncthreads();
+    // From the top bin down: the one in which the m-th lies. Thread t has bins 4 t .. 4 t + 3 from
+    // the top.
+    int mine[4], sum = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      mine[j] = bins[kBins - 1 - (4 * threadIdx.x + j)];
+      sum += mine[j];
+    }
+    int upto = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int x = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+      if (lane >= d) upto += x;
+    }
+    if (lane == 31) warp_n[0][warp] = upto;
+    __syncthreads();
+    int before = upto - sum;
+    for (int w = 0; w < warp; ++w) before += warp_n[0][w];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (before < m && m <= before + mine[j]) {
+        found = kBins - 1 - (4 * static_cast<int>(threadIdx.x) + j);
+        rest = m - before;
+      }
+      before += mine[j];
+    }
+    __syncthreads();
+    above |= static_cast<uint32_t>(found) << shift;
+    m = rest;
+    __syncthreads();
+  }
+  // Above `above` all stay, of those equal to it the first m. With none of the old to stay, none do.
+  const bool none = p.budget == p.recent;
+  const int each = ((old + kSelectWarps - 1) / kSelectWarps + 31) & ~31;  // old is at least 1
+  const int lo = min(old, warp * each), hi = min(old, lo + each);
+  int more = 0, equal = 0;
+  if (!none) {
+    for (int i = lo + lane; i < hi; i += 32) {
+      const uint32_t x = order_of(mass[i]);
+      more += x > above;
+      equal += x == above;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      more += __shfl_xor_sync(0xFFFFFFFFu, more, d);
+      equal += __shfl_xor_sync(0xFFFFFFFFu, equal, d);
+    }
+  }
+  if (lane == 0) {
+    warp_n[0][warp] = more;
+    warp_n[1][warp] = equal;
+  }
+  __syncthreads();
+  int n_more = 0, n_equal = 0;  // before the key at hand
+  for (int w = 0; w < warp; ++w) {
+    n_more += warp_n[0][w];
+    n_equal += warp_n[1][w];
+  }
+  int* src = p.src + static_cast<size_t>(blockIdx.x) * p.keep;
+  float* src_mass = p.src_mass + static_cast<size_t>(blockIdx.x) * p.keep;
+  auto put = [&](int d, int i) {
+    if (!dbg_ok(d >= 0 && d < p.keep && d <= i)) return;
+    src[d] = i;
+    src_mass[d] = mass[i];
+  };
+  // Keys before the first that goes stay where they are; the next kept one takes its place.
+  int first_gone = none ? 0 : p.keep;
+  if (!none) {
+    const uint32_t below = (1u << lane) - 1;
+    for (int base = lo; base < hi; base += 32) {
+      const int i = base + lane;
+      const uint32_t x = i < hi ? order_of(mass[i]) : 0u;
+      const uint32_t is_more = __ballot_sync(0xFFFFFFFFu, i < hi && x > above);
+      const uint32_t is_equal = __ballot_sync(0xFFFFFFFFu, i < hi && x == above);
+      const int eq = n_equal + __popc(is_equal & below);  // equal ones before this one
+      if (i < hi) {
+        if (x > above || (x == above && eq < m))
+          put(n_more + __popc(is_more & below) + min(eq, m), i);
+        else
+          first_gone = min(first_gone, i);
+      }
+      n_more += __popc(is_more);
+      n_equal += __popc(is_equal);
+    }
+  }
+  for (int i = threadIdx.x; i < p.recent; i += kSelectThreads) put(p.budget - p.recent + i, old + i);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) first_gone = min(first_gone, __shfl_xor_sync(0xFFFFFFFFu, first_gone, d));
+  if (lane == 0) atomicMin(&first_move, first_gone);
+  __syncthreads();
+  if (threadIdx.x == 0) p.head[blockIdx.x] = make_int2(len, first_move);
+}
+
+// ---------------------------------------------------------------- move
+constexpr int kCluster = 8;        // CTAs of a (sequence, kv head)
+constexpr int kMoveThreads = 256;
+constexpr int kMoveKeys = 4;       // keys a half-warp moves at once: 8 loads of 16 bytes a lane in flight
+constexpr int kMoveRound = kMoveThreads / 16 * kMoveKeys;  // keys of a CTA's round
+
+// The rounds of a (sequence, kv head): 512 keys over its cluster, read, a barrier, written.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kMoveThreads) attn_evict_move(const Params p) {
+  const int rank = static_cast<int>(ptx::cluster_ctarank());
+  const int item = blockIdx.x / kCluster, b = item / p.Hkv, kvh = item - b * p.Hkv;
+  ptx::grid_dependency_wait();
+  const int2 head = p.head[item];
+  const int len = head.x;
+  if (len < 0) return;  // the whole cluster
+  const int* pages = p.table + static_cast<size_t>(b) * p.max_pages;
+  const bool over = len > p.budget;
+  if (over) {
+    // A page that is listed twice would be written by two sequences, or read after it was written.
+    bool twice = false;
+    const int n = (len + p.page_size - 1) / p.page_size;
+    for (int i = threadIdx.x; i < n; i += kMoveThreads) twice = twice || p.listed[__ldg(pages + i)] != 1;
+    if (__syncthreads_or(twice)) {  // every CTA of the cluster, and every head, finds the same
+      if (threadIdx.x == 0 && rank == 0 && kvh == 0) atomicOr(&g_attn_status, 8u);
+      return;
+    }
+  }
+  const int left = over ? p.budget : len;
+  const size_t row = static_cast<size_t>(item) * p.cap, list = static_cast<size_t>(item) * p.keep;
+  for (int j = rank * kMoveThreads + threadIdx.x; j < p.cap; j += kCluster * kMoveThreads)
+    p.mass_out[row + j] = j >= left ? 0.f : over ? p.src_mass[list + j] : p.mass[row + j];
+  if (threadIdx.x == 0 && rank == 0 && kvh == 0) p.seqlens_out[b] = left;
+  if (!over) return;
+  const int half = threadIdx.x >> 4, chunk = threadIdx.x & 15;
+  auto at = [&](int key) {
+    const int page = page_of(p, key), i = key - page * p.page_size;
+    return __ldg(pages + page) * p.page_stride +
+           static_cast<long long>(p.layout == 0 ? kvh * p.page_size + i : i * p.Hkv + kvh) * kD + 8 * chunk;
+  };
+  for (int base = head.y; base < left; base += kCluster * kMoveRound) {
+    const int d0 = base + rank * kMoveRound + half * kMoveKeys;
+    uint4 k[kMoveKeys], v[kMoveKeys];
+    bool moves[kMoveKeys];
+#pragma unroll
+    for (int i = 0; i < kMoveKeys; ++i) {
+      const int key = d0 + i < left ? p.src[list + d0 + i] : 0;
+      moves[i] = d0 + i < left && dbg_ok(key > d0 + i && key < len);
+      if (moves[i]) {
+        const long long from = at(key);
+        k[i] = __ldcg(reinterpret_cast<const uint4*>(p.k + from));
+        v[i] = __ldcg(reinterpret_cast<const uint4*>(p.v + from));
+      }
+    }
+    __syncwarp();
+    ptx::cluster_sync();
+#pragma unroll
+    for (int i = 0; i < kMoveKeys; ++i) {
+      if (moves[i]) {
+        const long long to = at(d0 + i);
+        *reinterpret_cast<uint4*>(p.k + to) = k[i];
+        *reinterpret_cast<uint4*>(p.v + to) = v[i];
+      }
+    }
+    __syncwarp();
+  }
+}
+
+}  // namespace evict
+}  // namespace attn

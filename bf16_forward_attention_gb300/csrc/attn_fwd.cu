@@ -646,7 +646,8 @@ int attn_fwd_debug_selftest(const void* q, const void* k, const void* v, void* o
 int attn_fwd_last_error(void) {
   unsigned int s = 0;
   if (!take_status(attn::g_attn_status, &s) || !bwd_take_status(&s) ||
-      !prefix_take_status(&s) || !rope_take_status(&s) || !paged_take_status(&s))
+      !prefix_take_status(&s) || !rope_take_status(&s) || !paged_take_status(&s) ||
+      !evict_take_status(&s))
     return ATTN_ERR_NO_DEVICE;
   if (s == 0) return ATTN_OK;
   if (s & 1u) return ATTN_ERR_TIMEOUT;

@@ -94,6 +94,7 @@ bool bwd_take_status(unsigned int* s);     // attn_bwd.cu
 bool prefix_take_status(unsigned int* s);  // attn_prefix.cu
 bool rope_take_status(unsigned int* s);    // attn_rope.cu
 bool paged_take_status(unsigned int* s);   // attn_paged.cu
+bool evict_take_status(unsigned int* s);   // attn_evict.cu
 
 // Streaming multiprocessors of the current device (152, a GB300's, where there is
 // none: size queries work without one).

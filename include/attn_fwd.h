@@ -531,6 +531,41 @@ int64_t attn_fwd_paged_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64
                                        int64_t page_size, int64_t max_pages, int64_t d,
                                        int with_mass);
 
+/*
+ * attn_cache_evict - keeps a paged cache to a budget. Of a sequence of n > budget keys, each
+ * key/value head keeps its last `recent` keys and, of the n - recent before them, the
+ * budget - recent of greatest mass (of equal masses the earlier key; NaN is above all other
+ * values). The kept keys and values move together, in order, to places 0 .. budget - 1 of
+ * the sequence's pages, in place; heads keep different keys. Sequences of at most budget
+ * keys stay as they are. No counterpart on the pages.
+ *
+ *   k_pages, v_pages, page_table, seqlens   as attn_fwd_paged; pages are written. Places
+ *              from budget on are free afterwards, and keep what they held.
+ *   mass       device, fp32, (B, Hkv, max_pages * page_size): what attn_fwd_paged added up
+ *   mass_out   like mass, written: the masses at their keys' new places, 0 at and after the
+ *              new length (so that further keys start at 0); may be mass itself
+ *   seqlens_out  device, int32, B, written: min(n, budget); may be seqlens itself
+ *   budget     >= 1;  recent  0 .. budget
+ *   workspace  device, 16-byte aligned, attn_cache_evict_workspace_bytes(...) bytes, owned by
+ *              the caller; calls that share one must not overlap in time
+ * A sequence over its budget whose pages (of its n keys) are listed twice, by itself or by
+ * another sequence of the call, and one with a page number or a length out of range is found
+ * on the device: it stays as it was, its mass_out and seqlens_out unwritten, and
+ * attn_fwd_last_error() reports ATTN_ERR_INDEX, or ATTN_ERR_SEQLENS for the length. Results
+ * are the same from run to run. Written tensors overlap nothing else (keys and values may be
+ * halves of one tensor's pages). Stream and other rules as attn_fwd.
+ */
+int attn_cache_evict(void* k_pages, void* v_pages, const int32_t* page_table,
+                     const int32_t* seqlens, const float* mass, float* mass_out,
+                     int32_t* seqlens_out, int layout, int64_t B, int64_t Hkv, int64_t n_pages,
+                     int64_t page_size, int64_t page_stride, int64_t max_pages, int64_t d,
+                     int64_t budget, int64_t recent, void* workspace, int64_t workspace_bytes,
+                     void* stream);
+
+/* Workspace bytes attn_cache_evict needs, or a negative status. */
+int64_t attn_cache_evict_workspace_bytes(int64_t B, int64_t Hkv, int64_t n_pages,
+                                         int64_t page_size, int64_t max_pages, int64_t budget);
+
 /* Static English text for a status code (never NULL). */
 const char* attn_status_str(int status);
 
