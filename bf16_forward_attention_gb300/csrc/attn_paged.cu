@@ -1,6 +1,6 @@
 // attn_paged.cu - host side of attention over a paged cache, declared in include/attn_fwd.h:
 // checks the call, lays out the workspace and launches, on the caller's stream, the runs of
-// tiles, the join of the items they cut, and the keys' masses where they are wanted.
+// units, the join of the items they cut, and the keys' masses where they are wanted.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -26,16 +26,17 @@ std::mutex g_mutex;
 bool g_ready[kMaxDevices];
 
 using Kernel = void (*)(const paged::Params);
-// By 8-row tiles of a block, with and without the keys' masses; blocks of more than 16 rows are
-// bound by their instructions, so only caches that need it take the folding form.
-constexpr Kernel kFwd[2][6] = {
-    {paged::attn_paged_fwd<1, true, false>, paged::attn_paged_fwd<2, true, false>,
-     paged::attn_paged_fwd<3, false, false>, paged::attn_paged_fwd<4, false, false>,
-     paged::attn_paged_fwd<3, true, false>, paged::attn_paged_fwd<4, true, false>},
-    {paged::attn_paged_fwd<1, true, true>, paged::attn_paged_fwd<2, true, true>,
-     paged::attn_paged_fwd<3, false, true>, paged::attn_paged_fwd<4, false, true>,
-     paged::attn_paged_fwd<3, true, true>, paged::attn_paged_fwd<4, true, true>}};
-constexpr int64_t kFoldKeys = 16384;  // keys of a cache beyond which those take it
+// A block's rows, and the kernel for them, with and without the keys' masses.
+struct Form {
+  int rows, threads, smem, ctas;
+  Kernel fwd[2];
+};
+template <typename S>
+constexpr Form form() {
+  return {S::kRows, S::kThreads, S::kSmem, S::kCtas, {paged::attn_paged_fwd<S, false>, paged::attn_paged_fwd<S, true>}};
+}
+constexpr Form kForms[] = {form<paged::Rows8>(), form<paged::Rows16>(), form<paged::Rows24>(), form<paged::Rows32>(),
+                           form<paged::Rows48>()};
 
 int device_ready() {
   const int st = arch_here();
@@ -44,10 +45,10 @@ int device_ready() {
   cudaGetDevice(&dev);
   std::lock_guard<std::mutex> lock(g_mutex);
   if (g_ready[dev]) return ATTN_OK;
-  for (const auto& row : kFwd)
-    for (Kernel fn : row)
+  for (const Form& form : kForms)
+    for (Kernel fn : form.fwd)
       if (cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               paged::kSmem) != cudaSuccess) {
+                               form.smem) != cudaSuccess) {
         cudaGetLastError();
         return ATTN_ERR_LAUNCH;
       }
@@ -58,7 +59,8 @@ int device_ready() {
 constexpr int64_t kLim31 = (int64_t(1) << 31) - 1;
 
 struct Plan {
-  int64_t rows, blocks, block_rows, rows8, cap, runs;
+  const Form* form;
+  int64_t rows, rows4, blocks, block_rows, cap, runs;
   int64_t o_bytes, rl_bytes, cut_bytes, lse2_bytes, logit_bytes;
   int64_t bytes() const { return o_bytes + rl_bytes + cut_bytes + lse2_bytes + logit_bytes; }
 };
@@ -74,24 +76,28 @@ int make_plan(Plan* pl, int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int64_t 
   if (B > kLim31 || Hq > (1 << 20) || Sq > kLim31 / Hq || page_size > kLim31 || max_pages > (kLim31 - 64) / page_size)
     return ATTN_ERR_TOO_LARGE;  // a tile past the last key still has an int's number
   pl->cap = page_size * max_pages;
+  // Blocks of equal size, an even number of rows where there are several (pairs of logits).
   pl->rows = Sq * group;
+  pl->rows4 = (pl->rows + 3) & ~int64_t(3);
   pl->blocks = (pl->rows + paged::kMaxRows - 1) / paged::kMaxRows;
-  pl->block_rows = (pl->rows + pl->blocks - 1) / pl->blocks;
-  pl->rows8 = (pl->block_rows + 7) / 8 * 8;
+  pl->block_rows = pl->blocks == 1 ? pl->rows : ((pl->rows + pl->blocks - 1) / pl->blocks + 1) & ~int64_t(1);
+  pl->form = kForms;
+  while (pl->form->rows < pl->block_rows) ++pl->form;
   if (Hkv * pl->blocks > kLim31 || B > (int64_t(1) << 40) / (Hkv * pl->blocks)) return ATTN_ERR_TOO_LARGE;
   const int64_t items = B * Hkv * pl->blocks;
-  // Tiles of all items below 2^47: a run's bounds are products with the number of runs.
-  const int64_t tiles = (pl->cap + attn::few::kKeys - 1) / attn::few::kKeys;
-  if (items > (int64_t(1) << 47) / tiles) return ATTN_ERR_TOO_LARGE;
-  // Two CTAs an SM, what it holds at once; fewer where the caches are too small for as many runs.
-  const int64_t most = (items * tiles + paged::kMinTiles - 1) / paged::kMinTiles, fill = 2 * int64_t(sms_here());
+  // Units of all items below 2^47: a run's bounds are products with the number of runs.
+  const int64_t units = (pl->cap + paged::kUnit - 1) / paged::kUnit;
+  if (items > (int64_t(1) << 47) / units) return ATTN_ERR_TOO_LARGE;
+  // The CTAs that the GPU holds at once; fewer where the caches are too small for as many runs.
+  const int64_t most = (items * units + paged::kMinUnits - 1) / paged::kMinUnits;
+  const int64_t fill = pl->form->ctas * int64_t(sms_here());
   pl->runs = most < fill ? most : fill;
-  pl->o_bytes = 2 * pl->runs * pl->rows8 * attn::kD * 4;
-  pl->rl_bytes = up256(2 * pl->runs * pl->rows8 * 8);
+  pl->o_bytes = 2 * pl->runs * pl->form->rows * attn::kD * 4;
+  pl->rl_bytes = up256(2 * pl->runs * pl->form->rows * 8);
   pl->cut_bytes = up256(pl->runs * int64_t(sizeof(paged::Cut)));
   pl->lse2_bytes = pl->logit_bytes = 0;
   if (mass) {
-    const int64_t row_bytes = B * Hkv * pl->blocks * pl->rows8 * 4;
+    const int64_t row_bytes = B * Hkv * pl->rows4 * 4;
     if (row_bytes > (int64_t(1) << 50) / pl->cap) return ATTN_ERR_TOO_LARGE;
     pl->lse2_bytes = up256(row_bytes);
     pl->logit_bytes = up256(row_bytes * pl->cap);
@@ -185,17 +191,16 @@ int attn_fwd_paged(const void* q, const void* k_pages, const void* v_pages, cons
   p.max_pages = static_cast<int>(max_pages);
   p.page_rows = static_cast<int>(page_stride / attn::kD);
   p.rows = static_cast<int>(pl.rows);
+  p.rows4 = static_cast<int>(pl.rows4);
   p.blocks = static_cast<int>(pl.blocks);
   p.block_rows = static_cast<int>(pl.block_rows);
-  p.rows8 = static_cast<int>(pl.rows8);
+  p.rows8 = pl.form->rows;
   p.c = scale * 1.4426950408889634f;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const int64_t nt = pl.rows8 / 8;
-  if (!launch(kFwd[mass ? 1 : 0][nt - 1 + (nt > 2 && pl.cap > kFoldKeys ? 2 : 0)], pl.runs, paged::kThreads,
-              paged::kSmem, cs, false, p))
+  if (!launch(pl.form->fwd[mass ? 1 : 0], pl.runs, pl.form->threads, pl.form->smem, cs, false, p))
     return ATTN_ERR_LAUNCH;
-  const dim3 rows(static_cast<unsigned>(pl.runs), static_cast<unsigned>(pl.block_rows));
-  if (!launch(paged::attn_paged_join, rows, 32 * paged::kJoinWarps, 0, cs, true, p))
+  const dim3 groups(static_cast<unsigned>(pl.runs), static_cast<unsigned>((pl.block_rows + 7) / 8));
+  if (!launch(paged::attn_paged_join, groups, paged::kJoinThreads, static_cast<int>(pl.runs) * 32, cs, true, p))
     return ATTN_ERR_LAUNCH;
   if (mass && !launch(paged::attn_paged_mass, 4 * int64_t(sms_here()), paged::kMassThreads, 0, cs, true, p))
     return ATTN_ERR_LAUNCH;

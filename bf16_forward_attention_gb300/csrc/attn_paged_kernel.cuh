@@ -1,9 +1,9 @@
 // attn_paged_kernel.cuh - attention of new tokens over a paged key-value cache.
 //
 // The rows (new tokens times the group's heads) of a sequence and a key/value head go
-// through the sequence's keys in blocks of at most 32; an item is one such block with all its
-// keys, cut into tiles of 16. The keys are read once per block, so few rows are bound by HBM.
-// All items' tiles in a row, sequence by sequence, are cut into equal runs, one a CTA: lengths
+// through the sequence's keys in blocks of at most 48; an item is one such block with all its
+// keys, cut into units of 64. The keys are read once per block, so few rows are bound by HBM.
+// All items' units in a row, sequence by sequence, are cut into equal runs, one a CTA: lengths
 // are on the device, and a long sequence among short ones is spread over as many CTAs as its
 // keys are worth. A CTA that has an item whole finishes it; an item that is cut leaves
 // unnormalised rows and (reference, sum) per part, joined by attn_paged_join:
@@ -16,18 +16,29 @@
 namespace attn {
 namespace paged {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kStages = 3;
-constexpr int kStageBytes = 2 * few::kKvBytes;
-constexpr int kWarpBytes = kStages * kStageBytes;
-constexpr int kMaxRows = 32;                       // rows of a block at most
-constexpr int kOffQ = kWarps * kWarpBytes;         // the block's queries
-constexpr int kOffMl = kOffQ + kMaxRows * kD * 2;  // [warp][row][2] floats
-constexpr int kSmem = kOffMl + kWarps * kMaxRows * 8;
-constexpr int kRowPitch = kD + 4;                  // fp32 rows in shared memory: distinct banks
-static_assert(kWarpBytes >= kMaxRows * kRowPitch * 4, "a warp's stages hold its fp32 rows at the end");
-constexpr int kMinTiles = 8;                       // of a run: with fewer tiles there are fewer runs
+constexpr int kTeams = 4;                          // of a CTA, 16 keys of a unit each
+constexpr int kUnit = kTeams * few::kKeys;
+constexpr int kStageBytes = 2 * few::kKvBytes;     // a team's K and V
+constexpr int kMaxRows = 48;                       // rows of a block at most
+constexpr int kMinUnits = 1;                       // of a run: with fewer units there are fewer runs
+
+// kNT 8-row groups a warp, kGroups warps a team: blocks of up to 8 kNT kGroups rows.
+template <int kNT_, int kGroups_, int kStages_, int kCtas_>
+struct Shape {
+  static constexpr int kNT = kNT_, kGroups = kGroups_, kStages = kStages_, kCtas = kCtas_;
+  static constexpr int kThreads = 32 * kTeams * kGroups;
+  static constexpr int kRows = 8 * kNT * kGroups;
+  static constexpr int kOffX = kTeams * kStages * kStageBytes;       // half of every warp's O^T
+  static constexpr int kOffMl = kOffX + kTeams * kGroups * kNT * 4 * 512;  // [team][row][2] floats
+  static constexpr int kSmem = kOffMl + kTeams * kRows * 8;
+};
+// Two CTAs an SM while a team is small; more rows take more warps of one CTA, whose loads are
+// shared by the team.
+using Rows8 = Shape<1, 1, 3, 2>;
+using Rows16 = Shape<1, 2, 3, 2>;
+using Rows24 = Shape<1, 3, 5, 1>;
+using Rows32 = Shape<1, 4, 5, 1>;
+using Rows48 = Shape<2, 3, 5, 1>;
 
 // What a run leaves for the join: the item that it begins and does not end, and in how many
 // parts (0: none).
@@ -44,25 +55,25 @@ struct Params {
   uint16_t* out;
   float* lse;              // (B, Hq, Sq)
   float* mass;             // (B, Hkv, cap) or null
-  float* part_o;           // [2 run + begins its item][rows8][128]
+  float* part_o;           // [2 run + begins its item][8-row group][16-column group][lane][4]: as the warps hold it
   float* part_rl;          // [2 run + begins its item][rows8][2]
   Cut* cuts;               // [run]
-  float* lse2;             // with mass: [b][kv head][block][rows8], log2 units; +Inf: not to be used
-  float* logits;           // with mass: [b][kv head][cap][block][rows8], log2 units
+  float* lse2;             // with mass: [b][kv head][rows4], log2 units; +Inf: not to be used
+  float* logits;           // with mass: [b][kv head][cap][rows4], log2 units
   int B, Hq, Hkv, group, Sq, cap, layout, causal, mode;
   int n_pages, page_size, page_shift, max_pages;  // page_shift: log2 of the page size, or -1
   int page_rows;           // rows of 128 from a page to the next
-  int rows;                // Sq * group
-  int blocks, block_rows, rows8;  // blocks of at most block_rows rows; rows8: that, in eights
+  int rows, rows4;         // Sq * group; that, in fours
+  int blocks, block_rows, rows8;  // blocks of at most block_rows rows; rows8: the kernel's rows of a block
   float c;                 // scale * log2(e)
 };
 
-__device__ __forceinline__ int tiles_of(int len, int cap) {
-  return len < 0 || len > cap ? 1 : max(1, (len + few::kKeys - 1) / few::kKeys);
+__device__ __forceinline__ int units_of(int len, int cap) {
+  return len < 0 || len > cap ? 1 : max(1, (len + kUnit - 1) / kUnit);
 }
 
-// Where a run of tiles begins. Units: the tiles of all items in a row (sequence, then kv head
-// and block); `per` items a sequence.
+// Where a run of units begins: the units of all items in a row (sequence, then kv head and
+// block), `per` items a sequence.
 struct Run {
   long long lo, hi;     // units
   long long first;      // of sequence b
@@ -70,7 +81,7 @@ struct Run {
   int b, runs;
 };
 
-// Run blockIdx.x of at most gridDim.x runs of at least `least` tiles. All threads of the block;
+// Run blockIdx.x of at most gridDim.x runs of at least `least` units. All threads of the block;
 // false: there is no such run.
 template <int kBlock>
 __device__ __forceinline__ bool find_run(const int* seqlens, int B, int cap, int per, int least, Run& run) {
@@ -79,7 +90,7 @@ __device__ __forceinline__ bool find_run(const int* seqlens, int B, int cap, int
   const int each = (B + kBlock - 1) / kBlock;
   const int b0 = min(B, static_cast<int>(threadIdx.x) * each), b1 = min(B, b0 + each);
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += tiles_of(__ldg(seqlens + b), cap);
+  for (int b = b0; b < b1; ++b) mine += units_of(__ldg(seqlens + b), cap);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long upto = mine;
 #pragma unroll
@@ -106,7 +117,7 @@ __device__ __forceinline__ bool find_run(const int* seqlens, int B, int cap, int
     long long x = before;
     int b = b0;
     for (; b + 1 < b1; ++b) {
-      const int t = tiles_of(__ldg(seqlens + b), cap);
+      const int t = units_of(__ldg(seqlens + b), cap);
       if (run.lo < (x + t) * per) break;
       x += t;
     }
@@ -119,338 +130,427 @@ __device__ __forceinline__ bool find_run(const int* seqlens, int B, int cap, int
   return true;
 }
 
-// A row's result, four columns a lane, from its unnormalised sums and (reference, sum).
-__device__ __forceinline__ void store_row(const Params& p, int b, int kvh, int block, int r, int lane, float4 o,
-                                          float R, float L) {
-  const int row = block * p.block_rows + r;
-  if (!dbg_ok(r >= 0 && r < p.block_rows && row < p.rows && b >= 0 && b < p.B && kvh < p.Hkv)) return;
-  const float inv = __frcp_rn(L);
-  *reinterpret_cast<uint2*>(p.out + few::query_at(p.layout, p.Hq, p.Sq, p.group, b, kvh, row) + 4 * lane) =
-      make_uint2(round_bf16_bits(o.x * inv, p.mode) | (round_bf16_bits(o.y * inv, p.mode) << 16),
-                 round_bf16_bits(o.z * inv, p.mode) | (round_bf16_bits(o.w * inv, p.mode) << 16));
-  if (lane == 0) {
-    const int h = kvh * p.group + row % p.group;
-    store_lse(p.lse, (static_cast<size_t>(b) * p.Hq + h) * p.Sq + row / p.group, R, L);
-    if (p.mass)
-      p.lse2[(static_cast<size_t>(b) * p.Hkv + kvh) * p.blocks * p.rows8 + block * p.rows8 + r] = R + log2f(L);
+// A run's units one after another.
+struct Walk {
+  int b, item, t;       // sequence, its item, the item's unit
+  int len, units;       // the sequence's keys (-1: out of range), its items' units
+
+  __device__ __forceinline__ void enter(const Params& p) {
+    len = __ldg(p.seqlens + b);
+    units = units_of(len, p.cap);
+    if (len > p.cap) len = -1;
+    len = max(len, -1);
   }
+  __device__ __forceinline__ void start(const Params& p, const Run& run) {
+    b = run.b;
+    enter(p);
+    const long long rel = run.lo - run.first;
+    item = static_cast<int>(rel / units);
+    t = static_cast<int>(rel - static_cast<long long>(item) * units);
+  }
+  __device__ __forceinline__ void step(const Params& p, int per) {
+    if (++t < units) return;
+    t = 0;
+    if (++item < per) return;
+    item = 0;
+    if (++b < p.B) enter(p);
+  }
+};
+
+// An item's rows.
+struct Item {
+  int b, kvh, row0, n_rows;
+};
+__device__ __forceinline__ Item item_of(const Params& p, int b, int item) {
+  const int kvh = item / p.blocks, row0 = (item - kvh * p.blocks) * p.block_rows;
+  return {b, kvh, row0, min(p.block_rows, p.rows - row0)};
+}
+
+__device__ __forceinline__ float& lse2_at(const Params& p, const Item& it, int r) {
+  return p.lse2[(static_cast<size_t>(it.b) * p.Hkv + it.kvh) * p.rows4 + it.row0 + r];
+}
+
+// Rows 8 g + 2 (lane % 4) + {0, 1} of the item, columns 16 dt + lane / 4 (x[0], x[1]) and + 8: as
+// the warps hold O^T. Normalised, rounded and stored; a transposition puts a row's
+// neighbouring columns in one lane.
+__device__ __forceinline__ void store_out(const Params& p, const Item& it, int g, int dt, int lane, const float (&x)[4],
+                                          float inv0, float inv1) {
+  const uint32_t a = round_bf16_bits(x[0] * inv0, p.mode) | (round_bf16_bits(x[1] * inv1, p.mode) << 16);
+  const uint32_t c = round_bf16_bits(x[2] * inv0, p.mode) | (round_bf16_bits(x[3] * inv1, p.mode) << 16);
+  const uint32_t at = ptx::movmatrix_trans(a), ct = ptx::movmatrix_trans(c);
+  const int r = 8 * g + (lane >> 2);
+  if (r >= it.n_rows || !dbg_ok(it.row0 + r < p.rows && it.b < p.B && it.kvh < p.Hkv)) return;
+  uint16_t* to = p.out + few::query_at(p.layout, p.Hq, p.Sq, p.group, it.b, it.kvh, it.row0 + r) + 16 * dt + 2 * (lane & 3);
+  *reinterpret_cast<uint32_t*>(to) = at;
+  *reinterpret_cast<uint32_t*>(to + 8) = ct;
+}
+
+__device__ __forceinline__ void store_lse_of(const Params& p, const Item& it, int r, float R, float L) {
+  if (r >= it.n_rows) return;
+  const int row = it.row0 + r, i = row / p.group, h = it.kvh * p.group + row - i * p.group;
+  store_lse(p.lse, (static_cast<size_t>(it.b) * p.Hq + h) * p.Sq + i, R, L);
+  if (p.mass) lse2_at(p, it, r) = R + log2f(L);
 }
 
 // A row whose keys cannot be read: its results stay as they were, and attn_paged_mass is told.
-__device__ __forceinline__ void skip_row(const Params& p, int b, int kvh, int block, int r) {
-  if (p.mass)
-    p.lse2[(static_cast<size_t>(b) * p.Hkv + kvh) * p.blocks * p.rows8 + block * p.rows8 + r] =
-        __int_as_float(0x7F800000);
+__device__ __forceinline__ void skip_row(const Params& p, const Item& it, int r) {
+  if (r < it.n_rows && p.mass) lse2_at(p, it, r) = __int_as_float(0x7F800000);
 }
 
-// One CTA: a run of tiles. The four warps take an item's tiles in turn, each with a ring of its own
-// (cp.async, 3 stages of 8 KiB), and are joined in shared memory at the item's end.
-template <int kNT, bool kFold, bool kMass>
-__global__ void __launch_bounds__(kThreads, 2) attn_paged_fwd(const Params p) {
+// One CTA: a run of units. A team of kGroups warps takes 16 keys of every unit, each warp 8 kNT of
+// the block's rows, over a ring of its own (cp.async, kStages of 8 KiB) that runs on from item to
+// item; the teams meet only at an item's end, to add their rows.
+template <typename S, bool kMass>
+__global__ void __launch_bounds__(S::kThreads, S::kCtas) attn_paged_fwd(const Params p) {
+  constexpr int kNT = S::kNT, kGroups = S::kGroups, kStages = S::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int bad_page;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int team = warp / kGroups, grp = warp - team * kGroups;
   const float neg_inf = -__int_as_float(0x7F800000);
   const int per = p.Hkv * p.blocks;
   if (threadIdx.x == 0) p.cuts[blockIdx.x].parts = 0;
   Run run;
-  if (!find_run<kThreads>(p.seqlens, p.B, p.cap, per, kMinTiles, run)) return;
-  const uint32_t ring = ptx::smem_u32(smem) + warp * kWarpBytes, qs = ptx::smem_u32(smem) + kOffQ;
+  if (!find_run<S::kThreads>(p.seqlens, p.B, p.cap, per, kMinUnits, run)) return;
+  const uint32_t ring = ptx::smem_u32(smem) + team * kStages * kStageBytes;
   const int half = lane >> 4, chunk = lane & 15;
-  const uint32_t lane_dst = ring + few::row_at(half, chunk);  // keys 2 u + half: + 512 u, chunk turned by 2 u
 
-  long long u = run.lo, first = run.first;
-  int b = run.b;
-  while (u < run.hi) {
-    const int len = __ldg(p.seqlens + b), tiles = tiles_of(len, p.cap);
-    const int item = static_cast<int>((u - first) / tiles), t_first = static_cast<int>((u - first) % tiles);
-    const long long left = run.hi - u;
-    const int t_end = left < tiles - t_first ? t_first + static_cast<int>(left) : tiles;
-    const int kvh = item / p.blocks, block = item - kvh * p.blocks;
-    const int row0 = block * p.block_rows, n_rows = min(p.block_rows, p.rows - row0);
-    const bool whole = t_first == 0 && t_end == tiles;
-    if (!dbg_ok(b < p.B && item >= 0 && item < per && n_rows >= 1 && n_rows <= 8 * kNT && t_first < t_end)) return;
-    const int here = b;
-    const long long u_item = u - t_first;
-    u += t_end - t_first;
-    if (u == first + static_cast<long long>(tiles) * per) {
-      first = u;
-      ++b;
-    }
-    if (len < 0 || len > p.cap) {  // one tile a sequence, so this item is whole
-      if (threadIdx.x == 0) atomicOr(&g_attn_status, 2u);
-      for (int r = threadIdx.x; r < n_rows; r += kThreads) skip_row(p, here, kvh, block, r);
-      continue;
-    }
-    // ---- queries.
-    __syncthreads();  // the last item's rows have been read
-    if (threadIdx.x == 0) bad_page = 0;
+  // ---- loads: unit by unit, kStages - 1 ahead of the products.
+  Walk ahead;
+  ahead.start(p, run);
+  uint32_t bad_stages = 0;  // of those in the ring, which hold a key without a page
+  // Row of 128 (in the pages) of key `lane % 16` of the team's share of the unit, -1: none, -2: bad.
+  auto row_of = [&]() {
+    const int key = ahead.t * kUnit + team * few::kKeys + chunk;
+    if (key >= ahead.len) return -1;
+    const int page = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
+    const int at = key - page * p.page_size;
+    const int id = __ldg(p.table + static_cast<size_t>(ahead.b) * p.max_pages + page);
+    if (id < 0 || id >= p.n_pages) return -2;
+    const int kvh = ahead.item / p.blocks;
+    return id * p.page_rows + (p.layout == 0 ? kvh * p.page_size + at : at * p.Hkv + kvh);
+  };
+  auto load = [&](int row, int s) {
+    const bool bad = __any_sync(0xFFFFFFFFu, row == -2);
+    bad_stages = (bad_stages & ~(1u << s)) | (bad ? 1u << s : 0u);
+    const uint32_t dst = ring + s * kStageBytes;
 #pragma unroll
-    for (int it = 0; it < kNT; ++it) {
-      const int r = it * 8 + (threadIdx.x >> 4), c = threadIdx.x & 15;
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (r < n_rows)
-        x = __ldg(reinterpret_cast<const uint4*>(
-                      p.q + few::query_at(p.layout, p.Hq, p.Sq, p.group, here, kvh, row0 + r)) + c);
-      ptx::st_shared_v4(qs + few::row_at(r, c), x.x, x.y, x.z, x.w);
+    for (int x = 0; x < (few::kKeys / 2 + kGroups - 1) / kGroups; ++x) {
+      const int pair = x * kGroups + grp;
+      if (few::kKeys / 2 % kGroups != 0 && pair >= few::kKeys / 2) break;
+      const int r = __shfl_sync(0xFFFFFFFFu, row, half + 2 * pair);
+      const uint32_t d = dst + few::row_at(half + 2 * pair, chunk);
+      const size_t at = static_cast<size_t>(max(r, 0)) * kD + 8 * chunk;
+      ptx::cp_async16(d, p.k + at, r >= 0);
+      ptx::cp_async16(d + few::kKvBytes, p.v + at, r >= 0);
     }
-    few::Rows<kNT, kFold> rows;
-    rows.clear();
+  };
+  const int n = static_cast<int>(run.hi - run.lo);
+  int next = row_of();
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 8 * nt + 2 * (lane & 3) + e;
-        rows.lim[nt][e] = r < n_rows ? few::own_limit((row0 + r) / p.group, len, p.Sq, p.causal) : 0;
+  for (int s = 0; s < kStages - 1; ++s) {
+    if (s < n) {
+      load(next, s);
+      if (s + 1 < n) {
+        ahead.step(p, per);
+        next = row_of();
       }
-    const int min_lim = few::own_limit(row0 / p.group, len, p.Sq, p.causal);
+    }
+    ptx::cp_async_commit();
+  }
 
-    // Row of 128 (in the pages) of key `lane % 16` of tile t, -1: none.
-    const int* pages = p.table + static_cast<size_t>(here) * p.max_pages;
-    bool bad = false;
-    auto row_of = [&](int t) {
-      const int key = t * few::kKeys + chunk;
-      if (key >= len) return -1;
-      const int page = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
-      const int at = key - page * p.page_size, id = __ldg(pages + page);
-      if (id < 0 || id >= p.n_pages) {
-        bad = true;
-        return -1;
-      }
-      return id * p.page_rows + (p.layout == 0 ? kvh * p.page_size + at : at * p.Hkv + kvh);
-    };
-    auto load = [&](int row, int s) {
-      const uint32_t dst = lane_dst + s * kStageBytes;
+  // ---- products.
+  Walk at;
+  at.start(p, run);
+  few::Rows<kNT> rows;
+  Item it;
+  int t_first = 0, min_lim = 0;
+  bool bad = false, fresh = true;
+  for (int i = 0; i < n; ++i) {
+    if (fresh) {  // an item begins
+      fresh = false;
+      it = item_of(p, at.b, at.item);
+      t_first = at.t;
+      bad = false;
+      rows.clear();
+      const uint16_t* from[kNT];
 #pragma unroll
-      for (int x = 0; x < few::kKeys / 2; ++x) {
-        const int r = __shfl_sync(0xFFFFFFFFu, row, half + 2 * x);
-        const uint32_t d = (dst ^ ((2 * x & 6) << 4)) + 512 * x;
-        const size_t at = static_cast<size_t>(max(r, 0)) * kD + 8 * chunk;
-        ptx::cp_async16(d, p.k + at, r >= 0);
-        ptx::cp_async16(d + few::kKvBytes, p.v + at, r >= 0);
-      }
-    };
-    const int t0 = t_first + warp;
-    const int n = t0 < t_end ? (t_end - t0 + kWarps - 1) / kWarps : 0;  // this warp's tiles
+      for (int nt = 0; nt < kNT; ++nt) {
+        const int r = 8 * (grp * kNT + nt) + (lane >> 2);
+        from[nt] = r < it.n_rows && at.len >= 0
+                       ? p.q + few::query_at(p.layout, p.Hq, p.Sq, p.group, it.b, it.kvh, it.row0 + r)
+                       : nullptr;
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) {
-      if (s < n) load(row_of(t0 + s * kWarps), s);
-      ptx::cp_async_commit();
+        for (int e = 0; e < 2; ++e) {
+          const int x = 8 * (grp * kNT + nt) + 2 * (lane & 3) + e;
+          rows.lim[nt][e] = x < it.n_rows ? few::own_limit((it.row0 + x) / p.group, at.len, p.Sq, p.causal) : 0;
+        }
+      }
+      rows.load_q(from, lane);
+      min_lim = few::own_limit(it.row0 / p.group, at.len, p.Sq, p.causal);
     }
-    int next = kStages - 1 < n ? row_of(t0 + (kStages - 1) * kWarps) : -1;
-    __syncthreads();  // the queries
-    rows.load_q(qs, lane);
-    for (int i = 0; i < n; ++i) {
-      ptx::cp_async_wait<kStages - 2>();
-      __syncwarp();  // every lane's copies of this tile; every lane is done with the last one
-      if (i + kStages - 1 < n) load(next, (i + kStages - 1) % kStages);
-      ptx::cp_async_commit();
-      if (i + kStages < n) next = row_of(t0 + (i + kStages) * kWarps);
-      const uint32_t kt = ring + (i % kStages) * kStageBytes;
-      const int key0 = (t0 + i * kWarps) * few::kKeys;
+    // Every lane's copies of this unit; the team is done with the last one.
+    ptx::cp_async_wait<kStages - 2>();
+    if constexpr (kGroups == 1)
+      __syncwarp();
+    else
+      ptx::named_barrier_sync(1 + team, 32 * kGroups);
+    const int s = i % kStages;
+    const bool bad_now = bad_stages >> s & 1u;
+    if (i + kStages - 1 < n) load(next, (i + kStages - 1) % kStages);
+    ptx::cp_async_commit();
+    if (i + kStages < n) {
+      ahead.step(p, per);
+      next = row_of();
+    }
+    const uint32_t kt = ring + s * kStageBytes;
+    const int key0 = at.t * kUnit + team * few::kKeys;
+    bad = bad || bad_now;
+    if (key0 < at.len) {
       const bool masked = key0 + few::kKeys > min_lim;
       rows.tile(kt, kt + few::kKvBytes, key0, masked, masked && p.causal, p.c, lane,
-                [&](const float (&s)[kNT][4]) {
+                [&](const float (&x)[kNT][4]) {
                   if constexpr (kMass) {
-                    float* to = p.logits + ((static_cast<size_t>(here) * p.Hkv + kvh) * p.cap + key0 + (lane >> 2)) *
-                                               (p.blocks * p.rows8) + block * p.rows8 + 2 * (lane & 3);
+                    const int r = 8 * grp * kNT + 2 * (lane & 3);
+                    float* to = p.logits + ((static_cast<size_t>(it.b) * p.Hkv + it.kvh) * p.cap + key0 + (lane >> 2)) *
+                                               p.rows4 + it.row0 + r;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                      if (key0 + (lane >> 2) + 8 * e < len) {
+                      if (key0 + (lane >> 2) + 8 * e < at.len) {
 #pragma unroll
                         for (int nt = 0; nt < kNT; ++nt)
-                          *reinterpret_cast<float2*>(to + 8 * nt) = make_float2(s[nt][2 * e], s[nt][2 * e + 1]);
+                          if (r + 8 * nt < it.n_rows)
+                            *reinterpret_cast<float2*>(to + 8 * nt) = make_float2(x[nt][2 * e], x[nt][2 * e + 1]);
                       }
-                      to += 8 * (p.blocks * p.rows8);
+                      to += 8 * static_cast<size_t>(p.rows4);
                     }
                   }
                 });
     }
-    // ---- the warps' rows, joined through shared memory (each warp's own ring).
-    ptx::cp_async_wait<0>();
-    if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) {
-      atomicOr(&g_attn_status, 8u);
-      bad_page = 1;
+    const bool ends = at.t + 1 == at.units;
+    if (!ends && i + 1 < n) {
+      ++at.t;
+      continue;
     }
-    __syncwarp();
+    // ---- the item's end, or the run's: the teams' rows are added, 64 columns at a time.
+    fresh = true;
+    const bool whole = ends && t_first == 0;
     rows.finish_sums();
-    float* ml = reinterpret_cast<float*>(smem + kOffMl) + warp * kMaxRows * 2;
-    float* mine = reinterpret_cast<float*>(smem + warp * kWarpBytes);
-#pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 8 * nt + 2 * (lane & 3) + e;
-        if ((lane >> 2) == 0) {
-          ml[2 * r] = rows.ref[nt][e];
-          ml[2 * r + 1] = rows.sum[nt][e];
-        }
-#pragma unroll
-        for (int dt = 0; dt < 8; ++dt) {
-          mine[r * kRowPitch + 16 * dt + (lane >> 2)] = rows.o[dt][nt][e];
-          mine[r * kRowPitch + 16 * dt + 8 + (lane >> 2)] = rows.o[dt][nt][2 + e];
-        }
-      }
-    __syncthreads();
+    float2* ml = reinterpret_cast<float2*>(smem + S::kOffMl);  // [team][row]
+    float4* xs = reinterpret_cast<float4*>(smem + S::kOffX);   // [group][team][nt][dt % 4][lane]
     const size_t part = 2 * static_cast<size_t>(blockIdx.x) + (t_first == 0 ? 1 : 0);
-    const float2* all_ml = reinterpret_cast<const float2*>(smem + kOffMl);
-    for (int r = warp; r < n_rows; r += kWarps) {
-      float2 x2[kWarps];
-      float M = neg_inf;
+    float f[kTeams][kNT][2], R[kNT][2], L[kNT][2];
+    bool skip = false;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        x2[w] = all_ml[w * kMaxRows + r];
-        M = fmaxf(M, x2[w].x);
-      }
-      const float ref = M == neg_inf ? 0.f : M;
-      float L = 0.f;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int hf = 0; hf < 2; ++hf) {
+      __syncthreads();  // what was there has been read
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = ptx::ex2(x2[w].x - ref);
-        const float4 y = reinterpret_cast<const float4*>(smem + w * kWarpBytes)[r * (kRowPitch / 4) + lane];
-        L = fmaf(x2[w].y, f, L);
-        x.x = fmaf(y.x, f, x.x);
-        x.y = fmaf(y.y, f, x.y);
-        x.z = fmaf(y.z, f, x.z);
-        x.w = fmaf(y.w, f, x.w);
+      for (int nt = 0; nt < kNT; ++nt) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const float(&o)[4] = rows.o[4 * hf + d][nt];
+          xs[(((grp * kTeams + team) * kNT + nt) * 4 + d) * 32 + lane] = make_float4(o[0], o[1], o[2], o[3]);
+        }
+        if (hf == 0 && (lane >> 2) == 0) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e)  // a sum is not negative: -1 says that the rows cannot be formed
+            ml[team * S::kRows + 8 * (grp * kNT + nt) + 2 * lane + e] =
+                make_float2(rows.ref[nt][e], bad ? -1.f : rows.sum[nt][e]);
+        }
       }
-      if (whole) {
-        if (!bad_page)
-          store_row(p, here, kvh, block, r, lane, x, M, L);
-        else if (lane == 0)
-          skip_row(p, here, kvh, block, r);
-      } else {
-        reinterpret_cast<float4*>(p.part_o)[(part * p.rows8 + r) * (kD / 4) + lane] = x;
-        // A sum is not negative: -1 tells the join that the rows cannot be formed.
-        if (lane == 0)
-          reinterpret_cast<float2*>(p.part_rl)[part * p.rows8 + r] = make_float2(M, bad_page ? -1.f : L);
+      __syncthreads();
+      if (hf == 0) {
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = 8 * (grp * kNT + nt) + 2 * (lane & 3) + e;
+            float2 x[kTeams];
+            float M = neg_inf;
+#pragma unroll
+            for (int w = 0; w < kTeams; ++w) {
+              x[w] = ml[w * S::kRows + r];
+              M = fmaxf(M, x[w].x);
+              skip = skip || x[w].y < 0.f;
+            }
+            const float ref = M == neg_inf ? 0.f : M;
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kTeams; ++w) {
+              f[w][nt][e] = ptx::ex2(x[w].x - ref);
+              sum = fmaf(x[w].y, f[w][nt][e], sum);
+            }
+            R[nt][e] = M;
+            L[nt][e] = sum;
+          }
+        skip = __any_sync(0xFFFFFFFFu, skip);
+        if (team == 0 && (lane >> 2) == 0) {
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int r = 8 * (grp * kNT + nt) + 2 * lane + e;
+              if (!whole)
+                reinterpret_cast<float2*>(p.part_rl)[part * p.rows8 + r] = make_float2(R[nt][e], skip ? -1.f : L[nt][e]);
+              else if (skip || at.len < 0)
+                skip_row(p, it, r);
+              else
+                store_lse_of(p, it, r, R[nt][e], L[nt][e]);
+            }
+          if (lane == 0 && grp == 0 && (skip || at.len < 0)) atomicOr(&g_attn_status, skip ? 8u : 2u);
+        }
+      }
+      // This team's 16 of the 64 columns.
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) {
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kTeams; ++w) {
+          const float4 y = xs[(((grp * kTeams + w) * kNT + nt) * 4 + team) * 32 + lane];
+          x[0] = fmaf(y.x, f[w][nt][0], x[0]);
+          x[1] = fmaf(y.y, f[w][nt][1], x[1]);
+          x[2] = fmaf(y.z, f[w][nt][0], x[2]);
+          x[3] = fmaf(y.w, f[w][nt][1], x[3]);
+        }
+        const int g = grp * kNT + nt, dt = 4 * hf + team;
+        if (!whole)
+          reinterpret_cast<float4*>(p.part_o)[((part * (p.rows8 / 8) + g) * 8 + dt) * 32 + lane] =
+              make_float4(x[0], x[1], x[2], x[3]);
+        else if (!skip && at.len >= 0)
+          store_out(p, it, g, dt, lane, x, __frcp_rn(L[nt][0]), __frcp_rn(L[nt][1]));
       }
     }
-    if (t_first == 0 && !whole && threadIdx.x == 0) {
-      // The item's last tile is in the last run that begins before its end.
-      const long long end = u_item + tiles;
+    if (!ends && t_first == 0 && threadIdx.x == 0) {
+      // The item's last unit is in the last run that begins before its end.
+      const long long end = run.lo + i + (at.units - at.t);
       const int last = static_cast<int>((end * run.runs + run.total - 1) / run.total) - 1;
-      p.cuts[blockIdx.x] = {here, item, last - static_cast<int>(blockIdx.x) + 1, 0};
+      p.cuts[blockIdx.x] = {it.b, at.item, last - static_cast<int>(blockIdx.x) + 1, 0};
     }
+    if (i + 1 < n) at.step(p, per);
   }
 }
 
 // ---------------------------------------------------------------- join
-constexpr int kJoinWarps = 4;
+constexpr int kJoinSplits = 4;                     // warps that share an item's parts
+constexpr int kJoinThreads = 32 * 8 * kJoinSplits;
 
-// A block per (run, row): the run's cut item, if it has one, its parts over the four warps in a
-// fixed order.
-__global__ void __launch_bounds__(32 * kJoinWarps) attn_paged_join(const Params p) {
-  __shared__ float4 sum_o[kJoinWarps][32];
-  __shared__ float sum_l[kJoinWarps];
+// A block per (run, 8-row group): the run's cut item, if it has one. A warp takes 16 columns of
+// every fourth part; parts are added in a fixed order.
+__global__ void __launch_bounds__(kJoinThreads) attn_paged_join(const Params p) {
+  extern __shared__ __align__(16) float weights[];  // [part][8 rows]
+  __shared__ float4 sum_o[kJoinSplits - 1][8][32];
+  __shared__ float row_r[8], row_l[8];
   ptx::grid_dependency_wait();
   const Cut cut = p.cuts[blockIdx.x];
   if (cut.parts == 0) return;
-  const int kvh = cut.item / p.blocks, block = cut.item - kvh * p.blocks, r = blockIdx.y;
-  if (r >= min(p.block_rows, p.rows - block * p.block_rows)) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Item it = item_of(p, cut.b, cut.item);
+  const int g = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (8 * g >= it.n_rows || !dbg_ok(cut.b < p.B && cut.parts <= static_cast<int>(gridDim.x) - static_cast<int>(blockIdx.x)))
+    return;
   const float neg_inf = -__int_as_float(0x7F800000);
   const float2* rl = reinterpret_cast<const float2*>(p.part_rl);
   // Part 0 begins the item; the others are the first of their runs.
-  auto part_at = [&](int i) {
-    return (2 * (static_cast<size_t>(blockIdx.x) + i) + (i == 0 ? 1 : 0)) * p.rows8 + r;
-  };
-  float R = neg_inf;
+  auto part_at = [&](int i) { return 2 * (static_cast<size_t>(blockIdx.x) + i) + (i == 0 ? 1 : 0); };
+  // ---- a warp a row: the largest reference, the parts' weights, the sum.
   bool skip = false;
-  for (int i = lane; i < cut.parts; i += 32) {
-    const float2 x = rl[part_at(i)];
-    R = fmaxf(R, x.x);  // a NaN is left out: it comes back through its weight
-    skip = skip || x.y < 0.f;
-  }
+  if (warp < 8) {
+    float R = neg_inf;
+    for (int i = lane; i < cut.parts; i += 32) {
+      const float2 x = rl[part_at(i) * p.rows8 + 8 * g + warp];
+      R = fmaxf(R, x.x);  // a NaN is left out: it comes back through its weight
+      skip = skip || x.y < 0.f;
+    }
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) R = fmaxf(R, __shfl_xor_sync(0xFFFFFFFFu, R, d));
-  if (__any_sync(0xFFFFFFFFu, skip)) {
-    if (threadIdx.x == 0) skip_row(p, cut.b, kvh, block, r);
+    for (int d = 16; d > 0; d >>= 1) R = fmaxf(R, __shfl_xor_sync(0xFFFFFFFFu, R, d));
+    const float ref = R == neg_inf ? 0.f : R;
+    float L = 0.f;
+    for (int i = lane; i < cut.parts; i += 32) {
+      const float2 x = rl[part_at(i) * p.rows8 + 8 * g + warp];
+      const float w = ptx::ex2(x.x - ref);
+      weights[8 * i + warp] = w;
+      L = fmaf(x.y, w, L);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, d);
+    if (lane == 0) {
+      row_r[warp] = R;
+      row_l[warp] = L;
+    }
+  }
+  if (__syncthreads_or(skip)) {
+    if (threadIdx.x < 8) skip_row(p, it, 8 * g + threadIdx.x);
     return;
   }
-  const float ref = R == neg_inf ? 0.f : R;
-  float L = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = warp; i < cut.parts; i += kJoinWarps) {
-    const size_t at = part_at(i);
-    const float2 x = rl[at];
-    const float w = ptx::ex2(x.x - ref);
-    const float4 y = reinterpret_cast<const float4*>(p.part_o)[at * (kD / 4) + lane];
-    L = fmaf(x.y, w, L);
-    o.x = fmaf(y.x, w, o.x);
-    o.y = fmaf(y.y, w, o.y);
-    o.z = fmaf(y.z, w, o.z);
-    o.w = fmaf(y.w, w, o.w);
+  const int dt = warp & 7, split = warp >> 3;
+  float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+  for (int i = split; i < cut.parts; i += kJoinSplits) {
+    const float4 y = reinterpret_cast<const float4*>(p.part_o)[((part_at(i) * (p.rows8 / 8) + g) * 8 + dt) * 32 + lane];
+    const float2 w = *reinterpret_cast<const float2*>(weights + 8 * i + 2 * (lane & 3));
+    x[0] = fmaf(y.x, w.x, x[0]);
+    x[1] = fmaf(y.y, w.y, x[1]);
+    x[2] = fmaf(y.z, w.x, x[2]);
+    x[3] = fmaf(y.w, w.y, x[3]);
   }
-  sum_o[warp][lane] = o;
-  if (lane == 0) sum_l[warp] = L;
+  if (split != 0) sum_o[split - 1][dt][lane] = make_float4(x[0], x[1], x[2], x[3]);
   __syncthreads();
-  if (warp != 0) return;
+  if (split != 0) return;
 #pragma unroll
-  for (int w = 1; w < kJoinWarps; ++w) {
-    const float4 y = sum_o[w][lane];
-    L += sum_l[w];
-    o.x += y.x;
-    o.y += y.y;
-    o.z += y.z;
-    o.w += y.w;
+  for (int w = 0; w < kJoinSplits - 1; ++w) {
+    const float4 y = sum_o[w][dt][lane];
+    x[0] += y.x;
+    x[1] += y.y;
+    x[2] += y.z;
+    x[3] += y.w;
   }
-  store_row(p, cut.b, kvh, block, r, lane, o, R, L);
+  const int r = 2 * (lane & 3);
+  store_out(p, it, g, dt, lane, x, __frcp_rn(row_l[r]), __frcp_rn(row_l[r + 1]));
+  if (threadIdx.x < 8) store_lse_of(p, it, 8 * g + threadIdx.x, row_r[threadIdx.x], row_l[threadIdx.x]);
 }
 
 // ---------------------------------------------------------------- mass
 constexpr int kMassThreads = 128;
-constexpr int kMassTiles = 8;  // of a run at least: a key a thread
+constexpr int kMassUnits = 2;  // of a run at least: a key a thread
 
 // mass[b, kvh, j] += sum over the rows that see key j of 2^(s_ij - lse_i), a key a thread, the
 // rows in order. A row whose log-sum-exp is -Inf (it sees no key) adds nothing.
 __global__ void __launch_bounds__(kMassThreads) attn_paged_mass(const Params p) {
   const float inf = __int_as_float(0x7F800000);
   Run run;
-  const bool any = find_run<kMassThreads>(p.seqlens, p.B, p.cap, p.Hkv, kMassTiles, run);
+  const bool any = find_run<kMassThreads>(p.seqlens, p.B, p.cap, p.Hkv, kMassUnits, run);
   ptx::grid_dependency_wait();
   if (!any) return;
-  const int pitch = p.blocks * p.rows8;
   long long u = run.lo, first = run.first;
   int b = run.b;
   while (u < run.hi) {
-    const int len = __ldg(p.seqlens + b), tiles = tiles_of(len, p.cap);
-    const int kvh = static_cast<int>((u - first) / tiles), t_first = static_cast<int>((u - first) % tiles);
+    const int len = __ldg(p.seqlens + b), units = units_of(len, p.cap);
+    const int kvh = static_cast<int>((u - first) / units), t_first = static_cast<int>((u - first) % units);
     const long long left = run.hi - u;
-    const int t_end = left < tiles - t_first ? t_first + static_cast<int>(left) : tiles;
+    const int t_end = left < units - t_first ? t_first + static_cast<int>(left) : units;
     const int here = b;
     u += t_end - t_first;
-    if (u == first + static_cast<long long>(tiles) * p.Hkv) {
+    if (u == first + static_cast<long long>(units) * p.Hkv) {
       first = u;
       ++b;
     }
     if (len < 0 || len > p.cap) continue;
     const size_t head = static_cast<size_t>(here) * p.Hkv + kvh;
-    const float* lse2 = p.lse2 + head * pitch;
+    const float* lse2 = p.lse2 + head * p.rows4;
     bool skip = false;
-    for (int r = threadIdx.x; r < p.rows; r += kMassThreads)
-      skip = skip || lse2[r / p.block_rows * p.rows8 + r % p.block_rows] == inf;
+    for (int r = threadIdx.x; r < p.rows; r += kMassThreads) skip = skip || lse2[r] == inf;
     if (__syncthreads_or(skip)) continue;  // a page of the sequence could not be read
-    const int end = min(t_end * few::kKeys, len);
-    for (int key = t_first * few::kKeys + threadIdx.x; key < end; key += kMassThreads) {
-      const float* s = p.logits + (head * p.cap + key) * pitch;
+    const int end = min(t_end * kUnit, len);
+    for (int key = t_first * kUnit + threadIdx.x; key < end; key += kMassThreads) {
+      const float* s = p.logits + (head * p.cap + key) * p.rows4;
       float sum = 0.f;
-      for (int block = 0; block < p.blocks; ++block) {
-        const int n_rows = min(p.block_rows, p.rows - block * p.block_rows);
-        for (int r = 0; r < n_rows; r += 4) {
-          const float4 s4 = *reinterpret_cast<const float4*>(s + block * p.rows8 + r);
-          const float4 l4 = *reinterpret_cast<const float4*>(lse2 + block * p.rows8 + r);
-          const float sv[4] = {s4.x, s4.y, s4.z, s4.w}, lv[4] = {l4.x, l4.y, l4.z, l4.w};
+      for (int r = 0; r < p.rows; r += 4) {
+        const float4 s4 = *reinterpret_cast<const float4*>(s + r);
+        const float4 l4 = *reinterpret_cast<const float4*>(lse2 + r);
+        const float sv[4] = {s4.x, s4.y, s4.z, s4.w}, lv[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (r + e >= n_rows || lv[e] == -inf) continue;
-            if (p.causal &&
-                key >= few::own_limit((block * p.block_rows + r + e) / p.group, len, p.Sq, 1))
-              continue;
-            sum += ptx::ex2(sv[e] - lv[e]);
-          }
+        for (int e = 0; e < 4; ++e) {
+          if (r + e >= p.rows || lv[e] == -inf) continue;
+          if (p.causal && key >= few::own_limit((r + e) / p.group, len, p.Sq, 1)) continue;
+          sum += ptx::ex2(sv[e] - lv[e]);
         }
       }
       p.mass[head * p.cap + key] += sum;

@@ -33,11 +33,10 @@ __device__ __forceinline__ size_t query_at(int layout, int Hq, int Sq, int group
   return (layout != 0 ? (static_cast<size_t>(b) * Sq + i) * Hq + h : (static_cast<size_t>(b) * Hq + h) * Sq + i) * kD;
 }
 
-// The state of up to 8 kNT rows in one warp. kFold: a tile's two products of V start from 0
-// and are added to O^T to nearest; otherwise O^T accumulates in the tensor pipe, which
-// truncates, so that a warp's keys must not be many (99.96% of outputs within one unit in the
-// last place over 4096 unit-normal keys a warp, 99.88% over 8192).
-template <int kNT, bool kFold>
+// The state of up to 8 kNT rows in one warp. A tile's two products of V start from 0 and are added
+// to O^T to nearest: the tensor pipe truncates as it accumulates, which over 8192 unit-normal
+// keys a warp would leave 99.88% of outputs within one unit in the last place.
+template <int kNT>
 struct Rows {
   float o[8][kNT][4];   // O^T: d = 16 dt + lane / 4 (elements 0, 1) and + 8 (2, 3)
   float ref[kNT][2];    // the row's reference, log2 units
@@ -60,13 +59,15 @@ struct Rows {
     }
   }
 
-  // Queries from shared memory (rows by row_at).
-  __device__ __forceinline__ void load_q(uint32_t qs, int lane) {
+  // Queries: the lane's words of row 8 nt + lane / 4 at `row[nt]` (null: zeros).
+  __device__ __forceinline__ void load_q(const uint16_t* const (&row)[kNT], int lane) {
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
       for (int k2 = 0; k2 < 4; ++k2)
-        ptx::ldmatrix4(qs + row_at(8 * nt + (lane & 7), 4 * k2 + (lane >> 3)), q[nt][k2]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          q[nt][k2][j] = row[nt] ? __ldg(reinterpret_cast<const uint32_t*>(row[nt]) + 16 * k2 + 4 * j + (lane & 3)) : 0u;
   }
 
   // One tile: K at kt, V at vt (rows by row_at), keys key0 .. key0 + 15. masked: some row does
@@ -173,16 +174,11 @@ struct Rows {
         ptx::ldmatrix4_trans(vt + row_at(v_row, 2 * dt + v_chunk), vf);
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
-          if constexpr (kFold) {
-            float x[4] = {0.f, 0.f, 0.f, 0.f};
-            ptx::mma_16816(x, vf, pl[nt][0], pl[nt][1]);
-            ptx::mma_16816(x, vf, ph[nt][0], ph[nt][1]);
+          float x[4] = {0.f, 0.f, 0.f, 0.f};
+          ptx::mma_16816(x, vf, pl[nt][0], pl[nt][1]);
+          ptx::mma_16816(x, vf, ph[nt][0], ph[nt][1]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[dt][nt][e] += x[e];
-          } else {
-            ptx::mma_16816(o[dt][nt], vf, ph[nt][0], ph[nt][1]);
-            ptx::mma_16816(o[dt][nt], vf, pl[nt][0], pl[nt][1]);
-          }
+          for (int e = 0; e < 4; ++e) o[dt][nt][e] += x[e];
         }
       }
       return;
