@@ -14,7 +14,7 @@ import functools
 import math
 import os
 
-from .build import lib_path
+from .build import BINDING_PATH, lib_path
 
 LAYOUTS = {"bhsd": 0, "bshd": 1}
 ROUNDINGS = {"rtne": 0, "rtna": 1, "rtz": 2}
@@ -684,82 +684,46 @@ def attn_fwd_prefix(q, k_prefix, v_prefix, k, v, seqlens, *, causal: bool = Fals
     return out, lse
 
 
-@functools.lru_cache(maxsize=4096)
-def _strides(batch: int, token: int, head: int):
-    """Three strides as the C entry points read them (kept: making the array costs more than the
-    check of a small call's tensor)."""
-    return (ctypes.c_int64 * 3)(batch, token, head)
+def _native():
+    """The compiled part of this binding (csrc/binding.cpp) and the library's entry points as it
+    takes them: what checks the tensors of the calls below, whose GPU time may be a few
+    microseconds."""
+    lib = load_library()
+    if not hasattr(lib, "entry"):
+        lib.entry = {n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
+                     for n in ("attn_qk_norm_rope", "attn_qk_norm_rope_paged", "attn_qk_norm_rope_bwd",
+                               "attn_qk_norm_rope_bwd_workspace_bytes", "attn_fwd_paged",
+                               "attn_fwd_paged_workspace_bytes", "attn_cache_evict",
+                               "attn_cache_evict_workspace_bytes")}
+    return _binding or _load_binding(), lib.entry
 
 
-def _rows_of(name, t, layout, device=None):
-    """(B, S, H, strides) of a bf16 CUDA tensor of rows of 128: (tokens, heads, 128), or 4-D in
-    `layout`, with any strides of tokens and heads."""
-    import torch
-
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda:
-        raise TypeError(f"{name} must be a bf16 CUDA tensor")
-    if device is not None and t.get_device() != device:
-        raise ValueError(f"{name} must be on q's device")
-    shape, stride = t.shape, t.stride()
-    if len(shape) == 4:
-        if layout == "bshd":
-            B, S, H, _ = shape
-            at = _strides(stride[0], stride[1], stride[2])
-        else:
-            B, H, S, _ = shape
-            at = _strides(stride[0], stride[2], stride[1])
-    elif len(shape) == 3:
-        B, (S, H, _) = 1, shape
-        at = _strides(0, stride[0], stride[1])
-    else:
-        raise ValueError(f"{name} must be (tokens, heads, d) or 4-D")
-    if stride[-1] != 1 and shape[-1] != 1:
-        raise ValueError(f"{name}'s last dimension must be contiguous")
-    return B, S, H, at
+_binding = None
 
 
-def _rows_out(name, out, like, layout, device):
-    """An output of rows as given, or a new one shaped like `like`; with its strides."""
-    import torch
+def _load_binding():
+    """``_lib/attn_binding.so``; raises if it has not been built."""
+    global _binding
+    import importlib.machinery
+    import importlib.util
 
-    if out is None:
-        out = torch.empty(like.shape, dtype=torch.bfloat16, device=like.device)
-    elif not isinstance(out, torch.Tensor) or out.shape != like.shape:
-        raise ValueError(f"{name} must be a bf16 CUDA tensor of shape {tuple(like.shape)}")
-    return out, _rows_of(name, out, layout, device)[3]
+    import torch  # noqa: F401  (the module's symbols are torch's)
 
-
-def _check_rope(q, k, q_weight, k_weight, cos, sin, positions, layout, rounding):
-    """Checks what the norm-and-rotation calls share; (B, S, Hq, Hkv, D, max_pos, rotary_dim,
-    q's strides, k's strides)."""
-    import torch
-
-    if layout not in LAYOUTS or rounding not in ROUNDINGS:
-        raise ValueError("unknown layout or rounding mode")
-    B, S, Hq, q_at = _rows_of("q", q, layout)
-    device = q.get_device()
-    Bk, Sk, Hkv, k_at = _rows_of("k", k, layout, device)
-    D = q.shape[-1]
-    if (Bk, Sk, k.shape[-1]) != (B, S, D) or q.dim() != k.dim():
-        raise ValueError("shape mismatch")
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if (not isinstance(w, torch.Tensor) or w.dtype != torch.bfloat16 or tuple(w.shape) != (D,)
-                or not w.is_contiguous() or w.get_device() != device):
-            raise ValueError(f"{name} must be a contiguous bf16 tensor of {D} entries on q's device")
-    for name, t in (("cos", cos), ("sin", sin)):
-        if (not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.dim() != 2 or not t.is_contiguous()
-                or t.shape != cos.shape or t.get_device() != device):
-            raise ValueError(f"{name} must be a contiguous fp32 tensor of shape (max_pos, rotary_dim / 2) on q's device")
-    _check_per_token("positions", positions, B, S, q.dim(), device)
-    return B, S, Hq, Hkv, D, cos.shape[0], 2 * cos.shape[1], q_at, k_at
+    if not os.path.exists(BINDING_PATH):
+        raise RuntimeError(f"binding not built: {BINDING_PATH} is missing. Run "
+                           "`python -m bf16_forward_attention_gb300.build`.")
+    loader = importlib.machinery.ExtensionFileLoader("attn_binding", BINDING_PATH)
+    spec = importlib.util.spec_from_file_location("attn_binding", BINDING_PATH, loader=loader)
+    _binding = importlib.util.module_from_spec(spec)
+    loader.exec_module(_binding)
+    return _binding
 
 
-def _check_per_token(name, t, B, S, dim, device):
-    import torch
-
-    if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.get_device() != device
-            or tuple(t.shape) != ((S,) if dim == 3 else (B, S)) or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous int32 tensor with an entry for each token, on q's device")
+def _results(got):
+    """What a call of the compiled binding returned, or its nonzero status raised."""
+    if got.__class__ is int:
+        raise AttnError(got, status_str(got))
+    return got
 
 
 def attn_qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, *, eps: float = 1e-6,
@@ -775,37 +739,12 @@ def attn_qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, *, eps: flo
     q_out may be q and k_out k. A position outside 0..max_pos-1 is found on the device: check
     ``attn_fwd_last_error()`` after a sync. The gradients are what ``attn_qk_norm_rope_bwd``
     returns."""
-    B, S, Hq, Hkv, D, max_pos, rot, q_at, k_at = _check_rope(q, k, q_weight, k_weight, cos, sin, positions, layout,
-                                                            rounding)
-    device = q.get_device()
-    with _on_device(q.device):
-        q_out, qo_at = _rows_out("q_out", q_out, q, layout, device)
-        k_out, ko_at = _rows_out("k_out", k_out, k, layout, device)
-        _call(load_library().attn_qk_norm_rope, q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(),
-              cos.data_ptr(), sin.data_ptr(), positions.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), q_at, k_at,
-              qo_at, ko_at, B, S, Hq, Hkv, D, max_pos, rot, float(eps), ROUNDINGS[rounding],
-              ATTN_FLAG_INTERLEAVED if interleaved else 0, _stream_of(q))
-    return q_out, k_out
-
-
-def _check_pages(k_pages, v_pages, layout, device):
-    """(n_pages, page_size, Hkv, D, page stride) of a cache's pages: 4-D bf16 tensors whose pages
-    are dense and may lie apart (halves of one tensor, layers of one)."""
-    import torch
-
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda:
-            raise TypeError(f"{name} must be a bf16 CUDA tensor")
-        if t.get_device() != device:
-            raise ValueError(f"{name} must be on q's device")
-    shape, stride = k_pages.shape, k_pages.stride()
-    if v_pages.shape != shape or v_pages.stride() != stride or len(shape) != 4:
-        raise ValueError("k_pages and v_pages must be 4-D tensors of one shape and strides")
-    n, a, b, D = shape
-    if stride[1:] != (b * D, D, 1) and not k_pages.is_contiguous():
-        raise ValueError("a page of k_pages and v_pages must be contiguous")
-    page_size, Hkv = (a, b) if layout == "bshd" else (b, a)
-    return n, page_size, Hkv, D, stride[0] if n > 1 else a * b * D
+    if layout not in LAYOUTS or rounding not in ROUNDINGS:
+        raise ValueError("unknown layout or rounding mode")
+    native, entry = _native()
+    return _results(native.norm_rope(entry["attn_qk_norm_rope"], q, k, q_weight, k_weight, cos, sin, positions, q_out,
+                                     k_out, eps, LAYOUTS[layout], ROUNDINGS[rounding],
+                                     ATTN_FLAG_INTERLEAVED if interleaved else 0))
 
 
 def attn_qk_norm_rope_paged(q, k, v, q_weight, k_weight, cos, sin, positions, slots, k_pages, v_pages, *,
@@ -818,22 +757,12 @@ def attn_qk_norm_rope_paged(q, k, v, q_weight, k_weight, cos, sin, positions, sl
     Hkv, page_size, 128) for "bhsd", each page contiguous. slots: int32, one a token like
     positions, the place page * page_size + place in the page, or -1 for a token that is not
     stored (padding); the slots of a call differ. A slot out of range is found on the device."""
-    B, S, Hq, Hkv, D, max_pos, rot, q_at, k_at = _check_rope(q, k, q_weight, k_weight, cos, sin, positions, layout,
-                                                            rounding)
-    device = q.get_device()
-    Bv, Sv, Hv, v_at = _rows_of("v", v, layout, device)
-    n_pages, page_size, Hp, Dp, page_stride = _check_pages(k_pages, v_pages, layout, device)
-    if v.shape != k.shape or (Hp, Dp) != (Hkv, D):
-        raise ValueError("shape mismatch")
-    _check_per_token("slots", slots, B, S, q.dim(), device)
-    with _on_device(q.device):
-        q_out, qo_at = _rows_out("q_out", q_out, q, layout, device)
-        _call(load_library().attn_qk_norm_rope_paged, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_weight.data_ptr(),
-              k_weight.data_ptr(), cos.data_ptr(), sin.data_ptr(), positions.data_ptr(), slots.data_ptr(),
-              q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), q_at, k_at, v_at, qo_at, LAYOUTS[layout], B, S,
-              Hq, Hkv, n_pages, page_size, page_stride, D, max_pos, rot, float(eps), ROUNDINGS[rounding],
-              ATTN_FLAG_INTERLEAVED if interleaved else 0, _stream_of(q))
-    return q_out
+    if layout not in LAYOUTS or rounding not in ROUNDINGS:
+        raise ValueError("unknown layout or rounding mode")
+    native, entry = _native()
+    return _results(native.norm_rope_paged(entry["attn_qk_norm_rope_paged"], q, k, q_weight, k_weight, cos, sin,
+                                           positions, v, slots, k_pages, v_pages, q_out, eps, LAYOUTS[layout],
+                                           ROUNDINGS[rounding], ATTN_FLAG_INTERLEAVED if interleaved else 0))[0]
 
 
 def qk_norm_rope_bwd_workspace_bytes(B: int, S: int, Hq: int, Hkv: int, d: int = 128) -> int:
@@ -850,38 +779,13 @@ def attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, cos, sin, po
 
     ``workspace``: a CUDA tensor of at least ``qk_norm_rope_bwd_workspace_bytes(...)`` bytes;
     allocated here if not given (the C entry point itself never allocates)."""
-    import torch
-
-    B, S, Hq, Hkv, D, max_pos, rot, q_at, k_at = _check_rope(q, k, q_weight, k_weight, cos, sin, positions, layout,
-                                                            rounding)
-    device = q.get_device()
-    gq_at, gk_at = _rows_of("dq_out", dq_out, layout, device)[3], _rows_of("dk_out", dk_out, layout, device)[3]
-    if dq_out.shape != q.shape or dk_out.shape != k.shape:
-        raise ValueError("shape mismatch")
-    lib = load_library()
-    with _on_device(q.device):
-        dq, dq_at = _rows_out("dq", dq, q, layout, device)
-        dk, dk_at = _rows_out("dk", dk, k, layout, device)
-        dws = []
-        for name, dw in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
-            if dw is None:
-                dw = torch.empty(D, dtype=torch.float32, device=q.device)
-            elif (not isinstance(dw, torch.Tensor) or dw.dtype != torch.float32 or tuple(dw.shape) != (D,)
-                  or not dw.is_contiguous() or dw.get_device() != device):
-                raise ValueError(f"{name} must be a contiguous fp32 tensor of {D} entries on q's device")
-            dws.append(dw)
-        if workspace is None:
-            workspace = torch.empty(_workspace_of(lib, "attn_qk_norm_rope_bwd_workspace_bytes", device, B, S, Hq,
-                                                  Hkv, D), dtype=torch.uint8, device=q.device)
-        else:
-            _check_workspace(workspace, q.device)
-        _call(lib.attn_qk_norm_rope_bwd, dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(),
-              q_weight.data_ptr(), k_weight.data_ptr(), cos.data_ptr(), sin.data_ptr(), positions.data_ptr(),
-              dq.data_ptr(), dk.data_ptr(), dws[0].data_ptr(), dws[1].data_ptr(), gq_at, gk_at, q_at, k_at, dq_at,
-              dk_at, B, S, Hq, Hkv, D, max_pos, rot, float(eps), ROUNDINGS[rounding],
-              ATTN_FLAG_INTERLEAVED if interleaved else 0, workspace.data_ptr(),
-              workspace.numel() * workspace.element_size(), _stream_of(q))
-    return dq, dk, dws[0], dws[1]
+    if layout not in LAYOUTS or rounding not in ROUNDINGS:
+        raise ValueError("unknown layout or rounding mode")
+    native, entry = _native()
+    return _results(native.norm_rope_bwd(entry["attn_qk_norm_rope_bwd"], entry["attn_qk_norm_rope_bwd_workspace_bytes"],
+                                         q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, dq, dk,
+                                         dq_weight, dk_weight, workspace, eps, LAYOUTS[layout], ROUNDINGS[rounding],
+                                         ATTN_FLAG_INTERLEAVED if interleaved else 0))
 
 
 def paged_workspace_bytes(B: int, Hq: int, Hkv: int, Sq: int, page_size: int, max_pages: int, *,
@@ -890,30 +794,6 @@ def paged_workspace_bytes(B: int, Hq: int, Hkv: int, Sq: int, page_size: int, ma
     given a mass)."""
     return _workspace_of(load_library(), "attn_fwd_paged_workspace_bytes", _here(), B, Hq, Hkv, Sq, page_size,
                          max_pages, d, int(with_mass))
-
-
-def _check_table(page_table, seqlens, device):
-    """(B, max_pages) of a page table and the lengths that go with it."""
-    import torch
-
-    for name, t, dim in (("page_table", page_table, 2), ("seqlens", seqlens, 1)):
-        if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or t.dim() != dim
-                or not t.is_contiguous()):
-            raise TypeError(f"{name} must be a contiguous {dim}-D int32 CUDA tensor")
-        if t.get_device() != device:
-            raise ValueError(f"{name} must be on the pages' device")
-    B, max_pages = page_table.shape
-    if seqlens.numel() != B:
-        raise ValueError("seqlens must have an entry for each row of page_table")
-    return B, max_pages
-
-
-def _check_mass(name, mass, shape, device):
-    import torch
-
-    if (not isinstance(mass, torch.Tensor) or mass.dtype != torch.float32 or tuple(mass.shape) != shape
-            or not mass.is_contiguous() or mass.get_device() != device):
-        raise ValueError(f"{name} must be a contiguous fp32 tensor of shape {shape} on the pages' device")
 
 
 def attn_fwd_paged(q, k_pages, v_pages, page_table, seqlens, *, causal: bool = False, layout: str = "bhsd",
@@ -929,40 +809,12 @@ def attn_fwd_paged(q, k_pages, v_pages, page_table, seqlens, *, causal: bool = F
     before them. ``mass`` (fp32, (B, Hkv, max_pages * page_size)): every key's attention weight,
     summed over the new tokens and the group's heads, is added to it. A length or page number out
     of range is found on the device: check ``attn_fwd_last_error()`` after a sync."""
-    import torch
-
     if layout not in LAYOUTS or rounding not in ROUNDINGS:
         raise ValueError("unknown layout or rounding mode")
-    _check_bf16((("q", q),), 4, "4-D")
-    device = q.get_device()
-    B, Hq, Sq, D = _dims(q, layout)
-    n_pages, page_size, Hkv, Dp, page_stride = _check_pages(k_pages, v_pages, layout, device)
-    Bt, max_pages = _check_table(page_table, seqlens, device)
-    if (Bt, Dp) != (B, D) or Hkv < 1 or Hq % Hkv:
-        raise ValueError("shape mismatch")
-    if mass is not None:
-        _check_mass("mass", mass, (B, Hkv, max_pages * page_size), device)
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        _check_out(out, q)
-    lse = _lse_like(lse, (B, Hq, Sq), q.device)
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    lib = load_library()
-    with _on_device(q.device):
-        if workspace is None:
-            need = _workspace_of(lib, "attn_fwd_paged_workspace_bytes", device, B, Hq, Hkv, Sq, page_size, max_pages,
-                                 D, int(mass is not None))
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        else:
-            _check_workspace(workspace, q.device)
-        _call(lib.attn_fwd_paged, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-              seqlens.data_ptr(), out.data_ptr(), lse.data_ptr(), None if mass is None else mass.data_ptr(),
-              LAYOUTS[layout], B, Hq, Hkv, Sq, n_pages, page_size, page_stride, max_pages, D, float(scale),
-              ROUNDINGS[rounding], ATTN_FLAG_CAUSAL if causal else 0, workspace.data_ptr(),
-              workspace.numel() * workspace.element_size(), _stream_of(q))
-    return out, lse
+    native, entry = _native()
+    return _results(native.fwd_paged(entry["attn_fwd_paged"], entry["attn_fwd_paged_workspace_bytes"], q, k_pages,
+                                     v_pages, page_table, seqlens, out, lse, mass, workspace, scale, LAYOUTS[layout],
+                                     ROUNDINGS[rounding], ATTN_FLAG_CAUSAL if causal else 0))
 
 
 def evict_workspace_bytes(B: int, Hkv: int, n_pages: int, page_size: int, max_pages: int, budget: int) -> int:
@@ -981,38 +833,12 @@ def attn_cache_evict(k_pages, v_pages, page_table, seqlens, mass, budget: int, *
     the new lengths) may be mass, and seqlens_out seqlens. Pages and lengths out of range, and a
     page listed twice of a sequence to be cut, are found on the device: that sequence stays as it
     was; check ``attn_fwd_last_error()`` after a sync."""
-    import torch
-
     if layout not in LAYOUTS:
         raise ValueError("unknown layout")
-    if not isinstance(k_pages, torch.Tensor) or not k_pages.is_cuda:
-        raise TypeError("k_pages must be a bf16 CUDA tensor")
-    device = k_pages.get_device()
-    n_pages, page_size, Hkv, D, page_stride = _check_pages(k_pages, v_pages, layout, device)
-    B, max_pages = _check_table(page_table, seqlens, device)
-    shape = (B, Hkv, max_pages * page_size)
-    _check_mass("mass", mass, shape, device)
-    if mass_out is None:
-        mass_out = torch.empty_like(mass)
-    else:
-        _check_mass("mass_out", mass_out, shape, device)
-    if seqlens_out is None:
-        seqlens_out = torch.empty_like(seqlens)
-    else:
-        _check_table(page_table, seqlens_out, device)
-    lib = load_library()
-    with _on_device(k_pages.device):
-        if workspace is None:
-            workspace = torch.empty(_workspace_of(lib, "attn_cache_evict_workspace_bytes", -1, B, Hkv, n_pages,
-                                                  page_size, max_pages, int(budget)), dtype=torch.uint8,
-                                    device=k_pages.device)
-        else:
-            _check_workspace(workspace, k_pages.device)
-        _call(lib.attn_cache_evict, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), seqlens.data_ptr(),
-              mass.data_ptr(), mass_out.data_ptr(), seqlens_out.data_ptr(), LAYOUTS[layout], B, Hkv, n_pages,
-              page_size, page_stride, max_pages, D, int(budget), int(recent), workspace.data_ptr(),
-              workspace.numel() * workspace.element_size(), _stream_of(k_pages))
-    return seqlens_out, mass_out
+    native, entry = _native()
+    return _results(native.cache_evict(entry["attn_cache_evict"], entry["attn_cache_evict_workspace_bytes"], k_pages,
+                                       v_pages, page_table, seqlens, mass, mass_out, seqlens_out, workspace,
+                                       int(budget), int(recent), LAYOUTS[layout]))
 
 
 def host_workspace_bytes(B: int, Hq: int, Hkv: int, Sq: int, Sk: int, d: int = 128) -> int:

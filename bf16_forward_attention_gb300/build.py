@@ -7,18 +7,22 @@ same kernels with bounds and protocol checks that report through the device
 status word (see include/attn_fwd.h).
 
 One translation unit per group of kernels with their launcher (the forward ones,
-the backward ones, a batch on a shared prefix, norms with rotation,
-attention over a paged cache, its eviction) and the
-host-buffer pipeline, compiled at once, one -gencode; the CUDA runtime is linked statically and the driver's
-tensor-map encoder is looked up at run time, so the library loads (and
-reports ATTN_ERR_NO_DEVICE) on a machine without a GPU.
+the backward ones, a batch on a shared prefix, norms with rotation, attention
+over a paged cache, its eviction) and the host-buffer pipeline, compiled at once,
+one -gencode; the CUDA runtime is linked statically and the driver's tensor-map
+encoder is looked up at run time, so the library loads (and reports
+ATTN_ERR_NO_DEVICE) on a machine without a GPU. Beside it the host compiler builds
+``_lib/attn_binding.so``, the C++ part of the Python binding, against the installed
+torch; the library itself knows nothing of torch.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -27,6 +31,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libattn_fwd.so")
 LIB_PATH_DEBUG = os.path.join(LIB_DIR, "libattn_fwd_debug.so")
+BINDING_PATH = os.path.join(LIB_DIR, "attn_binding.so")
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 SOURCES = [os.path.join(CSRC, f) for f in ("attn_fwd.cu", "attn_bwd.cu", "attn_prefix.cu", "attn_rope.cu",
                                             "attn_paged.cu", "attn_evict.cu", "attn_host.cu")]
 GENCODE = "arch=compute_103a,code=sm_103a"
@@ -53,31 +59,61 @@ def lib_path(debug: bool = False) -> str:
     return LIB_PATH_DEBUG if debug else LIB_PATH
 
 
+def _newer(path: str, deps) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(d) <= os.path.getmtime(path) for d in deps)
+
+
+def _library_up_to_date(debug: bool = False) -> bool:
+    return _newer(lib_path(debug), _deps())
+
+
+def _binding_up_to_date() -> bool:
+    return _newer(BINDING_PATH, [BINDING_SOURCE, os.path.join(INCLUDE, "attn_fwd.h")])
+
+
 def up_to_date(debug: bool = False) -> bool:
-    path = lib_path(debug)
-    if not os.path.exists(path):
-        return False
-    t = os.path.getmtime(path)
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return _library_up_to_date(debug) and (debug or _binding_up_to_date())
+
+
+def _binding_build(force: bool):
+    """A running compilation of the binding's C++ part (no kernels) against the installed torch and
+    Python, and where its output is; None if it is newer than its sources."""
+    if not force and _binding_up_to_date():
+        return None
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "c++", "-std=c++17", "-O2", "-fPIC", "-shared", "-o", tmp, BINDING_SOURCE]
+    for d in (INCLUDE, os.path.join(torch_dir, "include"),
+              os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+              sysconfig.get_paths()["include"], cuda):
+        cmd += ["-I", d]
+    cmd += ["-L", os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python"]
+    return subprocess.Popen(cmd), cmd, tmp
 
 
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     """Compile the library (release, or the debug flavour) if any source is newer
-    than it. Returns its path."""
+    than it, and beside the release one the binding. Returns the library's path."""
     path = lib_path(debug)
-    if not force and up_to_date(debug):
-        return path
     os.makedirs(LIB_DIR, exist_ok=True)
-    tmp = path + f".tmp{os.getpid()}"
-    cmd = [nvcc_path(), "-gencode", GENCODE, "-O3", "-lineinfo", "-std=c++17",
-           "--threads", "0", "-Xcompiler", "-fPIC", "-shared", "-I", INCLUDE, "-o", tmp] + SOURCES
-    if debug:
-        cmd.insert(1, "-DATTN_DEBUG=1")
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, path)
+    binding = None if debug else _binding_build(force)
+    if force or not _library_up_to_date(debug):
+        tmp = path + f".tmp{os.getpid()}"
+        cmd = [nvcc_path(), "-gencode", GENCODE, "-O3", "-lineinfo", "-std=c++17",
+               "--threads", "0", "-Xcompiler", "-fPIC", "-shared", "-I", INCLUDE, "-o", tmp] + SOURCES
+        if debug:
+            cmd.insert(1, "-DATTN_DEBUG=1")
+        if verbose:
+            cmd.insert(1, "-Xptxas=-v")
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+        os.replace(tmp, path)
+    if binding:
+        run, cmd, tmp = binding
+        if run.wait() != 0:
+            raise subprocess.CalledProcessError(run.returncode, cmd)
+        os.replace(tmp, BINDING_PATH)
     return path
 
 
