@@ -110,7 +110,7 @@ int attn_cache_evict(void* k_pages, void* v_pages, const int32_t* page_table, co
   p.head = reinterpret_cast<int2*>(ws + pl.listed_bytes);
   p.src = reinterpret_cast<int*>(ws + pl.listed_bytes + pl.head_bytes);
   p.src_mass = reinterpret_cast<float*>(ws + pl.listed_bytes + pl.head_bytes + pl.src_bytes);
-  p.page_stride = page_stride;
+  p.page_rows = static_cast<int>(page_stride / attn::kD);
   p.B = static_cast<int>(B);
   p.Hkv = static_cast<int>(Hkv);
   p.cap = static_cast<int>(pl.cap);

@@ -25,7 +25,7 @@ struct Params {
   int2* head;              // [b * Hkv + kvh]: length (or -1: leave the sequence), first place that moves
   int* src;                // [b * Hkv + kvh][keep]: the kept keys of a sequence over its budget, ascending
   float* src_mass;         // their masses
-  long long page_stride;   // elements
+  int page_rows;           // rows of 128 from a page to the next
   int B, Hkv, cap, layout, n_pages, page_size, page_shift, max_pages;
   int budget, recent, keep;  // keep: min(budget, cap)
 };
@@ -36,6 +36,27 @@ __device__ __forceinline__ uint32_t order_of(float x) {
   if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 0xFFFFFFFFu;
   if ((u & 0x7FFFFFFFu) == 0) return 0x80000000u;
   return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+
+// The masses first .. end - 1 in turn, kStep apart a thread: fn(valid, index, mass). Eight reads are
+// in flight at once: what a pass over a long row waits for.
+constexpr int kBatch = 8;
+template <int kStep, typename Fn>
+__device__ __forceinline__ void each_mass(const float* mass, int first, int end, int lane, Fn&& fn) {
+  for (int base = first; base < end; base += kBatch * kStep) {
+    float x[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = base + j * kStep + lane;
+      x[j] = i < end ? __ldg(mass + i) : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if (base + j * kStep >= end) break;  // the same for all lanes
+      const int i = base + j * kStep + lane;
+      fn(i < end, i, x[j]);
+    }
+  }
 }
 
 __device__ __forceinline__ int page_of(const Params& p, int key) {
@@ -93,10 +114,10 @@ __global__ void __launch_bounds__(kSelectThreads) attn_evict_select(const Params
     shift -= width;
     for (int i = threadIdx.x; i < kBins; i += kSelectThreads) bins[i] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < old; i += kSelectThreads) {
-      const uint32_t x = order_of(mass[i]);
-      if ((x & high) == above) atomicAdd(&bins[(x >> shift) & ((1 << width) - 1)], 1);
-    }
+    each_mass<kSelectThreads>(mass, 0, old, threadIdx.x, [&](bool valid, int, float value) {
+      const uint32_t x = order_of(value);
+      if (valid && (x & high) == above) atomicAdd(&bins[(x >> shift) & ((1 << width) - 1)], 1);
+    });
     __syncthreads();
     // From the top bin down: the one in which the m-th lies. Thread t has bins 4 t .. 4 t + 3 from
     // the top.
@@ -135,11 +156,11 @@ __global__ void __launch_bounds__(kSelectThreads) attn_evict_select(const Params
   const int lo = min(old, warp * each), hi = min(old, lo + each);
   int more = 0, equal = 0;
   if (!none) {
-    for (int i = lo + lane; i < hi; i += 32) {
-      const uint32_t x = order_of(mass[i]);
-      more += x > above;
-      equal += x == above;
-    }
+    each_mass<32>(mass, lo, hi, lane, [&](bool valid, int, float value) {
+      const uint32_t x = order_of(value);
+      more += valid && x > above;
+      equal += valid && x == above;
+    });
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
       more += __shfl_xor_sync(0xFFFFFFFFu, more, d);
@@ -158,32 +179,31 @@ __global__ void __launch_bounds__(kSelectThreads) attn_evict_select(const Params
   }
   int* src = p.src + static_cast<size_t>(blockIdx.x) * p.keep;
   float* src_mass = p.src_mass + static_cast<size_t>(blockIdx.x) * p.keep;
-  auto put = [&](int d, int i) {
+  auto put = [&](int d, int i, float value) {
     if (!dbg_ok(d >= 0 && d < p.keep && d <= i)) return;
     src[d] = i;
-    src_mass[d] = mass[i];
+    src_mass[d] = value;
   };
   // Keys before the first that goes stay where they are; the next kept one takes its place.
   int first_gone = none ? 0 : p.keep;
   if (!none) {
     const uint32_t below = (1u << lane) - 1;
-    for (int base = lo; base < hi; base += 32) {
-      const int i = base + lane;
-      const uint32_t x = i < hi ? order_of(mass[i]) : 0u;
-      const uint32_t is_more = __ballot_sync(0xFFFFFFFFu, i < hi && x > above);
-      const uint32_t is_equal = __ballot_sync(0xFFFFFFFFu, i < hi && x == above);
+    each_mass<32>(mass, lo, hi, lane, [&](bool valid, int i, float value) {
+      const uint32_t x = order_of(value);
+      const uint32_t is_more = __ballot_sync(0xFFFFFFFFu, valid && x > above);
+      const uint32_t is_equal = __ballot_sync(0xFFFFFFFFu, valid && x == above);
       const int eq = n_equal + __popc(is_equal & below);  // equal ones before this one
-      if (i < hi) {
+      if (valid) {
         if (x > above || (x == above && eq < m))
-          put(n_more + __popc(is_more & below) + min(eq, m), i);
+          put(n_more + __popc(is_more & below) + min(eq, m), i, value);
         else
           first_gone = min(first_gone, i);
       }
       n_more += __popc(is_more);
       n_equal += __popc(is_equal);
-    }
+    });
   }
-  for (int i = threadIdx.x; i < p.recent; i += kSelectThreads) put(p.budget - p.recent + i, old + i);
+  for (int i = threadIdx.x; i < p.recent; i += kSelectThreads) put(p.budget - p.recent + i, old + i, mass[old + i]);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) first_gone = min(first_gone, __shfl_xor_sync(0xFFFFFFFFu, first_gone, d));
   if (lane == 0) atomicMin(&first_move, first_gone);
@@ -198,7 +218,7 @@ constexpr int kMoveKeys = 4;       // keys a half-warp moves at once: 8 loads of
 constexpr int kMoveRound = kMoveThreads / 16 * kMoveKeys;  // keys of a CTA's round
 
 // The rounds of a (sequence, kv head): 512 keys over its cluster, read, a barrier, written.
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kMoveThreads) attn_evict_move(const Params p) {
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kMoveThreads, 4) attn_evict_move(const Params p) {
   const int rank = static_cast<int>(ptx::cluster_ctarank());
   const int item = blockIdx.x / kCluster, b = item / p.Hkv, kvh = item - b * p.Hkv;
   ptx::grid_dependency_wait();
@@ -224,33 +244,43 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kMoveThreads)
   if (threadIdx.x == 0 && rank == 0 && kvh == 0) p.seqlens_out[b] = left;
   if (!over) return;
   const int half = threadIdx.x >> 4, chunk = threadIdx.x & 15;
-  auto at = [&](int key) {
+  auto row_of = [&](int key) {  // of 128, in the pages
     const int page = page_of(p, key), i = key - page * p.page_size;
-    return __ldg(pages + page) * p.page_stride +
-           static_cast<long long>(p.layout == 0 ? kvh * p.page_size + i : i * p.Hkv + kvh) * kD + 8 * chunk;
+    return __ldg(pages + page) * p.page_rows + (p.layout == 0 ? kvh * p.page_size + i : i * p.Hkv + kvh);
   };
-  for (int base = head.y; base < left; base += kCluster * kMoveRound) {
+  auto at = [&](uint16_t* t, int row) { return reinterpret_cast<uint4*>(t + static_cast<size_t>(row) * kD) + chunk; };
+  // Rows that a round reads and writes (-1: none), looked up while the round before is under way.
+  int from[kMoveKeys], to[kMoveKeys];
+  auto look_up = [&](int base) {
     const int d0 = base + rank * kMoveRound + half * kMoveKeys;
-    uint4 k[kMoveKeys], v[kMoveKeys];
-    bool moves[kMoveKeys];
 #pragma unroll
     for (int i = 0; i < kMoveKeys; ++i) {
-      const int key = d0 + i < left ? p.src[list + d0 + i] : 0;
-      moves[i] = d0 + i < left && dbg_ok(key > d0 + i && key < len);
-      if (moves[i]) {
-        const long long from = at(key);
-        k[i] = __ldcg(reinterpret_cast<const uint4*>(p.k + from));
-        v[i] = __ldcg(reinterpret_cast<const uint4*>(p.v + from));
+      const int key = d0 + i < left ? p.src[list + d0 + i] : -1;
+      const bool moves = key >= 0 && dbg_ok(key > d0 + i && key < len);
+      from[i] = moves ? row_of(key) : -1;
+      to[i] = moves ? row_of(d0 + i) : -1;
+    }
+  };
+  look_up(head.y);
+  for (int base = head.y; base < left; base += kCluster * kMoveRound) {
+    uint4 k[kMoveKeys], v[kMoveKeys];
+    int dst[kMoveKeys];
+#pragma unroll
+    for (int i = 0; i < kMoveKeys; ++i) {
+      dst[i] = to[i];
+      if (from[i] >= 0) {
+        k[i] = __ldcg(at(p.k, from[i]));
+        v[i] = __ldcg(at(p.v, from[i]));
       }
     }
+    look_up(base + kCluster * kMoveRound);
     __syncwarp();
     ptx::cluster_sync();
 #pragma unroll
     for (int i = 0; i < kMoveKeys; ++i) {
-      if (moves[i]) {
-        const long long to = at(d0 + i);
-        *reinterpret_cast<uint4*>(p.k + to) = k[i];
-        *reinterpret_cast<uint4*>(p.v + to) = v[i];
+      if (dst[i] >= 0) {
+        *at(p.k, dst[i]) = k[i];
+        *at(p.v, dst[i]) = v[i];
       }
     }
     __syncwarp();
