@@ -22,6 +22,8 @@ using namespace attn_host;
 namespace rope = attn::rope;
 
 constexpr int64_t kLim31 = (int64_t(1) << 31) - 1;
+constexpr int64_t kFwdWarps = 24;  // an SM's
+constexpr int64_t kMaxHeads = 1 << 18;  // chunks of a token: a grid's y
 
 // A dimension of one entry has no stride: what is given for it is not looked at (a batch of
 // single tokens counts as tokens one batch stride apart).
@@ -58,7 +60,7 @@ int check_call(const Call& c, const RowSet* tensors, int n) {
     return ATTN_ERR_UNSUPPORTED;
   if (c.flags & ~ATTN_FLAG_INTERLEAVED) return ATTN_ERR_UNSUPPORTED;
   if (c.mode < ATTN_ROUND_RTNE || c.mode > ATTN_ROUND_RTZ) return ATTN_ERR_UNSUPPORTED;
-  if (c.B > kLim31 || c.S > kLim31 / c.B || c.Hq > (1 << 20) || c.Hkv > (1 << 20) || c.max_pos > kLim31)
+  if (c.B > kLim31 || c.S > kLim31 / c.B || c.Hq > kMaxHeads || c.Hkv > kMaxHeads || c.max_pos > kLim31)
     return ATTN_ERR_TOO_LARGE;
   for (int i = 0; i < n; ++i) {
     if (!strides_in_range(tensors[i])) return ATTN_ERR_INVALID_ARG;
@@ -108,18 +110,55 @@ void fill(rope::Params* p, const Call& c) {
   p->half = static_cast<int>(c.rotary_dim / 2);
   p->mode = c.mode;
   p->eps = c.eps;
-  p->q_chunks = static_cast<int>((c.Hq + rope::kRows - 1) / rope::kRows);
-  p->kv_chunks = static_cast<int>((c.Hkv + rope::kRows - 1) / rope::kRows);
+  p->q_chunks = static_cast<int>((c.Hq + rope::kHeads - 1) / rope::kHeads);
+  p->kv_chunks = static_cast<int>((c.Hkv + rope::kHeads - 1) / rope::kHeads);
   p->chunks = p->q_chunks + p->kv_chunks;
-  p->items = c.B * c.S * p->chunks;
+  p->tokens = static_cast<int>(c.B * c.S);
 }
 
-int64_t fwd_blocks(const rope::Params& p) { return (p.items + rope::kWarps - 1) / rope::kWarps; }
+// Warps that share four tokens: as many as fill the GPU with `warps` of them, at most one a chunk.
+int parts_of(int64_t tokens, int64_t chunks, int64_t warps) {
+  const int64_t groups = (tokens + rope::kTokens - 1) / rope::kTokens, want = (warps + groups - 1) / groups;
+  return static_cast<int>(want < chunks ? want : chunks);
+}
 
-int64_t bwd_blocks(int64_t B, int64_t S, int64_t Hq, int64_t Hkv) {
-  const int64_t most = (Hq > Hkv ? Hq : Hkv), chunks = (most + rope::kRows - 1) / rope::kRows;
-  const int64_t fill = 2 * int64_t(sms_here()), need = (B * S * chunks + rope::kBwdWarps - 1) / rope::kBwdWarps;
-  return need < fill ? need : fill;
+rope::Form form_of(const Call& c) {
+  if (c.flags & ATTN_FLAG_INTERLEAVED) return rope::kNext;
+  return c.rotary_dim == attn::kD ? rope::kWhole : rope::kApart;
+}
+
+bool launch_fwd(rope::Params& p, bool paged, rope::Form form, void* stream) {
+  using Kernel = void (*)(const rope::Params);
+  static constexpr Kernel kFwd[3][2] = {
+      {rope::attn_rope_fwd<rope::kWhole, false>, rope::attn_rope_fwd<rope::kWhole, true>},
+      {rope::attn_rope_fwd<rope::kNext, false>, rope::attn_rope_fwd<rope::kNext, true>},
+      {rope::attn_rope_fwd<rope::kApart, false>, rope::attn_rope_fwd<rope::kApart, true>}};
+  p.parts = parts_of(p.tokens, p.chunks, kFwdWarps * int64_t(sms_here()));
+  constexpr int64_t kBlock = rope::kWarps * rope::kTokens;
+  const dim3 grid(static_cast<unsigned>((int64_t(p.tokens) + kBlock - 1) / kBlock), static_cast<unsigned>(p.parts));
+  return launch(kFwd[form][paged], grid, rope::kThreads, 0, static_cast<cudaStream_t>(stream), false, p);
+}
+
+struct BwdGrid {
+  int64_t blocks;
+  int parts;
+};
+BwdGrid bwd_grid(int64_t B, int64_t S, int64_t Hq, int64_t Hkv, int ctas) {
+  const int64_t fill = ctas * int64_t(sms_here()), groups = (B * S + rope::kTokens - 1) / rope::kTokens;
+  BwdGrid g;
+  g.parts = parts_of(B * S, Hq + Hkv, fill * rope::kWarps);
+  const int64_t need = (groups * g.parts + rope::kWarps - 1) / rope::kWarps;
+  g.blocks = need < fill ? need : fill;
+  return g;
+}
+// The form that has the most blocks.
+int64_t bwd_bytes(int64_t B, int64_t S, int64_t Hq, int64_t Hkv) {
+  int64_t most = 0;
+  for (int ctas : {rope::kBwdCtas<rope::kWhole>, rope::kBwdCtas<rope::kApart>}) {
+    const int64_t blocks = bwd_grid(B, S, Hq, Hkv, ctas).blocks;
+    if (blocks > most) most = blocks;
+  }
+  return most * 2 * attn::kD * 4;
 }
 
 }  // namespace
@@ -145,16 +184,13 @@ int attn_qk_norm_rope(const void* q, const void* k, const void* q_weight, const 
   if (rows_meet(t[2], t[3])) return ATTN_ERR_ALIASING;
   rope::Params p = {};
   fill(&p, c);
-  if (fwd_blocks(p) > kLim31) return ATTN_ERR_TOO_LARGE;
   st = arch_here();
   if (st != ATTN_OK) return st;
   p.q = rows_of(t[0]);
   p.k = rows_of(t[1]);
   p.q_out = rows_of(t[2]);
   p.k_out = rows_of(t[3]);
-  const auto fn = flags & ATTN_FLAG_INTERLEAVED ? rope::attn_rope_fwd<true, false> : rope::attn_rope_fwd<false, false>;
-  return launch(fn, fwd_blocks(p), rope::kThreads, 0, static_cast<cudaStream_t>(stream), false, p) ? ATTN_OK
-                                                                                                    : ATTN_ERR_LAUNCH;
+  return launch_fwd(p, false, form_of(c), stream) ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
 int attn_qk_norm_rope_paged(const void* q, const void* k, const void* v, const void* q_weight, const void* k_weight,
@@ -194,8 +230,6 @@ int attn_qk_norm_rope_paged(const void* q, const void* k, const void* v, const v
   rope::Params p = {};
   fill(&p, c);
   p.chunks += p.kv_chunks;  // the values
-  p.items = B * S * p.chunks;
-  if (fwd_blocks(p) > kLim31) return ATTN_ERR_TOO_LARGE;
   st = arch_here();
   if (st != ATTN_OK) return st;
   p.q = rows_of(t[0]);
@@ -209,16 +243,14 @@ int attn_qk_norm_rope_paged(const void* q, const void* k, const void* v, const v
   p.page_size = static_cast<int>(page_size);
   p.n_slots = static_cast<int>(n_pages * page_size);
   p.layout = layout;
-  const auto fn = flags & ATTN_FLAG_INTERLEAVED ? rope::attn_rope_fwd<true, true> : rope::attn_rope_fwd<false, true>;
-  return launch(fn, fwd_blocks(p), rope::kThreads, 0, static_cast<cudaStream_t>(stream), false, p) ? ATTN_OK
-                                                                                                    : ATTN_ERR_LAUNCH;
+  return launch_fwd(p, true, form_of(c), stream) ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
 int64_t attn_qk_norm_rope_bwd_workspace_bytes(int64_t B, int64_t S, int64_t Hq, int64_t Hkv, int64_t d) {
   if (B < 1 || S < 1 || Hq < 1 || Hkv < 1) return ATTN_ERR_INVALID_ARG;
   if (d != attn::kD) return ATTN_ERR_UNSUPPORTED;
-  if (B > kLim31 || S > kLim31 / B || Hq > (1 << 20) || Hkv > (1 << 20)) return ATTN_ERR_TOO_LARGE;
-  return bwd_blocks(B, S, Hq, Hkv) * 2 * attn::kD * 4;
+  if (B > kLim31 || S > kLim31 / B || Hq > kMaxHeads || Hkv > kMaxHeads) return ATTN_ERR_TOO_LARGE;
+  return bwd_bytes(B, S, Hq, Hkv);
 }
 
 int attn_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k, const void* q_weight,
@@ -238,7 +270,7 @@ int attn_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q,
                       row_set(dq, dq_strides, B, S, Hq),         row_set(dk, dk_strides, B, S, Hkv)};
   int st = check_call(c, t, 6);
   if (st != ATTN_OK) return st;
-  const int64_t blocks = bwd_blocks(B, S, Hq, Hkv), need = blocks * 2 * attn::kD * 4;
+  const int64_t need = bwd_bytes(B, S, Hq, Hkv);
   if (workspace_bytes < need) return ATTN_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(workspace) & 15u) return ATTN_ERR_MISALIGNED;
   if ((reinterpret_cast<uintptr_t>(dq_weight) | reinterpret_cast<uintptr_t>(dk_weight)) & 3u)
@@ -267,11 +299,17 @@ int attn_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q,
   p.f.k = rows_of(t[3]);
   p.dq = rows_of(t[4]);
   p.dk = rows_of(t[5]);
+  const rope::Form form = form_of(c);
+  const BwdGrid grid = bwd_grid(B, S, Hq, Hkv, form == rope::kWhole ? rope::kBwdCtas<rope::kWhole>
+                                                                    : rope::kBwdCtas<rope::kApart>);
+  p.f.parts = grid.parts;
   p.part = static_cast<float*>(workspace);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const auto fn = flags & ATTN_FLAG_INTERLEAVED ? rope::attn_rope_bwd<true> : rope::attn_rope_bwd<false>;
-  if (!launch(fn, blocks, rope::kBwdThreads, 0, cs, false, p)) return ATTN_ERR_LAUNCH;
-  const rope::JoinParams j = {p.part, dq_weight, dk_weight, static_cast<int>(blocks)};
+  const auto fn = form == rope::kWhole  ? rope::attn_rope_bwd<rope::kWhole>
+                  : form == rope::kNext ? rope::attn_rope_bwd<rope::kNext>
+                                        : rope::attn_rope_bwd<rope::kApart>;
+  if (!launch(fn, grid.blocks, rope::kThreads, rope::kBwdSmem, cs, false, p)) return ATTN_ERR_LAUNCH;
+  const rope::JoinParams j = {p.part, dq_weight, dk_weight, static_cast<int>(grid.blocks)};
   return launch(rope::attn_rope_join, 2 * attn::kD / rope::kJoinCols, rope::kJoinThreads, 0, cs, true, j)
              ? ATTN_OK
              : ATTN_ERR_LAUNCH;
