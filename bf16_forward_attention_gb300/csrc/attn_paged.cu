@@ -35,8 +35,12 @@ template <typename S>
 constexpr Form form() {
   return {S::kRows, S::kThreads, S::kSmem, S::kCtas, {paged::attn_paged_fwd<S, false>, paged::attn_paged_fwd<S, true>}};
 }
-constexpr Form kForms[] = {form<paged::Rows8>(), form<paged::Rows16>(), form<paged::Rows24>(), form<paged::Rows32>(),
-                           form<paged::Rows48>()};
+template <int kCopies>
+constexpr Form rows_form() {
+  return {128 / kCopies, paged::kRowsThreads, paged::kRowsSmem, 2,
+          {paged::attn_paged_rows<kCopies, false>, paged::attn_paged_rows<kCopies, true>}};
+}
+constexpr Form kForms[] = {form<paged::Rows8>(), form<paged::Rows16>(), rows_form<4>(), rows_form<2>(), rows_form<1>()};
 
 int device_ready() {
   const int st = arch_here();
@@ -196,6 +200,7 @@ int attn_fwd_paged(const void* q, const void* k_pages, const void* v_pages, cons
   p.block_rows = static_cast<int>(pl.block_rows);
   p.rows8 = pl.form->rows;
   p.c = scale * 1.4426950408889634f;
+  p.timeout_ns = kTimeoutNs;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (!launch(pl.form->fwd[mass ? 1 : 0], pl.runs, pl.form->threads, pl.form->smem, cs, false, p))
     return ATTN_ERR_LAUNCH;

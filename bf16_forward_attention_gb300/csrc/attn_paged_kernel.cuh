@@ -1,8 +1,10 @@
 // attn_paged_kernel.cuh - attention of new tokens over a paged key-value cache.
 //
 // The rows (new tokens times the group's heads) of a sequence and a key/value head go
-// through the sequence's keys in blocks of at most 48; an item is one such block with all its
+// through the sequence's keys in blocks of at most 128; an item is one such block with all its
 // keys, cut into units of 64. The keys are read once per block, so few rows are bound by HBM.
+// Up to 16 rows go through warp-level products (attn_paged_fwd), more through the tensor cores
+// (attn_paged_rows).
 // All items' units in a row, sequence by sequence, are cut into equal runs, one a CTA: lengths
 // are on the device, and a long sequence among short ones is spread over as many CTAs as its
 // keys are worth. A CTA that has an item whole finishes it; an item that is cut leaves
@@ -19,7 +21,7 @@ namespace paged {
 constexpr int kTeams = 4;                          // of a CTA, 16 keys of a unit each
 constexpr int kUnit = kTeams * few::kKeys;
 constexpr int kStageBytes = 2 * few::kKvBytes;     // a team's K and V
-constexpr int kMaxRows = 48;                       // rows of a block at most
+constexpr int kMaxRows = 128;                      // rows of a block at most
 constexpr int kMinUnits = 1;                       // of a run: with fewer units there are fewer runs
 
 // kNT 8-row groups a warp, kGroups warps a team: blocks of up to 8 kNT kGroups rows.
@@ -32,13 +34,8 @@ struct Shape {
   static constexpr int kOffMl = kOffX + kTeams * kGroups * kNT * 4 * 512;  // [team][row][2] floats
   static constexpr int kSmem = kOffMl + kTeams * kRows * 8;
 };
-// Two CTAs an SM while a team is small; more rows take more warps of one CTA, whose loads are
-// shared by the team.
 using Rows8 = Shape<1, 1, 3, 2>;
 using Rows16 = Shape<1, 2, 3, 2>;
-using Rows24 = Shape<1, 3, 5, 1>;
-using Rows32 = Shape<1, 4, 5, 1>;
-using Rows48 = Shape<2, 3, 5, 1>;
 
 // What a run leaves for the join: the item that it begins and does not end, and in how many
 // parts (0: none).
@@ -66,6 +63,7 @@ struct Params {
   int rows, rows4;         // Sq * group; that, in fours
   int blocks, block_rows, rows8;  // blocks of at most block_rows rows; rows8: the kernel's rows of a block
   float c;                 // scale * log2(e)
+  unsigned long long timeout_ns;  // of a wait for the tensor cores
 };
 
 __device__ __forceinline__ int units_of(int len, int cap) {
@@ -427,6 +425,420 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) attn_paged_fwd(const Pa
     }
     if (i + 1 < n) at.step(p, per);
   }
+}
+
+// ---------------------------------------------------------------- many rows
+// Blocks of 17 to 128 rows, on the tensor cores: S = Q K^T and O = P V as 128 x 64 x 128 and 128 x 128
+// x 64 products, Q and P in tensor memory. A block of up to 32 (64) rows stands in the 128 lanes
+// four times (twice): each copy takes its own 16 (32) of a unit's 64 keys and has zeros for P
+// elsewhere, so that all four warps have a share of the exponentials; the copies are added at the
+// item's end. A lane keeps its row of O in registers: each unit's product starts from 0 and is
+// added to it, to nearest.
+//
+// The CTA goes through a unit in step: loads (cp.async, two units ahead), S, exponentials, P V, the
+// addition; two CTAs an SM fill each other's waits. By warp-level products 35 rows took 205 us
+// where this takes TODO us (48 x 5 drafted tokens of 28/4 heads, caches of up to 5003 keys: 244 MB):
+// a product of 16 x 8 x 16 occupies a quarter of an SM's tensor core for some 24 to 32 cycles that way, 144
+// of them for every 16 keys.
+constexpr int kRowsThreads = 128;
+constexpr int kRowsStages = 3;
+constexpr int kRowsTile = kUnit * kD * 2;                 // 16 KiB: a unit's K or V, as two halves of 64 columns
+constexpr int kRowsStage = 2 * kRowsTile;
+constexpr int kRowsOffX = kRowsStages * kRowsStage;       // 16 columns of every lane's row
+constexpr int kXPitch = 20;                               // floats: distinct banks
+constexpr int kRowsOffMl = kRowsOffX + 128 * kXPitch * 4; // [lane of 128][2] floats
+constexpr int kRowsOffBar = kRowsOffMl + 128 * 8;
+constexpr int kRowsSmem = kRowsOffBar + 64 + 1024;        // slack to align the base to 1024 bytes
+static_assert(2 * (kRowsSmem + 1024 + 256) <= 228 * 1024, "two CTAs an SM");
+constexpr uint32_t kColS = 0, kColQ = 64, kColO = 128, kRowsCols = 256;  // tensor memory; P stands in S's place
+
+// Shared-memory offset of 16-byte chunk c of key r in a tile: 128-byte swizzle, 64 columns a half.
+__device__ __forceinline__ uint32_t swizzled(int r, int c) {
+  return static_cast<uint32_t>((c >> 3) * (kRowsTile / 2) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+// S = Q K^T, Q in tensor memory (K-major, 8 columns for 16 of head_dim), K the K-major B operand:
+// steps 4..7 use the second half, 8 KiB further.
+template <int... kK>
+__device__ __forceinline__ void issue_rows_s(uint32_t tmem, uint32_t k_lo, std::integer_sequence<int, kK...>) {
+  constexpr uint32_t idesc = idesc_bf16(128, kUnit, 0);
+  (ptx::mma_ts_warp<8 * kK, ((kK >> 2) << 9) + ((kK & 3) << 1)>(tmem + kColS, tmem + kColQ, k_lo, kDescHi, idesc,
+                                                                kK > 0 ? 1u : 0u),
+   ...);
+}
+// O = P_hi V + P_lo V from 0: 16 columns of P for 16 keys, P_hi in the first 8; V the MN-major B operand,
+// 16 keys 2048 bytes.
+template <int... kK>
+__device__ __forceinline__ void issue_rows_pv(uint32_t tmem, uint32_t v_lo, std::integer_sequence<int, kK...>) {
+  constexpr uint32_t idesc = idesc_bf16(128, kD, 1);
+  ((ptx::mma_ts_warp<16 * kK + 8, (kK << 7)>(tmem + kColO, tmem + kColS, v_lo, kDescHi, idesc, kK == 0 ? 0u : 1u),
+    ptx::mma_ts_warp<16 * kK, (kK << 7)>(tmem + kColO, tmem + kColS, v_lo, kDescHi, idesc, 1u)),
+   ...);
+}
+
+// Where column d of row r stands in a part's rows (attn_paged_fwd's order): in floats.
+__device__ __forceinline__ int part_place(int r, int d) {
+  const int lane = (d & 7) * 4 + ((r & 7) >> 1), e = (r & 1) + ((d & 8) >> 2);
+  return (((r >> 3) * 8 + (d >> 4)) * 32 + lane) * 4 + e;
+}
+
+template <int kCopies, bool kMass>
+__global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params p) {
+  constexpr int kLanes = 128 / kCopies;      // rows of a copy
+  constexpr int kChunks = kUnit / 16 / kCopies;  // 16-key chunks of a copy
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int copy = static_cast<int>(threadIdx.x) / kLanes;  // the same for a warp
+  const int r = static_cast<int>(threadIdx.x) % kLanes;     // this lane's row of the block
+  const float neg_inf = -__int_as_float(0x7F800000);
+  const int per = p.Hkv * p.blocks;
+  if (threadIdx.x == 0) p.cuts[blockIdx.x].parts = 0;
+  Run run;
+  if (!find_run<kRowsThreads>(p.seqlens, p.B, p.cap, per, kMinUnits, run)) return;
+
+  const uint32_t base = ptx::smem_u32(smem);
+  const uint32_t bar_s = base + kRowsOffBar, bar_o = bar_s + 8, bar_end = bar_s + 16;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kRowsOffBar + 24);
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + kRowsOffBar + 28);
+  if (threadIdx.x == 0) {
+    ptx::mbar_init(bar_s, 1);
+    ptx::mbar_init(bar_o, 1);
+    ptx::mbar_init(bar_end, 1);
+    ptx::fence_mbar_init();
+    *abort_flag = 0;
+  }
+  if (warp == 0) {
+    ptx::tmem_alloc(base + kRowsOffBar + 28, kRowsCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot, mine = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+
+  // ---- loads: a warp 16 keys of every unit, kRowsStages - 1 units ahead.
+  const int half = lane >> 4, chunk = lane & 15;
+  Walk ahead;
+  ahead.start(p, run);
+  uint32_t bad_stages = 0;
+  auto row_of = [&]() {  // as in attn_paged_fwd
+    const int key = ahead.t * kUnit + warp * 16 + chunk;
+    if (key >= ahead.len) return -1;
+    const int page = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
+    const int at = key - page * p.page_size;
+    const int id = __ldg(p.table + static_cast<size_t>(ahead.b) * p.max_pages + page);
+    if (id < 0 || id >= p.n_pages) return -2;
+    const int kvh = ahead.item / p.blocks;
+    return id * p.page_rows + (p.layout == 0 ? kvh * p.page_size + at : at * p.Hkv + kvh);
+  };
+  auto load = [&](int row, int s) {
+    const bool bad = __any_sync(0xFFFFFFFFu, row == -2);
+    bad_stages = (bad_stages & ~(1u << s)) | (bad ? 1u << s : 0u);
+    const uint32_t dst = base + s * kRowsStage;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const int from = __shfl_sync(0xFFFFFFFFu, row, half + 2 * x);
+      const uint32_t d = dst + swizzled(warp * 16 + half + 2 * x, chunk);
+      const size_t at = static_cast<size_t>(max(from, 0)) * kD + 8 * chunk;
+      ptx::cp_async16(d, p.k + at, from >= 0);
+      ptx::cp_async16(d + kRowsTile, p.v + at, from >= 0);
+    }
+  };
+  const int n = static_cast<int>(run.hi - run.lo);
+  int next = row_of();
+#pragma unroll
+  for (int s = 0; s < kRowsStages - 1; ++s) {
+    if (s < n) {
+      load(next, s);
+      if (s + 1 < n) {
+        ahead.step(p, per);
+        next = row_of();
+      }
+    }
+    ptx::cp_async_commit();
+  }
+
+  Walk at;
+  at.start(p, run);
+  Item it;
+  uint64_t o[kD / 2];                       // the lane's row, column pairs
+  float ref = neg_inf, sum = 0.f;
+  int lim = 0, min_lim = 0, t_first = 0;
+  bool bad = false, fresh = true, ok = true;
+  uint32_t phase_s = 0, phase_o = 0;
+  for (int i = 0; i < n; ++i) {
+    if (fresh) {  // an item begins
+      fresh = false;
+      it = item_of(p, at.b, at.item);
+      t_first = at.t;
+      bad = false;
+      ref = neg_inf;
+      sum = 0.f;
+#pragma unroll
+      for (int d = 0; d < kD / 2; ++d) o[d] = 0;
+      const bool there = r < it.n_rows && at.len >= 0;
+      lim = there ? few::own_limit((it.row0 + r) / p.group, at.len, p.Sq, p.causal) : 0;
+      min_lim = few::own_limit(it.row0 / p.group, at.len, p.Sq, p.causal);
+      const uint4* from = reinterpret_cast<const uint4*>(
+          p.q + (there ? few::query_at(p.layout, p.Hq, p.Sq, p.group, it.b, it.kvh, it.row0 + r) : 0));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // 32 of head_dim: 16 columns
+        uint32_t w[16];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint4 x = there ? __ldg(from + 4 * j + u) : make_uint4(0, 0, 0, 0);
+          w[4 * u] = x.x, w[4 * u + 1] = x.y, w[4 * u + 2] = x.z, w[4 * u + 3] = x.w;
+        }
+        ptx::tmem_st16(mine + kColQ + 16 * j, w);
+      }
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+    }
+    const int s = i % kRowsStages;
+    const uint32_t kt = base + s * kRowsStage, vt = kt + kRowsTile;
+    ptx::cp_async_wait<kRowsStages - 2>();
+    // A non-finite element of V times a weight of 0 (a hidden key's, another copy's) would be a NaN:
+    // such a unit goes key by key. Each lane looks at what it copied.
+    uint32_t acc = 0;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const uint4 v = ptx::ld_shared_v4(vt + swizzled(warp * 16 + half + 2 * x, chunk));
+      acc = ptx::bf16x2_nonfinite_acc(v.x, ptx::bf16x2_nonfinite_acc(v.y, acc));
+      acc = ptx::bf16x2_nonfinite_acc(v.z, ptx::bf16x2_nonfinite_acc(v.w, acc));
+    }
+    ptx::fence_proxy_async_smem();  // the copies, before the tensor cores read them
+    const bool apart = __syncthreads_or(acc != 0);
+    if (warp == 0) {
+      ptx::tc_fence_after();
+      issue_rows_s(tmem, desc_lo(kt, 16), std::make_integer_sequence<int, 8>{});
+      ptx::mma_commit_warp(bar_s);
+    }
+    bad = bad || (bad_stages >> s & 1u);
+    if (i + kRowsStages - 1 < n) load(next, (i + kRowsStages - 1) % kRowsStages);  // where unit i - 1 was
+    ptx::cp_async_commit();
+    if (i + kRowsStages < n) {
+      ahead.step(p, per);
+      next = row_of();
+    }
+    // ---- the copy's 16 kChunks keys of S.
+    ok = warp_wait(bar_s, phase_s & 1, abort_flag, p.timeout_ns) && ok;
+    ++phase_s;
+    ptx::tc_fence_after();
+    uint32_t x[kChunks][16];
+#pragma unroll
+    for (int u = 0; u < kChunks; ++u) ptx::tmem_ld16_nowait(mine + kColS + 16 * (copy * kChunks + u), x[u]);
+#pragma unroll
+    for (int u = 0; u < kChunks; ++u) ptx::tmem_wait_ld16(x[u]);
+    const int key0 = at.t * kUnit + copy * 16 * kChunks;
+    const bool masked = key0 + 16 * kChunks > min_lim;
+    float mx = neg_inf;
+#pragma unroll
+    for (int u = 0; u < kChunks; ++u)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        float v = __uint_as_float(x[u][j]) * p.c;
+        if (masked && key0 + 16 * u + j >= lim) v = neg_inf;
+        x[u][j] = __float_as_uint(v);
+        mx = fmaxf(mx, v);  // a NaN is left out here and comes back through its weight
+      }
+    if constexpr (kMass) {
+      if (r < it.n_rows) {
+        float* to = p.logits + ((static_cast<size_t>(it.b) * p.Hkv + it.kvh) * p.cap + key0) * p.rows4 + it.row0 + r;
+#pragma unroll
+        for (int u = 0; u < kChunks; ++u)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            if (key0 + 16 * u + j < at.len) *to = __uint_as_float(x[u][j]);
+            to += p.rows4;
+          }
+      }
+    }
+    float f = 1.f;
+    if (mx > ref + kTau) {
+      f = ptx::ex2(ref - mx);  // 0 from -Inf
+      ref = mx;
+    }
+    const float sub = ref == neg_inf ? 0.f : ref;
+    sum *= f;
+#pragma unroll
+    for (int u = 0; u < kUnit / 16; ++u) {  // all 64 keys' columns: zeros where another copy's are
+      uint32_t w[16];
+      const int v = u - copy * kChunks;
+      bool own = false;
+#pragma unroll
+      for (int y = 0; y < kChunks; ++y)
+        if (v == y) {
+          own = true;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float w0 = ptx::ex2(__uint_as_float(x[y][2 * j]) - sub);
+            const float w1 = ptx::ex2(__uint_as_float(x[y][2 * j + 1]) - sub);
+            sum += w0 + w1;
+            const uint32_t h = ptx::pack_bf16x2(w0, w1);
+            w[j] = h;
+            w[8 + j] = ptx::pack_bf16x2(w0 - __uint_as_float(h << 16), w1 - __uint_as_float(h & 0xFFFF0000u));
+          }
+        }
+      if (!own) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) w[j] = 0;
+      }
+      ptx::tmem_st16(mine + kColS + 16 * u, w);
+    }
+    ptx::tmem_wait_st();
+    ptx::tc_fence_before();
+    if (__syncthreads_or(!ok)) {
+      ok = false;
+      break;
+    }
+    const uint64_t f2 = ptx::f2_pack(f, f);
+    if (!apart) {
+      if (warp == 0) {
+        ptx::tc_fence_after();
+        issue_rows_pv(tmem, desc_lo(vt, kRowsTile / 2), std::make_integer_sequence<int, 4>{});
+        ptx::mma_commit_warp(bar_o);
+      }
+      ok = warp_wait(bar_o, phase_o & 1, abort_flag, p.timeout_ns);
+      ++phase_o;
+      ptx::tc_fence_after();
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t y[32];
+        ptx::tmem_ld32(mine + kColO + 32 * q, y);
+#pragma unroll
+        for (int d = 0; d < 16; ++d)
+          o[16 * q + d] = ptx::f2_fma(o[16 * q + d], f2, ptx::f2_pack(__uint_as_float(y[2 * d]), __uint_as_float(y[2 * d + 1])));
+      }
+      ptx::tc_fence_before();
+    } else {
+      // Key by key over what the row sees, weights read back two at a time.
+#pragma unroll
+      for (int d = 0; d < kD / 2; ++d) o[d] = ptx::f2_mul(o[d], f2);
+#pragma unroll 1
+      for (int j = 0; j < 8 * kChunks; ++j) {
+        const uint32_t col = mine + kColS + 16 * (copy * kChunks + (j >> 3)) + (j & 7);
+        const uint32_t h = ptx::tmem_ld1(col), l = ptx::tmem_ld1(col + 8);
+#pragma unroll 1
+        for (int e = 0; e < 2; ++e) {
+          if (key0 + 2 * j + e < lim) {
+            const float w = e == 0 ? __uint_as_float(h << 16) + __uint_as_float(l << 16)
+                                   : __uint_as_float(h & 0xFFFF0000u) + __uint_as_float(l & 0xFFFF0000u);
+            const uint64_t w2 = ptx::f2_pack(w, w);
+            const int key = copy * 16 * kChunks + 2 * j + e;
+#pragma unroll
+            for (int d = 0; d < 16; ++d) {
+              const uint4 v = ptx::ld_shared_v4(vt + swizzled(key, d));
+              const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                o[4 * d + y] = ptx::f2_fma(
+                    w2, ptx::f2_pack(__uint_as_float(vw[y] << 16), __uint_as_float(vw[y] & 0xFFFF0000u)), o[4 * d + y]);
+            }
+          }
+        }
+        __syncwarp();  // the loads from tensor memory are the whole warp's
+      }
+      __syncwarp();
+      ptx::tc_fence_before();
+    }
+    const bool ends = at.t + 1 == at.units;
+    if (!ends && i + 1 < n) {
+      ++at.t;
+      continue;
+    }
+    // ---- the item's end, or the run's: the copies are added, 16 columns at a time.
+    fresh = true;
+    const bool whole = ends && t_first == 0;
+    const int failed = __syncthreads_or((bad ? 1 : 0) | (ok ? 0 : 2));
+    if (__syncthreads_or(!ok)) {
+      ok = false;
+      break;
+    }
+    const bool skip = failed != 0;
+    float2* ml = reinterpret_cast<float2*>(smem + kRowsOffMl);
+    ml[threadIdx.x] = make_float2(ref, sum);
+    __syncthreads();
+    float M = neg_inf, L = 0.f;
+#pragma unroll
+    for (int y = 0; y < kCopies; ++y) M = fmaxf(M, ml[y * kLanes + r].x);
+    const float m0 = M == neg_inf ? 0.f : M, scale = ptx::ex2(ref - m0);
+#pragma unroll
+    for (int y = 0; y < kCopies; ++y) {
+      const float2 z = ml[y * kLanes + r];
+      L = fmaf(z.y, ptx::ex2(z.x - m0), L);
+    }
+    const size_t part = 2 * static_cast<size_t>(blockIdx.x) + (t_first == 0 ? 1 : 0);
+    const float inv = __frcp_rn(L);
+    float* xs = reinterpret_cast<float*>(smem + kRowsOffX);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      constexpr int kN = 16 / kCopies;  // columns of a lane in the end
+      float y[16];
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {
+        float lo, hi;
+        ptx::f2_unpack(o[8 * q + d], lo, hi);
+        y[2 * d] = lo * scale;
+        y[2 * d + 1] = hi * scale;
+      }
+      if constexpr (kCopies > 1) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+          *reinterpret_cast<float4*>(xs + threadIdx.x * kXPitch + 4 * d) = make_float4(y[4 * d], y[4 * d + 1], y[4 * d + 2], y[4 * d + 3]);
+        __syncthreads();
+#pragma unroll
+        for (int d = 0; d < kN; ++d) y[d] = 0.f;
+#pragma unroll
+        for (int z = 0; z < kCopies; ++z)
+#pragma unroll
+          for (int d = 0; d < kN; ++d) y[d] += xs[(z * kLanes + r) * kXPitch + copy * kN + d];
+        __syncthreads();
+      }
+      const int d0 = 16 * q + copy * kN;
+      if (r >= it.n_rows) {
+      } else if (!whole) {
+        float* to = p.part_o + part * p.rows8 * kD;
+#pragma unroll
+        for (int d = 0; d < kN; ++d) to[part_place(r, d0 + d)] = y[d];
+      } else if (!skip && at.len >= 0 && dbg_ok(it.row0 + r < p.rows && it.b < p.B && it.kvh < p.Hkv)) {
+        uint16_t* to = p.out + few::query_at(p.layout, p.Hq, p.Sq, p.group, it.b, it.kvh, it.row0 + r) + d0;
+#pragma unroll
+        for (int d = 0; d < kN; d += 4)
+          *reinterpret_cast<uint2*>(to + d) =
+              make_uint2(round_bf16_bits(y[d] * inv, p.mode) | (round_bf16_bits(y[d + 1] * inv, p.mode) << 16),
+                         round_bf16_bits(y[d + 2] * inv, p.mode) | (round_bf16_bits(y[d + 3] * inv, p.mode) << 16));
+      }
+    }
+    if (copy == 0) {
+      if (!whole)
+        reinterpret_cast<float2*>(p.part_rl)[part * p.rows8 + r] = make_float2(M, skip ? -1.f : L);
+      else if (skip || at.len < 0)
+        skip_row(p, it, r);
+      else
+        store_lse_of(p, it, r, M, L);
+    }
+    if (threadIdx.x == 0) {
+      if (skip || at.len < 0) atomicOr(&g_attn_status, skip ? 8u : 2u);
+      if (!ends && t_first == 0) {
+        const long long end = run.lo + i + (at.units - at.t);
+        const int last = static_cast<int>((end * run.runs + run.total - 1) / run.total) - 1;
+        p.cuts[blockIdx.x] = {it.b, at.item, last - static_cast<int>(blockIdx.x) + 1, 0};
+      }
+    }
+    if (i + 1 < n) at.step(p, per);
+  }
+  // ---- copies and products that are still under way (after a wait that ran out), then the end.
+  ptx::cp_async_wait<0>();
+  if (warp == 0) {
+    ptx::mma_commit_warp(bar_end);
+    wait_bounded(bar_end, 0, abort_flag, p.timeout_ns, false);
+    __syncwarp();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == 0) ptx::tmem_dealloc(tmem, kRowsCols);
 }
 
 // ---------------------------------------------------------------- join

@@ -345,6 +345,15 @@ __device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t (&r)[1
       : "r"(taddr));
 }
 
+// Warp-collective: 32 lanes x one 32-bit column (load + wait::ld).
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
+               : "=r"(r)
+               : "r"(taddr));
+  return r;
+}
+
 // Waits for every outstanding TMEM load of the thread. The array is an in/out
 // operand, which ties its registers to the wait: no use moves above it.
 __device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {

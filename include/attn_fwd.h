@@ -516,7 +516,7 @@ int64_t attn_qk_norm_rope_bwd_workspace_bytes(int64_t B, int64_t S, int64_t Hq, 
  * Results are bit-identical from run to run; the keys are cut into parts by all sequences'
  * lengths, so a row's last bits may depend on the others' lengths, not on their values.
  * Hidden keys take no part. Meant for few new tokens per sequence: their rows go through the
- * keys 48 at a time. Other arguments, ownership and errors as attn_fwd_ex.
+ * keys 128 at a time. Other arguments, ownership and errors as attn_fwd_ex.
  */
 int attn_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
                    const int32_t* page_table, const int32_t* seqlens, void* out, float* lse,

@@ -64,7 +64,13 @@ CASES = [
     ("bhsd", 1, 1, 1, 1, 128, 80, [10000], False),               # one row over every CTA
     ("bshd", 9, 2, 4, 2, 48, 20, [900, 1, 2, 3, 4, 5, 6, 7, 8], True),  # a long one among short ones
     ("bshd", 2, 32, 2, 2, 16, 9, [140, 33], True),               # 32 rows
-    ("bhsd", 2, 70, 1, 1, 16, 9, [140, 69], True),               # three blocks, more new tokens than keys
+    ("bhsd", 2, 70, 1, 1, 16, 9, [140, 69], True),               # 70 rows, more new tokens than keys
+    ("bshd", 3, 17, 1, 1, 16, 70, [1100, 1, 0], False),          # 17 rows, long, one key, none
+    ("bhsd", 2, 9, 14, 2, 10, 150, [1500, 640], True),           # 63 rows, several parts
+    ("bshd", 1, 128, 1, 1, 32, 40, [1280], True),                # 128 rows over many CTAs
+    ("bhsd", 1, 129, 1, 1, 32, 10, [300], True),                 # two blocks
+    ("bshd", 40, 6, 8, 2, 16, 8, None, True),                    # 24 rows, many short sequences
+    ("bhsd", 2, 20, 4, 1, 48, 11, [528, 100], False),            # 80 rows
 ]
 
 
@@ -128,11 +134,12 @@ def test_equals_the_contiguous_cache():
 
 @pytest.mark.parametrize("value", [math.nan, math.inf])
 @pytest.mark.parametrize("which", [1, 2])
-def test_non_finite_values_at_hidden_keys(which, value):
+@pytest.mark.parametrize("g", [3, 7, 13, 26])  # 15, 35, 65 and 130 rows a key/value head
+def test_non_finite_values_at_hidden_keys(which, value, g):
     """A drafted token's own key or value that earlier tokens do not see reaches only the tokens
     that see it, and only their masses."""
     Sq, n, page = 5, 37, 8
-    t = list(_paged.inputs("bshd", 2, Sq, 6, 2, page, 8, [n, n], seed=44))
+    t = list(_paged.inputs("bshd", 2, Sq, 2 * g, 2, page, 8, [n, n], seed=44))
     masses = [torch.zeros(2, 2, 64, device="cuda") for _ in range(2)]
     clean, _ = attn.attn_fwd_paged(*_cuda(t), layout="bshd", causal=True, mass=masses[0])
     j = n - 2                                 # the last but one new token's slot
@@ -141,16 +148,16 @@ def test_non_finite_values_at_hidden_keys(which, value):
     out, _ = attn.attn_fwd_paged(*_cuda(t), layout="bshd", causal=True, mass=masses[1])
     _ok()
     sees = torch.arange(Sq) + n - Sq >= j     # tokens 3 and 4
-    hit = torch.zeros(2, Sq, 6, 128, dtype=torch.bool)
+    hit = torch.zeros(2, Sq, 2 * g, 128, dtype=torch.bool)
     if which == 2:
-        hit[0, sees, 3:, 5] = True
+        hit[0, sees, g:, 5] = True
     elif value != value:
-        hit[0, sees, 3:] = True
+        hit[0, sees, g:] = True
     else:                                     # an infinite key: +Inf logits make the row NaN
-        pos = sees[:, None] & (t[0][0, :, 3:, 5].float() > 0)
-        hit[0, :, 3:][pos] = True
+        pos = sees[:, None] & (t[0][0, :, g:, 5].float() > 0)
+        hit[0, :, g:][pos] = True
     out = out.cpu()
-    assert (~torch.isfinite(out[hit])).all()
+    assert torch.isinf(out[hit]).all() if which == 2 and value == math.inf else torch.isnan(out[hit]).all()
     assert torch.isfinite(out[~hit]).all()
     hidden = torch.ones(2, Sq, dtype=torch.bool)
     hidden[0, sees] = False
