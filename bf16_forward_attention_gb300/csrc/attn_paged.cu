@@ -89,11 +89,11 @@ int make_plan(Plan* pl, int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int64_t 
   while (pl->form->rows < pl->block_rows) ++pl->form;
   if (Hkv * pl->blocks > kLim31 || B > (int64_t(1) << 40) / (Hkv * pl->blocks)) return ATTN_ERR_TOO_LARGE;
   const int64_t items = B * Hkv * pl->blocks;
-  // Units of all items below 2^47: a run's bounds are products with the number of runs.
-  const int64_t units = (pl->cap + paged::kUnit - 1) / paged::kUnit;
+  // Places of all items (see find_run) below 2^47: a run's bounds are products with the number of runs.
+  const int64_t units = (pl->cap + paged::kUnit - 1) / paged::kUnit + paged::kRowsItemCost;
   if (items > (int64_t(1) << 47) / units) return ATTN_ERR_TOO_LARGE;
   // The CTAs that the GPU holds at once; fewer where the caches are too small for as many runs.
-  const int64_t most = (items * units + paged::kMinUnits - 1) / paged::kMinUnits;
+  const int64_t most = items * units;
   const int64_t fill = pl->form->ctas * int64_t(sms_here());
   pl->runs = most < fill ? most : fill;
   pl->o_bytes = 2 * pl->runs * pl->form->rows * attn::kD * 4;

@@ -22,7 +22,10 @@ constexpr int kTeams = 4;                          // of a CTA, 16 keys of a uni
 constexpr int kUnit = kTeams * few::kKeys;
 constexpr int kStageBytes = 2 * few::kKvBytes;     // a team's K and V
 constexpr int kMaxRows = 128;                      // rows of a block at most
-constexpr int kMinUnits = 1;                       // of a run: with fewer units there are fewer runs
+// What an item costs a run beside its units, in units (its queries, its rows' addition and stores):
+// 1.5 us against 1.4 a unit, and 5 against 1.8 in attn_paged_rows. Runs of equal numbers of units made
+// those of many short items the last to end (48 x 5 drafted tokens: 63 to 108 us a run).
+constexpr int kItemCost = 1, kRowsItemCost = 3;
 
 // kNT 8-row groups a warp, kGroups warps a team: blocks of up to 8 kNT kGroups rows.
 template <int kNT_, int kGroups_, int kStages_, int kCtas_>
@@ -70,25 +73,26 @@ __device__ __forceinline__ int units_of(int len, int cap) {
   return len < 0 || len > cap ? 1 : max(1, (len + kUnit - 1) / kUnit);
 }
 
-// Where a run of units begins: the units of all items in a row (sequence, then kv head and
-// block), `per` items a sequence.
+// A run of units: all items in a row (sequence, then kv head and block; `per` items a sequence), each
+// as many places long as it has units and `cost` more in front, cut into runs of equal length.
 struct Run {
-  long long lo, hi;     // units
-  long long first;      // of sequence b
+  long long lo, hi;     // places
+  long long first;      // place of sequence b, in which the run begins
   long long total;
   int b, runs;
+  int n;                // units
 };
 
-// Run blockIdx.x of at most gridDim.x runs of at least `least` units. All threads of the block;
+// Run blockIdx.x of at most gridDim.x runs of at least `least` places. All threads of the block;
 // false: there is no such run.
 template <int kBlock>
-__device__ __forceinline__ bool find_run(const int* seqlens, int B, int cap, int per, int least, Run& run) {
-  __shared__ long long warp_sum[kBlock / 32], at_first;
-  __shared__ int at_b;
+__device__ __forceinline__ bool find_run(const int* seqlens, int B, int cap, int per, int cost, int least, Run& run) {
+  __shared__ long long warp_sum[kBlock / 32], at_first[2];
+  __shared__ int at_b[2];
   const int each = (B + kBlock - 1) / kBlock;
   const int b0 = min(B, static_cast<int>(threadIdx.x) * each), b1 = min(B, b0 + each);
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += units_of(__ldg(seqlens + b), cap);
+  for (int b = b0; b < b1; ++b) mine += units_of(__ldg(seqlens + b), cap) + cost;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long upto = mine;
 #pragma unroll
@@ -111,27 +115,40 @@ __device__ __forceinline__ bool find_run(const int* seqlens, int B, int cap, int
   if (static_cast<int>(blockIdx.x) >= run.runs) return false;
   run.lo = total * blockIdx.x / run.runs;
   run.hi = total * (blockIdx.x + 1) / run.runs;
-  if (run.lo >= before * per && run.lo < (before + mine) * per) {
-    long long x = before;
-    int b = b0;
-    for (; b + 1 < b1; ++b) {
-      const int t = units_of(__ldg(seqlens + b), cap);
-      if (run.lo < (x + t) * per) break;
-      x += t;
+  // The sequences of the first place, and of the last.
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const long long place = e == 0 ? run.lo : run.hi - 1;
+    if (place >= before * per && place < (before + mine) * per) {
+      long long x = before;
+      int b = b0;
+      for (; b + 1 < b1; ++b) {
+        const int t = units_of(__ldg(seqlens + b), cap) + cost;
+        if (place < (x + t) * per) break;
+        x += t;
+      }
+      at_b[e] = b;
+      at_first[e] = x * per;
     }
-    at_b = b;
-    at_first = x * per;
   }
   __syncthreads();
-  run.b = at_b;
-  run.first = at_first;
-  return true;
+  run.b = at_b[0];
+  run.first = at_first[0];
+  // Units before place x of sequence b, which begins at place `first`.
+  auto units_before = [&](long long x, int b, long long first) {
+    const int units = units_of(__ldg(seqlens + b), cap);
+    const long long item = (x - first) / (units + cost), in = (x - first) % (units + cost) - cost;
+    return first - static_cast<long long>(per) * cost * b + item * units + (in > 0 ? in : 0);
+  };
+  run.n = static_cast<int>(units_before(run.hi, at_b[1], at_first[1]) - units_before(run.lo, run.b, run.first));
+  return run.n > 0;
 }
 
 // A run's units one after another.
 struct Walk {
   int b, item, t;       // sequence, its item, the item's unit
   int len, units;       // the sequence's keys (-1: out of range), its items' units
+  long long first;      // place of the sequence
 
   __device__ __forceinline__ void enter(const Params& p) {
     len = __ldg(p.seqlens + b);
@@ -139,19 +156,27 @@ struct Walk {
     if (len > p.cap) len = -1;
     len = max(len, -1);
   }
-  __device__ __forceinline__ void start(const Params& p, const Run& run) {
+  __device__ __forceinline__ void start(const Params& p, const Run& run, int cost) {
     b = run.b;
+    first = run.first;
     enter(p);
     const long long rel = run.lo - run.first;
-    item = static_cast<int>(rel / units);
-    t = static_cast<int>(rel - static_cast<long long>(item) * units);
+    item = static_cast<int>(rel / (units + cost));
+    t = max(0, static_cast<int>(rel - static_cast<long long>(item) * (units + cost)) - cost);
   }
-  __device__ __forceinline__ void step(const Params& p, int per) {
+  __device__ __forceinline__ void step(const Params& p, int per, int cost) {
     if (++t < units) return;
     t = 0;
     if (++item < per) return;
     item = 0;
+    first += static_cast<long long>(per) * (units + cost);
     if (++b < p.B) enter(p);
+  }
+  // In how many runs the item lies, of which this one has its first unit: its last unit is in the last
+  // run that begins before its end.
+  __device__ __forceinline__ int parts(const Run& run, int cost) const {
+    const long long end = first + static_cast<long long>(item + 1) * (units + cost);
+    return static_cast<int>((end * run.runs + run.total - 1) / run.total) - static_cast<int>(blockIdx.x);
   }
 };
 
@@ -208,13 +233,14 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) attn_paged_fwd(const Pa
   const int per = p.Hkv * p.blocks;
   if (threadIdx.x == 0) p.cuts[blockIdx.x].parts = 0;
   Run run;
-  if (!find_run<S::kThreads>(p.seqlens, p.B, p.cap, per, kMinUnits, run)) return;
+  constexpr int kCost = kItemCost;
+  if (!find_run<S::kThreads>(p.seqlens, p.B, p.cap, per, kCost, kCost + 1, run)) return;
   const uint32_t ring = ptx::smem_u32(smem) + team * kStages * kStageBytes;
   const int half = lane >> 4, chunk = lane & 15;
 
   // ---- loads: unit by unit, kStages - 1 ahead of the products.
   Walk ahead;
-  ahead.start(p, run);
+  ahead.start(p, run, kCost);
   uint32_t bad_stages = 0;  // of those in the ring, which hold a key without a page
   // Row of 128 (in the pages) of key `lane % 16` of the team's share of the unit, -1: none, -2: bad.
   auto row_of = [&]() {
@@ -242,14 +268,14 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) attn_paged_fwd(const Pa
       ptx::cp_async16(d + few::kKvBytes, p.v + at, r >= 0);
     }
   };
-  const int n = static_cast<int>(run.hi - run.lo);
+  const int n = run.n;
   int next = row_of();
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) {
     if (s < n) {
       load(next, s);
       if (s + 1 < n) {
-        ahead.step(p, per);
+        ahead.step(p, per, kCost);
         next = row_of();
       }
     }
@@ -258,7 +284,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) attn_paged_fwd(const Pa
 
   // ---- products.
   Walk at;
-  at.start(p, run);
+  at.start(p, run, kCost);
   few::Rows<kNT> rows;
   Item it;
   int t_first = 0, min_lim = 0;
@@ -297,7 +323,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) attn_paged_fwd(const Pa
     if (i + kStages - 1 < n) load(next, (i + kStages - 1) % kStages);
     ptx::cp_async_commit();
     if (i + kStages < n) {
-      ahead.step(p, per);
+      ahead.step(p, per, kCost);
       next = row_of();
     }
     const uint32_t kt = ring + s * kStageBytes;
@@ -417,13 +443,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) attn_paged_fwd(const Pa
           store_out(p, it, g, dt, lane, x, __frcp_rn(L[nt][0]), __frcp_rn(L[nt][1]));
       }
     }
-    if (!ends && t_first == 0 && threadIdx.x == 0) {
-      // The item's last unit is in the last run that begins before its end.
-      const long long end = run.lo + i + (at.units - at.t);
-      const int last = static_cast<int>((end * run.runs + run.total - 1) / run.total) - 1;
-      p.cuts[blockIdx.x] = {it.b, at.item, last - static_cast<int>(blockIdx.x) + 1, 0};
-    }
-    if (i + 1 < n) at.step(p, per);
+    if (!ends && t_first == 0 && threadIdx.x == 0) p.cuts[blockIdx.x] = {it.b, at.item, at.parts(run, kCost), 0};
+    if (i + 1 < n) at.step(p, per, kCost);
   }
 }
 
@@ -432,11 +453,11 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) attn_paged_fwd(const Pa
 // x 64 products, Q and P in tensor memory. A block of up to 32 (64) rows stands in the 128 lanes
 // four times (twice): each copy takes its own 16 (32) of a unit's 64 keys and has zeros for P
 // elsewhere, so that all four warps have a share of the exponentials; the copies are added at the
-// item's end. A lane keeps its row of O in registers: each unit's product starts from 0 and is
-// added to it, to nearest.
+// item's end. A lane keeps its row of O in registers: what the tensor cores have summed over at most
+// four units is added to it, to nearest; a warp with a row whose reference rises does so at once.
 //
-// The CTA goes through a unit in step: loads (cp.async, two units ahead), S, exponentials, P V, the
-// addition; two CTAs an SM fill each other's waits. By warp-level products 35 rows took 205 us
+// The CTA goes through a unit in step: loads (cp.async, two units ahead), S, exponentials, P V; two CTAs
+// an SM fill each other's waits. P V is not waited for: the next S, behind it on the same pipe, is. By warp-level products 35 rows took 205 us
 // where this takes TODO us (48 x 5 drafted tokens of 28/4 heads, caches of up to 5003 keys: 244 MB):
 // a product of 16 x 8 x 16 occupies a quarter of an SM's tensor core for some 24 to 32 cycles that way, 144
 // of them for every 16 keys.
@@ -450,6 +471,7 @@ constexpr int kRowsOffMl = kRowsOffX + 128 * kXPitch * 4; // [lane of 128][2] fl
 constexpr int kRowsOffBar = kRowsOffMl + 128 * 8;
 constexpr int kRowsSmem = kRowsOffBar + 64 + 1024;        // slack to align the base to 1024 bytes
 static_assert(2 * (kRowsSmem + 1024 + 256) <= 228 * 1024, "two CTAs an SM");
+constexpr int kRowsFold = 4;                              // units that O is summed over in tensor memory
 constexpr uint32_t kColS = 0, kColQ = 64, kColO = 128, kRowsCols = 256;  // tensor memory; P stands in S's place
 
 // Shared-memory offset of 16-byte chunk c of key r in a tile: 128-byte swizzle, 64 columns a half.
@@ -466,12 +488,14 @@ __device__ __forceinline__ void issue_rows_s(uint32_t tmem, uint32_t k_lo, std::
                                                                 kK > 0 ? 1u : 0u),
    ...);
 }
-// O = P_hi V + P_lo V from 0: 16 columns of P for 16 keys, P_hi in the first 8; V the MN-major B operand,
-// 16 keys 2048 bytes.
+// O += P_hi V + P_lo V (from 0 unless `accumulate`): 16 columns of P for 16 keys, P_hi in the first 8; V the
+// MN-major B operand, 16 keys 2048 bytes.
 template <int... kK>
-__device__ __forceinline__ void issue_rows_pv(uint32_t tmem, uint32_t v_lo, std::integer_sequence<int, kK...>) {
+__device__ __forceinline__ void issue_rows_pv(uint32_t tmem, uint32_t v_lo, uint32_t accumulate,
+                                              std::integer_sequence<int, kK...>) {
   constexpr uint32_t idesc = idesc_bf16(128, kD, 1);
-  ((ptx::mma_ts_warp<16 * kK + 8, (kK << 7)>(tmem + kColO, tmem + kColS, v_lo, kDescHi, idesc, kK == 0 ? 0u : 1u),
+  ((ptx::mma_ts_warp<16 * kK + 8, (kK << 7)>(tmem + kColO, tmem + kColS, v_lo, kDescHi, idesc,
+                                             kK == 0 ? accumulate : 1u),
     ptx::mma_ts_warp<16 * kK, (kK << 7)>(tmem + kColO, tmem + kColS, v_lo, kDescHi, idesc, 1u)),
    ...);
 }
@@ -495,7 +519,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
   const int per = p.Hkv * p.blocks;
   if (threadIdx.x == 0) p.cuts[blockIdx.x].parts = 0;
   Run run;
-  if (!find_run<kRowsThreads>(p.seqlens, p.B, p.cap, per, kMinUnits, run)) return;
+  constexpr int kCost = kRowsItemCost;
+  if (!find_run<kRowsThreads>(p.seqlens, p.B, p.cap, per, kCost, kCost + 1, run)) return;
 
   const uint32_t base = ptx::smem_u32(smem);
   const uint32_t bar_s = base + kRowsOffBar, bar_o = bar_s + 8, bar_end = bar_s + 16;
@@ -520,7 +545,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
   // ---- loads: a warp 16 keys of every unit, kRowsStages - 1 units ahead.
   const int half = lane >> 4, chunk = lane & 15;
   Walk ahead;
-  ahead.start(p, run);
+  ahead.start(p, run, kCost);
   uint32_t bad_stages = 0;
   auto row_of = [&]() {  // as in attn_paged_fwd
     const int key = ahead.t * kUnit + warp * 16 + chunk;
@@ -545,14 +570,14 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
       ptx::cp_async16(d + kRowsTile, p.v + at, from >= 0);
     }
   };
-  const int n = static_cast<int>(run.hi - run.lo);
+  const int n = run.n;
   int next = row_of();
 #pragma unroll
   for (int s = 0; s < kRowsStages - 1; ++s) {
     if (s < n) {
       load(next, s);
       if (s + 1 < n) {
-        ahead.step(p, per);
+        ahead.step(p, per, kCost);
         next = row_of();
       }
     }
@@ -560,13 +585,24 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
   }
 
   Walk at;
-  at.start(p, run);
+  at.start(p, run, kCost);
   Item it;
   uint64_t o[kD / 2];                       // the lane's row, column pairs
   float ref = neg_inf, sum = 0.f;
   int lim = 0, min_lim = 0, t_first = 0;
   bool bad = false, fresh = true, ok = true;
   uint32_t phase_s = 0, phase_o = 0;
+  int summed = 0;                           // units of O in tensor memory
+  auto fold = [&]() {                       // o += what is there
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t y[32];
+      ptx::tmem_ld32(mine + kColO + 32 * q, y);
+#pragma unroll
+      for (int d = 0; d < 16; ++d)
+        o[16 * q + d] = ptx::f2_add(o[16 * q + d], ptx::f2_pack(__uint_as_float(y[2 * d]), __uint_as_float(y[2 * d + 1])));
+    }
+  };
   for (int i = 0; i < n; ++i) {
     if (fresh) {  // an item begins
       fresh = false;
@@ -575,6 +611,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
       bad = false;
       ref = neg_inf;
       sum = 0.f;
+      summed = 0;
 #pragma unroll
       for (int d = 0; d < kD / 2; ++d) o[d] = 0;
       const bool there = r < it.n_rows && at.len >= 0;
@@ -615,16 +652,16 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
       ptx::mma_commit_warp(bar_s);
     }
     bad = bad || (bad_stages >> s & 1u);
-    if (i + kRowsStages - 1 < n) load(next, (i + kRowsStages - 1) % kRowsStages);  // where unit i - 1 was
-    ptx::cp_async_commit();
-    if (i + kRowsStages < n) {
-      ahead.step(p, per);
-      next = row_of();
-    }
-    // ---- the copy's 16 kChunks keys of S.
+    // ---- the copy's 16 kChunks keys of S; the products before it are done too.
     ok = warp_wait(bar_s, phase_s & 1, abort_flag, p.timeout_ns) && ok;
     ++phase_s;
     ptx::tc_fence_after();
+    if (i + kRowsStages - 1 < n && ok) load(next, (i + kRowsStages - 1) % kRowsStages);  // where unit i - 1 was
+    ptx::cp_async_commit();
+    if (i + kRowsStages < n) {
+      ahead.step(p, per, kCost);
+      next = row_of();
+    }
     uint32_t x[kChunks][16];
 #pragma unroll
     for (int u = 0; u < kChunks; ++u) ptx::tmem_ld16_nowait(mine + kColS + 16 * (copy * kChunks + u), x[u]);
@@ -654,13 +691,26 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
           }
       }
     }
-    float f = 1.f;
-    if (mx > ref + kTau) {
-      f = ptx::ex2(ref - mx);  // 0 from -Inf
-      ref = mx;
+    const bool full = summed == kRowsFold || (apart && summed > 0);  // the same for all: O starts from 0 again
+    const bool rises = mx > ref + kTau;
+    if (full || __any_sync(0xFFFFFFFFu, rises)) {
+      if (summed > 0) {
+        fold();
+        if (!full) {  // the other warps' lanes go on
+          const uint32_t zero[16] = {};
+#pragma unroll
+          for (int q = 0; q < 8; ++q) ptx::tmem_st16(mine + kColO + 16 * q, zero);
+        }
+      }
+      const float f = rises ? ptx::ex2(ref - mx) : 1.f;  // 0 from -Inf
+      const uint64_t f2 = ptx::f2_pack(f, f);
+#pragma unroll
+      for (int d = 0; d < kD / 2; ++d) o[d] = ptx::f2_mul(o[d], f2);
+      sum *= f;
+      if (rises) ref = mx;
     }
+    if (full) summed = 0;
     const float sub = ref == neg_inf ? 0.f : ref;
-    sum *= f;
 #pragma unroll
     for (int u = 0; u < kUnit / 16; ++u) {  // all 64 keys' columns: zeros where another copy's are
       uint32_t w[16];
@@ -692,29 +742,14 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
       ok = false;
       break;
     }
-    const uint64_t f2 = ptx::f2_pack(f, f);
     if (!apart) {
       if (warp == 0) {
         ptx::tc_fence_after();
-        issue_rows_pv(tmem, desc_lo(vt, kRowsTile / 2), std::make_integer_sequence<int, 4>{});
-        ptx::mma_commit_warp(bar_o);
+        issue_rows_pv(tmem, desc_lo(vt, kRowsTile / 2), summed > 0 ? 1u : 0u, std::make_integer_sequence<int, 4>{});
       }
-      ok = warp_wait(bar_o, phase_o & 1, abort_flag, p.timeout_ns);
-      ++phase_o;
-      ptx::tc_fence_after();
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t y[32];
-        ptx::tmem_ld32(mine + kColO + 32 * q, y);
-#pragma unroll
-        for (int d = 0; d < 16; ++d)
-          o[16 * q + d] = ptx::f2_fma(o[16 * q + d], f2, ptx::f2_pack(__uint_as_float(y[2 * d]), __uint_as_float(y[2 * d + 1])));
-      }
-      ptx::tc_fence_before();
+      ++summed;
     } else {
       // Key by key over what the row sees, weights read back two at a time.
-#pragma unroll
-      for (int d = 0; d < kD / 2; ++d) o[d] = ptx::f2_mul(o[d], f2);
 #pragma unroll 1
       for (int j = 0; j < 8 * kChunks; ++j) {
         const uint32_t col = mine + kColS + 16 * (copy * kChunks + (j >> 3)) + (j & 7);
@@ -748,6 +783,14 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
       continue;
     }
     // ---- the item's end, or the run's: the copies are added, 16 columns at a time.
+    if (summed > 0) {
+      if (warp == 0) ptx::mma_commit_warp(bar_o);
+      ok = warp_wait(bar_o, phase_o & 1, abort_flag, p.timeout_ns);
+      ++phase_o;
+      ptx::tc_fence_after();
+      fold();
+      ptx::tc_fence_before();
+    }
     fresh = true;
     const bool whole = ends && t_first == 0;
     const int failed = __syncthreads_or((bad ? 1 : 0) | (ok ? 0 : 2));
@@ -820,13 +863,9 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
     }
     if (threadIdx.x == 0) {
       if (skip || at.len < 0) atomicOr(&g_attn_status, skip ? 8u : 2u);
-      if (!ends && t_first == 0) {
-        const long long end = run.lo + i + (at.units - at.t);
-        const int last = static_cast<int>((end * run.runs + run.total - 1) / run.total) - 1;
-        p.cuts[blockIdx.x] = {it.b, at.item, last - static_cast<int>(blockIdx.x) + 1, 0};
-      }
+      if (!ends && t_first == 0) p.cuts[blockIdx.x] = {it.b, at.item, at.parts(run, kCost), 0};
     }
-    if (i + 1 < n) at.step(p, per);
+    if (i + 1 < n) at.step(p, per, kCost);
   }
   // ---- copies and products that are still under way (after a wait that ran out), then the end.
   ptx::cp_async_wait<0>();
@@ -928,7 +967,7 @@ constexpr int kMassUnits = 2;  // of a run at least: a key a thread
 __global__ void __launch_bounds__(kMassThreads) attn_paged_mass(const Params p) {
   const float inf = __int_as_float(0x7F800000);
   Run run;
-  const bool any = find_run<kMassThreads>(p.seqlens, p.B, p.cap, p.Hkv, kMassUnits, run);
+  const bool any = find_run<kMassThreads>(p.seqlens, p.B, p.cap, p.Hkv, 0, kMassUnits, run);
   ptx::grid_dependency_wait();
   if (!any) return;
   long long u = run.lo, first = run.first;
