@@ -668,16 +668,33 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
 #pragma unroll
     for (int u = 0; u < kChunks; ++u) ptx::tmem_wait_ld16(x[u]);
     const int key0 = at.t * kUnit + copy * 16 * kChunks;
-    const bool masked = key0 + 16 * kChunks > min_lim;
-    float mx = neg_inf;
+    const uint64_t c2 = ptx::f2_pack(p.c, p.c);
+    uint64_t v[kChunks][8];  // logits of key pairs, log2 units
 #pragma unroll
     for (int u = 0; u < kChunks; ++u)
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        float v = __uint_as_float(x[u][j]) * p.c;
-        if (masked && key0 + 16 * u + j >= lim) v = neg_inf;
-        x[u][j] = __float_as_uint(v);
-        mx = fmaxf(mx, v);  // a NaN is left out here and comes back through its weight
+      for (int j = 0; j < 8; ++j)
+        v[u][j] = ptx::f2_mul(ptx::f2_pack(__uint_as_float(x[u][2 * j]), __uint_as_float(x[u][2 * j + 1])), c2);
+    if (key0 + 16 * kChunks > min_lim) {  // some row does not see some key
+#pragma unroll
+      for (int u = 0; u < kChunks; ++u)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float lo, hi;
+          ptx::f2_unpack(v[u][j], lo, hi);
+          if (key0 + 16 * u + 2 * j >= lim) lo = neg_inf;
+          if (key0 + 16 * u + 2 * j + 1 >= lim) hi = neg_inf;
+          v[u][j] = ptx::f2_pack(lo, hi);
+        }
+    }
+    float mx = neg_inf;  // a NaN is left out here and comes back through its weight
+#pragma unroll
+    for (int u = 0; u < kChunks; ++u)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float lo, hi;
+        ptx::f2_unpack(v[u][j], lo, hi);
+        mx = fmaxf(mx, fmaxf(lo, hi));
       }
     if constexpr (kMass) {
       if (r < it.n_rows) {
@@ -685,9 +702,12 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
 #pragma unroll
         for (int u = 0; u < kChunks; ++u)
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            if (key0 + 16 * u + j < at.len) *to = __uint_as_float(x[u][j]);
-            to += p.rows4;
+          for (int j = 0; j < 8; ++j) {
+            float lo, hi;
+            ptx::f2_unpack(v[u][j], lo, hi);
+            if (key0 + 16 * u + 2 * j < at.len) to[0] = lo;
+            if (key0 + 16 * u + 2 * j + 1 < at.len) to[p.rows4] = hi;
+            to += 2 * static_cast<size_t>(p.rows4);
           }
       }
     }
@@ -711,30 +731,37 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
     }
     if (full) summed = 0;
     const float sub = ref == neg_inf ? 0.f : ref;
+    const uint64_t sub2 = ptx::f2_pack(-sub, -sub);
+    uint64_t sum2 = 0;
 #pragma unroll
-    for (int u = 0; u < kUnit / 16; ++u) {  // all 64 keys' columns: zeros where another copy's are
+    for (int u = 0; u < kChunks; ++u) {
       uint32_t w[16];
-      const int v = u - copy * kChunks;
-      bool own = false;
 #pragma unroll
-      for (int y = 0; y < kChunks; ++y)
-        if (v == y) {
-          own = true;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float w0 = ptx::ex2(__uint_as_float(x[y][2 * j]) - sub);
-            const float w1 = ptx::ex2(__uint_as_float(x[y][2 * j + 1]) - sub);
-            sum += w0 + w1;
-            const uint32_t h = ptx::pack_bf16x2(w0, w1);
-            w[j] = h;
-            w[8 + j] = ptx::pack_bf16x2(w0 - __uint_as_float(h << 16), w1 - __uint_as_float(h & 0xFFFF0000u));
-          }
-        }
-      if (!own) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) w[j] = 0;
+      for (int j = 0; j < 8; ++j) {
+        float w0, w1;
+        ptx::f2_unpack(ptx::f2_add(v[u][j], sub2), w0, w1);
+        w0 = ptx::ex2(w0);
+        w1 = ptx::ex2(w1);
+        const uint64_t ww = ptx::f2_pack(w0, w1);
+        sum2 = ptx::f2_add(sum2, ww);
+        const uint32_t h = ptx::pack_bf16x2(w0, w1);
+        w[j] = h;
+        float l0, l1;
+        ptx::f2_unpack(ptx::f2_sub(ww, ptx::f2_pack(__uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u))), l0, l1);
+        w[8 + j] = ptx::pack_bf16x2(l0, l1);
       }
-      ptx::tmem_st16(mine + kColS + 16 * u, w);
+      ptx::tmem_st16(mine + kColS + 16 * (copy * kChunks + u), w);
+    }
+    {
+      float s0, s1;
+      ptx::f2_unpack(sum2, s0, s1);
+      sum += s0 + s1;
+    }
+    if constexpr (kCopies > 1) {  // zeros at the other copies' keys
+      const uint32_t zero[16] = {};
+#pragma unroll
+      for (int u = kChunks; u < kUnit / 16; ++u)
+        ptx::tmem_st16(mine + kColS + 16 * ((copy * kChunks + u) % (kUnit / 16)), zero);
     }
     ptx::tmem_wait_st();
     ptx::tc_fence_before();
