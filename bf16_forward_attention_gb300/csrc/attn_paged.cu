@@ -1,6 +1,6 @@
 // attn_paged.cu - host side of attention over a paged cache, declared in include/attn_fwd.h:
 // checks the call, lays out the workspace and launches, on the caller's stream, the runs of
-// units, the join of the items they cut, and the keys' masses where they are wanted.
+// units, then the join of the items they cut with, beside it, the keys' masses where they are wanted.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -28,16 +28,16 @@ bool g_ready[kMaxDevices];
 using Kernel = void (*)(const paged::Params);
 // A block's rows, and the kernel for them, with and without the keys' masses.
 struct Form {
-  int rows, threads, smem, ctas;
+  int rows, threads, smem, ctas, cost;
   Kernel fwd[2];
 };
 template <typename S>
 constexpr Form form() {
-  return {S::kRows, S::kThreads, S::kSmem, S::kCtas, {paged::attn_paged_fwd<S, false>, paged::attn_paged_fwd<S, true>}};
+  return {S::kRows, S::kThreads, S::kSmem, S::kCtas, paged::kItemCost, {paged::attn_paged_fwd<S, false>, paged::attn_paged_fwd<S, true>}};
 }
 template <int kCopies>
 constexpr Form rows_form() {
-  return {128 / kCopies, paged::kRowsThreads, paged::kRowsSmem, 2,
+  return {128 / kCopies, paged::kRowsThreads, paged::kRowsSmem, 2, paged::kRowsItemCost,
           {paged::attn_paged_rows<kCopies, false>, paged::attn_paged_rows<kCopies, true>}};
 }
 constexpr Form kForms[] = {form<paged::Rows8>(), form<paged::Rows16>(), rows_form<4>(), rows_form<2>(), rows_form<1>()};
@@ -199,15 +199,20 @@ int attn_fwd_paged(const void* q, const void* k_pages, const void* v_pages, cons
   p.blocks = static_cast<int>(pl.blocks);
   p.block_rows = static_cast<int>(pl.block_rows);
   p.rows8 = pl.form->rows;
+  p.cost = pl.form->cost;
+  p.runs = static_cast<int>(pl.runs);
+  p.join_groups = static_cast<int>((pl.block_rows + 7) / 8);
   p.c = scale * 1.4426950408889634f;
   p.timeout_ns = kTimeoutNs;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (!launch(pl.form->fwd[mass ? 1 : 0], pl.runs, pl.form->threads, pl.form->smem, cs, false, p))
     return ATTN_ERR_LAUNCH;
-  const dim3 groups(static_cast<unsigned>(pl.runs), static_cast<unsigned>((pl.block_rows + 7) / 8));
-  if (!launch(paged::attn_paged_join, groups, paged::kJoinThreads, static_cast<int>(pl.runs) * 32, cs, true, p))
-    return ATTN_ERR_LAUNCH;
-  if (mass && !launch(paged::attn_paged_mass, 4 * int64_t(sms_here()), paged::kMassThreads, 0, cs, true, p))
+  // The blocks of the masses: what the join's leave of an SM at once.
+  const bool few = pl.runs / (Hkv * pl.blocks) + 2 <= paged::kJoinFew;
+  const int64_t blocks = pl.runs * p.join_groups + (mass ? (few ? 3 : 1) * int64_t(sms_here()) : 0);
+  const Kernel finish = few ? (mass ? paged::attn_paged_finish<1, true> : paged::attn_paged_finish<1, false>)
+                            : (mass ? paged::attn_paged_finish<4, true> : paged::attn_paged_finish<4, false>);
+  if (!launch(finish, blocks, paged::kJoinThreads * (few ? 1 : 4), static_cast<int>(pl.runs) * 32, cs, true, p))
     return ATTN_ERR_LAUNCH;
   return ATTN_OK;
 }

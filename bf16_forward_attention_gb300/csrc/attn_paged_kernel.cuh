@@ -8,10 +8,10 @@
 // All items' units in a row, sequence by sequence, are cut into equal runs, one a CTA: lengths
 // are on the device, and a long sequence among short ones is spread over as many CTAs as its
 // keys are worth. A CTA that has an item whole finishes it; an item that is cut leaves
-// unnormalised rows and (reference, sum) per part, joined by attn_paged_join:
+// unnormalised rows and (reference, sum) per part, joined by attn_paged_finish:
 //   O = sum_s 2^(r_s - R) O_s / sum_s 2^(r_s - R) l_s,   lse = ln 2 (R + log2 L).
-// With the keys' weights wanted, the logits s_ij go to the workspace too, and
-// attn_paged_mass adds  sum_i 2^(s_ij - lse_i)  to every key's mass.
+// With the keys' weights wanted, the logits s_ij go to the workspace too, and blocks beside the
+// join's add  sum_i 2^(s_ij - lse_i)  to every key's mass.
 #pragma once
 #include "few_rows.cuh"
 
@@ -58,19 +58,30 @@ struct Params {
   float* part_o;           // [2 run + begins its item][8-row group][16-column group][lane][4]: as the warps hold it
   float* part_rl;          // [2 run + begins its item][rows8][2]
   Cut* cuts;               // [run]
-  float* lse2;             // with mass: [b][kv head][rows4], log2 units; +Inf: not to be used
+  float* lse2;             // with mass, of rows not cut: [b][kv head][rows4], log2 units; +Inf: not to be used
   float* logits;           // with mass: [b][kv head][cap][rows4], log2 units
   int B, Hq, Hkv, group, Sq, cap, layout, causal, mode;
   int n_pages, page_size, page_shift, max_pages;  // page_shift: log2 of the page size, or -1
   int page_rows;           // rows of 128 from a page to the next
   int rows, rows4;         // Sq * group; that, in fours
   int blocks, block_rows, rows8;  // blocks of at most block_rows rows; rows8: the kernel's rows of a block
+  int cost, runs;          // an item's cost and the most runs, as the kernel of the runs has them
+  int join_groups;         // blocks of a run in attn_paged_finish: 8-row groups
   float c;                 // scale * log2(e)
   unsigned long long timeout_ns;  // of a wait for the tensor cores
 };
 
 __device__ __forceinline__ int units_of(int len, int cap) {
   return len < 0 || len > cap ? 1 : max(1, (len + kUnit - 1) / kUnit);
+}
+
+__device__ __forceinline__ int runs_of(long long total, int least, int count) {
+  const long long most = (total + least - 1) / least;
+  return static_cast<int>(most < count ? most : static_cast<long long>(count));
+}
+// The run in which place x lies.
+__device__ __forceinline__ int run_of(long long x, long long total, int runs) {
+  return static_cast<int>(((x + 1) * runs + total - 1) / total) - 1;
 }
 
 // A run of units: all items in a row (sequence, then kv head and block; `per` items a sequence), each
@@ -83,10 +94,11 @@ struct Run {
   int n;                // units
 };
 
-// Run blockIdx.x of at most gridDim.x runs of at least `least` places. All threads of the block;
-// false: there is no such run.
+// Run `index` of at most `count` runs of at least `least` places. All threads of the block; false: there
+// is no such run.
 template <int kBlock>
-__device__ __forceinline__ bool find_run(const int* seqlens, int B, int cap, int per, int cost, int least, Run& run) {
+__device__ __forceinline__ bool find_run(const int* seqlens, int B, int cap, int per, int cost, int least, int index,
+                                         int count, Run& run) {
   __shared__ long long warp_sum[kBlock / 32], at_first[2];
   __shared__ int at_b[2];
   const int each = (B + kBlock - 1) / kBlock;
@@ -109,12 +121,11 @@ __device__ __forceinline__ bool find_run(const int* seqlens, int B, int cap, int
     total += warp_sum[w];
   }
   total *= per;
-  const long long most = (total + least - 1) / least;
-  run.runs = static_cast<int>(most < static_cast<long long>(gridDim.x) ? most : static_cast<long long>(gridDim.x));
+  run.runs = runs_of(total, least, count);
   run.total = total;
-  if (static_cast<int>(blockIdx.x) >= run.runs) return false;
-  run.lo = total * blockIdx.x / run.runs;
-  run.hi = total * (blockIdx.x + 1) / run.runs;
+  if (index >= run.runs) return false;
+  run.lo = total * index / run.runs;
+  run.hi = total * (index + 1) / run.runs;
   // The sequences of the first place, and of the last.
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
@@ -172,11 +183,10 @@ struct Walk {
     first += static_cast<long long>(per) * (units + cost);
     if (++b < p.B) enter(p);
   }
-  // In how many runs the item lies, of which this one has its first unit: its last unit is in the last
-  // run that begins before its end.
+  // In how many runs the item lies, of which this one has its first unit.
   __device__ __forceinline__ int parts(const Run& run, int cost) const {
     const long long end = first + static_cast<long long>(item + 1) * (units + cost);
-    return static_cast<int>((end * run.runs + run.total - 1) / run.total) - static_cast<int>(blockIdx.x);
+    return run_of(end - 1, run.total, run.runs) - static_cast<int>(blockIdx.x) + 1;
   }
 };
 
@@ -208,14 +218,15 @@ __device__ __forceinline__ void store_out(const Params& p, const Item& it, int g
   *reinterpret_cast<uint32_t*>(to + 8) = ct;
 }
 
-__device__ __forceinline__ void store_lse_of(const Params& p, const Item& it, int r, float R, float L) {
+__device__ __forceinline__ void store_lse_of(const Params& p, const Item& it, int r, float R, float L,
+                                             bool whole = true) {
   if (r >= it.n_rows) return;
   const int row = it.row0 + r, i = row / p.group, h = it.kvh * p.group + row - i * p.group;
   store_lse(p.lse, (static_cast<size_t>(it.b) * p.Hq + h) * p.Sq + i, R, L);
-  if (p.mass) lse2_at(p, it, r) = R + log2f(L);
+  if (whole && p.mass) lse2_at(p, it, r) = R + log2f(L);
 }
 
-// A row whose keys cannot be read: its results stay as they were, and attn_paged_mass is told.
+// A row whose keys cannot be read: its results stay as they were, and add_mass is told.
 __device__ __forceinline__ void skip_row(const Params& p, const Item& it, int r) {
   if (r < it.n_rows && p.mass) lse2_at(p, it, r) = __int_as_float(0x7F800000);
 }
@@ -234,7 +245,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) attn_paged_fwd(const Pa
   if (threadIdx.x == 0) p.cuts[blockIdx.x].parts = 0;
   Run run;
   constexpr int kCost = kItemCost;
-  if (!find_run<S::kThreads>(p.seqlens, p.B, p.cap, per, kCost, kCost + 1, run)) return;
+  if (!find_run<S::kThreads>(p.seqlens, p.B, p.cap, per, kCost, kCost + 1, blockIdx.x, gridDim.x, run)) return;
   const uint32_t ring = ptx::smem_u32(smem) + team * kStages * kStageBytes;
   const int half = lane >> 4, chunk = lane & 15;
 
@@ -520,7 +531,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
   if (threadIdx.x == 0) p.cuts[blockIdx.x].parts = 0;
   Run run;
   constexpr int kCost = kRowsItemCost;
-  if (!find_run<kRowsThreads>(p.seqlens, p.B, p.cap, per, kCost, kCost + 1, run)) return;
+  if (!find_run<kRowsThreads>(p.seqlens, p.B, p.cap, per, kCost, kCost + 1, blockIdx.x, gridDim.x, run)) return;
 
   const uint32_t base = ptx::smem_u32(smem);
   const uint32_t bar_s = base + kRowsOffBar, bar_o = bar_s + 8, bar_end = bar_s + 16;
@@ -907,33 +918,39 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
   if (warp == 0) ptx::tmem_dealloc(tmem, kRowsCols);
 }
 
-// ---------------------------------------------------------------- join
-constexpr int kJoinSplits = 4;                     // warps that share an item's parts
-constexpr int kJoinThreads = 32 * 8 * kJoinSplits;
+// ---------------------------------------------------------------- join and masses
+constexpr int kJoinThreads = 32 * 8;  // times kSplits
+// An item has at most runs / (kv heads * blocks) + 2 parts, as all of a sequence's are as long; with
+// more than this many, four warps share them. (With four always, 1024-thread blocks that mostly leave at
+// once took 5 waves: 14 us for 48 x 35 rows.)
+constexpr int kJoinFew = 96;
+constexpr int kJoinBatch = 8;         // parts on their way at once
+constexpr int kMassUnits = 2;         // of a run of keys at least
+constexpr int kMassRows = 256;        // whose log-sum-exp a block holds at once
+constexpr int kMassKeys = 4;          // of a thread at once
 
-// A block per (run, 8-row group): the run's cut item, if it has one. A warp takes 16 columns of
-// every fourth part; parts are added in a fixed order.
-__global__ void __launch_bounds__(kJoinThreads) attn_paged_join(const Params p) {
+__device__ __forceinline__ size_t part_at(int run, bool begins) { return 2 * static_cast<size_t>(run) + (begins ? 1 : 0); }
+
+// The cut item of `run`, if it has one, rows 8 g .. 8 g + 7. A warp takes 16 columns of every kSplits-th
+// part; parts are added in a fixed order.
+template <int kSplits>
+__device__ __forceinline__ void join(const Params& p, int run, int g) {
   extern __shared__ __align__(16) float weights[];  // [part][8 rows]
-  __shared__ float4 sum_o[kJoinSplits - 1][8][32];
+  __shared__ float4 sum_o[kSplits][8][32];          // of split 0: not used
   __shared__ float row_r[8], row_l[8];
-  ptx::grid_dependency_wait();
-  const Cut cut = p.cuts[blockIdx.x];
+  const Cut cut = p.cuts[run];
   if (cut.parts == 0) return;
   const Item it = item_of(p, cut.b, cut.item);
-  const int g = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (8 * g >= it.n_rows || !dbg_ok(cut.b < p.B && cut.parts <= static_cast<int>(gridDim.x) - static_cast<int>(blockIdx.x)))
-    return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (8 * g >= it.n_rows || !dbg_ok(cut.b < p.B && cut.parts <= p.runs - run)) return;
   const float neg_inf = -__int_as_float(0x7F800000);
   const float2* rl = reinterpret_cast<const float2*>(p.part_rl);
-  // Part 0 begins the item; the others are the first of their runs.
-  auto part_at = [&](int i) { return 2 * (static_cast<size_t>(blockIdx.x) + i) + (i == 0 ? 1 : 0); };
   // ---- a warp a row: the largest reference, the parts' weights, the sum.
   bool skip = false;
   if (warp < 8) {
     float R = neg_inf;
     for (int i = lane; i < cut.parts; i += 32) {
-      const float2 x = rl[part_at(i) * p.rows8 + 8 * g + warp];
+      const float2 x = rl[part_at(run + i, i == 0) * p.rows8 + 8 * g + warp];
       R = fmaxf(R, x.x);  // a NaN is left out: it comes back through its weight
       skip = skip || x.y < 0.f;
     }
@@ -942,7 +959,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join(const Params p) 
     const float ref = R == neg_inf ? 0.f : R;
     float L = 0.f;
     for (int i = lane; i < cut.parts; i += 32) {
-      const float2 x = rl[part_at(i) * p.rows8 + 8 * g + warp];
+      const float2 x = rl[part_at(run + i, i == 0) * p.rows8 + 8 * g + warp];
       const float w = ptx::ex2(x.x - ref);
       weights[8 * i + warp] = w;
       L = fmaf(x.y, w, L);
@@ -954,26 +971,36 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join(const Params p) 
       row_l[warp] = L;
     }
   }
-  if (__syncthreads_or(skip)) {
-    if (threadIdx.x < 8) skip_row(p, it, 8 * g + threadIdx.x);
-    return;
-  }
+  if (__syncthreads_or(skip)) return;  // a page of the sequence could not be read
   const int dt = warp & 7, split = warp >> 3;
   float x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-  for (int i = split; i < cut.parts; i += kJoinSplits) {
-    const float4 y = reinterpret_cast<const float4*>(p.part_o)[((part_at(i) * (p.rows8 / 8) + g) * 8 + dt) * 32 + lane];
-    const float2 w = *reinterpret_cast<const float2*>(weights + 8 * i + 2 * (lane & 3));
-    x[0] = fmaf(y.x, w.x, x[0]);
-    x[1] = fmaf(y.y, w.y, x[1]);
-    x[2] = fmaf(y.z, w.x, x[2]);
-    x[3] = fmaf(y.w, w.y, x[3]);
-  }
-  if (split != 0) sum_o[split - 1][dt][lane] = make_float4(x[0], x[1], x[2], x[3]);
-  __syncthreads();
-  if (split != 0) return;
+  const float4* part_o = reinterpret_cast<const float4*>(p.part_o) + (g * 8 + dt) * 32 + lane;
+  const size_t pitch = p.rows8 / 8 * 8 * 32;
+  for (int i0 = split; i0 < cut.parts; i0 += kJoinBatch * kSplits) {
+    float4 y[kJoinBatch];
 #pragma unroll
-  for (int w = 0; w < kJoinSplits - 1; ++w) {
+    for (int j = 0; j < kJoinBatch; ++j) {
+      const int i = i0 + j * kSplits;
+      y[j] = i < cut.parts ? part_o[part_at(run + i, i == 0) * pitch] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int j = 0; j < kJoinBatch; ++j) {
+      const int i = i0 + j * kSplits;
+      if (i >= cut.parts) break;
+      const float2 w = *reinterpret_cast<const float2*>(weights + 8 * i + 2 * (lane & 3));
+      x[0] = fmaf(y[j].x, w.x, x[0]);
+      x[1] = fmaf(y[j].y, w.y, x[1]);
+      x[2] = fmaf(y[j].z, w.x, x[2]);
+      x[3] = fmaf(y[j].w, w.y, x[3]);
+    }
+  }
+  if constexpr (kSplits > 1) {
+    if (split != 0) sum_o[split][dt][lane] = make_float4(x[0], x[1], x[2], x[3]);
+    __syncthreads();
+    if (split != 0) return;
+  }
+#pragma unroll
+  for (int w = 1; w < kSplits; ++w) {
     const float4 y = sum_o[w][dt][lane];
     x[0] += y.x;
     x[1] += y.y;
@@ -982,21 +1009,52 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join(const Params p) 
   }
   const int r = 2 * (lane & 3);
   store_out(p, it, g, dt, lane, x, __frcp_rn(row_l[r]), __frcp_rn(row_l[r + 1]));
-  if (threadIdx.x < 8) store_lse_of(p, it, 8 * g + threadIdx.x, row_r[threadIdx.x], row_l[threadIdx.x]);
+  if (threadIdx.x < 8) store_lse_of(p, it, 8 * g + threadIdx.x, row_r[threadIdx.x], row_l[threadIdx.x], false);
 }
 
-// ---------------------------------------------------------------- mass
-constexpr int kMassThreads = 128;
-constexpr int kMassUnits = 2;  // of a run at least: a key a thread
+// A row's log-sum-exp, log2 units, from what the runs left: its item's single run wrote it, or the parts
+// are added here as join adds them (beside this block, so not by way of it), a lane every 32nd part. +Inf:
+// not to be used. first: the place of the sequence, whose items have `units` units; total and runs of the
+// kernel of the runs. A warp.
+__device__ __forceinline__ float row_lse2(const Params& p, int b, int kvh, int row, long long first, int units,
+                                          long long total, int runs, int lane) {
+  const int block = row / p.block_rows, r = row - block * p.block_rows;
+  const long long place = first + static_cast<long long>(kvh * p.blocks + block) * (units + p.cost);
+  const int i0 = run_of(place + p.cost, total, runs), i1 = run_of(place + p.cost + units - 1, total, runs);
+  if (i0 == i1) return p.lse2[(static_cast<size_t>(b) * p.Hkv + kvh) * p.rows4 + row];
+  const float inf = __int_as_float(0x7F800000);
+  const float2* rl = reinterpret_cast<const float2*>(p.part_rl) + r;
+  float R = -inf, L = 0.f;
+  bool skip = false;
+  for (int i = i0 + lane; i <= i1; i += 32) {
+    const float2 x = rl[part_at(i, i == i0) * p.rows8];
+    skip = skip || x.y < 0.f;
+    R = fmaxf(R, x.x);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) R = fmaxf(R, __shfl_xor_sync(0xFFFFFFFFu, R, d));
+  const float ref = R == -inf ? 0.f : R;
+  for (int i = i0 + lane; i <= i1; i += 32) {
+    const float2 x = rl[part_at(i, i == i0) * p.rows8];
+    L = fmaf(x.y, ptx::ex2(x.x - ref), L);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, d);
+  return __any_sync(0xFFFFFFFFu, skip) ? inf : R + log2f(L);
+}
 
 // mass[b, kvh, j] += sum over the rows that see key j of 2^(s_ij - lse_i), a key a thread, the
-// rows in order. A row whose log-sum-exp is -Inf (it sees no key) adds nothing.
-__global__ void __launch_bounds__(kMassThreads) attn_paged_mass(const Params p) {
+// rows in order. A row whose log-sum-exp is -Inf (it sees no key) adds nothing. Runs of keys, `index` of
+// `count`.
+template <int kBlock>
+__device__ __forceinline__ void add_mass(const Params& p, int index, int count) {
+  __shared__ __align__(16) float lse2[kMassRows];
   const float inf = __int_as_float(0x7F800000);
   Run run;
-  const bool any = find_run<kMassThreads>(p.seqlens, p.B, p.cap, p.Hkv, 0, kMassUnits, run);
-  ptx::grid_dependency_wait();
-  if (!any) return;
+  if (!find_run<kBlock>(p.seqlens, p.B, p.cap, p.Hkv, 0, kMassUnits, index, count, run)) return;
+  // The places and runs of the kernel that left the logits.
+  const long long total = (run.total + static_cast<long long>(p.Hkv) * p.cost * p.B) * p.blocks;
+  const int runs = runs_of(total, p.cost + 1, p.runs);
   long long u = run.lo, first = run.first;
   int b = run.b;
   while (u < run.hi) {
@@ -1005,6 +1063,7 @@ __global__ void __launch_bounds__(kMassThreads) attn_paged_mass(const Params p) 
     const long long left = run.hi - u;
     const int t_end = left < units - t_first ? t_first + static_cast<int>(left) : units;
     const int here = b;
+    const long long place = (first + static_cast<long long>(p.Hkv) * p.cost * b) * p.blocks;
     u += t_end - t_first;
     if (u == first + static_cast<long long>(units) * p.Hkv) {
       first = u;
@@ -1012,28 +1071,63 @@ __global__ void __launch_bounds__(kMassThreads) attn_paged_mass(const Params p) 
     }
     if (len < 0 || len > p.cap) continue;
     const size_t head = static_cast<size_t>(here) * p.Hkv + kvh;
-    const float* lse2 = p.lse2 + head * p.rows4;
-    bool skip = false;
-    for (int r = threadIdx.x; r < p.rows; r += kMassThreads) skip = skip || lse2[r] == inf;
-    if (__syncthreads_or(skip)) continue;  // a page of the sequence could not be read
     const int end = min(t_end * kUnit, len);
-    for (int key = t_first * kUnit + threadIdx.x; key < end; key += kMassThreads) {
-      const float* s = p.logits + (head * p.cap + key) * p.rows4;
-      float sum = 0.f;
-      for (int r = 0; r < p.rows; r += 4) {
-        const float4 s4 = *reinterpret_cast<const float4*>(s + r);
-        const float4 l4 = *reinterpret_cast<const float4*>(lse2 + r);
-        const float sv[4] = {s4.x, s4.y, s4.z, s4.w}, lv[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (r + e >= p.rows || lv[e] == -inf) continue;
-          if (p.causal && key >= few::own_limit((r + e) / p.group, len, p.Sq, 1)) continue;
-          sum += ptx::ex2(sv[e] - lv[e]);
-        }
+    for (int r0 = 0; r0 < p.rows; r0 += kMassRows) {
+      const int n = min(kMassRows, p.rows - r0);
+      __syncthreads();  // the rows before have been read
+      bool skip = false;
+      for (int r = threadIdx.x >> 5; r < n; r += kBlock / 32) {
+        const float x = row_lse2(p, here, kvh, r0 + r, place, units, total, runs, threadIdx.x & 31);
+        if ((threadIdx.x & 31) == 0) lse2[r] = x;
+        skip = skip || x == inf;
       }
-      p.mass[head * p.cap + key] += sum;
+      if (__syncthreads_or(skip)) break;  // a page of the sequence could not be read: so say all its rows
+      for (int base = t_first * kUnit; base < end; base += kMassKeys * kBlock) {
+        float sum[kMassKeys] = {};
+        int key[kMassKeys];
+#pragma unroll
+        for (int j = 0; j < kMassKeys; ++j) key[j] = base + j * kBlock + static_cast<int>(threadIdx.x);
+        float* to = p.mass + head * p.cap;
+        float was[kMassKeys];
+#pragma unroll
+        for (int j = 0; j < kMassKeys; ++j) was[j] = key[j] < end ? to[key[j]] : 0.f;
+        for (int r = 0; r < n; r += 4) {
+          const float4 l4 = *reinterpret_cast<const float4*>(lse2 + r);
+          const float lv[4] = {l4.x, l4.y, l4.z, l4.w};
+          float4 s4[kMassKeys];
+#pragma unroll
+          for (int j = 0; j < kMassKeys; ++j)
+            if (key[j] < end)
+              s4[j] = *reinterpret_cast<const float4*>(p.logits + (head * p.cap + key[j]) * p.rows4 + r0 + r);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (r + e >= n || lv[e] == -inf) continue;
+            const int lim = p.causal ? few::own_limit((r0 + r + e) / p.group, len, p.Sq, 1) : len;
+#pragma unroll
+            for (int j = 0; j < kMassKeys; ++j) {
+              const float s = e == 0 ? s4[j].x : e == 1 ? s4[j].y : e == 2 ? s4[j].z : s4[j].w;
+              if (key[j] < end && key[j] < lim) sum[j] += ptx::ex2(s - lv[e]);
+            }
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kMassKeys; ++j)
+          if (key[j] < end) to[key[j]] = was[j] + sum[j];
+      }
     }
   }
+}
+
+// Blocks of join (run by run, join_groups each), and behind them those of the masses.
+template <int kSplits, bool kMass>
+__global__ void __launch_bounds__(kJoinThreads * kSplits, kSplits == 1 ? 4 : 1) attn_paged_finish(const Params p) {
+  ptx::grid_dependency_wait();
+  const int joins = p.runs * p.join_groups, block = blockIdx.x;
+  if (block < joins) {
+    join<kSplits>(p, block / p.join_groups, block % p.join_groups);
+    return;
+  }
+  if constexpr (kMass) add_mass<kJoinThreads * kSplits>(p, block - joins, static_cast<int>(gridDim.x) - joins);
 }
 
 }  // namespace paged
