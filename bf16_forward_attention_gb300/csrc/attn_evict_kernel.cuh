@@ -38,26 +38,46 @@ __device__ __forceinline__ uint32_t order_of(float x) {
   return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
 }
 
-// The masses first .. end - 1 in turn, kStep apart a thread: fn(valid, index, mass). Eight reads are
-// in flight at once: what a pass over a long row waits for.
-constexpr int kBatch = 8;
-template <int kStep, typename Fn>
-__device__ __forceinline__ void each_mass(const float* mass, int first, int end, int lane, Fn&& fn) {
-  for (int base = first; base < end; base += kBatch * kStep) {
-    float x[kBatch];
+// A warp's stretch of the masses, lo .. hi - 1, 32 at a time: the first kHeld of a lane stay in its
+// registers from pass to pass, the others are read again, kBatch on their way at once.
+constexpr int kHeld = 32, kBatch = 8;
+struct Stretch {
+  const float* mass;
+  int lo, hi, lane;
+  float held[kHeld];
+
+  __device__ __forceinline__ void load() {
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int i = base + j * kStep + lane;
-      x[j] = i < end ? __ldg(mass + i) : 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      if (base + j * kStep >= end) break;  // the same for all lanes
-      const int i = base + j * kStep + lane;
-      fn(i < end, i, x[j]);
+    for (int j = 0; j < kHeld; ++j) {
+      const int i = lo + 32 * j + lane;
+      held[j] = i < hi ? __ldg(mass + i) : 0.f;
     }
   }
-}
+  // fn(whether there is one, place, mass) for 32 places at a time, in order.
+  template <typename Fn>
+  __device__ __forceinline__ void each(Fn&& fn) const {
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      if (lo + 32 * j >= hi) break;  // the same for all lanes
+      const int i = lo + 32 * j + lane;
+      fn(i < hi, i, held[j]);
+    }
+    for (int base = lo + 32 * kHeld; base < hi; base += 32 * kBatch) {
+      float x[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = base + 32 * j + lane;
+        x[j] = i < hi ? __ldg(mass + i) : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        if (base + 32 * j >= hi) break;
+        const int i = base + 32 * j + lane;
+        fn(i < hi, i, x[j]);
+      }
+    }
+  }
+};
 
 __device__ __forceinline__ int page_of(const Params& p, int key) {
   return p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
@@ -72,10 +92,15 @@ constexpr int kBins = 2048;
 // among the latest, by its digits of 11, 11 and 10 bits from the top: a histogram of a digit among the
 // masses that share the digits above it. Then every warp counts, in its stretch of the keys,
 // those above that value and those equal to it, and writes its kept keys behind the others';
-// of the equal ones the first stay.
-__global__ void __launch_bounds__(kSelectThreads) attn_evict_select(const Params p) {
-  __shared__ int bins[kBins];
+// of the equal ones the first stay. A block's first 16384 masses are read once (read in each of
+// the five passes, 256 blocks of up to 16384 keys took 27 us).
+__global__ void __launch_bounds__(kSelectThreads, 2) attn_evict_select(const Params p) {
+  __shared__ __align__(16) int bins[kBins];
   __shared__ int warp_n[2][kSelectWarps];
+  // The sum of the warps' entries before this one's.
+  auto before_warp = [&](const int (&n)[kSelectWarps], int warp, int lane) {
+    return static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, lane < warp ? static_cast<unsigned>(n[lane & (kSelectWarps - 1)]) : 0u));
+  };
   __shared__ int found, rest, first_move;
   const int b = blockIdx.x / p.Hkv, kvh = blockIdx.x - b * p.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -105,6 +130,9 @@ __global__ void __launch_bounds__(kSelectThreads) attn_evict_select(const Params
   const float* mass = p.mass + static_cast<size_t>(blockIdx.x) * p.cap;
   const int old = len - p.recent;   // more than m
   int m = p.budget - p.recent;      // how many of them stay
+  const int each = ((old + kSelectWarps - 1) / kSelectWarps + 31) & ~31;  // of a warp; old is at least 1
+  Stretch stretch = {mass, min(old, warp * each), min(old, (warp + 1) * each), lane, {}};
+  stretch.load();
   uint32_t above = 0;               // the value's digits so far
   int shift = 32;
 #pragma unroll 1
@@ -112,21 +140,18 @@ __global__ void __launch_bounds__(kSelectThreads) attn_evict_select(const Params
     const int width = pass < 2 ? 11 : 10;
     const uint32_t high = pass == 0 ? 0u : 0xFFFFFFFFu << shift;
     shift -= width;
-    for (int i = threadIdx.x; i < kBins; i += kSelectThreads) bins[i] = 0;
+    static_assert(kBins == 4 * kSelectThreads, "four bins a thread");
+    reinterpret_cast<int4*>(bins)[threadIdx.x] = make_int4(0, 0, 0, 0);
     __syncthreads();
-    each_mass<kSelectThreads>(mass, 0, old, threadIdx.x, [&](bool valid, int, float value) {
+    stretch.each([&](bool valid, int, float value) {
       const uint32_t x = order_of(value);
       if (valid && (x & high) == above) atomicAdd(&bins[(x >> shift) & ((1 << width) - 1)], 1);
     });
     __syncthreads();
     // From the top bin down: the one in which the m-th lies. Thread t has bins 4 t .. 4 t + 3 from
     // the top.
-    int mine[4], sum = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      mine[j] = bins[kBins - 1 - (4 * threadIdx.x + j)];
-      sum += mine[j];
-    }
+    const int4 four = reinterpret_cast<const int4*>(bins)[kSelectThreads - 1 - threadIdx.x];
+    const int mine[4] = {four.w, four.z, four.y, four.x}, sum = (four.x + four.y) + (four.z + four.w);
     int upto = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -135,8 +160,7 @@ __global__ void __launch_bounds__(kSelectThreads) attn_evict_select(const Params
     }
     if (lane == 31) warp_n[0][warp] = upto;
     __syncthreads();
-    int before = upto - sum;
-    for (int w = 0; w < warp; ++w) before += warp_n[0][w];
+    int before = upto - sum + before_warp(warp_n[0], warp, lane);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (before < m && m <= before + mine[j]) {
@@ -152,11 +176,9 @@ __global__ void __launch_bounds__(kSelectThreads) attn_evict_select(const Params
   }
   // Above `above` all stay, of those equal to it the first m. With none of the old to stay, none do.
   const bool none = p.budget == p.recent;
-  const int each = ((old + kSelectWarps - 1) / kSelectWarps + 31) & ~31;  // old is at least 1
-  const int lo = min(old, warp * each), hi = min(old, lo + each);
   int more = 0, equal = 0;
   if (!none) {
-    each_mass<32>(mass, lo, hi, lane, [&](bool valid, int, float value) {
+    stretch.each([&](bool valid, int, float value) {
       const uint32_t x = order_of(value);
       more += valid && x > above;
       equal += valid && x == above;
@@ -172,11 +194,7 @@ __global__ void __launch_bounds__(kSelectThreads) attn_evict_select(const Params
     warp_n[1][warp] = equal;
   }
   __syncthreads();
-  int n_more = 0, n_equal = 0;  // before the key at hand
-  for (int w = 0; w < warp; ++w) {
-    n_more += warp_n[0][w];
-    n_equal += warp_n[1][w];
-  }
+  int n_more = before_warp(warp_n[0], warp, lane), n_equal = before_warp(warp_n[1], warp, lane);  // before the key at hand
   int* src = p.src + static_cast<size_t>(blockIdx.x) * p.keep;
   float* src_mass = p.src_mass + static_cast<size_t>(blockIdx.x) * p.keep;
   auto put = [&](int d, int i, float value) {
@@ -188,7 +206,7 @@ __global__ void __launch_bounds__(kSelectThreads) attn_evict_select(const Params
   int first_gone = none ? 0 : p.keep;
   if (!none) {
     const uint32_t below = (1u << lane) - 1;
-    each_mass<32>(mass, lo, hi, lane, [&](bool valid, int i, float value) {
+    stretch.each([&](bool valid, int i, float value) {
       const uint32_t x = order_of(value);
       const uint32_t is_more = __ballot_sync(0xFFFFFFFFu, valid && x > above);
       const uint32_t is_equal = __ballot_sync(0xFFFFFFFFu, valid && x == above);

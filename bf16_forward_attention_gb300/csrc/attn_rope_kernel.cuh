@@ -364,12 +364,13 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas<kForm>) attn_rope_bwd(const
   turn_lane<kForm>(lane, p.half, t);
 #pragma unroll 1
   for (int kind = 0; kind < 2; ++kind) {
-    // Every parts-th of the queries' and then the keys' heads is this warp's.
-    const int h_first = kind == 0 ? part : (part + p.parts - p.Hq % p.parts) % p.parts;
+    // This warp's part of the queries' and then the keys' heads: of one kind where there are many parts.
+    const int all = p.Hq + p.Hkv, before = kind == 0 ? 0 : p.Hq;
+    const int h_first = max(static_cast<int>(static_cast<long long>(all) * part / p.parts) - before, 0);
     const Rows& in = kind == 0 ? p.q : p.k;
     const Rows& gin = kind == 0 ? bp.dq_out : bp.dk_out;
     const Rows& out = kind == 0 ? bp.dq : bp.dk;
-    const int H = kind == 0 ? p.Hq : p.Hkv;
+    const int H = min(static_cast<int>(static_cast<long long>(all) * (part + 1) / p.parts) - before, kind == 0 ? p.Hq : p.Hkv);
     const Cols weight = load_cols((kind == 0 ? p.wq : p.wk) + 8 * (lane & 7));
     F8 dw[2] = {both(0.f), both(0.f)};
     for (long long first = static_cast<long long>(group) * kTokens;
@@ -378,7 +379,6 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas<kForm>) attn_rope_bwd(const
       const uint16_t* px = row_of(in, tk, h_first, lane);
       const uint16_t* py = row_of(gin, tk, h_first, lane);
       uint16_t* pd = row_of(out, tk, h_first, lane);
-      const long long in_step = p.parts * in.head, gin_step = p.parts * gin.head, out_step = p.parts * out.head;
       int h_load = h_first, s_load = 0;
       auto load = [&]() {  // the next head, if there is one, into the next stage
         if (h_load < H) {
@@ -387,9 +387,9 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas<kForm>) attn_rope_bwd(const
           ptx::cp_async16(to + 512, px + 64);
           ptx::cp_async16(to + 1024, py);
           ptx::cp_async16(to + 1536, py + 64);
-          px += in_step;
-          py += gin_step;
-          h_load += p.parts;
+          px += in.head;
+          py += gin.head;
+          ++h_load;
           s_load = s_load + 1 == kStages ? 0 : s_load + 1;
         }
         ptx::cp_async_commit();
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas<kForm>) attn_rope_bwd(const
       ok = ok && tk.there;
       turn_load<kForm, true>(p, lane, ok ? tk.pos : 0, t);
       int stage = 0;
-      for (int h = h_first; h < H; h += p.parts) {
+      for (int h = h_first; h < H; ++h) {
         __syncwarp();  // what the stage held has been read
         load();
         ptx::cp_async_wait<kStages - 1>();
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas<kForm>) attn_rope_bwd(const
 #pragma unroll
         for (int e = 0; e < 2; ++e) g[e] = mul(fma(a[e], m, g[e]), r8);
         if (ok) store_cols(pd, g, p.mode);
-        pd += out_step;
+        pd += out.head;
       }
     }
 #pragma unroll
