@@ -117,9 +117,9 @@ int attn_cache_evict(void* k_pages, void* v_pages, const int32_t* page_table, co
   p.layout = layout;
   p.n_pages = static_cast<int>(n_pages);
   p.page_size = static_cast<int>(page_size);
-  p.page_shift = -1;
-  for (int s = 0; s < 31; ++s)
-    if (page_size == int64_t(1) << s) p.page_shift = s;
+  const PageDivisor div = page_divisor(page_size);
+  p.page_mul = div.mul;
+  p.page_shift = div.shift;
   p.max_pages = static_cast<int>(max_pages);
   p.budget = static_cast<int>(budget);
   p.recent = static_cast<int>(recent);

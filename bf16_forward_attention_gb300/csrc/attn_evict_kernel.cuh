@@ -8,7 +8,7 @@
 // the two), and later rounds read places that no earlier one wrote: place d takes key src[d] >= d,
 // and a later round's keys lie behind all of this round's.
 #pragma once
-#include "attn_fwd_kernel.cuh"
+#include "few_rows.cuh"
 
 namespace attn {
 namespace evict {
@@ -27,6 +27,7 @@ struct Params {
   float* src_mass;         // their masses
   int page_rows;           // rows of 128 from a page to the next
   int B, Hkv, cap, layout, n_pages, page_size, page_shift, max_pages;
+  uint32_t page_mul;       // with page_shift: see page_divisor
   int budget, recent, keep;  // keep: min(budget, cap)
 };
 
@@ -78,10 +79,6 @@ struct Stretch {
     }
   }
 };
-
-__device__ __forceinline__ int page_of(const Params& p, int key) {
-  return p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
-}
 
 // ---------------------------------------------------------------- select
 constexpr int kSelectWarps = 16;
@@ -263,7 +260,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kMoveThreads,
   if (!over) return;
   const int half = threadIdx.x >> 4, chunk = threadIdx.x & 15;
   auto row_of = [&](int key) {  // of 128, in the pages
-    const int page = page_of(p, key), i = key - page * p.page_size;
+    const int page = few::page_of(key, p.page_mul, p.page_shift), i = key - page * p.page_size;
     return __ldg(pages + page) * p.page_rows + (p.layout == 0 ? kvh * p.page_size + i : i * p.Hkv + kvh);
   };
   auto at = [&](uint16_t* t, int row) { return reinterpret_cast<uint4*>(t + static_cast<size_t>(row) * kD) + chunk; };

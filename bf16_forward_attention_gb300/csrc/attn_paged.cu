@@ -189,9 +189,9 @@ int attn_fwd_paged(const void* q, const void* k_pages, const void* v_pages, cons
   p.mode = rounding_mode;
   p.n_pages = static_cast<int>(n_pages);
   p.page_size = static_cast<int>(page_size);
-  p.page_shift = -1;
-  for (int s = 0; s < 31; ++s)
-    if (page_size == int64_t(1) << s) p.page_shift = s;
+  const PageDivisor div = page_divisor(page_size);
+  p.page_mul = div.mul;
+  p.page_shift = div.shift;
   p.max_pages = static_cast<int>(max_pages);
   p.page_rows = static_cast<int>(page_stride / attn::kD);
   p.rows = static_cast<int>(pl.rows);

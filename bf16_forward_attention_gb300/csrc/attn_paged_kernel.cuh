@@ -61,7 +61,8 @@ struct Params {
   float* lse2;             // with mass, of rows not cut: [b][kv head][rows4], log2 units; +Inf: not to be used
   float* logits;           // with mass: [b][kv head][cap][rows4], log2 units
   int B, Hq, Hkv, group, Sq, cap, layout, causal, mode;
-  int n_pages, page_size, page_shift, max_pages;  // page_shift: log2 of the page size, or -1
+  int n_pages, page_size, page_shift, max_pages;
+  uint32_t page_mul;       // with page_shift: see page_divisor
   int page_rows;           // rows of 128 from a page to the next
   int rows, rows4;         // Sq * group; that, in fours
   int blocks, block_rows, rows8;  // blocks of at most block_rows rows; rows8: the kernel's rows of a block
@@ -158,11 +159,14 @@ __device__ __forceinline__ bool find_run(const int* seqlens, int B, int cap, int
 // A run's units one after another.
 struct Walk {
   int b, item, t;       // sequence, its item, the item's unit
+  int kvh, block;       // the item's kv head and block
   int len, units;       // the sequence's keys (-1: out of range), its items' units
+  int next_len;         // what the length of the next sequence reads, on its way
   long long first;      // place of the sequence
 
   __device__ __forceinline__ void enter(const Params& p) {
-    len = __ldg(p.seqlens + b);
+    len = next_len;
+    next_len = __ldg(p.seqlens + min(b + 1, p.B - 1));
     units = units_of(len, p.cap);
     if (len > p.cap) len = -1;
     len = max(len, -1);
@@ -170,16 +174,23 @@ struct Walk {
   __device__ __forceinline__ void start(const Params& p, const Run& run, int cost) {
     b = run.b;
     first = run.first;
+    next_len = __ldg(p.seqlens + b);
     enter(p);
     const long long rel = run.lo - run.first;
     item = static_cast<int>(rel / (units + cost));
     t = max(0, static_cast<int>(rel - static_cast<long long>(item) * (units + cost)) - cost);
+    kvh = item / p.blocks;
+    block = item - kvh * p.blocks;
   }
   __device__ __forceinline__ void step(const Params& p, int per, int cost) {
     if (++t < units) return;
     t = 0;
+    if (++block == p.blocks) {
+      block = 0;
+      ++kvh;
+    }
     if (++item < per) return;
-    item = 0;
+    item = kvh = 0;
     first += static_cast<long long>(per) * (units + cost);
     if (++b < p.B) enter(p);
   }
@@ -190,12 +201,29 @@ struct Walk {
   }
 };
 
+// A key's place in the pages, in two steps: the page's number is read a unit before it is looked at (a read
+// waited for at once cost 600 cycles a unit).
+struct Place {
+  int id, at;  // at: row of 128 within the page; -1: there is no such key
+};
+__device__ __forceinline__ Place place_of(const Params& p, const Walk& w, int key) {
+  if (key >= w.len) return {0, -1};
+  const int page = few::page_of(key, p.page_mul, p.page_shift), i = key - page * p.page_size;
+  return {__ldg(p.table + static_cast<size_t>(w.b) * p.max_pages + page),
+          p.layout == 0 ? w.kvh * p.page_size + i : i * p.Hkv + w.kvh};
+}
+// Its row of 128 in the pages; -1: none, -2: its page is out of range.
+__device__ __forceinline__ int row_of(const Params& p, const Place& x) {
+  if (x.at < 0) return -1;
+  return x.id >= 0 && x.id < p.n_pages ? x.id * p.page_rows + x.at : -2;
+}
+
 // An item's rows.
 struct Item {
   int b, kvh, row0, n_rows;
 };
-__device__ __forceinline__ Item item_of(const Params& p, int b, int item) {
-  const int kvh = item / p.blocks, row0 = (item - kvh * p.blocks) * p.block_rows;
+__device__ __forceinline__ Item item_of(const Params& p, int b, int kvh, int block) {
+  const int row0 = block * p.block_rows;
   return {b, kvh, row0, min(p.block_rows, p.rows - row0)};
 }
 
@@ -253,18 +281,9 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) attn_paged_fwd(const Pa
   Walk ahead;
   ahead.start(p, run, kCost);
   uint32_t bad_stages = 0;  // of those in the ring, which hold a key without a page
-  // Row of 128 (in the pages) of key `lane % 16` of the team's share of the unit, -1: none, -2: bad.
-  auto row_of = [&]() {
-    const int key = ahead.t * kUnit + team * few::kKeys + chunk;
-    if (key >= ahead.len) return -1;
-    const int page = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
-    const int at = key - page * p.page_size;
-    const int id = __ldg(p.table + static_cast<size_t>(ahead.b) * p.max_pages + page);
-    if (id < 0 || id >= p.n_pages) return -2;
-    const int kvh = ahead.item / p.blocks;
-    return id * p.page_rows + (p.layout == 0 ? kvh * p.page_size + at : at * p.Hkv + kvh);
-  };
-  auto load = [&](int row, int s) {
+  auto look_up = [&]() { return place_of(p, ahead, ahead.t * kUnit + team * few::kKeys + chunk); };
+  auto load = [&](const Place& place, int s) {
+    const int row = row_of(p, place);
     const bool bad = __any_sync(0xFFFFFFFFu, row == -2);
     bad_stages = (bad_stages & ~(1u << s)) | (bad ? 1u << s : 0u);
     const uint32_t dst = ring + s * kStageBytes;
@@ -280,14 +299,14 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) attn_paged_fwd(const Pa
     }
   };
   const int n = run.n;
-  int next = row_of();
+  Place next = look_up();
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) {
     if (s < n) {
       load(next, s);
       if (s + 1 < n) {
         ahead.step(p, per, kCost);
-        next = row_of();
+        next = look_up();
       }
     }
     ptx::cp_async_commit();
@@ -303,7 +322,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) attn_paged_fwd(const Pa
   for (int i = 0; i < n; ++i) {
     if (fresh) {  // an item begins
       fresh = false;
-      it = item_of(p, at.b, at.item);
+      it = item_of(p, at.b, at.kvh, at.block);
       t_first = at.t;
       bad = false;
       rows.clear();
@@ -335,7 +354,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) attn_paged_fwd(const Pa
     ptx::cp_async_commit();
     if (i + kStages < n) {
       ahead.step(p, per, kCost);
-      next = row_of();
+      next = look_up();
     }
     const uint32_t kt = ring + s * kStageBytes;
     const int key0 = at.t * kUnit + team * few::kKeys;
@@ -558,17 +577,9 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
   Walk ahead;
   ahead.start(p, run, kCost);
   uint32_t bad_stages = 0;
-  auto row_of = [&]() {  // as in attn_paged_fwd
-    const int key = ahead.t * kUnit + warp * 16 + chunk;
-    if (key >= ahead.len) return -1;
-    const int page = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
-    const int at = key - page * p.page_size;
-    const int id = __ldg(p.table + static_cast<size_t>(ahead.b) * p.max_pages + page);
-    if (id < 0 || id >= p.n_pages) return -2;
-    const int kvh = ahead.item / p.blocks;
-    return id * p.page_rows + (p.layout == 0 ? kvh * p.page_size + at : at * p.Hkv + kvh);
-  };
-  auto load = [&](int row, int s) {
+  auto look_up = [&]() { return place_of(p, ahead, ahead.t * kUnit + warp * 16 + chunk); };
+  auto load = [&](const Place& place, int s) {
+    const int row = row_of(p, place);
     const bool bad = __any_sync(0xFFFFFFFFu, row == -2);
     bad_stages = (bad_stages & ~(1u << s)) | (bad ? 1u << s : 0u);
     const uint32_t dst = base + s * kRowsStage;
@@ -582,14 +593,14 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
     }
   };
   const int n = run.n;
-  int next = row_of();
+  Place next = look_up();
 #pragma unroll
   for (int s = 0; s < kRowsStages - 1; ++s) {
     if (s < n) {
       load(next, s);
       if (s + 1 < n) {
         ahead.step(p, per, kCost);
-        next = row_of();
+        next = look_up();
       }
     }
     ptx::cp_async_commit();
@@ -617,7 +628,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
   for (int i = 0; i < n; ++i) {
     if (fresh) {  // an item begins
       fresh = false;
-      it = item_of(p, at.b, at.item);
+      it = item_of(p, at.b, at.kvh, at.block);
       t_first = at.t;
       bad = false;
       ref = neg_inf;
@@ -671,7 +682,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
     ptx::cp_async_commit();
     if (i + kRowsStages < n) {
       ahead.step(p, per, kCost);
-      next = row_of();
+      next = look_up();
     }
     uint32_t x[kChunks][16];
 #pragma unroll
@@ -852,9 +863,14 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
     const size_t part = 2 * static_cast<size_t>(blockIdx.x) + (t_first == 0 ? 1 : 0);
     const float inv = __frcp_rn(L);
     float* xs = reinterpret_cast<float*>(smem + kRowsOffX);
+    constexpr int kN = 16 / kCopies;  // columns of a lane in the end, of every 16
+    const bool there = r < it.n_rows && dbg_ok(it.row0 + r < p.rows && it.b < p.B && it.kvh < p.Hkv);
+    float* to_part = p.part_o + part * p.rows8 * kD + part_place(r, copy * kN);
+    uint16_t* to_out =
+        p.out + (there ? few::query_at(p.layout, p.Hq, p.Sq, p.group, it.b, it.kvh, it.row0 + r) : 0) + copy * kN;
+    const bool good = !skip && at.len >= 0;
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      constexpr int kN = 16 / kCopies;  // columns of a lane in the end
       float y[16];
 #pragma unroll
       for (int d = 0; d < 8; ++d) {
@@ -873,20 +889,23 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
 #pragma unroll
         for (int z = 0; z < kCopies; ++z)
 #pragma unroll
-          for (int d = 0; d < kN; ++d) y[d] += xs[(z * kLanes + r) * kXPitch + copy * kN + d];
+          for (int d = 0; d < kN; d += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(xs + (z * kLanes + r) * kXPitch + copy * kN + d);
+            y[d] += v.x;
+            y[d + 1] += v.y;
+            y[d + 2] += v.z;
+            y[d + 3] += v.w;
+          }
         __syncthreads();
       }
-      const int d0 = 16 * q + copy * kN;
-      if (r >= it.n_rows) {
-      } else if (!whole) {
-        float* to = p.part_o + part * p.rows8 * kD;
+      if (there && !whole) {
+        // Columns copy * kN + d of 16: d's bits 0..2 and the rest of them apart in part_place.
 #pragma unroll
-        for (int d = 0; d < kN; ++d) to[part_place(r, d0 + d)] = y[d];
-      } else if (!skip && at.len >= 0 && dbg_ok(it.row0 + r < p.rows && it.b < p.B && it.kvh < p.Hkv)) {
-        uint16_t* to = p.out + few::query_at(p.layout, p.Hq, p.Sq, p.group, it.b, it.kvh, it.row0 + r) + d0;
+        for (int d = 0; d < kN; ++d) to_part[q * 128 + (d & 7) * 16 + (d & 8) / 4] = y[d];
+      } else if (there && good) {
 #pragma unroll
         for (int d = 0; d < kN; d += 4)
-          *reinterpret_cast<uint2*>(to + d) =
+          *reinterpret_cast<uint2*>(to_out + 16 * q + d) =
               make_uint2(round_bf16_bits(y[d] * inv, p.mode) | (round_bf16_bits(y[d + 1] * inv, p.mode) << 16),
                          round_bf16_bits(y[d + 2] * inv, p.mode) | (round_bf16_bits(y[d + 3] * inv, p.mode) << 16));
       }
@@ -940,7 +959,8 @@ __device__ __forceinline__ void join(const Params& p, int run, int g) {
   __shared__ float row_r[8], row_l[8];
   const Cut cut = p.cuts[run];
   if (cut.parts == 0) return;
-  const Item it = item_of(p, cut.b, cut.item);
+  const int kvh = cut.item / p.blocks;
+  const Item it = item_of(p, cut.b, kvh, cut.item - kvh * p.blocks);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (8 * g >= it.n_rows || !dbg_ok(cut.b < p.B && cut.parts <= p.runs - run)) return;
   const float neg_inf = -__int_as_float(0x7F800000);

@@ -25,6 +25,11 @@ __device__ __forceinline__ int own_limit(int i, int len, int Sq, int causal) {
   return causal ? max(0, len - (Sq - 1 - i)) : len;
 }
 
+// The page of key `key`: mul and shift of page_divisor.
+__device__ __forceinline__ int page_of(int key, uint32_t mul, int shift) {
+  return shift < 0 ? key : static_cast<int>(__umulhi(static_cast<uint32_t>(key), mul) >> shift);
+}
+
 // Row r of a (sequence, kv head)'s Sq * group rows, tokens first: element offset of its
 // query (or output) row.
 __device__ __forceinline__ size_t query_at(int layout, int Hq, int Sq, int group, int b, int kvh, int r) {

@@ -111,4 +111,22 @@ inline bool pages_in_range(int64_t n_pages, int64_t page_size, int64_t page_stri
   return page_size <= lim / n_pages;
 }
 
+// key / page_size for 0 <= key < 2^31 as a multiplication (Granlund and Montgomery, "Division by
+// invariant integers using multiplication", 1994): with 2^(l-1) < page_size <= 2^l and mul =
+// ceil(2^(31+l) / page_size), which is below 2^32, it is key * mul / 2^(31+l), rounded down. The kernels
+// take the upper 32 bits of the product and shift them by l - 1; a page size of 1 (l = 0) has shift -1.
+struct PageDivisor {
+  uint32_t mul;
+  int shift;
+};
+inline PageDivisor page_divisor(int64_t page_size) {
+  int l = 0;
+  while ((int64_t(1) << l) < page_size) ++l;
+  const uint64_t n = uint64_t(1) << (31 + l), q = n / uint64_t(page_size) + (n % uint64_t(page_size) != 0);
+  return {static_cast<uint32_t>(q), l - 1};
+}
+inline int64_t page_of(int64_t key, PageDivisor d) {
+  return d.shift < 0 ? key : static_cast<int64_t>((uint64_t(key) * d.mul) >> 32 >> d.shift);
+}
+
 }  // namespace attn_host

@@ -18,7 +18,7 @@ int main() {
   char kind;
   long long x[14];
   while (std::cin >> kind) {
-    const int n = kind == 'd' ? 6 : kind == 'm' ? 14 : kind == 'p' ? 6 : 3;
+    const int n = kind == 'd' ? 6 : kind == 'm' ? 14 : kind == 'p' ? 6 : kind == 'q' ? 2 : 3;
     for (int i = 0; i < n; ++i) std::cin >> x[i];
     const char* base = nullptr;
     auto rows = [&](int i, long long off) {
@@ -30,6 +30,7 @@ int main() {
       const PageSet a{base + (1 << 20) + x[0] * 2, x[2], x[3], x[4]}, b{base + (1 << 20) + x[1] * 2, x[2], x[3], x[5]};
       std::printf("%d\n", pages_meet(a, b));
     }
+    if (kind == 'q') std::printf("%d\n", page_of(x[0], page_divisor(x[1])) == x[0] / x[1]);
     if (kind == 'e') {
       const RowSet r{base, x[0], x[1], x[2], (1LL << 31) - 1, (1LL << 31) - 1, 1 << 20};
       std::printf("%d\n", extent_in_range(r));
@@ -129,3 +130,19 @@ def test_extents_do_not_wrap(ask):
     big = (1 << 40) - 1
     assert ask("e", [(big, big, big), (1 << 20, 0, 0), (0, 128, 128), (0, 0, big), (1 << 19, 1 << 19, 0)]) == [
         False, False, True, False, False]
+
+
+def test_pages_of_keys(ask):
+    """The multiplication that stands for a division by the page size, at the borders of pages and of
+    31 bits."""
+    top = (1 << 31) - 1
+    rng = random.Random(4)
+    sizes = [*range(1, 70), 100, 127, 128, 129, 255, 256, 257, 1000, 65535, 65536, 65537, 1 << 30, (1 << 30) + 1, top]
+    sizes += [rng.randint(1, top) for _ in range(300)] + [rng.randint(1, 5000) for _ in range(300)]
+    cases = []
+    for d in sizes:
+        n = top // d
+        for q in {0, 1, 2, n // 2, n - 1, n, rng.randint(0, n)}:
+            cases += [(k, d) for k in (q * d - 1, q * d, q * d + 1, q * d + d - 1) if 0 <= k <= top]
+        cases += [(top, d), (top - 1, d), (rng.randint(0, top), d)]
+    assert all(ask("q", cases))
