@@ -25,7 +25,7 @@ constexpr int kMaxRows = 128;                      // rows of a block at most
 // What an item costs a run beside its units, in units (its queries, its rows' addition and stores):
 // 1.5 us against 1.4 a unit, and 5 against 1.8 in attn_paged_rows. Runs of equal numbers of units made
 // those of many short items the last to end (48 x 5 drafted tokens: 63 to 108 us a run).
-constexpr int kItemCost = 1, kRowsItemCost = 3;
+constexpr int kItemCost = 1, kRowsItemCost = 4;
 
 // kNT 8-row groups a warp, kGroups warps a team: blocks of up to 8 kNT kGroups rows.
 template <int kNT_, int kGroups_, int kStages_, int kCtas_>
@@ -869,16 +869,20 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
     uint16_t* to_out =
         p.out + (there ? few::query_at(p.layout, p.Hq, p.Sq, p.group, it.b, it.kvh, it.row0 + r) : 0) + copy * kN;
     const bool good = !skip && at.len >= 0;
-#pragma unroll
+    // A short loop that moves the row along: written out it was 2000 instructions that an item's end had to
+    // fetch (9400 cycles an item).
+#pragma unroll 1
     for (int q = 0; q < 8; ++q) {
       float y[16];
 #pragma unroll
       for (int d = 0; d < 8; ++d) {
         float lo, hi;
-        ptx::f2_unpack(o[8 * q + d], lo, hi);
+        ptx::f2_unpack(o[d], lo, hi);
         y[2 * d] = lo * scale;
         y[2 * d + 1] = hi * scale;
       }
+#pragma unroll
+      for (int d = 0; d < kD / 2 - 8; ++d) o[d] = o[d + 8];
       if constexpr (kCopies > 1) {
 #pragma unroll
         for (int d = 0; d < 4; ++d)
