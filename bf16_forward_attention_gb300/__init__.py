@@ -142,6 +142,8 @@ def load_library(debug: bool | None = None) -> ctypes.CDLL:
     lib.attn_qk_norm_rope_bwd_workspace_bytes.restype = i64
     lib.attn_fwd_paged.argtypes = [vp] * 8 + [ci] + [i64] * 9 + [cf, ci, ci, vp, i64, vp]
     lib.attn_fwd_paged.restype = ci
+    lib.attn_fwd_paged_timeout_selftest.argtypes = lib.attn_fwd_paged.argtypes + [ctypes.c_uint64]
+    lib.attn_fwd_paged_timeout_selftest.restype = ci
     lib.attn_fwd_paged_workspace_bytes.argtypes = [i64] * 7 + [ci]
     lib.attn_fwd_paged_workspace_bytes.restype = i64
     lib.attn_cache_evict.argtypes = [vp] * 7 + [ci] + [i64] * 9 + [vp, i64, vp]

@@ -29,15 +29,16 @@ using Kernel = void (*)(const paged::Params);
 // A block's rows, and the kernel for them, with and without the keys' masses.
 struct Form {
   int rows, threads, smem, ctas, cost;
+  bool waits;  // for the tensor cores
   Kernel fwd[2];
 };
 template <typename S>
 constexpr Form form() {
-  return {S::kRows, S::kThreads, S::kSmem, S::kCtas, paged::kItemCost, {paged::attn_paged_fwd<S, false>, paged::attn_paged_fwd<S, true>}};
+  return {S::kRows, S::kThreads, S::kSmem, S::kCtas, paged::kItemCost, false, {paged::attn_paged_fwd<S, false>, paged::attn_paged_fwd<S, true>}};
 }
 template <int kCopies>
 constexpr Form rows_form() {
-  return {128 / kCopies, paged::kRowsThreads, paged::kRowsSmem, 2, paged::kRowsItemCost,
+  return {128 / kCopies, paged::kRowsThreads, paged::kRowsSmem, 2, paged::kRowsItemCost, true,
           {paged::attn_paged_rows<kCopies, false>, paged::attn_paged_rows<kCopies, true>}};
 }
 constexpr Form kForms[] = {form<paged::Rows8>(), form<paged::Rows16>(), rows_form<4>(), rows_form<2>(), rows_form<1>()};
@@ -109,22 +110,11 @@ int make_plan(Plan* pl, int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int64_t 
   return ATTN_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-int64_t attn_fwd_paged_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int64_t page_size,
-                                       int64_t max_pages, int64_t d, int with_mass) {
-  Plan pl;
-  const int st = make_plan(&pl, B, Hq, Hkv, Sq, page_size, max_pages, d, with_mass != 0);
-  return st != ATTN_OK ? st : pl.bytes();
-}
-
-int attn_fwd_paged(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
+int run(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
                    const int32_t* seqlens, void* out, float* lse, float* mass, int layout, int64_t B, int64_t Hq,
                    int64_t Hkv, int64_t Sq, int64_t n_pages, int64_t page_size, int64_t page_stride,
                    int64_t max_pages, int64_t d, float scale, int rounding_mode, int flags, void* workspace,
-                   int64_t workspace_bytes, void* stream) {
+                   int64_t workspace_bytes, void* stream, uint64_t timeout_ns, bool withhold) {
   // ---- host-side validation (nothing is launched on failure)
   if (!q || !page_table || !seqlens || !out || !lse || !workspace) return ATTN_ERR_INVALID_ARG;
   if (!std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
@@ -137,6 +127,7 @@ int attn_fwd_paged(const void* q, const void* k_pages, const void* v_pages, cons
   st = check_pages(k_pages, v_pages, n_pages, page_size, page_stride, Hkv);
   if (st != ATTN_OK) return st;
   if (workspace_bytes < pl.bytes()) return ATTN_ERR_INVALID_ARG;
+  if (withhold && !pl.form->waits) return ATTN_ERR_UNSUPPORTED;
   for (const void* p : {q, static_cast<const void*>(out), static_cast<const void*>(workspace)})
     if (reinterpret_cast<uintptr_t>(p) & 15u) return ATTN_ERR_MISALIGNED;
   if ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(seqlens) |
@@ -203,7 +194,8 @@ int attn_fwd_paged(const void* q, const void* k_pages, const void* v_pages, cons
   p.runs = static_cast<int>(pl.runs);
   p.join_groups = static_cast<int>((pl.block_rows + 7) / 8);
   p.c = scale * 1.4426950408889634f;
-  p.timeout_ns = kTimeoutNs;
+  p.timeout_ns = timeout_ns;
+  p.withhold = withhold ? 1 : 0;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (!launch(pl.form->fwd[mass ? 1 : 0], pl.runs, pl.form->threads, pl.form->smem, cs, false, p))
     return ATTN_ERR_LAUNCH;
@@ -215,6 +207,39 @@ int attn_fwd_paged(const void* q, const void* k_pages, const void* v_pages, cons
   if (!launch(finish, blocks, paged::kJoinThreads * (few ? 1 : 4), static_cast<int>(pl.runs) * 32, cs, true, p))
     return ATTN_ERR_LAUNCH;
   return ATTN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t attn_fwd_paged_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int64_t page_size,
+                                       int64_t max_pages, int64_t d, int with_mass) {
+  Plan pl;
+  const int st = make_plan(&pl, B, Hq, Hkv, Sq, page_size, max_pages, d, with_mass != 0);
+  return st != ATTN_OK ? st : pl.bytes();
+}
+
+int attn_fwd_paged(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
+                   const int32_t* seqlens, void* out, float* lse, float* mass, int layout, int64_t B, int64_t Hq,
+                   int64_t Hkv, int64_t Sq, int64_t n_pages, int64_t page_size, int64_t page_stride,
+                   int64_t max_pages, int64_t d, float scale, int rounding_mode, int flags, void* workspace,
+                   int64_t workspace_bytes, void* stream) {
+  return run(q, k_pages, v_pages, page_table, seqlens, out, lse, mass, layout, B, Hq, Hkv, Sq, n_pages, page_size,
+             page_stride, max_pages, d, scale, rounding_mode, flags, workspace, workspace_bytes, stream, kTimeoutNs,
+             false);
+}
+
+int attn_fwd_paged_timeout_selftest(const void* q, const void* k_pages, const void* v_pages,
+                                    const int32_t* page_table, const int32_t* seqlens, void* out, float* lse,
+                                    float* mass, int layout, int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq,
+                                    int64_t n_pages, int64_t page_size, int64_t page_stride, int64_t max_pages,
+                                    int64_t d, float scale, int rounding_mode, int flags, void* workspace,
+                                    int64_t workspace_bytes, void* stream, uint64_t timeout_ns) {
+  if (timeout_ns < 1 || timeout_ns > 2000000000ull) return ATTN_ERR_INVALID_ARG;
+  return run(q, k_pages, v_pages, page_table, seqlens, out, lse, mass, layout, B, Hq, Hkv, Sq, n_pages, page_size,
+             page_stride, max_pages, d, scale, rounding_mode, flags, workspace, workspace_bytes, stream, timeout_ns,
+             true);
 }
 
 }  // extern "C"

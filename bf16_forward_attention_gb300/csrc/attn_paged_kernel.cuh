@@ -70,6 +70,7 @@ struct Params {
   int join_groups;         // blocks of a run in attn_paged_finish: 8-row groups
   float c;                 // scale * log2(e)
   unsigned long long timeout_ns;  // of a wait for the tensor cores
+  int withhold;            // self-test: never tell of a run's first S
 };
 
 __device__ __forceinline__ int units_of(int len, int cap) {
@@ -671,7 +672,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
     if (warp == 0) {
       ptx::tc_fence_after();
       issue_rows_s(tmem, desc_lo(kt, 16), std::make_integer_sequence<int, 8>{});
-      ptx::mma_commit_warp(bar_s);
+      if (!p.withhold) ptx::mma_commit_warp(bar_s);
     }
     bad = bad || (bad_stages >> s & 1u);
     // ---- the copy's 16 kChunks keys of S; the products before it are done too.

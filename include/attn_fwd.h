@@ -690,6 +690,21 @@ int attn_bwd_timeout_selftest(const void* dout, const void* q, const void* k, co
                               int rounding_mode, int flags, void* workspace, int64_t workspace_bytes,
                               void* stream, uint64_t timeout_ns, int kernel);
 
+/*
+ * attn_fwd_paged_timeout_selftest - the same for attention over a paged cache, in its form for
+ * more than 16 rows (Sq * Hq / Hkv; otherwise ATTN_ERR_UNSUPPORTED), the one that waits for the
+ * tensor cores: arguments, checks and launches of attn_fwd_paged, plus the wait limit. No run of
+ * tiles hears of its first products, so each gives up; out and lse keep their contents (the
+ * masses, where given, are undefined), and attn_fwd_last_error() reports ATTN_ERR_TIMEOUT.
+ */
+int attn_fwd_paged_timeout_selftest(const void* q, const void* k_pages, const void* v_pages,
+                                    const int32_t* page_table, const int32_t* seqlens, void* out,
+                                    float* lse, float* mass, int layout, int64_t B, int64_t Hq,
+                                    int64_t Hkv, int64_t Sq, int64_t n_pages, int64_t page_size,
+                                    int64_t page_stride, int64_t max_pages, int64_t d, float scale,
+                                    int rounding_mode, int flags, void* workspace,
+                                    int64_t workspace_bytes, void* stream, uint64_t timeout_ns);
+
 /* Library version, as MAJOR*10000 + MINOR*100 + PATCH. */
 int attn_fwd_version(void);
 

@@ -87,3 +87,19 @@ def test_python_refusals(change, exc):
         attn.attn_fwd_paged(bf(2, 1, 4, 128), bf(8, 16, 2, 128), bf(8, 16, 2, 128),
                             torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32),
                             **{"layout": "bshd", **change})
+
+
+@pytest.mark.parametrize("kw,ns,status", [
+    (dict(Hq=40), 0, INVALID), (dict(Hq=40), 2_000_000_001, INVALID), (dict(Hq=32), 20_000_000, UNSUPPORTED),
+    (dict(Hq=40, d=64), 20_000_000, UNSUPPORTED), (dict(Hq=40, o=A), 20_000_000, ALIASING),
+    (dict(Hq=40), 20_000_000, attn.ATTN_ERR_NO_DEVICE),
+])
+def test_selftest_refusals(lib, kw, ns, status):
+    """It takes attn_fwd_paged's refusals, a limit of 1 ns to 2 s, and only more than 16 rows."""
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are fake")
+    a = dict(o=6 * A, Hq=8, d=128)
+    a.update(kw)
+    assert lib.attn_fwd_paged_timeout_selftest(A, 2 * A, 3 * A, 4 * A, 5 * A, a["o"], 7 * A, 8 * A, 1, 4, a["Hq"], 2, 1,
+                                               100, 16, 16 * 2 * 128, 20, a["d"], ctypes.c_float(0.1), 0, 0, 9 * A,
+                                               1 << 31, 0, ns) == status
