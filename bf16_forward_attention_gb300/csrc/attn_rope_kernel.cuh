@@ -251,9 +251,14 @@ __device__ __forceinline__ uint16_t* row_of(const Rows& r, const Token& t, int h
   return r.p + t.b * r.batch + t.s * r.token + h * r.head + 8 * (lane & 7);
 }
 
+// Five CTAs an SM are 20 warps, 80 KiB on their way (16384 tokens of 20 heads: 25.5 us, 28 with four and 33
+// with six, which spill); the other forms need more registers.
+template <int kForm>
+constexpr int kFwdCtas = kForm == kWhole ? 5 : 4;
+
 // One warp: chunks of four tokens' heads. Bound by HBM: 512 bytes a row.
 template <int kForm, bool kPaged>
-__global__ void __launch_bounds__(kThreads) attn_rope_fwd(const Params p) {
+__global__ void __launch_bounds__(kThreads, kFwdCtas<kForm>) attn_rope_fwd(const Params p) {
   const int lane = threadIdx.x & 31;
   const long long first = (static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kTokens;
   if (first >= p.tokens) return;
