@@ -67,8 +67,14 @@ def _library_up_to_date(debug: bool = False) -> bool:
     return _newer(lib_path(debug), _deps())
 
 
+def _torch_dir():
+    """Where torch is installed; None without it (the library can be used from C all the same)."""
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec else None
+
+
 def _binding_up_to_date() -> bool:
-    return _newer(BINDING_PATH, [BINDING_SOURCE, os.path.join(INCLUDE, "attn_fwd.h")])
+    return _torch_dir() is None or _newer(BINDING_PATH, [BINDING_SOURCE, os.path.join(INCLUDE, "attn_fwd.h")])
 
 
 def up_to_date(debug: bool = False) -> bool:
@@ -77,10 +83,10 @@ def up_to_date(debug: bool = False) -> bool:
 
 def _binding_build(force: bool):
     """A running compilation of the binding's C++ part (no kernels) against the installed torch and
-    Python, and where its output is; None if it is newer than its sources."""
-    if not force and _binding_up_to_date():
+    Python, and where its output is; None if it is newer than its sources, or there is no torch."""
+    torch_dir = _torch_dir()
+    if torch_dir is None or (not force and _binding_up_to_date()):
         return None
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")
     tmp = BINDING_PATH + f".tmp{os.getpid()}"
     cmd = [shutil.which("g++") or "c++", "-std=c++17", "-O2", "-fPIC", "-shared", "-o", tmp, BINDING_SOURCE]

@@ -32,16 +32,18 @@ struct Form {
   bool waits;  // for the tensor cores
   Kernel fwd[2];
 };
-template <typename S>
+template <int kGroups>
 constexpr Form form() {
-  return {S::kRows, S::kThreads, S::kSmem, S::kCtas, paged::kItemCost, false, {paged::attn_paged_fwd<S, false>, paged::attn_paged_fwd<S, true>}};
+  using S = paged::Shape<kGroups>;
+  return {S::kRows, S::kThreads, S::kSmem, 2, paged::kItemCost, false,
+          {paged::attn_paged_fwd<kGroups, false>, paged::attn_paged_fwd<kGroups, true>}};
 }
 template <int kCopies>
 constexpr Form rows_form() {
   return {128 / kCopies, paged::kRowsThreads, paged::kRowsSmem, 2, paged::kRowsItemCost, true,
           {paged::attn_paged_rows<kCopies, false>, paged::attn_paged_rows<kCopies, true>}};
 }
-constexpr Form kForms[] = {form<paged::Rows8>(), form<paged::Rows16>(), rows_form<4>(), rows_form<2>(), rows_form<1>()};
+constexpr Form kForms[] = {form<1>(), form<2>(), rows_form<4>(), rows_form<2>(), rows_form<1>()};
 
 int device_ready() {
   const int st = arch_here();

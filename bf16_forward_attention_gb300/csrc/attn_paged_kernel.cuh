@@ -27,18 +27,16 @@ constexpr int kMaxRows = 128;                      // rows of a block at most
 // those of many short items the last to end (48 x 5 drafted tokens: 63 to 108 us a run).
 constexpr int kItemCost = 1, kRowsItemCost = 4;
 
-// kNT 8-row groups a warp, kGroups warps a team: blocks of up to 8 kNT kGroups rows.
-template <int kNT_, int kGroups_, int kStages_, int kCtas_>
+// kGroups warps a team, 8 rows each: blocks of up to 8 kGroups rows; two CTAs an SM.
+template <int kGroups_>
 struct Shape {
-  static constexpr int kNT = kNT_, kGroups = kGroups_, kStages = kStages_, kCtas = kCtas_;
+  static constexpr int kGroups = kGroups_, kStages = 3;
   static constexpr int kThreads = 32 * kTeams * kGroups;
-  static constexpr int kRows = 8 * kNT * kGroups;
+  static constexpr int kRows = 8 * kGroups;
   static constexpr int kOffX = kTeams * kStages * kStageBytes;       // half of every warp's O^T
-  static constexpr int kOffMl = kOffX + kTeams * kGroups * kNT * 4 * 512;  // [team][row][2] floats
+  static constexpr int kOffMl = kOffX + kTeams * kGroups * 4 * 512;  // [team][row][2] floats
   static constexpr int kSmem = kOffMl + kTeams * kRows * 8;
 };
-using Rows8 = Shape<1, 1, 3, 2>;
-using Rows16 = Shape<1, 2, 3, 2>;
 
 // What a run leaves for the join: the item that it begins and does not end, and in how many
 // parts (0: none).
@@ -260,12 +258,16 @@ __device__ __forceinline__ void skip_row(const Params& p, const Item& it, int r)
   if (r < it.n_rows && p.mass) lse2_at(p, it, r) = __int_as_float(0x7F800000);
 }
 
-// One CTA: a run of units. A team of kGroups warps takes 16 keys of every unit, each warp 8 kNT of
+// One CTA: a run of units. A team of kGroups warps takes 16 keys of every unit, each warp 8 of
 // the block's rows, over a ring of its own (cp.async, kStages of 8 KiB) that runs on from item to
-// item; the teams meet only at an item's end, to add their rows.
-template <typename S, bool kMass>
-__global__ void __launch_bounds__(S::kThreads, S::kCtas) attn_paged_fwd(const Params p) {
-  constexpr int kNT = S::kNT, kGroups = S::kGroups, kStages = S::kStages;
+// item; the teams meet only at an item's end, to add their rows. Bound by HBM where caches are long
+// (64 caches of up to 8192 keys, 8 kv heads of 4 rows, 1.08 GB: 165 us, 6.6 TB/s; runs end after 148 to
+// 163 us, as SMs differ in their share of the bandwidth); a few short ones by the chain of lengths, page
+// numbers, keys and products (7.5 us for 4 caches of up to 1000 keys).
+template <int kGroups, bool kMass>
+__global__ void __launch_bounds__(Shape<kGroups>::kThreads, 2) attn_paged_fwd(const Params p) {
+  using S = Shape<kGroups>;
+  constexpr int kStages = S::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int team = warp / kGroups, grp = warp - team * kGroups;
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) attn_paged_fwd(const Pa
   // ---- products.
   Walk at;
   at.start(p, run, kCost);
-  few::Rows<kNT> rows;
+  few::Rows rows;
   Item it;
   int t_first = 0, min_lim = 0;
   bool bad = false, fresh = true;
@@ -327,20 +329,16 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) attn_paged_fwd(const Pa
       t_first = at.t;
       bad = false;
       rows.clear();
-      const uint16_t* from[kNT];
+      const int r = 8 * grp + (lane >> 2);
+      rows.load_q(r < it.n_rows && at.len >= 0
+                      ? p.q + few::query_at(p.layout, p.Hq, p.Sq, p.group, it.b, it.kvh, it.row0 + r)
+                      : nullptr,
+                  lane);
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) {
-        const int r = 8 * (grp * kNT + nt) + (lane >> 2);
-        from[nt] = r < it.n_rows && at.len >= 0
-                       ? p.q + few::query_at(p.layout, p.Hq, p.Sq, p.group, it.b, it.kvh, it.row0 + r)
-                       : nullptr;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int x = 8 * (grp * kNT + nt) + 2 * (lane & 3) + e;
-          rows.lim[nt][e] = x < it.n_rows ? few::own_limit((it.row0 + x) / p.group, at.len, p.Sq, p.causal) : 0;
-        }
+      for (int e = 0; e < 2; ++e) {
+        const int x = 8 * grp + 2 * (lane & 3) + e;
+        rows.lim[e] = x < it.n_rows ? few::own_limit((it.row0 + x) / p.group, at.len, p.Sq, p.causal) : 0;
       }
-      rows.load_q(from, lane);
       min_lim = few::own_limit(it.row0 / p.group, at.len, p.Sq, p.causal);
     }
     // Every lane's copies of this unit; the team is done with the last one.
@@ -363,19 +361,16 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) attn_paged_fwd(const Pa
     if (key0 < at.len) {
       const bool masked = key0 + few::kKeys > min_lim;
       rows.tile(kt, kt + few::kKvBytes, key0, masked, masked && p.causal, p.c, lane,
-                [&](const float (&x)[kNT][4]) {
+                [&](const float (&x)[4]) {
                   if constexpr (kMass) {
-                    const int r = 8 * grp * kNT + 2 * (lane & 3);
+                    const int r = 8 * grp + 2 * (lane & 3);
+                    if (r >= it.n_rows) return;
                     float* to = p.logits + ((static_cast<size_t>(it.b) * p.Hkv + it.kvh) * p.cap + key0 + (lane >> 2)) *
                                                p.rows4 + it.row0 + r;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                      if (key0 + (lane >> 2) + 8 * e < at.len) {
-#pragma unroll
-                        for (int nt = 0; nt < kNT; ++nt)
-                          if (r + 8 * nt < it.n_rows)
-                            *reinterpret_cast<float2*>(to + 8 * nt) = make_float2(x[nt][2 * e], x[nt][2 * e + 1]);
-                      }
+                      if (key0 + (lane >> 2) + 8 * e < at.len)
+                        *reinterpret_cast<float2*>(to) = make_float2(x[2 * e], x[2 * e + 1]);
                       to += 8 * static_cast<size_t>(p.rows4);
                     }
                   }
@@ -391,88 +386,77 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) attn_paged_fwd(const Pa
     const bool whole = ends && t_first == 0;
     rows.finish_sums();
     float2* ml = reinterpret_cast<float2*>(smem + S::kOffMl);  // [team][row]
-    float4* xs = reinterpret_cast<float4*>(smem + S::kOffX);   // [group][team][nt][dt % 4][lane]
+    float4* xs = reinterpret_cast<float4*>(smem + S::kOffX);   // [group][team][dt % 4][lane]
     const size_t part = 2 * static_cast<size_t>(blockIdx.x) + (t_first == 0 ? 1 : 0);
-    float f[kTeams][kNT][2], R[kNT][2], L[kNT][2];
+    float f[kTeams][2], R[2], L[2];
     bool skip = false;
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       __syncthreads();  // what was there has been read
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) {
+      for (int d = 0; d < 4; ++d) {
+        const float(&o)[4] = rows.o[4 * hf + d];
+        xs[((grp * kTeams + team) * 4 + d) * 32 + lane] = make_float4(o[0], o[1], o[2], o[3]);
+      }
+      if (hf == 0 && (lane >> 2) == 0) {
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          const float(&o)[4] = rows.o[4 * hf + d][nt];
-          xs[(((grp * kTeams + team) * kNT + nt) * 4 + d) * 32 + lane] = make_float4(o[0], o[1], o[2], o[3]);
-        }
-        if (hf == 0 && (lane >> 2) == 0) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e)  // a sum is not negative: -1 says that the rows cannot be formed
-            ml[team * S::kRows + 8 * (grp * kNT + nt) + 2 * lane + e] =
-                make_float2(rows.ref[nt][e], bad ? -1.f : rows.sum[nt][e]);
-        }
+        for (int e = 0; e < 2; ++e)  // a sum is not negative: -1 says that the rows cannot be formed
+          ml[team * S::kRows + 8 * grp + 2 * lane + e] = make_float2(rows.ref[e], bad ? -1.f : rows.sum[e]);
       }
       __syncthreads();
       if (hf == 0) {
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * grp + 2 * (lane & 3) + e;
+          float2 x[kTeams];
+          float M = neg_inf;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = 8 * (grp * kNT + nt) + 2 * (lane & 3) + e;
-            float2 x[kTeams];
-            float M = neg_inf;
-#pragma unroll
-            for (int w = 0; w < kTeams; ++w) {
-              x[w] = ml[w * S::kRows + r];
-              M = fmaxf(M, x[w].x);
-              skip = skip || x[w].y < 0.f;
-            }
-            const float ref = M == neg_inf ? 0.f : M;
-            float sum = 0.f;
-#pragma unroll
-            for (int w = 0; w < kTeams; ++w) {
-              f[w][nt][e] = ptx::ex2(x[w].x - ref);
-              sum = fmaf(x[w].y, f[w][nt][e], sum);
-            }
-            R[nt][e] = M;
-            L[nt][e] = sum;
+          for (int w = 0; w < kTeams; ++w) {
+            x[w] = ml[w * S::kRows + r];
+            M = fmaxf(M, x[w].x);
+            skip = skip || x[w].y < 0.f;
           }
+          const float ref = M == neg_inf ? 0.f : M;
+          float sum = 0.f;
+#pragma unroll
+          for (int w = 0; w < kTeams; ++w) {
+            f[w][e] = ptx::ex2(x[w].x - ref);
+            sum = fmaf(x[w].y, f[w][e], sum);
+          }
+          R[e] = M;
+          L[e] = sum;
+        }
         skip = __any_sync(0xFFFFFFFFu, skip);
         if (team == 0 && (lane >> 2) == 0) {
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int r = 8 * (grp * kNT + nt) + 2 * lane + e;
-              if (!whole)
-                reinterpret_cast<float2*>(p.part_rl)[part * p.rows8 + r] = make_float2(R[nt][e], skip ? -1.f : L[nt][e]);
-              else if (skip || at.len < 0)
-                skip_row(p, it, r);
-              else
-                store_lse_of(p, it, r, R[nt][e], L[nt][e]);
-            }
+          for (int e = 0; e < 2; ++e) {
+            const int r = 8 * grp + 2 * lane + e;
+            if (!whole)
+              reinterpret_cast<float2*>(p.part_rl)[part * p.rows8 + r] = make_float2(R[e], skip ? -1.f : L[e]);
+            else if (skip || at.len < 0)
+              skip_row(p, it, r);
+            else
+              store_lse_of(p, it, r, R[e], L[e]);
+          }
           if (lane == 0 && grp == 0 && (skip || at.len < 0)) atomicOr(&g_attn_status, skip ? 8u : 2u);
         }
       }
       // This team's 16 of the 64 columns.
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) {
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < kTeams; ++w) {
-          const float4 y = xs[(((grp * kTeams + w) * kNT + nt) * 4 + team) * 32 + lane];
-          x[0] = fmaf(y.x, f[w][nt][0], x[0]);
-          x[1] = fmaf(y.y, f[w][nt][1], x[1]);
-          x[2] = fmaf(y.z, f[w][nt][0], x[2]);
-          x[3] = fmaf(y.w, f[w][nt][1], x[3]);
-        }
-        const int g = grp * kNT + nt, dt = 4 * hf + team;
-        if (!whole)
-          reinterpret_cast<float4*>(p.part_o)[((part * (p.rows8 / 8) + g) * 8 + dt) * 32 + lane] =
-              make_float4(x[0], x[1], x[2], x[3]);
-        else if (!skip && at.len >= 0)
-          store_out(p, it, g, dt, lane, x, __frcp_rn(L[nt][0]), __frcp_rn(L[nt][1]));
+      for (int w = 0; w < kTeams; ++w) {
+        const float4 y = xs[((grp * kTeams + w) * 4 + team) * 32 + lane];
+        x[0] = fmaf(y.x, f[w][0], x[0]);
+        x[1] = fmaf(y.y, f[w][1], x[1]);
+        x[2] = fmaf(y.z, f[w][0], x[2]);
+        x[3] = fmaf(y.w, f[w][1], x[3]);
       }
+      const int dt = 4 * hf + team;
+      if (!whole)
+        reinterpret_cast<float4*>(p.part_o)[((part * (p.rows8 / 8) + grp) * 8 + dt) * 32 + lane] =
+            make_float4(x[0], x[1], x[2], x[3]);
+      else if (!skip && at.len >= 0)
+        store_out(p, it, grp, dt, lane, x, __frcp_rn(L[0]), __frcp_rn(L[1]));
     }
     if (!ends && t_first == 0 && threadIdx.x == 0) p.cuts[blockIdx.x] = {it.b, at.item, at.parts(run, kCost), 0};
     if (i + 1 < n) at.step(p, per, kCost);
@@ -488,10 +472,11 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) attn_paged_fwd(const Pa
 // four units is added to it, to nearest; a warp with a row whose reference rises does so at once.
 //
 // The CTA goes through a unit in step: loads (cp.async, two units ahead), S, exponentials, P V; two CTAs
-// an SM fill each other's waits. P V is not waited for: the next S, behind it on the same pipe, is. By warp-level products 35 rows took 205 us
-// where this takes TODO us (48 x 5 drafted tokens of 28/4 heads, caches of up to 5003 keys: 244 MB):
-// a product of 16 x 8 x 16 occupies a quarter of an SM's tensor core for some 24 to 32 cycles that way, 144
-// of them for every 16 keys.
+// an SM fill each other's waits. P V is not waited for: the next S, behind it on the same pipe, is. 48 x 5
+// drafted tokens of 28/4 heads (35 rows, caches of up to 5003 keys, 244 MB): 67 us and 6 for the join, 3.6 TB/s.
+// By warp-level products it was 154 to 205 us: one of 16 x 8 x 16 occupies a quarter of an SM's tensor cores
+// for some 24 to 32 cycles, and there are 144 of them for every 16 keys. Bound by the instructions of 8 warps an SM
+// (820 a warp and unit, one in 5 cycles): O takes 128 registers a lane, so there is no room for more.
 constexpr int kRowsThreads = 128;
 constexpr int kRowsStages = 3;
 constexpr int kRowsTile = kUnit * kD * 2;                 // 16 KiB: a unit's K or V, as two halves of 64 columns

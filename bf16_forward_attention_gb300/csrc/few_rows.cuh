@@ -2,7 +2,7 @@
 // paged cache does with a tile of 16 keys.
 //
 // The products are transposed, S^T = K Q^T and O^T = V^T P^T, so that the rows are the short
-// side of the 16 x 8 x 16 products. A lane holds rows 8 nt + 2 (lane % 4) + {0, 1} of S^T and
+// side of the 16 x 8 x 16 products. A lane holds rows 2 (lane % 4) + {0, 1} of S^T and
 // of O^T alike, and P^T turns into an operand by movmatrix. P enters as two bf16 terms, as in
 // the fused kernel, so that outputs come within one unit in the last place.
 #pragma once
@@ -38,117 +38,96 @@ __device__ __forceinline__ size_t query_at(int layout, int Hq, int Sq, int group
   return (layout != 0 ? (static_cast<size_t>(b) * Sq + i) * Hq + h : (static_cast<size_t>(b) * Hq + h) * Sq + i) * kD;
 }
 
-// The state of up to 8 kNT rows in one warp. A tile's two products of V start from 0 and are added
+// The state of up to 8 rows in one warp. A tile's two products of V start from 0 and are added
 // to O^T to nearest: the tensor pipe truncates as it accumulates, which over 8192 unit-normal
 // keys a warp would leave 99.88% of outputs within one unit in the last place.
-template <int kNT>
 struct Rows {
-  float o[8][kNT][4];   // O^T: d = 16 dt + lane / 4 (elements 0, 1) and + 8 (2, 3)
-  float ref[kNT][2];    // the row's reference, log2 units
-  float sum[kNT][2];    // this lane's share of the row's sum
-  int lim[kNT][2];      // keys the row sees; 0 for rows past the end
-  uint32_t q[kNT][4][4];
+  float o[8][4];      // O^T: d = 16 dt + lane / 4 (elements 0, 1) and + 8 (2, 3)
+  float ref[2];       // the row's reference, log2 units
+  float sum[2];       // this lane's share of the row's sum
+  int lim[2];         // keys the row sees; 0 for rows past the end
+  uint32_t q[4][4];
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) {
+    for (int dt = 0; dt < 8; ++dt)
 #pragma unroll
-      for (int dt = 0; dt < 8; ++dt)
+      for (int e = 0; e < 4; ++e) o[dt][e] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[dt][nt][e] = 0.f;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        ref[nt][e] = -__int_as_float(0x7F800000);
-        sum[nt][e] = 0.f;
-      }
+    for (int e = 0; e < 2; ++e) {
+      ref[e] = -__int_as_float(0x7F800000);
+      sum[e] = 0.f;
     }
   }
 
-  // Queries: the lane's words of row 8 nt + lane / 4 at `row[nt]` (null: zeros).
-  __device__ __forceinline__ void load_q(const uint16_t* const (&row)[kNT], int lane) {
+  // Queries: the lane's words of row lane / 4 at `row` (null: zeros).
+  __device__ __forceinline__ void load_q(const uint16_t* row, int lane) {
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
+    for (int k2 = 0; k2 < 4; ++k2)
 #pragma unroll
-      for (int k2 = 0; k2 < 4; ++k2)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          q[nt][k2][j] = row[nt] ? __ldg(reinterpret_cast<const uint32_t*>(row[nt]) + 16 * k2 + 4 * j + (lane & 3)) : 0u;
+      for (int j = 0; j < 4; ++j)
+        q[k2][j] = row ? __ldg(reinterpret_cast<const uint32_t*>(row) + 16 * k2 + 4 * j + (lane & 3)) : 0u;
   }
 
   // One tile: K at kt, V at vt (rows by row_at), keys key0 .. key0 + 15. masked: some row does
   // not see some key of it. check_v: keys that only some rows see may lie in it (the causal
   // edge; keys past the end are zeros). c: scale * log2(e). keep(s): the masked logits, log2
-  // units: s[nt][0, 1] of key lane / 4 and [2, 3] of + 8.
+  // units: s[0, 1] of key lane / 4 and [2, 3] of + 8.
   template <typename Keep>
   __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, int key0, bool masked, bool check_v, float c,
                                        int lane, Keep&& keep) {
     const float neg_inf = -__int_as_float(0x7F800000);
     const int k_row = (((lane >> 3) & 1) << 3) + (lane & 7), k_chunk = lane >> 4;
     const int v_row = ((lane >> 4) << 3) + (lane & 7), v_chunk = (lane >> 3) & 1;
-    float s[kNT][4];
-#pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
       uint32_t kf[4];
       ptx::ldmatrix4(kt + row_at(k_row, 2 * ks + k_chunk), kf);
-#pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
-        ptx::mma_16816(s[nt], kf, q[nt][ks >> 1][2 * (ks & 1)], q[nt][ks >> 1][2 * (ks & 1) + 1]);
+      ptx::mma_16816(s, kf, q[ks >> 1][2 * (ks & 1)], q[ks >> 1][2 * (ks & 1) + 1]);
     }
+    float mx[2];
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        s[nt][e] *= c;
-        s[nt][2 + e] *= c;
-        if (masked) {
-          if (key0 + (lane >> 2) >= lim[nt][e]) s[nt][e] = neg_inf;
-          if (key0 + (lane >> 2) + 8 >= lim[nt][e]) s[nt][2 + e] = neg_inf;
-        }
+    for (int e = 0; e < 2; ++e) {
+      s[e] *= c;
+      s[2 + e] *= c;
+      if (masked) {
+        if (key0 + (lane >> 2) >= lim[e]) s[e] = neg_inf;
+        if (key0 + (lane >> 2) + 8 >= lim[e]) s[2 + e] = neg_inf;
       }
+      // The row's largest (a NaN is left out here and comes back through its weight).
+      mx[e] = fmaxf(s[e], s[2 + e]);
+      mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 4));
+      mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 8));
+      mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 16));
+    }
     keep(s);
-    uint32_t hi[kNT][2], lo[kNT][2];  // P^T: keys lane / 4 and + 8, the lane's two rows
+    const bool need0 = mx[0] > ref[0] + kTau, need1 = mx[1] > ref[1] + kTau;
+    if (__any_sync(0xFFFFFFFFu, need0 || need1)) {
+      const float f0 = need0 ? ptx::ex2(ref[0] - mx[0]) : 1.f;  // 0 from -Inf
+      const float f1 = need1 ? ptx::ex2(ref[1] - mx[1]) : 1.f;
+      if (need0) ref[0] = mx[0];
+      if (need1) ref[1] = mx[1];
+      sum[0] *= f0;
+      sum[1] *= f1;
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) {
-      float mx[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        // The row's largest (a NaN is left out here and comes back through its weight).
-        mx[e] = fmaxf(s[nt][e], s[nt][2 + e]);
-        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 4));
-        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 8));
-        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 16));
+      for (int dt = 0; dt < 8; ++dt) {
+        o[dt][0] *= f0;
+        o[dt][1] *= f1;
+        o[dt][2] *= f0;
+        o[dt][3] *= f1;
       }
-      const bool need0 = mx[0] > ref[nt][0] + kTau, need1 = mx[1] > ref[nt][1] + kTau;
-      if (__any_sync(0xFFFFFFFFu, need0 || need1)) {
-        const float f0 = need0 ? ptx::ex2(ref[nt][0] - mx[0]) : 1.f;  // 0 from -Inf
-        const float f1 = need1 ? ptx::ex2(ref[nt][1] - mx[1]) : 1.f;
-        if (need0) ref[nt][0] = mx[0];
-        if (need1) ref[nt][1] = mx[1];
-        sum[nt][0] *= f0;
-        sum[nt][1] *= f1;
+    }
+    const float ref0 = ref[0] == neg_inf ? 0.f : ref[0], ref1 = ref[1] == neg_inf ? 0.f : ref[1];
+    uint32_t hi[2], lo[2];  // P^T: keys lane / 4 and + 8, the lane's two rows
 #pragma unroll
-        for (int dt = 0; dt < 8; ++dt) {
-          o[dt][nt][0] *= f0;
-          o[dt][nt][1] *= f1;
-          o[dt][nt][2] *= f0;
-          o[dt][nt][3] *= f1;
-        }
-      }
-      const float ref0 = ref[nt][0] == neg_inf ? 0.f : ref[nt][0];
-      const float ref1 = ref[nt][1] == neg_inf ? 0.f : ref[nt][1];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const float w0 = ptx::ex2(s[nt][2 * u] - ref0), w1 = ptx::ex2(s[nt][2 * u + 1] - ref1);
-        sum[nt][0] += w0;
-        sum[nt][1] += w1;
-        const uint32_t h = ptx::pack_bf16x2(w0, w1);
-        hi[nt][u] = h;
-        lo[nt][u] = ptx::pack_bf16x2(w0 - __uint_as_float(h << 16), w1 - __uint_as_float(h & 0xFFFF0000u));
-      }
+    for (int u = 0; u < 2; ++u) {
+      const float w0 = ptx::ex2(s[2 * u] - ref0), w1 = ptx::ex2(s[2 * u + 1] - ref1);
+      sum[0] += w0;
+      sum[1] += w1;
+      const uint32_t h = ptx::pack_bf16x2(w0, w1);
+      hi[u] = h;
+      lo[u] = ptx::pack_bf16x2(w0 - __uint_as_float(h << 16), w1 - __uint_as_float(h & 0xFFFF0000u));
     }
     // A key that some row does not see has weight 0 there, and 0 * NaN would carry a
     // non-finite element of its V to that row: where V holds one, the rows are summed key by
@@ -165,51 +144,39 @@ struct Rows {
       apart = __any_sync(0xFFFFFFFFu, acc != 0);
     }
     if (!apart) {
-      uint32_t ph[kNT][2], pl[kNT][2];
-#pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          ph[nt][u] = ptx::movmatrix_trans(hi[nt][u]);
-          pl[nt][u] = ptx::movmatrix_trans(lo[nt][u]);
-        }
+      const uint32_t ph[2] = {ptx::movmatrix_trans(hi[0]), ptx::movmatrix_trans(hi[1])};
+      const uint32_t pl[2] = {ptx::movmatrix_trans(lo[0]), ptx::movmatrix_trans(lo[1])};
 #pragma unroll
       for (int dt = 0; dt < 8; ++dt) {
         uint32_t vf[4];
         ptx::ldmatrix4_trans(vt + row_at(v_row, 2 * dt + v_chunk), vf);
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+        ptx::mma_16816(x, vf, pl[0], pl[1]);
+        ptx::mma_16816(x, vf, ph[0], ph[1]);
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
-          float x[4] = {0.f, 0.f, 0.f, 0.f};
-          ptx::mma_16816(x, vf, pl[nt][0], pl[nt][1]);
-          ptx::mma_16816(x, vf, ph[nt][0], ph[nt][1]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[dt][nt][e] += x[e];
-        }
+        for (int e = 0; e < 4; ++e) o[dt][e] += x[e];
       }
       return;
     }
 #pragma unroll 1
     for (int kk = 0; kk < kKeys; ++kk) {
       const int src = ((kk & 7) << 2) | (lane & 3);
+      const uint32_t h = __shfl_sync(0xFFFFFFFFu, kk < 8 ? hi[0] : hi[1], src);
+      const uint32_t w = __shfl_sync(0xFFFFFFFFu, kk < 8 ? lo[0] : lo[1], src);
+      const float w0 = __uint_as_float(h << 16) + __uint_as_float(w << 16);
+      const float w1 = __uint_as_float(h & 0xFFFF0000u) + __uint_as_float(w & 0xFFFF0000u);
+      const bool see0 = key0 + kk < lim[0], see1 = key0 + kk < lim[1];
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) {
-        const uint32_t h = __shfl_sync(0xFFFFFFFFu, kk < 8 ? hi[nt][0] : hi[nt][1], src);
-        const uint32_t w = __shfl_sync(0xFFFFFFFFu, kk < 8 ? lo[nt][0] : lo[nt][1], src);
-        const float w0 = __uint_as_float(h << 16) + __uint_as_float(w << 16);
-        const float w1 = __uint_as_float(h & 0xFFFF0000u) + __uint_as_float(w & 0xFFFF0000u);
-        const bool see0 = key0 + kk < lim[nt][0], see1 = key0 + kk < lim[nt][1];
-#pragma unroll
-        for (int dt = 0; dt < 8; ++dt) {
-          const float a = ptx::ld_shared_bf16(vt + row_at(kk, 2 * dt) + 2 * (lane >> 2));
-          const float b = ptx::ld_shared_bf16(vt + row_at(kk, 2 * dt + 1) + 2 * (lane >> 2));
-          if (see0) {
-            o[dt][nt][0] = fmaf(w0, a, o[dt][nt][0]);
-            o[dt][nt][2] = fmaf(w0, b, o[dt][nt][2]);
-          }
-          if (see1) {
-            o[dt][nt][1] = fmaf(w1, a, o[dt][nt][1]);
-            o[dt][nt][3] = fmaf(w1, b, o[dt][nt][3]);
-          }
+      for (int dt = 0; dt < 8; ++dt) {
+        const float a = ptx::ld_shared_bf16(vt + row_at(kk, 2 * dt) + 2 * (lane >> 2));
+        const float b = ptx::ld_shared_bf16(vt + row_at(kk, 2 * dt + 1) + 2 * (lane >> 2));
+        if (see0) {
+          o[dt][0] = fmaf(w0, a, o[dt][0]);
+          o[dt][2] = fmaf(w0, b, o[dt][2]);
+        }
+        if (see1) {
+          o[dt][1] = fmaf(w1, a, o[dt][1]);
+          o[dt][3] = fmaf(w1, b, o[dt][3]);
         }
       }
     }
@@ -218,15 +185,13 @@ struct Rows {
   // The rows' sums over the lanes that share them.
   __device__ __forceinline__ void finish_sums() {
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float x = sum[nt][e];
-        x += __shfl_xor_sync(0xFFFFFFFFu, x, 4);
-        x += __shfl_xor_sync(0xFFFFFFFFu, x, 8);
-        x += __shfl_xor_sync(0xFFFFFFFFu, x, 16);
-        sum[nt][e] = x;
-      }
+    for (int e = 0; e < 2; ++e) {
+      float x = sum[e];
+      x += __shfl_xor_sync(0xFFFFFFFFu, x, 4);
+      x += __shfl_xor_sync(0xFFFFFFFFu, x, 8);
+      x += __shfl_xor_sync(0xFFFFFFFFu, x, 16);
+      sum[e] = x;
+    }
   }
 };
 

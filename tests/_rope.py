@@ -6,9 +6,9 @@ and 2^-7 toward zero:
     fp32 operations and two products per element, so |error| <= 2^-16 (|u_a cos| + |u_b sin|),
     then the rounding of the result;
   * backward: two such sums, |error| <= 2^-16 r (|dn| + |x r| mean|dn x r|) + rounding;
-  * weights: fp32 sums whose longest chain has at most 128 additions in these tests (rows of a
-    half-warp, 8 warps, every 32nd block, 32 terms) over terms off by some 2^-17 themselves:
-    |error| <= 2^-16 sum |terms|.
+  * weights: fp32 sums whose longest chain has at most 128 additions in these tests (a lane's
+    rows, a warp's four, four warps, every 32nd block, 32 terms) over terms off by some 2^-17
+    themselves: |error| <= 2^-16 sum |terms|.
 """
 import torch
 

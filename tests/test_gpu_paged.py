@@ -69,6 +69,7 @@ CASES = [
     ("bhsd", 2, 9, 14, 2, 10, 150, [1500, 640], True),           # 63 rows, several parts
     ("bshd", 1, 128, 1, 1, 32, 40, [1280], True),                # 128 rows over many CTAs
     ("bhsd", 1, 129, 1, 1, 32, 10, [300], True),                 # two blocks
+    ("bshd", 2, 301, 2, 2, 16, 40, [590, 301], True),            # 301 rows: three blocks
     ("bshd", 40, 6, 8, 2, 16, 8, None, True),                    # 24 rows, many short sequences
     ("bhsd", 2, 20, 4, 1, 48, 11, [528, 100], False),            # 80 rows
 ]

@@ -149,3 +149,19 @@ def test_python_refusals(change, exc):
         attn.attn_qk_norm_rope_bwd(q, k, q, k, w, w, t, t, at, **kw)
     with pytest.raises(exc):
         attn.attn_qk_norm_rope_paged(q, k, k, w, w, t, t, at, at, bf(3, 4, 2, 128), bf(3, 4, 2, 128), **kw)
+
+
+def test_arguments_of_the_wrong_type():
+    """Errors of the compiled binding arrive as Python's own, before any tensor is looked at."""
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    q, k, w, t, at = bf(5, 4, 128), bf(5, 2, 128), bf(128), torch.zeros(9, 64), torch.zeros(5, dtype=torch.int32)
+    for eps in ("small", None, [1e-6]):
+        with pytest.raises(TypeError):
+            attn.attn_qk_norm_rope(q, k, w, w, t, t, at, eps=eps)
+    for bad in (None, 3, "q", q.numpy if hasattr(q, "numpy") else object()):
+        with pytest.raises(TypeError):
+            attn.attn_qk_norm_rope(bad, k, w, w, t, t, at)
+    with pytest.raises((TypeError, ValueError)):
+        attn.attn_fwd_paged(bf(1, 1, 2, 128), None, None, None, None)
+    with pytest.raises((TypeError, ValueError)):
+        attn.attn_cache_evict(bf(3, 2, 4, 128), bf(3, 2, 4, 128), None, None, None, "all")
