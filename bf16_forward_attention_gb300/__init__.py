@@ -3,7 +3,8 @@
 The product is the C ABI in ``include/attn_fwd.h`` (library
 ``_lib/libattn_fwd.so``, built by ``build.py``). This module is the thin Python
 binding: it checks tensors, marshals pointers and sizes, and calls the library on
-the current torch stream. Every step of the computation runs in the CUDA kernel;
+the current torch stream; for the norm, rotation and paged-cache calls its compiled
+part does so (``_lib/attn_binding.so``). Every step of the computation runs in the CUDA kernel;
 there is no Python or CPU fallback - if the library is missing, calls raise.
 """
 from __future__ import annotations

@@ -22,9 +22,9 @@ constexpr int kTeams = 4;                          // of a CTA, 16 keys of a uni
 constexpr int kUnit = kTeams * few::kKeys;
 constexpr int kStageBytes = 2 * few::kKvBytes;     // a team's K and V
 constexpr int kMaxRows = 128;                      // rows of a block at most
-// What an item costs a run beside its units, in units (its queries, its rows' addition and stores):
-// 1.5 us against 1.4 a unit, and 5 against 1.8 in attn_paged_rows. Runs of equal numbers of units made
-// those of many short items the last to end (48 x 5 drafted tokens: 63 to 108 us a run).
+// What an item costs a run beside its units, in units (its queries, its rows' addition and stores). In
+// attn_paged_rows that is some 13700 cycles an item. Runs of equal numbers of units made those of many short
+// items the last to end (48 x 5 drafted tokens: 63 to 108 us a run, and 47 to 64 with the items counted).
 constexpr int kItemCost = 1, kRowsItemCost = 4;
 
 // kGroups warps a team, 8 rows each: blocks of up to 8 kGroups rows; two CTAs an SM.
@@ -473,10 +473,10 @@ __global__ void __launch_bounds__(Shape<kGroups>::kThreads, 2) attn_paged_fwd(co
 //
 // The CTA goes through a unit in step: loads (cp.async, two units ahead), S, exponentials, P V; two CTAs
 // an SM fill each other's waits. P V is not waited for: the next S, behind it on the same pipe, is. 48 x 5
-// drafted tokens of 28/4 heads (35 rows, caches of up to 5003 keys, 244 MB): 67 us and 6 for the join, 3.6 TB/s.
+// drafted tokens of 28/4 heads (35 rows, caches of up to 5003 keys, 244 MB): 63 to 67 us, 3.7 TB/s; the join 10 by itself.
 // By warp-level products it was 154 to 205 us: one of 16 x 8 x 16 occupies a quarter of an SM's tensor cores
 // for some 24 to 32 cycles, and there are 144 of them for every 16 keys. Bound by the instructions of 8 warps an SM
-// (820 a warp and unit, one in 5 cycles): O takes 128 registers a lane, so there is no room for more.
+// (issue slots 36% busy): O takes 128 registers a lane, so there is no room for more.
 constexpr int kRowsThreads = 128;
 constexpr int kRowsStages = 3;
 constexpr int kRowsTile = kUnit * kD * 2;                 // 16 KiB: a unit's K or V, as two halves of 64 columns
@@ -855,8 +855,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
     uint16_t* to_out =
         p.out + (there ? few::query_at(p.layout, p.Hq, p.Sq, p.group, it.b, it.kvh, it.row0 + r) : 0) + copy * kN;
     const bool good = !skip && at.len >= 0;
-    // A short loop that moves the row along: written out it was 2000 instructions that an item's end had to
-    // fetch (9400 cycles an item).
+    // A short loop that moves the row along, not eight copies of its body. (In one step with kRowsItemCost 4 for 3,
+    // not timed apart: 48 x 5 drafted tokens 80 -> 75 us.)
 #pragma unroll 1
     for (int q = 0; q < 8; ++q) {
       float y[16];

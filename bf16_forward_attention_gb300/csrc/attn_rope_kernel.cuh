@@ -13,7 +13,7 @@
 // rot = 128 both columns of a pair are in one lane, in either form, and a reduction is three
 // shuffles. A warp takes one head of four tokens at a time; the angles of a token stay in its
 // lanes' registers from head to head. (16 lanes a row and the same columns apart in two lanes took 82
-// instructions a row instead of about 30, and was bound by them.)
+// instructions a row instead of 37, and was bound by them.)
 #pragma once
 #include "attn_fwd_kernel.cuh"
 

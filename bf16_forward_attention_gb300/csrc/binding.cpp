@@ -1,6 +1,6 @@
 // binding.cpp - the Python binding's checks and marshalling for the calls around a paged cache
 // and a training step's norms, in C++: a call on one new token spends less time on the GPU
-// (2 to 4 us) than ctypes and Python take to look at its tensors (25 us; 9 us this way).
+// (2 to 4 us) than ctypes and Python take to look at its tensors (25 us; 7 us this way).
 //
 // It checks tensors as the Python wrappers document, allocates results and workspace where none
 // are given, and calls an entry point of the C library by its address on the current torch stream.
