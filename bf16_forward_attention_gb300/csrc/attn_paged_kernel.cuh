@@ -472,8 +472,8 @@ __global__ void __launch_bounds__(Shape<kGroups>::kThreads, 2) attn_paged_fwd(co
 // four units is added to it, to nearest; a warp with a row whose reference rises does so at once.
 //
 // The CTA goes through a unit in step: loads (cp.async, two units ahead), S, exponentials, P V; two CTAs
-// an SM fill each other's waits. P V is not waited for: the next S, behind it on the same pipe, is. 48 x 5
-// drafted tokens of 28/4 heads (35 rows, caches of up to 5003 keys, 244 MB): 63 to 67 us, 3.7 TB/s; the join 10 by itself.
+// an SM fill each other's waits. P V is waited for before the next S is issued (2 us of the case below). 48 x 5
+// drafted tokens of 28/4 heads (35 rows, caches of up to 5003 keys, 244 MB): 65 to 68 us, 3.7 TB/s; the join 10 by itself.
 // By warp-level products it was 154 to 205 us: one of 16 x 8 x 16 occupies a quarter of an SM's tensor cores
 // for some 24 to 32 cycles, and there are 144 of them for every 16 keys. Bound by the instructions of 8 warps an SM
 // (issue slots 36% busy): O takes 128 registers a lane, so there is no room for more.
@@ -599,7 +599,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
   float ref = neg_inf, sum = 0.f;
   int lim = 0, min_lim = 0, t_first = 0;
   bool bad = false, fresh = true, ok = true;
-  uint32_t phase_s = 0, phase_o = 0;
+  uint32_t phase_s = 0, phase_o = 0;        // phase_o: P V products issued
+  bool pv_pending = false;                  // the last one has not been waited for
   int summed = 0;                           // units of O in tensor memory
   auto fold = [&]() {                       // o += what is there
 #pragma unroll
@@ -655,10 +656,16 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
     ptx::fence_proxy_async_smem();  // the copies, before the tensor cores read them
     const bool apart = __syncthreads_or(acc != 0);
     if (warp == 0) {
+      // S comes where the last unit's P stands: products of other shapes and accumulators have no order of
+      // their own.
+      if (pv_pending) ok = warp_wait(bar_o, (phase_o & 1) ^ 1, abort_flag, p.timeout_ns) && ok;
       ptx::tc_fence_after();
-      issue_rows_s(tmem, desc_lo(kt, 16), std::make_integer_sequence<int, 8>{});
-      if (!p.withhold) ptx::mma_commit_warp(bar_s);
+      if (ok) {
+        issue_rows_s(tmem, desc_lo(kt, 16), std::make_integer_sequence<int, 8>{});
+        if (!p.withhold) ptx::mma_commit_warp(bar_s);
+      }
     }
+    pv_pending = false;
     bad = bad || (bad_stages >> s & 1u);
     // ---- the copy's 16 kChunks keys of S; the products before it are done too.
     ok = warp_wait(bar_s, phase_s & 1, abort_flag, p.timeout_ns) && ok;
@@ -781,7 +788,10 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
       if (warp == 0) {
         ptx::tc_fence_after();
         issue_rows_pv(tmem, desc_lo(vt, kRowsTile / 2), summed > 0 ? 1u : 0u, std::make_integer_sequence<int, 4>{});
+        ptx::mma_commit_warp(bar_o);
       }
+      ++phase_o;
+      pv_pending = true;
       ++summed;
     } else {
       // Key by key over what the row sees, weights read back two at a time.
@@ -818,10 +828,10 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
       continue;
     }
     // ---- the item's end, or the run's: the copies are added, 16 columns at a time.
+    // (Its last unit's P V, if that was not key by key: the ones before it are waited for already.)
     if (summed > 0) {
-      if (warp == 0) ptx::mma_commit_warp(bar_o);
-      ok = warp_wait(bar_o, phase_o & 1, abort_flag, p.timeout_ns);
-      ++phase_o;
+      ok = warp_wait(bar_o, (phase_o & 1) ^ 1, abort_flag, p.timeout_ns);
+      pv_pending = false;
       ptx::tc_fence_after();
       fold();
       ptx::tc_fence_before();
