@@ -139,10 +139,14 @@ __device__ __forceinline__ void store_cols(uint16_t* row, const F8 (&f)[2], int 
 enum Form : int { kWhole = 0, kNext = 1, kApart = 2 };
 
 // What a lane knows of the rotation: cos and +-sin of its columns, such that y = u c + (the
-// other half's u) s, and where the other halves are. Eights that are not turned have c = 1, s = 0.
+// other half's u) s, and where the other halves are. Eights that are not turned have c = 1, s = 0, and
+// zeros for the other half: what stands there, or in the neighbouring column, has no part in them, and an
+// infinity times 0 would be a NaN.
 struct Turn {
   F8 c[2], s[2];
   int src[2], slot[2];
+  uint32_t pick[2];  // kNext: of a word's bytes, the halves swapped or zeros; kApart: a mask
+  __device__ __forceinline__ bool turned(int e) const { return (pick[e] & 2u) != 0; }  // in either
 };
 
 // Eight e of a lane: its other halves' eight.
@@ -158,6 +162,8 @@ __device__ __forceinline__ void turn_lane(int lane, int half, Turn& t) {
     const int other = other_eight((lane & 7) + 8 * e, half);
     t.src[e] = (lane & 24) | (other & 7);
     t.slot[e] = other >> 3;
+    const bool turned = 8 * (lane & 7) + 64 * e < 2 * half;
+    t.pick[e] = kForm == kNext ? (turned ? 0x1032u : 0x4444u) : turned ? 0xFFFFFFFFu : 0u;
   }
 }
 
@@ -202,18 +208,18 @@ __device__ __forceinline__ void turn_load(const Params& p, int lane, int pos, Tu
   }
 }
 
-__device__ __forceinline__ uint4 halves_swapped(const uint4& x) {
-  return make_uint4(__funnelshift_l(x.x, x.x, 16), __funnelshift_l(x.y, x.y, 16), __funnelshift_l(x.z, x.z, 16),
-                    __funnelshift_l(x.w, x.w, 16));
+__device__ __forceinline__ uint4 halves_swapped(const uint4& x, uint32_t pick) {
+  return make_uint4(__byte_perm(x.x, 0, pick), __byte_perm(x.y, 0, pick), __byte_perm(x.z, 0, pick),
+                    __byte_perm(x.w, 0, pick));
 }
 
-// The other halves of a lane's columns.
+// The other halves of a lane's columns; zeros where there is none.
 template <int kForm>
 __device__ __forceinline__ Cols others(const Cols& x, const Turn& t) {
   if constexpr (kForm == kWhole) {
     return {{x.x[1], x.x[0]}};
   } else if constexpr (kForm == kNext) {
-    return {{halves_swapped(x.x[0]), halves_swapped(x.x[1])}};
+    return {{halves_swapped(x.x[0], t.pick[0]), halves_swapped(x.x[1], t.pick[1])}};
   } else {
     Cols o;
 #pragma unroll
@@ -223,7 +229,7 @@ __device__ __forceinline__ Cols others(const Cols& x, const Turn& t) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint32_t u = __shfl_sync(0xFFFFFFFFu, a[j], t.src[e]), v = __shfl_sync(0xFFFFFFFFu, b[j], t.src[e]);
-        r[j] = t.slot[e] ? v : u;
+        r[j] = (t.slot[e] ? v : u) & t.pick[e];
       }
       o.x[e] = make_uint4(r[0], r[1], r[2], r[3]);
     }
@@ -322,13 +328,14 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas<kForm>) attn_rope_fwd(const
       if (i >= ch.n) break;
       const Cols o = others<kForm>(x[i], t);
       F8 a[2] = {unpack8(x[i].x[0]), unpack8(x[i].x[1])};
-      const F8 r = both(rsqrtf(fmaf(row_sum(dot(a[0], a[0]) + dot(a[1], a[1])), 1.f / kD, p.eps)));
+      const float r = rsqrtf(fmaf(row_sum(dot(a[0], a[0]) + dot(a[1], a[1])), 1.f / kD, p.eps));
       F8 y[2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) a[e] = mul(a[e], r);
+      for (int e = 0; e < 2; ++e) a[e] = mul(a[e], both(r));
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        y[e] = fma(kForm == kWhole ? a[1 - e] : mul(unpack8(o.x[e]), r), t.s[e], mul(a[e], t.c[e]));
+        y[e] = fma(kForm == kWhole ? a[1 - e] : mul(unpack8(o.x[e]), both(t.turned(e) ? r : 0.f)), t.s[e],
+                   mul(a[e], t.c[e]));
       if (to) store_cols(dst + i * step, y, p.mode);
     }
   }
