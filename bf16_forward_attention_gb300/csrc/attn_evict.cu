@@ -2,15 +2,22 @@
 // the call, lays out the workspace and launches the selection and the moves.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "attn_evict_kernel.cuh"
 #include "attn_fwd.h"
 #include "host_common.h"
 
+namespace {
+
+std::atomic<bool> g_launched{false};
+
+}
+
 namespace attn_host {
 
-bool evict_take_status(unsigned int* s) { return take_status(attn::g_attn_status, s); }
+bool evict_take_status(unsigned int* s) { return take_status(attn::g_attn_status, g_launched, s); }
 
 }  // namespace attn_host
 
@@ -125,6 +132,7 @@ int attn_cache_evict(void* k_pages, void* v_pages, const int32_t* page_table, co
   p.recent = static_cast<int>(recent);
   p.keep = static_cast<int>(pl.keep);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  g_launched.store(true);
   if (cudaMemsetAsync(p.listed, 0, static_cast<size_t>(n_pages) * 4, cs) != cudaSuccess) {
     cudaGetLastError();
     return ATTN_ERR_LAUNCH;

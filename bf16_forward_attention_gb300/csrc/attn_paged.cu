@@ -3,6 +3,7 @@
 // units, then the join of the items they cut with, beside it, the keys' masses where they are wanted.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -11,9 +12,15 @@
 #include "attn_paged_kernel.cuh"
 #include "host_common.h"
 
+namespace {
+
+std::atomic<bool> g_launched{false};
+
+}
+
 namespace attn_host {
 
-bool paged_take_status(unsigned int* s) { return take_status(attn::g_attn_status, s); }
+bool paged_take_status(unsigned int* s) { return take_status(attn::g_attn_status, g_launched, s); }
 
 }  // namespace attn_host
 
@@ -199,6 +206,7 @@ int run(const void* q, const void* k_pages, const void* v_pages, const int32_t* 
   p.timeout_ns = timeout_ns;
   p.withhold = withhold ? 1 : 0;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  g_launched.store(true);
   if (!launch(pl.form->fwd[mass ? 1 : 0], pl.runs, pl.form->threads, pl.form->smem, cs, false, p))
     return ATTN_ERR_LAUNCH;
   // The blocks of the masses: what the join's leave of an SM at once.

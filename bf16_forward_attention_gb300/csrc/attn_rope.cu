@@ -2,6 +2,7 @@
 // include/attn_fwd.h: checks the call and launches on the caller's stream.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -10,9 +11,15 @@
 #include "host_common.h"
 #include "rows.h"
 
+namespace {
+
+std::atomic<bool> g_launched{false};
+
+}
+
 namespace attn_host {
 
-bool rope_take_status(unsigned int* s) { return take_status(attn::g_attn_status, s); }
+bool rope_take_status(unsigned int* s) { return take_status(attn::g_attn_status, g_launched, s); }
 
 }  // namespace attn_host
 
@@ -136,6 +143,7 @@ bool launch_fwd(rope::Params& p, bool paged, rope::Form form, void* stream) {
   p.parts = parts_of(p.tokens, p.chunks, kFwdWarps * int64_t(sms_here()));
   constexpr int64_t kBlock = rope::kWarps * rope::kTokens;
   const dim3 grid(static_cast<unsigned>((int64_t(p.tokens) + kBlock - 1) / kBlock), static_cast<unsigned>(p.parts));
+  g_launched.store(true);
   return launch(kFwd[form][paged], grid, rope::kThreads, 0, static_cast<cudaStream_t>(stream), false, p);
 }
 
@@ -308,6 +316,7 @@ int attn_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q,
   const auto fn = form == rope::kWhole  ? rope::attn_rope_bwd<rope::kWhole>
                   : form == rope::kNext ? rope::attn_rope_bwd<rope::kNext>
                                         : rope::attn_rope_bwd<rope::kApart>;
+  g_launched.store(true);
   if (!launch(fn, grid.blocks, rope::kThreads, rope::kBwdSmem, cs, false, p)) return ATTN_ERR_LAUNCH;
   const rope::JoinParams j = {p.part, dq_weight, dk_weight, static_cast<int>(grid.blocks)};
   return launch(rope::attn_rope_join, 2 * attn::kD / rope::kJoinCols, rope::kJoinThreads, 0, cs, true, j)
