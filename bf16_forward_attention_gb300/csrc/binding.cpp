@@ -162,10 +162,15 @@ Pages pages_of(PyObject* ko, PyObject* vo, int layout, int device = -1) {
   p.k = &bf16("k_pages", ko, device);
   p.v = &bf16("v_pages", vo, p.k->get_device());
   const auto n = p.k->sizes(), s = p.k->strides();
-  if (n.size() != 4 || p.v->sizes() != n || p.v->strides() != s)
-    value_error("k_pages and v_pages must be 4-D tensors of one shape and strides");
-  if ((s[1] != n[2] * n[3] || s[2] != n[3] || s[3] != 1) && !p.k->is_contiguous())
-    value_error("a page of k_pages and v_pages must be contiguous");
+  const auto vs = p.v->strides();
+  if (n.size() != 4 || p.v->sizes() != n) value_error("k_pages and v_pages must be 4-D tensors of one shape and strides");
+  // A dimension of one entry has no stride: what stands there is not looked at.
+  const int64_t dense[4] = {0, n[2] * n[3], n[3], 1};
+  for (int i = 0; i < 4; ++i) {
+    if (n[i] <= 1) continue;
+    if (vs[i] != s[i]) value_error("k_pages and v_pages must be 4-D tensors of one shape and strides");
+    if (i > 0 && s[i] != dense[i]) value_error("a page of k_pages and v_pages must be contiguous");
+  }
   const bool bshd = layout == ATTN_LAYOUT_BSHD;
   p.n = n[0];
   p.page = bshd ? n[1] : n[2];
