@@ -714,7 +714,7 @@ def _load_binding():
 
     if not os.path.exists(BINDING_PATH):
         raise RuntimeError(f"binding not built: {BINDING_PATH} is missing. Run "
-                           "`python -m bf16_forward_attention_gb300.build`.")
+                           "`python -m bf16_forward_attention_gb300.build` beside a torch with CUDA.")
     loader = importlib.machinery.ExtensionFileLoader("attn_binding", BINDING_PATH)
     spec = importlib.util.spec_from_file_location("attn_binding", BINDING_PATH, loader=loader)
     _binding = importlib.util.module_from_spec(spec)

@@ -68,9 +68,13 @@ def _library_up_to_date(debug: bool = False) -> bool:
 
 
 def _torch_dir():
-    """Where torch is installed; None without it (the library can be used from C all the same)."""
+    """Where torch is installed; None without it, or where it is one without CUDA, which has no tensors that
+    the binding takes (the library can be used from C all the same)."""
     spec = importlib.util.find_spec("torch")
-    return spec.submodule_search_locations[0] if spec else None
+    if not spec or not spec.submodule_search_locations:
+        return None
+    path = spec.submodule_search_locations[0]
+    return path if os.path.exists(os.path.join(path, "lib", "libc10_cuda.so")) else None
 
 
 def _binding_up_to_date() -> bool:
@@ -83,7 +87,7 @@ def up_to_date(debug: bool = False) -> bool:
 
 def _binding_build(force: bool):
     """A running compilation of the binding's C++ part (no kernels) against the installed torch and
-    Python, and where its output is; None if it is newer than its sources, or there is no torch."""
+    Python, and where its output is; None if it is newer than its sources, or there is no torch for it."""
     torch_dir = _torch_dir()
     if torch_dir is None or (not force and _binding_up_to_date()):
         return None
