@@ -4,7 +4,7 @@ The product is the C ABI in ``include/attn_fwd.h`` (library
 ``_lib/libattn_fwd.so``, built by ``build.py``). This module is the thin Python
 binding: it checks tensors, marshals pointers and sizes, and calls the library on
 the current torch stream; for the norm, rotation and paged-cache calls its compiled
-part does so (``_lib/attn_binding.so``). Every step of the computation runs in the CUDA kernel;
+part does so (``_lib/attn_binding-*.so``). Every step of the computation runs in the CUDA kernel;
 there is no Python or CPU fallback - if the library is missing, calls raise.
 """
 from __future__ import annotations
@@ -15,7 +15,7 @@ import functools
 import math
 import os
 
-from .build import BINDING_PATH, lib_path
+from .build import LIB_DIR, binding_path, lib_path
 
 LAYOUTS = {"bhsd": 0, "bshd": 1}
 ROUNDINGS = {"rtne": 0, "rtna": 1, "rtz": 2}
@@ -705,18 +705,19 @@ _binding = None
 
 
 def _load_binding():
-    """``_lib/attn_binding.so``; raises if it has not been built."""
+    """``_lib/attn_binding-*.so`` for this torch and Python; raises if it has not been built."""
     global _binding
     import importlib.machinery
     import importlib.util
 
     import torch  # noqa: F401  (the module's symbols are torch's)
 
-    if not os.path.exists(BINDING_PATH):
-        raise RuntimeError(f"binding not built: {BINDING_PATH} is missing. Run "
+    path = binding_path()
+    if not os.path.exists(path):
+        raise RuntimeError(f"binding not built: {path or LIB_DIR + '/attn_binding-*.so'} is missing. Run "
                            "`python -m bf16_forward_attention_gb300.build` beside a torch with CUDA.")
-    loader = importlib.machinery.ExtensionFileLoader("attn_binding", BINDING_PATH)
-    spec = importlib.util.spec_from_file_location("attn_binding", BINDING_PATH, loader=loader)
+    loader = importlib.machinery.ExtensionFileLoader("attn_binding", path)
+    spec = importlib.util.spec_from_file_location("attn_binding", path, loader=loader)
     _binding = importlib.util.module_from_spec(spec)
     loader.exec_module(_binding)
     return _binding

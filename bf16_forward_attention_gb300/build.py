@@ -12,13 +12,14 @@ over a paged cache, its eviction) and the host-buffer pipeline, compiled at once
 one -gencode; the CUDA runtime is linked statically and the driver's tensor-map
 encoder is looked up at run time, so the library loads (and reports
 ATTN_ERR_NO_DEVICE) on a machine without a GPU. Beside it the host compiler builds
-``_lib/attn_binding.so``, the C++ part of the Python binding, against the installed
-torch; the library itself knows nothing of torch.
+``_lib/attn_binding-*.so``, the C++ part of the Python binding, against the installed
+torch, whose version and Python's are in its name; the library itself knows nothing of torch.
 """
 from __future__ import annotations
 
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -31,7 +32,6 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libattn_fwd.so")
 LIB_PATH_DEBUG = os.path.join(LIB_DIR, "libattn_fwd_debug.so")
-BINDING_PATH = os.path.join(LIB_DIR, "attn_binding.so")
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 SOURCES = [os.path.join(CSRC, f) for f in ("attn_fwd.cu", "attn_bwd.cu", "attn_prefix.cu", "attn_rope.cu",
                                             "attn_paged.cu", "attn_evict.cu", "attn_host.cu")]
@@ -77,8 +77,21 @@ def _torch_dir():
     return path if os.path.exists(os.path.join(path, "lib", "libc10_cuda.so")) else None
 
 
+def binding_path() -> str:
+    """The C++ part of the binding for the torch and the Python that are here: it holds to the layout of their
+    objects, so that one built for others is never taken for it. "" where there is no torch for it."""
+    torch_dir = _torch_dir()
+    if torch_dir is None:
+        return ""
+    with open(os.path.join(torch_dir, "version.py")) as f:
+        version = re.search(r"__version__ *= *['\"]([^'\"]+)", f.read())
+    name = f"attn_binding-torch{version.group(1) if version else ''}{sysconfig.get_config_var('EXT_SUFFIX')}"
+    return os.path.join(LIB_DIR, name)
+
+
 def _binding_up_to_date() -> bool:
-    return _torch_dir() is None or _newer(BINDING_PATH, [BINDING_SOURCE, os.path.join(INCLUDE, "attn_fwd.h")])
+    path = binding_path()
+    return not path or _newer(path, [BINDING_SOURCE, os.path.join(INCLUDE, "attn_fwd.h")])
 
 
 def up_to_date(debug: bool = False) -> bool:
@@ -87,19 +100,20 @@ def up_to_date(debug: bool = False) -> bool:
 
 def _binding_build(force: bool):
     """A running compilation of the binding's C++ part (no kernels) against the installed torch and
-    Python, and where its output is; None if it is newer than its sources, or there is no torch for it."""
+    Python, its command, where its output is and where that belongs; None if it is newer than its sources, or there is no torch for it."""
     torch_dir = _torch_dir()
     if torch_dir is None or (not force and _binding_up_to_date()):
         return None
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")
-    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    path = binding_path()
+    tmp = path + f".tmp{os.getpid()}"
     cmd = [shutil.which("g++") or "c++", "-std=c++17", "-O2", "-fPIC", "-shared", "-o", tmp, BINDING_SOURCE]
     for d in (INCLUDE, os.path.join(torch_dir, "include"),
               os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
               sysconfig.get_paths()["include"], cuda):
         cmd += ["-I", d]
     cmd += ["-L", os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python"]
-    return subprocess.Popen(cmd), cmd, tmp
+    return subprocess.Popen(cmd), cmd, tmp, path
 
 
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
@@ -120,10 +134,10 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
         subprocess.run(cmd, check=True)
         os.replace(tmp, path)
     if binding:
-        run, cmd, tmp = binding
+        run, cmd, tmp, to = binding
         if run.wait() != 0:
             raise subprocess.CalledProcessError(run.returncode, cmd)
-        os.replace(tmp, BINDING_PATH)
+        os.replace(tmp, to)
     return path
 
 
