@@ -21,6 +21,7 @@ import importlib.util
 import os
 import re
 import shutil
+import signal
 import subprocess
 import sys
 import sysconfig
@@ -113,7 +114,7 @@ def _binding_build(force: bool):
               sysconfig.get_paths()["include"], cuda):
         cmd += ["-I", d]
     cmd += ["-L", os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python"]
-    return subprocess.Popen(cmd), cmd, tmp, path
+    return subprocess.Popen(cmd, start_new_session=True), cmd, tmp, path  # a group: the compiler has children
 
 
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
@@ -122,22 +123,31 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     path = lib_path(debug)
     os.makedirs(LIB_DIR, exist_ok=True)
     binding = None if debug else _binding_build(force)
-    if force or not _library_up_to_date(debug):
-        tmp = path + f".tmp{os.getpid()}"
-        cmd = [nvcc_path(), "-gencode", GENCODE, "-O3", "-lineinfo", "-std=c++17",
-               "--threads", "0", "-Xcompiler", "-fPIC", "-shared", "-I", INCLUDE, "-o", tmp] + SOURCES
-        if debug:
-            cmd.insert(1, "-DATTN_DEBUG=1")
-        if verbose:
-            cmd.insert(1, "-Xptxas=-v")
-            print(" ".join(cmd), flush=True)
-        subprocess.run(cmd, check=True)
-        os.replace(tmp, path)
-    if binding:
-        run, cmd, tmp, to = binding
-        if run.wait() != 0:
-            raise subprocess.CalledProcessError(run.returncode, cmd)
-        os.replace(tmp, to)
+    try:
+        if force or not _library_up_to_date(debug):
+            tmp = path + f".tmp{os.getpid()}"
+            cmd = [nvcc_path(), "-gencode", GENCODE, "-O3", "-lineinfo", "-std=c++17",
+                   "--threads", "0", "-Xcompiler", "-fPIC", "-shared", "-I", INCLUDE, "-o", tmp] + SOURCES
+            if debug:
+                cmd.insert(1, "-DATTN_DEBUG=1")
+            if verbose:
+                cmd.insert(1, "-Xptxas=-v")
+                print(" ".join(cmd), flush=True)
+            subprocess.run(cmd, check=True)
+            os.replace(tmp, path)
+        if binding:
+            run, cmd, tmp, to = binding
+            if run.wait() != 0:
+                raise subprocess.CalledProcessError(run.returncode, cmd)
+            os.replace(tmp, to)
+    finally:
+        if binding:  # nothing of it is left, however the library's compilation ended
+            run, _, tmp, _ = binding
+            if run.poll() is None:
+                os.killpg(run.pid, signal.SIGTERM)
+                run.wait()
+            if os.path.exists(tmp):
+                os.remove(tmp)
     return path
 
 

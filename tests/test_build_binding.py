@@ -1,7 +1,9 @@
 """The build of the binding's C++ part."""
 import importlib.util
 import os
+import subprocess
 import sys
+import time
 import types
 
 import pytest
@@ -49,7 +51,7 @@ def _compiler(monkeypatch):
     class Run:
         returncode = 0
 
-        def __init__(self, cmd):
+        def __init__(self, cmd, **kw):
             runs.append(cmd)
             with open(cmd[cmd.index("-o") + 1], "w") as f:
                 f.write(" ".join(cmd))
@@ -91,3 +93,45 @@ def test_the_built_binding_is_found_and_loads():
     build.build()
     assert hasattr(attn._load_binding(), "fwd_paged")
     assert os.path.exists(build.binding_path()) and "torch" in sys.modules
+
+
+def test_no_compilation_is_left_behind_when_the_library_fails(sandbox, monkeypatch):
+    """The host compiler runs beside nvcc: where that fails, it is ended and waited for, and its file removed."""
+    _fake_torch(sandbox, monkeypatch, cuda=True)
+    (sandbox / "_lib" / "libattn_fwd.so").unlink()
+    started = []
+
+    def popen(cmd, **kw):
+        to = cmd[cmd.index("-o") + 1]
+        run = real([sys.executable, "-c", "import sys, time; open(sys.argv[1], 'w').close(); time.sleep(60)", to], **kw)
+        while not os.path.exists(to) and run.poll() is None:
+            time.sleep(0.01)
+        started.append((run, to))
+        return run
+
+    def fails(cmd, **kw):
+        raise subprocess.CalledProcessError(1, cmd)
+
+    real = subprocess.Popen
+    monkeypatch.setattr(build.subprocess, "Popen", popen)
+    monkeypatch.setattr(build.subprocess, "run", fails)
+    try:
+        with pytest.raises(subprocess.CalledProcessError):
+            build.build()
+        (run, to), = started
+        assert run.returncode is not None, "still running"
+        assert not os.path.exists(to)
+    finally:
+        for run, _ in started:
+            run.kill()
+            run.wait()
+
+
+def test_a_failed_binding_leaves_no_file(sandbox, monkeypatch):
+    _fake_torch(sandbox, monkeypatch, cuda=True)
+    real = subprocess.Popen
+    monkeypatch.setattr(build.subprocess, "Popen", lambda cmd, **kw: real(
+        [sys.executable, "-c", "import sys; open(sys.argv[1], 'w').close(); sys.exit(3)", cmd[cmd.index("-o") + 1]], **kw))
+    with pytest.raises(subprocess.CalledProcessError):
+        build.build()
+    assert os.listdir(sandbox / "_lib") == ["libattn_fwd.so"]
