@@ -50,6 +50,11 @@ constexpr Form rows_form() {
   return {128 / kCopies, paged::kRowsThreads, paged::kRowsSmem, 2, paged::kRowsItemCost, true,
           {paged::attn_paged_rows<kCopies, false>, paged::attn_paged_rows<kCopies, true>}};
 }
+// The first that holds a block's rows. Up to 16 the warp-level form, from 17 on the tensor cores: us a call with
+// the one / the other at 1, 8, 9 and 16 rows a kv head, pages of 16:
+//   64 caches of up to 8192 keys, 8 kv heads  178 / 199  178 / 199  197 / 200  201 / 202
+//   64 of up to 300                            23 / 34    25 / 34    29 / 35    31 / 35
+//   one of 100000                              75 / 85    75 / 85    81 / 87    81 / 86
 constexpr Form kForms[] = {form<1>(), form<2>(), rows_form<4>(), rows_form<2>(), rows_form<1>()};
 
 int device_ready() {

@@ -25,6 +25,10 @@ constexpr int kMaxRows = 128;                      // rows of a block at most
 // What an item costs a run beside its units, in units (its queries, its rows' addition and stores). In
 // attn_paged_rows that is some 13700 cycles an item. Runs of equal numbers of units made those of many short
 // items the last to end (48 x 5 drafted tokens: 63 to 108 us a run, and 47 to 64 with the items counted).
+// One number for all its rows, us a call at 24 / 35 / 64 / 128 of them (4, 2, 2 copies and 1):
+//   64 caches of up to 300 keys:   3: 38.5 / 44.8 / 50.8 / 69.2   4: 37.5 / 43.3 / 48.2 / 66.6   6: 38.1 / 45.4 / 50.2 / 67.7
+//   48 of up to 5003, 4 kv heads:  3: 67.0 / 81.4 / 88.5 / 121    4: 66.3 / 80.5 / 86.9 / 120    6: 67.2 / 80.5 / 85.8 / 119
+//   64 of up to 8192, 8 kv heads:  3: 219 / 264 / 282 / 393       4: 209 / 255 / 270 / 375       6: 208 / 247 / 261 / 367
 constexpr int kItemCost = 1, kRowsItemCost = 4;
 
 // kGroups warps a team, 8 rows each: blocks of up to 8 kGroups rows; two CTAs an SM.
@@ -476,7 +480,8 @@ __global__ void __launch_bounds__(Shape<kGroups>::kThreads, 2) attn_paged_fwd(co
 // drafted tokens of 28/4 heads (35 rows, caches of up to 5003 keys, 244 MB): 65 to 68 us, 3.7 TB/s; the join 10 by itself.
 // By warp-level products it was 154 to 205 us: one of 16 x 8 x 16 occupies a quarter of an SM's tensor cores
 // for some 24 to 32 cycles, and there are 144 of them for every 16 keys. Bound by the instructions of 8 warps an SM
-// (issue slots 36% busy): O takes 128 registers a lane, so there is no room for more.
+// (issue slots 36% busy): O takes 128 registers a lane, so there is no room for more. P enters as two bf16 terms
+// (few_rows.cuh says what that leaves); a third would need 32 columns of tensor memory that two CTAs an SM do not have.
 constexpr int kRowsThreads = 128;
 constexpr int kRowsStages = 3;
 constexpr int kRowsTile = kUnit * kD * 2;                 // 16 KiB: a unit's K or V, as two halves of 64 columns
@@ -865,8 +870,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2) attn_paged_rows(const Params 
     uint16_t* to_out =
         p.out + (there ? few::query_at(p.layout, p.Hq, p.Sq, p.group, it.b, it.kvh, it.row0 + r) : 0) + copy * kN;
     const bool good = !skip && at.len >= 0;
-    // A short loop that moves the row along, not eight copies of its body. (In one step with kRowsItemCost 4 for 3,
-    // not timed apart: 48 x 5 drafted tokens 80 -> 75 us.)
+    // A short loop that moves the row along, not eight copies of its body (48 x 5 drafted tokens 80 -> 75 us, of
+    // which kRowsItemCost 4 for 3 is one).
 #pragma unroll 1
     for (int q = 0; q < 8; ++q) {
       float y[16];

@@ -394,7 +394,8 @@ int attn_fwd_splitkv_noalloc(const void* q, const void* k, const void* v, void* 
  *   u = x * weight * r,  r = (mean(x^2) + eps)^(-1/2),  and for each of rotary_dim / 2
  *   pairs (a, b) of columns:  y_a = u_a cos - u_b sin,  y_b = u_b cos + u_a sin
  * with cos and sin at (t, i); columns at and after rotary_dim are u. Formed in fp32 and
- * rounded once, per rounding_mode. The pages describe attention alone and have no
+ * rounded once, per rounding_mode; a NaN or an infinity reaches the results whose formula has
+ * it, in fp32, and no others. The pages describe attention alone and have no
  * counterpart of these calls.
  *
  *   q, q_out   device, bf16, (B, S, Hq, 128);  k, k_out (B, S, Hkv, 128), each wherever
@@ -505,8 +506,9 @@ int64_t attn_qk_norm_rope_bwd_workspace_bytes(int64_t B, int64_t S, int64_t Hq, 
  *   mass       device, fp32, (B, Hkv, max_pages * page_size), or NULL: added to it, for every
  *              key, its attention weight summed over the sequence's Sq tokens and the query
  *              heads of the group, exp(scale q.k - lse). Entries at and after a sequence's
- *              length are left as they are; a row that sees no key adds nothing. (What
- *              attn_cache_evict goes by.)
+ *              length are left as they are; a row whose lse is -Inf (it sees no key, or only
+ *              logits of -Inf) adds nothing, one whose lse is NaN makes the masses of the keys
+ *              it sees NaN. (What attn_cache_evict goes by.)
  *   flags      0: a query sees all its sequence's keys; ATTN_FLAG_CAUSAL: query i sees key
  *              j iff j <= i + seqlens[b] - Sq (the Sq new tokens are the sequence's last)
  *   workspace  device, 16-byte aligned, attn_fwd_paged_workspace_bytes(...) bytes, owned by
