@@ -139,9 +139,9 @@ __device__ __forceinline__ void store_cols(uint16_t* row, const F8 (&f)[2], int 
 enum Form : int { kWhole = 0, kNext = 1, kApart = 2 };
 
 // What a lane knows of the rotation: cos and +-sin of its columns, such that y = u c + (the
-// other half's u) s, and where the other halves are. Eights that are not turned have c = 1, s = 0, and
+// other half's u) s, and where the other halves are. Eights that are not turned have c = 1, s = -0, and
 // zeros for the other half: what stands there, or in the neighbouring column, has no part in them, and an
-// infinity times 0 would be a NaN.
+// infinity times 0 would be a NaN. What is added is then -0, which leaves a zero its sign.
 struct Turn {
   F8 c[2], s[2];
   int src[2], slot[2];
@@ -180,7 +180,7 @@ __device__ __forceinline__ void turn_load(const Params& p, int lane, int pos, Tu
       for (int j = 0; j < 4; ++j) t.s[1].p[j] = ptx::f2_sub(0, t.s[0].p[j]);
     } else if (c0 >= 2 * p.half) {
       t.c[e] = both(1.f);
-      t.s[e] = both(0.f);
+      t.s[e] = both(-0.f);
     } else if constexpr (kForm == kNext) {
       const float4 c = __ldg(reinterpret_cast<const float4*>(p.cos + row + c0 / 2));
       const float4 s = __ldg(reinterpret_cast<const float4*>(p.sin + row + c0 / 2));

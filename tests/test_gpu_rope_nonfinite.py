@@ -118,3 +118,19 @@ def test_a_root_that_overflows(rot, inter):
     _ok()
     want = math.inf * torch.sign(c[0][3, 0, rot:].float() * c[2][rot:].float().sign())
     assert torch.equal(got[3, 0, rot:].cpu().float(), want)
+
+
+@pytest.mark.parametrize("rot,inter", [f for f in FORMS if f[0] < 128])
+def test_signed_zeros(rot, inter):
+    """A zero in a column that is not rotated keeps its sign, times the weight's, beside values and zeros of
+    either sign."""
+    c, _ = _case(rot, seed=700)
+    signs = torch.tensor([1.0, -1.0, -1.0, 1.0]).repeat(32).to(torch.bfloat16)
+    c[0][2, 1, rot:] = 0.0 * signs[rot:]
+    c[0][3, 0, rot + 1::2] = -0.0
+    c[2][rot + 3::4] *= -1
+    d = [t.cuda() for t in c]
+    got, _ = attn.attn_qk_norm_rope(*d, interleaved=inter)
+    _ok()
+    want = torch.signbit(c[0]) ^ torch.signbit(c[2])
+    assert torch.equal(torch.signbit(got.cpu())[..., rot:], want[..., rot:])
