@@ -101,7 +101,8 @@ def up_to_date(debug: bool = False) -> bool:
 
 def _binding_build(force: bool):
     """A running compilation of the binding's C++ part (no kernels) against the installed torch and
-    Python, its command, where its output is and where that belongs; None if it is newer than its sources, or there is no torch for it."""
+    Python, its command, where its output is and where that belongs; None if the binding is newer
+    than its sources, or there is no torch for it."""
     torch_dir = _torch_dir()
     if torch_dir is None or (not force and _binding_up_to_date()):
         return None
